@@ -13,22 +13,28 @@ PyTorch only provides device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+from typing import NamedTuple
 
 import torch
 
 from . import _lib
 from ._lib import DsaError, KEY_BF16, KEY_FP8_E4M3, KEY_INT8  # noqa: F401
 from ._lib import DEVICE_BAD_PAGE, DEVICE_CONFIG, DEVICE_MMA_TIMEOUT, DEVICE_TMA_TIMEOUT  # noqa: F401
+from ._lib import DEVICE_BAD_LENGTH, DEVICE_POOL_EMPTY, DEVICE_POOL_FULL, DEVICE_ROWS_FULL  # noqa: F401
 
 INDEX_HEADS, INDEX_DIM, HEADS, LATENT_DIM, ROPE_DIM, ROW_DIM = 32, 128, 64, 512, 64, 576
+KV_DIM = 128                   # head width of the dense layer's K/V cache
 DEFAULT_SCALE = 1.0 / 16.0     # 1/sqrt(192 + 64)
 _FORMATS = {"bf16": KEY_BF16, "fp8": KEY_FP8_E4M3, "int8": KEY_INT8, None: KEY_BF16}
 _LATENT_FORMATS = {"bf16": _lib.LATENT_BF16, "fp8": _lib.LATENT_E4M3}
 
 __all__ = ["LayerCache", "Batch", "kv_append", "kv_append_layers", "indexer_scores_topk", "indexer_page_topk", "sparse_mla_decode", "sparse_mla_decode_layers", "sparse_mla_prefill",
            "cache_bytes", "indexer_workspace_bytes", "mla_workspace_bytes", "DsaError", "DEFAULT_SCALE",
-           "dcp_candidates", "dcp_select", "dcp_merge", "read_status"]
+           "dcp_candidates", "dcp_select", "dcp_merge", "read_status",
+           "PagePool", "StepPlan", "step_plan", "pages_release", "BlockKvCache", "kv8_append", "paged_attention",
+           "paged_attention_workspace_bytes"]
 
 
 def _ptr(t):
@@ -378,4 +384,231 @@ def dcp_merge(outs, lses, out=None, lse=None, stream=None):
     _need(out, torch.bfloat16, (R, HEADS, LATENT_DIM), "out")
     _need(lse, torch.float32, (R, HEADS), "lse")
     _lib.check(_lib.load().dsa_dcp_merge(_ptr(outs), _ptr(lses), world, R, _ptr(out), _ptr(lse), _stream(stream)))
+    return out, lse
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# the step planner, and the dense (draft) layer over its 8-bit K/V cache
+# ---------------------------------------------------------------------------------------------------------------------
+def _on(device, stream):
+    """The context in which a call allocates and launches: the tensors' device, and the stream given."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows(t, heads, name):
+    """A [rows, heads, 128] bf16 view whose rows may lie apart (a slice of a fused projection); returns the row stride."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != KV_DIM:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (rows, {heads}, {KV_DIM})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != KV_DIM)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * KV_DIM)
+
+
+class PagePool:
+    """The stack of free pages of a paged cache: pages [capacity] int32, count [1] int32 (device tensors).  Layers
+    that share block tables share one pool."""
+
+    def __init__(self, num_pages: int, device="cuda"):
+        self.pages = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.count = torch.full((1,), num_pages, dtype=torch.int32, device=device)
+
+    @classmethod
+    def of(cls, pages, count):
+        """A pool over existing tensors."""
+        _need(pages, torch.int32, (pages.shape[0],), "pages")
+        _need(count, torch.int32, (1,), "count")
+        pool = cls.__new__(cls)
+        pool.pages, pool.count = pages, count
+        return pool
+
+
+class StepPlan(NamedTuple):
+    """What step_plan built: seq_lens [B] and query_start_loc [B + 1] int32 for Batch, slot_mapping [rows] int64 for
+    kv_append, positions [rows] int32, free_count [1] int32."""
+    seq_lens: torch.Tensor
+    query_start_loc: torch.Tensor
+    slot_mapping: torch.Tensor
+    positions: torch.Tensor
+    free_count: torch.Tensor
+
+
+def step_plan(pool: PagePool, seq_lens, new_lens, block_table, page_size: int, num_rows: int, seq_lens_out=None,
+              query_start_loc=None, slot_mapping=None, positions=None, free_count_out=None, workspace=None, stream=None,
+              check=False) -> StepPlan:
+    """Block tables and slot maps of a step, on the device: request b holds seq_lens[b] tokens and brings new_lens[b].
+    Pages come off the pool's stack; block_table [B, stride] gets the new page ids in place.  num_rows is a host
+    bound on the new tokens: rows behind the last have slot and position -1.  The requests admitted are the longest
+    prefix that rows and pages last for (check=True raises DsaError where some were not).  Pass seq_lens as
+    seq_lens_out and pool.count as free_count_out to carry the step out; without, the plan is a proposal and the
+    inputs keep their values (but for block-table entries behind a request's pages)."""
+    B = int(seq_lens.shape[0])
+    _need(seq_lens, torch.int32, (B,), "seq_lens")
+    dev = seq_lens.device
+    with _on(dev, stream):
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)   # noqa: E731
+        seq_lens_out = new((B,), torch.int32) if seq_lens_out is None else seq_lens_out
+        query_start_loc = new((B + 1,), torch.int32) if query_start_loc is None else query_start_loc
+        slot_mapping = new((num_rows,), torch.int64) if slot_mapping is None else slot_mapping
+        positions = new((num_rows,), torch.int32) if positions is None else positions
+        free_count_out = new((1,), torch.int32) if free_count_out is None else free_count_out
+        for t, dtype, shape, name in ((new_lens, torch.int32, (B,), "new_lens"),
+                                      (block_table, torch.int32, (B, block_table.shape[-1]), "block_table"),
+                                      (pool.pages, torch.int32, pool.pages.shape, "pool.pages"),
+                                      (pool.count, torch.int32, (1,), "pool.count"),
+                                      (seq_lens_out, torch.int32, (B,), "seq_lens_out"),
+                                      (query_start_loc, torch.int32, (B + 1,), "query_start_loc"),
+                                      (slot_mapping, torch.int64, (num_rows,), "slot_mapping"),
+                                      (positions, torch.int32, (num_rows,), "positions"),
+                                      (free_count_out, torch.int32, (1,), "free_count_out")):
+            _need(t, dtype, shape, name)
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if check and workspace is None:
+            workspace = _workspace(256, dev)
+        _same_device(dev, workspace=workspace)
+        _lib.check(_lib.load().dsa_step_plan(
+            _ptr(seq_lens), _ptr(new_lens), B, page_size, _ptr(block_table), int(block_table.shape[1]), _ptr(pool.pages),
+            int(pool.pages.shape[0]), _ptr(pool.count), num_rows, _ptr(seq_lens_out), _ptr(query_start_loc),
+            _ptr(slot_mapping), _ptr(positions), _ptr(free_count_out), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        if check:
+            _check_device(workspace, stream)
+    return StepPlan(seq_lens_out, query_start_loc, slot_mapping, positions, free_count_out)
+
+
+def pages_release(pool: PagePool, finished, seq_lens, block_table, page_size: int, num_pages: int, workspace=None,
+                  stream=None, check=False):
+    """Return the pages of the requests with finished[b] != 0 to the pool, in place: their table entries become -1
+    and their lengths 0."""
+    B = int(seq_lens.shape[0])
+    _need(seq_lens, torch.int32, (B,), "seq_lens")
+    dev = seq_lens.device
+    _need(finished, torch.int32, (B,), "finished")
+    _need(block_table, torch.int32, (B, block_table.shape[-1]), "block_table")
+    _need(pool.pages, torch.int32, pool.pages.shape, "pool.pages")
+    _need(pool.count, torch.int32, (1,), "pool.count")
+    _same_device(dev, finished=finished, block_table=block_table, pages=pool.pages, count=pool.count, workspace=workspace)
+    with _on(dev, stream):
+        if check and workspace is None:
+            workspace = _workspace(256, dev)
+        _lib.check(_lib.load().dsa_pages_release(
+            _ptr(finished), _ptr(seq_lens), B, page_size, _ptr(block_table), int(block_table.shape[1]), num_pages,
+            _ptr(pool.pages), int(pool.pages.shape[0]), _ptr(pool.count), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        if check:
+            _check_device(workspace, stream)
+
+
+class BlockKvCache:
+    """A dense grouped-head layer's paged 8-bit K/V cache: k_codes / v_codes [num_pages, kv_heads, page_size, 128] uint8
+    (e4m3 codes) and k_scales / v_scales [num_pages, kv_heads] fp32, one scale per block (= page) and head."""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, device="cuda"):
+        shape = (int(num_pages), int(kv_heads), int(page_size), KV_DIM)
+        self._set(*(torch.zeros(shape, dtype=torch.uint8, device=device) for _ in "kv"),
+                  *(torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in "kv"))
+
+    @classmethod
+    def of(cls, k_codes, v_codes, k_scales, v_scales):
+        """A cache over existing tensors."""
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            if t.dim() != 4 or t.shape[3] != KV_DIM:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (pages, heads, page size, {KV_DIM})")
+            _need(t, torch.uint8, k_codes.shape, name)
+        _need(k_scales, torch.float32, k_codes.shape[:2], "k_scales")
+        _need(v_scales, torch.float32, k_codes.shape[:2], "v_scales")
+        _same_device(k_codes.device, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales)
+        cache = cls.__new__(cls)
+        cache._set(k_codes, v_codes, k_scales, v_scales)
+        return cache
+
+    def _set(self, k_codes, v_codes, k_scales, v_scales):
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.num_pages, self.kv_heads, self.page_size = (int(n) for n in k_codes.shape[:3])
+
+    def struct(self) -> _lib.DsaKv8Cache:
+        return _lib.DsaKv8Cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
+                                self.v_scales.data_ptr(), self.num_pages, self.page_size, self.kv_heads, 0)
+
+
+def _batch_device(batch, device):
+    _same_device(device, block_table=batch.block_table, seq_lens=batch.seq_lens, query_start_loc=batch.query_start_loc)
+
+
+def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None):
+    """Append the step's tokens to an 8-bit K/V cache: k, v [rows, kv_heads, 128] bf16 (rows may be strided), row r of
+    the batch at its own position.  A page whose new tokens need a larger scale than it has is re-coded."""
+    k_stride, v_stride = _rows(k, cache.kv_heads, "k"), _rows(v, cache.kv_heads, "v")
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape[0] != batch.num_rows:
+            raise ValueError(f"{name}: {t.shape[0]} rows, expected {batch.num_rows}")
+    dev = cache.k_codes.device
+    _same_device(dev, k=k, v=v)
+    _batch_device(batch, dev)
+    with _on(dev, stream):
+        c, b = cache.struct(), batch.struct()
+        _lib.check(_lib.load().dsa_kv8_append(ctypes.byref(c), ctypes.byref(b), _ptr(k), k_stride, _ptr(v), v_stride,
+                                              _stream(stream)))
+
+
+def paged_attention_workspace_bytes() -> int:
+    return int(_lib.load().dsa_paged_attention_workspace_bytes())
+
+
+def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM ** -0.5, max_query_len: int | None = None,
+                    softcap: float = 0.0, slopes=None, prefix_lens=None, out=None, lse=None, workspace=None, stream=None,
+                    check=False):
+    """Dense attention over an 8-bit K/V cache for decode, verify and prompt rows: q [rows, q_heads, 128] bf16 (rows may
+    be strided); returns (out [rows, q_heads, 128] bf16, lse).  max_query_len is a host bound on the rows of a request
+    (the number of rows where it is not given).  softcap > 0 caps scores by a tanh, slopes [q_heads] fp32 subtracts
+    slopes[h] * distance, prefix_lens [requests] int32 lets every row see the request's first positions.  Rows behind the
+    last request's are not written.  lse (optional) [rows, q_heads] fp32 is filled."""
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (rows, heads, {KV_DIM})")
+    R, heads = batch.num_rows, int(q.shape[1])
+    q_stride = _rows(q, heads, "q")
+    if q.shape[0] != R:
+        raise ValueError(f"q: {q.shape[0]} rows, expected {R}")
+    dev = cache.k_codes.device
+    _same_device(dev, q=q, slopes=slopes, prefix_lens=prefix_lens, out=out, lse=lse, workspace=workspace)
+    _batch_device(batch, dev)
+    mods = None
+    if softcap or slopes is not None or prefix_lens is not None:
+        if slopes is not None:
+            _need(slopes, torch.float32, (heads,), "slopes")
+        if prefix_lens is not None:
+            _need(prefix_lens, torch.int32, (batch.num_requests,), "prefix_lens")
+        mods = ctypes.byref(_lib.DsaAttnMods(float(softcap), 0, 0 if slopes is None else slopes.data_ptr(),
+                                             0 if prefix_lens is None else prefix_lens.data_ptr()))
+    if max_query_len is None:
+        max_query_len = R if batch.query_start_loc is not None else 1
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((R, heads, KV_DIM), dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, torch.bfloat16, (R, heads, KV_DIM), "out")
+        if lse is not None:
+            _need(lse, torch.float32, (R, heads), "lse")
+        if workspace is None:
+            workspace = _workspace(paged_attention_workspace_bytes(), dev)
+        c, b = cache.struct(), batch.struct()
+        _lib.check(_lib.load().dsa_paged_attention(
+            ctypes.byref(c), ctypes.byref(b), _ptr(q), q_stride, heads, float(scale), max(int(max_query_len), 1), mods, _ptr(out),
+            _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        if check:
+            _check_device(workspace, stream)
     return out, lse

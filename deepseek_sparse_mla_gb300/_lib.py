@@ -17,6 +17,7 @@ STATUS_NAMES = {0: "DSA_OK", -1: "DSA_ERR_INVALID_ARG", -2: "DSA_ERR_UNSUPPORTED
                 -4: "DSA_ERR_CUDA", -5: "DSA_ERR_DEVICE_CHECK"}
 # device status bits (dsa_read_status)
 DEVICE_TMA_TIMEOUT, DEVICE_MMA_TIMEOUT, DEVICE_BAD_PAGE, DEVICE_CONFIG = 0x1, 0x2, 0x4, 0x8
+DEVICE_POOL_EMPTY, DEVICE_ROWS_FULL, DEVICE_BAD_LENGTH, DEVICE_POOL_FULL = 0x10, 0x20, 0x40, 0x80
 KEY_BF16, KEY_FP8_E4M3, KEY_INT8 = 0, 1, 2
 LATENT_BF16, LATENT_E4M3 = 0, 1
 
@@ -25,7 +26,9 @@ EXPORTS = ("dsa_abi_version", "dsa_last_error", "dsa_kernel_launches", "dsa_cach
            "dsa_mla_workspace_bytes", "dsa_kv_append", "dsa_indexer_scores_topk", "dsa_indexer_scores_topk_static",
            "dsa_indexer_page_workspace_bytes", "dsa_indexer_page_topk", "dsa_sparse_mla_decode", "dsa_sparse_mla_prefill",
            "dsa_dcp_candidates", "dsa_dcp_select", "dsa_dcp_merge", "dsa_sparse_mla_decode_ragged",
-           "dsa_kv_append_layers", "dsa_read_status", "dsa_check_device_status", "dsa_sparse_mla_decode_layers")
+           "dsa_kv_append_layers", "dsa_read_status", "dsa_check_device_status", "dsa_sparse_mla_decode_layers",
+           "dsa_step_plan", "dsa_pages_release", "dsa_kv8_append", "dsa_paged_attention_workspace_bytes",
+           "dsa_paged_attention")
 
 
 class DsaCache(ctypes.Structure):
@@ -39,6 +42,17 @@ class DsaBatch(ctypes.Structure):
                 ("query_start_loc", ctypes.c_void_p), ("num_requests", ctypes.c_int32),
                 ("num_rows", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
                 ("block_table_stride", ctypes.c_int32)]
+
+
+class DsaKv8Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class DsaAttnMods(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
 
 
 class DsaError(RuntimeError):
@@ -105,6 +119,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                  ctypes.c_float, P, P, P, SZ, P]
     lib.dsa_dcp_merge.restype = I32
     lib.dsa_dcp_merge.argtypes = [P, P, I32, I32, P, P, P]
+    lib.dsa_step_plan.restype = I32
+    lib.dsa_step_plan.argtypes = [P, P, I32, I32, P, I32, P, I32, P, I32, P, P, P, P, P, P, SZ, P]
+    lib.dsa_pages_release.restype = I32
+    lib.dsa_pages_release.argtypes = [P, P, I32, I32, P, I32, I32, P, I32, P, P, SZ, P]
+    lib.dsa_kv8_append.restype = I32
+    lib.dsa_kv8_append.argtypes = [ctypes.POINTER(DsaKv8Cache), ctypes.POINTER(DsaBatch), P, ctypes.c_int64, P,
+                                   ctypes.c_int64, P]
+    lib.dsa_paged_attention_workspace_bytes.restype = SZ
+    lib.dsa_paged_attention_workspace_bytes.argtypes = []
+    lib.dsa_paged_attention.restype = I32
+    lib.dsa_paged_attention.argtypes = [ctypes.POINTER(DsaKv8Cache), ctypes.POINTER(DsaBatch), P, ctypes.c_int64, I32,
+                                        ctypes.c_float, I32, ctypes.POINTER(DsaAttnMods), P, P, P, SZ, P]
     _lib = lib
     return lib
 

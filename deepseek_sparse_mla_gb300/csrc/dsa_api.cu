@@ -227,7 +227,9 @@ dsa_status dsa_check_device_status(uint32_t bits) {
   std::string names;
   const struct { uint32_t bit; const char* name; } known[] = {
       {DSA_DEVICE_TMA_TIMEOUT, "DSA_DEVICE_TMA_TIMEOUT"}, {DSA_DEVICE_MMA_TIMEOUT, "DSA_DEVICE_MMA_TIMEOUT"},
-      {DSA_DEVICE_BAD_PAGE, "DSA_DEVICE_BAD_PAGE"}, {DSA_DEVICE_CONFIG, "DSA_DEVICE_CONFIG"}};
+      {DSA_DEVICE_BAD_PAGE, "DSA_DEVICE_BAD_PAGE"}, {DSA_DEVICE_CONFIG, "DSA_DEVICE_CONFIG"},
+      {DSA_DEVICE_POOL_EMPTY, "DSA_DEVICE_POOL_EMPTY"}, {DSA_DEVICE_ROWS_FULL, "DSA_DEVICE_ROWS_FULL"},
+      {DSA_DEVICE_BAD_LENGTH, "DSA_DEVICE_BAD_LENGTH"}, {DSA_DEVICE_POOL_FULL, "DSA_DEVICE_POOL_FULL"}};
   uint32_t rest = bits;
   for (const auto& k : known)
     if (bits & k.bit) {
@@ -553,6 +555,220 @@ dsa_status dsa_dcp_merge(const void* outs, const float* lses, int32_t world, int
   if (!aligned16(outs) || !aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "dcp_merge: outs/out not 16-byte aligned");
   cudaError_t e = launch_dcp_merge(outs, lses, world, num_rows, out, lse, static_cast<cudaStream_t>(stream));
   return cuda_status(e, "dcp merge launch");
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// an optional 256-byte workspace that holds nothing but the status header
+static dsa_status check_status_workspace(const void* workspace, size_t workspace_bytes) {
+  if (!workspace) return ok();
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(DSA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  if (workspace_bytes < kWorkspaceHeader)
+    return fail(DSA_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes of a status header", workspace_bytes,
+                kWorkspaceHeader);
+  return ok();
+}
+
+dsa_status dsa_step_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_t num_requests, int32_t page_size,
+                         int32_t* block_table, int32_t block_table_stride, const int32_t* free_pages,
+                         int32_t free_capacity, const int32_t* free_count, int32_t num_rows, int32_t* seq_lens_out,
+                         int32_t* query_start_loc, int64_t* slot_mapping, int32_t* positions, int32_t* free_count_out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (num_requests <= 0) return fail(DSA_ERR_INVALID_ARG, "num_requests must be positive");
+  if (num_requests > DSA_MAX_REQUESTS)
+    return fail(DSA_ERR_UNSUPPORTED, "num_requests %d is more than %d", num_requests, DSA_MAX_REQUESTS);
+  if (!pow2(page_size) || page_size > 1024)
+    return fail(DSA_ERR_INVALID_ARG, "page_size must be a power of two in 1..1024 (got %d)", page_size);
+  if (block_table_stride <= 0) return fail(DSA_ERR_INVALID_ARG, "block_table_stride must be positive");
+  if (free_capacity < 0 || num_rows < 0) return fail(DSA_ERR_INVALID_ARG, "free_capacity / num_rows is negative");
+  if (!seq_lens || !new_lens || !block_table || !free_count || !seq_lens_out || !query_start_loc || !free_count_out ||
+      (!free_pages && free_capacity > 0) || (!slot_mapping && num_rows > 0))
+    return fail(DSA_ERR_INVALID_ARG, "a step plan array is NULL");
+  if (!aligned4(seq_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) || !aligned4(free_count) ||
+      !aligned4(seq_lens_out) || !aligned4(query_start_loc) || !aligned4(positions) || !aligned4(free_count_out) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return fail(DSA_ERR_INVALID_ARG, "a step plan array is not aligned to its elements");
+  dsa_status st = check_status_workspace(workspace, workspace_bytes);
+  if (st != DSA_OK) return st;
+  StepPlanArgs a = {};
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.num_requests = num_requests;
+  a.log2_page = ilog2(page_size);
+  a.table_stride = block_table_stride;
+  a.free_capacity = free_capacity;
+  a.num_rows = num_rows;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.seq_lens_out = seq_lens_out;
+  a.query_start_loc = query_start_loc;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.free_count_out = free_count_out;
+  a.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_step_plan(a, (cudaStream_t)stream), "step plan launch");
+}
+
+dsa_status dsa_pages_release(const int32_t* finished, int32_t* seq_lens, int32_t num_requests, int32_t page_size,
+                             int32_t* block_table, int32_t block_table_stride, int32_t num_pages, int32_t* free_pages,
+                             int32_t free_capacity, int32_t* free_count, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (num_requests <= 0) return fail(DSA_ERR_INVALID_ARG, "num_requests must be positive");
+  if (num_requests > DSA_MAX_REQUESTS)
+    return fail(DSA_ERR_UNSUPPORTED, "num_requests %d is more than %d", num_requests, DSA_MAX_REQUESTS);
+  if (!pow2(page_size) || page_size > 1024)
+    return fail(DSA_ERR_INVALID_ARG, "page_size must be a power of two in 1..1024 (got %d)", page_size);
+  if (block_table_stride <= 0 || num_pages <= 0 || free_capacity <= 0)
+    return fail(DSA_ERR_INVALID_ARG, "block_table_stride / num_pages / free_capacity must be positive");
+  if (!finished || !seq_lens || !block_table || !free_pages || !free_count)
+    return fail(DSA_ERR_INVALID_ARG, "a page release array is NULL");
+  if (!aligned4(finished) || !aligned4(seq_lens) || !aligned4(block_table) || !aligned4(free_pages) || !aligned4(free_count))
+    return fail(DSA_ERR_INVALID_ARG, "a page release array is not aligned to its elements");
+  dsa_status st = check_status_workspace(workspace, workspace_bytes);
+  if (st != DSA_OK) return st;
+  PagesReleaseArgs a = {};
+  a.finished = finished;
+  a.seq_lens = seq_lens;
+  a.num_requests = num_requests;
+  a.log2_page = ilog2(page_size);
+  a.table_stride = block_table_stride;
+  a.num_pages = num_pages;
+  a.free_capacity = free_capacity;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.status = static_cast<uint32_t*>(workspace);
+  return cuda_status(launch_pages_release(a, (cudaStream_t)stream), "page release launch");
+}
+
+static dsa_status check_kv8(const dsa_kv8_cache* c) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)
+    return fail(DSA_ERR_INVALID_ARG, "a code or scale array of the cache is NULL");
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes))
+    return fail(DSA_ERR_INVALID_ARG, "cache.k_codes / v_codes is not 16-byte aligned");
+  if (!aligned4(c->k_scales) || !aligned4(c->v_scales))
+    return fail(DSA_ERR_INVALID_ARG, "cache.k_scales / v_scales is not 4-byte aligned");
+  if (c->num_pages <= 0) return fail(DSA_ERR_INVALID_ARG, "cache.num_pages must be positive (got %d)", c->num_pages);
+  if (!pow2(c->page_size) || c->page_size < kKvMinPage || c->page_size > kKvMaxPage)
+    return fail(DSA_ERR_UNSUPPORTED, "cache.page_size must be %d, 32, 64 or %d (got %d)", kKvMinPage, kKvMaxPage, c->page_size);
+  if (c->kv_heads <= 0) return fail(DSA_ERR_INVALID_ARG, "cache.kv_heads must be positive (got %d)", c->kv_heads);
+  if (c->kv_heads > 65535 || (int64_t)c->num_pages * c->kv_heads * c->page_size > (int64_t)INT32_MAX)
+    return fail(DSA_ERR_UNSUPPORTED, "cache holds more than 2^31 rows (pages * heads * page size)");
+  if (c->reserved) return fail(DSA_ERR_INVALID_ARG, "cache.reserved must be 0");
+  return ok();
+}
+
+// rows of heads: 16-byte aligned, with a row stride that keeps them so and does not overlap
+static dsa_status check_rows(const char* name, const void* p, int64_t stride, int heads) {
+  if (!p) return fail(DSA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(p)) return fail(DSA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  if (stride < (int64_t)heads * kKvDim || stride % 8)
+    return fail(DSA_ERR_INVALID_ARG, "%s's row stride %lld must be a multiple of 8 and at least %d heads * %d", name,
+                (long long)stride, heads, kKvDim);
+  return ok();
+}
+
+dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, void* stream) {
+  dsa_status st = check_kv8(cache);
+  if (st != DSA_OK) return st;
+  st = check_batch(batch, false);
+  if (st != DSA_OK) return st;
+  if (batch->num_rows == 0) return ok();
+  st = check_rows("k", k, k_stride, cache->kv_heads);
+  if (st != DSA_OK) return st;
+  st = check_rows("v", v, v_stride, cache->kv_heads);
+  if (st != DSA_OK) return st;
+  if ((int64_t)batch->num_rows + 2 * (int64_t)batch->num_requests > INT32_MAX)
+    return fail(DSA_ERR_UNSUPPORTED, "num_rows / num_requests is too large");
+  Kv8AppendArgs a = {};
+  a.k_codes = static_cast<uint8_t*>(cache->k_codes);
+  a.v_codes = static_cast<uint8_t*>(cache->v_codes);
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  a.num_pages = cache->num_pages;
+  a.log2_page = ilog2(cache->page_size);
+  a.kv_heads = cache->kv_heads;
+  a.block_table = batch->block_table;
+  a.seq_lens = batch->seq_lens;
+  a.query_start_loc = batch->query_start_loc;
+  a.num_requests = batch->num_requests;
+  a.num_rows = batch->num_rows;
+  a.table_stride = batch->block_table_stride;
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  return cuda_status(launch_kv8_append(a, (cudaStream_t)stream), "8-bit K/V append launch");
+}
+
+size_t dsa_paged_attention_workspace_bytes(void) { return plan_paged_attention().workspace_bytes; }
+
+dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
+                               int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,
+                               float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  dsa_status st = check_kv8(cache);
+  if (st != DSA_OK) return st;
+  st = check_batch(batch, false);
+  if (st != DSA_OK) return st;
+  if (batch->num_requests > DSA_MAX_REQUESTS)
+    return fail(DSA_ERR_UNSUPPORTED, "batch.num_requests %d is more than %d", batch->num_requests, DSA_MAX_REQUESTS);
+  if (q_heads <= 0 || q_heads % cache->kv_heads)
+    return fail(DSA_ERR_INVALID_ARG, "q_heads %d is not a multiple of cache.kv_heads %d", q_heads, cache->kv_heads);
+  const int group = q_heads / cache->kv_heads;
+  if (group > DSA_MAX_GROUP)
+    return fail(DSA_ERR_UNSUPPORTED, "%d query heads per K/V head are more than %d", group, DSA_MAX_GROUP);
+  if (!(scale > 0.f) || scale > 1e30f) return fail(DSA_ERR_INVALID_ARG, "scale must be finite and positive");
+  if (max_query_len < 1) return fail(DSA_ERR_INVALID_ARG, "max_query_len must be positive");
+  if (mods) {
+    if (!(mods->softcap >= 0.f) || mods->softcap > 1e30f || (mods->softcap > 0.f && mods->softcap < 1e-30f))
+      return fail(DSA_ERR_INVALID_ARG, "softcap must be 0 or a positive finite number");
+    if (mods->reserved) return fail(DSA_ERR_INVALID_ARG, "mods.reserved must be 0");
+    if (!aligned4(mods->slopes) || !aligned4(mods->prefix_lens))
+      return fail(DSA_ERR_INVALID_ARG, "slopes / prefix_lens is not 4-byte aligned");
+  }
+  if (batch->num_rows == 0) return ok();
+  st = check_rows("q", q, q_stride, q_heads);
+  if (st != DSA_OK) return st;
+  if (!out) return fail(DSA_ERR_INVALID_ARG, "out is NULL");
+  if (!aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "out is not 16-byte aligned");
+  if (!aligned4(lse)) return fail(DSA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  if ((int64_t)batch->num_rows * q_heads > INT32_MAX / 2)
+    return fail(DSA_ERR_UNSUPPORTED, "num_rows * q_heads is too large");
+  const PagedAttnPlan plan = plan_paged_attention();
+  if (!workspace || workspace_bytes < plan.workspace_bytes)
+    return fail(DSA_ERR_WORKSPACE,
+                "workspace of %zu bytes is smaller than the %zu bytes dsa_paged_attention_workspace_bytes requires",
+                workspace_bytes, plan.workspace_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(DSA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  PagedAttnArgs a = {};
+  a.block_table = batch->block_table;
+  a.seq_lens = batch->seq_lens;
+  a.query_start_loc = batch->query_start_loc;
+  a.num_requests = batch->num_requests;
+  a.num_rows = batch->num_rows;
+  a.table_stride = batch->block_table_stride;
+  a.num_pages = cache->num_pages;
+  a.log2_page = ilog2(cache->page_size);
+  a.kv_heads = cache->kv_heads;
+  a.group = group;
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.cap_log2 = mods ? mods->softcap * 1.4426950408889634f : 0.f;
+  a.slopes = mods ? mods->slopes : nullptr;
+  a.prefix_lens = mods ? mods->prefix_lens : nullptr;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  return cuda_status(launch_paged_attention(a, static_cast<const uint8_t*>(cache->k_codes),
+                                            static_cast<const uint8_t*>(cache->v_codes),
+                                            batch->query_start_loc ? max_query_len : 1, workspace, plan,
+                                            (cudaStream_t)stream),
+                     "paged attention launch");
 }
 
 }  // extern "C"

@@ -206,6 +206,82 @@ cudaError_t launch_dcp_merge(const void* outs, const float* lses, int world, int
                              cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// the step planner, and the dense layer's 8-bit K/V cache
+// ---------------------------------------------------------------------------
+constexpr int kKvDim = DSA_KV_DIM;                 // 128
+constexpr int kKvMinPage = 16, kKvMaxPage = 128;   // tokens of a page of the 8-bit K/V cache
+constexpr int kPlanMaxRequests = DSA_MAX_REQUESTS; // sums over the requests are kept in shared memory
+
+struct StepPlanArgs {
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t num_requests, log2_page, table_stride, free_capacity, num_rows;
+  int32_t* block_table;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* seq_lens_out;
+  int32_t* query_start_loc;
+  int64_t* slot_mapping;
+  int32_t* positions;        // optional
+  int32_t* free_count_out;
+  uint32_t* status;          // optional: a workspace header
+};
+cudaError_t launch_step_plan(const StepPlanArgs& a, cudaStream_t s);
+
+struct PagesReleaseArgs {
+  const int32_t* finished;
+  int32_t* seq_lens;
+  int32_t num_requests, log2_page, table_stride, num_pages, free_capacity;
+  int32_t* block_table;
+  int32_t* free_pages;
+  int32_t* free_count;
+  uint32_t* status;          // optional: a workspace header
+};
+cudaError_t launch_pages_release(const PagesReleaseArgs& a, cudaStream_t s);
+
+struct Kv8AppendArgs {
+  uint8_t *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+  int32_t num_pages, log2_page, kv_heads;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;   // nullptr: one row per request
+  int32_t num_requests, num_rows, table_stride;
+  const void *k, *v;
+  int64_t k_stride, v_stride;       // elements between tokens
+};
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s);
+
+// Dense attention over the 8-bit K/V cache (see paged_attention.cu).
+struct PagedAttnArgs {
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;   // nullptr: one row per request
+  int32_t num_requests, num_rows, table_stride;
+  int32_t num_pages, log2_page, kv_heads, group;   // group = query heads per K/V head
+  const float *k_scales, *v_scales;
+  const __nv_bfloat16* q;
+  int64_t q_stride;                 // elements between rows
+  float scale_log2;                 // softmax scale * log2(e)
+  float cap_log2;                   // score cap * log2(e), 0: none
+  const float* slopes;              // [query heads] distance bias, or nullptr
+  const int32_t* prefix_lens;       // [requests] positions that every row sees, or nullptr
+  __nv_bfloat16* out;
+  float* lse;
+  uint32_t* err;                    // the workspace header
+  int32_t* rec;                     // [ctas][4]: where each CTA's first piece lies
+  float* part_o;                    // [2 * ctas][columns][128]
+  float* part_ml;                   // [2 * ctas][columns][2]
+};
+constexpr int kPagedAttnColumns = 32;     // (row, head) pairs of a K/V head taken together, at most
+struct PagedAttnPlan {
+  size_t rec_offset, part_offset, workspace_bytes;
+};
+PagedAttnPlan plan_paged_attention();
+cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_query_len,
+                                   void* workspace, const PagedAttnPlan& plan, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // device helpers
 // ---------------------------------------------------------------------------
 // Request and absolute position of query row r: row i of request b sits at L_b - q_len_b + i.

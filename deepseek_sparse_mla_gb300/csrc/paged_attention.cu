@@ -1,0 +1,880 @@
+// Dense grouped-head attention over the paged 8-bit K/V cache, on tcgen05 tensor cores.
+//
+//   z_s = scale * q[r,h] . (k_code_s * ks)        [then the cap and the distance bias]
+//   out[r,h] = sum_s softmax(z)_s * (v_code_s * vs),   lse[r,h] = ln sum_s exp(z_s)
+// with one scale ks, vs per page and K/V head, and q bf16.
+//
+// The codes go to the tensor cores as they are (kind::f8f6f4), so nothing is expanded on chip, and the
+// other operand is split into two e4m3 terms to keep its bits:
+//   x = (hi + lo / 16) * 2^k,  hi = e4m3(x / 2^k),  lo = e4m3(16 (x / 2^k - hi)).
+// e4m3 has 4 significant bits, so hi leaves a remainder of at most 2^-4 of x, which fits lo: bf16's 8 bits
+// are kept exactly for values down to 2^-14 of the row's largest, and a probability keeps 8 bits or more
+// (its remainder is rounded to 4 bits), with an absolute step of 2^-20 of the largest contribution.
+// hi and lo are separate columns of the small operand and are added in fp32 after the products, which
+// costs nothing: the large operand (128 keys, or 128 value dims) sets the time of these MMAs.
+//
+// A (row, head) pair of one request and K/V head is a column; up to 32 are taken together:
+//   S^T [128 keys x columns]  = K [128 x 128] (K-major)   * Q^T          (M = 128, N = 2 x columns, K = 128)
+//   O^T [128 dims x columns] += V^T (the same tile layout, MN-major) * P^T
+// A thread of the softmax warpgroup holds one key's scores, so masks, scales and page lookups are per
+// thread, and a column's maximum is one warp-wide redux.
+//
+// The v scale would be lost in P's 8 bits if pages differ, so P' = p * vs is what is coded, against a
+// running maximum of its own (of z + log2 vs), next to the softmax's maximum that the denominator uses.
+// Both maxima move only when exceeded by 2^2, and the accumulator in TMEM is then rescaled.
+//
+// Work: (request, K/V head, column group, tile of 128 keys) units, laid out in that order and split into one
+// contiguous range per CTA (persistent, one CTA per SM).  A segment (all tiles of one request, head and
+// group) inside one CTA is written directly; one that is cut leaves fp32 pieces that a second kernel joins.
+//
+// Per CTA (8 warps): warp 0 looks pages up and issues TMA loads into a ring of 32 KB stages (K and V of
+// a tile); warp 1 issues the MMAs; warps 2-3 split the next segment's queries; warps 4-7 are the softmax.
+#include "dsa_internal.cuh"
+#include "sm100.cuh"
+#include "tmap.cuh"
+
+namespace dsa {
+using namespace sm100;
+
+namespace pa {
+constexpr int kTok = 128;                       // keys per tile
+constexpr int kTileBytes = kTok * kKvDim;       // 16 KB of codes
+constexpr int kStageBytes = 2 * kTileBytes;     // K, then V
+constexpr int kStages = 5;
+constexpr int kColMax = kPagedAttnColumns;
+constexpr int kQBytes = 2 * kColMax * kKvDim;   // hi and lo rows of 32 columns
+constexpr int kPBytes = kTok * 2 * kColMax;
+constexpr int kMaxPages = kTok / kKvMinPage;    // pages of a tile
+constexpr int kThreads = 256;
+constexpr int kMmaWarp = 1, kQWarp0 = 2, kSoftWarp0 = 4;
+constexpr uint32_t kTmemCols = 256;             // S^T of parity b at 64 b, O^T of parity b at 128 + 64 b
+constexpr uint32_t kColO = 128;
+constexpr float kSlack = 2.f;                   // log2 by which a maximum may be exceeded
+constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
+constexpr uint32_t kPolls = 1u << 22;
+constexpr int kFixedSmem = kStages * kStageBytes + 2 * kQBytes + 2 * kPBytes + 1024;
+}  // namespace pa
+
+// Units of request b: column groups * key tiles (times K/V heads)
+struct PaShape {
+  int rows, groups, tiles, len;
+};
+
+// rows of request b, its first row, and the keys it may read
+__device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, int cols, int max_rows, int& row0, uint32_t& bits) {
+  PaShape s = {0, 0, 0, 0};
+  int n = 1;
+  row0 = b;
+  if (a.query_start_loc) {
+    row0 = a.query_start_loc[b];
+    const int64_t d = (int64_t)a.query_start_loc[b + 1] - row0;
+    if (d <= 0 || row0 < 0 || row0 + d > a.num_rows) return s;
+    if (d > max_rows) {
+      bits |= DSA_DEVICE_BAD_LENGTH;
+      return s;
+    }
+    n = (int)d;
+  }
+  const int64_t room = (int64_t)a.table_stride << a.log2_page;
+  int64_t len = max(a.seq_lens[b], 0);
+  if (len > room) {
+    bits |= DSA_DEVICE_BAD_PAGE;
+    len = room;
+  }
+  s.rows = n;
+  s.len = (int)len;
+  s.groups = (int)(((int64_t)n * a.group + cols - 1) / cols);
+  s.tiles = max(1, (int)((len + pa::kTok - 1) / pa::kTok));
+  return s;
+}
+
+// A run of tiles of one segment
+struct PaSeg {
+  int b, h, cg, tile, n;       // first tile and number of tiles of this piece
+  int rows, row0, len, tiles;
+};
+
+// The segment that unit u lies in, cut at u1.  end[b] = column groups * tiles of requests 0 .. b.
+__device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_t* end, int cols, int64_t u, int64_t u1) {
+  int lo = 0, hi = a.num_requests - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)end[mid] * a.kv_heads > u) hi = mid;
+    else lo = mid + 1;
+  }
+  PaSeg s;
+  s.b = lo;
+  const int first = lo ? end[lo - 1] : 0;
+  uint32_t none = 0;
+  const PaShape sh = pa_shape(a, lo, cols, INT32_MAX, s.row0, none);
+  s.rows = sh.rows;
+  s.len = sh.len;
+  s.tiles = sh.tiles;
+  const int64_t in = u - (int64_t)first * a.kv_heads;
+  const int per_head = end[lo] - first;
+  s.h = (int)(in / per_head);
+  const int rest = (int)(in - (int64_t)s.h * per_head);
+  s.cg = rest / sh.tiles;
+  s.tile = rest - s.cg * sh.tiles;
+  s.n = (int)min((int64_t)(sh.tiles - s.tile), u1 - u);
+  return s;
+}
+
+__device__ __forceinline__ int64_t pa_unit_start(int c, int64_t units, int ctas) { return units * c / ctas; }
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_ld_cols<8>(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) tmem_ld_cols<8>(taddr + i, r + i);
+}
+
+// two e4m3 codes of (a, b), and of 16 times what they leave
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
+  const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+  lo = __nv_cvt_float2_to_fp8x2(make_float2(16.f * (a - back.x), 16.f * (b - back.y)), __NV_SATFINITE, __NV_E4M3);
+}
+
+// What the query warps leave about a segment's columns
+struct PaColumns {
+  float factor[pa::kColMax];    // 2^k of the split query * softmax scale * log2 e
+  int limit[pa::kColMax];       // keys below it are seen
+  int pos[pa::kColMax];
+  float slope[pa::kColMax];     // * log2 e
+  int min_limit[2];             // over each query warp's columns
+};
+
+// kCE columns (8, 16 or 32); kMods: score cap and distance bias compiled in
+template <int kCE, bool kMods>
+__global__ void __launch_bounds__(pa::kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                           const __grid_constant__ PagedAttnArgs a, int max_rows, int shared_keys) {
+  using namespace pa;
+  constexpr int kHalf = kCE < 16 ? 16 : kCE;          // columns of the hi half (and of the lo half)
+  constexpr int kN = 2 * kHalf;                       // MMA N: 32 or 64
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = smem;
+  uint8_t* sQ = sKV + kStages * kStageBytes;
+  uint8_t* sP = sQ + 2 * kQBytes;
+  int32_t* end = reinterpret_cast<int32_t*>(sP + 2 * kPBytes);   // [requests]
+
+  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], s_full[2], s_empty[2], p_full[2], p_empty[2];
+  __shared__ uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2], mma_done;
+  __shared__ float sks[kStages][kMaxPages], svs[kStages][kMaxPages];
+  __shared__ uint32_t sbad[kStages];
+  __shared__ __align__(16) PaColumns cols[2];
+  __shared__ float wmax[2][4][kCE], wlv[2][4], red[4][kCE], fin[kCE];
+  __shared__ uint32_t nan_keys[4];
+  __shared__ int32_t scan[kThreads / 32];
+  __shared__ uint32_t tmem_base, bits_all;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+      mbar_init(&p_full[i], 1);
+      mbar_init(&p_empty[i], 1);
+      mbar_init(&q_full[i], 2);
+      mbar_init(&q_empty[i], 5);          // the last product that reads it, and four softmax warps
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], 4);
+    }
+    mbar_init(&mma_done, 1);
+    bits_all = 0;
+    fence_mbar_init();
+    prefetch_tmap(&k_map);
+    prefetch_tmap(&v_map);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  if (kCE < kHalf)                                     // columns that no query fills stay zero
+    for (int i = tid; i < 2 * kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+  pdl_wait();
+  // running sums of the requests' units: every thread a run of consecutive requests
+  {
+    uint32_t bits = 0;
+    const int B = a.num_requests, per = (B + kThreads - 1) / kThreads;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      int row0;
+      const PaShape s = pa_shape(a, b, kCE, max_rows, row0, bits);
+      sum += s.groups * s.tiles;
+      end[b] = sum;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    for (int b = b0; b < b1; ++b) end[b] += before;
+    if (bits) atomicOr(&bits_all, bits);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const int64_t units = (int64_t)end[a.num_requests - 1] * a.kv_heads;
+  const int64_t u0 = pa_unit_start(cta, units, ctas), u1 = pa_unit_start(cta + 1, units, ctas);
+  uint32_t* const err = &bits_all;                    // this CTA's status bits, stored at the end
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
+    const int lp = a.log2_page, ppt = kTok >> lp;
+    const uint32_t page_bytes = (uint32_t)kKvDim << lp;
+    int i = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      const int pages = (s.len + (1 << lp) - 1) >> lp;
+      int batch = -1, page = -1;                       // 32 pages at a time, one a lane
+      float ks = 0.f, vs = 0.f;
+      for (int t = 0; t < s.n && ok; ++t, ++i) {
+        const int p0 = (s.tile + t) * ppt;
+        if ((p0 >> 5) != batch) {
+          batch = p0 >> 5;
+          const int p = 32 * batch + lane;
+          page = -1;
+          ks = vs = 0.f;
+          if (p < pages) {
+            page = a.block_table[(int64_t)s.b * a.table_stride + p];
+            if (page < 0 || page >= a.num_pages) {
+              atomicOr(err, kErrBadPage);
+              page = -1;
+            }
+          }
+          if (page >= 0) {
+            ks = a.k_scales[(int64_t)page * a.kv_heads + s.h];
+            vs = a.v_scales[(int64_t)page * a.kv_heads + s.h];
+          }
+        }
+        const int st = i % kStages, use = i / kStages;
+        if (use > 0 && !mbar_wait(&kv_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) {
+          ok = false;
+          break;
+        }
+        // this tile's pages sit in lanes o .. o + ppt - 1; lanes 0 .. ppt - 1 load K, 16 .. 16 + ppt - 1 V
+        const int o = p0 & 31, mine = lane & 15;
+        const int pg = __shfl_sync(0xffffffffu, page, (o + mine) & 31);
+        const float k1 = __shfl_sync(0xffffffffu, ks, (o + mine) & 31), v1 = __shfl_sync(0xffffffffu, vs, (o + mine) & 31);
+        const bool load = mine < ppt && pg >= 0;
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+        const uint32_t bad = __ballot_sync(0xffffffffu, mine < ppt && pg < 0) & 0xFFFFu;
+        if (lane < ppt) {
+          sks[st][lane] = k1;
+          svs[st][lane] = v1;
+        }
+        if (lane == 0) sbad[st] = bad;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], loads * page_bytes);
+        __syncwarp();
+        if (load)
+          tma_load_2d_hint(sKV + st * kStageBytes + (lane >> 4) * kTileBytes + mine * page_bytes,
+                           lane < 16 ? &k_map : &v_map, 0, (pg * a.kv_heads + s.h) << lp, &kv_full[st], policy);
+      }
+      u += s.n;
+    }
+    // nothing may still be landing in shared memory when the CTA exits
+    for (int st = 0; st < kStages; ++st) {
+      const int uses = (i - st + kStages - 1) / kStages;
+      if (i > st) mbar_wait(&kv_full[st], (uses - 1) & 1, err, kErrTmaTimeout, kPolls);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t id_qk = idesc_e4m3(kTok, kN);
+      const uint32_t id_pv = idesc_e4m3(kKvDim, kN) | (1u << 15) | (1u << 16);   // both operands MN-major
+      constexpr SmemSwizzle kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
+      const uint64_t d_k = smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
+      const uint64_t d_v = smem_desc(smem_u32(sKV + kTileBytes), 16, 1024, kSwizzle128B);
+      const uint64_t d_q = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+      const uint64_t d_p = smem_desc(smem_u32(sP), 16, 8 * kN, kPSwizzle);
+      const int n_tiles = (int)(u1 - u0);
+      // segments are walked twice: by the scores (iq, ahead by one tile) and by the outputs (ip)
+      int64_t uq = u0, up = u0;
+      int q_left = 0, p_left = 0, q_seg = -1, p_seg = -1;
+      bool ok = true, p_first = false;
+      for (int step = 0; step <= n_tiles && ok; ++step) {
+        if (step < n_tiles) {
+          const int i = step, st = i % kStages, sb = i & 1;
+          if (q_left == 0) {
+            const PaSeg s = pa_segment(a, end, kCE, uq, u1);
+            q_left = s.n;
+            uq += s.n;
+            ++q_seg;
+            ok = mbar_wait(&q_full[q_seg & 1], (q_seg >> 1) & 1, err, kErrMmaTimeout, kPolls);
+          }
+          ok = ok && mbar_spin(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout);
+          if (ok && i >= 2) ok = mbar_spin(&s_empty[sb], ((i >> 1) - 1) & 1, err, kErrMmaTimeout);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t k = d_k + (uint64_t)((st * kStageBytes) >> 4), q = d_q + (uint64_t)(((q_seg & 1) * kQBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kKvDim / 32; ++kk) mma_ss_f8(tmem + 64 * sb, k + 2 * kk, q + 2 * kk, id_qk, kk > 0);
+          mma_commit(&s_full[sb]);
+          if (--q_left == 0) mma_commit(&q_empty[q_seg & 1]);
+        }
+        if (step > 0) {
+          const int i = step - 1, st = i % kStages, pb = i & 1;
+          if (p_left == 0) {
+            const PaSeg s = pa_segment(a, end, kCE, up, u1);
+            p_left = s.n;
+            up += s.n;
+            ++p_seg;
+            p_first = true;
+            if (p_seg >= 2) ok = mbar_wait(&o_empty[p_seg & 1], ((p_seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+          }
+          ok = ok && mbar_spin(&p_full[pb], (i >> 1) & 1, err, kErrMmaTimeout);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v = d_v + (uint64_t)((st * kStageBytes) >> 4), p = d_p + (uint64_t)((pb * kPBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 32; ++kk)
+            mma_ss_f8(tmem + kColO + 64 * (p_seg & 1), v + (uint64_t)((kk * 32 * kKvDim) >> 4),
+                      p + (uint64_t)((kk * 32 * kN) >> 4), id_pv, !p_first || kk > 0);
+          p_first = false;
+          mma_commit(&kv_empty[st]);
+          mma_commit(&p_empty[pb]);
+          if (--p_left == 0) mma_commit(&o_full[p_seg & 1]);
+        }
+      }
+      // every MMA issued here has finished before TMEM is released
+      mma_commit(&mma_done);
+      mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+    }
+  } else if (warp < kSoftWarp0) {
+    // ---------------------------------------------------------------- queries: 16 threads a column
+    const int qw = warp - kQWarp0, part = lane & 15;
+    int seg = 0;
+    for (int64_t u = u0; u < u1; ++seg) {
+      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      u += s.n;
+      const int buf = seg & 1;
+      if (seg >= 2 && !mbar_wait(&q_empty[buf], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      uint8_t* q_hi = sQ + buf * kQBytes;
+      PaColumns& cm = cols[buf];
+      const int pairs = s.rows * a.group, prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
+      const int start = a.seq_lens[s.b] - s.rows;     // position of row 0
+      uint4 x[kCE / 4];
+#pragma unroll
+      for (int it = 0; it < kCE / 4; ++it) {
+        const int n = s.cg * kCE + 4 * it + 2 * qw + (lane >> 4);
+        x[it] = make_uint4(0, 0, 0, 0);
+        if (n < pairs) {
+          const int i = n / a.group, g = n - i * a.group;
+          x[it] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (s.h * a.group + g) * kKvDim + 8 * part);
+        }
+      }
+      int low = INT32_MAX;
+#pragma unroll
+      for (int it = 0; it < kCE / 4; ++it) {
+        const int c = 4 * it + 2 * qw + (lane >> 4), n = s.cg * kCE + c;
+        const uint32_t w[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+        uint32_t top = 0;                             // largest finite |x|, as bf16 bits
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t p = w[e] & 0x7FFFu, r = (w[e] >> 16) & 0x7FFFu;
+          if (p < 0x7F80u) top = max(top, p);
+          if (r < 0x7F80u) top = max(top, r);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
+        const int E = max((int)(top >> 7) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
+          const uint32_t wl = w[e] << 16, wh = w[e] & 0xFFFF0000u;
+          const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
+          const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
+          split2(xl, xh, hi[e], lo[e]);
+        }
+        const uint32_t at = (((part >> 1) ^ (c & 7)) << 4) + 8 * (part & 1);
+        *reinterpret_cast<uint2*>(q_hi + c * kKvDim + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2*>(q_hi + (kHalf + c) * kKvDim + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        const int i = n / a.group;
+        const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
+        if (n < pairs) low = min(low, limit);
+        if (part == 0) {
+          // 2^(E - 7) is exact; a column past the last pair sees everything and is not written
+          cm.factor[c] = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;
+          cm.limit[c] = n < pairs ? limit : INT32_MAX;
+          cm.pos[c] = pos;
+          cm.slope[c] = kMods && a.slopes && n < pairs ? a.slopes[s.h * a.group + (n - i * a.group)] * 1.4426950408889634f : 0.f;
+        }
+      }
+      low = __reduce_min_sync(0xffffffffu, low);
+      if (lane == 0) cm.min_limit[qw] = low;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[buf]);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax and outputs: one key a thread
+    const int quarter = warp & 3, row = 32 * quarter + lane;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    int i = 0, seg = 0;
+    for (int64_t u = u0; u < u1; ++seg) {
+      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      u += s.n;
+      const int qb = seg & 1;
+      if (!mbar_wait(&q_full[qb], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      const PaColumns& cm = cols[qb];
+      const int min_limit = min(cm.min_limit[0], cm.min_limit[1]);
+      // the references of column `lane` (m: of z, mv: of z + log2 vs), and every column's in registers
+      float m_lane = -INFINITY, mv_lane = -INFINITY;
+      float m[kCE], e[kCE], l[kCE];
+#pragma unroll
+      for (int c = 0; c < kCE; ++c) {
+        m[c] = 0.f;
+        e[c] = kPOne;
+        l[c] = 0.f;
+      }
+      uint32_t poison = 0;                             // columns whose output at dim `row` is NaN
+      bool ok = true;
+      for (int t = 0; t < s.n; ++t, ++i) {
+        const int st = i % kStages, sb = i & 1;
+        const int key0 = (s.tile + t) * kTok, j = key0 + row;
+        ok = mbar_wait(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
+             mbar_wait(&s_full[sb], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
+        if (!ok) break;
+        tc_fence_after();
+        float z[kCE];
+        const int pg = row >> a.log2_page;
+        const float ks = sks[st][pg], vs = svs[st][pg];
+        {
+          uint32_t hi[kCE], lo[kCE];
+          tmem_ld_cols<kCE>(tmem + lanes + 64 * sb, hi);
+          tmem_ld_cols<kCE>(tmem + lanes + 64 * sb + kHalf, lo);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[sb]);
+#pragma unroll
+          for (int c = 0; c < kCE; ++c)
+            z[c] = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c]);
+        }
+        if (kMods) {
+          if (a.cap_log2 > 0.f) {
+            // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap))), in log2 units throughout
+            const float in = 2.f * 1.4426950408889634f / a.cap_log2;
+#pragma unroll
+            for (int c = 0; c < kCE; ++c) {
+              const float x = z[c] * in;
+              z[c] = a.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(x > 64.f ? 64.f : x)));   // NaN stays
+            }
+          }
+          if (a.slopes) {
+#pragma unroll
+            for (int c = 0; c < kCE; ++c) z[c] -= cm.slope[c] * (float)abs(cm.pos[c] - j);
+          }
+        }
+        const bool masked = key0 + kTok > min_limit || sbad[st] != 0;      // uniform in the CTA
+        bool has_nan = false;
+        if (masked) {
+          const bool exists = j < s.len && !((sbad[st] >> pg) & 1u);
+#pragma unroll
+          for (int c = 0; c < kCE; ++c)
+            if (!exists || j >= cm.limit[c]) z[c] = -INFINITY;
+          // A key's values meet a probability of 0 where it is not seen, and 0 * NaN is NaN: what lies behind
+          // the request's tokens is zeroed here, and NaN codes of keys that only some columns see are
+          // taken out below.
+          uint4* vrow = reinterpret_cast<uint4*>(sKV + st * kStageBytes + kTileBytes + row * kKvDim);
+          if (!exists) {
+#pragma unroll
+            for (int q = 0; q < kKvDim / 16; ++q) vrow[q] = make_uint4(0, 0, 0, 0);
+          } else if (j >= min_limit) {
+            uint32_t hit = 0;
+            for (int q = 0; q < kKvDim / 16; ++q) {
+              const uint4 w = vrow[q];
+              hit |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                     ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+            }
+            has_nan = (hit & 0x80808080u) != 0;
+          }
+        }
+        // column maxima over the tile: lane c of every warp ends up with column c's
+        float mine = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kCE; ++c) {
+          const float r = warp_max_f32(z[c]);
+          if (lane == c) mine = r;
+        }
+        const float lv = fmaxf(__log2f(fabsf(vs)), -126.f);
+        const float lv_max = warp_max_f32(lv);
+        if (lane < kCE) wmax[sb][quarter][lane] = mine;
+        if (lane == 0) wlv[sb][quarter] = lv_max;
+        const bool any_nan = named_bar_or(1, 128, has_nan);
+        float M = -INFINITY, MV = -INFINITY;
+        if (lane < kCE) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float x = wmax[sb][w][lane];
+            M = fmaxf(M, x);
+            MV = fmaxf(MV, x + wlv[sb][w]);
+          }
+        }
+        const bool grow = M > m_lane + kSlack || MV > mv_lane + kSlack || (m_lane == -INFINITY && M > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {             // the same in all four warps
+          const float m_new = fmaxf(m_lane, M), mv_new = fmaxf(mv_lane, MV);
+          const float al = m_lane == -INFINITY ? 0.f : ex2_approx(m_lane - m_new);
+          const float ao = mv_lane == -INFINITY ? 0.f : ex2_approx(mv_lane - mv_new);
+          const float e_new = mv_new == -INFINITY ? kPOne : ex2_approx(m_new - mv_new) * kPOne;
+          m_lane = m_new;
+          mv_lane = mv_new;
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;
+#pragma unroll
+          for (int c = 0; c < kCE; ++c) {
+            l[c] *= __shfl_sync(0xffffffffu, al, c);
+            m[c] = __shfl_sync(0xffffffffu, m_use, c);
+            e[c] = __shfl_sync(0xffffffffu, e_new, c);
+          }
+          if (t > 0) {
+            // the accumulator is settled once the previous tile's product has completed
+            ok = mbar_wait(&p_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, err, kErrMmaTimeout, kPolls);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t o = tmem + lanes + kColO + 64 * qb;
+#pragma unroll
+            for (int c0 = 0; c0 < kCE; c0 += 8) {
+              uint32_t r[16];
+              tmem_ld_cols<8>(o + c0, r);
+              tmem_ld_cols<8>(o + kHalf + c0, r + 8);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float f = __shfl_sync(0xffffffffu, ao, c0 + c);
+                r[c] = __float_as_uint(__uint_as_float(r[c]) * f);
+                r[8 + c] = __float_as_uint(__uint_as_float(r[8 + c]) * f);
+              }
+              tmem_st8(o + c0, r);
+              tmem_st8(o + kHalf + c0, r + 8);
+            }
+            tmem_wait_st();
+          }
+        }
+        if (any_nan) {
+          const uint32_t who = __ballot_sync(0xffffffffu, has_nan);
+          if (lane == 0) nan_keys[quarter] = who;
+          named_bar_sync(1, 128);
+          const uint8_t* vt = sKV + st * kStageBytes + kTileBytes;
+          for (int w = 0; w < 4; ++w)
+            for (uint32_t left = nan_keys[w]; left; left &= left - 1) {
+              const int k = 32 * w + __ffs(left) - 1;
+              const uint8_t code = vt[k * kKvDim + ((((uint32_t)row >> 4) ^ (k & 7)) << 4) + (row & 15)];
+              if ((code & 0x7Fu) == 0x7Fu)
+                for (int c = 0; c < kCE; ++c)
+                  if (key0 + k < cm.limit[c]) poison |= 1u << c;
+            }
+          named_bar_sync(1, 128);
+          if (has_nan) {
+            uint32_t* vrow = reinterpret_cast<uint32_t*>(sKV + st * kStageBytes + kTileBytes + row * kKvDim);
+            for (int q = 0; q < kKvDim / 4; ++q) {
+              const uint32_t w = vrow[q], f = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of NaN bytes
+              vrow[q] = w & ~((f >> 7) * 0xFFu);
+            }
+          }
+        }
+        // the probabilities, and their contributions in two e4m3 terms
+        uint32_t hi[kHalf / 4], lo[kHalf / 4];
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 4) {
+          if (c >= kCE) {
+            hi[c / 4] = lo[c / 4] = 0;
+            continue;
+          }
+          float x[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float p = ex2_approx(z[c + q] - m[c + q]);
+            l[c + q] += p;
+            x[q] = p * (vs * e[c + q]);
+          }
+          uint32_t h0, l0, h1, l1;
+          split2(x[0], x[1], h0, l0);
+          split2(x[2], x[3], h1, l1);
+          hi[c / 4] = h0 | h1 << 16;
+          lo[c / 4] = l0 | l1 << 16;
+        }
+        // the buffer is free once the product two tiles back has completed
+        if (i >= 2) {
+          ok = mbar_wait(&p_empty[sb], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+          if (!ok) break;
+        }
+        uint8_t* prow = sP + sb * kPBytes + row * kN;
+        const int sw = kN == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+#pragma unroll
+        for (int q = 0; q < kHalf / 16; ++q) {
+          *reinterpret_cast<uint4*>(prow + ((q ^ sw) << 4)) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+          *reinterpret_cast<uint4*>(prow + (((q + kHalf / 16) ^ sw) << 4)) =
+              make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        named_bar_sync(1, 128);
+        if (row == 0) mbar_arrive(&p_full[sb]);
+      }
+      if (!ok) break;
+      // ---- the segment's end: denominators, then O^T out of TMEM (this thread: dim `row` of every column)
+#pragma unroll
+      for (int c = 0; c < kCE; ++c) {
+        float v = l[c];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) red[quarter][c] = v;
+      }
+      named_bar_sync(1, 128);
+      const bool whole = s.n == s.tiles;
+      const int pairs = s.rows * a.group;
+      // a piece that starts its segment is its CTA's last unless it also starts the CTA's range
+      const int slot = u - s.n == u0 ? 2 * cta : 2 * cta + 1;
+      if (quarter == 0 && lane < kCE) {
+        const float L = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        const float back = 1.f / (mv_lane == -INFINITY ? kPOne : ex2_approx(m_lane - mv_lane) * kPOne);
+        const bool any = L > 0.f || L != L;
+        fin[lane] = !any ? 0.f : whole ? back / L : back;
+        const int n = s.cg * kCE + lane;
+        if (whole) {
+          if (a.lse && n < pairs) {
+            const int r = n / a.group;
+            a.lse[(int64_t)(s.row0 + r) * a.kv_heads * a.group + s.h * a.group + (n - r * a.group)] =
+                any ? (m_lane + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+          }
+        } else {
+          float* ml = a.part_ml + ((int64_t)slot * kColMax + lane) * 2;
+          ml[0] = m_lane;
+          ml[1] = L;
+        }
+      }
+      if (row == 0 && u - s.n == u0) {                   // for the join: this CTA's first piece
+        int32_t* rec = a.rec + 4 * cta;
+        rec[0] = s.b;
+        rec[1] = s.h;
+        rec[2] = s.cg;
+        rec[3] = s.tile;
+      }
+      named_bar_sync(1, 128);
+      if (!mbar_wait(&o_full[qb], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      tc_fence_after();
+      const uint32_t o = tmem + lanes + kColO + 64 * qb;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kCE; c0 += 8) {
+        uint32_t r[16];
+        tmem_ld_cols<8>(o + c0, r);
+        tmem_ld_cols<8>(o + kHalf + c0, r + 8);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int n = s.cg * kCE + c0 + c;
+          if (n >= pairs) break;
+          const float f = fin[c0 + c];
+          float v = fmaf(__uint_as_float(r[8 + c]), 0.0625f, __uint_as_float(r[c])) * f;
+          if (f == 0.f) v = 0.f;                       // nothing seen: the accumulator holds nothing of it
+          if ((poison >> (c0 + c)) & 1u) v = __int_as_float(0x7FC00000);
+          if (whole) {
+            const int i2 = n / a.group;
+            a.out[((int64_t)(s.row0 + i2) * a.kv_heads * a.group + s.h * a.group + (n - i2 * a.group)) * kKvDim + row] =
+                __float2bfloat16_rn(v);
+          } else {
+            a.part_o[((int64_t)slot * kColMax + c0 + c) * kKvDim + row] = v;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&o_empty[qb]);
+        mbar_arrive(&q_empty[qb]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid == 0) {
+    a.err[kStatusCtaWords + cta] = bits_all;
+    if (cta == 0) {
+      a.err[0] = 0;
+      a.err[1] = (uint32_t)ctas;
+      *reinterpret_cast<int64_t*>(a.err + 2) = units;
+    }
+  }
+}
+
+__device__ __forceinline__ int pa_cta_of_unit(int64_t u, int64_t units, int ctas) {
+  int c = (int)(u * ctas / units);
+  while (c + 1 < ctas && pa_unit_start(c + 1, units, ctas) <= u) ++c;
+  while (c > 0 && pa_unit_start(c, units, ctas) > u) --c;
+  return c;
+}
+
+// Joins the pieces of the segments that CTA boundaries cut:
+//   out = sum_p w_p O_p,  w_p = 2^{m_p - M} / L,  L = sum_p 2^{m_p - M} l_p.
+// CTA (c - 1, g) handles the boundary in front of range c if it is the first that cuts its segment, and
+// columns 8 g .. 8 g + 7: a warp a column, four dims a lane.
+__global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ PagedAttnArgs a, int columns,
+                                                                   int ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t units = *reinterpret_cast<const int64_t*>(a.err + 2);
+  const int c = blockIdx.x + 1;
+  const int64_t u = pa_unit_start(c, units, ctas);
+  if (u == pa_unit_start(c + 1, units, ctas)) return;    // a range without units
+  const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + 4 * c));
+  const int b = rec.x, h = rec.y, cg = rec.z, tile = rec.w;
+  if (tile == 0) return;                                  // the range begins with a segment
+  const int64_t seg = u - tile;
+  const int first = pa_cta_of_unit(u - 1, units, ctas);
+  if (pa_unit_start(first, units, ctas) > seg) return;    // an earlier boundary cuts it, too
+  int row0;
+  uint32_t none = 0;
+  const PaShape s = pa_shape(a, b, columns, INT32_MAX, row0, none);
+  const int col = 8 * blockIdx.y + warp, n = cg * columns + col;
+  if (n >= s.rows * a.group) return;
+  const int last = pa_cta_of_unit(seg + s.tiles - 1, units, ctas);
+  const int first_slot = pa_unit_start(first, units, ctas) == seg ? 2 * first : 2 * first + 1;
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kGroup = 4;                               // pieces whose loads are in flight together
+  for (int p0 = first; p0 <= last; p0 += kGroup) {
+    float mj[kGroup], lj[kGroup];
+    float4 x[kGroup];
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const int p = p0 + g;
+      mj[g] = -INFINITY;
+      lj[g] = 0.f;
+      x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p <= last && pa_unit_start(p, units, ctas) < pa_unit_start(p + 1, units, ctas)) {
+        const int64_t at = (int64_t)(p == first ? first_slot : 2 * p) * kPagedAttnColumns + col;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
+        mj[g] = ml.x;
+        lj[g] = ml.y;
+        x[g] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kKvDim) + lane);
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) Mn = fmaxf(Mn, mj[g]);
+    const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn);
+    L *= sc;
+    acc.x *= sc;
+    acc.y *= sc;
+    acc.z *= sc;
+    acc.w *= sc;
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const float w = lj[g] == 0.f ? 0.f : exp2f(mj[g] - Mn);
+      L = fmaf(w, lj[g], L);
+      acc.x = fmaf(w, x[g].x, acc.x);
+      acc.y = fmaf(w, x[g].y, acc.y);
+      acc.z = fmaf(w, x[g].z, acc.z);
+      acc.w = fmaf(w, x[g].w, acc.w);
+    }
+    M = Mn;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int i = n / a.group;
+  const int64_t at = (int64_t)(row0 + i) * a.kv_heads * a.group + h * a.group + (n - i * a.group);
+  const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), v1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(a.out + at * kKvDim)[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+  if (a.lse && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+PagedAttnPlan plan_paged_attention() {
+  PagedAttnPlan p;
+  const int ctas = device_sm_count();
+  p.rec_offset = kWorkspaceHeader + ((size_t)ctas * sizeof(uint32_t) + 255) / 256 * 256;
+  p.part_offset = p.rec_offset + ((size_t)ctas * 4 * sizeof(int32_t) + 255) / 256 * 256;
+  p.workspace_bytes = p.part_offset + (size_t)2 * ctas * kPagedAttnColumns * (kKvDim + 2) * sizeof(float);
+  return p;
+}
+
+namespace {
+template <int kCE>
+cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int max_rows, int ctas,
+                           cudaStream_t s) {
+  const size_t smem = pa::kFixedSmem + (size_t)a.num_requests * sizeof(int32_t);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = once_per_device(ready, [] {
+    const int most = pa::kFixedSmem + DSA_MAX_REQUESTS * (int)sizeof(int32_t);
+    cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<kCE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(paged_attention_kernel<kCE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  const int shared_keys = (int64_t)max_rows * a.group > kCE ? 1 : 0;   // several column groups read the same keys
+  auto kernel = a.cap_log2 > 0.f || a.slopes ? paged_attention_kernel<kCE, true> : paged_attention_kernel<kCE, false>;
+  e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, max_rows, shared_keys);
+  count_launches(1);
+  if (e != cudaSuccess) return e;
+  if (ctas > 1) {
+    e = launch_pdl(paged_attention_join_kernel, dim3(ctas - 1, kCE / 8), dim3(256), 0, s, a, kCE, ctas);
+    count_launches(1);
+  }
+  return e;
+}
+}  // namespace
+
+cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_query_len,
+                                   void* workspace, const PagedAttnPlan& plan, cudaStream_t s) {
+  char* ws = static_cast<char*>(workspace);
+  const int ctas = device_sm_count();
+  a.err = reinterpret_cast<uint32_t*>(ws);
+  a.rec = reinterpret_cast<int32_t*>(ws + plan.rec_offset);
+  a.part_o = reinterpret_cast<float*>(ws + plan.part_offset);
+  a.part_ml = a.part_o + (size_t)2 * ctas * kPagedAttnColumns * kKvDim;
+  const uint64_t rows = (uint64_t)a.num_pages * a.kv_heads << a.log2_page;
+  CUtensorMap k_map, v_map;
+  if (!encode_2d(&k_map, k_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kKvDim, rows, kKvDim, kKvDim, 1u << a.log2_page) ||
+      !encode_2d(&v_map, v_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kKvDim, rows, kKvDim, kKvDim, 1u << a.log2_page))
+    return cudaErrorInvalidValue;
+  const int64_t pairs = (int64_t)max_query_len * a.group;
+  cudaError_t e = pairs <= 8    ? launch_columns<8>(a, k_map, v_map, max_query_len, ctas, s)
+                  : pairs <= 16 ? launch_columns<16>(a, k_map, v_map, max_query_len, ctas, s)
+                                : launch_columns<32>(a, k_map, v_map, max_query_len, ctas, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace dsa

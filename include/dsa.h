@@ -11,6 +11,10 @@
  * packed 8-bit latent cache (dsa_cache.latent_format), the device steps of
  * decode context parallelism (dsa_dcp_*, dsa_sparse_mla_decode_ragged), and
  * the append of every layer of a step in one launch (dsa_kv_append_layers).
+ * Around the sparse layers: the step's block tables and slot maps built on the
+ * device (dsa_step_plan, dsa_pages_release), and the dense grouped-head layer
+ * that a draft (MTP) model runs over its own paged 8-bit K/V cache
+ * (dsa_kv8_append, dsa_paged_attention).
  *
  * Sources: "GLM-5.2 on vLLM Ascend: Request-to-Backend Inference Path",
  * section 8 "The SFA backend, step by step" (write paged cache, select tokens,
@@ -70,6 +74,9 @@ extern "C" {
 #define DSA_LATENT_DIM 512   /* c_KV latent width (also the output width)        */
 #define DSA_ROPE_DIM 64      /* k_R / q_rope width                               */
 #define DSA_ROW_DIM 576      /* one cached latent row: [c_KV(512) | k_R(64)]     */
+#define DSA_KV_DIM 128       /* head width of the dense layer's K/V cache        */
+#define DSA_MAX_GROUP 64     /* query heads per K/V head of the dense layer      */
+#define DSA_MAX_REQUESTS 4096 /* requests of a planned step or a dense attention call */
 #define DSA_MAX_TOPK 8192    /* largest supported top-k budget                   */
 #define DSA_STATIC_SCRATCH_BYTES (16u << 20)  /* scratch of dsa_indexer_scores_topk_static */
 
@@ -95,6 +102,14 @@ typedef enum {
                                        and the indexer's scores at those positions are unspecified      */
 #define DSA_DEVICE_CONFIG 0x8u      /* a kernel met a launch shape it cannot hold (the entry points never
                                        launch one)                                                      */
+/* bits of dsa_step_plan and dsa_pages_release */
+#define DSA_DEVICE_POOL_EMPTY 0x10u /* the free pages did not last: the requests from the first that did not
+                                       fit on got no rows in this step                                 */
+#define DSA_DEVICE_ROWS_FULL 0x20u  /* the requests' new tokens exceed num_rows: likewise              */
+#define DSA_DEVICE_BAD_LENGTH 0x40u /* a negative length, or more tokens than the request's table row
+                                       has pages for: that request got no rows                         */
+#define DSA_DEVICE_POOL_FULL 0x80u  /* more pages came back than the stack holds: the requests from the
+                                       first that did not fit on were not released                     */
 
 typedef enum {
   DSA_KEY_BF16 = 0,     /* index keys stored as bf16 [.., 128]                        */
@@ -466,6 +481,125 @@ DSA_API dsa_status dsa_dcp_select(const float* cand_scores, const int32_t* cand_
  */
 DSA_API dsa_status dsa_dcp_merge(const void* outs, const float* lses, int32_t world, int32_t num_rows, void* out,
                                  float* lse, void* stream);
+
+/*
+ * The step's block tables and slot maps from the requests' lengths, built on the device
+ * ("GLM-5.2 on vLLM Ascend", section 4 "NPU batch preparation and attention metadata": cumulative
+ * query lengths, sequence lengths, block tables and per-token slot mappings).
+ * Request b holds seq_lens[b] tokens and brings new_lens[b] more (0: it rests).  The requests
+ * admitted are the longest prefix whose rows fit num_rows and whose new pages the stack of free pages
+ * holds; the others keep their length and get no rows (DSA_DEVICE_ROWS_FULL / _POOL_EMPTY), as does a
+ * request whose lengths make no sense or whose table row is too short (DSA_DEVICE_BAD_LENGTH).
+ *   page_size        power of two, 1..1024.
+ *   block_table      device int32 [num_requests, block_table_stride], in and out: new page i of request b
+ *                    is written after the ceil(seq_lens[b] / page_size) that it has; no other entry is.
+ *   free_pages, free_count  device int32 [free_capacity] and [1]: the stack; its top is free_pages[count - 1].
+ *                    Pages are taken from the top, in request order.  The stack's entries are not written.
+ *   seq_lens_out     device int32 [num_requests]: lengths after the step; may be seq_lens.
+ *   query_start_loc  device int32 [num_requests + 1]: rows of request b.
+ *   slot_mapping     device int64 [num_rows]: slot of each row (dsa_kv_append's), -1 behind the last row.
+ *   positions        device int32 [num_rows] or NULL: position of each row, -1 behind the last.
+ *   free_count_out   device int32 [1]: the count after the step; may be free_count.
+ *   workspace        256 bytes, 256-byte aligned, for the status that dsa_read_status reads, or NULL.
+ * One launch.  Apart from the two pairs named, outputs do not overlap inputs.  Calling it again with the same
+ * inputs gives the same outputs: a step takes effect when seq_lens_out and free_count_out are the next
+ * call's seq_lens and free_count.  DSA_ERR_UNSUPPORTED for more than DSA_MAX_REQUESTS requests.
+ */
+DSA_API dsa_status dsa_step_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_t num_requests,
+                                 int32_t page_size, int32_t* block_table, int32_t block_table_stride,
+                                 const int32_t* free_pages, int32_t free_capacity, const int32_t* free_count,
+                                 int32_t num_rows, int32_t* seq_lens_out, int32_t* query_start_loc,
+                                 int64_t* slot_mapping, int32_t* positions, int32_t* free_count_out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Return the pages of finished requests to the stack, in place: for every b with finished[b] != 0 the
+ * ceil(seq_lens[b] / page_size) leading entries of its table row are pushed onto free_pages and set to
+ * -1, seq_lens[b] becomes 0 and *free_count grows.  Entries outside [0, num_pages) are not pushed
+ * (DSA_DEVICE_BAD_PAGE); a request that the stack has no room for stays as it is, as do those after it
+ * (DSA_DEVICE_POOL_FULL).  Pages must belong to one request each.  workspace as for dsa_step_plan.
+ */
+DSA_API dsa_status dsa_pages_release(const int32_t* finished, int32_t* seq_lens, int32_t num_requests,
+                                     int32_t page_size, int32_t* block_table, int32_t block_table_stride,
+                                     int32_t num_pages, int32_t* free_pages, int32_t free_capacity, int32_t* free_count,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A dense grouped-head layer's paged 8-bit K/V cache (caller-owned device memory): the draft (MTP)
+ * layer's, which attends to every cached token (the pages' dense draft-layer attention backend).
+ *   k_codes, v_codes    [num_pages, kv_heads, page_size, 128] e4m3 codes, 16-byte aligned.
+ *   k_scales, v_scales  [num_pages, kv_heads] fp32, one per block (= page) and head: value = code * scale.
+ *                       dsa_kv8_append writes powers of two from 2^-126 to 2^120; attention takes any
+ *                       finite scale of that range, and 0.
+ * Token s of request b lies in page block_table[b][s / page_size], at offset s % page_size.
+ */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t num_pages;
+  int32_t page_size;     /* 16, 32, 64 or 128 */
+  int32_t kv_heads;
+  int32_t reserved;      /* 0 */
+} dsa_kv8_cache;
+
+/*
+ * Append the step's K and V to a dense layer's 8-bit cache.  Rows, requests and positions come from
+ * batch (seq_lens after this append; a row behind the last request's is skipped).  For each page and
+ * head that the step writes:
+ *   want  = 2^ceil(log2(amax / 448)) over the new tokens' finite values, at least 2^-126
+ *   scale = want, or the larger of want and the page's scale if the page holds older tokens of the request
+ *   code  = e4m3(x / scale), nearest-even, saturating (infinities too); NaN stays NaN
+ * and where the scale grew, the page's older codes become e4m3(code * (old scale / scale)).  Codes of
+ * unwritten offsets keep their contents.  What a page holds thus depends on how its tokens were
+ * grouped into calls, by roundings of codes below 2^-6 only.
+ *   k, v      device bf16, token t's heads at k + t * k_stride (elements): [kv_heads, 128] contiguous,
+ *             16-byte aligned, strides a multiple of 8 and at least kv_heads * 128.
+ * A page that is written belongs to one request.  Out-of-range page ids are skipped.
+ */
+DSA_API dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, void* stream);
+
+/* Scratch bytes dsa_paged_attention needs on the current device (the same for every shape). */
+DSA_API size_t dsa_paged_attention_workspace_bytes(void);
+
+/*
+ * What a dense attention call may add to the plain causal form (all optional).
+ *   softcap      > 0: a score z becomes softcap * tanh(z / softcap); 0: none.
+ *   slopes       device fp32 [q_heads] or NULL: after the cap, slopes[h] * |position - s| is subtracted.
+ *   prefix_lens  device int32 [num_requests] or NULL: every row of request b also sees the positions
+ *                below prefix_lens[b] (and below its length), its own future ones included.
+ */
+typedef struct {
+  float softcap;
+  int32_t reserved;      /* 0 */
+  const float* slopes;
+  const int32_t* prefix_lens;
+} dsa_attn_mods;
+
+/*
+ * Dense attention over the 8-bit K/V cache, for decode, verify and prompt rows alike (mixed in one
+ * call): row i of request b sits at position pos = L_b - q_len_b + i, sees positions 0..pos, and
+ *   z_s = scale * q[r,h] . (k_code_s * k_scale_s)      h' = h / (q_heads / kv_heads)
+ *   out[r,h] = sum_s softmax(z)_s * (v_code_s * v_scale_s),   lse[r,h] = ln sum_s exp(z_s)
+ *   q          device bf16, row r's heads at q + r * q_stride (elements): [q_heads, 128] contiguous,
+ *              16-byte aligned, q_stride a multiple of 8 and at least q_heads * 128.
+ *   q_heads    a multiple of kv_heads, at most DSA_MAX_GROUP per K/V head.
+ *   max_query_len  host upper bound on every request's rows (a request with more is refused on the
+ *              device: DSA_DEVICE_BAD_LENGTH, its rows are left as they were).
+ *   out        device bf16 [num_rows, q_heads, 128]; lse fp32 [num_rows, q_heads] or NULL.
+ *   workspace  dsa_paged_attention_workspace_bytes(), 256-byte aligned; calls that may run at the same
+ *              time take one each.
+ * A row that sees nothing (an empty request) gets zeros and an lse of -inf.  Rows behind the last request's
+ * are left as they were.  What lies in the cache behind a request's tokens is never used, NaN codes included.
+ * A visible position without a valid page is skipped and reported (DSA_DEVICE_BAD_PAGE).
+ * Sums, maxima and lse are fp32; q keeps all of bf16's bits in the products, a probability 8 or more.
+ */
+DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q,
+                                       int64_t q_stride, int32_t q_heads, float scale, int32_t max_query_len,
+                                       const dsa_attn_mods* mods, void* out, float* lse, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
