@@ -27,8 +27,15 @@
 // contiguous range per CTA (persistent, one CTA per SM).  A segment (all tiles of one request, head and
 // group) inside one CTA is written directly; one that is cut leaves fp32 pieces that a second kernel joins.
 //
-// Per CTA (8 warps): warp 0 looks pages up and issues TMA loads into a ring of 32 KB stages (K and V of
-// a tile); warp 1 issues the MMAs; warps 2-3 split the next segment's queries; warps 4-7 are the softmax.
+// Per CTA (12 warps): warp 0 looks pages up and issues TMA loads into a ring of 32 KB stages (K and V of
+// a tile); warps 1 and 3 issue the products of the scores and of the outputs, each at its own pace (one warp
+// doing both spent 1,500 cycles a tile on waits and issue: 788 us instead of 685 for 64 requests of
+// 16K-128K tokens); warp 2 splits the coming segments' queries; warps 4-7 and 8-11 are two
+// softmax warpgroups that take the even and the odd tiles.  A tile's softmax is one chain of waits (scores
+// out of TMEM, maxima across the warps, probabilities into shared memory) about 2,000 cycles long, while at
+// full HBM speed a tile arrives every 1,360 cycles; two chains side by side keep up.  They share nothing while they
+// run: each has its own maxima, denominators and accumulator, joined in the segment's epilogue, which
+// the warpgroups take in turn.
 #include "dsa_internal.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
@@ -45,14 +52,16 @@ constexpr int kColMax = kPagedAttnColumns;
 constexpr int kQBytes = 2 * kColMax * kKvDim;   // hi and lo rows of 32 columns
 constexpr int kPBytes = kTok * 2 * kColMax;
 constexpr int kMaxPages = kTok / kKvMinPage;    // pages of a tile
-constexpr int kThreads = 256;
-constexpr int kMmaWarp = 1, kQWarp0 = 2, kSoftWarp0 = 4;
-constexpr uint32_t kTmemCols = 256;             // S^T of parity b at 64 b, O^T of parity b at 128 + 64 b
+constexpr int kThreads = 384;
+constexpr int kScoreWarp = 1, kOutWarp = 3, kSoftWarp0 = 4;
+constexpr uint32_t kRegsLow = 88, kRegsSoft = 208;   // 88 + 2 * 208 = 3 * 168, the launch's
+constexpr int kQBufs = 3;                       // the scores run two tiles, so up to two segments, ahead of the outputs
+constexpr uint32_t kTmemCols = 512;             // S^T of warpgroup w at 64 w, O^T at 128 + 128 (segment % 2) + 64 w
 constexpr uint32_t kColO = 128;
 constexpr float kSlack = 2.f;                   // log2 by which a maximum may be exceeded
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
 constexpr uint32_t kPolls = 1u << 22;
-constexpr int kFixedSmem = kStages * kStageBytes + 2 * kQBytes + 2 * kPBytes + 1024;
+constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 }  // namespace pa
 
 // Units of request b: column groups * key tiles (times K/V heads)
@@ -149,13 +158,13 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = __nv_cvt_float2_to_fp8x2(make_float2(16.f * (a - back.x), 16.f * (b - back.y)), __NV_SATFINITE, __NV_E4M3);
 }
 
-// What the query warps leave about a segment's columns
+// What the query warp leaves about a segment's columns
 struct PaColumns {
   float factor[pa::kColMax];    // 2^k of the split query * softmax scale * log2 e
   int limit[pa::kColMax];       // keys below it are seen
   int pos[pa::kColMax];
   float slope[pa::kColMax];     // * log2 e
-  int min_limit[2];             // over each query warp's columns
+  int min_limit;                // over the columns
 };
 
 // kCE columns (8, 16 or 32); kMods: score cap and distance bias compiled in
@@ -170,16 +179,18 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
   uint8_t* sQ = sKV + kStages * kStageBytes;
-  uint8_t* sP = sQ + 2 * kQBytes;
+  uint8_t* sP = sQ + kQBufs * kQBytes;
   int32_t* end = reinterpret_cast<int32_t*>(sP + 2 * kPBytes);   // [requests]
 
-  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], s_full[2], s_empty[2], p_full[2], p_empty[2];
-  __shared__ uint64_t q_full[2], q_empty[2], o_full[2], o_empty[2], mma_done;
+  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], s_full[2], s_empty[2], p_full[2];
+  __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[2], o_empty[2], mma_done;
   __shared__ float sks[kStages][kMaxPages], svs[kStages][kMaxPages];
   __shared__ uint32_t sbad[kStages];
-  __shared__ __align__(16) PaColumns cols[2];
-  __shared__ float wmax[2][4][kCE], wlv[2][4], red[4][kCE], fin[kCE];
-  __shared__ uint32_t nan_keys[4];
+  __shared__ __align__(16) PaColumns cols[kQBufs];
+  __shared__ float wmax[2][4][kCE], wlv[2][4], red[2][4][kCE], fin[2][2][kCE];
+  __shared__ float stat[kQBufs][2][3][kCE];            // each warpgroup's m, mv and l of a segment
+  __shared__ uint32_t stat_nan[kQBufs][2][kKvDim];
+  __shared__ uint32_t nan_keys[2][4];
   __shared__ int32_t scan[kThreads / 32];
   __shared__ uint32_t tmem_base, bits_all;
 
@@ -194,24 +205,26 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
       mbar_init(&p_full[i], 1);
-      mbar_init(&p_empty[i], 1);
-      mbar_init(&q_full[i], 2);
-      mbar_init(&q_empty[i], 5);          // the last product that reads it, and four softmax warps
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 4);
     }
-    mbar_init(&mma_done, 1);
+    for (int i = 0; i < kQBufs; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 9);          // the last product that reads it, and eight softmax warps
+      mbar_init(&stat_full[i], 8);
+    }
+    mbar_init(&mma_done, 2);
     bits_all = 0;
     fence_mbar_init();
     prefetch_tmap(&k_map);
     prefetch_tmap(&v_map);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
   if (kCE < kHalf)                                     // columns that no query fills stay zero
-    for (int i = tid; i < 2 * kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kQBufs * kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   // running sums of the requests' units: every thread a run of consecutive requests
   {
@@ -247,6 +260,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   const int64_t u0 = pa_unit_start(cta, units, ctas), u1 = pa_unit_start(cta + 1, units, ctas);
   uint32_t* const err = &bits_all;                    // this CTA's status bits, stored at the end
 
+  if (warp < kSoftWarp0) {
+  regs_dec<kRegsLow>();
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
@@ -309,96 +324,105 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const int uses = (i - st + kStages - 1) / kStages;
       if (i > st) mbar_wait(&kv_full[st], (uses - 1) & 1, err, kErrTmaTimeout, kPolls);
     }
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t id_qk = idesc_e4m3(kTok, kN);
-      const uint32_t id_pv = idesc_e4m3(kKvDim, kN) | (1u << 15) | (1u << 16);   // both operands MN-major
-      constexpr SmemSwizzle kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
-      const uint64_t d_k = smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
-      const uint64_t d_v = smem_desc(smem_u32(sKV + kTileBytes), 16, 1024, kSwizzle128B);
-      const uint64_t d_q = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
-      const uint64_t d_p = smem_desc(smem_u32(sP), 16, 8 * kN, kPSwizzle);
-      const int n_tiles = (int)(u1 - u0);
-      // segments are walked twice: by the scores (iq, ahead by one tile) and by the outputs (ip)
-      int64_t uq = u0, up = u0;
-      int q_left = 0, p_left = 0, q_seg = -1, p_seg = -1;
-      bool ok = true, p_first = false;
-      for (int step = 0; step <= n_tiles && ok; ++step) {
-        if (step < n_tiles) {
-          const int i = step, st = i % kStages, sb = i & 1;
-          if (q_left == 0) {
-            const PaSeg s = pa_segment(a, end, kCE, uq, u1);
-            q_left = s.n;
-            uq += s.n;
-            ++q_seg;
-            ok = mbar_wait(&q_full[q_seg & 1], (q_seg >> 1) & 1, err, kErrMmaTimeout, kPolls);
-          }
-          ok = ok && mbar_spin(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout);
-          if (ok && i >= 2) ok = mbar_spin(&s_empty[sb], ((i >> 1) - 1) & 1, err, kErrMmaTimeout);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t k = d_k + (uint64_t)((st * kStageBytes) >> 4), q = d_q + (uint64_t)(((q_seg & 1) * kQBytes) >> 4);
+  } else if (warp == kScoreWarp) {
+    // ---------------------------------------------------------------- products of the scores
+    // The warp walks together and one elected lane issues: addresses stay in uniform registers.  With
+    // the walk itself inside a one-lane branch, issuing a tile's products took twice as long.
+    const bool leader = elect_one();
+    const uint32_t id_qk = idesc_e4m3(kTok, kN);
+    const uint64_t d_k = smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
+    const uint64_t d_q = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+    int i = 0, seg = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok; ++seg) {
+      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      u += s.n;
+      const int qb = seg % kQBufs;
+      ok = mbar_wait(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls);
+      for (int t = 0; t < s.n && ok; ++t, ++i) {
+        const int st = i % kStages, sb = i & 1;
+        ok = mbar_spin(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout);
+        if (ok && i >= 2) ok = mbar_spin(&s_empty[sb], ((i >> 1) - 1) & 1, err, kErrMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t k = d_k + (uint64_t)((st * kStageBytes) >> 4), q = d_q + (uint64_t)((qb * kQBytes) >> 4);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kKvDim / 32; ++kk) mma_ss_f8(tmem + 64 * sb, k + 2 * kk, q + 2 * kk, id_qk, kk > 0);
           mma_commit(&s_full[sb]);
-          if (--q_left == 0) mma_commit(&q_empty[q_seg & 1]);
+          if (t + 1 == s.n) mma_commit(&q_empty[qb]);
         }
-        if (step > 0) {
-          const int i = step - 1, st = i % kStages, pb = i & 1;
-          if (p_left == 0) {
-            const PaSeg s = pa_segment(a, end, kCE, up, u1);
-            p_left = s.n;
-            up += s.n;
-            ++p_seg;
-            p_first = true;
-            if (p_seg >= 2) ok = mbar_wait(&o_empty[p_seg & 1], ((p_seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
-          }
-          ok = ok && mbar_spin(&p_full[pb], (i >> 1) & 1, err, kErrMmaTimeout);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t v = d_v + (uint64_t)((st * kStageBytes) >> 4), p = d_p + (uint64_t)((pb * kPBytes) >> 4);
+        __syncwarp();
+      }
+    }
+    // every MMA issued here has finished before TMEM is released
+    if (leader) mma_commit(&mma_done);
+    mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+  } else if (warp == kOutWarp) {
+    // ---------------------------------------------------------------- products of the outputs
+    const bool leader = elect_one();
+    const uint32_t id_pv = idesc_e4m3(kKvDim, kN) | (1u << 15) | (1u << 16);   // both operands MN-major
+    constexpr SmemSwizzle kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
+    const uint64_t d_v = smem_desc(smem_u32(sKV + kTileBytes), 16, 1024, kSwizzle128B);
+    const uint64_t d_p = smem_desc(smem_u32(sP), 16, 8 * kN, kPSwizzle);
+    int i = 0, seg = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok; ++seg) {
+      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      u += s.n;
+      uint32_t fresh = 3;                              // accumulators of the segment without a product yet
+      if (seg >= 2) ok = mbar_wait(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+      for (int t = 0; t < s.n && ok; ++t, ++i) {
+        const int st = i % kStages, pb = i & 1;
+        ok = mbar_spin(&p_full[pb], (i >> 1) & 1, err, kErrMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v = d_v + (uint64_t)((st * kStageBytes) >> 4), p = d_p + (uint64_t)((pb * kPBytes) >> 4);
+        const bool first = (fresh >> pb) & 1u;
+        fresh &= ~(1u << pb);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kTok / 32; ++kk)
-            mma_ss_f8(tmem + kColO + 64 * (p_seg & 1), v + (uint64_t)((kk * 32 * kKvDim) >> 4),
-                      p + (uint64_t)((kk * 32 * kN) >> 4), id_pv, !p_first || kk > 0);
-          p_first = false;
-          mma_commit(&kv_empty[st]);
-          mma_commit(&p_empty[pb]);
-          if (--p_left == 0) mma_commit(&o_full[p_seg & 1]);
+            mma_ss_f8(tmem + kColO + 128 * (seg & 1) + 64 * pb, v + (uint64_t)((kk * 32 * kKvDim) >> 4),
+                      p + (uint64_t)((kk * 32 * kN) >> 4), id_pv, !first || kk > 0);
+          mma_commit(&kv_empty[st]);                   // K, V and this tile's probabilities have been read
+          if (t + 1 == s.n) mma_commit(&o_full[seg & 1]);
         }
+        __syncwarp();
       }
-      // every MMA issued here has finished before TMEM is released
-      mma_commit(&mma_done);
-      mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
     }
-  } else if (warp < kSoftWarp0) {
+    if (leader) mma_commit(&mma_done);
+    mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+  } else {
     // ---------------------------------------------------------------- queries: 16 threads a column
-    const int qw = warp - kQWarp0, part = lane & 15;
+    const int part = lane & 15;
     int seg = 0;
     for (int64_t u = u0; u < u1; ++seg) {
       const PaSeg s = pa_segment(a, end, kCE, u, u1);
       u += s.n;
-      const int buf = seg & 1;
-      if (seg >= 2 && !mbar_wait(&q_empty[buf], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      const int buf = seg % kQBufs;
+      if (seg >= kQBufs && !mbar_wait(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       uint8_t* q_hi = sQ + buf * kQBytes;
       PaColumns& cm = cols[buf];
       const int pairs = s.rows * a.group, prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
       const int start = a.seq_lens[s.b] - s.rows;     // position of row 0
-      uint4 x[kCE / 4];
+      int low = INT32_MAX;
+      // eight columns at a time: their loads are in flight together
+#pragma unroll 1
+      for (int c0 = 0; c0 < kCE; c0 += 8) {
+      uint4 x[4];
 #pragma unroll
-      for (int it = 0; it < kCE / 4; ++it) {
-        const int n = s.cg * kCE + 4 * it + 2 * qw + (lane >> 4);
+      for (int it = 0; it < 4; ++it) {
+        const int n = s.cg * kCE + c0 + 2 * it + (lane >> 4);
         x[it] = make_uint4(0, 0, 0, 0);
         if (n < pairs) {
           const int i = n / a.group, g = n - i * a.group;
           x[it] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (s.h * a.group + g) * kKvDim + 8 * part);
         }
       }
-      int low = INT32_MAX;
 #pragma unroll
-      for (int it = 0; it < kCE / 4; ++it) {
-        const int c = 4 * it + 2 * qw + (lane >> 4), n = s.cg * kCE + c;
+      for (int it = 0; it < 4; ++it) {
+        const int c = c0 + 2 * it + (lane >> 4), n = s.cg * kCE + c;
         const uint32_t w[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
         uint32_t top = 0;                             // largest finite |x|, as bf16 bits
 #pragma unroll
@@ -435,24 +459,29 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           cm.slope[c] = kMods && a.slopes && n < pairs ? a.slopes[s.h * a.group + (n - i * a.group)] * 1.4426950408889634f : 0.f;
         }
       }
+      }
       low = __reduce_min_sync(0xffffffffu, low);
-      if (lane == 0) cm.min_limit[qw] = low;
+      if (lane == 0) cm.min_limit = low;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
     }
+  }
   } else {
+    regs_inc<kRegsSoft>();
     // ---------------------------------------------------------------- softmax and outputs: one key a thread
+    const int wg = (warp - kSoftWarp0) >> 2, bar = 1 + wg;
     const int quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    int i = 0, seg = 0;
+    int i0 = 0, seg = 0;                               // i0: the CTA's tiles before this segment
     for (int64_t u = u0; u < u1; ++seg) {
       const PaSeg s = pa_segment(a, end, kCE, u, u1);
       u += s.n;
-      const int qb = seg & 1;
-      if (!mbar_wait(&q_full[qb], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      const int qb = seg % kQBufs;
+      if (!mbar_wait(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
+      const uint32_t acc = tmem + lanes + kColO + 128 * (seg & 1);
       const PaColumns& cm = cols[qb];
-      const int min_limit = min(cm.min_limit[0], cm.min_limit[1]);
+      const int min_limit = cm.min_limit;
       // the references of column `lane` (m: of z, mv: of z + log2 vs), and every column's in registers
       float m_lane = -INFINITY, mv_lane = -INFINITY;
       float m[kCE], e[kCE], l[kCE];
@@ -463,9 +492,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         l[c] = 0.f;
       }
       uint32_t poison = 0;                             // columns whose output at dim `row` is NaN
-      bool ok = true;
-      for (int t = 0; t < s.n; ++t, ++i) {
-        const int st = i % kStages, sb = i & 1;
+      bool ok = true, fresh = true;
+      for (int t = (i0 + wg) & 1; t < s.n; t += 2) {
+        const int i = i0 + t, st = i % kStages, sb = wg;
         const int key0 = (s.tile + t) * kTok, j = key0 + row;
         ok = mbar_wait(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
              mbar_wait(&s_full[sb], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
@@ -536,7 +565,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         const float lv_max = warp_max_f32(lv);
         if (lane < kCE) wmax[sb][quarter][lane] = mine;
         if (lane == 0) wlv[sb][quarter] = lv_max;
-        const bool any_nan = named_bar_or(1, 128, has_nan);
+        const bool any_nan = named_bar_or(bar, 128, has_nan);
         float M = -INFINITY, MV = -INFINITY;
         if (lane < kCE) {
 #pragma unroll
@@ -561,12 +590,12 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             m[c] = __shfl_sync(0xffffffffu, m_use, c);
             e[c] = __shfl_sync(0xffffffffu, e_new, c);
           }
-          if (t > 0) {
-            // the accumulator is settled once the previous tile's product has completed
-            ok = mbar_wait(&p_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, err, kErrMmaTimeout, kPolls);
+          if (!fresh) {
+            // the accumulator is settled once this warpgroup's previous product has completed
+            ok = mbar_wait(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t o = tmem + lanes + kColO + 64 * qb;
+            const uint32_t o = acc + 64 * wg;
 #pragma unroll
             for (int c0 = 0; c0 < kCE; c0 += 8) {
               uint32_t r[16];
@@ -587,18 +616,18 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         }
         if (any_nan) {
           const uint32_t who = __ballot_sync(0xffffffffu, has_nan);
-          if (lane == 0) nan_keys[quarter] = who;
-          named_bar_sync(1, 128);
+          if (lane == 0) nan_keys[wg][quarter] = who;
+          named_bar_sync(bar, 128);
           const uint8_t* vt = sKV + st * kStageBytes + kTileBytes;
           for (int w = 0; w < 4; ++w)
-            for (uint32_t left = nan_keys[w]; left; left &= left - 1) {
+            for (uint32_t left = nan_keys[wg][w]; left; left &= left - 1) {
               const int k = 32 * w + __ffs(left) - 1;
               const uint8_t code = vt[k * kKvDim + ((((uint32_t)row >> 4) ^ (k & 7)) << 4) + (row & 15)];
               if ((code & 0x7Fu) == 0x7Fu)
                 for (int c = 0; c < kCE; ++c)
                   if (key0 + k < cm.limit[c]) poison |= 1u << c;
             }
-          named_bar_sync(1, 128);
+          named_bar_sync(bar, 128);
           if (has_nan) {
             uint32_t* vrow = reinterpret_cast<uint32_t*>(sKV + st * kStageBytes + kTileBytes + row * kKvDim);
             for (int q = 0; q < kKvDim / 4; ++q) {
@@ -628,9 +657,10 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           hi[c / 4] = h0 | h1 << 16;
           lo[c / 4] = l0 | l1 << 16;
         }
-        // the buffer is free once the product two tiles back has completed
+        fresh = false;
+        // the buffer is free once this warpgroup's previous product has completed
         if (i >= 2) {
-          ok = mbar_wait(&p_empty[sb], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+          ok = mbar_wait(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
           if (!ok) break;
         }
         uint8_t* prow = sP + sb * kPBytes + row * kN;
@@ -643,38 +673,56 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        named_bar_sync(1, 128);
+        named_bar_sync(bar, 128);
         if (row == 0) mbar_arrive(&p_full[sb]);
       }
       if (!ok) break;
-      // ---- the segment's end: denominators, then O^T out of TMEM (this thread: dim `row` of every column)
+      i0 += s.n;
+      // ---- the segment's end: each warpgroup leaves its maxima and denominators, and one writes the outputs
 #pragma unroll
       for (int c = 0; c < kCE; ++c) {
         float v = l[c];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) red[quarter][c] = v;
+        if (lane == 0) red[wg][quarter][c] = v;
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(bar, 128);
+      if (quarter == 0 && lane < kCE) {
+        stat[qb][wg][0][lane] = m_lane;
+        stat[qb][wg][1][lane] = mv_lane;
+        stat[qb][wg][2][lane] = (red[wg][0][lane] + red[wg][1][lane]) + (red[wg][2][lane] + red[wg][3][lane]);
+      }
+      stat_nan[qb][wg][row] = poison;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&stat_full[qb]);
+      if ((seg & 1) != wg) {
+        if (lane == 0) mbar_arrive(&q_empty[qb]);
+        continue;
+      }
+      if (!mbar_wait(&stat_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
       const bool whole = s.n == s.tiles;
       const int pairs = s.rows * a.group;
       // a piece that starts its segment is its CTA's last unless it also starts the CTA's range
       const int slot = u - s.n == u0 ? 2 * cta : 2 * cta + 1;
       if (quarter == 0 && lane < kCE) {
-        const float L = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-        const float back = 1.f / (mv_lane == -INFINITY ? kPOne : ex2_approx(m_lane - mv_lane) * kPOne);
-        const bool any = L > 0.f || L != L;
-        fin[lane] = !any ? 0.f : whole ? back / L : back;
+        // out = sum_w f_w O_w: f_w = 2^(m_w - M) / (L 64 2^(m_w - mv_w)) = 2^(mv_w - M) / (64 L), without L for a piece
+        const float ma = stat[qb][0][0][lane], mb = stat[qb][1][0][lane], la = stat[qb][0][2][lane], lb = stat[qb][1][2][lane];
+        const bool has_a = la > 0.f || la != la, has_b = lb > 0.f || lb != lb;   // NaN counts as seen
+        const float M = fmaxf(ma, mb);
+        const float L = (has_a ? la * ex2_approx(ma - M) : 0.f) + (has_b ? lb * ex2_approx(mb - M) : 0.f);
+        const float over = (whole ? 1.f / L : 1.f) / kPOne;
+        fin[wg][0][lane] = has_a ? ex2_approx(stat[qb][0][1][lane] - M) * over : 0.f;
+        fin[wg][1][lane] = has_b ? ex2_approx(stat[qb][1][1][lane] - M) * over : 0.f;
         const int n = s.cg * kCE + lane;
         if (whole) {
           if (a.lse && n < pairs) {
             const int r = n / a.group;
             a.lse[(int64_t)(s.row0 + r) * a.kv_heads * a.group + s.h * a.group + (n - r * a.group)] =
-                any ? (m_lane + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+                has_a || has_b ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
           }
         } else {
           float* ml = a.part_ml + ((int64_t)slot * kColMax + lane) * 2;
-          ml[0] = m_lane;
+          ml[0] = M;
           ml[1] = L;
         }
       }
@@ -685,23 +733,27 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         rec[2] = s.cg;
         rec[3] = s.tile;
       }
-      named_bar_sync(1, 128);
-      if (!mbar_wait(&o_full[qb], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      poison = stat_nan[qb][0][row] | stat_nan[qb][1][row];
+      named_bar_sync(bar, 128);
+      if (!mbar_wait(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       tc_fence_after();
-      const uint32_t o = tmem + lanes + kColO + 64 * qb;
 #pragma unroll 1
       for (int c0 = 0; c0 < kCE; c0 += 8) {
-        uint32_t r[16];
-        tmem_ld_cols<8>(o + c0, r);
-        tmem_ld_cols<8>(o + kHalf + c0, r + 8);
+        uint32_t r[32];
+        tmem_ld_cols<8>(acc + c0, r);
+        tmem_ld_cols<8>(acc + kHalf + c0, r + 8);
+        tmem_ld_cols<8>(acc + 64 + c0, r + 16);
+        tmem_ld_cols<8>(acc + 64 + kHalf + c0, r + 24);
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const int n = s.cg * kCE + c0 + c;
           if (n >= pairs) break;
-          const float f = fin[c0 + c];
-          float v = fmaf(__uint_as_float(r[8 + c]), 0.0625f, __uint_as_float(r[c])) * f;
-          if (f == 0.f) v = 0.f;                       // nothing seen: the accumulator holds nothing of it
+          const float fa = fin[wg][0][c0 + c], fb = fin[wg][1][c0 + c];
+          // an accumulator without a seen key holds nothing of this column (or was never written)
+          float v = 0.f;
+          if (fa != 0.f) v = fmaf(__uint_as_float(r[8 + c]), 0.0625f, __uint_as_float(r[c])) * fa;
+          if (fb != 0.f) v = fmaf(fmaf(__uint_as_float(r[24 + c]), 0.0625f, __uint_as_float(r[16 + c])), fb, v);
           if ((poison >> (c0 + c)) & 1u) v = __int_as_float(0x7FC00000);
           if (whole) {
             const int i2 = n / a.group;
@@ -715,14 +767,14 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&o_empty[qb]);
+        mbar_arrive(&o_empty[seg & 1]);
         mbar_arrive(&q_empty[qb]);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

@@ -380,6 +380,17 @@ __device__ __forceinline__ void mma_ss_lh(uint32_t d_tmem, uint32_t a_lo, uint32
         : "memory");
 }
 
+// True in one lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // A value the compiler must treat as new at this point (keeps per-tile offsets from being hoisted
 // into dozens of live registers).
 __device__ __forceinline__ uint32_t opaque_u32(uint32_t x) {
