@@ -565,8 +565,8 @@ def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None):
                                               _stream(stream)))
 
 
-def paged_attention_workspace_bytes() -> int:
-    return int(_lib.load().dsa_paged_attention_workspace_bytes())
+def paged_attention_workspace_bytes(q_heads: int, kv_heads: int, max_query_len: int) -> int:
+    return int(_lib.load().dsa_paged_attention_workspace_bytes(q_heads, kv_heads, max_query_len))
 
 
 def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM ** -0.5, max_query_len: int | None = None,
@@ -596,6 +596,7 @@ def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM 
                                              0 if prefix_lens is None else prefix_lens.data_ptr()))
     if max_query_len is None:
         max_query_len = R if batch.query_start_loc is not None else 1
+    max_query_len = max(int(max_query_len), 1)
     with _on(dev, stream):
         if out is None:
             out = torch.empty((R, heads, KV_DIM), dtype=torch.bfloat16, device=dev)
@@ -604,10 +605,10 @@ def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM 
         if lse is not None:
             _need(lse, torch.float32, (R, heads), "lse")
         if workspace is None:
-            workspace = _workspace(paged_attention_workspace_bytes(), dev)
+            workspace = _workspace(paged_attention_workspace_bytes(heads, cache.kv_heads, max_query_len), dev)
         c, b = cache.struct(), batch.struct()
         _lib.check(_lib.load().dsa_paged_attention(
-            ctypes.byref(c), ctypes.byref(b), _ptr(q), q_stride, heads, float(scale), max(int(max_query_len), 1), mods, _ptr(out),
+            ctypes.byref(c), ctypes.byref(b), _ptr(q), q_stride, heads, float(scale), max_query_len, mods, _ptr(out),
             _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
         if check:
             _check_device(workspace, stream)

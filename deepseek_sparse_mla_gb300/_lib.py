@@ -127,7 +127,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_kv8_append.argtypes = [ctypes.POINTER(DsaKv8Cache), ctypes.POINTER(DsaBatch), P, ctypes.c_int64, P,
                                    ctypes.c_int64, P]
     lib.dsa_paged_attention_workspace_bytes.restype = SZ
-    lib.dsa_paged_attention_workspace_bytes.argtypes = []
+    lib.dsa_paged_attention_workspace_bytes.argtypes = [I32, I32, I32]
     lib.dsa_paged_attention.restype = I32
     lib.dsa_paged_attention.argtypes = [ctypes.POINTER(DsaKv8Cache), ctypes.POINTER(DsaBatch), P, ctypes.c_int64, I32,
                                         ctypes.c_float, I32, ctypes.POINTER(DsaAttnMods), P, P, P, SZ, P]

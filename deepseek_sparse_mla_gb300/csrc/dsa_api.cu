@@ -4,6 +4,7 @@
 // dynamically, allocates nothing and never synchronises: it records launches
 // on the caller's stream.  Launch plans are pure functions of the shape, so the
 // workspace sizes reported to the caller are exactly what the launches use.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -704,7 +705,10 @@ dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, co
   return cuda_status(launch_kv8_append(a, (cudaStream_t)stream), "8-bit K/V append launch");
 }
 
-size_t dsa_paged_attention_workspace_bytes(void) { return plan_paged_attention().workspace_bytes; }
+size_t dsa_paged_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t max_query_len) {
+  if (kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads || max_query_len < 1) return 0;
+  return plan_paged_attention(max_query_len, q_heads / kv_heads).workspace_bytes;
+}
 
 dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
                                int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,
@@ -737,7 +741,8 @@ dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batc
   if (!aligned4(lse)) return fail(DSA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
   if ((int64_t)batch->num_rows * q_heads > INT32_MAX / 2)
     return fail(DSA_ERR_UNSUPPORTED, "num_rows * q_heads is too large");
-  const PagedAttnPlan plan = plan_paged_attention();
+  const int rows_max = batch->query_start_loc ? std::min(max_query_len, batch->num_rows) : 1;
+  const PagedAttnPlan plan = plan_paged_attention(rows_max, group);
   if (!workspace || workspace_bytes < plan.workspace_bytes)
     return fail(DSA_ERR_WORKSPACE,
                 "workspace of %zu bytes is smaller than the %zu bytes dsa_paged_attention_workspace_bytes requires",
@@ -764,9 +769,9 @@ dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batc
   a.prefix_lens = mods ? mods->prefix_lens : nullptr;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
+  a.max_rows = rows_max;
   return cuda_status(launch_paged_attention(a, static_cast<const uint8_t*>(cache->k_codes),
-                                            static_cast<const uint8_t*>(cache->v_codes),
-                                            batch->query_start_loc ? max_query_len : 1, workspace, plan,
+                                            static_cast<const uint8_t*>(cache->v_codes), workspace, plan,
                                             (cudaStream_t)stream),
                      "paged attention launch");
 }

@@ -268,18 +268,26 @@ struct PagedAttnArgs {
   const int32_t* prefix_lens;       // [requests] positions that every row sees, or nullptr
   __nv_bfloat16* out;
   float* lse;
+  int32_t max_rows;                 // of a request; one with more is refused
+  int32_t lo_pairs, hi_pairs;       // a kernel takes requests of lo < rows * group <= hi pairs
   uint32_t* err;                    // the workspace header
-  int32_t* rec;                     // [ctas][4]: where each CTA's first piece lies
-  float* part_o;                    // [2 * ctas][columns][128]
+  int32_t* rec;                     // [ctas][8]: where each CTA's first piece lies
+  float* part_o;                    // [2 * ctas] pieces of a segment: [columns][128]
   float* part_ml;                   // [2 * ctas][columns][2]
 };
 constexpr int kPagedAttnColumns = 32;     // (row, head) pairs of a K/V head taken together, at most
+constexpr int kPagedAttnDirect = 64;      // requests of more pairs go to the prompt kernel
+constexpr int kPromptPairs = 256;         // pairs that it takes together
 struct PagedAttnPlan {
+  bool prompt;                            // a request may bring more than kPagedAttnDirect pairs
   size_t rec_offset, part_offset, workspace_bytes;
 };
-PagedAttnPlan plan_paged_attention();
-cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_query_len,
-                                   void* workspace, const PagedAttnPlan& plan, cudaStream_t s);
+PagedAttnPlan plan_paged_attention(int max_query_len, int group);
+cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, void* workspace,
+                                   const PagedAttnPlan& plan, cudaStream_t s);
+// requests of many rows (paged_prompt.cu)
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const uint8_t* k_codes, const uint8_t* v_codes, int ctas,
+                                cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // device helpers

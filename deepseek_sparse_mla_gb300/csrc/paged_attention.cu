@@ -36,15 +36,17 @@
 // full HBM speed a tile arrives every 1,360 cycles; two chains side by side keep up.  They share nothing while they
 // run: each has its own maxima, denominators and accumulator, joined in the segment's epilogue, which
 // the warpgroups take in turn.
-#include "dsa_internal.cuh"
+#include "paged_attention.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
+
+#include <algorithm>
 
 namespace dsa {
 using namespace sm100;
 
 namespace pa {
-constexpr int kTok = 128;                       // keys per tile
+constexpr int kTok = kPaTok;                    // keys per tile
 constexpr int kTileBytes = kTok * kKvDim;       // 16 KB of codes
 constexpr int kStageBytes = 2 * kTileBytes;     // K, then V
 constexpr int kStages = 5;
@@ -64,39 +66,6 @@ constexpr uint32_t kPolls = 1u << 22;
 constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 }  // namespace pa
 
-// Units of request b: column groups * key tiles (times K/V heads)
-struct PaShape {
-  int rows, groups, tiles, len;
-};
-
-// rows of request b, its first row, and the keys it may read
-__device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, int cols, int max_rows, int& row0, uint32_t& bits) {
-  PaShape s = {0, 0, 0, 0};
-  int n = 1;
-  row0 = b;
-  if (a.query_start_loc) {
-    row0 = a.query_start_loc[b];
-    const int64_t d = (int64_t)a.query_start_loc[b + 1] - row0;
-    if (d <= 0 || row0 < 0 || row0 + d > a.num_rows) return s;
-    if (d > max_rows) {
-      bits |= DSA_DEVICE_BAD_LENGTH;
-      return s;
-    }
-    n = (int)d;
-  }
-  const int64_t room = (int64_t)a.table_stride << a.log2_page;
-  int64_t len = max(a.seq_lens[b], 0);
-  if (len > room) {
-    bits |= DSA_DEVICE_BAD_PAGE;
-    len = room;
-  }
-  s.rows = n;
-  s.len = (int)len;
-  s.groups = (int)(((int64_t)n * a.group + cols - 1) / cols);
-  s.tiles = max(1, (int)((len + pa::kTok - 1) / pa::kTok));
-  return s;
-}
-
 // A run of tiles of one segment
 struct PaSeg {
   int b, h, cg, tile, n;       // first tile and number of tiles of this piece
@@ -104,7 +73,7 @@ struct PaSeg {
 };
 
 // The segment that unit u lies in, cut at u1.  end[b] = column groups * tiles of requests 0 .. b.
-__device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_t* end, int cols, int64_t u, int64_t u1) {
+__device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_t* end, int64_t u, int64_t u1) {
   int lo = 0, hi = a.num_requests - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -115,7 +84,8 @@ __device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_
   s.b = lo;
   const int first = lo ? end[lo - 1] : 0;
   uint32_t none = 0;
-  const PaShape sh = pa_shape(a, lo, cols, INT32_MAX, s.row0, none);
+  const PaShape sh = pa_shape(a, lo, none);
+  s.row0 = sh.row0;
   s.rows = sh.rows;
   s.len = sh.len;
   s.tiles = sh.tiles;
@@ -128,8 +98,6 @@ __device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_
   s.n = (int)min((int64_t)(sh.tiles - s.tile), u1 - u);
   return s;
 }
-
-__device__ __forceinline__ int64_t pa_unit_start(int c, int64_t units, int ctas) { return units * c / ctas; }
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r);
@@ -171,7 +139,7 @@ struct PaColumns {
 template <int kCE, bool kMods>
 __global__ void __launch_bounds__(pa::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                           const __grid_constant__ PagedAttnArgs a, int max_rows, int shared_keys) {
+                           const __grid_constant__ PagedAttnArgs a, int shared_keys) {
   using namespace pa;
   constexpr int kHalf = kCE < 16 ? 16 : kCE;          // columns of the hi half (and of the lo half)
   constexpr int kN = 2 * kHalf;                       // MMA N: 32 or 64
@@ -233,9 +201,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
-      int row0;
-      const PaShape s = pa_shape(a, b, kCE, max_rows, row0, bits);
-      sum += s.groups * s.tiles;
+      const PaShape s = pa_shape(a, b, bits);
+      sum += (s.rows * a.group + kCE - 1) / kCE * s.tiles;
       end[b] = sum;
     }
     int incl = sum;
@@ -270,7 +237,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     int i = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
-      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      const PaSeg s = pa_segment(a, end, u, u1);
       const int pages = (s.len + (1 << lp) - 1) >> lp;
       int batch = -1, page = -1;                       // 32 pages at a time, one a lane
       float ks = 0.f, vs = 0.f;
@@ -335,7 +302,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     int i = 0, seg = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       const int qb = seg % kQBufs;
       ok = mbar_wait(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls);
@@ -368,7 +335,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     int i = 0, seg = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       uint32_t fresh = 3;                              // accumulators of the segment without a product yet
       if (seg >= 2) ok = mbar_wait(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
@@ -398,7 +365,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     const int part = lane & 15;
     int seg = 0;
     for (int64_t u = u0; u < u1; ++seg) {
-      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       const int buf = seg % kQBufs;
       if (seg >= kQBufs && !mbar_wait(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
@@ -475,7 +442,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     int i0 = 0, seg = 0;                               // i0: the CTA's tiles before this segment
     for (int64_t u = u0; u < u1; ++seg) {
-      const PaSeg s = pa_segment(a, end, kCE, u, u1);
+      const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       const int qb = seg % kQBufs;
       if (!mbar_wait(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
@@ -727,7 +694,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         }
       }
       if (row == 0 && u - s.n == u0) {                   // for the join: this CTA's first piece
-        int32_t* rec = a.rec + 4 * cta;
+        int32_t* rec = a.rec + 8 * cta;
         rec[0] = s.b;
         rec[1] = s.h;
         rec[2] = s.cg;
@@ -788,13 +755,6 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   }
 }
 
-__device__ __forceinline__ int pa_cta_of_unit(int64_t u, int64_t units, int ctas) {
-  int c = (int)(u * ctas / units);
-  while (c + 1 < ctas && pa_unit_start(c + 1, units, ctas) <= u) ++c;
-  while (c > 0 && pa_unit_start(c, units, ctas) > u) --c;
-  return c;
-}
-
 // Joins the pieces of the segments that CTA boundaries cut:
 //   out = sum_p w_p O_p,  w_p = 2^{m_p - M} / L,  L = sum_p 2^{m_p - M} l_p.
 // CTA (c - 1, g) handles the boundary in front of range c if it is the first that cuts its segment, and
@@ -808,15 +768,14 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
   const int c = blockIdx.x + 1;
   const int64_t u = pa_unit_start(c, units, ctas);
   if (u == pa_unit_start(c + 1, units, ctas)) return;    // a range without units
-  const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + 4 * c));
+  const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + 8 * c));
   const int b = rec.x, h = rec.y, cg = rec.z, tile = rec.w;
   if (tile == 0) return;                                  // the range begins with a segment
   const int64_t seg = u - tile;
   const int first = pa_cta_of_unit(u - 1, units, ctas);
   if (pa_unit_start(first, units, ctas) > seg) return;    // an earlier boundary cuts it, too
-  int row0;
   uint32_t none = 0;
-  const PaShape s = pa_shape(a, b, columns, INT32_MAX, row0, none);
+  const PaShape s = pa_shape(a, b, none);
   const int col = 8 * blockIdx.y + warp, n = cg * columns + col;
   if (n >= s.rows * a.group) return;
   const int last = pa_cta_of_unit(seg + s.tiles - 1, units, ctas);
@@ -863,7 +822,7 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int i = n / a.group;
-  const int64_t at = (int64_t)(row0 + i) * a.kv_heads * a.group + h * a.group + (n - i * a.group);
+  const int64_t at = (int64_t)(s.row0 + i) * a.kv_heads * a.group + h * a.group + (n - i * a.group);
   const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), v1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   reinterpret_cast<uint2*>(a.out + at * kKvDim)[lane] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
@@ -873,19 +832,20 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-PagedAttnPlan plan_paged_attention() {
+PagedAttnPlan plan_paged_attention(int max_query_len, int group) {
   PagedAttnPlan p;
   const int ctas = device_sm_count();
+  p.prompt = (int64_t)max_query_len * group > kPagedAttnDirect;
   p.rec_offset = kWorkspaceHeader + ((size_t)ctas * sizeof(uint32_t) + 255) / 256 * 256;
-  p.part_offset = p.rec_offset + ((size_t)ctas * 4 * sizeof(int32_t) + 255) / 256 * 256;
-  p.workspace_bytes = p.part_offset + (size_t)2 * ctas * kPagedAttnColumns * (kKvDim + 2) * sizeof(float);
+  p.part_offset = p.rec_offset + ((size_t)ctas * 8 * sizeof(int32_t) + 255) / 256 * 256;
+  p.workspace_bytes =
+      p.part_offset + (size_t)2 * ctas * (p.prompt ? kPromptPairs : kPagedAttnColumns) * (kKvDim + 2) * sizeof(float);
   return p;
 }
 
 namespace {
 template <int kCE>
-cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int max_rows, int ctas,
-                           cudaStream_t s) {
+cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int ctas, cudaStream_t s) {
   const size_t smem = pa::kFixedSmem + (size_t)a.num_requests * sizeof(int32_t);
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = once_per_device(ready, [] {
@@ -896,9 +856,9 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
     return r;
   });
   if (e != cudaSuccess) return e;
-  const int shared_keys = (int64_t)max_rows * a.group > kCE ? 1 : 0;   // several column groups read the same keys
+  const int shared_keys = std::min<int64_t>((int64_t)a.max_rows * a.group, a.hi_pairs) > kCE ? 1 : 0;   // column groups share keys
   auto kernel = a.cap_log2 > 0.f || a.slopes ? paged_attention_kernel<kCE, true> : paged_attention_kernel<kCE, false>;
-  e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, max_rows, shared_keys);
+  e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, shared_keys);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (ctas > 1) {
@@ -909,23 +869,31 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
 }
 }  // namespace
 
-cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_query_len,
-                                   void* workspace, const PagedAttnPlan& plan, cudaStream_t s) {
+cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, void* workspace,
+                                   const PagedAttnPlan& plan, cudaStream_t s) {
   char* ws = static_cast<char*>(workspace);
   const int ctas = device_sm_count();
   a.err = reinterpret_cast<uint32_t*>(ws);
   a.rec = reinterpret_cast<int32_t*>(ws + plan.rec_offset);
   a.part_o = reinterpret_cast<float*>(ws + plan.part_offset);
+  a.lo_pairs = 0;
+  a.hi_pairs = plan.prompt ? kPagedAttnDirect : INT32_MAX;
   a.part_ml = a.part_o + (size_t)2 * ctas * kPagedAttnColumns * kKvDim;
   const uint64_t rows = (uint64_t)a.num_pages * a.kv_heads << a.log2_page;
   CUtensorMap k_map, v_map;
   if (!encode_2d(&k_map, k_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kKvDim, rows, kKvDim, kKvDim, 1u << a.log2_page) ||
       !encode_2d(&v_map, v_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kKvDim, rows, kKvDim, kKvDim, 1u << a.log2_page))
     return cudaErrorInvalidValue;
-  const int64_t pairs = (int64_t)max_query_len * a.group;
-  cudaError_t e = pairs <= 8    ? launch_columns<8>(a, k_map, v_map, max_query_len, ctas, s)
-                  : pairs <= 16 ? launch_columns<16>(a, k_map, v_map, max_query_len, ctas, s)
-                                : launch_columns<32>(a, k_map, v_map, max_query_len, ctas, s);
+  const int64_t pairs = (int64_t)a.max_rows * a.group;
+  cudaError_t e = pairs <= 8    ? launch_columns<8>(a, k_map, v_map, ctas, s)
+                  : pairs <= 16 ? launch_columns<16>(a, k_map, v_map, ctas, s)
+                                : launch_columns<32>(a, k_map, v_map, ctas, s);
+  if (e == cudaSuccess && plan.prompt) {
+    a.lo_pairs = kPagedAttnDirect;
+    a.hi_pairs = INT32_MAX;
+    a.part_ml = a.part_o + (size_t)2 * ctas * kPromptPairs * kKvDim;
+    e = launch_paged_prompt(a, k_codes, v_codes, ctas, s);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

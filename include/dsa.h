@@ -561,8 +561,8 @@ typedef struct {
 DSA_API dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride,
                                   const void* v, int64_t v_stride, void* stream);
 
-/* Scratch bytes dsa_paged_attention needs on the current device (the same for every shape). */
-DSA_API size_t dsa_paged_attention_workspace_bytes(void);
+/* Scratch bytes dsa_paged_attention needs on the current device.  0 for invalid arguments. */
+DSA_API size_t dsa_paged_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t max_query_len);
 
 /*
  * What a dense attention call may add to the plain causal form (all optional).
