@@ -37,7 +37,6 @@ constexpr int kTileBytes = kTok * kKvDim * 2;        // 32 KB of fp16: two 64-wi
 constexpr int kChunkBytes = kTok * 128;
 constexpr int kThreads = 512;
 constexpr int kConvWarp0 = 8, kMmaWarp = 12, kQueryWarp0 = 13;
-constexpr uint32_t kRegsSoft = 176, kRegsConv = 104, kRegsRest = 56;   // 2 * 176 + 104 + 56 = 512 = 4 * 128
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
@@ -126,6 +125,115 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ uint32_t mul2(uint32_t x, __half2 f) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), f);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 16 consecutive 32-bit columns of the warp's lanes written from registers
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14,"
+      " %15, %16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15},"
+      " [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// A softmax thread's row of a tile: its scores lie in TMEM and are read twice, one 16-key group at a time
+// (holding all 128 took 176 registers and spilled), once for the maximum and once for the probabilities.
+struct PpRow {
+  uint32_t tS;                     // TMEM address of the scores
+  int key0, limit, pos;
+  uint32_t bad;                    // 16-key groups without a valid page
+  float slope;
+};
+
+// The largest score, times its page's factor.  With mods the scores are capped, biased and masked here, and go
+// back to TMEM; without, only masked ones are left out.
+template <bool kMods, bool kMasked>
+__device__ __forceinline__ float pp_max(const PpRow& w, const PagedAttnArgs& a, const float* ks, float cf) {
+  float top = -INFINITY;
+  const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
+  uint32_t r[2][16];
+  tmem_ld16(w.tS, r[0]);
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    tmem_wait_ld();
+    if (g < 7) tmem_ld16(w.tS + 16 * (g + 1), r[(g + 1) & 1]);
+    uint32_t* x = r[g & 1];
+    const float kc = ks[g] * cf;
+    float z[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) z[c] = __uint_as_float(x[c]);
+    if (kMods) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        z[c] *= kc;
+        if (in != 0.f) {
+          const float y = z[c] * in;
+          z[c] = a.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(y > 64.f ? 64.f : y)));   // NaN stays
+        }
+        z[c] -= w.slope * (float)abs(w.pos - (w.key0 + 16 * g + c));
+      }
+    }
+    if (kMasked) {
+      const int left = ((w.bad >> g) & 1u) ? 0 : w.limit - w.key0 - 16 * g;   // keys of the group that are seen
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        if (c >= left) z[c] = -INFINITY;
+    }
+    float m = z[0];
+#pragma unroll
+    for (int c = 1; c < 16; ++c) m = fmaxf(m, z[c]);
+    // a scale of 0 makes every score 0, where -inf * 0 would be NaN
+    top = fmaxf(top, kMods || (kMasked && m == -INFINITY) ? m : m * kc);
+    if (kMods) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(z[c]);
+      tmem_st16(w.tS + 16 * g, x);
+    }
+  }
+  if (kMods) tmem_wait_st();
+  return top;
+}
+
+// P = 2^(z + shift) in fp16 over the scores' first columns; returns the row's sum of it in fp32.
+template <bool kMods, bool kMasked>
+__device__ __forceinline__ float pp_exp(const PpRow& w, const float* ks, float cf, float shift) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t r[2][16], p[16];
+  tmem_ld16(w.tS, r[0]);
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    tmem_wait_ld();
+    if (g < 7) tmem_ld16(w.tS + 16 * (g + 1), r[(g + 1) & 1]);
+    const uint32_t* x = r[g & 1];
+    const float kc = kMods ? 1.f : ks[g] * cf;
+    const int left = !kMasked || kMods ? 16 : ((w.bad >> g) & 1u) ? 0 : w.limit - w.key0 - 16 * g;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      float y0 = fmaf(__uint_as_float(x[c]), kc, shift), y1 = fmaf(__uint_as_float(x[c + 1]), kc, shift);
+      if (kMasked && !kMods) {
+        if (c >= left) y0 = -INFINITY;
+        if (c + 1 >= left) y1 = -INFINITY;
+      }
+      y0 = ex2_approx(y0);
+      y1 = ex2_approx(y1);
+      sum[(c >> 1) & 3] += y0 + y1;
+      const __half2 h = __floats2half2_rn(y0, y1);
+      p[8 * (g & 1) + (c >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    // the columns written, 8 (g - 1) .. 8 g + 7, hold scores that have been read
+    if (g & 1) tmem_st16(w.tS + 8 * (g - 1), p);
+  }
+  tmem_wait_st();
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 template <bool kMods>
@@ -260,7 +368,6 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   }
 
   if (warp < kConvWarp0) {
-    regs_inc<kRegsSoft>();
     // ---------------------------------------------------------------- softmax and outputs: one pair a thread
     const int q = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
@@ -287,66 +394,24 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (t == 0) cf = factor[seg & 1][kHalfPairs * q + row];
-        float z[kTok];
-        {
-          uint32_t(*rr)[32] = reinterpret_cast<uint32_t(*)[32]>(z);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, rr[c]);
-        }
-        float kc[8];
-        {
-          const float4 x = *reinterpret_cast<const float4*>(&sks[i % kMetaBufs][0]), y = *reinterpret_cast<const float4*>(&sks[i % kMetaBufs][4]);
-          kc[0] = x.x * cf, kc[1] = x.y * cf, kc[2] = x.z * cf, kc[3] = x.w * cf;
-          kc[4] = y.x * cf, kc[5] = y.y * cf, kc[6] = y.z * cf, kc[7] = y.w * cf;
-        }
-        const uint32_t bad = sbad[i % kMetaBufs];
-        tmem_wait_ld();
-        if (kMods) {
-          if (a.cap_log2 > 0.f) {
-            const float in = 2.f * 1.4426950408889634f / a.cap_log2;
-#pragma unroll
-            for (int c = 0; c < kTok; ++c) {
-              const float x = z[c] * (kc[c >> 4] * in);
-              z[c] = a.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(x > 64.f ? 64.f : x)));   // NaN stays
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kTok; ++c) z[c] *= kc[c >> 4];
-          }
-#pragma unroll
-          for (int c = 0; c < kTok; ++c) z[c] -= slope * (float)abs(pos - (key0 + c));
-#pragma unroll
-          for (int g = 0; g < 8; ++g) kc[g] = 1.f;
-        }
-        if (key0 + kTok > min_limit || bad) {          // uniform in the warpgroup
-#pragma unroll
-          for (int c = 0; c < kTok; ++c)
-            if (key0 + c >= limit || ((bad >> (c >> 4)) & 1u)) z[c] = -INFINITY;
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float x = z[16 * g];
-#pragma unroll
-          for (int c = 1; c < 16; ++c) x = fmaxf(x, z[16 * g + c]);
-          // a scale of 0 makes every score 0, where -inf * 0 would be NaN
-          top = fmaxf(top, x == -INFINITY ? x : x * kc[g]);
-        }
+        const float* ks = sks[i % kMetaBufs];
+        const PpRow w = {tS, key0, limit, pos, sbad[i % kMetaBufs], slope};
+        const bool masked = key0 + kTok > min_limit || w.bad;          // uniform in the warpgroup
+        const float top = masked ? pp_max<kMods, true>(w, a, ks, cf) : pp_max<kMods, false>(w, a, ks, cf);
         const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? top : m;
-          const float al = m == -INFINITY ? 0.f : ex2_approx(m - m_new);
+          const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - m_new);
           if (t > 0) {
             // the accumulator is settled: this half's previous product came before these scores
-            l *= m_new == m ? 1.f : al;
+            l *= al;
 #pragma unroll 1
             for (int c = 0; c < kKvDim; c += 32) {
               uint32_t o[32];
               tmem_ld32(tO + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                o[k] = m_new == m ? o[k] : __float_as_uint(__uint_as_float(o[k]) * al);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
               tmem_st32(tO + c, o);
             }
             tmem_wait_st();
@@ -354,28 +419,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           m = m_new;
         }
         const float shift = kPLog2 - (m == -INFINITY ? 0.f : m);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c0 = 0; c0 < kTok; c0 += 64) {
-          uint32_t p[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            float x0, x1;
-            if (key0 + kTok > min_limit || bad) {      // a masked score stays out of a product with a scale of 0
-              x0 = z[c0 + c] == -INFINITY ? 0.f : ex2_approx(fmaf(z[c0 + c], kc[(c0 + c) >> 4], shift));
-              x1 = z[c0 + c + 1] == -INFINITY ? 0.f : ex2_approx(fmaf(z[c0 + c + 1], kc[(c0 + c) >> 4], shift));
-            } else {
-              x0 = ex2_approx(fmaf(z[c0 + c], kc[(c0 + c) >> 4], shift));
-              x1 = ex2_approx(fmaf(z[c0 + c + 1], kc[(c0 + c) >> 4], shift));
-            }
-            sum[(c >> 1) & 3] += x0 + x1;
-            const __half2 h = __floats2half2_rn(x0, x1);
-            p[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          tmem_st32(tS + (c0 >> 1), p);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
+        l += masked ? pp_exp<kMods, true>(w, ks, cf, shift) : pp_exp<kMods, false>(w, ks, cf, shift);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[q]);
@@ -445,7 +489,6 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       if (lane == 0) mbar_arrive(&o_empty[q]);
     }
   } else if (warp < kMmaWarp) {
-    regs_dec<kRegsConv>();
     // ---------------------------------------------------------------- K and V tiles: codes to fp16
     // Eight lanes a row of 16-byte pieces, 16 rows a pass over the four warps: a pass is one 16-key group, and so
     // lies in one page.  The next tile's codes are in flight while this one is converted.
@@ -577,7 +620,6 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       }
     }
   } else {
-    regs_dec<kRegsRest>();
     if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- products
       // Order: .. O0(i) S0(i+1) O1(i) S1(i+1) ..: while one half's softmax runs, the tensor cores work for the other.
