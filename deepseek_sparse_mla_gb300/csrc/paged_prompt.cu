@@ -18,9 +18,9 @@
 // (persistent, one CTA per SM), as in paged_attention.cu; a segment that is cut leaves fp32 pieces for a join.
 // Segments count the tiles their last row sees, so causal rows are balanced over the CTAs.
 //
-// Per CTA (16 warps): warps 0-3 and 4-7 are the softmax of the two 128-pair halves, one pair a thread (no
-// cross-lane work at all), which alternate with each other on the tensor cores; warps 8-11 load codes, widen
-// them and write the K and V tiles; warp 12 issues the products; warps 13-15 load the next segment's queries.
+// Per CTA (20 warps): warps 0-3 and 4-7 are the softmax of the two 128-pair halves, one pair a thread (no
+// cross-lane work at all), which alternate with each other on the tensor cores; warps 8-15 load codes, widen
+// them and write the K and V tiles; warp 16 issues the products; warps 17-19 load the next segment's queries.
 // TMEM (all 512 columns): S of half q at 128 q, with P over its first 64 columns; O of half q at 256 + 128 q.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
@@ -35,13 +35,14 @@ constexpr int kTok = kPaTok;
 constexpr int kHalfPairs = 128;
 constexpr int kTileBytes = kTok * kKvDim * 2;        // 32 KB of fp16: two 64-wide column chunks of 128-byte rows
 constexpr int kChunkBytes = kTok * 128;
-constexpr int kThreads = 512;
-constexpr int kConvWarp0 = 8, kMmaWarp = 12, kQueryWarp0 = 13;
+constexpr int kThreads = 640;
+constexpr int kConvWarp0 = 8, kMmaWarp = 16, kQueryWarp0 = 17;
+constexpr uint32_t kRegsSoft = 112, kRegsConv = 96, kRegsRest = 64;   // 2 * 112 + 2 * 96 + 64 = 480 = 5 * 96, the launch's
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
 constexpr uint32_t kPolls = 1u << 22;
-constexpr int kRuns = kThreads;                      // runs of (request, pairs) entries that are summed
+constexpr int kRuns = 512;                           // runs of (request, pairs) entries that are summed
 constexpr int kMetaBufs = 4;
 constexpr int kFixedSmem = 6 * kTileBytes + 1024;    // two halves of Q, two K tiles, two V tiles
 }  // namespace pp
@@ -127,6 +128,26 @@ __device__ __forceinline__ uint32_t mul2(uint32_t x, __half2 f) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// two fp32 values in one 64-bit register pair (one instruction for both)
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // 16 consecutive 32-bit columns of the warp's lanes written from registers
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -145,95 +166,121 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// A softmax thread's row of a tile: its scores lie in TMEM and are read twice, one 16-key group at a time
-// (holding all 128 took 176 registers and spilled), once for the maximum and once for the probabilities.
+// eight columns, as tmem_st16
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// A softmax thread's row: its reference m (log2 units), its sum l of P, and what masks and biases need.
 struct PpRow {
-  uint32_t tS;                     // TMEM address of the scores
-  int key0, limit, pos;
-  uint32_t bad;                    // 16-key groups without a valid page
-  float slope;
+  float m, l, cf, slope;
+  int limit, pos;
 };
 
-// The largest score, times its page's factor.  With mods the scores are capped, biased and masked here, and go
-// back to TMEM; without, only masked ones are left out.
+// A row's reference moves from m to m + something: what was summed and stored against the old one shrinks by al.
+// done: 16-key groups of this tile whose P is in TMEM already.
+__device__ __forceinline__ void pp_shrink(uint32_t tS, uint32_t tO, int done, bool has_o, float al) {
+  const __half2 h = __float2half2_rn(al);
+#pragma unroll 1
+  for (int g = 0; g < done; ++g) {
+    uint32_t p[8];
+    tmem_ld8(tS + 8 * g, p);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = mul2(p[k], h);
+    tmem_st8(tS + 8 * g, p);
+  }
+  if (has_o) {
+#pragma unroll 1
+    for (int c = 0; c < kKvDim; c += 8) {
+      uint32_t o[8];
+      tmem_ld8(tO + c, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+      tmem_st8(tO + c, o);
+    }
+  }
+  tmem_wait_st();
+}
+
+// One tile of a row, in one pass over its scores: 16 keys at a time the scores come out of TMEM, their largest
+// is held against the reference (which moves only when exceeded by 2^kSlack, seldom after the first
+// keys), and P goes back over scores that have been read.  Holding all 128 scores for an exact maximum
+// first took 176 registers, and reading them twice 15 % more time.
 template <bool kMods, bool kMasked>
-__device__ __forceinline__ float pp_max(const PpRow& w, const PagedAttnArgs& a, const float* ks, float cf) {
-  float top = -INFINITY;
+__device__ __forceinline__ void pp_tile(PpRow& w, const PagedAttnArgs& a, uint32_t tS, uint32_t tO, int key0, uint32_t bad,
+                                        const float* ks, bool has_o) {
   const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
+  uint64_t sum = 0;
   uint32_t r[2][16];
-  tmem_ld16(w.tS, r[0]);
+  float shift = pp::kPLog2 - (w.m == -INFINITY ? 0.f : w.m);
+  tmem_ld16(tS, r[0]);
 #pragma unroll
   for (int g = 0; g < 8; ++g) {
     tmem_wait_ld();
-    if (g < 7) tmem_ld16(w.tS + 16 * (g + 1), r[(g + 1) & 1]);
+    if (g < 7) tmem_ld16(tS + 16 * (g + 1), r[(g + 1) & 1]);
     uint32_t* x = r[g & 1];
-    const float kc = ks[g] * cf;
-    float z[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) z[c] = __uint_as_float(x[c]);
+    float kc = ks[g] * w.cf;
     if (kMods) {
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        z[c] *= kc;
+        float z = __uint_as_float(x[c]) * kc;
         if (in != 0.f) {
-          const float y = z[c] * in;
-          z[c] = a.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(y > 64.f ? 64.f : y)));   // NaN stays
+          const float y = z * in;
+          z = a.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(y > 64.f ? 64.f : y)));   // NaN stays
         }
-        z[c] -= w.slope * (float)abs(w.pos - (w.key0 + 16 * g + c));
+        x[c] = __float_as_uint(z - w.slope * (float)abs(w.pos - (key0 + 16 * g + c)));
       }
+      kc = 1.f;
     }
     if (kMasked) {
-      const int left = ((w.bad >> g) & 1u) ? 0 : w.limit - w.key0 - 16 * g;   // keys of the group that are seen
+      // a masked score is -inf whatever the factor (which may be 0): they are scaled first
+      const int left = ((bad >> g) & 1u) ? 0 : w.limit - key0 - 16 * g;   // keys of the group that are seen
 #pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (c >= left) z[c] = -INFINITY;
+      for (int c = 0; c < 16; ++c) x[c] = c < left ? __float_as_uint(__uint_as_float(x[c]) * kc) : 0xFF800000u;
+      kc = 1.f;
     }
-    float m = z[0];
+    float top = __uint_as_float(x[0]);
 #pragma unroll
-    for (int c = 1; c < 16; ++c) m = fmaxf(m, z[c]);
-    // a scale of 0 makes every score 0, where -inf * 0 would be NaN
-    top = fmaxf(top, kMods || (kMasked && m == -INFINITY) ? m : m * kc);
-    if (kMods) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(z[c]);
-      tmem_st16(w.tS + 16 * g, x);
+    for (int c = 1; c < 16; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+    top *= kc;
+    const bool grow = top > w.m + pp::kSlack || (w.m == -INFINITY && top > w.m);
+    if (__any_sync(0xffffffffu, grow)) {
+      const float m_new = grow ? top : w.m;
+      const float al = m_new == w.m ? 1.f : w.m == -INFINITY ? 0.f : ex2_approx(w.m - m_new);
+      pp_shrink(tS, tO, g, has_o, al);
+      w.l *= al;
+      sum = fma2(sum, pack2(al, al), 0);
+      w.m = m_new;
+      shift = pp::kPLog2 - (m_new == -INFINITY ? 0.f : m_new);
     }
-  }
-  if (kMods) tmem_wait_st();
-  return top;
-}
-
-// P = 2^(z + shift) in fp16 over the scores' first columns; returns the row's sum of it in fp32.
-template <bool kMods, bool kMasked>
-__device__ __forceinline__ float pp_exp(const PpRow& w, const float* ks, float cf, float shift) {
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  uint32_t r[2][16], p[16];
-  tmem_ld16(w.tS, r[0]);
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    tmem_wait_ld();
-    if (g < 7) tmem_ld16(w.tS + 16 * (g + 1), r[(g + 1) & 1]);
-    const uint32_t* x = r[g & 1];
-    const float kc = kMods ? 1.f : ks[g] * cf;
-    const int left = !kMasked || kMods ? 16 : ((w.bad >> g) & 1u) ? 0 : w.limit - w.key0 - 16 * g;
+    const uint64_t kc2 = pack2(kc, kc), shift2 = pack2(shift, shift);
+    uint32_t p[8];
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
-      float y0 = fmaf(__uint_as_float(x[c]), kc, shift), y1 = fmaf(__uint_as_float(x[c + 1]), kc, shift);
-      if (kMasked && !kMods) {
-        if (c >= left) y0 = -INFINITY;
-        if (c + 1 >= left) y1 = -INFINITY;
-      }
+      float y0, y1;
+      unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), kc2, shift2), y0, y1);
       y0 = ex2_approx(y0);
       y1 = ex2_approx(y1);
-      sum[(c >> 1) & 3] += y0 + y1;
+      sum = add2(sum, pack2(y0, y1));
       const __half2 h = __floats2half2_rn(y0, y1);
-      p[8 * (g & 1) + (c >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
+      p[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    // the columns written, 8 (g - 1) .. 8 g + 7, hold scores that have been read
-    if (g & 1) tmem_st16(w.tS + 8 * (g - 1), p);
+    // columns 8 g .. 8 g + 7 hold scores that have been read
+    tmem_st8(tS + 8 * g, p);
   }
+  float s0, s1;
+  unpack2(sum, s0, s1);
+  w.l += s0 + s1;
   tmem_wait_st();
-  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 template <bool kMods>
@@ -328,7 +375,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   };
   {
     int sum = 0;
-    const int x0 = min(entries, tid * run), x1 = min(entries, x0 + run);
+    const int x0 = min(entries, min(tid, kRuns) * run), x1 = tid < kRuns ? min(entries, x0 + run) : x0;
     if (x0 < x1) {
       PpCursor c;
       find(x0, c);
@@ -343,7 +390,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       }
     }
     const int incl = block_sum(sum);
-    run_units[tid] = incl - sum;
+    if (tid < kRuns) run_units[tid] = incl - sum;
     __syncthreads();
     if (tid == kThreads - 1) scan[0] = incl;
   }
@@ -368,6 +415,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   }
 
   if (warp < kConvWarp0) {
+    regs_inc<kRegsSoft>();
     // ---------------------------------------------------------------- softmax and outputs: one pair a thread
     const int q = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
@@ -385,7 +433,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       // keys below it are seen by every pair of this half
       const int min_limit = pp_limit(s.e, min(s.e.qt * kPromptPairs + kHalfPairs * q, pairs - 1) / a.group);
       const float slope = kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f;
-      float cf = 0.f, m = -INFINITY, l = 0.f;
+      PpRow w = {-INFINITY, 0.f, 0.f, slope, limit, pos};
       for (int t = 0; t < s.n; ++t, ++i) {
         const int key0 = (s.tile + t) * kTok;
         // The scores' arrival also stands for the tile's scales and the queries' factors: their own barriers may be
@@ -393,33 +441,11 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         ok = mbar_wait(&s_full[q], i & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         tc_fence_after();
-        if (t == 0) cf = factor[seg & 1][kHalfPairs * q + row];
+        if (t == 0) w.cf = factor[seg & 1][kHalfPairs * q + row];
         const float* ks = sks[i % kMetaBufs];
-        const PpRow w = {tS, key0, limit, pos, sbad[i % kMetaBufs], slope};
-        const bool masked = key0 + kTok > min_limit || w.bad;          // uniform in the warpgroup
-        const float top = masked ? pp_max<kMods, true>(w, a, ks, cf) : pp_max<kMods, false>(w, a, ks, cf);
-        const bool grow = top > m + kSlack || (m == -INFINITY && top > m);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = grow ? top : m;
-          const float al = m_new == m ? 1.f : m == -INFINITY ? 0.f : ex2_approx(m - m_new);
-          if (t > 0) {
-            // the accumulator is settled: this half's previous product came before these scores
-            l *= al;
-#pragma unroll 1
-            for (int c = 0; c < kKvDim; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-              tmem_st32(tO + c, o);
-            }
-            tmem_wait_st();
-          }
-          m = m_new;
-        }
-        const float shift = kPLog2 - (m == -INFINITY ? 0.f : m);
-        l += masked ? pp_exp<kMods, true>(w, ks, cf, shift) : pp_exp<kMods, false>(w, ks, cf, shift);
+        const uint32_t bad = sbad[i % kMetaBufs];
+        if (key0 + kTok > min_limit || bad) pp_tile<kMods, true>(w, a, tS, tO, key0, bad, ks, t > 0);
+        else pp_tile<kMods, false>(w, a, tS, tO, key0, bad, ks, t > 0);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[q]);
@@ -431,6 +457,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       ok = mbar_wait(&o_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
       tc_fence_after();
+      const float m = w.m, l = w.l;
       const bool any = l > 0.f || l != l;
       const int64_t at = (int64_t)(s.e.shape.row0 + r) * a.kv_heads * a.group + head;
       const float vref = v_ref[seg % kMetaBufs];
@@ -489,11 +516,19 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       if (lane == 0) mbar_arrive(&o_empty[q]);
     }
   } else if (warp < kMmaWarp) {
+    regs_dec<kRegsConv>();
     // ---------------------------------------------------------------- K and V tiles: codes to fp16
-    // Eight lanes a row of 16-byte pieces, 16 rows a pass over the four warps: a pass is one 16-key group, and so
-    // lies in one page.  The next tile's codes are in flight while this one is converted.
-    const int cw = warp - kConvWarp0, part = lane & 7, sub = 4 * cw + (lane >> 3), lp = a.log2_page;
+    // Four warps for K and four for V: eight lanes a row of 16-byte pieces, 16 rows a pass, so that a pass is one
+    // 16-key group and lies in one page.  A tile's loads go out right after the last tile's fence, which
+    // waits for the loads in flight too: one warp doing both K and V with its loads ahead took 7,000 cycles
+    // a tile, most of them in fences, against the 2,000 of the products.
+    const bool is_v = warp >= kConvWarp0 + 4;
+    const int cw = (warp - kConvWarp0) & 3, part = lane & 7, sub = 4 * cw + (lane >> 3), lp = a.log2_page;
     const int unit = 2 * (part & 3), swap = part >> 2;
+    uint64_t* const full = is_v ? v_full : k_full;
+    uint64_t* const empty = is_v ? v_empty : k_empty;
+    const float* const scales = is_v ? a.v_scales : a.k_scales;
+    uint8_t* const tiles = (is_v ? sV : sK) + (part >> 2) * kChunkBytes;
     int i = 0, seg = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
@@ -501,95 +536,71 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       u += s.n;
       const int len = s.e.shape.len, pages = (len + (1 << lp) - 1) >> lp;
       const int32_t* table = a.block_table + (int64_t)s.e.b * a.table_stride;
-      auto page_of = [&](int key) {
+      // this lane's 16 bytes of row 0 of page 0; a page further is page_step bytes on
+      const uint8_t* const base = (is_v ? v_codes : k_codes) + ((int64_t)s.h << lp) * kKvDim + 16 * part;
+      const int64_t page_step = ((int64_t)a.kv_heads << lp) * kKvDim;
+      constexpr int kNoPage = INT32_MIN;               // past the request's pages
+      auto id_of = [&](int key) {
         const int p = key >> lp;
-        int id = -1;
-        if (p < pages) {
-          id = table[p];
-          if (id < 0 || id >= a.num_pages) {
-            atomicOr(err, kErrBadPage);
-            id = -1;
-          }
-        }
-        return id;
+        return p < pages ? table[p] : kNoPage;
+      };
+      auto checked = [&](int id) {
+        if (id >= 0 && id < a.num_pages) return id;
+        if (id != kNoPage) atomicOr(err, kErrBadPage);
+        return -1;
       };
       // V's reference: the power of two at or below the piece's largest scale
-      {
+      float vinv = 1.f;
+      if (is_v) {
         float top = 0.f;
         const int p0 = (s.tile * kTok) >> lp, p1 = min(pages, ((s.tile + s.n) * kTok) >> lp);
 #pragma unroll 4
         for (int p = p0 + 32 * cw + lane; p < p1; p += 128) {
           const int id = table[p];
-          if (id >= 0 && id < a.num_pages) top = fmaxf(top, fabsf(a.v_scales[(int64_t)id * a.kv_heads + s.h]));
+          if (id >= 0 && id < a.num_pages) top = fmaxf(top, fabsf(scales[(int64_t)id * a.kv_heads + s.h]));
         }
         top = warp_max_f32(top);
         if (lane == 0) vmax_part[cw] = top;
         nan_key[seg % kMetaBufs][32 * cw + lane] = INT32_MAX;
         named_bar_sync(1, 128);
+        top = fmaxf(fmaxf(vmax_part[0], vmax_part[1]), fmaxf(vmax_part[2], vmax_part[3]));
+        const uint32_t top_bits = __float_as_uint(top) & 0x7F800000u;
+        const float vref = top_bits && top_bits < 0x7F800000u ? __uint_as_float(top_bits) : 1.f;
+        if (cw == 0 && lane == 0) v_ref[seg % kMetaBufs] = vref;
+        vinv = 1.f / vref;
+        named_bar_sync(1, 128);
       }
-      const float top = fmaxf(fmaxf(vmax_part[0], vmax_part[1]), fmaxf(vmax_part[2], vmax_part[3]));
-      const uint32_t top_bits = __float_as_uint(top) & 0x7F800000u;
-      const float vref = top_bits && top_bits < 0x7F800000u ? __uint_as_float(top_bits) : 1.f;
-      if (cw == 0 && lane == 0) v_ref[seg % kMetaBufs] = vref;
-      const float vinv = 1.f / vref;
-      named_bar_sync(1, 128);
       const int min_limit = pp_limit(s.e, min(s.e.qt * kPromptPairs, s.e.shape.rows * a.group - 1) / a.group);
 
-      uint4 kx[8], vx[8];
-      auto load = [&](const uint8_t* codes, int id8, int key0, uint4* x) {
+      uint4 x[8];
+      float scale = 0.f;
+      // lane g (and g + 8, ..): the page of 16-key group g, of this tile and (not checked yet) of the next one
+      int id = checked(id_of(s.tile * kTok + 16 * part)), id2 = id_of((s.tile + 1) * kTok + 16 * part);
+      auto load = [&](int key0) {
+        scale = id >= 0 ? scales[(int64_t)id * a.kv_heads + s.h] : 0.f;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          const int id = __shfl_sync(0xffffffffu, id8, g), key = key0 + 16 * g + sub;
+          const int page = __shfl_sync(0xffffffffu, id, g), key = key0 + 16 * g + sub;
           x[g] = make_uint4(0, 0, 0, 0);
-          if (id >= 0 && key < len) {
-            const int64_t row = (((int64_t)id * a.kv_heads + s.h) << lp) + (key & ((1 << lp) - 1));
-            x[g] = __ldg(reinterpret_cast<const uint4*>(codes + row * kKvDim) + part);
-          }
+          if (page >= 0 && key < len)
+            x[g] = __ldg(reinterpret_cast<const uint4*>(base + page * page_step + (key & ((1 << lp) - 1)) * kKvDim));
         }
       };
-      auto scale_of = [&](const float* scales, int id) { return id >= 0 ? scales[(int64_t)id * a.kv_heads + s.h] : 0.f; };
-      int id = page_of(s.tile * kTok + 16 * part);     // lane g: the page of 16-key group g (lanes 8.. repeat)
-      float ks = scale_of(a.k_scales, id), vs = scale_of(a.v_scales, id);
-      load(k_codes, id, s.tile * kTok, kx);
-      load(v_codes, id, s.tile * kTok, vx);
-      for (int t = 0; t < s.n && ok; ++t, ++i) {
+      load(s.tile * kTok);
+      for (int t = 0; t < s.n; ++t, ++i) {
         const int key0 = (s.tile + t) * kTok, buf = i & 1;
-        const bool more = t + 1 < s.n;
-        const int next_id = more ? page_of(key0 + kTok + 16 * part) : -1;
-        if (i >= 2) ok = mbar_wait(&k_empty[buf], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+        if (i >= 2) ok = mbar_wait(&empty[buf], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
-        uint8_t* kt = sK + buf * kTileBytes + (part >> 2) * kChunkBytes;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const int r = 16 * g + sub;
-          const uint4 lo = widen8(kx[g].x, kx[g].y), hi = widen8(kx[g].z, kx[g].w);
-          // lanes of the two column chunks start with different units, so that eight lanes fill all banks
-          *reinterpret_cast<uint4*>(kt + r * 128 + (((unit + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(kt + r * 128 + (((unit + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
-        }
-        if (cw == 0) {
-          if (lane < 8) sks[i % kMetaBufs][lane] = ks;
-          const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && id < 0);
-          if (lane == 0) sbad[i % kMetaBufs] = bad;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[buf]);
-        const float ratio = vs * vinv;
-        if (more) {
-          ks = scale_of(a.k_scales, next_id);
-          vs = scale_of(a.v_scales, next_id);
-          load(k_codes, next_id, key0 + kTok, kx);
-        }
         // a NaN code of a key that only some rows see: out of the tile, and noted for the rows that see it
-        if (key0 + kTok > min_limit) {
+        if (is_v && key0 + kTok > min_limit) {
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(&vx[g]);
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x[g]);
             uint32_t any = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) any |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
             if (any) {
+#pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const uint32_t f = ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                 for (int k = 0; k < 4; ++k)
@@ -599,27 +610,38 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             }
           }
         }
-        if (i >= 2) ok = mbar_wait(&v_empty[buf], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
-        if (!ok) break;
-        uint8_t* vt = sV + buf * kTileBytes + (part >> 2) * kChunkBytes;
+        uint8_t* tile = tiles + buf * kTileBytes;
+        const float ratio = scale * vinv;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const int r = 16 * g + sub;
-          const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, g));
-          uint4 lo = widen8(vx[g].x, vx[g].y), hi = widen8(vx[g].z, vx[g].w);
-          lo = make_uint4(mul2(lo.x, f), mul2(lo.y, f), mul2(lo.z, f), mul2(lo.w, f));
-          hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
-          *reinterpret_cast<uint4*>(vt + r * 128 + (((unit + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(vt + r * 128 + (((unit + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+          uint4 lo = widen8(x[g].x, x[g].y), hi = widen8(x[g].z, x[g].w);
+          if (is_v) {
+            const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, g));
+            lo = make_uint4(mul2(lo.x, f), mul2(lo.y, f), mul2(lo.z, f), mul2(lo.w, f));
+            hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
+          }
+          // lanes of the two column chunks start with different units, so that eight lanes fill all banks
+          *reinterpret_cast<uint4*>(tile + r * 128 + (((unit + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(tile + r * 128 + (((unit + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+        }
+        if (!is_v && cw == 0) {
+          if (lane < 8) sks[i % kMetaBufs][lane] = scale;
+          const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && id < 0);
+          if (lane == 0) sbad[i % kMetaBufs] = bad;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_full[buf]);
-        if (more) load(v_codes, next_id, key0 + kTok, vx);
-        id = next_id;
+        if (lane == 0) mbar_arrive(&full[buf]);
+        if (t + 1 < s.n) {
+          id = checked(id2);
+          id2 = id_of(key0 + 2 * kTok + 16 * part);
+          load(key0 + kTok);
+        }
       }
     }
   } else {
+    regs_dec<kRegsRest>();
     if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- products
       // Order: .. O0(i) S0(i+1) O1(i) S1(i+1) ..: while one half's softmax runs, the tensor cores work for the other.
