@@ -285,9 +285,6 @@ struct PagedAttnPlan {
 PagedAttnPlan plan_paged_attention(int max_query_len, int group);
 cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, void* workspace,
                                    const PagedAttnPlan& plan, cudaStream_t s);
-// requests of many rows (paged_prompt.cu)
-cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const uint8_t* k_codes, const uint8_t* v_codes, int ctas,
-                                cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // device helpers

@@ -62,7 +62,7 @@ constexpr uint32_t kTmemCols = 512;             // S^T of warpgroup w at 64 w, O
 constexpr uint32_t kColO = 128;
 constexpr float kSlack = 2.f;                   // log2 by which a maximum may be exceeded
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
-constexpr uint32_t kPolls = 1u << 22;
+constexpr uint32_t kPolls = 1u << 17;           // about a second
 constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 }  // namespace pa
 
@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   if (kCE < kHalf)                                     // columns that no query fills stay zero
     for (int i = tid; i < kQBufs * kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
+  if (tid == 0) a.rec[8 * cta] = -1;                   // no piece to join until it has been written
   // running sums of the requests' units: every thread a run of consecutive requests
   {
     uint32_t bits = 0;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           }
         }
         const int st = i % kStages, use = i / kStages;
-        if (use > 0 && !mbar_wait(&kv_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) {
+        if (use > 0 && !mbar_wait_warp(&kv_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) {
           ok = false;
           break;
         }
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     // nothing may still be landing in shared memory when the CTA exits
     for (int st = 0; st < kStages; ++st) {
       const int uses = (i - st + kStages - 1) / kStages;
-      if (i > st) mbar_wait(&kv_full[st], (uses - 1) & 1, err, kErrTmaTimeout, kPolls);
+      if (i > st) mbar_wait_warp(&kv_full[st], (uses - 1) & 1, err, kErrTmaTimeout, kPolls);
     }
   } else if (warp == kScoreWarp) {
     // ---------------------------------------------------------------- products of the scores
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       const int qb = seg % kQBufs;
-      ok = mbar_wait(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls);
+      ok = mbar_wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls);
       for (int t = 0; t < s.n && ok; ++t, ++i) {
         const int st = i % kStages, sb = i & 1;
         ok = mbar_spin(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout);
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     }
     // every MMA issued here has finished before TMEM is released
     if (leader) mma_commit(&mma_done);
-    mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+    mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
   } else if (warp == kOutWarp) {
     // ---------------------------------------------------------------- products of the outputs
     const bool leader = elect_one();
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       uint32_t fresh = 3;                              // accumulators of the segment without a product yet
-      if (seg >= 2) ok = mbar_wait(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+      if (seg >= 2) ok = mbar_wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
       for (int t = 0; t < s.n && ok; ++t, ++i) {
         const int st = i % kStages, pb = i & 1;
         ok = mbar_spin(&p_full[pb], (i >> 1) & 1, err, kErrMmaTimeout);
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       }
     }
     if (leader) mma_commit(&mma_done);
-    mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+    mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
   } else {
     // ---------------------------------------------------------------- queries: 16 threads a column
     const int part = lane & 15;
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       const int buf = seg % kQBufs;
-      if (seg >= kQBufs && !mbar_wait(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       uint8_t* q_hi = sQ + buf * kQBytes;
       PaColumns& cm = cols[buf];
       const int pairs = s.rows * a.group, prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const PaSeg s = pa_segment(a, end, u, u1);
       u += s.n;
       const int qb = seg % kQBufs;
-      if (!mbar_wait(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
+      if (!mbar_wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
       const uint32_t acc = tmem + lanes + kColO + 128 * (seg & 1);
       const PaColumns& cm = cols[qb];
       const int min_limit = cm.min_limit;
@@ -463,8 +464,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       for (int t = (i0 + wg) & 1; t < s.n; t += 2) {
         const int i = i0 + t, st = i % kStages, sb = wg;
         const int key0 = (s.tile + t) * kTok, j = key0 + row;
-        ok = mbar_wait(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
-             mbar_wait(&s_full[sb], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
+        ok = mbar_wait_warp(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
+             mbar_wait_warp(&s_full[sb], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         tc_fence_after();
         float z[kCE];
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           }
           if (!fresh) {
             // the accumulator is settled once this warpgroup's previous product has completed
-            ok = mbar_wait(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
+            ok = mbar_wait_warp(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
             if (!ok) break;
             tc_fence_after();
             const uint32_t o = acc + 64 * wg;
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         fresh = false;
         // the buffer is free once this warpgroup's previous product has completed
         if (i >= 2) {
-          ok = mbar_wait(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
+          ok = mbar_wait_warp(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
           if (!ok) break;
         }
         uint8_t* prow = sP + sb * kPBytes + row * kN;
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         if (lane == 0) mbar_arrive(&q_empty[qb]);
         continue;
       }
-      if (!mbar_wait(&stat_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
+      if (!mbar_wait_warp(&stat_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
       const bool whole = s.n == s.tiles;
       const int pairs = s.rows * a.group;
       // a piece that starts its segment is its CTA's last unless it also starts the CTA's range
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       }
       poison = stat_nan[qb][0][row] | stat_nan[qb][1][row];
       named_bar_sync(bar, 128);
-      if (!mbar_wait(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      if (!mbar_wait_warp(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < kCE; c0 += 8) {
@@ -770,7 +771,7 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
   if (u == pa_unit_start(c + 1, units, ctas)) return;    // a range without units
   const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + 8 * c));
   const int b = rec.x, h = rec.y, cg = rec.z, tile = rec.w;
-  if (tile == 0) return;                                  // the range begins with a segment
+  if (b < 0 || tile == 0) return;                         // nothing was written, or the range begins with a segment
   const int64_t seg = u - tile;
   const int first = pa_cta_of_unit(u - 1, units, ctas);
   if (pa_unit_start(first, units, ctas) > seg) return;    // an earlier boundary cuts it, too
@@ -892,7 +893,7 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, cons
     a.lo_pairs = kPagedAttnDirect;
     a.hi_pairs = INT32_MAX;
     a.part_ml = a.part_o + (size_t)2 * ctas * kPromptPairs * kKvDim;
-    e = launch_paged_prompt(a, k_codes, v_codes, ctas, s);
+    e = launch_paged_prompt(a, k_map, v_codes, ctas, s);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }

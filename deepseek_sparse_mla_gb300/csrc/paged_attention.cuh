@@ -1,6 +1,8 @@
 // Shared by the two dense attention kernels: what a request brings, and the split of the units over CTAs.
 #pragma once
 
+#include <cuda.h>
+
 #include "dsa_internal.cuh"
 
 namespace dsa {
@@ -39,6 +41,10 @@ __device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, uint3
   s.tiles = max(1, (int)((len + kPaTok - 1) / kPaTok));
   return s;
 }
+
+// Requests of many rows (paged_prompt.cu); k_map: the K codes in boxes of a page.
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, const uint8_t* v_codes, int ctas,
+                                cudaStream_t s);
 
 // Units [start(c), start(c + 1)) belong to CTA c.
 __device__ __forceinline__ int64_t pa_unit_start(int c, int64_t units, int ctas) { return units * c / ctas; }

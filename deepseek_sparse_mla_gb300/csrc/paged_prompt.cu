@@ -2,28 +2,28 @@
 // cores.  Definition as in paged_attention.cu:
 //   z_s = scale * q[r,h] . (k_code_s * ks),  out = softmax(z) (v_code * vs),  lse = ln sum exp(z)
 //
-// Here the products bound the call (4 * 128 flop per visible pair and head), so the tiles are square and the
-// codes are widened once per tile for 256 (row, head) pairs:
-//   S [128 pairs x 128 keys]  = Q [128 x 128] K^T     Q and K in fp16 from shared memory
-//   O [128 pairs x 128 dims] += P [128 x 128] V       P in fp16 from TMEM, V in fp16 from shared memory
-// fp16 holds e4m3 codes exactly, and bf16 queries too once a row is scaled by a power of two that brings its
-// largest value below 2^15 (8 bits down to 2^-31 of it).  ks stays out of K: it multiplies the scores of its
-// page, one fp32 factor per 16 keys.  vs goes into V relative to the largest of the request's pages, exactly
-// for the powers of two that the append writes.  P carries 2^8 times the probability (11 bits of it, and
-// an absolute step of 2^-33 of the row's largest), so that V's and P's ranges together fit fp16.
-// e4m3 products with a two-term Q would take the same time (fp8 runs twice as fast) but keep only 2^-18
-// of a row's largest value, as both terms would have to share one accumulator.
+// Here the products bound the call (4 * 128 flop per visible pair and head), so the tiles are square:
+//   S [128 pairs x 128 keys]  = Q [128 x 128] K^T     K's codes as they are, Q in two e4m3 terms, from shared memory
+//   O [128 pairs x 128 dims] += P [128 x 128] V       P in fp16 from TMEM, V widened to fp16 in shared memory
+// Two e4m3 products take as long as one in fp16 or bf16 and K needs no widening.  Q = hi + lo in units of 2^-8 of
+// the row's largest value: 8 bits of bf16 are kept down to 2^-10 of it, with an absolute error of at most 2^-18
+// below (bf16 itself has 2^-9 of each value; one accumulator for both terms leaves no room for a scale
+// of lo's own).  ks multiplies the scores of its page, one fp32 factor per 16 keys.  V as fp16 holds codes exactly;
+// vs goes into it relative to the largest of the piece's pages, exactly for the powers of two that the append writes.
+// P carries 2^8 times the probability (11 bits of it, with an absolute step of 2^-33 of the row's largest).
 //
 // Work: (request, 256 pairs, K/V head, tile of 128 keys) units split into one contiguous range per CTA
 // (persistent, one CTA per SM), as in paged_attention.cu; a segment that is cut leaves fp32 pieces for a join.
 // Segments count the tiles their last row sees, so causal rows are balanced over the CTAs.
 //
 // Per CTA (20 warps): warps 0-3 and 4-7 are the softmax of the two 128-pair halves, one pair a thread (no
-// cross-lane work at all), which alternate with each other on the tensor cores; warps 8-15 load codes, widen
-// them and write the K and V tiles; warp 16 issues the products; warps 17-19 load the next segment's queries.
+// cross-lane work at all); each half has a warp of its own that issues its products (16 and 17), so that one
+// half's softmax runs while the tensor cores work for the other, and P goes to them 64 keys at a time.
+// Warp 18 loads K tiles by TMA; warps 8-11 and 12-15 widen the V tiles, even and odd ones.
 // TMEM (all 512 columns): S of half q at 128 q, with P over its first 64 columns; O of half q at 256 + 128 q.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
+#include "tmap.cuh"
 
 #include <cuda_fp16.h>
 
@@ -33,18 +33,22 @@ using namespace sm100;
 namespace pp {
 constexpr int kTok = kPaTok;
 constexpr int kHalfPairs = 128;
-constexpr int kTileBytes = kTok * kKvDim * 2;        // 32 KB of fp16: two 64-wide column chunks of 128-byte rows
+constexpr int kQTermBytes = kHalfPairs * kKvDim;     // 16 KB: one e4m3 term of one half's queries
+constexpr int kKBytes = kTok * kKvDim;               // 16 KB of codes
+constexpr int kVBytes = kTok * kKvDim * 2;           // 32 KB of fp16: two 64-wide column chunks of 128-byte rows
 constexpr int kChunkBytes = kTok * 128;
+constexpr int kKStages = 4;
 constexpr int kThreads = 640;
-constexpr int kConvWarp0 = 8, kMmaWarp = 16, kQueryWarp0 = 17;
-constexpr uint32_t kRegsSoft = 112, kRegsConv = 96, kRegsRest = 64;   // 2 * 112 + 2 * 96 + 64 = 480 = 5 * 96, the launch's
+constexpr int kConvWarp0 = 8, kMmaWarp0 = 16, kLoadWarp = 18;
+constexpr uint32_t kRegsSoft = 128, kRegsConv = 88, kRegsRest = 48;   // 2 * 128 + 2 * 88 + 48 = 480 = 5 * 96, the launch's
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
-constexpr uint32_t kPolls = 1u << 22;
+constexpr uint32_t kPolls = 1u << 17;                // about a second
 constexpr int kRuns = 512;                           // runs of (request, pairs) entries that are summed
-constexpr int kMetaBufs = 4;
-constexpr int kFixedSmem = 6 * kTileBytes + 1024;    // two halves of Q, two K tiles, two V tiles
+constexpr int kMetaBufs = 8;                         // tiles whose K scales are kept (a tile's outlive its K stage)
+constexpr int kSegBufs = 4;
+constexpr int kFixedSmem = 4 * kQTermBytes + kKStages * kKBytes + 2 * kVBytes + 1024;
 }  // namespace pp
 
 // (request, 256 pairs): its rows' last key, and the tiles that they see
@@ -166,67 +170,30 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 
-// eight columns, as tmem_st16
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-
 // A softmax thread's row: its reference m (log2 units), its sum l of P, and what masks and biases need.
 struct PpRow {
   float m, l, cf, slope;
   int limit, pos;
 };
 
-// A row's reference moves from m to m + something: what was summed and stored against the old one shrinks by al.
-// done: 16-key groups of this tile whose P is in TMEM already.
-__device__ __forceinline__ void pp_shrink(uint32_t tS, uint32_t tO, int done, bool has_o, float al) {
-  const __half2 h = __float2half2_rn(al);
-#pragma unroll 1
-  for (int g = 0; g < done; ++g) {
-    uint32_t p[8];
-    tmem_ld8(tS + 8 * g, p);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) p[k] = mul2(p[k], h);
-    tmem_st8(tS + 8 * g, p);
-  }
-  if (has_o) {
-#pragma unroll 1
-    for (int c = 0; c < kKvDim; c += 8) {
-      uint32_t o[8];
-      tmem_ld8(tO + c, o);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-      tmem_st8(tO + c, o);
-    }
-  }
-  tmem_wait_st();
-}
-
-// One tile of a row, in one pass over its scores: 16 keys at a time the scores come out of TMEM, their largest
-// is held against the reference (which moves only when exceeded by 2^kSlack, seldom after the first
-// keys), and P goes back over scores that have been read.  Holding all 128 scores for an exact maximum
-// first took 176 registers, and reading them twice 15 % more time.
+// 64 keys of a row, in one pass over their scores: 16 at a time they come out of TMEM (the next 16 in flight),
+// and P = 2^(z - m + 8) is formed against the reference that the row has.  P stays in registers until the largest
+// score (returned) is known to exceed it by no more than the slack, as for nearly every tile; else the pass is
+// repeated.  An exact maximum first would read the scores twice, or hold them all (176 registers).
 template <bool kMods, bool kMasked>
-__device__ __forceinline__ void pp_tile(PpRow& w, const PagedAttnArgs& a, uint32_t tS, uint32_t tO, int key0, uint32_t bad,
-                                        const float* ks, bool has_o) {
+__device__ __forceinline__ float pp_half(const PpRow& w, const PagedAttnArgs& a, uint32_t tS, int key0, uint32_t bad,
+                                         const float* ks, uint32_t (&p)[32], float& sum_out) {
   const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
-  uint64_t sum = 0;
+  const float shift = pp::kPLog2 - (w.m == -INFINITY ? 0.f : w.m);
+  const uint64_t shift2 = pack2(shift, shift);
+  uint64_t sum[2] = {0, 0};
   uint32_t r[2][16];
-  float shift = pp::kPLog2 - (w.m == -INFINITY ? 0.f : w.m);
+  float top = -INFINITY;
   tmem_ld16(tS, r[0]);
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
+  for (int g = 0; g < 4; ++g) {
     tmem_wait_ld();
-    if (g < 7) tmem_ld16(tS + 16 * (g + 1), r[(g + 1) & 1]);
+    if (g < 3) tmem_ld16(tS + 16 * (g + 1), r[(g + 1) & 1]);
     uint32_t* x = r[g & 1];
     float kc = ks[g] * w.cf;
     if (kMods) {
@@ -248,89 +215,142 @@ __device__ __forceinline__ void pp_tile(PpRow& w, const PagedAttnArgs& a, uint32
       for (int c = 0; c < 16; ++c) x[c] = c < left ? __float_as_uint(__uint_as_float(x[c]) * kc) : 0xFF800000u;
       kc = 1.f;
     }
-    float top = __uint_as_float(x[0]);
-#pragma unroll
-    for (int c = 1; c < 16; ++c) top = fmaxf(top, __uint_as_float(x[c]));
-    top *= kc;
-    const bool grow = top > w.m + pp::kSlack || (w.m == -INFINITY && top > w.m);
-    if (__any_sync(0xffffffffu, grow)) {
-      const float m_new = grow ? top : w.m;
-      const float al = m_new == w.m ? 1.f : w.m == -INFINITY ? 0.f : ex2_approx(w.m - m_new);
-      pp_shrink(tS, tO, g, has_o, al);
-      w.l *= al;
-      sum = fma2(sum, pack2(al, al), 0);
-      w.m = m_new;
-      shift = pp::kPLog2 - (m_new == -INFINITY ? 0.f : m_new);
-    }
-    const uint64_t kc2 = pack2(kc, kc), shift2 = pack2(shift, shift);
-    uint32_t p[8];
+    float m = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    const uint64_t kc2 = pack2(kc, kc);
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
+      if (c) m = fmaxf(m, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
       float y0, y1;
       unpack2(fma2(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), kc2, shift2), y0, y1);
       y0 = ex2_approx(y0);
       y1 = ex2_approx(y1);
-      sum = add2(sum, pack2(y0, y1));
+      sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(y0, y1));
       const __half2 h = __floats2half2_rn(y0, y1);
-      p[c >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+      p[8 * g + (c >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    // columns 8 g .. 8 g + 7 hold scores that have been read
-    tmem_st8(tS + 8 * g, p);
+    top = fmaxf(top, m * kc);
   }
-  float s0, s1;
-  unpack2(sum, s0, s1);
-  w.l += s0 + s1;
+  float s0, s1, s2, s3;
+  unpack2(sum[0], s0, s1);
+  unpack2(sum[1], s2, s3);
+  sum_out = (s0 + s1) + (s2 + s3);
+  return top;
+}
+
+// 16 columns a step: the accumulator of a row whose reference moved
+__device__ __forceinline__ void pp_shrink(uint32_t tO, float al) {
+#pragma unroll 1
+  for (int c = 0; c < kKvDim; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(tO + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+    tmem_st16(tO + c, o);
+  }
   tmem_wait_st();
+}
+
+// This thread's query row in two e4m3 terms; returns the factor of its scores.
+__device__ __forceinline__ float pp_query(const PagedAttnArgs& a, const __nv_bfloat16* src, bool there, uint8_t* q_hi, int row) {
+  uint4 x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = there ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+  uint32_t top = 0;                                    // largest finite |x|, as bf16 bits
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t p = w[e] & 0x7FFFu, y = (w[e] >> 16) & 0x7FFFu;
+      if (p < 0x7F80u) top = max(top, p);
+      if (y < 0x7F80u) top = max(top, y);
+    }
+  }
+  // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
+  const int E = max((int)(top >> 7) - 127, -100);
+  const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {                        // 16 values: one 16-byte unit of each term
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t h2[2], l2[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = 2 * k + e;
+        const uint4 y = x[2 * i + (j >> 2)];
+        const uint32_t w = (j & 3) == 0 ? y.x : (j & 3) == 1 ? y.y : (j & 3) == 2 ? y.z : y.w;
+        // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
+        const uint32_t wl = w << 16, wh = w & 0xFFFF0000u;
+        const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
+        const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
+        h2[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl, xh), __NV_SATFINITE, __NV_E4M3);
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2[e], __NV_E4M3);
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+        l2[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl - back.x, xh - back.y), __NV_SATFINITE, __NV_E4M3);
+      }
+      hi[k] = h2[0] | h2[1] << 16;
+      lo[k] = l2[0] | l2[1] << 16;
+    }
+    const uint32_t at = sw128_offset(row, i);
+    *reinterpret_cast<uint4*>(q_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(q_hi + pp::kQTermBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  return __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;
 }
 
 template <bool kMods>
 __global__ void __launch_bounds__(pp::kThreads, 1)
-    paged_prompt_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes,
+    paged_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const uint8_t* __restrict__ v_codes,
                         const __grid_constant__ PagedAttnArgs a) {
   using namespace pp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + 2 * kTileBytes;
-  uint8_t* sV = sK + 2 * kTileBytes;
-  int32_t* entry_end = reinterpret_cast<int32_t*>(sV + 2 * kTileBytes);   // [requests] entries of requests 0 .. b
+  uint8_t* sK = sQ + 4 * kQTermBytes;
+  uint8_t* sV = sK + kKStages * kKBytes;
+  int32_t* entry_end = reinterpret_cast<int32_t*>(sV);   // [requests] entries of requests 0 .. b, before V is there
 
-  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-  __shared__ uint64_t q_full, q_empty, mma_done;
+  __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2], s_full[2], p_full[2][2], pv_done[2];
+  __shared__ uint64_t q_full[2], o_full[2], o_empty[2], mma_done;
   __shared__ __align__(16) float sks[kMetaBufs][8];   // K scale of each 16 keys of a tile
   __shared__ uint32_t sbad[kMetaBufs];                // 16-key groups without a valid page
-  __shared__ float factor[2][kPromptPairs];
-  __shared__ int nan_key[kMetaBufs][kKvDim];          // first key with a NaN code that only some rows see, by dim
+  __shared__ int nan_key[kSegBufs][kKvDim];           // first key with a NaN code that only some rows see, by dim
   __shared__ int32_t run_units[kRuns];                // units (without heads) of the runs before
   __shared__ int32_t scan[kThreads / 32];
-  __shared__ float vmax_part[4], v_ref[kMetaBufs];    // V's reference of a segment
-  __shared__ int seg_tiles[kMetaBufs];
+  __shared__ float vmax_part[8], v_ref[kSegBufs];     // V's reference of a segment
+  __shared__ int seg_tiles[2][2];
   __shared__ uint32_t tmem_base, bits_all;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
   if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 2);                       // both halves' products
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 4);
-      mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 4);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 2);
       mbar_init(&s_full[i], 2);                        // the products, and their issuer
-      mbar_init(&p_full[i], 4);
+      for (int h = 0; h < 2; ++h) mbar_init(&p_full[i][h], 4);
+      mbar_init(&pv_done[i], 1);                       // the first 64 keys' product
+      mbar_init(&q_full[i], 4);
       mbar_init(&o_full[i], 2);
       mbar_init(&o_empty[i], 4);
     }
-    mbar_init(&q_full, 3);
-    mbar_init(&q_empty, 1);
-    mbar_init(&mma_done, 1);
+    mbar_init(&mma_done, 2);
+    prefetch_tmap(&k_map);
     bits_all = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp0) {
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
   pdl_wait();
+  if (tid == 0) a.rec[8 * cta] = -1;                   // no piece to join until it has been written
   const int B = a.num_requests;
   // block-wide inclusive sum of one value a thread
   auto block_sum = [&](int v) {
@@ -413,6 +433,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     cur.before = (int64_t)run_units[lo] * a.kv_heads;
     find(min(lo * run, entries - 1), cur);
   }
+  __syncthreads();                                     // V's tiles take the place of the entries' sums
 
   if (warp < kConvWarp0) {
     regs_inc<kRegsSoft>();
@@ -420,83 +441,136 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     const int q = warp >> 2, quarter = warp & 3, row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t tS = tmem + lanes + 128 * q, tO = tmem + lanes + kColO + 128 * q;
+    uint8_t* const q_hi = sQ + 2 * q * kQTermBytes;
+    // this thread's pair of a segment: its row and head (of the last pair where there are fewer)
+    auto pair_of = [&](const PpSeg& s, int& r, int& head) {
+      const int n = min(s.e.qt * kPromptPairs + kHalfPairs * q + row, s.e.shape.rows * a.group - 1);
+      r = n / a.group;
+      head = s.h * a.group + (n - r * a.group);
+      return s.e.qt * kPromptPairs + kHalfPairs * q + row == n;
+    };
+    // the queries of a segment, once the last segment's scores have been computed
+    auto load_queries = [&](const PpSeg& s, int seg) {
+      int r, head;
+      const bool there = pair_of(s, r, head);
+      const float cf = pp_query(a, a.q + (int64_t)(s.e.shape.row0 + r) * a.q_stride + (int64_t)head * kKvDim, there, q_hi, row);
+      if (row == 0) seg_tiles[q][seg & 1] = s.n;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[q]);
+      return cf;
+    };
     int i = 0, seg = 0;
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const PpSeg s = pp_segment(a, cur, u, u1);
+    PpSeg s = {};
+    float cf = 0.f;
+    int64_t u = u0;
+    if (u < u1) {
+      s = pp_segment(a, cur, u, u1);
+      cf = load_queries(s, 0);
+    }
+    while (u < u1) {
       const int64_t u_first = u;
       u += s.n;
-      const int pairs = s.e.shape.rows * a.group;
-      const int n = s.e.qt * kPromptPairs + kHalfPairs * q + row;     // this thread's pair
-      const int r = min(n, pairs - 1) / a.group, head = s.h * a.group + (min(n, pairs - 1) - r * a.group);
-      const int limit = pp_limit(s.e, r), pos = s.e.start + r;
+      int r, head;
+      const bool there = pair_of(s, r, head);
+      PpRow w = {-INFINITY, 0.f, cf, kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f, pp_limit(s.e, r),
+                 s.e.start + r};
       // keys below it are seen by every pair of this half
-      const int min_limit = pp_limit(s.e, min(s.e.qt * kPromptPairs + kHalfPairs * q, pairs - 1) / a.group);
-      const float slope = kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f;
-      PpRow w = {-INFINITY, 0.f, 0.f, slope, limit, pos};
-      for (int t = 0; t < s.n; ++t, ++i) {
+      const int min_limit = pp_limit(s.e, min(s.e.qt * kPromptPairs + kHalfPairs * q, s.e.shape.rows * a.group - 1) / a.group);
+      for (int t = 0; t < s.n && ok; ++t, ++i) {
         const int key0 = (s.tile + t) * kTok;
-        // The scores' arrival also stands for the tile's scales and the queries' factors: their own barriers may be
-        // a phase further by the time this warpgroup looks.
-        ok = mbar_wait(&s_full[q], i & 1, err, kErrMmaTimeout, kPolls);
+        // the scores' arrival also stands for the tile's scales: K's own barrier may be a phase further by now
+        ok = mbar_wait_warp(&s_full[q], i & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         tc_fence_after();
-        if (t == 0) w.cf = factor[seg & 1][kHalfPairs * q + row];
-        const float* ks = sks[i % kMetaBufs];
         const uint32_t bad = sbad[i % kMetaBufs];
-        if (key0 + kTok > min_limit || bad) pp_tile<kMods, true>(w, a, tS, tO, key0, bad, ks, t > 0);
-        else pp_tile<kMods, false>(w, a, tS, tO, key0, bad, ks, t > 0);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[q]);
+        const bool masked = key0 + kTok > min_limit || bad;          // uniform in the warpgroup
+#pragma unroll 1
+        for (int h = 0; h < 2 && ok; ++h) {
+          uint32_t p[32];
+          float sum;
+          for (;;) {
+            const float* ks = sks[i % kMetaBufs] + 4 * h;
+            const float top = masked ? pp_half<kMods, true>(w, a, tS + 64 * h, key0 + 64 * h, bad >> (4 * h), ks, p, sum)
+                                     : pp_half<kMods, false>(w, a, tS + 64 * h, key0 + 64 * h, 0, ks, p, sum);
+            const bool grow = top > w.m + kSlack || (w.m == -INFINITY && top > w.m);
+            if (!__any_sync(0xffffffffu, grow)) break;
+            const float m_new = grow ? top : w.m;
+            const float al = m_new == w.m ? 1.f : w.m == -INFINITY ? 0.f : ex2_approx(w.m - m_new);
+            if (t > 0 || h > 0) {
+              // The accumulator is settled when this tile's first half has been added; the last tile's was before
+              // these scores were computed.
+              if (h > 0) ok = mbar_wait_warp(&pv_done[q], i & 1, err, kErrMmaTimeout, kPolls);
+              if (!ok) break;
+              tc_fence_after();
+              pp_shrink(tO, al);
+              w.l *= al;
+            }
+            w.m = m_new;
+          }
+          if (!ok) break;
+          w.l += sum;
+          // P takes 32 columns of scores that have been read
+          tmem_st32(tS + 32 * h, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[q][h]);
+        }
       }
       if (!ok) break;
+      PpSeg next = {};
+      if (u < u1) {
+        next = pp_segment(a, cur, u, u1);
+        cf = load_queries(next, seg + 1);
+      }
       // ---- the segment's end
       const bool whole = s.n == s.e.tiles;
       const int slot = u_first == u0 ? 2 * cta : 2 * cta + 1;
-      ok = mbar_wait(&o_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
+      ok = mbar_wait_warp(&o_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
       tc_fence_after();
       const float m = w.m, l = w.l;
       const bool any = l > 0.f || l != l;
       const int64_t at = (int64_t)(s.e.shape.row0 + r) * a.kv_heads * a.group + head;
-      const float vref = v_ref[seg % kMetaBufs];
+      const float vref = v_ref[seg % kSegBufs];
       const float f = !any ? 0.f : whole ? vref / l : vref;
-      const int* nk = nan_key[seg % kMetaBufs];
+      const int* nk = nan_key[seg % kSegBufs];
 #pragma unroll 1
-      for (int c = 0; c < kKvDim; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tO + c, o);
+      for (int c = 0; c < kKvDim; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(tO + c, o);
         tmem_wait_ld();
-        if (n < pairs) {
-          float x[32];
+        if (there) {
+          float x[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+          for (int k = 0; k < 16; ++k) {
             x[k] = any ? __uint_as_float(o[k]) * f : 0.f;
-            if (nk[c + k] < limit) x[k] = __int_as_float(0x7FC00000);
+            if (nk[c + k] < w.limit) x[k] = __int_as_float(0x7FC00000);
           }
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + at * kKvDim + c);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 w;
-              uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+            for (int k = 0; k < 2; ++k) {
+              uint4 v;
+              uint32_t* vv = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
               for (int k2 = 0; k2 < 4; ++k2) {
                 const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[8 * k + 2 * k2], x[8 * k + 2 * k2 + 1]);
-                ww[k2] = *reinterpret_cast<const uint32_t*>(&b2);
+                vv[k2] = *reinterpret_cast<const uint32_t*>(&b2);
               }
-              dst[k] = w;
+              dst[k] = v;
             }
           } else {
             // [slot][dim / 4][pair] float4: a warp's stores are contiguous
             float4* dst = reinterpret_cast<float4*>(a.part_o) + ((int64_t)slot * (kKvDim / 4) + c / 4) * kPromptPairs + kHalfPairs * q + row;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k * kPromptPairs] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) dst[k * kPromptPairs] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
           }
         }
       }
-      if (n < pairs) {
+      if (there) {
         if (!whole) {
           reinterpret_cast<float2*>(a.part_ml)[(int64_t)slot * kPromptPairs + kHalfPairs * q + row] = make_float2(m, l);
         } else if (a.lse) {
@@ -514,22 +588,19 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[q]);
+      s = next;
+      ++seg;
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp < kMmaWarp0) {
     regs_dec<kRegsConv>();
-    // ---------------------------------------------------------------- K and V tiles: codes to fp16
-    // Four warps for K and four for V: eight lanes a row of 16-byte pieces, 16 rows a pass, so that a pass is one
-    // 16-key group and lies in one page.  A tile's loads go out right after the last tile's fence, which
-    // waits for the loads in flight too: one warp doing both K and V with its loads ahead took 7,000 cycles
-    // a tile, most of them in fences, against the 2,000 of the products.
-    const bool is_v = warp >= kConvWarp0 + 4;
-    const int cw = (warp - kConvWarp0) & 3, part = lane & 7, sub = 4 * cw + (lane >> 3), lp = a.log2_page;
+    // ---------------------------------------------------------------- V tiles: codes to fp16
+    // Two groups of four warps take alternate tiles: eight lanes a row of 16-byte pieces, 16 rows a pass, so that a
+    // pass is one 16-key group and lies in one page.  A tile's loads go out after the last tile's fence, which
+    // would wait for loads in flight too.
+    const int grp = (warp - kConvWarp0) >> 2, cw = warp & 3, part = lane & 7, sub = 4 * cw + (lane >> 3), lp = a.log2_page;
     const int unit = 2 * (part & 3), swap = part >> 2;
-    uint64_t* const full = is_v ? v_full : k_full;
-    uint64_t* const empty = is_v ? v_empty : k_empty;
-    const float* const scales = is_v ? a.v_scales : a.k_scales;
-    uint8_t* const tiles = (is_v ? sV : sK) + (part >> 2) * kChunkBytes;
-    int i = 0, seg = 0;
+    uint8_t* const tile = sV + grp * kVBytes + (part >> 2) * kChunkBytes;
+    int i0 = 0, seg = 0;                               // i0: the CTA's tiles before this segment
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
       const PpSeg s = pp_segment(a, cur, u, u1);
@@ -537,47 +608,42 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       const int len = s.e.shape.len, pages = (len + (1 << lp) - 1) >> lp;
       const int32_t* table = a.block_table + (int64_t)s.e.b * a.table_stride;
       // this lane's 16 bytes of row 0 of page 0; a page further is page_step bytes on
-      const uint8_t* const base = (is_v ? v_codes : k_codes) + ((int64_t)s.h << lp) * kKvDim + 16 * part;
+      const uint8_t* const base = v_codes + ((int64_t)s.h << lp) * kKvDim + 16 * part;
       const int64_t page_step = ((int64_t)a.kv_heads << lp) * kKvDim;
-      constexpr int kNoPage = INT32_MIN;               // past the request's pages
+      // the page of a key, -1 where there is none (the loader of K reports bad ids)
       auto id_of = [&](int key) {
         const int p = key >> lp;
-        return p < pages ? table[p] : kNoPage;
-      };
-      auto checked = [&](int id) {
-        if (id >= 0 && id < a.num_pages) return id;
-        if (id != kNoPage) atomicOr(err, kErrBadPage);
-        return -1;
+        const int id = p < pages ? table[p] : -1;
+        return id < a.num_pages ? id : -1;
       };
       // V's reference: the power of two at or below the piece's largest scale
-      float vinv = 1.f;
-      if (is_v) {
-        float top = 0.f;
-        const int p0 = (s.tile * kTok) >> lp, p1 = min(pages, ((s.tile + s.n) * kTok) >> lp);
+      float top = 0.f;
+      const int p0 = (s.tile * kTok) >> lp, p1 = min(pages, ((s.tile + s.n) * kTok) >> lp);
 #pragma unroll 4
-        for (int p = p0 + 32 * cw + lane; p < p1; p += 128) {
-          const int id = table[p];
-          if (id >= 0 && id < a.num_pages) top = fmaxf(top, fabsf(scales[(int64_t)id * a.kv_heads + s.h]));
-        }
-        top = warp_max_f32(top);
-        if (lane == 0) vmax_part[cw] = top;
-        nan_key[seg % kMetaBufs][32 * cw + lane] = INT32_MAX;
-        named_bar_sync(1, 128);
-        top = fmaxf(fmaxf(vmax_part[0], vmax_part[1]), fmaxf(vmax_part[2], vmax_part[3]));
-        const uint32_t top_bits = __float_as_uint(top) & 0x7F800000u;
-        const float vref = top_bits && top_bits < 0x7F800000u ? __uint_as_float(top_bits) : 1.f;
-        if (cw == 0 && lane == 0) v_ref[seg % kMetaBufs] = vref;
-        vinv = 1.f / vref;
-        named_bar_sync(1, 128);
+      for (int p = p0 + 32 * (warp - kConvWarp0) + lane; p < p1; p += 256) {
+        const int id = table[p];
+        if (id >= 0 && id < a.num_pages) top = fmaxf(top, fabsf(a.v_scales[(int64_t)id * a.kv_heads + s.h]));
       }
+      top = warp_max_f32(top);
+      if (lane == 0) vmax_part[warp - kConvWarp0] = top;
+      if (grp == 0) nan_key[seg % kSegBufs][32 * cw + lane] = INT32_MAX;
+      named_bar_sync(1, 256);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, vmax_part[k]);
+      const uint32_t top_bits = __float_as_uint(top) & 0x7F800000u;
+      const float vref = top_bits && top_bits < 0x7F800000u ? __uint_as_float(top_bits) : 1.f;
+      if (warp == kConvWarp0 && lane == 0) v_ref[seg % kSegBufs] = vref;
+      const float vinv = 1.f / vref;
+      named_bar_sync(1, 256);
       const int min_limit = pp_limit(s.e, min(s.e.qt * kPromptPairs, s.e.shape.rows * a.group - 1) / a.group);
 
       uint4 x[8];
       float scale = 0.f;
-      // lane g (and g + 8, ..): the page of 16-key group g, of this tile and (not checked yet) of the next one
-      int id = checked(id_of(s.tile * kTok + 16 * part)), id2 = id_of((s.tile + 1) * kTok + 16 * part);
+      int t = (i0 + grp) & 1;
+      // lane g (and g + 8, ..): the page of 16-key group g, of the tile to load and of this group's next one
+      int id = id_of((s.tile + t) * kTok + 16 * part), id2 = id_of((s.tile + t + 2) * kTok + 16 * part);
       auto load = [&](int key0) {
-        scale = id >= 0 ? scales[(int64_t)id * a.kv_heads + s.h] : 0.f;
+        scale = id >= 0 ? a.v_scales[(int64_t)id * a.kv_heads + s.h] : 0.f;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const int page = __shfl_sync(0xffffffffu, id, g), key = key0 + 16 * g + sub;
@@ -586,13 +652,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             x[g] = __ldg(reinterpret_cast<const uint4*>(base + page * page_step + (key & ((1 << lp) - 1)) * kKvDim));
         }
       };
-      load(s.tile * kTok);
-      for (int t = 0; t < s.n; ++t, ++i) {
-        const int key0 = (s.tile + t) * kTok, buf = i & 1;
-        if (i >= 2) ok = mbar_wait(&empty[buf], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+      if (t < s.n) load((s.tile + t) * kTok);
+      for (; t < s.n; t += 2) {
+        const int key0 = (s.tile + t) * kTok, i = i0 + t;
+        if (i >= 2) ok = mbar_wait_warp(&v_empty[grp], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         // a NaN code of a key that only some rows see: out of the tile, and noted for the rows that see it
-        if (is_v && key0 + kTok > min_limit) {
+        if (key0 + kTok > min_limit) {
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
             uint32_t* w = reinterpret_cast<uint32_t*>(&x[g]);
@@ -604,184 +670,157 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
               for (int e = 0; e < 4; ++e) {
                 const uint32_t f = ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                 for (int k = 0; k < 4; ++k)
-                  if ((f >> (8 * k + 7)) & 1u) atomicMin(&nan_key[seg % kMetaBufs][16 * part + 4 * e + k], key0 + 16 * g + sub);
+                  if ((f >> (8 * k + 7)) & 1u) atomicMin(&nan_key[seg % kSegBufs][16 * part + 4 * e + k], key0 + 16 * g + sub);
                 w[e] &= ~((f >> 7) * 0xFFu);
               }
             }
           }
         }
-        uint8_t* tile = tiles + buf * kTileBytes;
         const float ratio = scale * vinv;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const int r = 16 * g + sub;
+          const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, g));
           uint4 lo = widen8(x[g].x, x[g].y), hi = widen8(x[g].z, x[g].w);
-          if (is_v) {
-            const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, g));
-            lo = make_uint4(mul2(lo.x, f), mul2(lo.y, f), mul2(lo.z, f), mul2(lo.w, f));
-            hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
-          }
+          lo = make_uint4(mul2(lo.x, f), mul2(lo.y, f), mul2(lo.z, f), mul2(lo.w, f));
+          hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
           // lanes of the two column chunks start with different units, so that eight lanes fill all banks
           *reinterpret_cast<uint4*>(tile + r * 128 + (((unit + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
           *reinterpret_cast<uint4*>(tile + r * 128 + (((unit + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
         }
-        if (!is_v && cw == 0) {
-          if (lane < 8) sks[i % kMetaBufs][lane] = scale;
-          const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && id < 0);
-          if (lane == 0) sbad[i % kMetaBufs] = bad;
-        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[buf]);
-        if (t + 1 < s.n) {
-          id = checked(id2);
-          id2 = id_of(key0 + 2 * kTok + 16 * part);
-          load(key0 + kTok);
+        if (lane == 0) mbar_arrive(&v_full[grp]);
+        if (t + 2 < s.n) {
+          id = id2;
+          id2 = id_of(key0 + 4 * kTok + 16 * part);
+          load(key0 + 2 * kTok);
         }
       }
+      i0 += s.n;
     }
   } else {
     regs_dec<kRegsRest>();
-    if (warp == kMmaWarp) {
-      // ---------------------------------------------------------------- products
-      // Order: .. O0(i) S0(i+1) O1(i) S1(i+1) ..: while one half's softmax runs, the tensor cores work for the other.
-      // S0(i+1) overwrites P0(i), which O0(i) has read (products issue and complete in order).
+    if (warp < kLoadWarp) {
+      // ---------------------------------------------------------------- products of one half
+      // S(i + 1) overwrites P(i), which O(i) has read: products of one thread run in order.
+      const int q = warp - kMmaWarp0;
       const bool leader = elect_one();
-      const uint32_t id_s = idesc_f16(128, kTok, false, false, false, false);
+      const uint32_t id_s = idesc_e4m3(128, kTok);
       const uint32_t id_o = idesc_f16(128, kKvDim, false, false, false, true);
-      const uint64_t d_q = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+      const uint64_t d_q = smem_desc(smem_u32(sQ + 2 * q * kQTermBytes), 16, 1024, kSwizzle128B);
       const uint64_t d_k = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
       const uint64_t d_v = smem_desc(smem_u32(sV), kChunkBytes, 1024, kSwizzle128B);
-      const int n_tiles = (int)(u1 - u0);
-      int s_left = 0, o_left = 0, s_seg = -1, o_seg = -1;
-      bool ok = true, o_first = false;
-      for (int i = -1; i < n_tiles && ok; ++i) {
+      const int n_all = (int)(u1 - u0);
+      bool ok = true;
+      auto scores = [&](int i) {
+        const int st = i % kKStages;
+        ok = ok && mbar_spin(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t k = d_k + (uint64_t)((st * kKBytes) >> 4);
+        if (leader) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (i >= 0) {
-            if (q == 0) {
-              if (o_left == 0) {
-                ++o_seg;
-                o_left = seg_tiles[o_seg % kMetaBufs];
-                o_first = true;
-              }
-              --o_left;
-              ok = ok && mbar_spin(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout);
-            }
-            if (o_first && o_seg > 0) ok = ok && mbar_spin(&o_empty[q], (o_seg - 1) & 1, err, kErrMmaTimeout);
-            ok = ok && mbar_spin(&p_full[q], i & 1, err, kErrMmaTimeout);
+          for (int kk = 0; kk < 8; ++kk)               // hi, then lo
+            mma_ss_f8(tmem + 128 * q, d_q + (uint64_t)(((kk >> 2) * kQTermBytes + (kk & 3) * 32) >> 4), k + 2 * (kk & 3), id_s, kk > 0);
+          mma_commit(&s_full[q]);
+          mbar_arrive(&s_full[q]);
+          mma_commit(&k_empty[st]);
+        }
+        __syncwarp();
+      };
+      int i = 0;
+      for (int seg = 0; i < n_all && ok; ++seg) {
+        ok = mbar_wait_warp(&q_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
+        if (!ok) break;
+        const int n = seg_tiles[q][seg & 1];
+        scores(i);
+        if (seg > 0) ok = ok && mbar_wait_warp(&o_empty[q], (seg - 1) & 1, err, kErrMmaTimeout, kPolls);
+        for (int t = 0; t < n && ok; ++t, ++i) {
+          const uint64_t v = d_v + (uint64_t)(((i & 1) * kVBytes) >> 4);
+          ok = mbar_spin(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && mbar_spin(&p_full[q][h], i & 1, err, kErrMmaTimeout);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t v = d_v + (uint64_t)(((i & 1) * kTileBytes) >> 4);
             if (leader) {
 #pragma unroll
-              for (int kk = 0; kk < kTok / 16; ++kk)
-                mma_ts(tmem + kColO + 128 * q, tmem + 128 * q + 8 * kk, v + (uint64_t)((kk * 16 * 128) >> 4), id_o, !o_first || kk > 0);
-              if (q == 1) mma_commit(&v_empty[i & 1]);
-              if (o_left == 0) {
-                mma_commit(&o_full[q]);
-                mbar_arrive(&o_full[q]);
-              }
-            }
-            __syncwarp();
-            if (q == 1) o_first = false;
-          }
-          if (i + 1 < n_tiles) {
-            const int j = i + 1;
-            if (q == 0) {
-              if (s_left == 0) {
-                ++s_seg;
-                ok = ok && mbar_wait(&q_full, s_seg & 1, err, kErrMmaTimeout, kPolls);
-                s_left = seg_tiles[s_seg % kMetaBufs];
-              }
-              --s_left;
-              ok = ok && mbar_spin(&k_full[j & 1], (j >> 1) & 1, err, kErrMmaTimeout);
-            }
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t qd = d_q + (uint64_t)((q * kTileBytes) >> 4), k = d_k + (uint64_t)(((j & 1) * kTileBytes) >> 4);
-            if (leader) {
-#pragma unroll
-              for (int kk = 0; kk < kKvDim / 16; ++kk) {
-                const uint64_t off = (uint64_t)(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
-                mma_ss(tmem + 128 * q, qd + off, k + off, id_s, kk > 0);
-              }
-              mma_commit(&s_full[q]);
-              mbar_arrive(&s_full[q]);
-              if (q == 1) {
-                mma_commit(&k_empty[j & 1]);
-                if (s_left == 0) mma_commit(&q_empty);
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                mma_ts(tmem + kColO + 128 * q, tmem + 128 * q + 8 * kk, v + (uint64_t)((kk * 16 * 128) >> 4), id_o, t > 0 || kk > 0);
+              if (h == 0) {
+                mma_commit(&pv_done[q]);
+              } else {
+                mma_commit(&v_empty[i & 1]);
+                if (t + 1 == n) {
+                  mma_commit(&o_full[q]);
+                  mbar_arrive(&o_full[q]);
+                }
               }
             }
             __syncwarp();
           }
+          if (t + 1 < n) scores(i + 1);
         }
       }
       if (leader) mma_commit(&mma_done);
       mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
-    } else {
-      // ---------------------------------------------------------------- queries: 16 lanes a row
-      const int slot = 2 * (warp - kQueryWarp0) + (lane >> 4), part = lane & 15;
-      int seg = 0;
-      for (int64_t u = u0; u < u1; ++seg) {
+    } else if (warp == kLoadWarp) {
+      // ---------------------------------------------------------------- K tiles
+      const uint64_t policy = l2_evict_normal();
+      const int lp = a.log2_page, ppt = kTok >> lp;
+      const uint32_t page_bytes = (uint32_t)kKvDim << lp;
+      int i = 0;
+      bool ok = true;
+      for (int64_t u = u0; u < u1 && ok;) {
         const PpSeg s = pp_segment(a, cur, u, u1);
         u += s.n;
-        if (seg > 0 && !mbar_wait(&q_empty, (seg - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
-        const int pairs = s.e.shape.rows * a.group;
-        if (warp == kQueryWarp0 && lane == 0) seg_tiles[seg % kMetaBufs] = s.n;
-#pragma unroll 1
-        for (int r0 = 0; r0 < kPromptPairs; r0 += 24) {
-          uint4 x[4];
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int r = r0 + 6 * it + slot, n = s.e.qt * kPromptPairs + r;
-            x[it] = make_uint4(0, 0, 0, 0);
-            if (r < kPromptPairs && n < pairs) {
-              const int i = n / a.group, g = n - i * a.group;
-              x[it] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.e.shape.row0 + i) * a.q_stride + (s.h * a.group + g) * kKvDim + 8 * part);
+        const int pages = (s.e.shape.len + (1 << lp) - 1) >> lp;
+        int batch = -1, page = -1;                     // 32 pages at a time, one a lane
+        float ks = 0.f;
+        for (int t = 0; t < s.n; ++t, ++i) {
+          const int p0 = (s.tile + t) * ppt;
+          if ((p0 >> 5) != batch) {
+            batch = p0 >> 5;
+            const int p = 32 * batch + lane;
+            page = -1;
+            if (p < pages) {
+              page = a.block_table[(int64_t)s.e.b * a.table_stride + p];
+              if (page < 0 || page >= a.num_pages) {
+                if (p >= p0 && p < (s.tile + s.n) * ppt) atomicOr(err, kErrBadPage);
+                page = -1;
+              }
             }
+            ks = page >= 0 ? a.k_scales[(int64_t)page * a.kv_heads + s.h] : 0.f;
           }
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int r = r0 + 6 * it + slot;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x[it]);
-            uint32_t top = 0;                          // largest finite |x|, as bf16 bits
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t p = w[e] & 0x7FFFu, y = (w[e] >> 16) & 0x7FFFu;
-              if (p < 0x7F80u) top = max(top, p);
-              if (y < 0x7F80u) top = max(top, y);
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // the largest goes to [2^14, 2^15): x * 2^(14 - E), E its exponent (held at -100: smaller rows score 0)
-            const int E = max((int)(top >> 7) - 127, -100);
-            const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
-              const uint32_t wl = w[e] << 16, wh = w[e] & 0xFFFF0000u;
-              const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
-              const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
-              const __half2 h = __floats2half2_rn(xl, xh);
-              w[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            if (r < kPromptPairs) {
-              const int rr = r & (kHalfPairs - 1);
-              *reinterpret_cast<uint4*>(sQ + (r >> 7) * kTileBytes + (part >> 3) * kChunkBytes + rr * 128 + (((part & 7) ^ (rr & 7)) << 4)) = x[it];
-              if (part == 0) factor[seg & 1][r] = __uint_as_float((uint32_t)(E - 14 + 127) << 23) * a.scale_log2;
-            }
-          }
+          const int st = i % kKStages, use = i / kKStages;
+          if (use > 0) ok = mbar_wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls);
+          if (!ok) break;
+          const int o = p0 & 31;
+          const int pg = __shfl_sync(0xffffffffu, page, (o + lane) & 31);
+          // 16-key group g lies in page g * 16 / page size of the tile
+          const int of_group = (o + ((16 * (lane & 7)) >> lp)) & 31;
+          const float kg = __shfl_sync(0xffffffffu, ks, of_group);
+          const int pg_g = __shfl_sync(0xffffffffu, page, of_group);   // every lane takes part
+          const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && pg_g < 0);
+          const bool load = lane < ppt && pg >= 0;
+          const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+          if (lane < 8) sks[i % kMetaBufs][lane] = kg;
+          if (lane == 0) sbad[i % kMetaBufs] = bad;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[st], loads * page_bytes);
+          __syncwarp();
+          if (load) tma_load_2d_hint(sK + st * kKBytes + lane * page_bytes, &k_map, 0, (pg * a.kv_heads + s.h) << lp, &k_full[st], policy);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
       }
+      // nothing may still be landing in shared memory when the CTA exits
+      for (int st = 0; st < kKStages; ++st)
+        if (i > st) mbar_wait(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -802,7 +841,7 @@ __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const _
   if (u == pa_unit_start(c + 1, units, ctas)) return;     // a range without units
   const int32_t* rec = a.rec + 8 * c;
   const int b = __ldcg(rec), h = __ldcg(rec + 1), qt = __ldcg(rec + 2), tile = __ldcg(rec + 3), tiles = __ldcg(rec + 4);
-  if (tile == 0) return;                                   // the range begins with a segment
+  if (b < 0 || tile == 0) return;                          // nothing was written, or the range begins with a segment
   const int64_t seg = u - tile;
   const int first = pa_cta_of_unit(u - 1, units, ctas);
   if (pa_unit_start(first, units, ctas) > seg) return;     // an earlier boundary cuts it, too
@@ -850,19 +889,18 @@ __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const _
   if (a.lse && blockIdx.y == 0) a.lse[at] = L == 0.f ? -INFINITY : (M - pp::kPLog2 + log2f(L)) * 0.69314718055994530942f;
 }
 
-cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const uint8_t* k_codes, const uint8_t* v_codes, int ctas,
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, const uint8_t* v_codes, int ctas,
                                 cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = once_per_device(ready, [] {
-    const int most = pp::kFixedSmem + DSA_MAX_REQUESTS * (int)sizeof(int32_t);
+    const int most = pp::kFixedSmem;
     cudaError_t r = cudaFuncSetAttribute(paged_prompt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return r;
   });
   if (e != cudaSuccess) return e;
-  const size_t smem = pp::kFixedSmem + (size_t)a.num_requests * sizeof(int32_t);
   e = launch_pdl(a.cap_log2 > 0.f || a.slopes ? paged_prompt_kernel<true> : paged_prompt_kernel<false>, dim3(ctas),
-                 dim3(pp::kThreads), smem, s, k_codes, v_codes, a);
+                 dim3(pp::kThreads), pp::kFixedSmem, s, k_map, v_codes, a);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (ctas > 1) {

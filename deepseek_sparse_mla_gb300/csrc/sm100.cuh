@@ -93,6 +93,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   return false;
 }
 
+// mbar_wait for a whole warp that goes on with warp-wide operations: every lane gets the same answer, also where
+// the polls run out just as the phase completes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code,
+                                               uint32_t max_polls) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, code, max_polls));
+}
+
 // ---------------------------------------------------------------------------
 // proxy fences
 // ---------------------------------------------------------------------------
