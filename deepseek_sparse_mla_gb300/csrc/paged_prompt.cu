@@ -19,7 +19,8 @@
 // Per CTA (20 warps): warps 0-3 and 4-7 are the softmax of the two 128-pair halves, one pair a thread (no
 // cross-lane work at all); each half has a warp of its own that issues its products (16 and 17), so that one
 // half's softmax runs while the tensor cores work for the other, and P goes to them 64 keys at a time.
-// Warp 18 loads K tiles by TMA; warps 8-11 and 12-15 widen the V tiles, even and odd ones.
+// Warp 18 loads K tiles by TMA; warps 8-11 and 12-15 widen the V tiles, even and odd ones; warp 19 finds the CTA's
+// segments, ahead of the others (each finding them for itself cost 30 registers in every role, and spills).
 // TMEM (all 512 columns): S of half q at 128 q, with P over its first 64 columns; O of half q at 256 + 128 q.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
@@ -39,8 +40,8 @@ constexpr int kVBytes = kTok * kKvDim * 2;           // 32 KB of fp16: two 64-wi
 constexpr int kChunkBytes = kTok * 128;
 constexpr int kKStages = 4;
 constexpr int kThreads = 640;
-constexpr int kConvWarp0 = 8, kMmaWarp0 = 16, kLoadWarp = 18;
-constexpr uint32_t kRegsSoft = 128, kRegsConv = 88, kRegsRest = 48;   // 2 * 128 + 2 * 88 + 48 = 480 = 5 * 96, the launch's
+constexpr int kConvWarp0 = 8, kMmaWarp0 = 16, kLoadWarp = 18, kSchedWarp = 19;
+constexpr uint32_t kRegsSoft = 128, kRegsConv = 80, kRegsRest = 64;   // 2 * 128 + 2 * 80 + 64 = 480 = 5 * 96, the launch's
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
@@ -79,21 +80,24 @@ __device__ __forceinline__ PpEntry pp_entry(const PagedAttnArgs& a, int b, int q
   return e;
 }
 
-// A run of tiles of one segment (entry and K/V head)
-struct PpSeg {
-  PpEntry e;
-  int h, tile, n;
+// A run of tiles of one segment (entry and K/V head), as the scheduler warp leaves it in shared memory for the others
+struct __align__(16) PpSeg {
+  int n, tile, h, qt;              // its tiles and the first of them (n = 0: no further segment)
+  int b, tiles, slot, rows;        // the segment's tiles; where a piece goes
+  int row0, len, start, prefix;    // as in PaShape and PpEntry
 };
 
-// Where a role stands: the entry and how many units before it
+__device__ __forceinline__ int pp_limit(const PpSeg& s, int row) { return min(max(s.start + row + 1, s.prefix), s.len); }
+
+// Where the scheduler stands: the entry and how many units before it
 struct PpCursor {
   int b, qt;
   int64_t before;                  // units of the entries before this one
 };
 
 // The segment that unit u lies in, cut at u1; the cursor moves up to its entry.
-__device__ __forceinline__ PpSeg pp_segment(const PagedAttnArgs& a, PpCursor& c, int64_t u, int64_t u1) {
-  PpSeg s;
+__device__ __forceinline__ PpSeg pp_segment(const PagedAttnArgs& a, PpCursor& c, int64_t u, int64_t u0, int64_t u1, int cta) {
+  PpEntry e;
   for (;;) {
     uint32_t none = 0;
     const PaShape sh = pa_shape(a, c.b, none);
@@ -102,16 +106,26 @@ __device__ __forceinline__ PpSeg pp_segment(const PagedAttnArgs& a, PpCursor& c,
       c.qt = 0;
       continue;
     }
-    s.e = pp_entry(a, c.b, c.qt);
-    const int64_t units = (int64_t)s.e.tiles * a.kv_heads;
+    e = pp_entry(a, c.b, c.qt);
+    const int64_t units = (int64_t)e.tiles * a.kv_heads;
     if (u < c.before + units) break;
     c.before += units;
     ++c.qt;
   }
+  PpSeg s;
   const int in = (int)(u - c.before);
-  s.h = in / s.e.tiles;
-  s.tile = in - s.h * s.e.tiles;
-  s.n = (int)min((int64_t)(s.e.tiles - s.tile), u1 - u);
+  s.h = in / e.tiles;
+  s.tile = in - s.h * e.tiles;
+  s.n = (int)min((int64_t)(e.tiles - s.tile), u1 - u);
+  s.qt = e.qt;
+  s.b = e.b;
+  s.tiles = e.tiles;
+  s.slot = u == u0 ? 2 * cta : 2 * cta + 1;
+  s.rows = e.shape.rows;
+  s.row0 = e.shape.row0;
+  s.len = e.shape.len;
+  s.start = e.start;
+  s.prefix = e.prefix;
   return s;
 }
 
@@ -320,7 +334,8 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   __shared__ int32_t run_units[kRuns];                // units (without heads) of the runs before
   __shared__ int32_t scan[kThreads / 32];
   __shared__ float vmax_part[8], v_ref[kSegBufs];     // V's reference of a segment
-  __shared__ int seg_tiles[2][2];
+  __shared__ PpSeg segs[kSegBufs];
+  __shared__ uint64_t seg_full[kSegBufs], seg_empty[kSegBufs];
   __shared__ uint32_t tmem_base, bits_all;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -339,6 +354,10 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       mbar_init(&q_full[i], 4);
       mbar_init(&o_full[i], 2);
       mbar_init(&o_empty[i], 4);
+    }
+    for (int i = 0; i < kSegBufs; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 19);                    // every warp of the other roles
     }
     mbar_init(&mma_done, 2);
     prefetch_tmap(&k_map);
@@ -421,9 +440,9 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   const int64_t units = (int64_t)scan[0] * a.kv_heads;
   const int64_t u0 = pa_unit_start(cta, units, ctas), u1 = pa_unit_start(cta + 1, units, ctas);
   uint32_t* const err = &bits_all;
-  // every role starts at the run that holds u0
+  // the scheduler starts at the run that holds u0
   PpCursor cur = {0, 0, 0};
-  if (u0 < u1) {
+  if (warp == kSchedWarp && u0 < u1) {
     int lo = 0, hi = kRuns - 1;                       // the last run whose units begin at or before u0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -444,42 +463,37 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     uint8_t* const q_hi = sQ + 2 * q * kQTermBytes;
     // this thread's pair of a segment: its row and head (of the last pair where there are fewer)
     auto pair_of = [&](const PpSeg& s, int& r, int& head) {
-      const int n = min(s.e.qt * kPromptPairs + kHalfPairs * q + row, s.e.shape.rows * a.group - 1);
+      const int n = min(s.qt * kPromptPairs + kHalfPairs * q + row, s.rows * a.group - 1);
       r = n / a.group;
       head = s.h * a.group + (n - r * a.group);
-      return s.e.qt * kPromptPairs + kHalfPairs * q + row == n;
+      return s.qt * kPromptPairs + kHalfPairs * q + row == n;
     };
     // the queries of a segment, once the last segment's scores have been computed
-    auto load_queries = [&](const PpSeg& s, int seg) {
+    auto load_queries = [&](const PpSeg& s) {
       int r, head;
       const bool there = pair_of(s, r, head);
-      const float cf = pp_query(a, a.q + (int64_t)(s.e.shape.row0 + r) * a.q_stride + (int64_t)head * kKvDim, there, q_hi, row);
-      if (row == 0) seg_tiles[q][seg & 1] = s.n;
+      const float cf = pp_query(a, a.q + (int64_t)(s.row0 + r) * a.q_stride + (int64_t)head * kKvDim, there, q_hi, row);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[q]);
       return cf;
     };
-    int i = 0, seg = 0;
-    bool ok = true;
-    PpSeg s = {};
+    int i = 0;
+    bool ok = mbar_wait_warp(&seg_full[0], 0, err, kErrMmaTimeout, kPolls);
     float cf = 0.f;
-    int64_t u = u0;
-    if (u < u1) {
-      s = pp_segment(a, cur, u, u1);
-      cf = load_queries(s, 0);
-    }
-    while (u < u1) {
-      const int64_t u_first = u;
-      u += s.n;
+    if (ok && segs[0].n) cf = load_queries(segs[0]);
+    for (int seg = 0; ok; ++seg) {
+      const PpSeg& s = segs[seg % kSegBufs];
+      const int tiles = s.n;
+      if (tiles == 0) break;
       int r, head;
       const bool there = pair_of(s, r, head);
-      PpRow w = {-INFINITY, 0.f, cf, kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f, pp_limit(s.e, r),
-                 s.e.start + r};
+      PpRow w = {-INFINITY, 0.f, cf, kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f, pp_limit(s, r), s.start + r};
       // keys below it are seen by every pair of this half
-      const int min_limit = pp_limit(s.e, min(s.e.qt * kPromptPairs + kHalfPairs * q, s.e.shape.rows * a.group - 1) / a.group);
-      for (int t = 0; t < s.n && ok; ++t, ++i) {
-        const int key0 = (s.tile + t) * kTok;
+      const int min_limit = pp_limit(s, min(s.qt * kPromptPairs + kHalfPairs * q, s.rows * a.group - 1) / a.group);
+      const int tile0 = s.tile;
+      for (int t = 0; t < tiles && ok; ++t, ++i) {
+        const int key0 = (tile0 + t) * kTok;
         // the scores' arrival also stands for the tile's scales: K's own barrier may be a phase further by now
         ok = mbar_wait_warp(&s_full[q], i & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
@@ -520,20 +534,19 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         }
       }
       if (!ok) break;
-      PpSeg next = {};
-      if (u < u1) {
-        next = pp_segment(a, cur, u, u1);
-        cf = load_queries(next, seg + 1);
-      }
+      const int nx = (seg + 1) % kSegBufs;
+      ok = mbar_wait_warp(&seg_full[nx], ((seg + 1) / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+      if (!ok) break;
+      if (segs[nx].n) cf = load_queries(segs[nx]);
       // ---- the segment's end
-      const bool whole = s.n == s.e.tiles;
-      const int slot = u_first == u0 ? 2 * cta : 2 * cta + 1;
+      const bool whole = s.n == s.tiles;
       ok = mbar_wait_warp(&o_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
       tc_fence_after();
       const float m = w.m, l = w.l;
       const bool any = l > 0.f || l != l;
-      const int64_t at = (int64_t)(s.e.shape.row0 + r) * a.kv_heads * a.group + head;
+      const int64_t at = (int64_t)(s.row0 + r) * a.kv_heads * a.group + head;
+      const int slot = s.slot;
       const float vref = v_ref[seg % kSegBufs];
       const float f = !any ? 0.f : whole ? vref / l : vref;
       const int* nk = nan_key[seg % kSegBufs];
@@ -577,36 +590,43 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           a.lse[at] = any ? (m - kPLog2 + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
         }
       }
-      if (tid == 0 && u_first == u0) {                 // for the join: this CTA's first piece
+      if (tid == 0 && seg == 0) {                      // for the join: this CTA's first piece
         int32_t* rec = a.rec + 8 * cta;
-        rec[0] = s.e.b;
+        rec[0] = s.b;
         rec[1] = s.h;
-        rec[2] = s.e.qt;
+        rec[2] = s.qt;
         rec[3] = s.tile;
-        rec[4] = s.e.tiles;
+        rec[4] = s.tiles;
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&o_empty[q]);
-      s = next;
-      ++seg;
+      if (lane == 0) {
+        mbar_arrive(&o_empty[q]);
+        mbar_arrive(&seg_empty[seg % kSegBufs]);
+      }
     }
   } else if (warp < kMmaWarp0) {
     regs_dec<kRegsConv>();
     // ---------------------------------------------------------------- V tiles: codes to fp16
     // Two groups of four warps take alternate tiles: eight lanes a row of 16-byte pieces, 16 rows a pass, so that a
-    // pass is one 16-key group and lies in one page.  A tile's loads go out after the last tile's fence, which
+    // pass is one 16-key group and lies in one page.  Eight neighbouring lanes hold half of two rows each, whose
+    // units in the swizzled tile do not share a bank.  A tile's loads go out after the last tile's fence, which
     // would wait for loads in flight too.
-    const int grp = (warp - kConvWarp0) >> 2, cw = warp & 3, part = lane & 7, sub = 4 * cw + (lane >> 3), lp = a.log2_page;
-    const int unit = 2 * (part & 3), swap = part >> 2;
-    uint8_t* const tile = sV + grp * kVBytes + (part >> 2) * kChunkBytes;
-    int i0 = 0, seg = 0;                               // i0: the CTA's tiles before this segment
+    const int grp = (warp - kConvWarp0) >> 2, cw = warp & 3, lp = a.log2_page;
+    const int part = (lane & 3) + 4 * (lane >> 4), sub = 4 * cw + ((lane >> 2) & 3);
+    uint8_t* const tile = sV + grp * kVBytes + (part >> 2) * kChunkBytes + sub * 128;   // row 16 g + sub: 2048 g on
+    const int at_lo = ((2 * (part & 3)) ^ (sub & 7)) << 4, at_hi = ((2 * (part & 3) + 1) ^ (sub & 7)) << 4;
+    int i0 = 0;                                        // the CTA's tiles before this segment
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const PpSeg s = pp_segment(a, cur, u, u1);
-      u += s.n;
-      const int len = s.e.shape.len, pages = (len + (1 << lp) - 1) >> lp;
-      const int32_t* table = a.block_table + (int64_t)s.e.b * a.table_stride;
+    for (int seg = 0;; ++seg) {
+      ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+      if (!ok) break;
+      const PpSeg s = segs[seg % kSegBufs];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
+      if (s.n == 0) break;
+      const int len = s.len, pages = (len + (1 << lp) - 1) >> lp;
+      const int32_t* table = a.block_table + (int64_t)s.b * a.table_stride;
       // this lane's 16 bytes of row 0 of page 0; a page further is page_step bytes on
       const uint8_t* const base = v_codes + ((int64_t)s.h << lp) * kKvDim + 16 * part;
       const int64_t page_step = ((int64_t)a.kv_heads << lp) * kKvDim;
@@ -635,13 +655,14 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       if (warp == kConvWarp0 && lane == 0) v_ref[seg % kSegBufs] = vref;
       const float vinv = 1.f / vref;
       named_bar_sync(1, 256);
-      const int min_limit = pp_limit(s.e, min(s.e.qt * kPromptPairs, s.e.shape.rows * a.group - 1) / a.group);
+      const int min_limit = pp_limit(s, min(s.qt * kPromptPairs, s.rows * a.group - 1) / a.group);
 
       uint4 x[8];
       float scale = 0.f;
       int t = (i0 + grp) & 1;
       // lane g (and g + 8, ..): the page of 16-key group g, of the tile to load and of this group's next one
-      int id = id_of((s.tile + t) * kTok + 16 * part), id2 = id_of((s.tile + t + 2) * kTok + 16 * part);
+      const int own = 16 * (lane & 7);
+      int id = id_of((s.tile + t) * kTok + own), id2 = id_of((s.tile + t + 2) * kTok + own);
       auto load = [&](int key0) {
         scale = id >= 0 ? a.v_scales[(int64_t)id * a.kv_heads + s.h] : 0.f;
 #pragma unroll
@@ -679,24 +700,23 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         const float ratio = scale * vinv;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          const int r = 16 * g + sub;
           const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, g));
           uint4 lo = widen8(x[g].x, x[g].y), hi = widen8(x[g].z, x[g].w);
           lo = make_uint4(mul2(lo.x, f), mul2(lo.y, f), mul2(lo.z, f), mul2(lo.w, f));
           hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
-          // lanes of the two column chunks start with different units, so that eight lanes fill all banks
-          *reinterpret_cast<uint4*>(tile + r * 128 + (((unit + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(tile + r * 128 + (((unit + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+          *reinterpret_cast<uint4*>(tile + 2048 * g + at_lo) = lo;
+          *reinterpret_cast<uint4*>(tile + 2048 * g + at_hi) = hi;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[grp]);
         if (t + 2 < s.n) {
           id = id2;
-          id2 = id_of(key0 + 4 * kTok + 16 * part);
+          id2 = id_of(key0 + 4 * kTok + own);
           load(key0 + 2 * kTok);
         }
       }
+      if (!ok) break;
       i0 += s.n;
     }
   } else {
@@ -711,11 +731,10 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       const uint64_t d_q = smem_desc(smem_u32(sQ + 2 * q * kQTermBytes), 16, 1024, kSwizzle128B);
       const uint64_t d_k = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
       const uint64_t d_v = smem_desc(smem_u32(sV), kChunkBytes, 1024, kSwizzle128B);
-      const int n_all = (int)(u1 - u0);
       bool ok = true;
       auto scores = [&](int i) {
         const int st = i % kKStages;
-        ok = ok && mbar_spin(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout);
+        ok = ok && mbar_wait(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout, kPolls);
         if (!ok) return;
         tc_fence_after();
         const uint64_t k = d_k + (uint64_t)((st * kKBytes) >> 4);
@@ -730,18 +749,23 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         __syncwarp();
       };
       int i = 0;
-      for (int seg = 0; i < n_all && ok; ++seg) {
+      for (int seg = 0;; ++seg) {
+        ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+        if (!ok) break;
+        const int n = segs[seg % kSegBufs].n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
+        if (n == 0) break;
         ok = mbar_wait_warp(&q_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
-        const int n = seg_tiles[q][seg & 1];
         scores(i);
         if (seg > 0) ok = ok && mbar_wait_warp(&o_empty[q], (seg - 1) & 1, err, kErrMmaTimeout, kPolls);
         for (int t = 0; t < n && ok; ++t, ++i) {
           const uint64_t v = d_v + (uint64_t)(((i & 1) * kVBytes) >> 4);
-          ok = mbar_spin(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout);
+          ok = mbar_wait(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            ok = ok && mbar_spin(&p_full[q][h], i & 1, err, kErrMmaTimeout);
+            ok = ok && mbar_wait(&p_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
@@ -762,6 +786,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           }
           if (t + 1 < n) scores(i + 1);
         }
+        if (!ok) break;
       }
       if (leader) mma_commit(&mma_done);
       mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
@@ -772,10 +797,14 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       const uint32_t page_bytes = (uint32_t)kKvDim << lp;
       int i = 0;
       bool ok = true;
-      for (int64_t u = u0; u < u1 && ok;) {
-        const PpSeg s = pp_segment(a, cur, u, u1);
-        u += s.n;
-        const int pages = (s.e.shape.len + (1 << lp) - 1) >> lp;
+      for (int seg = 0;; ++seg) {
+        ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+        if (!ok) break;
+        const PpSeg s = segs[seg % kSegBufs];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
+        if (s.n == 0) break;
+        const int pages = (s.len + (1 << lp) - 1) >> lp;
         int batch = -1, page = -1;                     // 32 pages at a time, one a lane
         float ks = 0.f;
         for (int t = 0; t < s.n; ++t, ++i) {
@@ -785,7 +814,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             const int p = 32 * batch + lane;
             page = -1;
             if (p < pages) {
-              page = a.block_table[(int64_t)s.e.b * a.table_stride + p];
+              page = a.block_table[(int64_t)s.b * a.table_stride + p];
               if (page < 0 || page >= a.num_pages) {
                 if (p >= p0 && p < (s.tile + s.n) * ppt) atomicOr(err, kErrBadPage);
                 page = -1;
@@ -812,10 +841,26 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           __syncwarp();
           if (load) tma_load_2d_hint(sK + st * kKBytes + lane * page_bytes, &k_map, 0, (pg * a.kv_heads + s.h) << lp, &k_full[st], policy);
         }
+        if (!ok) break;
       }
       // nothing may still be landing in shared memory when the CTA exits
       for (int st = 0; st < kKStages; ++st)
         if (i > st) mbar_wait(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
+    } else {
+      // ---------------------------------------------------------------- scheduler: the segments, and an end mark
+      int64_t u = u0;
+      for (int seg = 0;; ++seg) {
+        if (seg >= kSegBufs && !mbar_wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+        PpSeg s = {};
+        if (u < u1) s = pp_segment(a, cur, u, u0, u1, cta);
+        if (lane == 0) {
+          segs[seg % kSegBufs] = s;
+          mbar_arrive(&seg_full[seg % kSegBufs]);
+        }
+        __syncwarp();
+        if (s.n == 0) break;
+        u += s.n;
+      }
     }
   }
   tc_fence_before();
