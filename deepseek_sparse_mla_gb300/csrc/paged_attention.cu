@@ -62,7 +62,7 @@ constexpr uint32_t kTmemCols = 512;             // S^T of warpgroup w at 64 w, O
 constexpr uint32_t kColO = 128;
 constexpr float kSlack = 2.f;                   // log2 by which a maximum may be exceeded
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
-constexpr uint32_t kPolls = 1u << 17;           // about a second
+constexpr uint32_t kPolls = 1u << 11;           // of a millisecond at most
 constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 }  // namespace pa
 

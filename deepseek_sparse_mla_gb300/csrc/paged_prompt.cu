@@ -17,16 +17,21 @@
 // Segments count the tiles their last row sees, so causal rows are balanced over the CTAs.
 //
 // Per CTA (20 warps): warps 0-3 and 4-7 are the softmax of the two 128-pair halves, one pair a thread (no
-// cross-lane work at all); each half has a warp of its own that issues its products (16 and 17), so that one
-// half's softmax runs while the tensor cores work for the other, and P goes to them 64 keys at a time.
+// cross-lane work at all); each half has a warp of its own that issues its products (16 and 17).  A half goes
+// through a tile as two times 64 keys, each with its own 64 columns of TMEM for S and then P: while the
+// softmax works on one, the tensor cores add the other to O and compute the next tile's S in its place.  One
+// S of 128 keys a half, its softmax and its products taking turns, took 4,500 cycles a tile (3.8 ms
+// for 4,096 rows at 64K); the scores' products are a half slower at 64 keys, which this more than pays for.
 // Warp 18 loads K tiles by TMA; warps 8-11 and 12-15 widen the V tiles, even and odd ones; warp 19 finds the CTA's
 // segments, ahead of the others (each finding them for itself cost 30 registers in every role, and spills).
-// TMEM (all 512 columns): S of half q at 128 q, with P over its first 64 columns; O of half q at 256 + 128 q.
+// TMEM (all 512 columns): S of half q and key half h at 128 q + 64 h, with P over its first 32; O of half q at 256 + 128 q.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 namespace dsa {
 using namespace sm100;
@@ -45,7 +50,7 @@ constexpr uint32_t kRegsSoft = 128, kRegsConv = 80, kRegsRest = 64;   // 2 * 128
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
-constexpr uint32_t kPolls = 1u << 17;                // about a second
+constexpr uint32_t kPolls = 1u << 11;                // of a millisecond at most
 constexpr int kRuns = 512;                           // runs of (request, pairs) entries that are summed
 constexpr int kMetaBufs = 8;                         // tiles whose K scales are kept (a tile's outlive its K stage)
 constexpr int kSegBufs = 4;
@@ -326,7 +331,8 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   uint8_t* sV = sK + kKStages * kKBytes;
   int32_t* entry_end = reinterpret_cast<int32_t*>(sV);   // [requests] entries of requests 0 .. b, before V is there
 
-  __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2], s_full[2], p_full[2][2], pv_done[2];
+  __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2];
+  __shared__ uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // by pairs' half and keys' half
   __shared__ uint64_t q_full[2], o_full[2], o_empty[2], mma_done;
   __shared__ __align__(16) float sks[kMetaBufs][8];   // K scale of each 16 keys of a tile
   __shared__ uint32_t sbad[kMetaBufs];                // 16-key groups without a valid page
@@ -348,9 +354,11 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], 2);
-      mbar_init(&s_full[i], 2);                        // the products, and their issuer
-      for (int h = 0; h < 2; ++h) mbar_init(&p_full[i][h], 4);
-      mbar_init(&pv_done[i], 1);                       // the first 64 keys' product
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&s_full[i][h], 2);                   // the products, and their issuer
+        mbar_init(&p_full[i][h], 4);
+        mbar_init(&pv_done[i][h], 1);
+      }
       mbar_init(&q_full[i], 4);
       mbar_init(&o_full[i], 2);
       mbar_init(&o_empty[i], 4);
@@ -492,45 +500,48 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       // keys below it are seen by every pair of this half
       const int min_limit = pp_limit(s, min(s.qt * kPromptPairs + kHalfPairs * q, s.rows * a.group - 1) / a.group);
       const int tile0 = s.tile;
+      // 64 keys of tile t.  The masked form is a separate body as a whole, not a variant of a part of it: with one
+      // body and the scores' pass chosen inside it the unmasked tiles took 5,400 cycles instead of 3,400.
+      auto keys64 = [&](auto masked, int t, int h, uint32_t bad) {
+        const int key0 = (tile0 + t) * kTok + 64 * h;
+        const float* ks = sks[i % kMetaBufs] + 4 * h;
+        uint32_t p[32];
+        float sum;
+        for (;;) {
+          const float top = pp_half<kMods, decltype(masked)::value>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks, p, sum);
+          const bool grow = top > w.m + kSlack || (w.m == -INFINITY && top > w.m);
+          if (!__any_sync(0xffffffffu, grow)) break;
+          const float m_new = grow ? top : w.m;
+          const float al = m_new == w.m ? 1.f : w.m == -INFINITY ? 0.f : ex2_approx(w.m - m_new);
+          if (t > 0 || h > 0) {
+            // the accumulator is settled when the 64 keys before have been added
+            ok = mbar_wait_warp(&pv_done[q][h ^ 1], (i - 1 + h) & 1, err, kErrMmaTimeout, kPolls);
+            if (!ok) return;
+            tc_fence_after();
+            pp_shrink(tO, al);
+            w.l *= al;
+          }
+          w.m = m_new;
+        }
+        w.l += sum;
+        // P takes the first half of the scores' columns
+        tmem_st32(tS + 64 * h, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[q][h]);
+      };
       for (int t = 0; t < tiles && ok; ++t, ++i) {
-        const int key0 = (tile0 + t) * kTok;
-        // the scores' arrival also stands for the tile's scales: K's own barrier may be a phase further by now
-        ok = mbar_wait_warp(&s_full[q], i & 1, err, kErrMmaTimeout, kPolls);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t bad = sbad[i % kMetaBufs];
-        const bool masked = key0 + kTok > min_limit || bad;          // uniform in the warpgroup
+        const int key_end = (tile0 + t + 1) * kTok;
 #pragma unroll 1
         for (int h = 0; h < 2 && ok; ++h) {
-          uint32_t p[32];
-          float sum;
-          for (;;) {
-            const float* ks = sks[i % kMetaBufs] + 4 * h;
-            const float top = masked ? pp_half<kMods, true>(w, a, tS + 64 * h, key0 + 64 * h, bad >> (4 * h), ks, p, sum)
-                                     : pp_half<kMods, false>(w, a, tS + 64 * h, key0 + 64 * h, 0, ks, p, sum);
-            const bool grow = top > w.m + kSlack || (w.m == -INFINITY && top > w.m);
-            if (!__any_sync(0xffffffffu, grow)) break;
-            const float m_new = grow ? top : w.m;
-            const float al = m_new == w.m ? 1.f : w.m == -INFINITY ? 0.f : ex2_approx(w.m - m_new);
-            if (t > 0 || h > 0) {
-              // The accumulator is settled when this tile's first half has been added; the last tile's was before
-              // these scores were computed.
-              if (h > 0) ok = mbar_wait_warp(&pv_done[q], i & 1, err, kErrMmaTimeout, kPolls);
-              if (!ok) break;
-              tc_fence_after();
-              pp_shrink(tO, al);
-              w.l *= al;
-            }
-            w.m = m_new;
-          }
+          // the scores' arrival also stands for the tile's scales: K's own barrier may be a phase further by now
+          ok = mbar_wait_warp(&s_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
           if (!ok) break;
-          w.l += sum;
-          // P takes 32 columns of scores that have been read
-          tmem_st32(tS + 32 * h, p);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[q][h]);
+          tc_fence_after();
+          const uint32_t bad = sbad[i % kMetaBufs];
+          if (__any_sync(0xffffffffu, key_end > min_limit || bad)) keys64(std::true_type{}, t, h, bad);
+          else keys64(std::false_type{}, t, h, 0);
         }
       }
       if (!ok) break;
@@ -723,28 +734,29 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     regs_dec<kRegsRest>();
     if (warp < kLoadWarp) {
       // ---------------------------------------------------------------- products of one half
-      // S(i + 1) overwrites P(i), which O(i) has read: products of one thread run in order.
+      // Order: .. O(i, h) S(i + 1, h) ..: S takes the place of the P that O has read (products of one thread run in order).
       const int q = warp - kMmaWarp0;
       const bool leader = elect_one();
-      const uint32_t id_s = idesc_e4m3(128, kTok);
+      const uint32_t id_s = idesc_e4m3(128, 64);
       const uint32_t id_o = idesc_f16(128, kKvDim, false, false, false, true);
       const uint64_t d_q = smem_desc(smem_u32(sQ + 2 * q * kQTermBytes), 16, 1024, kSwizzle128B);
       const uint64_t d_k = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
       const uint64_t d_v = smem_desc(smem_u32(sV), kChunkBytes, 1024, kSwizzle128B);
       bool ok = true;
-      auto scores = [&](int i) {
+      auto scores = [&](int i, int h) {
         const int st = i % kKStages;
-        ok = ok && mbar_wait(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout, kPolls);
+        if (h == 0) ok = ok && mbar_wait_warp(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout, kPolls);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t k = d_k + (uint64_t)((st * kKBytes) >> 4);
+        const uint64_t k = d_k + (uint64_t)((st * kKBytes + 64 * h * kKvDim) >> 4);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)               // hi, then lo
-            mma_ss_f8(tmem + 128 * q, d_q + (uint64_t)(((kk >> 2) * kQTermBytes + (kk & 3) * 32) >> 4), k + 2 * (kk & 3), id_s, kk > 0);
-          mma_commit(&s_full[q]);
-          mbar_arrive(&s_full[q]);
-          mma_commit(&k_empty[st]);
+            mma_ss_f8(tmem + 128 * q + 64 * h, d_q + (uint64_t)(((kk >> 2) * kQTermBytes + (kk & 3) * 32) >> 4), k + 2 * (kk & 3), id_s,
+                      kk > 0);
+          mma_commit(&s_full[q][h]);
+          mbar_arrive(&s_full[q][h]);
+          if (h == 1) mma_commit(&k_empty[st]);
         }
         __syncwarp();
       };
@@ -758,23 +770,24 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (n == 0) break;
         ok = mbar_wait_warp(&q_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
-        scores(i);
+        scores(i, 0);
+        scores(i, 1);
         if (seg > 0) ok = ok && mbar_wait_warp(&o_empty[q], (seg - 1) & 1, err, kErrMmaTimeout, kPolls);
         for (int t = 0; t < n && ok; ++t, ++i) {
           const uint64_t v = d_v + (uint64_t)(((i & 1) * kVBytes) >> 4);
-          ok = mbar_wait(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
+          ok = mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            ok = ok && mbar_wait(&p_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
+            ok = ok && mbar_wait_warp(&p_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
 #pragma unroll
-              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                mma_ts(tmem + kColO + 128 * q, tmem + 128 * q + 8 * kk, v + (uint64_t)((kk * 16 * 128) >> 4), id_o, t > 0 || kk > 0);
-              if (h == 0) {
-                mma_commit(&pv_done[q]);
-              } else {
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(tmem + kColO + 128 * q, tmem + 128 * q + 64 * h + 8 * kk, v + (uint64_t)(((64 * h + 16 * kk) * 128) >> 4), id_o,
+                       t > 0 || h > 0 || kk > 0);
+              mma_commit(&pv_done[q][h]);
+              if (h == 1) {
                 mma_commit(&v_empty[i & 1]);
                 if (t + 1 == n) {
                   mma_commit(&o_full[q]);
@@ -783,13 +796,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
               }
             }
             __syncwarp();
+            if (t + 1 < n) scores(i + 1, h);
           }
-          if (t + 1 < n) scores(i + 1);
         }
         if (!ok) break;
       }
       if (leader) mma_commit(&mma_done);
-      mbar_wait(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+      mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
     } else if (warp == kLoadWarp) {
       // ---------------------------------------------------------------- K tiles
       const uint64_t policy = l2_evict_normal();
@@ -845,7 +858,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       }
       // nothing may still be landing in shared memory when the CTA exits
       for (int st = 0; st < kKStages; ++st)
-        if (i > st) mbar_wait(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
+        if (i > st) mbar_wait_warp(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
     } else {
       // ---------------------------------------------------------------- scheduler: the segments, and an end mark
       int64_t u = u0;

@@ -94,10 +94,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 }
 
 // mbar_wait for a whole warp that goes on with warp-wide operations: every lane gets the same answer, also where
-// the polls run out just as the phase completes.
+// the polls run out just as the phase completes.  Each poll may suspend the warp for up to a millisecond: many
+// warps that poll a shared-memory barrier in short turns delay every other access to shared memory (a
+// softmax warp's single load took 1,000 cycles beside a dozen of them).
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code,
                                                uint32_t max_polls) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, code, max_polls));
+  for (uint32_t i = 0; i < max_polls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+  }
+  atomicOr(err, code);
+  return false;
 }
 
 // ---------------------------------------------------------------------------
