@@ -689,24 +689,14 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         const int key0 = (s.tile + t) * kTok, i = i0 + t;
         if (i >= 2) ok = mbar_wait_warp(&v_empty[grp], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
-        // a NaN code of a key that only some rows see: out of the tile, and noted for the rows that see it
+        // NaN codes of a tile that only some rows see in full
+        uint32_t any_nan = 0;
         if (key0 + kTok > min_limit) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x[g]);
-            uint32_t any = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) any |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            if (any) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t f = ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                for (int k = 0; k < 4; ++k)
-                  if ((f >> (8 * k + 7)) & 1u) atomicMin(&nan_key[seg % kSegBufs][16 * part + 4 * e + k], key0 + 16 * g + sub);
-                w[e] &= ~((f >> 7) * 0xFFu);
-              }
-            }
-          }
+          for (int g = 0; g < 8; ++g)
+            any_nan |= ((x[g].x & 0x7F7F7F7Fu) + 0x01010101u) | ((x[g].y & 0x7F7F7F7Fu) + 0x01010101u) |
+                       ((x[g].z & 0x7F7F7F7Fu) + 0x01010101u) | ((x[g].w & 0x7F7F7F7Fu) + 0x01010101u);
+          any_nan &= 0x80808080u;
         }
         const float ratio = scale * vinv;
 #pragma unroll
@@ -717,6 +707,18 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
           *reinterpret_cast<uint4*>(tile + 2048 * g + at_lo) = lo;
           *reinterpret_cast<uint4*>(tile + 2048 * g + at_hi) = hi;
+        }
+        if (any_nan) {
+          // out of the tile, and noted for the rows that see the key
+#pragma unroll 1
+          for (int k = 0; k < 8 * 16; ++k) {
+            const int g = k >> 4, e = k & 15;
+            uint16_t* v = reinterpret_cast<uint16_t*>(tile + 2048 * g + (e < 8 ? at_lo : at_hi)) + (e & 7);
+            if ((*v & 0x7FFFu) > 0x7C00u) {
+              *v = 0;
+              atomicMin(&nan_key[seg % kSegBufs][16 * part + e], key0 + 16 * g + sub);
+            }
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
