@@ -13,8 +13,8 @@ PyTorch only provides device memory and streams.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -390,32 +390,50 @@ def dcp_merge(outs, lses, out=None, lse=None, stream=None):
 # ---------------------------------------------------------------------------------------------------------------------
 # the step planner, and the dense (draft) layer over its 8-bit K/V cache
 # ---------------------------------------------------------------------------------------------------------------------
-def _on(device, stream):
-    """The context in which a call allocates and launches: the tensors' device, and the stream given."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _elsewhere(device, stream):
+    """None where a call can go out as things are: no stream given, and the tensors on the current device.  Else the
+    context to make it in, with that stream (or the tensors' device and its current stream)."""
+    if stream is None:
+        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+# the current stream's handle, without the object around it (which costs as much as a launch)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t, heads, name):
+def _fits(t, dtype, shape, device, name):
+    """_need, and the device; one pass over the conditions where they hold."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _on_device(device, t, name):
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows(t, rows, heads, device, name):
     """A [rows, heads, 128] bf16 view whose rows may lie apart (a slice of a fused projection); returns the row stride."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != KV_DIM:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (rows, {heads}, {KV_DIM})")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != KV_DIM)):
+    if t.shape != (rows, heads, KV_DIM):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, heads, KV_DIM)}")
+    _on_device(device, t, name)
+    if rows == 0:
+        return heads * KV_DIM
+    apart, head, inner = t.stride()
+    if inner != 1 or (heads > 1 and head != KV_DIM):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * KV_DIM)
+    return apart if rows > 1 else heads * KV_DIM
+
+
+def _workspace_args(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 class PagePool:
@@ -455,38 +473,44 @@ def step_plan(pool: PagePool, seq_lens, new_lens, block_table, page_size: int, n
     prefix that rows and pages last for (check=True raises DsaError where some were not).  Pass seq_lens as
     seq_lens_out and pool.count as free_count_out to carry the step out; without, the plan is a proposal and the
     inputs keep their values (but for block-table entries behind a request's pages)."""
-    B = int(seq_lens.shape[0])
-    _need(seq_lens, torch.int32, (B,), "seq_lens")
     dev = seq_lens.device
-    with _on(dev, stream):
-        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)   # noqa: E731
-        seq_lens_out = new((B,), torch.int32) if seq_lens_out is None else seq_lens_out
-        query_start_loc = new((B + 1,), torch.int32) if query_start_loc is None else query_start_loc
-        slot_mapping = new((num_rows,), torch.int64) if slot_mapping is None else slot_mapping
-        positions = new((num_rows,), torch.int32) if positions is None else positions
-        free_count_out = new((1,), torch.int32) if free_count_out is None else free_count_out
-        for t, dtype, shape, name in ((new_lens, torch.int32, (B,), "new_lens"),
-                                      (block_table, torch.int32, (B, block_table.shape[-1]), "block_table"),
-                                      (pool.pages, torch.int32, pool.pages.shape, "pool.pages"),
-                                      (pool.count, torch.int32, (1,), "pool.count"),
-                                      (seq_lens_out, torch.int32, (B,), "seq_lens_out"),
-                                      (query_start_loc, torch.int32, (B + 1,), "query_start_loc"),
-                                      (slot_mapping, torch.int64, (num_rows,), "slot_mapping"),
-                                      (positions, torch.int32, (num_rows,), "positions"),
-                                      (free_count_out, torch.int32, (1,), "free_count_out")):
-            _need(t, dtype, shape, name)
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if check and workspace is None:
-            workspace = _workspace(256, dev)
-        _same_device(dev, workspace=workspace)
-        _lib.check(_lib.load().dsa_step_plan(
-            _ptr(seq_lens), _ptr(new_lens), B, page_size, _ptr(block_table), int(block_table.shape[1]), _ptr(pool.pages),
-            int(pool.pages.shape[0]), _ptr(pool.count), num_rows, _ptr(seq_lens_out), _ptr(query_start_loc),
-            _ptr(slot_mapping), _ptr(positions), _ptr(free_count_out), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
-        if check:
-            _check_device(workspace, stream)
+    _need(seq_lens, torch.int32, seq_lens.shape, "seq_lens")
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return step_plan(pool, seq_lens, new_lens, block_table, page_size, num_rows, seq_lens_out, query_start_loc,
+                             slot_mapping, positions, free_count_out, workspace, None, check)
+    (B,) = seq_lens.shape
+    i32 = torch.int32
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty((B,), dtype=i32, device=dev)
+    if query_start_loc is None:
+        query_start_loc = torch.empty((B + 1,), dtype=i32, device=dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty((num_rows,), dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty((num_rows,), dtype=i32, device=dev)
+    if free_count_out is None:
+        free_count_out = torch.empty((1,), dtype=i32, device=dev)
+    _fits(new_lens, i32, (B,), dev, "new_lens")
+    _fits(block_table, i32, (B, block_table.shape[-1]), dev, "block_table")
+    _fits(pool.pages, i32, (pool.pages.shape[0],), dev, "pool.pages")
+    _fits(pool.count, i32, (1,), dev, "pool.count")
+    _fits(seq_lens_out, i32, (B,), dev, "seq_lens_out")
+    _fits(query_start_loc, i32, (B + 1,), dev, "query_start_loc")
+    _fits(slot_mapping, torch.int64, (num_rows,), dev, "slot_mapping")
+    _fits(positions, i32, (num_rows,), dev, "positions")
+    _fits(free_count_out, i32, (1,), dev, "free_count_out")
+    if check and workspace is None:
+        workspace = _workspace(256, dev)
+    _on_device(dev, workspace, "workspace")
+    _lib.check(_lib.load().dsa_step_plan(
+        seq_lens.data_ptr(), new_lens.data_ptr(), B, page_size, block_table.data_ptr(), block_table.shape[1],
+        pool.pages.data_ptr(), pool.pages.shape[0], pool.count.data_ptr(), num_rows, seq_lens_out.data_ptr(),
+        query_start_loc.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), free_count_out.data_ptr(),
+        *_workspace_args(workspace), _raw_stream(dev.index)))
+    if check:
+        _check_device(workspace, None)
     return StepPlan(seq_lens_out, query_start_loc, slot_mapping, positions, free_count_out)
 
 
@@ -494,23 +518,26 @@ def pages_release(pool: PagePool, finished, seq_lens, block_table, page_size: in
                   stream=None, check=False):
     """Return the pages of the requests with finished[b] != 0 to the pool, in place: their table entries become -1
     and their lengths 0."""
-    B = int(seq_lens.shape[0])
-    _need(seq_lens, torch.int32, (B,), "seq_lens")
     dev = seq_lens.device
-    _need(finished, torch.int32, (B,), "finished")
-    _need(block_table, torch.int32, (B, block_table.shape[-1]), "block_table")
-    _need(pool.pages, torch.int32, pool.pages.shape, "pool.pages")
-    _need(pool.count, torch.int32, (1,), "pool.count")
-    _same_device(dev, finished=finished, block_table=block_table, pages=pool.pages, count=pool.count, workspace=workspace)
-    with _on(dev, stream):
-        if check and workspace is None:
-            workspace = _workspace(256, dev)
-        _lib.check(_lib.load().dsa_pages_release(
-            _ptr(finished), _ptr(seq_lens), B, page_size, _ptr(block_table), int(block_table.shape[1]), num_pages,
-            _ptr(pool.pages), int(pool.pages.shape[0]), _ptr(pool.count), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
-        if check:
-            _check_device(workspace, stream)
+    _need(seq_lens, torch.int32, seq_lens.shape, "seq_lens")
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return pages_release(pool, finished, seq_lens, block_table, page_size, num_pages, workspace, None, check)
+    (B,) = seq_lens.shape
+    _fits(finished, torch.int32, (B,), dev, "finished")
+    _fits(block_table, torch.int32, (B, block_table.shape[-1]), dev, "block_table")
+    _fits(pool.pages, torch.int32, (pool.pages.shape[0],), dev, "pool.pages")
+    _fits(pool.count, torch.int32, (1,), dev, "pool.count")
+    if check and workspace is None:
+        workspace = _workspace(256, dev)
+    _on_device(dev, workspace, "workspace")
+    _lib.check(_lib.load().dsa_pages_release(
+        finished.data_ptr(), seq_lens.data_ptr(), B, page_size, block_table.data_ptr(), block_table.shape[1], num_pages,
+        pool.pages.data_ptr(), pool.pages.shape[0], pool.count.data_ptr(), *_workspace_args(workspace),
+        _raw_stream(dev.index)))
+    if check:
+        _check_device(workspace, None)
 
 
 class BlockKvCache:
@@ -531,7 +558,8 @@ class BlockKvCache:
             _need(t, torch.uint8, k_codes.shape, name)
         _need(k_scales, torch.float32, k_codes.shape[:2], "k_scales")
         _need(v_scales, torch.float32, k_codes.shape[:2], "v_scales")
-        _same_device(k_codes.device, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales)
+        for t, name in ((v_codes, "v_codes"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+            _on_device(k_codes.device, t, name)
         cache = cls.__new__(cls)
         cache._set(k_codes, v_codes, k_scales, v_scales)
         return cache
@@ -545,28 +573,35 @@ class BlockKvCache:
                                 self.v_scales.data_ptr(), self.num_pages, self.page_size, self.kv_heads, 0)
 
 
-def _batch_device(batch, device):
-    _same_device(device, block_table=batch.block_table, seq_lens=batch.seq_lens, query_start_loc=batch.query_start_loc)
+def _batch_on(device, batch):
+    _on_device(device, batch.block_table, "batch.block_table")
+    _on_device(device, batch.seq_lens, "batch.seq_lens")
+    _on_device(device, batch.query_start_loc, "batch.query_start_loc")
 
 
 def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None):
     """Append the step's tokens to an 8-bit K/V cache: k, v [rows, kv_heads, 128] bf16 (rows may be strided), row r of
     the batch at its own position.  A page whose new tokens need a larger scale than it has is re-coded."""
-    k_stride, v_stride = _rows(k, cache.kv_heads, "k"), _rows(v, cache.kv_heads, "v")
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape[0] != batch.num_rows:
-            raise ValueError(f"{name}: {t.shape[0]} rows, expected {batch.num_rows}")
     dev = cache.k_codes.device
-    _same_device(dev, k=k, v=v)
-    _batch_device(batch, dev)
-    with _on(dev, stream):
-        c, b = cache.struct(), batch.struct()
-        _lib.check(_lib.load().dsa_kv8_append(ctypes.byref(c), ctypes.byref(b), _ptr(k), k_stride, _ptr(v), v_stride,
-                                              _stream(stream)))
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return kv8_append(cache, batch, k, v)
+    k_stride = _rows(k, batch.num_rows, cache.kv_heads, dev, "k")
+    v_stride = _rows(v, batch.num_rows, cache.kv_heads, dev, "v")
+    _batch_on(dev, batch)
+    _lib.check(_lib.load().dsa_kv8_append(ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), k.data_ptr(), k_stride,
+                                          v.data_ptr(), v_stride, _raw_stream(dev.index)))
 
 
 def paged_attention_workspace_bytes(q_heads: int, kv_heads: int, max_query_len: int) -> int:
     return int(_lib.load().dsa_paged_attention_workspace_bytes(q_heads, kv_heads, max_query_len))
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_attention_bytes(device_index, q_heads, kv_heads, max_query_len):
+    """The size alone, which depends on the device (current where this is called) and these three numbers."""
+    return paged_attention_workspace_bytes(q_heads, kv_heads, max_query_len)
 
 
 def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM ** -0.5, max_query_len: int | None = None,
@@ -576,40 +611,43 @@ def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM 
     be strided); returns (out [rows, q_heads, 128] bf16, lse).  max_query_len is a host bound on the rows of a request
     (the number of rows where it is not given).  softcap > 0 caps scores by a tanh, slopes [q_heads] fp32 subtracts
     slopes[h] * distance, prefix_lens [requests] int32 lets every row see the request's first positions.  Rows behind the
-    last request's are not written.  lse (optional) [rows, q_heads] fp32 is filled."""
+    last request's are not written.  lse (optional) [rows, q_heads] fp32 is filled.  Calls that may run at the same
+    time need a workspace each (one is allocated where none is given)."""
+    dev = cache.k_codes.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return paged_attention(cache, batch, q, scale, max_query_len, softcap, slopes, prefix_lens, out, lse, workspace,
+                                   None, check)
     if q.dim() != 3:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected (rows, heads, {KV_DIM})")
-    R, heads = batch.num_rows, int(q.shape[1])
-    q_stride = _rows(q, heads, "q")
-    if q.shape[0] != R:
-        raise ValueError(f"q: {q.shape[0]} rows, expected {R}")
-    dev = cache.k_codes.device
-    _same_device(dev, q=q, slopes=slopes, prefix_lens=prefix_lens, out=out, lse=lse, workspace=workspace)
-    _batch_device(batch, dev)
+    R, heads = batch.num_rows, q.shape[1]
+    q_stride = _rows(q, R, heads, dev, "q")
+    _batch_on(dev, batch)
     mods = None
     if softcap or slopes is not None or prefix_lens is not None:
         if slopes is not None:
-            _need(slopes, torch.float32, (heads,), "slopes")
+            _fits(slopes, torch.float32, (heads,), dev, "slopes")
         if prefix_lens is not None:
-            _need(prefix_lens, torch.int32, (batch.num_requests,), "prefix_lens")
+            _fits(prefix_lens, torch.int32, (batch.num_requests,), dev, "prefix_lens")
         mods = ctypes.byref(_lib.DsaAttnMods(float(softcap), 0, 0 if slopes is None else slopes.data_ptr(),
                                              0 if prefix_lens is None else prefix_lens.data_ptr()))
     if max_query_len is None:
         max_query_len = R if batch.query_start_loc is not None else 1
     max_query_len = max(int(max_query_len), 1)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((R, heads, KV_DIM), dtype=torch.bfloat16, device=dev)
-        else:
-            _need(out, torch.bfloat16, (R, heads, KV_DIM), "out")
-        if lse is not None:
-            _need(lse, torch.float32, (R, heads), "lse")
-        if workspace is None:
-            workspace = _workspace(paged_attention_workspace_bytes(heads, cache.kv_heads, max_query_len), dev)
-        c, b = cache.struct(), batch.struct()
-        _lib.check(_lib.load().dsa_paged_attention(
-            ctypes.byref(c), ctypes.byref(b), _ptr(q), q_stride, heads, float(scale), max_query_len, mods, _ptr(out),
-            _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
-        if check:
-            _check_device(workspace, stream)
+    shape = (R, heads, KV_DIM)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _fits(out, torch.bfloat16, shape, dev, "out")
+    if lse is not None:
+        _fits(lse, torch.float32, (R, heads), dev, "lse")
+    if workspace is None:
+        workspace = _workspace(_paged_attention_bytes(dev.index, heads, cache.kv_heads, max_query_len), dev)
+    _on_device(dev, workspace, "workspace")
+    _lib.check(_lib.load().dsa_paged_attention(
+        ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), q.data_ptr(), q_stride, heads, float(scale), max_query_len,
+        mods, out.data_ptr(), None if lse is None else lse.data_ptr(), *_workspace_args(workspace), _raw_stream(dev.index)))
+    if check:
+        _check_device(workspace, None)
     return out, lse
