@@ -771,7 +771,7 @@ dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batc
   a.lse = lse;
   a.max_rows = rows_max;
   return cuda_status(launch_paged_attention(a, static_cast<const uint8_t*>(cache->k_codes),
-                                            static_cast<const uint8_t*>(cache->v_codes), workspace, plan,
+                                            static_cast<const uint8_t*>(cache->v_codes), batch->max_seq_len, workspace, plan,
                                             (cudaStream_t)stream),
                      "paged attention launch");
 }

@@ -269,6 +269,7 @@ struct PagedAttnArgs {
   __nv_bfloat16* out;
   float* lse;
   int32_t max_rows;                 // of a request; one with more is refused
+  bool whole;                       // segments are not cut (no pieces to join)
   int32_t lo_pairs, hi_pairs;       // a kernel takes requests of lo < rows * group <= hi pairs
   uint32_t* err;                    // the workspace header
   int32_t* rec;                     // [ctas][8]: where each CTA's first piece lies
@@ -283,8 +284,8 @@ struct PagedAttnPlan {
   size_t rec_offset, part_offset, workspace_bytes;
 };
 PagedAttnPlan plan_paged_attention(int max_query_len, int group);
-cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, void* workspace,
-                                   const PagedAttnPlan& plan, cudaStream_t s);
+cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_seq_len,
+                                   void* workspace, const PagedAttnPlan& plan, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // device helpers

@@ -17,11 +17,13 @@
 //   S^T [128 keys x columns]  = K [128 x 128] (K-major)   * Q^T          (M = 128, N = 2 x columns, K = 128)
 //   O^T [128 dims x columns] += V^T (the same tile layout, MN-major) * P^T
 // A thread of the softmax warpgroup holds one key's scores, so masks, scales and page lookups are per
-// thread, and a column's maximum is one warp-wide redux.
+// thread, and a column's maximum, where it is needed, is one warp-wide redux.
 //
 // The v scale would be lost in P's 8 bits if pages differ, so P' = p * vs is what is coded, against a
 // running maximum of its own (of z + log2 vs), next to the softmax's maximum that the denominator uses.
-// Both maxima move only when exceeded by 2^2, and the accumulator in TMEM is then rescaled.
+// Both maxima move only when exceeded by 2^2, and the accumulator in TMEM is then rescaled.  A tile is first taken
+// against the references as they are; only where a contribution exceeds them (one predicate over the
+// warpgroup, on the barrier that P needs anyway) are the exact maxima found and the tile taken again.
 //
 // Work: (request, K/V head, column group, tile of 128 keys) units, laid out in that order and split into one
 // contiguous range per CTA (persistent, one CTA per SM).  A segment (all tiles of one request, head and
@@ -41,6 +43,7 @@
 #include "tmap.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace dsa {
 using namespace sm100;
@@ -58,9 +61,10 @@ constexpr int kThreads = 384;
 constexpr int kScoreWarp = 1, kOutWarp = 3, kSoftWarp0 = 4;
 constexpr uint32_t kRegsLow = 88, kRegsSoft = 208;   // 88 + 2 * 208 = 3 * 168, the launch's
 constexpr int kQBufs = 3;                       // the scores run two tiles, so up to two segments, ahead of the outputs
-constexpr uint32_t kTmemCols = 512;             // S^T of warpgroup w at 64 w, O^T at 128 + 128 (segment % 2) + 64 w
-constexpr uint32_t kColO = 128;
-constexpr float kSlack = 2.f;                   // log2 by which a maximum may be exceeded
+constexpr uint32_t kTmemCols = 512;             // S^T of tile i at 64 (i % 4), O^T at 256 + 128 (segment % 2) + 64 warpgroup
+constexpr uint32_t kColO = 256;
+constexpr int kSBufs = 4;                       // two a warpgroup: one is kept until its tile is known to be done
+constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
 constexpr uint32_t kPolls = 1u << 11;           // of a millisecond at most
 constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
@@ -99,10 +103,7 @@ __device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_
   return s;
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r);
-template <>
-__device__ __forceinline__ void tmem_ld_cols<8>(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld_cols8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
@@ -111,11 +112,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
-}
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8) tmem_ld_cols<8>(taddr + i, r + i);
 }
 
 // two e4m3 codes of (a, b), and of 16 times what they leave
@@ -130,7 +126,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 struct PaColumns {
   float factor[pa::kColMax];    // 2^k of the split query * softmax scale * log2 e
   int limit[pa::kColMax];       // keys below it are seen
-  int pos[pa::kColMax];
+  float pos[pa::kColMax];
   float slope[pa::kColMax];     // * log2 e
   int min_limit;                // over the columns
 };
@@ -150,12 +146,13 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   uint8_t* sP = sQ + kQBufs * kQBytes;
   int32_t* end = reinterpret_cast<int32_t*>(sP + 2 * kPBytes);   // [requests]
 
-  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], s_full[2], s_empty[2], p_full[2];
+  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], s_full[kSBufs], s_empty[kSBufs], p_full[2];
   __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[2], o_empty[2], mma_done;
   __shared__ float sks[kStages][kMaxPages], svs[kStages][kMaxPages];
   __shared__ uint32_t sbad[kStages];
   __shared__ __align__(16) PaColumns cols[kQBufs];
-  __shared__ float wmax[2][4][kCE], wlv[2][4], red[2][4][kCE], fin[2][2][kCE];
+  __shared__ __align__(16) float refs[2][2][kCE];
+  __shared__ float wmax[2][4][kCE], wlv[2][4], fin[2][2][kCE];
   __shared__ float stat[kQBufs][2][3][kCE];            // each warpgroup's m, mv and l of a segment
   __shared__ uint32_t stat_nan[kQBufs][2][kKvDim];
   __shared__ uint32_t nan_keys[2][4];
@@ -170,11 +167,13 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       mbar_init(&kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
       mbar_init(&p_full[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 4);
+    }
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
     }
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
@@ -225,7 +224,14 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   const int64_t units = (int64_t)end[a.num_requests - 1] * a.kv_heads;
-  const int64_t u0 = pa_unit_start(cta, units, ctas), u1 = pa_unit_start(cta + 1, units, ctas);
+  int64_t u0 = pa_unit_start(cta, units, ctas);
+  const int64_t u1 = pa_unit_start(cta + 1, units, ctas);
+  // segments are cut where the range ends, or (short requests) belong to the range they begin in as a whole
+  const int64_t cut = a.whole ? units : u1;
+  if (a.whole && u0 < u1) {
+    const PaSeg s = pa_segment(a, end, u0, units);
+    if (s.tile > 0) u0 += s.n;
+  }
   uint32_t* const err = &bits_all;                    // this CTA's status bits, stored at the end
 
   if (warp < kSoftWarp0) {
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     int i = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
-      const PaSeg s = pa_segment(a, end, u, u1);
+      const PaSeg s = pa_segment(a, end, u, cut);
       const int pages = (s.len + (1 << lp) - 1) >> lp;
       int batch = -1, page = -1;                       // 32 pages at a time, one a lane
       float ks = 0.f, vs = 0.f;
@@ -303,14 +309,14 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     int i = 0, seg = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const PaSeg s = pa_segment(a, end, u, u1);
+      const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
       const int qb = seg % kQBufs;
       ok = mbar_wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls);
       for (int t = 0; t < s.n && ok; ++t, ++i) {
-        const int st = i % kStages, sb = i & 1;
+        const int st = i % kStages, sb = i % kSBufs;
         ok = mbar_spin(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout);
-        if (ok && i >= 2) ok = mbar_spin(&s_empty[sb], ((i >> 1) - 1) & 1, err, kErrMmaTimeout);
+        if (ok && i >= kSBufs) ok = mbar_spin(&s_empty[sb], (i / kSBufs - 1) & 1, err, kErrMmaTimeout);
         if (!ok) break;
         tc_fence_after();
         const uint64_t k = d_k + (uint64_t)((st * kStageBytes) >> 4), q = d_q + (uint64_t)((qb * kQBytes) >> 4);
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     int i = 0, seg = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const PaSeg s = pa_segment(a, end, u, u1);
+      const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
       uint32_t fresh = 3;                              // accumulators of the segment without a product yet
       if (seg >= 2) ok = mbar_wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     const int part = lane & 15;
     int seg = 0;
     for (int64_t u = u0; u < u1; ++seg) {
-      const PaSeg s = pa_segment(a, end, u, u1);
+      const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
       const int buf = seg % kQBufs;
       if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
@@ -423,7 +429,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           // 2^(E - 7) is exact; a column past the last pair sees everything and is not written
           cm.factor[c] = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;
           cm.limit[c] = n < pairs ? limit : INT32_MAX;
-          cm.pos[c] = pos;
+          cm.pos[c] = (float)pos;
           cm.slope[c] = kMods && a.slopes && n < pairs ? a.slopes[s.h * a.group + (n - i * a.group)] * 1.4426950408889634f : 0.f;
         }
       }
@@ -443,77 +449,44 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     int i0 = 0, seg = 0;                               // i0: the CTA's tiles before this segment
     for (int64_t u = u0; u < u1; ++seg) {
-      const PaSeg s = pa_segment(a, end, u, u1);
+      const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
       const int qb = seg % kQBufs;
       if (!mbar_wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
       const uint32_t acc = tmem + lanes + kColO + 128 * (seg & 1);
       const PaColumns& cm = cols[qb];
       const int min_limit = cm.min_limit;
-      // the references of column `lane` (m: of z, mv: of z + log2 vs), and every column's in registers
+      const int live = min(s.rows * a.group - s.cg * kCE, kCE);   // columns in use
+      // the references of column `lane` (m: of z, mv: of z + log2 vs); every column's are in shared memory, as m and as
+      // kPOne * 2^(m - mv)
       float m_lane = -INFINITY, mv_lane = -INFINITY;
-      float m[kCE], e[kCE], l[kCE];
+      float* const ref_m = refs[wg][0];
+      float* const ref_e = refs[wg][1];
+      float l[kCE];
 #pragma unroll
-      for (int c = 0; c < kCE; ++c) {
-        m[c] = 0.f;
-        e[c] = kPOne;
-        l[c] = 0.f;
-      }
+      for (int c = 0; c < kCE; ++c) l[c] = 0.f;
       uint32_t poison = 0;                             // columns whose output at dim `row` is NaN
       bool ok = true, fresh = true;
-      for (int t = (i0 + wg) & 1; t < s.n; t += 2) {
-        const int i = i0 + t, st = i % kStages, sb = wg;
-        const int key0 = (s.tile + t) * kTok, j = key0 + row;
-        ok = mbar_wait_warp(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
-             mbar_wait_warp(&s_full[sb], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
-        if (!ok) break;
-        tc_fence_after();
-        float z[kCE];
-        const int pg = row >> a.log2_page;
+      // One tile, with kNC columns in use (blocks of 8, 16 or 32).  Each form is a body of its own, chosen once a tile: with
+      // guards and branches inside one body, the verify case (32 columns) took 394 us instead of XXX.
+      auto tile = [&](auto columns, auto with_masks, int i, int key0) {
+        constexpr int kNC = decltype(columns)::value;
+        constexpr bool kMasked = decltype(with_masks)::value;
+        const int st = i % kStages, sb = i % kSBufs, j = key0 + row, pg = row >> a.log2_page;
         const float ks = sks[st][pg], vs = svs[st][pg];
-        {
-          uint32_t hi[kCE], lo[kCE];
-          tmem_ld_cols<kCE>(tmem + lanes + 64 * sb, hi);
-          tmem_ld_cols<kCE>(tmem + lanes + 64 * sb + kHalf, lo);
-          tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[sb]);
-#pragma unroll
-          for (int c = 0; c < kCE; ++c)
-            z[c] = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c]);
-        }
-        if (kMods) {
-          if (a.cap_log2 > 0.f) {
-            // cap * tanh(z / cap) = cap * (1 - 2 / (1 + e^(2 z / cap))), in log2 units throughout
-            const float in = 2.f * 1.4426950408889634f / a.cap_log2;
-#pragma unroll
-            for (int c = 0; c < kCE; ++c) {
-              const float x = z[c] * in;
-              z[c] = a.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(x > 64.f ? 64.f : x)));   // NaN stays
-            }
-          }
-          if (a.slopes) {
-#pragma unroll
-            for (int c = 0; c < kCE; ++c) z[c] -= cm.slope[c] * (float)abs(cm.pos[c] - j);
-          }
-        }
-        const bool masked = key0 + kTok > min_limit || sbad[st] != 0;      // uniform in the CTA
-        bool has_nan = false;
-        if (masked) {
-          const bool exists = j < s.len && !((sbad[st] >> pg) & 1u);
-#pragma unroll
-          for (int c = 0; c < kCE; ++c)
-            if (!exists || j >= cm.limit[c]) z[c] = -INFINITY;
+        const bool exists = !kMasked || (j < s.len && !((sbad[st] >> pg) & 1u));
+        const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
+        if (kMasked) {
           // A key's values meet a probability of 0 where it is not seen, and 0 * NaN is NaN: what lies behind
-          // the request's tokens is zeroed here, and NaN codes of keys that only some columns see are
-          // taken out below.
+          // the request's tokens is zeroed here, and NaN codes of keys that only some columns see are taken out.
           uint4* vrow = reinterpret_cast<uint4*>(sKV + st * kStageBytes + kTileBytes + row * kKvDim);
+          bool has_nan = false;
           if (!exists) {
 #pragma unroll
             for (int q = 0; q < kKvDim / 16; ++q) vrow[q] = make_uint4(0, 0, 0, 0);
           } else if (j >= min_limit) {
             uint32_t hit = 0;
+#pragma unroll 1
             for (int q = 0; q < kKvDim / 16; ++q) {
               const uint4 w = vrow[q];
               hit |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
@@ -521,54 +494,91 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             }
             has_nan = (hit & 0x80808080u) != 0;
           }
-        }
-        // column maxima over the tile: lane c of every warp ends up with column c's
-        float mine = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kCE; ++c) {
-          const float r = warp_max_f32(z[c]);
-          if (lane == c) mine = r;
-        }
-        const float lv = fmaxf(__log2f(fabsf(vs)), -126.f);
-        const float lv_max = warp_max_f32(lv);
-        if (lane < kCE) wmax[sb][quarter][lane] = mine;
-        if (lane == 0) wlv[sb][quarter] = lv_max;
-        const bool any_nan = named_bar_or(bar, 128, has_nan);
-        float M = -INFINITY, MV = -INFINITY;
-        if (lane < kCE) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float x = wmax[sb][w][lane];
-            M = fmaxf(M, x);
-            MV = fmaxf(MV, x + wlv[sb][w]);
+          if (named_bar_or(bar, 128, has_nan)) {
+            const uint32_t who = __ballot_sync(0xffffffffu, has_nan);
+            if (lane == 0) nan_keys[wg][quarter] = who;
+            named_bar_sync(bar, 128);
+            const uint8_t* vt = sKV + st * kStageBytes + kTileBytes;
+            for (int w = 0; w < 4; ++w)
+              for (uint32_t left = nan_keys[wg][w]; left; left &= left - 1) {
+                const int k = 32 * w + __ffs(left) - 1;
+                const uint8_t code = vt[k * kKvDim + ((((uint32_t)row >> 4) ^ (k & 7)) << 4) + (row & 15)];
+                if ((code & 0x7Fu) == 0x7Fu)
+                  for (int c = 0; c < kCE; ++c)
+                    if (key0 + k < cm.limit[c]) poison |= 1u << c;
+              }
+            named_bar_sync(bar, 128);
+            if (has_nan) {
+              uint32_t* words = reinterpret_cast<uint32_t*>(vrow);
+              for (int q = 0; q < kKvDim / 4; ++q) {
+                const uint32_t w = words[q], f = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of NaN bytes
+                words[q] = w & ~((f >> 7) * 0xFFu);
+              }
+            }
           }
         }
-        const bool grow = M > m_lane + kSlack || MV > mv_lane + kSlack || (m_lane == -INFINITY && M > -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {             // the same in all four warps
-          const float m_new = fmaxf(m_lane, M), mv_new = fmaxf(mv_lane, MV);
+        auto scores = [&](float (&z)[kNC]) {
+#pragma unroll
+          for (int c0 = 0; c0 < kNC; c0 += 16) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int c = 0; c < 16 && c0 + c < kNC; c += 8) {
+              tmem_ld_cols8(tmem + lanes + 64 * sb + c0 + c, hi + c);
+              tmem_ld_cols8(tmem + lanes + 64 * sb + kHalf + c0 + c, lo + c);
+            }
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16 && c0 + c < kNC; ++c) {
+              float x = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
+              if (kMods) {
+                if (in != 0.f) x = capped(x, in, a.cap_log2);
+                x = fmaf(-cm.slope[c0 + c], fabsf(cm.pos[c0 + c] - (float)j), x);
+              }
+              if (kMasked && (!exists || j >= cm.limit[c0 + c])) x = -INFINITY;
+              z[c0 + c] = x;
+            }
+          }
+        };
+        // the exact maxima over the tile, where the references do not hold: they, and what was formed against them, move
+        auto raise = [&]() {
+          float z[kNC], mine = -INFINITY;
+          scores(z);
+#pragma unroll
+          for (int c = 0; c < kNC; ++c) {
+            const float r = warp_max_f32(z[c]);
+            if (lane == c) mine = r;                   // lane c of every warp ends up with column c's
+          }
+          const float lv_max = warp_max_f32(fmaxf(__log2f(fabsf(vs)), -126.f));
+          if (lane < kCE) wmax[wg][quarter][lane] = mine;
+          if (lane == 0) wlv[wg][quarter] = lv_max;
+          named_bar_sync(bar, 128);
+          float m_new = m_lane, mv_new = mv_lane;
+          if (lane < kCE) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float x = wmax[wg][w][lane];
+              m_new = fmaxf(m_new, x);
+              mv_new = fmaxf(mv_new, x + wlv[wg][w]);
+            }
+          }
           const float al = m_lane == -INFINITY ? 0.f : ex2_approx(m_lane - m_new);
           const float ao = mv_lane == -INFINITY ? 0.f : ex2_approx(mv_lane - mv_new);
-          const float e_new = mv_new == -INFINITY ? kPOne : ex2_approx(m_new - mv_new) * kPOne;
           m_lane = m_new;
           mv_lane = mv_new;
-          const float m_use = m_new == -INFINITY ? 0.f : m_new;
-#pragma unroll
-          for (int c = 0; c < kCE; ++c) {
-            l[c] *= __shfl_sync(0xffffffffu, al, c);
-            m[c] = __shfl_sync(0xffffffffu, m_use, c);
-            e[c] = __shfl_sync(0xffffffffu, e_new, c);
+          if (quarter == 0 && lane < kCE) {
+            ref_m[lane] = m_new == -INFINITY ? 0.f : m_new;
+            ref_e[lane] = mv_new == -INFINITY ? kPOne : ex2_approx(m_new - mv_new) * kPOne;
           }
           if (!fresh) {
-            // the accumulator is settled once this warpgroup's previous product has completed
-            ok = mbar_wait_warp(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
-            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < kNC; ++c) l[c] *= __shfl_sync(0xffffffffu, al, c);
             tc_fence_after();
             const uint32_t o = acc + 64 * wg;
-#pragma unroll
-            for (int c0 = 0; c0 < kCE; c0 += 8) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < kNC; c0 += 8) {
               uint32_t r[16];
-              tmem_ld_cols<8>(o + c0, r);
-              tmem_ld_cols<8>(o + kHalf + c0, r + 8);
+              tmem_ld_cols8(o + c0, r);
+              tmem_ld_cols8(o + kHalf + c0, r + 8);
               tmem_wait_ld();
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
@@ -581,68 +591,86 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             }
             tmem_wait_st();
           }
-        }
-        if (any_nan) {
-          const uint32_t who = __ballot_sync(0xffffffffu, has_nan);
-          if (lane == 0) nan_keys[wg][quarter] = who;
           named_bar_sync(bar, 128);
-          const uint8_t* vt = sKV + st * kStageBytes + kTileBytes;
-          for (int w = 0; w < 4; ++w)
-            for (uint32_t left = nan_keys[wg][w]; left; left &= left - 1) {
-              const int k = 32 * w + __ffs(left) - 1;
-              const uint8_t code = vt[k * kKvDim + ((((uint32_t)row >> 4) ^ (k & 7)) << 4) + (row & 15)];
-              if ((code & 0x7Fu) == 0x7Fu)
-                for (int c = 0; c < kCE; ++c)
-                  if (key0 + k < cm.limit[c]) poison |= 1u << c;
-            }
-          named_bar_sync(bar, 128);
-          if (has_nan) {
-            uint32_t* vrow = reinterpret_cast<uint32_t*>(sKV + st * kStageBytes + kTileBytes + row * kKvDim);
-            for (int q = 0; q < kKvDim / 4; ++q) {
-              const uint32_t w = vrow[q], f = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of NaN bytes
-              vrow[q] = w & ~((f >> 7) * 0xFFu);
-            }
-          }
-        }
-        // the probabilities, and their contributions in two e4m3 terms
-        uint32_t hi[kHalf / 4], lo[kHalf / 4];
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 4) {
-          if (c >= kCE) {
-            hi[c / 4] = lo[c / 4] = 0;
-            continue;
-          }
-          float x[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float p = ex2_approx(z[c + q] - m[c + q]);
-            l[c + q] += p;
-            x[q] = p * (vs * e[c + q]);
-          }
-          uint32_t h0, l0, h1, l1;
-          split2(x[0], x[1], h0, l0);
-          split2(x[2], x[3], h1, l1);
-          hi[c / 4] = h0 | h1 << 16;
-          lo[c / 4] = l0 | l1 << 16;
-        }
-        fresh = false;
-        // the buffer is free once this warpgroup's previous product has completed
+        };
+        // the buffer is free, and the accumulator settled, once this warpgroup's previous product has completed
         if (i >= 2) {
           ok = mbar_wait_warp(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
-          if (!ok) break;
+          if (!ok) return;
         }
-        uint8_t* prow = sP + sb * kPBytes + row * kN;
+        uint8_t* prow = sP + wg * kPBytes + row * kN;
         const int sw = kN == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+        float z[kNC];                                  // scores, then probabilities
+        bool raised = fresh;
+        if (fresh) raise();
+        for (;;) {
+          scores(z);
+          // the probabilities, and their contributions in two e4m3 terms
+          uint32_t hi[kHalf / 4], lo[kHalf / 4];
+          float p_top = 0.f, x_top = 0.f;
 #pragma unroll
-        for (int q = 0; q < kHalf / 16; ++q) {
-          *reinterpret_cast<uint4*>(prow + ((q ^ sw) << 4)) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-          *reinterpret_cast<uint4*>(prow + (((q + kHalf / 16) ^ sw) << 4)) =
-              make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+          for (int c = 0; c < kHalf; c += 4) {
+            hi[c / 4] = lo[c / 4] = 0;
+            if (c >= kNC) continue;
+            const float4 m4 = *reinterpret_cast<const float4*>(ref_m + c), e4 = *reinterpret_cast<const float4*>(ref_e + c);
+            const float mm[4] = {m4.x, m4.y, m4.z, m4.w}, ee[4] = {e4.x, e4.y, e4.z, e4.w};
+            float x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              z[c + q] = ex2_approx(z[c + q] - mm[q]);
+              x[q] = z[c + q] * (vs * ee[q]);
+              p_top = fmaxf(p_top, z[c + q]);
+              x_top = fmaxf(x_top, x[q]);
+            }
+            uint32_t h0, l0, h1, l1;
+            split2(x[0], x[1], h0, l0);
+            split2(x[2], x[3], h1, l1);
+            hi[c / 4] = h0 | h1 << 16;
+            lo[c / 4] = l0 | l1 << 16;
+          }
+#pragma unroll
+          for (int q = 0; q < kHalf / 16; ++q) {
+            *reinterpret_cast<uint4*>(prow + ((q ^ sw) << 4)) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+            *reinterpret_cast<uint4*>(prow + (((q + kHalf / 16) ^ sw) << 4)) =
+                make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          if (!named_bar_or(bar, 128, !raised && (p_top > kSlackP || x_top > kSlackP * kPOne))) break;
+          raised = true;                               // the same in all four warps
+          raise();
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        named_bar_sync(bar, 128);
-        if (row == 0) mbar_arrive(&p_full[sb]);
+#pragma unroll
+        for (int c = 0; c < kNC; ++c) l[c] += z[c];
+        fresh = false;
+        if (row == 0) mbar_arrive(&p_full[wg]);
+        if (lane == 0) mbar_arrive(&s_empty[sb]);
+      };
+      for (int t = (i0 + wg) & 1; t < s.n && ok; t += 2) {
+        const int i = i0 + t, key0 = (s.tile + t) * kTok;
+        ok = mbar_wait_warp(&kv_full[i % kStages], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
+             mbar_wait_warp(&s_full[i % kSBufs], (i / kSBufs) & 1, err, kErrMmaTimeout, kPolls);
+        if (!ok) break;
+        tc_fence_after();
+        using std::integral_constant;
+        // a cap or a bias take the masks along: their calls are not bound here
+        const bool masked = kMods || __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[i % kStages] != 0);
+        if constexpr (kCE > 16) {
+          if (live > 16) {
+            if (masked) tile(integral_constant<int, 32>{}, std::true_type{}, i, key0);
+            else if constexpr (!kMods) tile(integral_constant<int, 32>{}, std::false_type{}, i, key0);
+            continue;
+          }
+        }
+        if constexpr (kCE > 8) {
+          if (live > 8) {
+            if (masked) tile(integral_constant<int, 16>{}, std::true_type{}, i, key0);
+            else if constexpr (!kMods) tile(integral_constant<int, 16>{}, std::false_type{}, i, key0);
+            continue;
+          }
+        }
+        if (masked) tile(integral_constant<int, 8>{}, std::true_type{}, i, key0);
+        else if constexpr (!kMods) tile(integral_constant<int, 8>{}, std::false_type{}, i, key0);
       }
       if (!ok) break;
       i0 += s.n;
@@ -652,13 +680,13 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         float v = l[c];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) red[wg][quarter][c] = v;
+        if (lane == 0) wmax[wg][quarter][c] = v;
       }
       named_bar_sync(bar, 128);
       if (quarter == 0 && lane < kCE) {
         stat[qb][wg][0][lane] = m_lane;
         stat[qb][wg][1][lane] = mv_lane;
-        stat[qb][wg][2][lane] = (red[wg][0][lane] + red[wg][1][lane]) + (red[wg][2][lane] + red[wg][3][lane]);
+        stat[qb][wg][2][lane] = (wmax[wg][0][lane] + wmax[wg][1][lane]) + (wmax[wg][2][lane] + wmax[wg][3][lane]);
       }
       stat_nan[qb][wg][row] = poison;
       __syncwarp();
@@ -708,10 +736,10 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
 #pragma unroll 1
       for (int c0 = 0; c0 < kCE; c0 += 8) {
         uint32_t r[32];
-        tmem_ld_cols<8>(acc + c0, r);
-        tmem_ld_cols<8>(acc + kHalf + c0, r + 8);
-        tmem_ld_cols<8>(acc + 64 + c0, r + 16);
-        tmem_ld_cols<8>(acc + 64 + kHalf + c0, r + 24);
+        tmem_ld_cols8(acc + c0, r);
+        tmem_ld_cols8(acc + kHalf + c0, r + 8);
+        tmem_ld_cols8(acc + 64 + c0, r + 16);
+        tmem_ld_cols8(acc + 64 + kHalf + c0, r + 24);
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -862,7 +890,7 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
   e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, shared_keys);
   count_launches(1);
   if (e != cudaSuccess) return e;
-  if (ctas > 1) {
+  if (ctas > 1 && !a.whole) {
     e = launch_pdl(paged_attention_join_kernel, dim3(ctas - 1, kCE / 8), dim3(256), 0, s, a, kCE, ctas);
     count_launches(1);
   }
@@ -870,13 +898,16 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
 }
 }  // namespace
 
-cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, void* workspace,
+cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_seq_len, void* workspace,
                                    const PagedAttnPlan& plan, cudaStream_t s) {
   char* ws = static_cast<char*>(workspace);
   const int ctas = device_sm_count();
   a.err = reinterpret_cast<uint32_t*>(ws);
   a.rec = reinterpret_cast<int32_t*>(ws + plan.rec_offset);
   a.part_o = reinterpret_cast<float*>(ws + plan.part_offset);
+  // Requests of at most 1,024 keys are not cut: a CTA takes such a segment in less time than a second launch to join
+  // its pieces would (one request of 300 keys: XXX instead of YYY us).
+  a.whole = max_seq_len <= 8 * kPaTok;
   a.lo_pairs = 0;
   a.hi_pairs = plan.prompt ? kPagedAttnDirect : INT32_MAX;
   a.part_ml = a.part_o + (size_t)2 * ctas * kPagedAttnColumns * kKvDim;

@@ -254,15 +254,13 @@ __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a
       uint32_t* x = r + 16 * gg;
       const float kc = ks[g + gg] * w.cf;
       const int left = ((bad >> (g + gg)) & 1u) ? 0 : w.limit - key0 - 16 * (g + gg);   // keys of the group that are seen
+      const float away = kMods ? (float)(w.pos - key0 - 16 * (g + gg)) : 0.f;           // of the row from the first of them
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         float z = __uint_as_float(x[c]) * kc;
         if (kMods) {
-          if (in != 0.f) {
-            const float y = z * in;
-            z = a.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(y > 64.f ? 64.f : y)));   // NaN stays
-          }
-          z -= w.slope * (float)abs(w.pos - (key0 + 16 * (g + gg) + c));
+          if (in != 0.f) z = capped(z, in, a.cap_log2);
+          z = fmaf(-w.slope, fabsf(away - (float)c), z);
         }
         // a masked score is -inf whatever the factor (which may be 0)
         x[c] = c < left ? __float_as_uint(z) : 0xFF800000u;
@@ -924,7 +922,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       for (int seg = 0;; ++seg) {
         if (seg >= kSegBufs && !mbar_wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
         PpSeg s = {};
-        if (u < u1) s = pp_segment(a, cur, u, u0, u1, cta);
+        // segments are cut where the range ends, or (short requests) belong to the range they begin in as a whole
+        if (u < u1) s = pp_segment(a, cur, u, u0, a.whole ? units : u1, cta);
+        if (a.whole && s.n && s.tile > 0) {
+          u += s.n;
+          s.n = 0;
+          if (u < u1) s = pp_segment(a, cur, u, u0, units, cta);
+        }
         if (lane == 0) {
           segs[seg % kSegBufs] = s;
           mbar_arrive(&seg_full[seg % kSegBufs]);
@@ -1020,7 +1024,7 @@ cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map
                  dim3(pp::kThreads), pp::kFixedSmem, s, k_map, v_codes, a);
   count_launches(1);
   if (e != cudaSuccess) return e;
-  if (ctas > 1) {
+  if (ctas > 1 && !a.whole) {
     e = launch_pdl(paged_prompt_join_kernel, dim3(ctas - 1, kKvDim / 16), dim3(kPromptPairs), 0, s, a, ctas);
     count_launches(1);
   }

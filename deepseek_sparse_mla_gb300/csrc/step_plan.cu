@@ -168,21 +168,32 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
     const int held = (int)(((int64_t)old_len[b] + P - 1) >> a.log2_page);
     a.block_table[(int64_t)b * a.table_stride + held + ((int)k - first)] = a.free_pages[count - 1 - k];
   }
-  for (int64_t r = rank * kPlanThreads + tid; r < a.num_rows; r += stride) {
-    int64_t slot = -1;
-    int pos = -1;
-    if (r < R) {
-      const int b = request_of(row_end, B, (int)r);
-      const int first = b ? row_end[b - 1] : 0, page_first_b = b ? page_end[b - 1] : 0;
-      pos = old_len[b] + ((int)r - first);
-      const int held = (int)(((int64_t)old_len[b] + P - 1) >> a.log2_page), lp = pos >> a.log2_page;
-      // a page that this call hands out is read from the stack: another thread writes its table entry
-      const int page = lp < held ? a.block_table[(int64_t)b * a.table_stride + lp]
-                                 : a.free_pages[count - 1 - (page_first_b + (lp - held))];
-      slot = page < 0 ? -1 : ((int64_t)page << a.log2_page) + (pos & (P - 1));
+  // four rows at a time: their page ids are in flight together
+  for (int64_t r0 = rank * kPlanThreads + tid; r0 < a.num_rows; r0 += 4 * stride) {
+    int page[4], pos[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t r = r0 + k * stride;
+      page[k] = -1;
+      pos[k] = -1;
+      if (r < R) {
+        const int b = request_of(row_end, B, (int)r);
+        const int first = b ? row_end[b - 1] : 0, page_first_b = b ? page_end[b - 1] : 0;
+        pos[k] = old_len[b] + ((int)r - first);
+        const int held = (int)(((int64_t)old_len[b] + P - 1) >> a.log2_page), lp = pos[k] >> a.log2_page;
+        // a page that this call hands out is read from the stack: another thread writes its table entry
+        page[k] = lp < held ? a.block_table[(int64_t)b * a.table_stride + lp]
+                            : a.free_pages[count - 1 - (page_first_b + (lp - held))];
+      }
     }
-    a.slot_mapping[r] = slot;
-    if (a.positions) a.positions[r] = pos;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t r = r0 + k * stride;
+      if (r < a.num_rows) {
+        a.slot_mapping[r] = page[k] < 0 ? -1 : ((int64_t)page[k] << a.log2_page) + (pos[k] & (P - 1));
+        if (a.positions) a.positions[r] = pos[k];
+      }
+    }
   }
 }
 
