@@ -11,15 +11,15 @@
 //
 // What bounds it: a prompt, the bytes (4 read and 2 written per cached value pair); a decode step, latency.
 // One CTA owns one page of one head of K or of V, so nothing is shared and no atomics are needed: it
-// holds the page's new values in registers between the maximum and the coding, and reads them once.
+// holds the page's new values in registers between the maximum and the coding, and reads them once.  At
+// most four 32-byte pieces a thread keep several CTAs on an SM (with eight a prompt took XXX us instead of YYY), and
+// the values are asked for before the page's id and old scale, on which they do not depend.
 #include "dsa_internal.cuh"
 
 namespace dsa {
 
 namespace {
-constexpr int kAppendThreads = 128;
 constexpr int kRowParts = kKvDim / 16;                                    // 16 values a thread
-constexpr int kItems = kKvMaxPage * kRowParts / kAppendThreads;           // of a full page of 128 tokens
 
 // 16 values of one token's head times `inv` (a power of two), as e4m3 codes
 __device__ __forceinline__ uint4 code16(const uint4 (&v)[2], float inv) {
@@ -41,8 +41,10 @@ __device__ __forceinline__ uint4 code16(const uint4 (&v)[2], float inv) {
   return out;
 }
 
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8AppendArgs a) {
-  __shared__ uint32_t warp_max[kAppendThreads / 32];
+// kItems: pieces of a full page a thread
+template <int kThreads, int kItems>
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArgs a) {
+  __shared__ uint32_t warp_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
@@ -82,41 +84,45 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
   const int first = max((int)(start - page_pos), 0);                      // new tokens: offsets first .. last - 1
   const int last = (int)min((int64_t)P, (int64_t)start + n - page_pos);
   if (first >= last || lp >= a.table_stride) return;
+  const uint4* src = reinterpret_cast<const uint4*>(is_v ? a.v : a.k);
+  const int64_t src_stride = (is_v ? a.v_stride : a.k_stride) / 8;        // in 16-byte chunks
+  const int64_t row = row0 + (page_pos + first - start);                  // row of offset `first`
+  uint4 v[kItems][2];
+  const int items = (last - first) * kRowParts;
+#pragma unroll
+  for (int it = 0; it < kItems; ++it) {
+    const int i = tid + it * kThreads;
+    v[it][0] = v[it][1] = make_uint4(0, 0, 0, 0);
+    if (i < items) {
+      const uint4* p = src + (row + i / kRowParts) * src_stride + h * (kKvDim / 8) + 2 * (i % kRowParts);
+      v[it][0] = p[0];
+      v[it][1] = p[1];
+    }
+  }
   const int page = a.block_table[(int64_t)b * a.table_stride + lp];
   if (page < 0 || page >= a.num_pages) return;
   const int64_t block = (int64_t)page * a.kv_heads + h;
   uint4* codes = reinterpret_cast<uint4*>((is_v ? a.v_codes : a.k_codes) + ((block << a.log2_page) * kKvDim));
   float* scale_at = (is_v ? a.v_scales : a.k_scales) + block;
-  const uint4* src = reinterpret_cast<const uint4*>(is_v ? a.v : a.k);
-  const int64_t src_stride = (is_v ? a.v_stride : a.k_stride) / 8;        // in 16-byte chunks
-  const int64_t row = row0 + (page_pos + first - start);                  // row of offset `first`
   const float old_scale = first > 0 ? *scale_at : 0.f;
 
-  uint4 v[kItems][2];
   uint32_t top = 0;                                                       // largest finite |x|, as bf16 bits
-  const int items = (last - first) * kRowParts;
 #pragma unroll
-  for (int it = 0; it < kItems; ++it) {
-    const int i = tid + it * kAppendThreads;
-    if (i < items) {
-      const uint4* p = src + (row + i / kRowParts) * src_stride + h * (kKvDim / 8) + 2 * (i % kRowParts);
-      v[it][0] = p[0];
-      v[it][1] = p[1];
+  for (int it = 0; it < kItems; ++it)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t w = reinterpret_cast<const uint32_t*>(&v[it][q])[e];
-          const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
-          if (lo < 0x7F80u) top = max(top, lo);
-          if (hi < 0x7F80u) top = max(top, hi);
-        }
-    }
-  }
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&v[it][q])[e];
+        const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+        if (lo < 0x7F80u) top = max(top, lo);
+        if (hi < 0x7F80u) top = max(top, hi);
+      }
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) warp_max[tid >> 5] = top;
   __syncthreads();                                                        // the old scale has been read, too
-  top = max(max(warp_max[0], warp_max[1]), max(warp_max[2], warp_max[3]));
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) top = max(top, warp_max[w]);
   // 448 = 1.75 * 2^8: amax = m * 2^E with m in [1, 2) wants 2^(E - 8), or 2^(E - 7) for m > 1.75
   const uint32_t f = top << 16;
   int e = (int)(f >> 23) - 127 - 8 + ((f & 0x7FFFFFu) > 0x600000u ? 1 : 0);
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
   const float inv = pow2 ? __fdiv_rn(1.0f, scale) : 1.0f;
 #pragma unroll
   for (int it = 0; it < kItems; ++it) {
-    const int i = tid + it * kAppendThreads;
+    const int i = tid + it * kThreads;
     if (i < items) {
       uint4 c;
       if (pow2) {
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
   }
   if (grown) {
     const float ratio = __fdiv_rn(old_scale, scale);
-    for (int i = tid; i < first * kRowParts; i += kAppendThreads) {
+    for (int i = tid; i < first * kRowParts; i += kThreads) {
       uint4 c = codes[i];
       uint32_t* w = reinterpret_cast<uint32_t*>(&c);
 #pragma unroll
@@ -175,7 +181,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
 
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s) {
   const int64_t units = (a.query_start_loc ? (a.num_rows >> a.log2_page) : 0) + (int64_t)2 * a.num_requests;
-  cudaError_t e = launch_pdl(kv8_append_kernel, dim3((unsigned)units, a.kv_heads, 2), dim3(kAppendThreads), 0, s, a);
+  const dim3 grid((unsigned)units, a.kv_heads, 2);
+  const cudaError_t e = a.log2_page == 4   ? launch_pdl(kv8_append_kernel<128, 1>, grid, dim3(128), 0, s, a)
+                        : a.log2_page == 5 ? launch_pdl(kv8_append_kernel<256, 1>, grid, dim3(256), 0, s, a)
+                        : a.log2_page == 6 ? launch_pdl(kv8_append_kernel<256, 2>, grid, dim3(256), 0, s, a)
+                                           : launch_pdl(kv8_append_kernel<256, 4>, grid, dim3(256), 0, s, a);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

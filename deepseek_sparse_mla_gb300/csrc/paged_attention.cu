@@ -190,10 +190,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (kCE < kHalf)                                     // columns that no query fills stay zero
-    for (int i = tid; i < kQBufs * kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
-  if (tid == 0) a.rec[8 * cta] = -1;                   // no piece to join until it has been written
+  if (tid == 0) reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;   // no piece to join until it has been written
   // running sums of the requests' units: every thread a run of consecutive requests
   {
     uint32_t bits = 0;
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
               page = -1;
             }
           }
-          if (page >= 0) {
+          if (page >= 0) {                             // (not waited for until the tile's loads are out)
             ks = a.k_scales[(int64_t)page * a.kv_heads + s.h];
             vs = a.v_scales[(int64_t)page * a.kv_heads + s.h];
           }
@@ -275,10 +273,14 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         // this tile's pages sit in lanes o .. o + ppt - 1; lanes 0 .. ppt - 1 load K, 16 .. 16 + ppt - 1 V
         const int o = p0 & 31, mine = lane & 15;
         const int pg = __shfl_sync(0xffffffffu, page, (o + mine) & 31);
-        const float k1 = __shfl_sync(0xffffffffu, ks, (o + mine) & 31), v1 = __shfl_sync(0xffffffffu, vs, (o + mine) & 31);
         const bool load = mine < ppt && pg >= 0;
         const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
         const uint32_t bad = __ballot_sync(0xffffffffu, mine < ppt && pg < 0) & 0xFFFFu;
+        if (load)
+          tma_load_2d_hint(sKV + st * kStageBytes + (lane >> 4) * kTileBytes + mine * page_bytes,
+                           lane < 16 ? &k_map : &v_map, 0, (pg * a.kv_heads + s.h) << lp, &kv_full[st], policy);
+        // the tile's arrival also stands for its scales
+        const float k1 = __shfl_sync(0xffffffffu, ks, (o + mine) & 31), v1 = __shfl_sync(0xffffffffu, vs, (o + mine) & 31);
         if (lane < ppt) {
           sks[st][lane] = k1;
           svs[st][lane] = v1;
@@ -286,10 +288,6 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         if (lane == 0) sbad[st] = bad;
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], loads * page_bytes);
-        __syncwarp();
-        if (load)
-          tma_load_2d_hint(sKV + st * kStageBytes + (lane >> 4) * kTileBytes + mine * page_bytes,
-                           lane < 16 ? &k_map : &v_map, 0, (pg * a.kv_heads + s.h) << lp, &kv_full[st], policy);
       }
       u += s.n;
     }
@@ -381,30 +379,25 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const int pairs = s.rows * a.group, prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
       const int start = a.seq_lens[s.b] - s.rows;     // position of row 0
       int low = INT32_MAX;
-      // eight columns at a time: their loads are in flight together
+      // Two columns a step, a half-warp each, with the next two on their way: a rolled loop, as code that a CTA
+      // runs once or twice costs its way from L2.  Columns without a pair are left as they are: nothing reads them.
+      const int live = min(pairs - s.cg * kCE, kCE);
+      auto load = [&](int c) {
+        const int n = s.cg * kCE + c;
+        if (c >= live) return make_uint4(0, 0, 0, 0);
+        const int i = n / a.group, g = n - i * a.group;
+        return *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (s.h * a.group + g) * kKvDim + 8 * part);
+      };
+      uint4 x = load(lane >> 4), next = load(2 + (lane >> 4));
 #pragma unroll 1
-      for (int c0 = 0; c0 < kCE; c0 += 8) {
-      uint4 x[4];
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int n = s.cg * kCE + c0 + 2 * it + (lane >> 4);
-        x[it] = make_uint4(0, 0, 0, 0);
-        if (n < pairs) {
-          const int i = n / a.group, g = n - i * a.group;
-          x[it] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (s.h * a.group + g) * kKvDim + 8 * part);
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int c = c0 + 2 * it + (lane >> 4), n = s.cg * kCE + c;
-        const uint32_t w[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
-        uint32_t top = 0;                             // largest finite |x|, as bf16 bits
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t p = w[e] & 0x7FFFu, r = (w[e] >> 16) & 0x7FFFu;
-          if (p < 0x7F80u) top = max(top, p);
-          if (r < 0x7F80u) top = max(top, r);
-        }
+      for (int c0 = 0; c0 < live; c0 += 2) {
+        const int c = c0 + (lane >> 4), n = s.cg * kCE + c;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        x = next;
+        next = load(c + 4);
+        // the largest |x| as bf16 bits; a row with an infinity or NaN is NaN whatever its scale
+        uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+        top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
@@ -419,20 +412,19 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
           split2(xl, xh, hi[e], lo[e]);
         }
+        if (c >= live) continue;
         const uint32_t at = (((part >> 1) ^ (c & 7)) << 4) + 8 * (part & 1);
         *reinterpret_cast<uint2*>(q_hi + c * kKvDim + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
         *reinterpret_cast<uint2*>(q_hi + (kHalf + c) * kKvDim + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         const int i = n / a.group;
         const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
-        if (n < pairs) low = min(low, limit);
+        low = min(low, limit);
         if (part == 0) {
-          // 2^(E - 7) is exact; a column past the last pair sees everything and is not written
-          cm.factor[c] = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;
-          cm.limit[c] = n < pairs ? limit : INT32_MAX;
+          cm.factor[c] = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
+          cm.limit[c] = limit;
           cm.pos[c] = (float)pos;
-          cm.slope[c] = kMods && a.slopes && n < pairs ? a.slopes[s.h * a.group + (n - i * a.group)] * 1.4426950408889634f : 0.f;
+          cm.slope[c] = kMods && a.slopes ? a.slopes[s.h * a.group + (n - i * a.group)] * 1.4426950408889634f : 0.f;
         }
-      }
       }
       low = __reduce_min_sync(0xffffffffu, low);
       if (lane == 0) cm.min_limit = low;
@@ -722,13 +714,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           ml[1] = L;
         }
       }
-      if (row == 0 && u - s.n == u0) {                   // for the join: this CTA's first piece
-        int32_t* rec = a.rec + 8 * cta;
-        rec[0] = s.b;
-        rec[1] = s.h;
-        rec[2] = s.cg;
-        rec[3] = s.tile;
-      }
+      if (row == 0 && u - s.n == u0)                     // for the join: this CTA's first piece
+        reinterpret_cast<PaRecord*>(a.rec)[cta] = {units, s.tile, s.tiles, s.row0, pairs, s.cg * kCE, s.h};
       poison = stat_nan[qb][0][row] | stat_nan[qb][1][row];
       named_bar_sync(bar, 128);
       if (!mbar_wait_warp(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
@@ -779,7 +766,6 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     if (cta == 0) {
       a.err[0] = 0;
       a.err[1] = (uint32_t)ctas;
-      *reinterpret_cast<int64_t*>(a.err + 2) = units;
     }
   }
 }
@@ -788,27 +774,16 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
 //   out = sum_p w_p O_p,  w_p = 2^{m_p - M} / L,  L = sum_p 2^{m_p - M} l_p.
 // CTA (c - 1, g) handles the boundary in front of range c if it is the first that cuts its segment, and
 // columns 8 g .. 8 g + 7: a warp a column, four dims a lane.
-__global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ PagedAttnArgs a, int columns,
-                                                                   int ctas) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x + 1;
   pdl_wait();
   pdl_trigger();
-  const int64_t units = *reinterpret_cast<const int64_t*>(a.err + 2);
-  const int c = blockIdx.x + 1;
-  const int64_t u = pa_unit_start(c, units, ctas);
-  if (u == pa_unit_start(c + 1, units, ctas)) return;    // a range without units
-  const int4 rec = __ldcg(reinterpret_cast<const int4*>(a.rec + 8 * c));
-  const int b = rec.x, h = rec.y, cg = rec.z, tile = rec.w;
-  if (b < 0 || tile == 0) return;                         // nothing was written, or the range begins with a segment
-  const int64_t seg = u - tile;
-  const int first = pa_cta_of_unit(u - 1, units, ctas);
-  if (pa_unit_start(first, units, ctas) > seg) return;    // an earlier boundary cuts it, too
-  uint32_t none = 0;
-  const PaShape s = pa_shape(a, b, none);
-  const int col = 8 * blockIdx.y + warp, n = cg * columns + col;
-  if (n >= s.rows * a.group) return;
-  const int last = pa_cta_of_unit(seg + s.tiles - 1, units, ctas);
-  const int first_slot = pa_unit_start(first, units, ctas) == seg ? 2 * first : 2 * first + 1;
+  const PaRecord rec = pa_load_record(a, c);
+  int first, last, first_slot;
+  if (!pa_pieces(rec, c, ctas, first, last, first_slot)) return;
+  const int col = 8 * blockIdx.y + warp, n = rec.first_pair + col;
+  if (n >= rec.pairs) return;
+  const int64_t units = rec.units;
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kGroup = 4;                               // pieces whose loads are in flight together
@@ -851,7 +826,7 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int i = n / a.group;
-  const int64_t at = (int64_t)(s.row0 + i) * a.kv_heads * a.group + h * a.group + (n - i * a.group);
+  const int64_t at = (int64_t)(rec.row0 + i) * a.kv_heads * a.group + rec.h * a.group + (n - i * a.group);
   const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), v1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   reinterpret_cast<uint2*>(a.out + at * kKvDim)[lane] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
@@ -891,7 +866,7 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (ctas > 1 && !a.whole) {
-    e = launch_pdl(paged_attention_join_kernel, dim3(ctas - 1, kCE / 8), dim3(256), 0, s, a, kCE, ctas);
+    e = launch_pdl(paged_attention_join_kernel, dim3(ctas - 1, kCE / 8), dim3(256), 0, s, a, ctas);
     count_launches(1);
   }
   return e;

@@ -55,14 +55,55 @@ __device__ __forceinline__ float capped(float z, float in, float cap) {
   return fmaf(-2.f * cap, r, cap);
 }
 
-// Units [start(c), start(c + 1)) belong to CTA c.
-__device__ __forceinline__ int64_t pa_unit_start(int c, int64_t units, int ctas) { return units * c / ctas; }
+// Units [start(c), start(c + 1)) belong to CTA c: units * c / ctas.
+__device__ __forceinline__ int64_t pa_unit_start(int c, int64_t units, int ctas) {
+  if (units < (int64_t(1) << 31)) {                     // 32-bit divisions: (q ctas + r) c / ctas = q c + r c / ctas
+    const uint32_t n = (uint32_t)units, q = n / (uint32_t)ctas, r = n - q * (uint32_t)ctas;
+    return (int64_t)q * c + r * (uint32_t)c / (uint32_t)ctas;
+  }
+  return units * c / ctas;
+}
 
 __device__ __forceinline__ int pa_cta_of_unit(int64_t u, int64_t units, int ctas) {
-  int c = (int)(u * ctas / units);
+  int c = units < (int64_t(1) << 31) / ctas ? (int)((uint32_t)u * (uint32_t)ctas / (uint32_t)units) : (int)(u * ctas / units);
   while (c + 1 < ctas && pa_unit_start(c + 1, units, ctas) <= u) ++c;
   while (c > 0 && pa_unit_start(c, units, ctas) > u) --c;
   return c;
+}
+
+// What a CTA leaves about the first segment of its range, for the join: all that it needs besides the pieces.
+struct __align__(16) PaRecord {
+  int64_t units;
+  int32_t tile, tiles;             // the segment's tiles, and which of them the range begins with (-1: nothing written)
+  int32_t row0, pairs;             // the request's first row, and its (row, head) pairs
+  int32_t first_pair, h;           // the segment's first pair, and its K/V head
+};
+static_assert(sizeof(PaRecord) == 32, "two 16-byte loads");
+
+__device__ __forceinline__ PaRecord pa_load_record(const PagedAttnArgs& a, int c) {
+  union {
+    int4 w[2];
+    PaRecord r;
+  } x;
+  const int4* p = reinterpret_cast<const int4*>(a.rec) + 2 * c;
+  x.w[0] = __ldcg(p);
+  x.w[1] = __ldcg(p + 1);
+  return x.r;
+}
+
+// The pieces of the segment that the boundary in front of range c cuts: CTAs first .. last, the first one's in
+// first_slot (the others' in slot 2 * CTA).  False where there is none, or an earlier boundary cuts it too.
+__device__ __forceinline__ bool pa_pieces(const PaRecord& r, int c, int ctas, int& first, int& last, int& first_slot) {
+  if (r.tile <= 0) return false;                          // nothing written, or the range begins with a segment
+  const int64_t u = pa_unit_start(c, r.units, ctas);
+  if (u == pa_unit_start(c + 1, r.units, ctas)) return false;
+  const int64_t seg = u - r.tile;
+  first = pa_cta_of_unit(u - 1, r.units, ctas);
+  const int64_t at = pa_unit_start(first, r.units, ctas);
+  if (at > seg) return false;
+  last = pa_cta_of_unit(seg + r.tiles - 1, r.units, ctas);
+  first_slot = at == seg ? 2 * first : 2 * first + 1;
+  return true;
 }
 
 }  // namespace dsa

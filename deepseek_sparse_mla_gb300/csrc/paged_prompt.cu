@@ -318,34 +318,31 @@ __device__ __forceinline__ void pp_shrink(uint32_t tO, float al) {
 
 // This thread's query row in two e4m3 terms; returns the factor of its scores.
 __device__ __forceinline__ float pp_query(const PagedAttnArgs& a, const __nv_bfloat16* src, bool there, uint8_t* q_hi, int row) {
-  uint4 x[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = there ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
-  uint32_t top = 0;                                    // largest finite |x|, as bf16 bits
+  // the row is read twice (the second time out of L1), as holding it would unroll the split 128 times, code that is
+  // run once a segment
+  const uint4* row16 = reinterpret_cast<const uint4*>(src);
+  uint32_t top2 = 0;                                   // largest |x| of each half word, as bf16 bits
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t p = w[e] & 0x7FFFu, y = (w[e] >> 16) & 0x7FFFu;
-      if (p < 0x7F80u) top = max(top, p);
-      if (y < 0x7F80u) top = max(top, y);
-    }
+    const uint4 w = row16[i];
+    top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
   }
-  // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
+  const uint32_t top = there ? max(top2 & 0xFFFFu, top2 >> 16) : 0u;
+  // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0); a row with an
+  // infinity or NaN is NaN whatever its scale
   const int E = max((int)(top >> 7) - 127, -100);
-  const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
-#pragma unroll
+  const float up = there ? __uint_as_float((uint32_t)(7 - E + 127) << 23) : 0.f;
+#pragma unroll 1
   for (int i = 0; i < 8; ++i) {                        // 16 values: one 16-byte unit of each term
+    const uint4 y[2] = {row16[2 * i], row16[2 * i + 1]};
+    const uint32_t* w8 = reinterpret_cast<const uint32_t*>(y);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t h2[2], l2[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = 2 * k + e;
-        const uint4 y = x[2 * i + (j >> 2)];
-        const uint32_t w = (j & 3) == 0 ? y.x : (j & 3) == 1 ? y.y : (j & 3) == 2 ? y.z : y.w;
+        const uint32_t w = w8[2 * k + e];
         // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
         const uint32_t wl = w << 16, wh = w & 0xFFFF0000u;
         const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
@@ -423,7 +420,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  if (tid == 0) a.rec[8 * cta] = -1;                   // no piece to join until it has been written
+  if (tid == 0) reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;   // no piece to join until it has been written
   const int B = a.num_requests;
   // block-wide inclusive sum of one value a thread
   auto block_sum = [&](int v) {
@@ -656,14 +653,8 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           a.lse[at] = any ? (m - kPLog2 + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
         }
       }
-      if (tid == 0 && seg == 0) {                      // for the join: this CTA's first piece
-        int32_t* rec = a.rec + 8 * cta;
-        rec[0] = s.b;
-        rec[1] = s.h;
-        rec[2] = s.qt;
-        rec[3] = s.tile;
-        rec[4] = s.tiles;
-      }
+      if (tid == 0 && seg == 0)                        // for the join: this CTA's first piece
+        reinterpret_cast<PaRecord*>(a.rec)[cta] = {units, s.tile, s.tiles, s.row0, s.rows * a.group, s.qt * kPromptPairs, s.h};
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -947,7 +938,6 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   }
   if (tid == 0) {
     a.err[kStatusCtaWords + cta] |= bits_all;          // beside what the first kernel reported
-    if (cta == 0) *reinterpret_cast<int64_t*>(a.err + 4) = units;
   }
 }
 
@@ -956,22 +946,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
 __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
   pdl_wait();
   pdl_trigger();
-  const int64_t units = *reinterpret_cast<const int64_t*>(a.err + 4);
   const int c = blockIdx.x + 1;
-  const int64_t u = pa_unit_start(c, units, ctas);
-  if (u == pa_unit_start(c + 1, units, ctas)) return;     // a range without units
-  const int32_t* rec = a.rec + 8 * c;
-  const int b = __ldcg(rec), h = __ldcg(rec + 1), qt = __ldcg(rec + 2), tile = __ldcg(rec + 3), tiles = __ldcg(rec + 4);
-  if (b < 0 || tile == 0) return;                          // nothing was written, or the range begins with a segment
-  const int64_t seg = u - tile;
-  const int first = pa_cta_of_unit(u - 1, units, ctas);
-  if (pa_unit_start(first, units, ctas) > seg) return;     // an earlier boundary cuts it, too
-  uint32_t none = 0;
-  const PaShape s = pa_shape(a, b, none);
-  const int n = qt * kPromptPairs + threadIdx.x;
-  if (n >= s.rows * a.group) return;
-  const int last = pa_cta_of_unit(seg + tiles - 1, units, ctas);
-  const int first_slot = pa_unit_start(first, units, ctas) == seg ? 2 * first : 2 * first + 1;
+  const PaRecord rec = pa_load_record(a, c);
+  int first, last, first_slot;
+  if (!pa_pieces(rec, c, ctas, first, last, first_slot)) return;
+  const int n = rec.first_pair + threadIdx.x;
+  if (n >= rec.pairs) return;
+  const int64_t units = rec.units;
   float M = -INFINITY, L = 0.f;
   float acc[16];
 #pragma unroll
@@ -980,11 +961,11 @@ __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const _
     if (pa_unit_start(p, units, ctas) == pa_unit_start(p + 1, units, ctas)) continue;
     const int64_t slot = p == first ? first_slot : 2 * p;
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * kPromptPairs + threadIdx.x);
-    if (ml.y == 0.f) continue;                             // a piece that sees nothing (NaN counts as seen)
     float4 x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (kKvDim / 4) + 4 * blockIdx.y + k) * kPromptPairs + threadIdx.x);
+    if (ml.y == 0.f) continue;                             // a piece that sees nothing (NaN counts as seen)
     const float Mn = fmaxf(M, ml.x);
     const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml.x - Mn);
     L = L * sc + w * ml.y;
@@ -999,7 +980,7 @@ __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const _
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int i = n / a.group;
-  const int64_t at = (int64_t)(s.row0 + i) * a.kv_heads * a.group + h * a.group + (n - i * a.group);
+  const int64_t at = (int64_t)(rec.row0 + i) * a.kv_heads * a.group + rec.h * a.group + (n - i * a.group);
   uint4 v[2];
   __nv_bfloat162* xo = reinterpret_cast<__nv_bfloat162*>(v);
 #pragma unroll

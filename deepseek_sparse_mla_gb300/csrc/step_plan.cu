@@ -71,6 +71,23 @@ __device__ __forceinline__ int request_of(const int32_t* ends, int n, int r) {
   return lo;
 }
 
+// The same from a b whose predecessors are known to end at or before r: neighbouring rows are mostly few requests on,
+// so the range is doubled until it holds the answer.
+__device__ __forceinline__ int request_from(const int32_t* ends, int n, int b, int r) {
+  int lo = b, step = 1;
+  while (lo + step - 1 < n - 1 && ends[lo + step - 1] <= r) {
+    lo += step;
+    step *= 2;
+  }
+  int hi = min(lo + step - 1, n - 1);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > r) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanArgs a) {
   extern __shared__ int32_t plan_smem[];
   const int B = a.num_requests;
@@ -168,28 +185,35 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
     const int held = (int)(((int64_t)old_len[b] + P - 1) >> a.log2_page);
     a.block_table[(int64_t)b * a.table_stride + held + ((int)k - first)] = a.free_pages[count - 1 - k];
   }
-  // four rows at a time: their page ids are in flight together
-  for (int64_t r0 = rank * kPlanThreads + tid; r0 < a.num_rows; r0 += 4 * stride) {
+  // Each warp takes a run of consecutive rows, 128 at a time (four a lane, their page ids in flight together): one
+  // search finds the request of the first, and the others' are looked for from there on.
+  const int warps = ctas * (kPlanThreads / 32), lane = tid & 31;
+  const int64_t run = ((a.num_rows + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t run0 = run * (rank * (kPlanThreads / 32) + (tid >> 5)), run1 = min((int64_t)a.num_rows, run0 + run);
+  int near = run0 < R ? request_of(row_end, B, (int)run0) : 0;
+  for (int64_t r0 = run0; r0 < run1; r0 += 128) {
     int page[4], pos[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int64_t r = r0 + k * stride;
+      const int64_t r = r0 + 32 * k + lane;
       page[k] = -1;
       pos[k] = -1;
-      if (r < R) {
-        const int b = request_of(row_end, B, (int)r);
+      if (r < R && r < run1) {
+        const int b = request_from(row_end, B, near, (int)r);
         const int first = b ? row_end[b - 1] : 0, page_first_b = b ? page_end[b - 1] : 0;
         pos[k] = old_len[b] + ((int)r - first);
         const int held = (int)(((int64_t)old_len[b] + P - 1) >> a.log2_page), lp = pos[k] >> a.log2_page;
         // a page that this call hands out is read from the stack: another thread writes its table entry
         page[k] = lp < held ? a.block_table[(int64_t)b * a.table_stride + lp]
                             : a.free_pages[count - 1 - (page_first_b + (lp - held))];
+        near = b;
       }
+      near = __shfl_sync(0xffffffffu, near, 0);          // the first lane's row is the lowest
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int64_t r = r0 + k * stride;
-      if (r < a.num_rows) {
+      const int64_t r = r0 + 32 * k + lane;
+      if (r < run1) {
         a.slot_mapping[r] = page[k] < 0 ? -1 : ((int64_t)page[k] << a.log2_page) + (pos[k] & (P - 1));
         if (a.positions) a.positions[r] = pos[k];
       }
