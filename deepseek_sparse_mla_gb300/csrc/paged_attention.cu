@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             for (int c = 0; c < 16 && c0 + c < kNC; ++c) {
               float x = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
               if (kMods) {
-                if (in != 0.f) x = capped(x, in, a.cap_log2);
+                if (in != 0.f) x = capped(x * in, a.cap_log2);
                 x = fmaf(-cm.slope[c0 + c], fabsf(cm.pos[c0 + c] - (float)j), x);
               }
               if (kMasked && (!exists || j >= cm.limit[c0 + c])) x = -INFINITY;
@@ -645,24 +645,23 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         using std::integral_constant;
-        // a cap or a bias take the masks along: their calls are not bound here
-        const bool masked = kMods || __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[i % kStages] != 0);
+        const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[i % kStages] != 0);
         if constexpr (kCE > 16) {
           if (live > 16) {
             if (masked) tile(integral_constant<int, 32>{}, std::true_type{}, i, key0);
-            else if constexpr (!kMods) tile(integral_constant<int, 32>{}, std::false_type{}, i, key0);
+            else tile(integral_constant<int, 32>{}, std::false_type{}, i, key0);
             continue;
           }
         }
         if constexpr (kCE > 8) {
           if (live > 8) {
             if (masked) tile(integral_constant<int, 16>{}, std::true_type{}, i, key0);
-            else if constexpr (!kMods) tile(integral_constant<int, 16>{}, std::false_type{}, i, key0);
+            else tile(integral_constant<int, 16>{}, std::false_type{}, i, key0);
             continue;
           }
         }
         if (masked) tile(integral_constant<int, 8>{}, std::true_type{}, i, key0);
-        else if constexpr (!kMods) tile(integral_constant<int, 8>{}, std::false_type{}, i, key0);
+        else tile(integral_constant<int, 8>{}, std::false_type{}, i, key0);
       }
       if (!ok) break;
       i0 += s.n;

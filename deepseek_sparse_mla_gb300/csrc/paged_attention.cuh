@@ -46,11 +46,11 @@ __device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, uint3
 cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, const uint8_t* v_codes, int ctas,
                                 cudaStream_t s);
 
-// A capped score: cap * tanh(z / cap) = cap * (1 - 2 / (1 + 2^(in z))), in = 2 log2(e) / cap, all in log2 units.  Exact
-// to about 2^-21 of the cap; past the range of 2^x the quotient is 0 or 2, and NaN stays.
-__device__ __forceinline__ float capped(float z, float in, float cap) {
+// A capped score: cap * tanh(z / cap) = cap * (1 - 2 / (1 + 2^y)), y = 2 log2(e) / cap * z, all in log2 units.  Exact
+// to about 2^-21 of the cap; past the range of 2^y the quotient is 0 or 2, and NaN stays.
+__device__ __forceinline__ float capped(float y, float cap) {
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * in));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return fmaf(-2.f * cap, r, cap);
 }

@@ -72,12 +72,11 @@ __device__ __forceinline__ int pp_entries(const PagedAttnArgs& a, const PaShape&
   return (int)(((int64_t)s.rows * a.group + kPromptPairs - 1) / kPromptPairs);
 }
 
-__device__ __forceinline__ PpEntry pp_entry(const PagedAttnArgs& a, int b, int qt) {
+__device__ __forceinline__ PpEntry pp_entry(const PagedAttnArgs& a, const PaShape& shape, int b, int qt) {
   PpEntry e;
-  uint32_t none = 0;
   e.b = b;
   e.qt = qt;
-  e.shape = pa_shape(a, b, none);
+  e.shape = shape;
   e.start = a.seq_lens[b] - e.shape.rows;
   e.prefix = a.prefix_lens ? min(a.prefix_lens[b], e.shape.len) : 0;
   const int last = min(e.shape.rows - 1, ((qt + 1) * kPromptPairs - 1) / a.group);
@@ -111,7 +110,7 @@ __device__ __forceinline__ PpSeg pp_segment(const PagedAttnArgs& a, PpCursor& c,
       c.qt = 0;
       continue;
     }
-    e = pp_entry(a, c.b, c.qt);
+    e = pp_entry(a, sh, c.b, c.qt);
     const int64_t units = (int64_t)e.tiles * a.kv_heads;
     if (u < c.before + units) break;
     c.before += units;
@@ -240,7 +239,7 @@ __device__ __forceinline__ float pp_half(const PpRow& w, uint32_t tS, const floa
 
 // 64 keys with masks, a cap or a bias, in two rolled passes (one body of each: unrolled like the plain form, the call
 // with a cap and a bias took a fifth longer): the scores are made final and written back, with their largest ..
-template <bool kMods>
+template <bool kMods, bool kMasked>
 __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a, uint32_t tS, int key0, uint32_t bad, const float* ks) {
   const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
   float top = -INFINITY;
@@ -252,18 +251,18 @@ __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a
 #pragma unroll
     for (int gg = 0; gg < 2; ++gg) {
       uint32_t* x = r + 16 * gg;
-      const float kc = ks[g + gg] * w.cf;
+      const float kc = ks[g + gg] * (in != 0.f ? w.cf * in : w.cf);
       const int left = ((bad >> (g + gg)) & 1u) ? 0 : w.limit - key0 - 16 * (g + gg);   // keys of the group that are seen
       const float away = kMods ? (float)(w.pos - key0 - 16 * (g + gg)) : 0.f;           // of the row from the first of them
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         float z = __uint_as_float(x[c]) * kc;
         if (kMods) {
-          if (in != 0.f) z = capped(z, in, a.cap_log2);
+          if (in != 0.f) z = capped(z, a.cap_log2);
           z = fmaf(-w.slope, fabsf(away - (float)c), z);
         }
         // a masked score is -inf whatever the factor (which may be 0)
-        x[c] = c < left ? __float_as_uint(z) : 0xFF800000u;
+        x[c] = !kMasked || c < left ? __float_as_uint(z) : 0xFF800000u;
       }
 #pragma unroll
       for (int c = 0; c < 16; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
@@ -316,50 +315,52 @@ __device__ __forceinline__ void pp_shrink(uint32_t tO, float al) {
   tmem_wait_st();
 }
 
-// This thread's query row in two e4m3 terms; returns the factor of its scores.
-__device__ __forceinline__ float pp_query(const PagedAttnArgs& a, const __nv_bfloat16* src, bool there, uint8_t* q_hi, int row) {
-  // the row is read twice (the second time out of L1), as holding it would unroll the split 128 times, code that is
-  // run once a segment
-  const uint4* row16 = reinterpret_cast<const uint4*>(src);
-  uint32_t top2 = 0;                                   // largest |x| of each half word, as bf16 bits
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint4 w = row16[i];
-    top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
-  }
-  const uint32_t top = there ? max(top2 & 0xFFFFu, top2 >> 16) : 0u;
-  // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0); a row with an
-  // infinity or NaN is NaN whatever its scale
-  const int E = max((int)(top >> 7) - 127, -100);
-  const float up = there ? __uint_as_float((uint32_t)(7 - E + 127) << 23) : 0.f;
+// The queries of the warp's 32 pairs (first, first + 1, ..; there are none from `pairs` on) of one half, in two e4m3 terms
+// from row `row0` of q_hi on; returns the factor of the lane's own row's scores.  16 lanes a row, so that loads are
+// whole lines, two rows a step and two steps ahead; rolled, as it is run once a segment.
+__device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg& s, int first, int pairs, uint8_t* q_hi, int row0) {
+  const int lane = threadIdx.x & 31, part = lane & 15, half = lane >> 4;
+  auto load = [&](int k) {
+    const int n = first + 2 * k + half;
+    if (k >= 16 || n >= pairs) return make_uint4(0, 0, 0, 0);
+    const int i = n / a.group, g = n - i * a.group;
+    return __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (int64_t)(s.h * a.group + g) * kKvDim) + part);
+  };
+  float cf = 0.f;
+  uint4 x = load(0), next = load(1);
 #pragma unroll 1
-  for (int i = 0; i < 8; ++i) {                        // 16 values: one 16-byte unit of each term
-    const uint4 y[2] = {row16[2 * i], row16[2 * i + 1]};
-    const uint32_t* w8 = reinterpret_cast<const uint32_t*>(y);
+  for (int k = 0; k < 16; ++k) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    x = next;
+    next = load(k + 2);
+    // the largest |x| as bf16 bits; a row with an infinity or NaN is NaN whatever its scale
+    uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
+    const int E = max((int)(top >> 7) - 127, -100);
+    const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t h2[2], l2[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t w = w8[2 * k + e];
-        // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
-        const uint32_t wl = w << 16, wh = w & 0xFFFF0000u;
-        const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
-        const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
-        h2[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl, xh), __NV_SATFINITE, __NV_E4M3);
-        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2[e], __NV_E4M3);
-        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-        l2[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl - back.x, xh - back.y), __NV_SATFINITE, __NV_E4M3);
-      }
-      hi[k] = h2[0] | h2[1] << 16;
-      lo[k] = l2[0] | l2[1] << 16;
+    for (int e = 0; e < 4; ++e) {
+      // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
+      const uint32_t wl = w[e] << 16, wh = w[e] & 0xFFFF0000u;
+      const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
+      const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
+      hi[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl, xh), __NV_SATFINITE, __NV_E4M3);
+      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
+      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+      lo[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl - back.x, xh - back.y), __NV_SATFINITE, __NV_E4M3);
     }
-    const uint32_t at = sw128_offset(row, i);
-    *reinterpret_cast<uint4*>(q_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(q_hi + pp::kQTermBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    const uint32_t at = sw128_offset(row0 + 2 * k + half, part >> 1) + 8 * (part & 1);
+    *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2*>(q_hi + pp::kQTermBytes + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    const float f = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
+    const float own = __shfl_sync(0xffffffffu, f, 16 * (lane & 1));
+    if ((lane >> 1) == k) cf = own;
   }
-  return __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;
+  return cf;
 }
 
 template <bool kMods>
@@ -471,11 +472,12 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       find(x0, c);
       for (int x = x0; x < x1; ++x) {
         uint32_t none = 0;
-        while (c.qt >= pp_entries(a, pa_shape(a, c.b, none))) {
-          ++c.b;
+        PaShape sh = pa_shape(a, c.b, none);
+        while (c.qt >= pp_entries(a, sh)) {
+          sh = pa_shape(a, ++c.b, none);
           c.qt = 0;
         }
-        sum += pp_entry(a, c.b, c.qt).tiles;
+        sum += pp_entry(a, sh, c.b, c.qt).tiles;
         ++c.qt;
       }
     }
@@ -521,9 +523,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     };
     // the queries of a segment, once the last segment's scores have been computed
     auto load_queries = [&](const PpSeg& s) {
-      int r, head;
-      const bool there = pair_of(s, r, head);
-      const float cf = pp_query(a, a.q + (int64_t)(s.row0 + r) * a.q_stride + (int64_t)head * kKvDim, there, q_hi, row);
+      const float cf = pp_queries(a, s, s.qt * kPromptPairs + kHalfPairs * q + 32 * quarter, s.rows * a.group, q_hi, 32 * quarter);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[q]);
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           return true;
         };
         if constexpr (kMods || decltype(masked)::value) {
-          raise(pp_max64<kMods>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks));
+          raise(pp_max64<kMods, decltype(masked)::value>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks));
           if (!ok) return;
           w.l += pp_exp64(w, tS + 64 * h);
         } else {
