@@ -128,6 +128,7 @@ struct PaColumns {
   int limit[pa::kColMax];       // keys below it are seen
   float pos[pa::kColMax];
   float slope[pa::kColMax];     // * log2 e
+  int at[pa::kColMax];          // row * query heads + head
   int min_limit;                // over the columns
 };
 
@@ -423,6 +424,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           cm.factor[c] = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
           cm.limit[c] = limit;
           cm.pos[c] = (float)pos;
+          cm.at[c] = (s.row0 + i) * a.kv_heads * a.group + s.h * a.group + (n - i * a.group);
           cm.slope[c] = kMods && a.slopes ? a.slopes[s.h * a.group + (n - i * a.group)] * 1.4426950408889634f : 0.f;
         }
       }
@@ -667,14 +669,18 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       i0 += s.n;
       // ---- the segment's end: each warpgroup leaves its maxima and denominators, and one writes the outputs
 #pragma unroll
-      for (int c = 0; c < kCE; ++c) {
-        float v = l[c];
+      for (int c0 = 0; c0 < kCE; c0 += 8) {
+        if (c0 >= live) continue;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) wmax[wg][quarter][c] = v;
+        for (int c = c0; c < c0 + 8; ++c) {
+          float v = l[c];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == 0) wmax[wg][quarter][c] = v;
+        }
       }
       named_bar_sync(bar, 128);
-      if (quarter == 0 && lane < kCE) {
+      if (quarter == 0 && lane < live) {
         stat[qb][wg][0][lane] = m_lane;
         stat[qb][wg][1][lane] = mv_lane;
         stat[qb][wg][2][lane] = (wmax[wg][0][lane] + wmax[wg][1][lane]) + (wmax[wg][2][lane] + wmax[wg][3][lane]);
@@ -691,7 +697,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const int pairs = s.rows * a.group;
       // a piece that starts its segment is its CTA's last unless it also starts the CTA's range
       const int slot = u - s.n == u0 ? 2 * cta : 2 * cta + 1;
-      if (quarter == 0 && lane < kCE) {
+      if (quarter == 0 && lane < live) {
         // out = sum_w f_w O_w: f_w = 2^(m_w - M) / (L 64 2^(m_w - mv_w)) = 2^(mv_w - M) / (64 L), without L for a piece
         const float ma = stat[qb][0][0][lane], mb = stat[qb][1][0][lane], la = stat[qb][0][2][lane], lb = stat[qb][1][2][lane];
         const bool has_a = la > 0.f || la != la, has_b = lb > 0.f || lb != lb;   // NaN counts as seen
@@ -700,13 +706,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         const float over = (whole ? 1.f / L : 1.f) / kPOne;
         fin[wg][0][lane] = has_a ? ex2_approx(stat[qb][0][1][lane] - M) * over : 0.f;
         fin[wg][1][lane] = has_b ? ex2_approx(stat[qb][1][1][lane] - M) * over : 0.f;
-        const int n = s.cg * kCE + lane;
         if (whole) {
-          if (a.lse && n < pairs) {
-            const int r = n / a.group;
-            a.lse[(int64_t)(s.row0 + r) * a.kv_heads * a.group + s.h * a.group + (n - r * a.group)] =
-                has_a || has_b ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
-          }
+          if (a.lse) a.lse[cm.at[lane]] = has_a || has_b ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
         } else {
           float* ml = a.part_ml + ((int64_t)slot * kColMax + lane) * 2;
           ml[0] = M;
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       if (!mbar_wait_warp(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < kCE; c0 += 8) {
+      for (int c0 = 0; c0 < live; c0 += 8) {
         uint32_t r[32];
         tmem_ld_cols8(acc + c0, r);
         tmem_ld_cols8(acc + kHalf + c0, r + 8);
@@ -729,8 +730,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const int n = s.cg * kCE + c0 + c;
-          if (n >= pairs) break;
+          if (c0 + c >= live) break;
           const float fa = fin[wg][0][c0 + c], fb = fin[wg][1][c0 + c];
           // an accumulator without a seen key holds nothing of this column (or was never written)
           float v = 0.f;
@@ -738,9 +738,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           if (fb != 0.f) v = fmaf(fmaf(__uint_as_float(r[24 + c]), 0.0625f, __uint_as_float(r[16 + c])), fb, v);
           if ((poison >> (c0 + c)) & 1u) v = __int_as_float(0x7FC00000);
           if (whole) {
-            const int i2 = n / a.group;
-            a.out[((int64_t)(s.row0 + i2) * a.kv_heads * a.group + s.h * a.group + (n - i2 * a.group)) * kKvDim + row] =
-                __float2bfloat16_rn(v);
+            a.out[(int64_t)cm.at[c0 + c] * kKvDim + row] = __float2bfloat16_rn(v);
           } else {
             a.part_o[((int64_t)slot * kColMax + c0 + c) * kKvDim + row] = v;
           }
@@ -795,7 +793,7 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
       mj[g] = -INFINITY;
       lj[g] = 0.f;
       x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p <= last && pa_unit_start(p, units, ctas) < pa_unit_start(p + 1, units, ctas)) {
+      if (p <= last && (units >= ctas || pa_unit_start(p, units, ctas) < pa_unit_start(p + 1, units, ctas))) {
         const int64_t at = (int64_t)(p == first ? first_slot : 2 * p) * kPagedAttnColumns + col;
         const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
         mj[g] = ml.x;

@@ -317,7 +317,7 @@ __device__ __forceinline__ void pp_shrink(uint32_t tO, float al) {
 
 // The queries of the warp's 32 pairs (first, first + 1, ..; there are none from `pairs` on) of one half, in two e4m3 terms
 // from row `row0` of q_hi on; returns the factor of the lane's own row's scores.  16 lanes a row, so that loads are
-// whole lines, two rows a step and two steps ahead; rolled, as it is run once a segment.
+// whole lines, two rows a step and four steps ahead; rolled, as it is run once a segment.
 __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg& s, int first, int pairs, uint8_t* q_hi, int row0) {
   const int lane = threadIdx.x & 31, part = lane & 15, half = lane >> 4;
   auto load = [&](int k) {
@@ -327,12 +327,16 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
     return __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (int64_t)(s.h * a.group + g) * kKvDim) + part);
   };
   float cf = 0.f;
-  uint4 x = load(0), next = load(1);
+  uint4 x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = load(j);
 #pragma unroll 1
-  for (int k = 0; k < 16; ++k) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    x = next;
-    next = load(k + 2);
+  for (int k0 = 0; k0 < 16; k0 += 4) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = k0 + j;
+    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+    x[j] = load(k + 4);
     // the largest |x| as bf16 bits; a row with an infinity or NaN is NaN whatever its scale
     uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
     top = max(top & 0xFFFFu, top >> 16);
@@ -359,6 +363,7 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
     const float f = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
     const float own = __shfl_sync(0xffffffffu, f, 16 * (lane & 1));
     if ((lane >> 1) == k) cf = own;
+  }
   }
   return cf;
 }
@@ -925,6 +930,15 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           mbar_arrive(&seg_full[seg % kSegBufs]);
         }
         __syncwarp();
+        // its queries on their way into L2: they are loaded when the segment before ends, with nothing to hide them
+        if (seg > 0 && s.n) {
+          const int first = s.qt * kPromptPairs, last = min(first + kPromptPairs, s.rows * a.group);
+          for (int n = first + (lane >> 1); n < last; n += 16) {
+            const int i = n / a.group, g = n - i * a.group;
+            const __nv_bfloat16* p = a.q + (int64_t)(s.row0 + i) * a.q_stride + (int64_t)(s.h * a.group + g) * kKvDim + 64 * (lane & 1);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+          }
+        }
         if (s.n == 0) break;
         u += s.n;
       }
@@ -957,26 +971,37 @@ __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const _
   float acc[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  for (int p = first; p <= last; ++p) {
-    if (pa_unit_start(p, units, ctas) == pa_unit_start(p + 1, units, ctas)) continue;
-    const int64_t slot = p == first ? first_slot : 2 * p;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * kPromptPairs + threadIdx.x);
-    float4 x[4];
+  constexpr int kGroup = 2;                                // pieces whose loads are in flight together
+  for (int p0 = first; p0 <= last; p0 += kGroup) {
+    float2 ml[kGroup];
+    float4 x[kGroup][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (kKvDim / 4) + 4 * blockIdx.y + k) * kPromptPairs + threadIdx.x);
-    if (ml.y == 0.f) continue;                             // a piece that sees nothing (NaN counts as seen)
-    const float Mn = fmaxf(M, ml.x);
-    const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml.x - Mn);
-    L = L * sc + w * ml.y;
+    for (int g = 0; g < kGroup; ++g) {
+      const int p = p0 + g;
+      ml[g] = make_float2(-INFINITY, 0.f);
+      if (p <= last && (units >= ctas || pa_unit_start(p, units, ctas) < pa_unit_start(p + 1, units, ctas))) {
+        const int64_t slot = p == first ? first_slot : 2 * p;
+        ml[g] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * kPromptPairs + threadIdx.x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      acc[4 * k] = fmaf(w, x[k].x, acc[4 * k] * sc);
-      acc[4 * k + 1] = fmaf(w, x[k].y, acc[4 * k + 1] * sc);
-      acc[4 * k + 2] = fmaf(w, x[k].z, acc[4 * k + 2] * sc);
-      acc[4 * k + 3] = fmaf(w, x[k].w, acc[4 * k + 3] * sc);
+        for (int k = 0; k < 4; ++k)
+          x[g][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (kKvDim / 4) + 4 * blockIdx.y + k) * kPromptPairs + threadIdx.x);
+      }
     }
-    M = Mn;
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      if (ml[g].y == 0.f) continue;                        // a piece that sees nothing (NaN counts as seen)
+      const float Mn = fmaxf(M, ml[g].x);
+      const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml[g].x - Mn);
+      L = L * sc + w * ml[g].y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[4 * k] = fmaf(w, x[g][k].x, acc[4 * k] * sc);
+        acc[4 * k + 1] = fmaf(w, x[g][k].y, acc[4 * k + 1] * sc);
+        acc[4 * k + 2] = fmaf(w, x[g][k].z, acc[4 * k + 2] * sc);
+        acc[4 * k + 3] = fmaf(w, x[g][k].w, acc[4 * k + 3] * sc);
+      }
+      M = Mn;
+    }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int i = n / a.group;
