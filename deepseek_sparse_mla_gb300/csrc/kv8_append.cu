@@ -12,7 +12,7 @@
 // What bounds it: a prompt, the bytes (4 read and 2 written per cached value pair); a decode step, latency.
 // One CTA owns one page of one head of K or of V, so nothing is shared and no atomics are needed: it
 // holds the page's new values in registers between the maximum and the coding, and reads them once.  At
-// most four 32-byte pieces a thread keep several CTAs on an SM (with eight a prompt took XXX us instead of YYY), and
+// most four 32-byte pieces a thread keep several CTAs on an SM (with eight, four prompts of 4,096 took 29.5 us instead of 20.8), and
 // the values are asked for before the page's id and old scale, on which they do not depend.
 #include "dsa_internal.cuh"
 

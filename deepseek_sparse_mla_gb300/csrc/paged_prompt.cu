@@ -17,13 +17,15 @@
 // Segments count the tiles their last row sees, so causal rows are balanced over the CTAs.
 //
 // Per CTA (20 warps): warps 0-3 and 4-7 are the softmax of the two 128-pair halves, one pair a thread (no
-// cross-lane work at all); each half has a warp of its own that issues its products (16 and 17).  A half goes
-// through a tile as two times 64 keys, each with its own 64 columns of TMEM for S and then P: while the
-// softmax works on one, the tensor cores add the other to O and compute the next tile's S in its place.  One
-// S of 128 keys a half, its softmax and its products taking turns, took 4,500 cycles a tile (3.8 ms
-// for 4,096 rows at 64K); the scores' products are a half slower at 64 keys, which this more than pays for.
-// Warp 18 loads K tiles by TMA; warps 8-11 and 12-15 widen the V tiles, even and odd ones; warp 19 finds the CTA's
-// segments, ahead of the others (each finding them for itself cost 30 registers in every role, and spills).
+// cross-lane work at all).  A half goes through a tile as two times 64 keys, each with its own 64 columns of TMEM
+// for S and then P: while the softmax works on one, the tensor cores add the other to O and compute the next
+// tile's S in its place.  One S of 128 keys a half, its softmax and its products taking turns, took 4,500
+// cycles a tile (3.8 ms for 4,096 rows at 64K); the scores' products are a half slower at 64 keys, which this
+// more than pays for.  Warp 16 issues the output products, warps 17 and 18 one half's scores each, as soon as
+// the output product that read the P in their place is known to be done (products of different kinds are not
+// promised to run in order; one warp a half for both kinds, waiting for that, took 3.57 ms instead of 3.31).
+// Warps 8-11 and 12-15 widen the V tiles, even and odd ones; warp 19 loads K tiles by TMA and finds the CTA's
+// segments for everyone (each role finding them for itself cost 30 registers, and spills).
 // TMEM (all 512 columns): S of half q and key half h at 128 q + 64 h, with P over its first 32; O of half q at 256 + 128 q.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
@@ -45,7 +47,7 @@ constexpr int kVBytes = kTok * kKvDim * 2;           // 32 KB of fp16: two 64-wi
 constexpr int kChunkBytes = kTok * 128;
 constexpr int kKStages = 4;
 constexpr int kThreads = 640;
-constexpr int kConvWarp0 = 8, kMmaWarp0 = 16, kLoadWarp = 18, kSchedWarp = 19;
+constexpr int kConvWarp0 = 8, kOutWarp = 16, kScoreWarp0 = 17, kLoadWarp = 19;
 constexpr uint32_t kRegsSoft = 128, kRegsConv = 80, kRegsRest = 64;   // 2 * 128 + 2 * 80 + 64 = 480 = 5 * 96, the launch's
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
@@ -194,14 +196,10 @@ struct PpRow {
   int limit, pos;
 };
 
-// 64 keys of a row, in one pass over their scores: 16 at a time they come out of TMEM (the next 16 in flight),
-// and P = 2^(z - m + 8) is formed against the reference that the row has.  P stays in registers until the largest
-// score (returned) is known to exceed it by no more than the slack, as for nearly every tile; else the pass is
-// repeated.  An exact maximum first would read the scores twice, or hold them all (176 registers).
 // 64 keys of a row that sees them all, in one pass over their scores: 16 at a time they come out of TMEM (the next
 // 16 in flight), and P = 2^(z - m + 8) is formed against the reference that the row has.  P stays in registers until
 // the largest score (returned) is known to exceed it by no more than the slack, as for nearly every tile; else
-// the pass is repeated.  (Two passes, as below, took 3.15 ms instead of 2.94 for 4,096 rows at 64K.)
+// the pass is repeated.  (Two passes, as below, take 7 % longer for 4,096 rows at 64K.)
 __device__ __forceinline__ float pp_half(const PpRow& w, uint32_t tS, const float* ks, uint32_t (&p)[32], float& sum_out) {
   const float shift = pp::kPLog2 - (w.m == -INFINITY ? 0.f : w.m);
   const uint64_t shift2 = pack2(shift, shift);
@@ -333,37 +331,37 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
 #pragma unroll 1
   for (int k0 = 0; k0 < 16; k0 += 4) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int k = k0 + j;
-    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-    x[j] = load(k + 4);
-    // the largest |x| as bf16 bits; a row with an infinity or NaN is NaN whatever its scale
-    uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-    top = max(top & 0xFFFFu, top >> 16);
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j;
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      x[j] = load(k + 4);
+      // the largest |x| as bf16 bits; a row with an infinity or NaN is NaN whatever its scale
+      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
-    const int E = max((int)(top >> 7) - 127, -100);
-    const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
-    uint32_t hi[4], lo[4];
+      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
+      const int E = max((int)(top >> 7) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+      uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
-      const uint32_t wl = w[e] << 16, wh = w[e] & 0xFFFF0000u;
-      const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
-      const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
-      hi[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl, xh), __NV_SATFINITE, __NV_E4M3);
-      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
-      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-      lo[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl - back.x, xh - back.y), __NV_SATFINITE, __NV_E4M3);
+      for (int e = 0; e < 4; ++e) {
+        // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
+        const uint32_t wl = w[e] << 16, wh = w[e] & 0xFFFF0000u;
+        const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
+        const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
+        hi[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl, xh), __NV_SATFINITE, __NV_E4M3);
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
+        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+        lo[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl - back.x, xh - back.y), __NV_SATFINITE, __NV_E4M3);
+      }
+      const uint32_t at = sw128_offset(row0 + 2 * k + half, part >> 1) + 8 * (part & 1);
+      *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2*>(q_hi + pp::kQTermBytes + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      const float f = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
+      const float own = __shfl_sync(0xffffffffu, f, 16 * (lane & 1));
+      if ((lane >> 1) == k) cf = own;
     }
-    const uint32_t at = sw128_offset(row0 + 2 * k + half, part >> 1) + 8 * (part & 1);
-    *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-    *reinterpret_cast<uint2*>(q_hi + pp::kQTermBytes + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-    const float f = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
-    const float own = __shfl_sync(0xffffffffu, f, 16 * (lane & 1));
-    if ((lane >> 1) == k) cf = own;
-  }
   }
   return cf;
 }
@@ -398,11 +396,11 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 2);                       // both halves' products
+      mbar_init(&k_empty[i], 2);                       // both halves' scores
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 4);
-      mbar_init(&v_empty[i], 2);
+      mbar_init(&v_empty[i], 1);
       for (int h = 0; h < 2; ++h) {
         mbar_init(&s_full[i][h], 2);                   // the products, and their issuer
         mbar_init(&p_full[i][h], 4);
@@ -416,12 +414,12 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], 19);                    // every warp of the other roles
     }
-    mbar_init(&mma_done, 2);
+    mbar_init(&mma_done, 3);
     prefetch_tmap(&k_map);
     bits_all = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp0) {
+  if (warp == kOutWarp) {
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -500,7 +498,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   uint32_t* const err = &bits_all;
   // the scheduler starts at the run that holds u0
   PpCursor cur = {0, 0, 0};
-  if (warp == kSchedWarp && u0 < u1) {
+  if (warp == kLoadWarp && u0 < u1) {
     int lo = 0, hi = kRuns - 1;                       // the last run whose units begin at or before u0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -667,7 +665,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         mbar_arrive(&seg_empty[seg % kSegBufs]);
       }
     }
-  } else if (warp < kMmaWarp0) {
+  } else if (warp < kOutWarp) {
     regs_dec<kRegsConv>();
     // ---------------------------------------------------------------- V tiles: codes to fp16
     // Two groups of four warps take alternate tiles: eight lanes a row of 16-byte pieces, 16 rows a pass, so that a
@@ -785,34 +783,58 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     }
   } else {
     regs_dec<kRegsRest>();
-    if (warp < kLoadWarp) {
-      // ---------------------------------------------------------------- products of one half
-      // Order: .. O(i, h) S(i + 1, h) ..: S takes the place of the P that O has read (products of one thread run in order).
-      const int q = warp - kMmaWarp0;
+    if (warp == kOutWarp) {
+      // ---------------------------------------------------------------- output products of both halves
       const bool leader = elect_one();
-      const uint32_t id_s = idesc_e4m3(128, 64);
       const uint32_t id_o = idesc_f16(128, kKvDim, false, false, false, true);
-      const uint64_t d_q = smem_desc(smem_u32(sQ + 2 * q * kQTermBytes), 16, 1024, kSwizzle128B);
-      const uint64_t d_k = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
       const uint64_t d_v = smem_desc(smem_u32(sV), kChunkBytes, 1024, kSwizzle128B);
       bool ok = true;
-      auto scores = [&](int i, int h) {
-        const int st = i % kKStages;
-        if (h == 0) ok = ok && mbar_wait_warp(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout, kPolls);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t k = d_k + (uint64_t)((st * kKBytes + 64 * h * kKvDim) >> 4);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)               // hi, then lo
-            mma_ss_f8(tmem + 128 * q + 64 * h, d_q + (uint64_t)(((kk >> 2) * kQTermBytes + (kk & 3) * 32) >> 4), k + 2 * (kk & 3), id_s,
-                      kk > 0);
-          mma_commit(&s_full[q][h]);
-          mbar_arrive(&s_full[q][h]);
-          if (h == 1) mma_commit(&k_empty[st]);
-        }
+      int i = 0;
+      for (int seg = 0;; ++seg) {
+        ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+        if (!ok) break;
+        const int n = segs[seg % kSegBufs].n;
         __syncwarp();
-      };
+        if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
+        if (n == 0) break;
+        for (int t = 0; t < n && ok; ++t, ++i) {
+          const uint64_t v = d_v + (uint64_t)(((i & 1) * kVBytes) >> 4);
+          ok = mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              if (t == 0 && h == 0 && seg > 0) ok = ok && mbar_wait_warp(&o_empty[q], (seg - 1) & 1, err, kErrMmaTimeout, kPolls);
+              ok = ok && mbar_wait_warp(&p_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ts(tmem + kColO + 128 * q, tmem + 128 * q + 64 * h + 8 * kk, v + (uint64_t)(((64 * h + 16 * kk) * 128) >> 4),
+                         id_o, t > 0 || h > 0 || kk > 0);
+                mma_commit(&pv_done[q][h]);
+                if (h == 1 && q == 1) mma_commit(&v_empty[i & 1]);
+                if (h == 1 && t + 1 == n) {
+                  mma_commit(&o_full[q]);
+                  mbar_arrive(&o_full[q]);
+                }
+              }
+              __syncwarp();
+            }
+        }
+        if (!ok) break;
+      }
+      if (leader) mma_commit(&mma_done);
+      mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+    } else if (warp < kLoadWarp) {
+      // ---------------------------------------------------------------- score products of one half
+      const int q = warp - kScoreWarp0;
+      const bool leader = elect_one();
+      const uint32_t id_s = idesc_e4m3(128, 64);
+      const uint64_t d_q = smem_desc(smem_u32(sQ + 2 * q * kQTermBytes), 16, 1024, kSwizzle128B);
+      const uint64_t d_k = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
+      bool ok = true;
       int i = 0;
       for (int seg = 0;; ++seg) {
         ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
@@ -822,54 +844,67 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
         if (n == 0) break;
         ok = mbar_wait_warp(&q_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
-        if (!ok) break;
-        scores(i, 0);
-        scores(i, 1);
-        if (seg > 0) ok = ok && mbar_wait_warp(&o_empty[q], (seg - 1) & 1, err, kErrMmaTimeout, kPolls);
         for (int t = 0; t < n && ok; ++t, ++i) {
-          const uint64_t v = d_v + (uint64_t)(((i & 1) * kVBytes) >> 4);
-          ok = mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
+          const int st = i % kKStages;
+          ok = mbar_wait_warp(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout, kPolls);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            ok = ok && mbar_wait_warp(&p_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
+            // S takes the place of the P of the tile before, once O has read it
+            if (i > 0) ok = ok && mbar_wait_warp(&pv_done[q][h], (i - 1) & 1, err, kErrMmaTimeout, kPolls);
             if (!ok) break;
             tc_fence_after();
+            const uint64_t k = d_k + (uint64_t)((st * kKBytes + 64 * h * kKvDim) >> 4);
             if (leader) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts(tmem + kColO + 128 * q, tmem + 128 * q + 64 * h + 8 * kk, v + (uint64_t)(((64 * h + 16 * kk) * 128) >> 4), id_o,
-                       t > 0 || h > 0 || kk > 0);
-              mma_commit(&pv_done[q][h]);
-              if (h == 1) {
-                mma_commit(&v_empty[i & 1]);
-                if (t + 1 == n) {
-                  mma_commit(&o_full[q]);
-                  mbar_arrive(&o_full[q]);
-                }
-              }
+              for (int kk = 0; kk < 8; ++kk)           // hi, then lo
+                mma_ss_f8(tmem + 128 * q + 64 * h, d_q + (uint64_t)(((kk >> 2) * kQTermBytes + (kk & 3) * 32) >> 4), k + 2 * (kk & 3),
+                          id_s, kk > 0);
+              mma_commit(&s_full[q][h]);
+              mbar_arrive(&s_full[q][h]);
+              if (h == 1) mma_commit(&k_empty[st]);
             }
             __syncwarp();
-            if (t + 1 < n) scores(i + 1, h);
           }
         }
         if (!ok) break;
       }
       if (leader) mma_commit(&mma_done);
       mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
-    } else if (warp == kLoadWarp) {
-      // ---------------------------------------------------------------- K tiles
+    } else {
+      // ---------------------------------------------------------------- segments (and an end mark), and their K tiles
       const uint64_t policy = l2_evict_normal();
       const int lp = a.log2_page, ppt = kTok >> lp;
       const uint32_t page_bytes = (uint32_t)kKvDim << lp;
       int i = 0;
+      int64_t u = u0;
       bool ok = true;
       for (int seg = 0;; ++seg) {
-        ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+        if (seg >= kSegBufs) ok = mbar_wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
-        const PpSeg s = segs[seg % kSegBufs];
+        PpSeg s = {};
+        // segments are cut where the range ends, or (short requests) belong to the range they begin in as a whole
+        if (u < u1) s = pp_segment(a, cur, u, u0, a.whole ? units : u1, cta);
+        if (a.whole && s.n && s.tile > 0) {
+          u += s.n;
+          s.n = 0;
+          if (u < u1) s = pp_segment(a, cur, u, u0, units, cta);
+        }
+        if (lane == 0) {
+          segs[seg % kSegBufs] = s;
+          mbar_arrive(&seg_full[seg % kSegBufs]);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
         if (s.n == 0) break;
+        u += s.n;
+        // its queries on their way into L2: they are loaded when the segment before ends, with nothing to hide them
+        if (seg > 0) {
+          const int first = s.qt * kPromptPairs, last = min(first + kPromptPairs, s.rows * a.group);
+          for (int n = first + (lane >> 1); n < last; n += 16) {
+            const int r = n / a.group, g = n - r * a.group;
+            const __nv_bfloat16* p = a.q + (int64_t)(s.row0 + r) * a.q_stride + (int64_t)(s.h * a.group + g) * kKvDim + 64 * (lane & 1);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+          }
+        }
         const int pages = (s.len + (1 << lp) - 1) >> lp;
         int batch = -1, page = -1;                     // 32 pages at a time, one a lane
         float ks = 0.f;
@@ -912,41 +947,11 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       // nothing may still be landing in shared memory when the CTA exits
       for (int st = 0; st < kKStages; ++st)
         if (i > st) mbar_wait_warp(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
-    } else {
-      // ---------------------------------------------------------------- scheduler: the segments, and an end mark
-      int64_t u = u0;
-      for (int seg = 0;; ++seg) {
-        if (seg >= kSegBufs && !mbar_wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
-        PpSeg s = {};
-        // segments are cut where the range ends, or (short requests) belong to the range they begin in as a whole
-        if (u < u1) s = pp_segment(a, cur, u, u0, a.whole ? units : u1, cta);
-        if (a.whole && s.n && s.tile > 0) {
-          u += s.n;
-          s.n = 0;
-          if (u < u1) s = pp_segment(a, cur, u, u0, units, cta);
-        }
-        if (lane == 0) {
-          segs[seg % kSegBufs] = s;
-          mbar_arrive(&seg_full[seg % kSegBufs]);
-        }
-        __syncwarp();
-        // its queries on their way into L2: they are loaded when the segment before ends, with nothing to hide them
-        if (seg > 0 && s.n) {
-          const int first = s.qt * kPromptPairs, last = min(first + kPromptPairs, s.rows * a.group);
-          for (int n = first + (lane >> 1); n < last; n += 16) {
-            const int i = n / a.group, g = n - i * a.group;
-            const __nv_bfloat16* p = a.q + (int64_t)(s.row0 + i) * a.q_stride + (int64_t)(s.h * a.group + g) * kKvDim + 64 * (lane & 1);
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-          }
-        }
-        if (s.n == 0) break;
-        u += s.n;
-      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp0) {
+  if (warp == kOutWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
