@@ -719,6 +719,8 @@ dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batc
   if (st != DSA_OK) return st;
   if (batch->num_requests > DSA_MAX_REQUESTS)
     return fail(DSA_ERR_UNSUPPORTED, "batch.num_requests %d is more than %d", batch->num_requests, DSA_MAX_REQUESTS);
+  if ((int64_t)batch->block_table_stride * cache->page_size > int64_t(1) << 30)   // positions of the next tiles stay in 32 bits
+    return fail(DSA_ERR_UNSUPPORTED, "block_table_stride * cache.page_size is more than 2^30 tokens");
   if (q_heads <= 0 || q_heads % cache->kv_heads)
     return fail(DSA_ERR_INVALID_ARG, "q_heads %d is not a multiple of cache.kv_heads %d", q_heads, cache->kv_heads);
   const int group = q_heads / cache->kv_heads;

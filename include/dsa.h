@@ -594,7 +594,11 @@ typedef struct {
  * A row that sees nothing (an empty request) gets zeros and an lse of -inf.  Rows behind the last request's
  * are left as they were.  What lies in the cache behind a request's tokens is never used, NaN codes included.
  * A visible position without a valid page is skipped and reported (DSA_DEVICE_BAD_PAGE).
- * Sums, maxima and lse are fp32; q keeps all of bf16's bits in the products, a probability 8 or more.
+ * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-18 of its
+ * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), a contribution to the output 8
+ * bits or more with one of 2^-20 of the largest contribution; requests of more rows hold V to 2^-25 of the
+ * largest V scale of the request's pages.
+ * DSA_ERR_UNSUPPORTED for more than DSA_MAX_REQUESTS requests, and for block-table rows of more than 2^30 tokens.
  */
 DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q,
                                        int64_t q_stride, int32_t q_heads, float scale, int32_t max_query_len,
