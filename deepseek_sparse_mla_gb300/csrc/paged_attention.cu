@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             const float r = warp_max_f32(z[c]);
             if (lane == c) mine = r;                   // lane c of every warp ends up with column c's
           }
-          const float lv_max = warp_max_f32(fmaxf(__log2f(fabsf(vs)), -126.f));
+          // held at -118: 4 * kPOne * 2^(m - mv) stays finite for pages whose scales are smaller, or 0
+          const float lv_max = warp_max_f32(fmaxf(__log2f(fabsf(vs)), -118.f));
           if (lane < kCE) wmax[wg][quarter][lane] = mine;
           if (lane == 0) wlv[wg][quarter] = lv_max;
           named_bar_sync(bar, 128);
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               z[c + q] = ex2_approx(z[c + q] - mm[q]);
-              x[q] = z[c + q] * (vs * ee[q]);
+              x[q] = (z[c + q] * ee[q]) * vs;         // in this order: 0 stays 0 whatever the scale of an unseen key
               p_top = fmaxf(p_top, z[c + q]);
               x_top = fmaxf(x_top, x[q]);
             }
