@@ -110,7 +110,8 @@ dsa_status static_scratch_of_current_device(void** out);
 // or exits, and calls pdl_trigger() (if at all: without it the next grid starts when this one
 // completes) only after its own pdl_wait().  A grid can then start only when its predecessor has
 // passed its wait, so every grid before that predecessor has completed; a grid completes only
-// after its predecessor has.  (Both are no-ops in a plain launch.)
+// after its predecessor has.  (Both are no-ops in a plain launch.  A later kernel of one call may read that call's
+// inputs without waiting: the call's first kernel has waited for them.)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

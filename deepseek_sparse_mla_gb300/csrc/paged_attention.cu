@@ -396,23 +396,16 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         x = next;
         next = load(c + 4);
-        // the largest |x| as bf16 bits; a row with an infinity or NaN is NaN whatever its scale
+        // the largest |x| as bf16 bits
         uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
         top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
-        const int E = max((int)(top >> 7) - 127, -100);
-        const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+        const int E = pa_exponent(top);
+        const __nv_bfloat162 up = pa_up(E);
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
-          const uint32_t wl = w[e] << 16, wh = w[e] & 0xFFFF0000u;
-          const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
-          const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
-          split2(xl, xh, hi[e], lo[e]);
-        }
+        for (int e = 0; e < 4; ++e) pa_split<16>(w[e], up, hi[e], lo[e]);
         if (c >= live) continue;
         const uint32_t at = (((part >> 1) ^ (c & 7)) << 4) + 8 * (part & 1);
         *reinterpret_cast<uint2*>(q_hi + c * kKvDim + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -421,7 +414,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
         low = min(low, limit);
         if (part == 0) {
-          cm.factor[c] = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
+          cm.factor[c] = pa_factor(top, E, a.scale_log2);
           cm.limit[c] = limit;
           cm.pos[c] = (float)pos;
           cm.at[c] = (s.row0 + i) * a.kv_heads * a.group + s.h * a.group + (n - i * a.group);
@@ -521,15 +514,23 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
               tmem_ld_cols8(tmem + lanes + 64 * sb + kHalf + c0 + c, lo + c);
             }
             tmem_wait_ld();
+            // a loop each: a choice made inside one of them would leave the values no instructions to overlap with
 #pragma unroll
-            for (int c = 0; c < 16 && c0 + c < kNC; ++c) {
-              float x = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
-              if (kMods) {
-                if (in != 0.f) x = capped(x * in, a.cap_log2);
-                x = fmaf(-cm.slope[c0 + c], fabsf(cm.pos[c0 + c] - (float)j), x);
-              }
-              if (kMasked && (!exists || j >= cm.limit[c0 + c])) x = -INFINITY;
-              z[c0 + c] = x;
+            for (int c = 0; c < 16 && c0 + c < kNC; ++c)
+              z[c0 + c] = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
+            if (kMods && in != 0.f) {
+#pragma unroll
+              for (int c = 0; c < 16 && c0 + c < kNC; ++c) z[c0 + c] = capped(z[c0 + c] * in, a.cap_log2);
+            }
+            if (kMods) {
+#pragma unroll
+              for (int c = 0; c < 16 && c0 + c < kNC; ++c)
+                z[c0 + c] = fmaf(-cm.slope[c0 + c], fabsf(cm.pos[c0 + c] - (float)j), z[c0 + c]);
+            }
+            if (kMasked) {
+#pragma unroll
+              for (int c = 0; c < 16 && c0 + c < kNC; ++c)
+                if (!exists || j >= cm.limit[c0 + c]) z[c0 + c] = -INFINITY;
             }
           }
         };

@@ -2,6 +2,9 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "dsa_internal.cuh"
 
@@ -40,6 +43,32 @@ __device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, uint3
   s.len = (int)len;
   s.tiles = max(1, (int)((len + kPaTok - 1) / kPaTok));
   return s;
+}
+
+// Two bf16 values as two e4m3 terms: hi = e4m3(x up), lo = e4m3(kLo (x up - hi)), with up a power of two that brings the
+// row's largest value to [128, 256).  x up is exact in bf16, and in fp16 too but far below e4m3's smallest step; so are the
+// difference and its product with kLo.  Half the instructions of the same steps in fp32.
+template <int kLo>
+__device__ __forceinline__ void pa_split(uint32_t w, __nv_bfloat162 up, uint32_t& hi, uint32_t& lo) {
+  const float2 x = __bfloat1622float2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), up));
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3);
+  __half2 d = __hsub2(h, __half2(back));
+  if (kLo != 1) d = __hmul2(d, __float2half2_rn((float)kLo));
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(d), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The exponent of a row's largest value (its bf16 bits, sign off), held at -100: smaller rows score 0.
+__device__ __forceinline__ int pa_exponent(uint32_t top) { return max((int)(top >> 7) - 127, -100); }
+__device__ __forceinline__ __nv_bfloat162 pa_up(int E) {        // 2^(7 - E), twice
+  const uint32_t b = (uint32_t)(7 - E + 127) << 7, bb = b | b << 16;
+  return *reinterpret_cast<const __nv_bfloat162*>(&bb);
+}
+// What a row's scores are multiplied with: 2^(E - 7) (exact) times the scale.  A row with an infinity or NaN scores NaN,
+// as the infinity's product with a key's zeros or mixed signs does.
+__device__ __forceinline__ float pa_factor(uint32_t top, int E, float scale) {
+  return top >= 0x7F80u ? __int_as_float(0x7FC00000) : __uint_as_float((uint32_t)(E - 7 + 127) << 23) * scale;
 }
 
 // Requests of many rows (paged_prompt.cu); k_map: the K codes in boxes of a page.

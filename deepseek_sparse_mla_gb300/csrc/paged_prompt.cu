@@ -252,16 +252,21 @@ __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a
       const float kc = ks[g + gg] * (in != 0.f ? w.cf * in : w.cf);
       const int left = ((bad >> (g + gg)) & 1u) ? 0 : w.limit - key0 - 16 * (g + gg);   // keys of the group that are seen
       const float away = kMods ? (float)(w.pos - key0 - 16 * (g + gg)) : 0.f;           // of the row from the first of them
+      // a loop each: a choice made inside one of them would leave the values no instructions to overlap with
+      float z[16];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        float z = __uint_as_float(x[c]) * kc;
-        if (kMods) {
-          if (in != 0.f) z = capped(z, a.cap_log2);
-          z = fmaf(-w.slope, fabsf(away - (float)c), z);
-        }
-        // a masked score is -inf whatever the factor (which may be 0)
-        x[c] = !kMasked || c < left ? __float_as_uint(z) : 0xFF800000u;
+      for (int c = 0; c < 16; ++c) z[c] = __uint_as_float(x[c]) * kc;
+      if (kMods && in != 0.f) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) z[c] = capped(z[c], a.cap_log2);
       }
+      if (kMods) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) z[c] = fmaf(-w.slope, fabsf(away - (float)c), z[c]);
+      }
+      // a masked score is -inf whatever the factor (which may be 0)
+#pragma unroll
+      for (int c = 0; c < 16; ++c) x[c] = !kMasked || c < left ? __float_as_uint(z[c]) : 0xFF800000u;
 #pragma unroll
       for (int c = 0; c < 16; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
     }
@@ -335,30 +340,20 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
       const int k = k0 + j;
       const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
       x[j] = load(k + 4);
-      // the largest |x| as bf16 bits; a row with an infinity or NaN is NaN whatever its scale
+      // the largest |x| as bf16 bits
       uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
       top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // the largest goes to [128, 256): x * 2^(7 - E), E its exponent (held at -100: smaller rows score 0)
-      const int E = max((int)(top >> 7) - 127, -100);
-      const float up = __uint_as_float((uint32_t)(7 - E + 127) << 23);
+      const int E = pa_exponent(top);
+      const __nv_bfloat162 up = pa_up(E);
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // an infinity becomes NaN, as its product with a key's zeros or mixed signs is
-        const uint32_t wl = w[e] << 16, wh = w[e] & 0xFFFF0000u;
-        const float xl = (wl & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wl) * up;
-        const float xh = (wh & 0x7F800000u) == 0x7F800000u ? __int_as_float(0x7FC00000) : __uint_as_float(wh) * up;
-        hi[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl, xh), __NV_SATFINITE, __NV_E4M3);
-        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
-        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-        lo[e] = __nv_cvt_float2_to_fp8x2(make_float2(xl - back.x, xh - back.y), __NV_SATFINITE, __NV_E4M3);
-      }
+      for (int e = 0; e < 4; ++e) pa_split<1>(w[e], up, hi[e], lo[e]);
       const uint32_t at = sw128_offset(row0 + 2 * k + half, part >> 1) + 8 * (part & 1);
       *reinterpret_cast<uint2*>(q_hi + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *reinterpret_cast<uint2*>(q_hi + pp::kQTermBytes + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      const float f = __uint_as_float((uint32_t)(E - 7 + 127) << 23) * a.scale_log2;   // 2^(E - 7) is exact
+      const float f = pa_factor(top, E, a.scale_log2);
       const float own = __shfl_sync(0xffffffffu, f, 16 * (lane & 1));
       if ((lane >> 1) == k) cf = own;
     }
@@ -390,6 +385,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   __shared__ PpSeg segs[kSegBufs];
   __shared__ uint64_t seg_full[kSegBufs], seg_empty[kSegBufs];
   __shared__ uint32_t tmem_base, bits_all;
+  __shared__ bool rec_open;                           // thread 0's: its record has not been written yet
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -417,14 +413,15 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     mbar_init(&mma_done, 3);
     prefetch_tmap(&k_map);
     bits_all = 0;
+    rec_open = true;
     fence_mbar_init();
   }
   if (warp == kOutWarp) {
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  pdl_wait();
-  if (tid == 0) reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;   // no piece to join until it has been written
+  // No pdl_wait() yet: the kernel before this one is of the same call, and began once the call's inputs were
+  // complete.  What waits for it to end is the first write (its pieces' join reads the workspace).
   const int B = a.num_requests;
   // block-wide inclusive sum of one value a thread
   auto block_sum = [&](int v) {
@@ -604,6 +601,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       ok = mbar_wait_warp(&seg_full[nx], ((seg + 1) / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
       if (segs[nx].n) cf = load_queries(segs[nx]);
+      if (seg == 0) {
+        pdl_wait();
+        if (tid == 0) {
+          reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;   // no piece to join until it has been written
+          rec_open = false;
+        }
+      }
       // ---- the segment's end
       const bool whole = s.n == s.tiles;
       ok = mbar_wait_warp(&o_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
@@ -964,6 +968,8 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     tmem_dealloc(tmem, kTmemCols);
   }
   if (tid == 0) {
+    pdl_wait();
+    if (rec_open) reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;
     a.err[kStatusCtaWords + cta] |= bits_all;          // beside what the first kernel reported
   }
 }
