@@ -91,6 +91,10 @@ struct __align__(16) PpSeg {
   int n, tile, h, qt;              // its tiles and the first of them (n = 0: no further segment)
   int b, tiles, slot, rows;        // the segment's tiles; where a piece goes
   int row0, len, start, prefix;    // as in PaShape and PpEntry
+
+  // Its t-th tile: the last keys come first.  A bias on distance makes scores grow towards a row's own position, and
+  // with them the reference, tile by tile in rising order (a fifth of such a call's time); in falling order it stands.
+  __device__ __forceinline__ int tile_at(int t) const { return tile + n - 1 - t; }
 };
 
 __device__ __forceinline__ int pp_limit(const PpSeg& s, int row) { return min(max(s.start + row + 1, s.prefix), s.len); }
@@ -542,11 +546,10 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       PpRow w = {-INFINITY, 0.f, cf, kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f, pp_limit(s, r), s.start + r};
       // keys below it are seen by every pair of this half
       const int min_limit = pp_limit(s, min(s.qt * kPromptPairs + kHalfPairs * q, s.rows * a.group - 1) / a.group);
-      const int tile0 = s.tile;
       // 64 keys of tile t.  The masked form is a separate body as a whole, not a variant of a part of it: with one
       // body and the scores' pass chosen inside it the unmasked tiles took 5,400 cycles instead of 3,400.
       auto keys64 = [&](auto masked, int t, int h, uint32_t bad) {
-        const int key0 = (tile0 + t) * kTok + 64 * h;
+        const int key0 = s.tile_at(t) * kTok + 64 * h;
         const float* ks = sks[i % kMetaBufs] + 4 * h;
         // moves the rows' references where their scores ask for it; true where some did
         auto raise = [&](float top) {
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[q][h]);
       };
       for (int t = 0; t < tiles && ok; ++t, ++i) {
-        const int key_end = (tile0 + t + 1) * kTok;
+        const int key_end = (s.tile_at(t) + 1) * kTok;
 #pragma unroll 1
         for (int h = 0; h < 2 && ok; ++h) {
           // the scores' arrival also stands for the tile's scales: K's own barrier may be a phase further by now
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       int t = (i0 + grp) & 1;
       // lane g (and g + 8, ..): the page of 16-key group g, of the tile to load and of this group's next one
       const int own = 16 * (lane & 7);
-      int id = id_of((s.tile + t) * kTok + own), id2 = id_of((s.tile + t + 2) * kTok + own);
+      int id = t < s.n ? id_of(s.tile_at(t) * kTok + own) : -1, id2 = t + 2 < s.n ? id_of(s.tile_at(t + 2) * kTok + own) : -1;
       auto load = [&](int key0) {
         scale = id >= 0 ? a.v_scales[(int64_t)id * a.kv_heads + s.h] : 0.f;
 #pragma unroll
@@ -737,9 +740,9 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             x[g] = __ldg(reinterpret_cast<const uint4*>(base + page * page_step + (key & ((1 << lp) - 1)) * kKvDim));
         }
       };
-      if (t < s.n) load((s.tile + t) * kTok);
+      if (t < s.n) load(s.tile_at(t) * kTok);
       for (; t < s.n; t += 2) {
-        const int key0 = (s.tile + t) * kTok, i = i0 + t;
+        const int key0 = s.tile_at(t) * kTok, i = i0 + t;
         if (i >= 2) ok = mbar_wait_warp(&v_empty[grp], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         // NaN codes of a tile that only some rows see in full
@@ -786,8 +789,8 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (lane == 0) mbar_arrive(&v_full[grp]);
         if (t + 2 < s.n) {
           id = id2;
-          id2 = id_of(key0 + 4 * kTok + own);
-          load(key0 + 2 * kTok);
+          id2 = t + 4 < s.n ? id_of(key0 - 4 * kTok + own) : -1;
+          load(key0 - 2 * kTok);
         }
       }
       if (!ok) break;
@@ -921,7 +924,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         int batch = -1, page = -1;                     // 32 pages at a time, one a lane
         float ks = 0.f;
         for (int t = 0; t < s.n; ++t, ++i) {
-          const int p0 = (s.tile + t) * ppt;
+          const int p0 = s.tile_at(t) * ppt;
           if ((p0 >> 5) != batch) {
             batch = p0 >> 5;
             const int p = 32 * batch + lane;
@@ -929,7 +932,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             if (p < pages) {
               page = a.block_table[(int64_t)s.b * a.table_stride + p];
               if (page < 0 || page >= a.num_pages) {
-                if (p >= p0 && p < (s.tile + s.n) * ppt) atomicOr(err, kErrBadPage);
+                if (p >= s.tile * ppt && p < p0 + ppt) atomicOr(err, kErrBadPage);
                 page = -1;
               }
             }

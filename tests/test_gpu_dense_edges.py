@@ -142,6 +142,19 @@ def test_visible_positions_without_a_page_are_skipped_and_reported(shape):
         attend(case)
 
 
+@pytest.mark.parametrize("shape", [([700, 300], [1, 2], 32, 2, 8), ([700, 300], [20, 30], 32, 2, 8)], ids=["decode", "prompt"])
+@pytest.mark.parametrize("gone", ["first", "last", "middle"])
+def test_whole_tiles_without_a_page_before_keys_that_score_low(shape, gone):
+    case = DenseCase(20, *shape)
+    P = case.P
+    lo, hi = {"first": (0, 256), "last": (384, 700), "middle": (128, 640)}[gone]
+    case.table[0, -(-lo // P):hi // P + 1] = -1
+    case.table[1, :4] = -1
+    slopes = np.full(case.heads, 2.0, np.float32)            # keys 100 away score -200 and less
+    got, lse = attend(case, check=False, slopes=slopes)
+    check_attention(got, lse, case.oracle(slopes=slopes), reach=2.0 * 700)
+
+
 @pytest.mark.parametrize("shape", [DECODE, PROMPT], ids=["decode", "prompt"])
 def test_a_request_longer_than_its_table_row_is_read_as_far_as_it_goes(shape):
     import deepseek_sparse_mla_gb300 as dsa
