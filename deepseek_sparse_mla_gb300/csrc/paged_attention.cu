@@ -101,7 +101,7 @@ __device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_
   s.tiles = sh.tiles;
   const int64_t in = u - (int64_t)first * a.kv_heads;
   const int per_head = end[lo] - first;
-  s.h = (int)(in / per_head);
+  s.h = in < (int64_t(1) << 31) ? (int)((uint32_t)in / (uint32_t)per_head) : (int)(in / per_head);
   const int rest = (int)(in - (int64_t)s.h * per_head);
   s.cg = rest / sh.tiles;
   s.tile = rest - s.cg * sh.tiles;
@@ -373,58 +373,63 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     if (leader) mma_commit(&mma_done);
     mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
   } else {
-    // ---------------------------------------------------------------- queries: 16 threads a column
-    const int part = lane & 15;
+    // ---------------------------------------------------------------- queries
     int seg = 0;
     for (int64_t u = u0; u < u1; ++seg) {
       const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
       const int buf = seg % kQBufs;
+      // first what a lane knows of a column of its own (columns without a pair are left as they are: nothing reads them)
+      const int live = min(s.rows * a.group - s.cg * kCE, kCE);
+      const int n = s.cg * kCE + min(lane, live - 1), i = n / a.group, head = s.h * a.group + (n - i * a.group);
+      const int64_t from = (int64_t)(s.row0 + i) * a.q_stride + (int64_t)head * kKvDim;
+      const int start = a.seq_lens[s.b] - s.rows;      // position of row 0
+      const int prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
+      const float slope = kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f;
       if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       uint8_t* q_hi = sQ + buf * kQBytes;
       PaColumns& cm = cols[buf];
-      const int pairs = s.rows * a.group, prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
-      const int start = a.seq_lens[s.b] - s.rows;     // position of row 0
-      int low = INT32_MAX;
-      // Two columns a step, a half-warp each, with the next two on their way: a rolled loop, as code that a CTA
-      // runs once or twice costs its way from L2.  Columns without a pair are left as they are: nothing reads them.
-      const int live = min(pairs - s.cg * kCE, kCE);
+      // then the values, 16 lanes a column: four columns a step, the next four on their way; a rolled loop, as code that a
+      // CTA runs once or twice costs its way from L2
+      const int part = lane & 15, half = lane >> 4;
       auto load = [&](int c) {
-        const int n = s.cg * kCE + c;
-        if (c >= live) return make_uint4(0, 0, 0, 0);
-        const int i = n / a.group, g = n - i * a.group;
-        return *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (s.h * a.group + g) * kKvDim + 8 * part);
+        const int64_t at = __shfl_sync(0xffffffffu, from, c & 31);
+        return c < live ? *reinterpret_cast<const uint4*>(a.q + at + 8 * part) : make_uint4(0, 0, 0, 0);
       };
-      uint4 x = load(lane >> 4), next = load(2 + (lane >> 4));
+      uint4 x[2] = {load(half), load(2 + half)};
+      const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
+      if (lane < live) {
+        cm.limit[lane] = limit;
+        cm.pos[lane] = (float)pos;
+        cm.at[lane] = (s.row0 + i) * a.kv_heads * a.group + head;
+        cm.slope[lane] = slope;
+      }
+      int low = limit;                                 // (lanes without a column hold the last one's)
 #pragma unroll 1
-      for (int c0 = 0; c0 < live; c0 += 2) {
-        const int c = c0 + (lane >> 4), n = s.cg * kCE + c;
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        x = next;
-        next = load(c + 4);
-        // the largest |x| as bf16 bits
-        uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-        top = max(top & 0xFFFFu, top >> 16);
+      for (int c0 = 0; c0 < live; c0 += 4) {
+        const uint4 y[2] = {x[0], x[1]};
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int E = pa_exponent(top);
-        const __nv_bfloat162 up = pa_up(E);
-        uint32_t hi[4], lo[4];
+        for (int k = 0; k < 2; ++k) x[k] = load(c0 + 4 + 2 * k + half);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pa_split<16>(w[e], up, hi[e], lo[e]);
-        if (c >= live) continue;
-        const uint32_t at = (((part >> 1) ^ (c & 7)) << 4) + 8 * (part & 1);
-        *reinterpret_cast<uint2*>(q_hi + c * kKvDim + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-        *reinterpret_cast<uint2*>(q_hi + (kHalf + c) * kKvDim + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-        const int i = n / a.group;
-        const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
-        low = min(low, limit);
-        if (part == 0) {
-          cm.factor[c] = pa_factor(top, E, a.scale_log2);
-          cm.limit[c] = limit;
-          cm.pos[c] = (float)pos;
-          cm.at[c] = (s.row0 + i) * a.kv_heads * a.group + s.h * a.group + (n - i * a.group);
-          cm.slope[c] = kMods && a.slopes ? a.slopes[s.h * a.group + (n - i * a.group)] * 1.4426950408889634f : 0.f;
+        for (int k = 0; k < 2; ++k) {
+          const int c = c0 + 2 * k + half;
+          const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+          // the largest |x| as bf16 bits
+          uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+          top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int E = pa_exponent(top);
+          const __nv_bfloat162 up = pa_up(E);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pa_split<16>(w[e], up, hi[e], lo[e]);
+          if (c < live) {
+            const uint32_t at = (((part >> 1) ^ (c & 7)) << 4) + 8 * (part & 1);
+            *reinterpret_cast<uint2*>(q_hi + c * kKvDim + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(q_hi + (kHalf + c) * kKvDim + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if (part == 0) cm.factor[c] = pa_factor(top, E, a.scale_log2);
+          }
         }
       }
       low = __reduce_min_sync(0xffffffffu, low);
@@ -510,44 +515,62 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             }
           }
         }
+        // the scores of c1 columns from what their products left
+        auto finish = [&](auto& z, const uint32_t* hi, const uint32_t* lo, int c0, int c1) {
+          // a loop each: a choice made inside one of them would leave the values no instructions to overlap with
+#pragma unroll
+          for (int c = 0; c < c1; ++c) z[c] = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
+          if (kMods && in != 0.f) {
+#pragma unroll
+            for (int c = 0; c < c1; ++c) z[c] = capped(z[c] * in, a.cap_log2);
+          }
+          if (kMods) {
+#pragma unroll
+            for (int c = 0; c < c1; ++c) z[c] = fmaf(-cm.slope[c0 + c], fabsf(cm.pos[c0 + c] - (float)j), z[c]);
+          }
+          if (kMasked) {
+#pragma unroll
+            for (int c = 0; c < c1; ++c)
+              if (!exists || j >= cm.limit[c0 + c]) z[c] = -INFINITY;
+          }
+        };
+        auto scores8 = [&](float (&z)[8], int c0) {
+          uint32_t hi[8], lo[8];
+          tmem_ld_cols8(tmem + lanes + 64 * sb + c0, hi);
+          tmem_ld_cols8(tmem + lanes + 64 * sb + kHalf + c0, lo);
+          tmem_wait_ld();
+          finish(z, hi, lo, c0, 8);
+        };
         auto scores = [&](float (&z)[kNC]) {
+          constexpr int kC = kNC < 16 ? kNC : 16;      // columns at a time
 #pragma unroll
-          for (int c0 = 0; c0 < kNC; c0 += 16) {
-            uint32_t hi[16], lo[16];
+          for (int c0 = 0; c0 < kNC; c0 += kC) {
+            uint32_t hi[kC], lo[kC];
 #pragma unroll
-            for (int c = 0; c < 16 && c0 + c < kNC; c += 8) {
+            for (int c = 0; c < kC; c += 8) {
               tmem_ld_cols8(tmem + lanes + 64 * sb + c0 + c, hi + c);
               tmem_ld_cols8(tmem + lanes + 64 * sb + kHalf + c0 + c, lo + c);
             }
             tmem_wait_ld();
-            // a loop each: a choice made inside one of them would leave the values no instructions to overlap with
+            float y[kC];
+            finish(y, hi, lo, c0, kC);
 #pragma unroll
-            for (int c = 0; c < 16 && c0 + c < kNC; ++c)
-              z[c0 + c] = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
-            if (kMods && in != 0.f) {
-#pragma unroll
-              for (int c = 0; c < 16 && c0 + c < kNC; ++c) z[c0 + c] = capped(z[c0 + c] * in, a.cap_log2);
-            }
-            if (kMods) {
-#pragma unroll
-              for (int c = 0; c < 16 && c0 + c < kNC; ++c)
-                z[c0 + c] = fmaf(-cm.slope[c0 + c], fabsf(cm.pos[c0 + c] - (float)j), z[c0 + c]);
-            }
-            if (kMasked) {
-#pragma unroll
-              for (int c = 0; c < 16 && c0 + c < kNC; ++c)
-                if (!exists || j >= cm.limit[c0 + c]) z[c0 + c] = -INFINITY;
-            }
+            for (int c = 0; c < kC; ++c) z[c0 + c] = y[c];
           }
         };
         // the exact maxima over the tile, where the references do not hold: they, and what was formed against them, move
         auto raise = [&]() {
-          float z[kNC], mine = -INFINITY;
-          scores(z);
+          // rolled: it runs for a segment's first tile, where a second copy of all columns' scores would have to come from L2
+          float mine = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kNC; c0 += 8) {
+            float z[8];
+            scores8(z, c0);
 #pragma unroll
-          for (int c = 0; c < kNC; ++c) {
-            const float r = warp_max_f32(z[c]);
-            if (lane == c) mine = r;                   // lane c of every warp ends up with column c's
+            for (int c = 0; c < 8; ++c) {
+              const float r = warp_max_f32(z[c]);
+              if (lane == c0 + c) mine = r;            // lane c of every warp ends up with column c's
+            }
           }
           // held at -118: 4 * kPOne * 2^(m - mv) stays finite for pages whose scales are smaller, or 0
           const float lv_max = warp_max_f32(fmaxf(__log2f(fabsf(vs)), -118.f));

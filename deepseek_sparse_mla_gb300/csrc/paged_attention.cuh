@@ -20,6 +20,7 @@ struct PaShape {
 
 __device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, uint32_t& bits) {
   PaShape s = {0, b, 0, 0};
+  const int held = a.seq_lens[b];    // with the offsets, not after them: at the start every load is a trip to L2
   int n = 1;
   if (a.query_start_loc) {
     s.row0 = a.query_start_loc[b];
@@ -34,7 +35,7 @@ __device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, uint3
   const int64_t pairs = (int64_t)n * a.group;
   if (pairs <= a.lo_pairs || pairs > a.hi_pairs) return s;
   const int64_t room = (int64_t)a.table_stride << a.log2_page;
-  int64_t len = max(a.seq_lens[b], 0);
+  int64_t len = max(held, 0);
   if (len > room) {
     bits |= DSA_DEVICE_BAD_PAGE;
     len = room;

@@ -327,11 +327,12 @@ __device__ __forceinline__ void pp_shrink(uint32_t tO, float al) {
 // whole lines, two rows a step and four steps ahead; rolled, as it is run once a segment.
 __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg& s, int first, int pairs, uint8_t* q_hi, int row0) {
   const int lane = threadIdx.x & 31, part = lane & 15, half = lane >> 4;
+  // where the lane's own pair lies
+  const int own_n = min(first + lane, pairs - 1), own_i = own_n / a.group;
+  const int64_t from = (int64_t)(s.row0 + own_i) * a.q_stride + (int64_t)(s.h * a.group + own_n - own_i * a.group) * kKvDim;
   auto load = [&](int k) {
-    const int n = first + 2 * k + half;
-    if (k >= 16 || n >= pairs) return make_uint4(0, 0, 0, 0);
-    const int i = n / a.group, g = n - i * a.group;
-    return __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + i) * a.q_stride + (int64_t)(s.h * a.group + g) * kKvDim) + part);
+    const int64_t at = __shfl_sync(0xffffffffu, from, (2 * k + half) & 31);
+    return k < 16 && first + 2 * k + half < pairs ? __ldg(reinterpret_cast<const uint4*>(a.q + at) + part) : make_uint4(0, 0, 0, 0);
   };
   float cf = 0.f;
   uint4 x[4];
