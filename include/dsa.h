@@ -556,7 +556,7 @@ typedef struct {
  * grouped into calls, by roundings of codes below 2^-6 only.
  *   k, v      device bf16, token t's heads at k + t * k_stride (elements): [kv_heads, 128] contiguous,
  *             16-byte aligned, strides a multiple of 8 and at least kv_heads * 128.
- * A page that is written belongs to one request.  Out-of-range page ids are skipped.
+ * A page that is written belongs to one request and stands once in its table row.  Out-of-range page ids are skipped.
  */
 DSA_API dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride,
                                   const void* v, int64_t v_stride, void* stream);
@@ -598,7 +598,8 @@ typedef struct {
  * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), a contribution to the output 8
  * bits or more with one of 2^-20 of the largest contribution; requests of more rows hold V to 2^-25 of the
  * largest V scale of the request's pages.
- * DSA_ERR_UNSUPPORTED for more than DSA_MAX_REQUESTS requests, and for block-table rows of more than 2^30 tokens.
+ * DSA_ERR_UNSUPPORTED for more than DSA_MAX_REQUESTS requests, for block-table rows of more than 2^30 tokens, and where
+ * the table's tokens / 128 times max(2 * requests, rows * heads per K/V head / 256 + requests) exceeds 2^31.
  */
 DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q,
                                        int64_t q_stride, int32_t q_heads, float scale, int32_t max_query_len,

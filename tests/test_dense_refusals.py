@@ -73,7 +73,8 @@ def test_attention_rejects_bad_caches(lib, kw, status, word):
 
 
 @pytest.mark.parametrize("kw,status,word", BAD_BATCHES + [(dict(B=4097), UNSUPPORTED, "num_requests"),
-                                                          (dict(stride=(1 << 24) + 1), UNSUPPORTED, "2^30")])
+                                                          (dict(stride=(1 << 24) + 1), UNSUPPORTED, "2^30"),
+                                                          (dict(stride=1 << 24, B=4096, rows=4096), UNSUPPORTED, "2^31")])
 def test_attention_rejects_bad_batches(lib, kw, status, word):
     _said(lib, _attend(lib, batch=_batch(**kw)), status, word)
 

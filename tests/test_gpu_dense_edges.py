@@ -337,6 +337,30 @@ def test_two_captured_calls_replayed_over_changing_inputs(shape):
             q.copy_(wlm.bits_to_torch(c.q_bits, "cuda"))
 
 
+def test_calls_in_a_row_share_a_workspace():
+    """Few-row and many-row requests whose pieces are joined, call after call without a wait in between."""
+    import torch
+    import deepseek_sparse_mla_gb300 as dsa
+    cases = [DenseCase(22 + i, seq, new, 32, 2, 8) for i, (seq, new) in enumerate(
+        [([2300, 77, 1500], [1, 3, 60]), ([1200, 1900], [40, 2]), ([1700], [1]), ([1500], [70])])]
+    tensors = [c.gpu() for c in cases]
+    ws = torch.empty(dsa.paged_attention_workspace_bytes(16, 2, 70), dtype=torch.uint8, device="cuda")
+    outs = []
+    torch.cuda.synchronize()
+    for turn in range(12):
+        for c, (cache, batch, q) in zip(cases, tensors):
+            out = torch.full((c.rows, c.heads, 128), -7.0, dtype=torch.bfloat16, device="cuda")
+            lse = torch.full((c.rows, c.heads), -7.0, dtype=torch.float32, device="cuda")
+            dsa.paged_attention(cache, batch, q, max_query_len=int(c.q_lens.max()), out=out, lse=lse, workspace=ws)
+            outs.append((out, lse))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(outs):
+        first = outs[i % len(cases)]
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    for c, (out, lse) in zip(cases, outs):
+        check_attention(o.bf16_to_f64(wlm.torch_to_bits(out)), lse.cpu().numpy().astype(np.float64), c.oracle())
+
+
 @pytest.mark.parametrize("shape", [DECODE, PROMPT], ids=["decode", "prompt"])
 def test_pages_past_four_gigabytes(shape):
     """The case's pages at the end of a cache of more than 2^32 bytes of K and of V."""
