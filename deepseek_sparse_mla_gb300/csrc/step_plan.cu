@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
   int32_t* row_end = plan_smem + B;       // [B] admitted rows of requests 0 .. b
   int32_t* page_end = plan_smem + 2 * B;  // [B] admitted new pages of requests 0 .. b
   __shared__ int64_t part[32][2];
-  __shared__ unsigned long long total_rows, total_pages;
+  __shared__ uint32_t total_rows, total_pages;         // at most num_rows, and the count of free pages
   __shared__ uint32_t bits;
   const int tid = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
   if (tid == 0) {
@@ -108,9 +108,20 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
   const int64_t count = min(max(*a.free_count, 0), a.free_capacity);
   // each request's new rows and pages: none where its lengths do not make sense or its table row is too short
   uint32_t my_bits = 0;
-  for (int b = tid; b < B; b += kPlanThreads) {
-    const int64_t L = a.seq_lens[b];
-    int64_t n = a.new_lens[b], need = 0;
+  constexpr int kEach = kPlanMaxRequests / kPlanThreads;
+  int tokens[kEach], brings[kEach];                     // every load in flight before the first is used
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int b = tid + k * kPlanThreads;
+    tokens[k] = b < B ? a.seq_lens[b] : 0;
+    brings[k] = b < B ? a.new_lens[b] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int b = tid + k * kPlanThreads;
+    if (b >= B) break;
+    const int64_t L = tokens[k];
+    int64_t n = brings[k], need = 0;
     const int64_t pages = (L + n + P - 1) >> a.log2_page;
     if (L < 0 || n < 0 || L + n > INT32_MAX || (n > 0 && pages > a.table_stride)) {
       my_bits |= DSA_DEVICE_BAD_LENGTH;
@@ -146,11 +157,16 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
       my_bits |= row_sum > a.num_rows ? DSA_DEVICE_ROWS_FULL : DSA_DEVICE_POOL_EMPTY;
     }
   }
-  if (row_top) atomicMax(&total_rows, (unsigned long long)row_top);
-  if (page_top) atomicMax(&total_pages, (unsigned long long)page_top);
-  if (my_bits) atomicOr(&bits, my_bits);
+  // one atomic a warp: 1,024 of 64 bits took 8,900 cycles
+  const uint32_t warp_rows = __reduce_max_sync(0xffffffffu, (uint32_t)row_top), warp_pages = __reduce_max_sync(0xffffffffu, (uint32_t)page_top);
+  my_bits = __reduce_or_sync(0xffffffffu, my_bits);
+  if ((tid & 31) == 0) {
+    atomicMax(&total_rows, warp_rows);
+    atomicMax(&total_pages, warp_pages);
+    if (my_bits) atomicOr(&bits, my_bits);
+  }
   __syncthreads();
-  const int64_t R = (int64_t)total_rows, N = (int64_t)total_pages;
+  const int64_t R = total_rows, N = total_pages;
   // beyond the last admitted request the sums stay at their totals (they only grow from there)
   row_sum = row_first;
   page_sum = page_first;
@@ -185,30 +201,44 @@ __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepPlanA
     const int held = (int)(((int64_t)old_len[b] + P - 1) >> a.log2_page);
     a.block_table[(int64_t)b * a.table_stride + held + ((int)k - first)] = a.free_pages[count - 1 - k];
   }
-  // Each warp takes a run of consecutive rows, 128 at a time (four a lane, their page ids in flight together): one
-  // search finds the request of the first, and the others' are looked for from there on.
+  // Each warp takes a run of consecutive rows, 128 at a time (four a lane, their page ids in flight together): the
+  // requests of the first and the last bound the others', which are searched for side by side.
   const int warps = ctas * (kPlanThreads / 32), lane = tid & 31;
   const int64_t run = ((a.num_rows + warps - 1) / warps + 31) / 32 * 32;
   const int64_t run0 = run * (rank * (kPlanThreads / 32) + (tid >> 5)), run1 = min((int64_t)a.num_rows, run0 + run);
-  int near = run0 < R ? request_of(row_end, B, (int)run0) : 0;
+  int low = run0 < R ? request_of(row_end, B, (int)run0) : 0;
   for (int64_t r0 = run0; r0 < run1; r0 += 128) {
-    int page[4], pos[4];
+    int page[4], pos[4], of[4], high[4];
+    const int64_t end = min(min(r0 + 128, run1), R);   // the rows that requests have
+    const int top = end > r0 ? request_from(row_end, B, low, (int)end - 1) : low;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      of[k] = low;
+      high[k] = top;
+    }
+    for (int w = top - low; w > 0; w >>= 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int mid = (of[k] + high[k]) >> 1;
+        if (row_end[mid] > r0 + 32 * k + lane) high[k] = mid;
+        else of[k] = min(mid + 1, top);
+      }
+    }
+    low = top;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t r = r0 + 32 * k + lane;
       page[k] = -1;
       pos[k] = -1;
-      if (r < R && r < run1) {
-        const int b = request_from(row_end, B, near, (int)r);
+      if (r < end) {
+        const int b = of[k];
         const int first = b ? row_end[b - 1] : 0, page_first_b = b ? page_end[b - 1] : 0;
         pos[k] = old_len[b] + ((int)r - first);
         const int held = (int)(((int64_t)old_len[b] + P - 1) >> a.log2_page), lp = pos[k] >> a.log2_page;
         // a page that this call hands out is read from the stack: another thread writes its table entry
         page[k] = lp < held ? a.block_table[(int64_t)b * a.table_stride + lp]
                             : a.free_pages[count - 1 - (page_first_b + (lp - held))];
-        near = b;
       }
-      near = __shfl_sync(0xffffffffu, near, 0);          // the first lane's row is the lowest
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
