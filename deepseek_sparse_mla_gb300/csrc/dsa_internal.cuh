@@ -282,7 +282,7 @@ constexpr int kPagedAttnDirect = 64;      // requests of more pairs go to the pr
 constexpr int kPromptPairs = 256;         // pairs that it takes together
 struct PagedAttnPlan {
   bool prompt;                            // a request may bring more than kPagedAttnDirect pairs
-  size_t rec_offset, part_offset, workspace_bytes;
+  size_t rec_offset, part_offset, prompt_rec_offset, prompt_part_offset, workspace_bytes;
 };
 PagedAttnPlan plan_paged_attention(int max_query_len, int group);
 cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_seq_len,

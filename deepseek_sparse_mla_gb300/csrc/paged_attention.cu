@@ -198,6 +198,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
+  // The prompt kernel may start as SMs fall free (mixed batch 107 -> 98 us in a replayed graph).  A join may not: its CTAs
+  // coming early cost 32 requests at 8K 2 us.
+  if (a.hi_pairs != INT32_MAX) pdl_trigger();
   if (tid == 0) reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;   // no piece to join until it has been written
   // running sums of the requests' units: every thread a run of consecutive requests
   {
@@ -798,67 +801,11 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   }
 }
 
-// Joins the pieces of the segments that CTA boundaries cut:
-//   out = sum_p w_p O_p,  w_p = 2^{m_p - M} / L,  L = sum_p 2^{m_p - M} l_p.
-// CTA (c - 1, g) handles the boundary in front of range c if it is the first that cuts its segment, and
-// columns 8 g .. 8 g + 7: a warp a column, four dims a lane.
+// Joins the pieces of segments that were cut, where no request may have so many rows that the other kernel runs too
 __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x + 1;
   pdl_wait();
   pdl_trigger();
-  const PaRecord rec = pa_load_record(a, c);
-  int first, last, first_slot;
-  if (!pa_pieces(rec, c, ctas, first, last, first_slot)) return;
-  const int col = 8 * blockIdx.y + warp, n = rec.first_pair + col;
-  if (n >= rec.pairs) return;
-  const int64_t units = rec.units;
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kGroup = 4;                               // pieces whose loads are in flight together
-  for (int p0 = first; p0 <= last; p0 += kGroup) {
-    float mj[kGroup], lj[kGroup];
-    float4 x[kGroup];
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      const int p = p0 + g;
-      mj[g] = -INFINITY;
-      lj[g] = 0.f;
-      x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p <= last && (units >= ctas || pa_unit_start(p, units, ctas) < pa_unit_start(p + 1, units, ctas))) {
-        const int64_t at = (int64_t)(p == first ? first_slot : 2 * p) * kPagedAttnColumns + col;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
-        mj[g] = ml.x;
-        lj[g] = ml.y;
-        x[g] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kKvDim) + lane);
-      }
-    }
-    float Mn = M;
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) Mn = fmaxf(Mn, mj[g]);
-    const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn);
-    L *= sc;
-    acc.x *= sc;
-    acc.y *= sc;
-    acc.z *= sc;
-    acc.w *= sc;
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      const float w = lj[g] == 0.f ? 0.f : exp2f(mj[g] - Mn);
-      L = fmaf(w, lj[g], L);
-      acc.x = fmaf(w, x[g].x, acc.x);
-      acc.y = fmaf(w, x[g].y, acc.y);
-      acc.z = fmaf(w, x[g].z, acc.z);
-      acc.w = fmaf(w, x[g].w, acc.w);
-    }
-    M = Mn;
-  }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int i = n / a.group;
-  const int64_t at = (int64_t)(rec.row0 + i) * a.kv_heads * a.group + rec.h * a.group + (n - i * a.group);
-  const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), v1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(a.out + at * kKvDim)[lane] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
-  if (a.lse && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+  pa_join(a, ctas, blockIdx.x + 1, blockIdx.y);
 }
 
 // ---------------------------------------------------------------------------
@@ -869,15 +816,20 @@ PagedAttnPlan plan_paged_attention(int max_query_len, int group) {
   const int ctas = device_sm_count();
   p.prompt = (int64_t)max_query_len * group > kPagedAttnDirect;
   p.rec_offset = kWorkspaceHeader + ((size_t)ctas * sizeof(uint32_t) + 255) / 256 * 256;
-  p.part_offset = p.rec_offset + ((size_t)ctas * 8 * sizeof(int32_t) + 255) / 256 * 256;
-  p.workspace_bytes =
-      p.part_offset + (size_t)2 * ctas * (p.prompt ? kPromptPairs : kPagedAttnColumns) * (kKvDim + 2) * sizeof(float);
+  // each kernel's records and pieces: one launch joins both kernels'
+  const size_t recs = ((size_t)ctas * sizeof(PaRecord) + 255) / 256 * 256, few = (size_t)2 * ctas * kPagedAttnColumns * (kKvDim + 2);
+  const size_t many = p.prompt ? (size_t)2 * ctas * kPromptPairs * (kKvDim + 2) : 0;
+  p.prompt_rec_offset = p.rec_offset + recs;
+  p.part_offset = p.prompt_rec_offset + (p.prompt ? recs : 0);
+  p.prompt_part_offset = p.part_offset + few * sizeof(float);
+  p.workspace_bytes = p.prompt_part_offset + many * sizeof(float);
   return p;
 }
 
 namespace {
 template <int kCE>
-cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int ctas, cudaStream_t s) {
+cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int ctas, bool join,
+                           cudaStream_t s) {
   const size_t smem = pa::kFixedSmem + (size_t)a.num_requests * sizeof(int32_t);
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = once_per_device(ready, [] {
@@ -893,7 +845,7 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
   e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, shared_keys);
   count_launches(1);
   if (e != cudaSuccess) return e;
-  if (ctas > 1 && !a.whole) {
+  if (ctas > 1 && !a.whole && join) {
     e = launch_pdl(paged_attention_join_kernel, dim3(ctas - 1, kCE / 8), dim3(256), 0, s, a, ctas);
     count_launches(1);
   }
@@ -920,14 +872,17 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, cons
       !encode_2d(&v_map, v_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kKvDim, rows, kKvDim, kKvDim, 1u << a.log2_page))
     return cudaErrorInvalidValue;
   const int64_t pairs = (int64_t)a.max_rows * a.group;
-  cudaError_t e = pairs <= 8    ? launch_columns<8>(a, k_map, v_map, ctas, s)
-                  : pairs <= 16 ? launch_columns<16>(a, k_map, v_map, ctas, s)
-                                : launch_columns<32>(a, k_map, v_map, ctas, s);
+  cudaError_t e = pairs <= 8    ? launch_columns<8>(a, k_map, v_map, ctas, !plan.prompt, s)
+                  : pairs <= 16 ? launch_columns<16>(a, k_map, v_map, ctas, !plan.prompt, s)
+                                : launch_columns<32>(a, k_map, v_map, ctas, !plan.prompt, s);
   if (e == cudaSuccess && plan.prompt) {
-    a.lo_pairs = kPagedAttnDirect;
-    a.hi_pairs = INT32_MAX;
-    a.part_ml = a.part_o + (size_t)2 * ctas * kPromptPairs * kKvDim;
-    e = launch_paged_prompt(a, k_map, v_codes, ctas, s);
+    PagedAttnArgs many = a;
+    many.lo_pairs = kPagedAttnDirect;
+    many.hi_pairs = INT32_MAX;
+    many.rec = reinterpret_cast<int32_t*>(ws + plan.prompt_rec_offset);
+    many.part_o = reinterpret_cast<float*>(ws + plan.prompt_part_offset);
+    many.part_ml = many.part_o + (size_t)2 * ctas * kPromptPairs * kKvDim;
+    e = launch_paged_prompt(many, a, kPagedAttnColumns / 8, k_map, v_codes, ctas, s);   // more than 64 pairs: 32 columns above
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }

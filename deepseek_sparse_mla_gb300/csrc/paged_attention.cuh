@@ -72,9 +72,10 @@ __device__ __forceinline__ float pa_factor(uint32_t top, int E, float scale) {
   return top >= 0x7F80u ? __int_as_float(0x7FC00000) : __uint_as_float((uint32_t)(E - 7 + 127) << 23) * scale;
 }
 
-// Requests of many rows (paged_prompt.cu); k_map: the K codes in boxes of a page.
-cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, const uint8_t* v_codes, int ctas,
-                                cudaStream_t s);
+// Requests of many rows (paged_prompt.cu), and the join of both kernels' pieces (few: the first kernel's arguments, few_y
+// groups of 8 columns); k_map: the K codes in boxes of a page.
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
+                                const uint8_t* v_codes, int ctas, cudaStream_t s);
 
 // A capped score: cap * tanh(z / cap) = cap * (1 - 2 / (1 + 2^y)), y = 2 log2(e) / cap * z, all in log2 units.  Exact
 // to about 2^-21 of the cap; past the range of 2^y the quotient is 0 or 2, and NaN stays.
@@ -134,6 +135,67 @@ __device__ __forceinline__ bool pa_pieces(const PaRecord& r, int c, int ctas, in
   last = pa_cta_of_unit(seg + r.tiles - 1, r.units, ctas);
   first_slot = at == seg ? 2 * first : 2 * first + 1;
   return true;
+}
+
+// Joins the pieces of the segments that CTA boundaries cut:
+//   out = sum_p w_p O_p,  w_p = 2^{m_p - M} / L,  L = sum_p 2^{m_p - M} l_p.
+// A block (c, y) handles the boundary in front of range c if it is the first that cuts its segment, and
+// columns 8 y .. 8 y + 7: a warp a column, four dims a lane.
+__device__ __forceinline__ void pa_join(const PagedAttnArgs& a, int ctas, int c, int y) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PaRecord rec = pa_load_record(a, c);
+  int first, last, first_slot;
+  if (!pa_pieces(rec, c, ctas, first, last, first_slot)) return;
+  const int col = 8 * y + warp, n = rec.first_pair + col;
+  if (n >= rec.pairs) return;
+  const int64_t units = rec.units;
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kGroup = 4;                               // pieces whose loads are in flight together
+  for (int p0 = first; p0 <= last; p0 += kGroup) {
+    float mj[kGroup], lj[kGroup];
+    float4 x[kGroup];
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const int p = p0 + g;
+      mj[g] = -INFINITY;
+      lj[g] = 0.f;
+      x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p <= last && (units >= ctas || pa_unit_start(p, units, ctas) < pa_unit_start(p + 1, units, ctas))) {
+        const int64_t at = (int64_t)(p == first ? first_slot : 2 * p) * kPagedAttnColumns + col;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
+        mj[g] = ml.x;
+        lj[g] = ml.y;
+        x[g] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kKvDim) + lane);
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) Mn = fmaxf(Mn, mj[g]);
+    const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn);
+    L *= sc;
+    acc.x *= sc;
+    acc.y *= sc;
+    acc.z *= sc;
+    acc.w *= sc;
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const float w = lj[g] == 0.f ? 0.f : exp2f(mj[g] - Mn);
+      L = fmaf(w, lj[g], L);
+      acc.x = fmaf(w, x[g].x, acc.x);
+      acc.y = fmaf(w, x[g].y, acc.y);
+      acc.z = fmaf(w, x[g].z, acc.z);
+      acc.w = fmaf(w, x[g].w, acc.w);
+    }
+    M = Mn;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int i = n / a.group;
+  const int64_t at = (int64_t)(rec.row0 + i) * a.kv_heads * a.group + rec.h * a.group + (n - i * a.group);
+  const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), v1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(a.out + at * kKvDim)[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+  if (a.lse && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
 }  // namespace dsa

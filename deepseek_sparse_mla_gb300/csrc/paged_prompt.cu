@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     tmem_alloc(&tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  // No pdl_wait() yet: the kernel before this one is of the same call, and began once the call's inputs were
-  // complete.  What waits for it to end is the first write (its pieces' join reads the workspace).
+  // No pdl_wait() yet: the kernel before this one is of the same call and lets this one start only once the call's inputs
+  // are complete.  The first write waits for its end, so that this grid's end stands for both.
   const int B = a.num_requests;
   // block-wide inclusive sum of one value a thread
   auto block_sum = [&](int v) {
@@ -978,12 +978,8 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   }
 }
 
-// Joins the pieces of the segments that CTA boundaries cut, as paged_attention_join_kernel: a thread a pair, 16 dims
-// of it per blockIdx.y.
-__global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x + 1;
+// Joins the pieces of the segments that CTA boundaries cut, as pa_join: a thread a pair, 16 dims of it per y.
+__device__ __forceinline__ void pp_join(const PagedAttnArgs& a, int ctas, int c, int y) {
   const PaRecord rec = pa_load_record(a, c);
   int first, last, first_slot;
   if (!pa_pieces(rec, c, ctas, first, last, first_slot)) return;
@@ -1007,7 +1003,7 @@ __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const _
         ml[g] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * kPromptPairs + threadIdx.x);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          x[g][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (kKvDim / 4) + 4 * blockIdx.y + k) * kPromptPairs + threadIdx.x);
+          x[g][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (kKvDim / 4) + 4 * y + k) * kPromptPairs + threadIdx.x);
       }
     }
 #pragma unroll
@@ -1033,14 +1029,25 @@ __global__ void __launch_bounds__(kPromptPairs) paged_prompt_join_kernel(const _
   __nv_bfloat162* xo = reinterpret_cast<__nv_bfloat162*>(v);
 #pragma unroll
   for (int e = 0; e < 8; ++e) xo[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  uint4* dst = reinterpret_cast<uint4*>(a.out + at * kKvDim) + 2 * blockIdx.y;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + at * kKvDim) + 2 * y;
   dst[0] = v[0];
   dst[1] = v[1];
-  if (a.lse && blockIdx.y == 0) a.lse[at] = L == 0.f ? -INFINITY : (M - pp::kPLog2 + log2f(L)) * 0.69314718055994530942f;
+  if (a.lse && y == 0) a.lse[at] = L == 0.f ? -INFINITY : (M - pp::kPLog2 + log2f(L)) * 0.69314718055994530942f;
 }
 
-cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, const uint8_t* v_codes, int ctas,
-                                cudaStream_t s) {
+// Both kernels' joins in one launch, so that nothing stands between the two kernels
+__global__ void __launch_bounds__(kPromptPairs)
+    paged_prompt_join_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ PagedAttnArgs few, int few_y, int ctas) {
+  static_assert(kPromptPairs == 256, "pa_join's block");
+  pdl_wait();
+  pdl_trigger();
+  const int y = blockIdx.y;
+  if (y < few_y) pa_join(few, ctas, blockIdx.x + 1, y);
+  else pp_join(a, ctas, blockIdx.x + 1, y - few_y);
+}
+
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
+                                const uint8_t* v_codes, int ctas, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = once_per_device(ready, [] {
     const int most = pp::kFixedSmem;
@@ -1054,7 +1061,7 @@ cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (ctas > 1 && !a.whole) {
-    e = launch_pdl(paged_prompt_join_kernel, dim3(ctas - 1, kKvDim / 16), dim3(kPromptPairs), 0, s, a, ctas);
+    e = launch_pdl(paged_prompt_join_kernel, dim3(ctas - 1, few_y + kKvDim / 16), dim3(kPromptPairs), 0, s, a, few, few_y, ctas);
     count_launches(1);
   }
   return e;
