@@ -648,6 +648,6 @@ def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM 
     _lib.check(_lib.load().dsa_paged_attention(
         ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), q.data_ptr(), q_stride, heads, float(scale), max_query_len,
         mods, out.data_ptr(), None if lse is None else lse.data_ptr(), *_workspace_args(workspace), _raw_stream(dev.index)))
-    if check:
+    if check and R:                                   # without rows nothing ran, and the workspace holds what it held
         _check_device(workspace, None)
     return out, lse

@@ -591,6 +591,7 @@ typedef struct {
  *   out        device bf16 [num_rows, q_heads, 128]; lse fp32 [num_rows, q_heads] or NULL.
  *   workspace  dsa_paged_attention_workspace_bytes(), 256-byte aligned; calls that may run at the same
  *              time take one each.
+ * Without rows nothing is launched, and the workspace (its status, too) stays as it was.
  * A row that sees nothing (an empty request) gets zeros and an lse of -inf.  Rows behind the last request's
  * are left as they were.  What lies in the cache behind a request's tokens is never used, NaN codes included.
  * A visible position without a valid page is skipped and reported (DSA_DEVICE_BAD_PAGE).

@@ -393,6 +393,24 @@ def test_pages_past_four_gigabytes(shape):
         assert not torch.any(a[:first] != a[0]).item()
 
 
+def test_calls_without_rows():
+    import torch
+    import deepseek_sparse_mla_gb300 as dsa
+    case = DenseCase(26, [50, 0], [0, 0], 16, 2, 2, extra_rows=1)
+    cache, batch, q = case.gpu()
+    got, lse = attend(case, (cache, batch, q), longest=40)   # a padded row only: it is left alone, and nothing is wrong
+    assert np.all(got == -7.0) and np.all(lse == -7.0)
+    none = dsa.Batch(batch.block_table, batch.seq_lens, batch.query_start_loc, num_rows=0, max_seq_len=50)
+    ws = torch.full((dsa.paged_attention_workspace_bytes(4, 2, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    out, _ = dsa.paged_attention(cache, none, q[:0], workspace=ws, check=True)
+    assert out.shape == (0, 4, 128)
+    kv = wlm.bits_to_torch(case.new["k"], "cuda")[:0]
+    before = cache.k_codes.clone()
+    dsa.kv8_append(cache, none, kv, kv)
+    torch.cuda.synchronize()
+    assert torch.equal(before, cache.k_codes)
+
+
 def test_refusals():
     import torch
     import deepseek_sparse_mla_gb300 as dsa
