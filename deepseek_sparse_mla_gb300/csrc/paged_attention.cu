@@ -392,14 +392,16 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       uint8_t* q_hi = sQ + buf * kQBytes;
       PaColumns& cm = cols[buf];
-      // then the values, 16 lanes a column: four columns a step, the next four on their way; a rolled loop, as code that a
+      // then the values, 16 lanes a column: eight columns a step, the next eight on their way; a rolled loop, as code that a
       // CTA runs once or twice costs its way from L2
       const int part = lane & 15, half = lane >> 4;
       auto load = [&](int c) {
         const int64_t at = __shfl_sync(0xffffffffu, from, c & 31);
         return c < live ? *reinterpret_cast<const uint4*>(a.q + at + 8 * part) : make_uint4(0, 0, 0, 0);
       };
-      uint4 x[2] = {load(half), load(2 + half)};
+      uint4 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = load(2 * k + half);
       const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
       if (lane < live) {
         cm.limit[lane] = limit;
@@ -409,19 +411,27 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       }
       int low = limit;                                 // (lanes without a column hold the last one's)
 #pragma unroll 1
-      for (int c0 = 0; c0 < live; c0 += 4) {
-        const uint4 y[2] = {x[0], x[1]};
+      for (int c0 = 0; c0 < live; c0 += 8) {
+        uint4 y[4];
+        uint32_t tops[4];                              // the largest |x| of each column as bf16 bits, side by side
 #pragma unroll
-        for (int k = 0; k < 2; ++k) x[k] = load(c0 + 4 + 2 * k + half);
+        for (int k = 0; k < 4; ++k) {
+          y[k] = x[k];
+          const uint32_t m = __vmaxu2(__vmaxu2(y[k].x & 0x7FFF7FFFu, y[k].y & 0x7FFF7FFFu), __vmaxu2(y[k].z & 0x7FFF7FFFu, y[k].w & 0x7FFF7FFFu));
+          tops[k] = max(m & 0xFFFFu, m >> 16);
+        }
+        if (c0 + 8 < live) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 4; ++k) x[k] = load(c0 + 8 + 2 * k + half);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tops[k] = max(tops[k], __shfl_xor_sync(0xffffffffu, tops[k], o));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
           const int c = c0 + 2 * k + half;
-          const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
-          // the largest |x| as bf16 bits
-          uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-          top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w}, top = tops[k];
           const int E = pa_exponent(top);
           const __nv_bfloat162 up = pa_up(E);
           uint32_t hi[4], lo[4];

@@ -340,16 +340,24 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
   for (int j = 0; j < 4; ++j) x[j] = load(j);
 #pragma unroll 1
   for (int k0 = 0; k0 < 16; k0 += 4) {
+    uint4 y[4];
+    uint32_t tops[4];                                  // the largest |x| of each step's rows as bf16 bits, side by side
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      y[j] = x[j];
+      const uint32_t m = __vmaxu2(__vmaxu2(y[j].x & 0x7FFF7FFFu, y[j].y & 0x7FFF7FFFu), __vmaxu2(y[j].z & 0x7FFF7FFFu, y[j].w & 0x7FFF7FFFu));
+      tops[j] = max(m & 0xFFFFu, m >> 16);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = load(k0 + j + 4);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tops[j] = max(tops[j], __shfl_xor_sync(0xffffffffu, tops[j], o));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int k = k0 + j;
-      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-      x[j] = load(k + 4);
-      // the largest |x| as bf16 bits
-      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-      top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const uint32_t w[4] = {y[j].x, y[j].y, y[j].z, y[j].w}, top = tops[j];
       const int E = pa_exponent(top);
       const __nv_bfloat162 up = pa_up(E);
       uint32_t hi[4], lo[4];
@@ -625,21 +633,21 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       const float f = !any ? 0.f : whole ? vref / l : vref;
       const int* nk = nan_key[seg % kSegBufs];
 #pragma unroll 1
-      for (int c = 0; c < kKvDim; c += 16) {
-        uint32_t o[16];
-        tmem_ld16(tO + c, o);
+      for (int c = 0; c < kKvDim; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c, o);
         tmem_wait_ld();
         if (there) {
-          float x[16];
+          float x[32];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int k = 0; k < 32; ++k) {
             x[k] = any ? __uint_as_float(o[k]) * f : 0.f;
             if (nk[c + k] < w.limit) x[k] = __int_as_float(0x7FC00000);
           }
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + at * kKvDim + c);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 4; ++k) {
               uint4 v;
               uint32_t* vv = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
@@ -653,7 +661,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             // [slot][dim / 4][pair] float4: a warp's stores are contiguous
             float4* dst = reinterpret_cast<float4*>(a.part_o) + ((int64_t)slot * (kKvDim / 4) + c / 4) * kPromptPairs + kHalfPairs * q + row;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) dst[k * kPromptPairs] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            for (int k = 0; k < 8; ++k) dst[k * kPromptPairs] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
           }
         }
       }
