@@ -744,7 +744,7 @@ dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batc
   if ((int64_t)batch->num_rows * q_heads > INT32_MAX / 2)
     return fail(DSA_ERR_UNSUPPORTED, "num_rows * q_heads is too large");
   // the kernels' running sums over the requests count (column group, tile of 128 keys) pairs in 32 bits
-  const int64_t tiles = (int64_t)batch->block_table_stride * cache->page_size / 128 + 1;
+  const int64_t tiles = (int64_t)batch->block_table_stride * cache->page_size / 128 + 5;   // a segment's ends count as 4
   const int64_t groups = std::max<int64_t>(2 * (int64_t)batch->num_requests, (int64_t)batch->num_rows * group / 256 + batch->num_requests);
   if (tiles * groups > INT32_MAX)
     return fail(DSA_ERR_UNSUPPORTED, "the block table's rows could hold more than 2^31 tiles of 128 tokens for the batch's rows");

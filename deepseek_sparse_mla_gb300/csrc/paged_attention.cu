@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       if (!mbar_wait_warp(&stat_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
       const bool whole = s.n == s.tiles;
       const int pairs = s.rows * a.group;
-      // a piece that starts its segment is its CTA's last unless it also starts the CTA's range
-      const int slot = u - s.n == u0 ? 2 * cta : 2 * cta + 1;
+      // of a CTA's two cut segments, the one that it goes on with and the one that it begins
+      const int slot = s.tile > 0 ? 2 * cta : 2 * cta + 1;
       if (quarter == 0 && lane < live) {
         // out = sum_w f_w O_w: f_w = 2^(m_w - M) / (L 64 2^(m_w - mv_w)) = 2^(mv_w - M) / (64 L), without L for a piece
         const float ma = stat[qb][0][0][lane], mb = stat[qb][1][0][lane], la = stat[qb][0][2][lane], lb = stat[qb][1][2][lane];

@@ -122,18 +122,18 @@ __device__ __forceinline__ PaRecord pa_load_record(const PagedAttnArgs& a, int c
   return x.r;
 }
 
-// The pieces of the segment that the boundary in front of range c cuts: CTAs first .. last, the first one's in
-// first_slot (the others' in slot 2 * CTA).  False where there is none, or an earlier boundary cuts it too.
+// The pieces of the segment that the boundary in front of range c cuts: CTAs first .. last, the first one's (which begins
+// with the segment's first tile) in first_slot, the others' in slot 2 * CTA.  False where there is none, or an
+// earlier boundary cuts it too.
 __device__ __forceinline__ bool pa_pieces(const PaRecord& r, int c, int ctas, int& first, int& last, int& first_slot) {
   if (r.tile <= 0) return false;                          // nothing written, or the range begins with a segment
   const int64_t u = pa_unit_start(c, r.units, ctas);
   if (u == pa_unit_start(c + 1, r.units, ctas)) return false;
   const int64_t seg = u - r.tile;
   first = pa_cta_of_unit(u - 1, r.units, ctas);
-  const int64_t at = pa_unit_start(first, r.units, ctas);
-  if (at > seg) return false;
+  if (pa_unit_start(first, r.units, ctas) > seg) return false;
   last = pa_cta_of_unit(seg + r.tiles - 1, r.units, ctas);
-  first_slot = at == seg ? 2 * first : 2 * first + 1;
+  first_slot = 2 * first + 1;
   return true;
 }
 

@@ -53,6 +53,10 @@ constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
 constexpr uint32_t kPolls = 1u << 11;                // of a millisecond at most
+// A segment counts as this many tiles beside its own: loading its queries and writing its outputs is not hidden.  (2
+// prompts of 1,633 rows and 64 heads, 1 to 13 tiles a segment: 217 us; without, 390.)  Capped and biased tiles take
+// longer, so their segments' ends weigh less.
+constexpr int kSegUnits = 4, kModsSegUnits = 2;
 constexpr int kRuns = 512;                           // runs of (request, pairs) entries that are summed
 constexpr int kMetaBufs = 8;                         // tiles whose K scales are kept (a tile's outlive its K stage)
 constexpr int kSegBufs = 4;
@@ -105,8 +109,10 @@ struct PpCursor {
   int64_t before;                  // units of the entries before this one
 };
 
-// The segment that unit u lies in, cut at u1; the cursor moves up to its entry.
-__device__ __forceinline__ PpSeg pp_segment(const PagedAttnArgs& a, PpCursor& c, int64_t u, int64_t u0, int64_t u1, int cta) {
+// The segment that unit u lies in (its first kEnds units stand for no tile, the others for one each), cut at u1; u
+// moves to the next one and the cursor up to the entry.  n is 0 where no tile of the segment lies in [u, u1).
+template <int kEnds>
+__device__ __forceinline__ PpSeg pp_segment(const PagedAttnArgs& a, PpCursor& c, int64_t& u, int64_t u1, int cta) {
   PpEntry e;
   for (;;) {
     uint32_t none = 0;
@@ -117,20 +123,23 @@ __device__ __forceinline__ PpSeg pp_segment(const PagedAttnArgs& a, PpCursor& c,
       continue;
     }
     e = pp_entry(a, sh, c.b, c.qt);
-    const int64_t units = (int64_t)e.tiles * a.kv_heads;
+    const int64_t units = (int64_t)(e.tiles + kEnds) * a.kv_heads;
     if (u < c.before + units) break;
     c.before += units;
     ++c.qt;
   }
   PpSeg s;
-  const int in = (int)(u - c.before);
-  s.h = in / e.tiles;
-  s.tile = in - s.h * e.tiles;
-  s.n = (int)min((int64_t)(e.tiles - s.tile), u1 - u);
+  const int64_t in = u - c.before;
+  const int per = e.tiles + kEnds;
+  s.h = in < (int64_t(1) << 31) ? (int)((uint32_t)in / (uint32_t)per) : (int)(in / per);
+  const int at = (int)(in - (int64_t)s.h * per), end = (int)min((int64_t)per, at + (u1 - u));
+  s.tile = max(at - kEnds, 0);
+  s.n = max(end - kEnds, 0) - s.tile;
+  u += end - at;
   s.qt = e.qt;
   s.b = e.b;
   s.tiles = e.tiles;
-  s.slot = u == u0 ? 2 * cta : 2 * cta + 1;
+  s.slot = s.tile > 0 ? 2 * cta : 2 * cta + 1;
   s.rows = e.shape.rows;
   s.row0 = e.shape.row0;
   s.len = e.shape.len;
@@ -379,6 +388,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const uint8_t* __restrict__ v_codes,
                         const __grid_constant__ PagedAttnArgs a) {
   using namespace pp;
+  constexpr int kEnds = kMods ? kModsSegUnits : kSegUnits;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           sh = pa_shape(a, ++c.b, none);
           c.qt = 0;
         }
-        sum += pp_entry(a, sh, c.b, c.qt).tiles;
+        sum += pp_entry(a, sh, c.b, c.qt).tiles + kEnds;
         ++c.qt;
       }
     }
@@ -906,12 +916,10 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (seg >= kSegBufs) ok = mbar_wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         PpSeg s = {};
-        // segments are cut where the range ends, or (short requests) belong to the range they begin in as a whole
-        if (u < u1) s = pp_segment(a, cur, u, u0, a.whole ? units : u1, cta);
-        if (a.whole && s.n && s.tile > 0) {
-          u += s.n;
-          s.n = 0;
-          if (u < u1) s = pp_segment(a, cur, u, u0, units, cta);
+        // segments are cut where the range ends, or (short requests) belong as a whole to the range with their first tile
+        while (u < u1 && s.n == 0) {
+          s = pp_segment<kEnds>(a, cur, u, a.whole ? units : u1, cta);
+          if (a.whole && (s.tile > 0 || u - s.n >= u1)) s.n = 0;
         }
         if (lane == 0) {
           segs[seg % kSegBufs] = s;
@@ -919,7 +927,6 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         }
         __syncwarp();
         if (s.n == 0) break;
-        u += s.n;
         // its queries on their way into L2: they are loaded when the segment before ends, with nothing to hide them
         if (seg > 0) {
           const int first = s.qt * kPromptPairs, last = min(first + kPromptPairs, s.rows * a.group);

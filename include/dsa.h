@@ -600,7 +600,7 @@ typedef struct {
  * bits or more with one of 2^-20 of the largest contribution; requests of more rows hold V to 2^-25 of the
  * largest V scale of the request's pages.
  * DSA_ERR_UNSUPPORTED for more than DSA_MAX_REQUESTS requests, for block-table rows of more than 2^30 tokens, and where
- * the table's tokens / 128 times max(2 * requests, rows * heads per K/V head / 256 + requests) exceeds 2^31.
+ * (the table's tokens / 128 + 5) times max(2 * requests, rows * heads per K/V head / 256 + requests) exceeds 2^31.
  */
 DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q,
                                        int64_t q_stride, int32_t q_heads, float scale, int32_t max_query_len,
