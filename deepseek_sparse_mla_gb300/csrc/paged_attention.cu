@@ -734,6 +734,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       if (lane == 0) mbar_arrive(&stat_full[qb]);
       if ((seg & 1) != wg) {
         if (lane == 0) mbar_arrive(&q_empty[qb]);
+        named_bar_sync(bar, 128);                      // the next segment's maxima go where these sums were read
         continue;
       }
       if (!mbar_wait_warp(&stat_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
