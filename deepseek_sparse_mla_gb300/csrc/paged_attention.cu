@@ -323,8 +323,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       ok = mbar_wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls);
       for (int t = 0; t < s.n && ok; ++t, ++i) {
         const int st = i % kStages, sb = i % kSBufs;
-        ok = mbar_spin(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout);
-        if (ok && i >= kSBufs) ok = mbar_spin(&s_empty[sb], (i / kSBufs - 1) & 1, err, kErrMmaTimeout);
+        ok = mbar_spin_warp(&kv_full[st], (i / kStages) & 1, err, kErrTmaTimeout);
+        if (ok && i >= kSBufs) ok = mbar_spin_warp(&s_empty[sb], (i / kSBufs - 1) & 1, err, kErrMmaTimeout);
         if (!ok) break;
         tc_fence_after();
         const uint64_t k = d_k + (uint64_t)((st * kStageBytes) >> 4), q = d_q + (uint64_t)((qb * kQBytes) >> 4);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       if (seg >= 2) ok = mbar_wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
       for (int t = 0; t < s.n && ok; ++t, ++i) {
         const int st = i % kStages, pb = i & 1;
-        ok = mbar_spin(&p_full[pb], (i >> 1) & 1, err, kErrMmaTimeout);
+        ok = mbar_spin_warp(&p_full[pb], (i >> 1) & 1, err, kErrMmaTimeout);
         if (!ok) break;
         tc_fence_after();
         const uint64_t v = d_v + (uint64_t)((st * kStageBytes) >> 4), p = d_p + (uint64_t)((pb * kPBytes) >> 4);
@@ -505,10 +505,10 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             }
             has_nan = (hit & 0x80808080u) != 0;
           }
-          if (named_bar_or(bar, 128, has_nan)) {
+          if (group_or(bar, 128, has_nan)) {
             const uint32_t who = __ballot_sync(0xffffffffu, has_nan);
             if (lane == 0) nan_keys[wg][quarter] = who;
-            named_bar_sync(bar, 128);
+            group_sync(bar, 128);
             const uint8_t* vt = sKV + st * kStageBytes + kTileBytes;
             for (int w = 0; w < 4; ++w)
               for (uint32_t left = nan_keys[wg][w]; left; left &= left - 1) {
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
                   for (int c = 0; c < kCE; ++c)
                     if (key0 + k < cm.limit[c]) poison |= 1u << c;
               }
-            named_bar_sync(bar, 128);
+            group_sync(bar, 128);
             if (has_nan) {
               uint32_t* words = reinterpret_cast<uint32_t*>(vrow);
               for (int q = 0; q < kKvDim / 4; ++q) {
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           const float lv_max = warp_max_f32(fmaxf(__log2f(fabsf(vs)), -118.f));
           if (lane < kCE) wmax[wg][quarter][lane] = mine;
           if (lane == 0) wlv[wg][quarter] = lv_max;
-          named_bar_sync(bar, 128);
+          group_sync(bar, 128);
           float m_new = m_lane, mv_new = mv_lane;
           if (lane < kCE) {
 #pragma unroll
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
             }
             tmem_wait_st();
           }
-          named_bar_sync(bar, 128);
+          group_sync(bar, 128);
         };
         // the buffer is free, and the accumulator settled, once this warpgroup's previous product has completed
         if (i >= 2) {
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          if (!named_bar_or(bar, 128, !raised && (p_top > kSlackP || x_top > kSlackP * kPOne))) break;
+          if (!group_or(bar, 128, !raised && (p_top > kSlackP || x_top > kSlackP * kPOne))) break;
           raised = true;                               // the same in all four warps
           raise();
         }
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           if (lane == 0) wmax[wg][quarter][c] = v;
         }
       }
-      named_bar_sync(bar, 128);
+      group_sync(bar, 128);
       if (quarter == 0 && lane < live) {
         stat[qb][wg][0][lane] = m_lane;
         stat[qb][wg][1][lane] = mv_lane;
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       if (lane == 0) mbar_arrive(&stat_full[qb]);
       if ((seg & 1) != wg) {
         if (lane == 0) mbar_arrive(&q_empty[qb]);
-        named_bar_sync(bar, 128);                      // the next segment's maxima go where these sums were read
+        group_sync(bar, 128);                      // the next segment's maxima go where these sums were read
         continue;
       }
       if (!mbar_wait_warp(&stat_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       if (row == 0 && u - s.n == u0)                     // for the join: this CTA's first piece
         reinterpret_cast<PaRecord*>(a.rec)[cta] = {units, s.tile, s.tiles, s.row0, pairs, s.cg * kCE, s.h};
       poison = stat_nan[qb][0][row] | stat_nan[qb][1][row];
-      named_bar_sync(bar, 128);
+      group_sync(bar, 128);
       if (!mbar_wait_warp(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       tc_fence_after();
 #pragma unroll 1
@@ -796,6 +796,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         mbar_arrive(&q_empty[qb]);
       }
     }
+    group_leave(bar, 128);
   }
   tc_fence_before();
   __syncthreads();

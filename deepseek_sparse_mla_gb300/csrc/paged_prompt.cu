@@ -733,14 +733,14 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       top = warp_max_f32(top);
       if (lane == 0) vmax_part[warp - kConvWarp0] = top;
       if (grp == 0) nan_key[seg % kSegBufs][32 * cw + lane] = INT32_MAX;
-      named_bar_sync(1, 256);
+      group_sync(1, 256);
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = fmaxf(top, vmax_part[k]);
       const uint32_t top_bits = __float_as_uint(top) & 0x7F800000u;
       const float vref = top_bits && top_bits < 0x7F800000u ? __uint_as_float(top_bits) : 1.f;
       if (warp == kConvWarp0 && lane == 0) v_ref[seg % kSegBufs] = vref;
       const float vinv = 1.f / vref;
-      named_bar_sync(1, 256);
+      group_sync(1, 256);
       const int min_limit = pp_limit(s, min(s.qt * kPromptPairs, s.rows * a.group - 1) / a.group);
 
       uint4 x[8];
@@ -815,6 +815,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       if (!ok) break;
       i0 += s.n;
     }
+    group_leave(1, 256);
   } else {
     regs_dec<kRegsRest>();
     if (warp == kOutWarp) {

@@ -84,6 +84,12 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, uint32
   return false;
 }
 
+// mbar_spin for a whole warp that goes on with warp-wide operations: every lane gets the same answer.
+__device__ __forceinline__ bool mbar_spin_warp(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
+  const bool ok = mbar_spin(bar, parity, err, code);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Poll until the phase with the given parity completes; false (and err |= code) after max_polls.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code,
                                           uint32_t max_polls = 1u << 24) {
@@ -181,6 +187,34 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t threads, bool
 // Barrier over a subset of the CTA's warps (id 1..15; `threads` a multiple of 32).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The same, with the number of threads whose predicate holds.
+__device__ __forceinline__ uint32_t named_bar_count(uint32_t id, uint32_t threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "bar.red.popc.u32 %0, %1, %2, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)pred)
+      : "memory");
+  return r;
+}
+
+// Barriers of a group of warps each of which may have to give up on a bounded wait of its own.  A warp that left the group
+// behind would leave the others at its next barrier for good, so it takes part in all of them until everyone is done,
+// and the group leaves at the same one: a warp that has nothing more to do votes with all 32 threads, one that goes on with
+// none or 31.  All barriers of the group are this one primitive, so they pair up whatever each warp is doing; what
+// the others compute meanwhile is not used (the error has been recorded).
+__device__ __forceinline__ void group_sync(uint32_t id, uint32_t threads) { (void)named_bar_count(id, threads, false); }
+__device__ __forceinline__ bool group_or(uint32_t id, uint32_t threads, bool pred) {
+  const bool any = __any_sync(0xffffffffu, pred);
+  return (named_bar_count(id, threads, any && (threadIdx.x & 31) != 0) & 31u) != 0;   // those that left do not count
+}
+__device__ __forceinline__ void group_leave(uint32_t id, uint32_t threads) {
+  while (named_bar_count(id, threads, true) != threads) {
+  }
 }
 
 // ---------------------------------------------------------------------------
