@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   __shared__ uint32_t sbad[kMetaBufs];                // 16-key groups without a valid page
   __shared__ int nan_key[kSegBufs][kKvDim];           // first key with a NaN code that only some rows see, by dim
   __shared__ int32_t run_units[kRuns];                // units (without heads) of the runs before
-  __shared__ int32_t scan[kThreads / 32];
+  __shared__ uint32_t scan[kThreads / 32];
   __shared__ float vmax_part[8], v_ref[kSegBufs];     // V's reference of a segment
   __shared__ PpSeg segs[kSegBufs];
   __shared__ uint64_t seg_full[kSegBufs], seg_empty[kSegBufs];
@@ -447,34 +447,39 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   // are complete.  The first write waits for its end, so that this grid's end stands for both.
   const int B = a.num_requests;
   // block-wide inclusive sum of one value a thread
-  auto block_sum = [&](int v) {
-    int incl = v;
+  auto block_sum = [&](uint32_t v) {
+    uint32_t incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     __syncthreads();
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    int before = 0;
+    uint32_t before = 0;
     for (int w = 0; w < warp; ++w) before += scan[w];
     return before + incl;
   };
+  // Requests that share no rows have no more entries than this (2^22 + 4096 at most, so no sum below passes 32 bits, and by the
+  // host's check no sum of their tiles does).  Starts that run back can name the same rows again and again: refused.
+  const uint32_t most_entries = (uint32_t)((int64_t)a.num_rows * a.group / kPromptPairs) + B;
   {
     uint32_t bits = 0;
     const int per = (B + kThreads - 1) / kThreads, b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int sum = 0;
+    uint32_t sum = 0;
     for (int b = b0; b < b1; ++b) {
-      sum += pp_entries(a, pa_shape(a, b, bits));
+      sum = min(sum + pp_entries(a, pa_shape(a, b, bits)), most_entries + 1);
       entry_end[b] = sum;
     }
-    const int before = block_sum(sum) - sum;
+    const uint32_t before = block_sum(sum) - sum;
     for (int b = b0; b < b1; ++b) entry_end[b] += before;
     if (bits) atomicOr(&bits_all, bits);
   }
   __syncthreads();
-  const int entries = entry_end[B - 1];
+  const bool shared_rows = (uint32_t)entry_end[B - 1] > most_entries;
+  if (shared_rows && tid == 0) atomicOr(&bits_all, (uint32_t)DSA_DEVICE_BAD_LENGTH);
+  const int entries = shared_rows ? 0 : entry_end[B - 1];
   const int run = (entries + kRuns - 1) / kRuns;
   // the entry with index x
   auto find = [&](int x, PpCursor& c) {

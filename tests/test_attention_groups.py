@@ -67,3 +67,19 @@ def test_groups_have_no_barrier_that_a_warp_that_gave_up_would_miss():
         assert rest[0] == "}" and rest[1] in ("else", "tc_fence_before();")
         # and a warp's lanes agree on giving up
         assert not re.search(r"\bmbar_(spin|wait)\(", text)
+
+
+def test_the_sums_of_the_prompt_kernels_split_stay_in_32_bits():
+    """Its sums over the requests, for the largest batches that the host lets through, whatever the row offsets say: a thread's
+    share of the entries is held at one more than requests without shared rows can have, and more of them are refused."""
+    requests, pairs = 4096, 2 ** 30                        # DSA_MAX_REQUESTS; rows * heads, as checked by the host
+    most = pairs // 256 + requests
+    threads, entries = 640, pairs // 256                   # of one request that names every row
+    alternating = requests // 2 * entries                  # every other request does
+    assert alternating > 2 ** 31                           # what an unchecked sum would be
+    assert threads * (most + 1) < 2 ** 32
+    text = source("paged_prompt.cu")
+    assert "min(sum + pp_entries(a, pa_shape(a, b, bits)), most_entries + 1)" in text
+    assert re.search(r"const int entries = shared_rows \? 0 : entry_end\[B - 1\];", text)
+    api = source("dsa_api.cu")
+    assert "num_rows * q_heads > INT32_MAX / 2" in api and "num_rows * group / 256 + batch->num_requests" in api
