@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
       const int buf = seg % kQBufs;
-      // first what a lane knows of a column of its own (columns without a pair are left as they are: nothing reads them)
+      // first what a lane knows of a column of its own.  A column without a pair scores NaN whatever an earlier segment or
+      // kernel left of it in shared memory: NaN is no maximum, so it moves no references, and nobody takes its output.
       const int live = min(s.rows * a.group - s.cg * kCE, kCE);
       const int n = s.cg * kCE + min(lane, live - 1), i = n / a.group, head = s.h * a.group + (n - i * a.group);
       const int64_t from = (int64_t)(s.row0 + i) * a.q_stride + (int64_t)head * kKvDim;
@@ -408,6 +409,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         cm.pos[lane] = (float)pos;
         cm.at[lane] = (s.row0 + i) * a.kv_heads * a.group + head;
         cm.slope[lane] = slope;
+      } else if (lane < kCE) {
+        cm.factor[lane] = __int_as_float(0x7FC00000);
       }
       int low = limit;                                 // (lanes without a column hold the last one's)
 #pragma unroll 1

@@ -46,3 +46,23 @@ def test_starts_that_run_back_are_refused(B, stride):
     with pytest.raises(dsa.DsaError, match="BAD_LENGTH"):
         dsa.paged_attention(cache, batch, q, max_query_len=rows, out=out, check=True)
     assert torch.all(out == -7.0).item()
+
+
+@pytest.mark.parametrize("group", [1, 5, 6, 20, 24])
+def test_equal_calls_give_equal_bits_whatever_ran_between_them(group):
+    """Columns of a tile that no query fills keep what an earlier call left in shared memory: they do not count."""
+    case = DenseCase(37, [2300, 1800, 2777, 900] * 10, [1] * 40, 64, 2, group)
+    wide = 8 if group <= 8 else 32
+    others = [DenseCase(38, [2500] * 40, [1] * 40, 64, 2, wide), DenseCase(39, [700] * 40, [1] * 40, 64, 2, wide)]
+    for c, up in zip(others, (64.0, 2.0 ** -20)):
+        c.q_bits = wlm.bf16_bits((c.q * up).astype(np.float32))
+    tensors, busy = case.gpu(), [c.gpu() for c in others]
+    first = None
+    for between in (None, 0, 1, 0, None):
+        if between is not None:
+            attend(others[between], busy[between])
+        got = attend(case, tensors)
+        first = first or got
+        same = np.array_equal(got[0], first[0]) and np.array_equal(got[1], first[1])
+        assert same, f"after {between}"
+    check_attention(*first, case.oracle())
