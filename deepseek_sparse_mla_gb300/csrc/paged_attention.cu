@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   __shared__ uint32_t sbad[kStages];
   __shared__ __align__(16) PaColumns cols[kQBufs];
   __shared__ __align__(16) float refs[2][2][kCE];
-  __shared__ float wmax[2][4][kCE], wlv[2][4], fin[2][2][kCE];
+  __shared__ float wmax[2][4][kCE], fin[2][2][kCE];
   __shared__ float stat[kQBufs][2][3][kCE];            // each warpgroup's m, mv and l of a segment
   __shared__ uint32_t stat_nan[kQBufs][2][kKvDim];
   __shared__ uint32_t nan_keys[2][4];
@@ -577,7 +577,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         // the exact maxima over the tile, where the references do not hold: they, and what was formed against them, move
         auto raise = [&]() {
           // rolled: it runs for a segment's first tile, where a second copy of all columns' scores would have to come from L2
-          float mine = -INFINITY;
+          // log2 of the key's scale, held at -118: 4 * kPOne * 2^(m - mv) stays finite for pages whose scales are smaller, or 0
+          const float lv = fmaxf(__log2f(fabsf(vs)), -118.f);
+          float mine = -INFINITY, mine_v = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < kNC; c0 += 8) {
             float z[8];
@@ -587,19 +589,28 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
               const float r = warp_max_f32(z[c]);
               if (lane == c0 + c) mine = r;            // lane c of every warp ends up with column c's
             }
+            // a warp's 32 keys have one scale, but for pages of 16: there the maximum of z + lv may be another key's
+            if (a.log2_page == 4) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float r = warp_max_f32(z[c] + lv);
+                if (lane == c0 + c) mine_v = r;
+              }
+            }
           }
-          // held at -118: 4 * kPOne * 2^(m - mv) stays finite for pages whose scales are smaller, or 0
-          const float lv_max = warp_max_f32(fmaxf(__log2f(fabsf(vs)), -118.f));
-          if (lane < kCE) wmax[wg][quarter][lane] = mine;
-          if (lane == 0) wlv[wg][quarter] = lv_max;
+          if (a.log2_page != 4) mine_v = mine + lv;
+          float* const wmax_v = reinterpret_cast<float*>(sP + wg * kPBytes);   // [4][kCE], before the tile's P is there
+          if (lane < kCE) {
+            wmax[wg][quarter][lane] = mine;
+            wmax_v[quarter * kCE + lane] = mine_v;
+          }
           group_sync(bar, 128);
           float m_new = m_lane, mv_new = mv_lane;
           if (lane < kCE) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const float x = wmax[wg][w][lane];
-              m_new = fmaxf(m_new, x);
-              mv_new = fmaxf(mv_new, x + wlv[wg][w]);
+              m_new = fmaxf(m_new, wmax[wg][w][lane]);
+              mv_new = fmaxf(mv_new, wmax_v[w * kCE + lane]);
             }
           }
           const float al = m_lane == -INFINITY ? 0.f : ex2_approx(m_lane - m_new);

@@ -66,3 +66,47 @@ def test_equal_calls_give_equal_bits_whatever_ran_between_them(group):
         same = np.array_equal(got[0], first[0]) and np.array_equal(got[1], first[1])
         assert same, f"after {between}"
     check_attention(*first, case.oracle())
+
+
+def largest_contribution(case, lse, scale=128 ** -0.5):
+    """max_s p_s |v_scale_s| * sum_s |v_code_s|, in the place of the oracle's C, which takes both maxima apart."""
+    codes, C = {n: o.e4m3_to_f64(case.codes[n]) for n in "kv"}, np.zeros((case.rows, case.heads, 128))
+    for b, L in enumerate(int(v) for v in case.seq_lens):
+        at = np.arange(L)
+        page, off = case.table[b, at // case.P], at % case.P
+        for r in range(case.starts[b], case.starts[b + 1]):
+            see = slice(0, L - case.q_lens[b] + 1 + r - case.starts[b])
+            for head in range(case.heads):
+                h = head // case.group
+                k = codes["k"][page[see], h, off[see]] * case.scales["k"][page[see], h].astype(np.float64)[:, None]
+                p = np.exp(scale * (k @ case.q[r, head]) - lse[r, head])
+                vs = np.abs(case.scales["v"][page[see], h].astype(np.float64))
+                C[r, head] = (p * vs).max() * np.abs(codes["v"][page[see], h, off[see]]).sum(0)
+    return C
+
+
+@pytest.mark.parametrize("seq,new", [([49], [3]), ([64, 81, 33], [5, 4, 2]), ([143, 17], [16, 2])])
+def test_a_page_that_only_later_rows_see_leaves_the_others_their_bits(seq, new):
+    """Pages of 16 tokens, two to a warp's 32 keys: the last one, with a scale far above the others', shares them with one that
+    the earlier rows see."""
+    case = DenseCase(31, seq, new, 16, 2, 4)
+    for b, L in enumerate(seq):
+        last = (L - 1) // 16
+        case.scales["v"][case.table[b, :last]] *= np.float32(2.0 ** -30)
+        case.scales["v"][case.table[b, last]] = 2.0 ** 118
+    out, lse, A, _, Z = case.oracle()
+    got, got_lse = attend(case)
+    check_attention(got, got_lse, (out, lse, A, largest_contribution(case, lse), Z))
+
+
+@pytest.mark.parametrize("P", [16, 32, 64])
+@pytest.mark.parametrize("step", [3, 12])
+@pytest.mark.parametrize("scale", [128 ** -0.5, 1.0])
+def test_scales_far_apart_keep_the_bits_of_the_largest_contribution(P, step, scale):
+    """Neighbouring pages whose scales of V, and with a scale of 1 whose scores too, lie far apart."""
+    case = DenseCase(32, [300, 77, 129, 700], [1, 3, 2, 4], P, 2, 8)
+    rng = np.random.default_rng(32)
+    case.scales["v"] *= np.exp2(rng.integers(-2, 3, case.scales["v"].shape) * step).astype(np.float32)
+    out, lse, A, _, Z = case.oracle(scale=scale)
+    got, got_lse = attend(case, scale=scale)
+    check_attention(got, got_lse, (out, lse, A, largest_contribution(case, lse, scale), Z))
