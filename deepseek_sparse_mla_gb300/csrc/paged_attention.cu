@@ -138,12 +138,13 @@ struct PaColumns {
   int min_limit;                // over the columns
 };
 
-// kCE columns (8, 16 or 32); kMods: score cap and distance bias compiled in
-template <int kCE, bool kMods>
+// kCE columns (8, 16 or 32); kModSet: score cap and distance bias compiled in
+template <int kCE, PaMods kModSet>
 __global__ void __launch_bounds__(pa::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                            const __grid_constant__ PagedAttnArgs a, int shared_keys) {
   using namespace pa;
+  constexpr bool kMods = kModSet != kPaPlain;
   constexpr int kHalf = kCE < 16 ? 16 : kCE;          // columns of the hi half (and of the lo half)
   constexpr int kN = 2 * kHalf;                       // MMA N: 32 or 64
   extern __shared__ uint8_t smem_raw[];
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           for (int c = 0; c < c1; ++c) z[c] = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
           if (kMods && in != 0.f) {
 #pragma unroll
-            for (int c = 0; c < c1; ++c) z[c] = capped(z[c] * in, a.cap_log2);
+            for (int c = 0; c < c1; ++c) z[c] = capped<kModSet>(z[c] * in, a.cap_log2);
           }
           if (kMods) {
 #pragma unroll
@@ -860,14 +861,19 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = once_per_device(ready, [] {
     const int most = pa::kFixedSmem + DSA_MAX_REQUESTS * (int)sizeof(int32_t);
-    cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<kCE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<kCE, kPaPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (r == cudaSuccess)
-      r = cudaFuncSetAttribute(paged_attention_kernel<kCE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      r = cudaFuncSetAttribute(paged_attention_kernel<kCE, kPaCapBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(paged_attention_kernel<kCE, kPaLargeCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return r;
   });
   if (e != cudaSuccess) return e;
   const int shared_keys = std::min<int64_t>((int64_t)a.max_rows * a.group, a.hi_pairs) > kCE ? 1 : 0;   // column groups share keys
-  auto kernel = a.cap_log2 > 0.f || a.slopes ? paged_attention_kernel<kCE, true> : paged_attention_kernel<kCE, false>;
+  const PaMods mods = pa_mods(a);
+  auto kernel = mods == kPaPlain     ? paged_attention_kernel<kCE, kPaPlain>
+                : mods == kPaCapBias ? paged_attention_kernel<kCE, kPaCapBias>
+                                     : paged_attention_kernel<kCE, kPaLargeCap>;
   e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, shared_keys);
   count_launches(1);
   if (e != cudaSuccess) return e;

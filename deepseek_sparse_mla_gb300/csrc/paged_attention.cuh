@@ -77,13 +77,33 @@ __device__ __forceinline__ float pa_factor(uint32_t top, int E, float scale) {
 cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
                                 const uint8_t* v_codes, int ctas, cudaStream_t s);
 
-// A capped score: cap * tanh(z / cap) = cap * (1 - 2 / (1 + 2^y)), y = 2 log2(e) / cap * z, all in log2 units.  Exact
-// to about 2^-21 of the cap; past the range of 2^y the quotient is 0 or 2, and NaN stays.
+// A capped score: cap * tanh(z / cap), with y = 2 log2(e) / cap * z and all in log2 units.
+//   small caps: cap * (1 - 2 / (1 + 2^y)), exact to about 2^-22 of the cap (1.5e-5 of a score at a cap of 64); past the
+//   range of 2^y the quotient is 0 or 2, and NaN stays.
+//   large caps: an error of the cap's size would be one of 0.1 at a cap of 1e6, and past 1e8 every score would be 0.  Where
+//   |z / cap| is below 0.3 the odd series takes over, t - t^3/3 + 2 t^5/15 - 17 t^7/315 + 62 t^9/2835 with t = z / cap =
+//   ln(2) / 2 y: the next term is below 2^-24 of the score, and a score is held to 2^-21 of itself.
+// The series' eight instructions a score cost the mixed capped batch 118 us instead of 102, and 109 even where a branch steps
+// around them, so kernels for large caps are compiled apart.
+constexpr float kLargeCap = 64.f * 1.44269504f;         // log2 units
+enum PaMods : int { kPaPlain, kPaCapBias, kPaLargeCap };   // plain scores; a cap, a distance bias or both; with a large cap
+__host__ __device__ __forceinline__ PaMods pa_mods(const PagedAttnArgs& a) {
+  return a.cap_log2 > kLargeCap ? kPaLargeCap : a.cap_log2 > 0.f || a.slopes ? kPaCapBias : kPaPlain;
+}
+template <PaMods kModSet>
 __device__ __forceinline__ float capped(float y, float cap) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return fmaf(-2.f * cap, r, cap);
+  const float quotient = fmaf(-2.f * cap, r, cap);
+  if (kModSet != kPaLargeCap) return quotient;
+  constexpr float kHalfLn2 = 0.34657359f, kSq = kHalfLn2 * kHalfLn2;
+  const float s = y * y;
+  float p = fmaf(62.f / 2835.f * kSq * kSq * kSq * kSq, s, -17.f / 315.f * kSq * kSq * kSq);
+  p = fmaf(p, s, 2.f / 15.f * kSq * kSq);
+  p = fmaf(p, s, -1.f / 3.f * kSq);
+  p = fmaf(p, s, 1.f);
+  return fabsf(y) < 0.86f ? kHalfLn2 * cap * y * p : quotient;
 }
 
 // Units [start(c), start(c + 1)) belong to CTA c: units * c / ctas.

@@ -250,8 +250,9 @@ __device__ __forceinline__ float pp_half(const PpRow& w, uint32_t tS, const floa
 
 // 64 keys with masks, a cap or a bias, in two rolled passes (one body of each: unrolled like the plain form, the call
 // with a cap and a bias took a fifth longer): the scores are made final and written back, with their largest ..
-template <bool kMods, bool kMasked>
+template <PaMods kModSet, bool kMasked>
 __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a, uint32_t tS, int key0, uint32_t bad, const float* ks) {
+  constexpr bool kMods = kModSet != kPaPlain;
   const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
   float top = -INFINITY;
 #pragma unroll 1
@@ -271,7 +272,7 @@ __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a
       for (int c = 0; c < 16; ++c) z[c] = __uint_as_float(x[c]) * kc;
       if (kMods && in != 0.f) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) z[c] = capped(z[c], a.cap_log2);
+        for (int c = 0; c < 16; ++c) z[c] = capped<kModSet>(z[c], a.cap_log2);
       }
       if (kMods) {
 #pragma unroll
@@ -383,11 +384,12 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
   return cf;
 }
 
-template <bool kMods>
+template <PaMods kModSet>
 __global__ void __launch_bounds__(pp::kThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const uint8_t* __restrict__ v_codes,
                         const __grid_constant__ PagedAttnArgs a) {
   using namespace pp;
+  constexpr bool kMods = kModSet != kPaPlain;
   constexpr int kEnds = kMods ? kModsSegUnits : kSegUnits;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           return true;
         };
         if constexpr (kMods || decltype(masked)::value) {
-          raise(pp_max64<kMods, decltype(masked)::value>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks));
+          raise(pp_max64<kModSet, decltype(masked)::value>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks));
           if (!ok) return;
           w.l += pp_exp64(w, tS + 64 * h);
         } else {
@@ -1072,13 +1074,17 @@ cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = once_per_device(ready, [] {
     const int most = pp::kFixedSmem;
-    cudaError_t r = cudaFuncSetAttribute(paged_prompt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    cudaError_t r = cudaFuncSetAttribute(paged_prompt_kernel<kPaPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<kPaCapBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<kPaLargeCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return r;
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(a.cap_log2 > 0.f || a.slopes ? paged_prompt_kernel<true> : paged_prompt_kernel<false>, dim3(ctas),
-                 dim3(pp::kThreads), pp::kFixedSmem, s, k_map, v_codes, a);
+  const PaMods mods = pa_mods(a);
+  auto kernel = mods == kPaPlain     ? paged_prompt_kernel<kPaPlain>
+                : mods == kPaCapBias ? paged_prompt_kernel<kPaCapBias>
+                                     : paged_prompt_kernel<kPaLargeCap>;
+  e = launch_pdl(kernel, dim3(ctas), dim3(pp::kThreads), pp::kFixedSmem, s, k_map, v_codes, a);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (ctas > 1 && !a.whole) {

@@ -110,3 +110,33 @@ def test_scales_far_apart_keep_the_bits_of_the_largest_contribution(P, step, sca
     out, lse, A, _, Z = case.oracle(scale=scale)
     got, got_lse = attend(case, scale=scale)
     check_attention(got, got_lse, (out, lse, A, largest_contribution(case, lse, scale), Z))
+
+
+SHAPES = {"decode": ([900, 77, 129], [1, 3, 2], 32, 2, 8), "prompt": ([900, 77, 129], [45, 9, 129], 32, 2, 8)}
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("cap", [24.0, 96.0, 1e3, 1e4, 1e6, 1e8, 1e12, 1e30])
+def test_large_caps_leave_scores_as_they_are(shape, cap):
+    """The bound does not grow with the cap: scores are held to their own rounding."""
+    case = DenseCase(34, *SHAPES[shape])
+    got, lse = attend(case, scale=0.5, softcap=cap)
+    check_attention(got, lse, case.oracle(scale=0.5, softcap=cap))
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 0.1])
+def test_small_caps(shape, cap):
+    case = DenseCase(35, *SHAPES[shape])
+    got, lse = attend(case, softcap=cap)
+    check_attention(got, lse, case.oracle(softcap=cap))
+
+
+@pytest.mark.parametrize("shape", list(SHAPES))
+@pytest.mark.parametrize("cap", [63.0, 65.0, 1e5])
+def test_a_large_cap_with_a_bias_and_a_prefix(shape, cap):
+    case = DenseCase(40, *SHAPES[shape])
+    prefix = np.array([200, 77, 10], np.int32)
+    got, lse = attend(case, scale=0.5, softcap=cap, slopes=case.slopes, prefix_lens=prefix)
+    want = case.oracle(scale=0.5, softcap=cap, slopes=case.slopes, prefix=prefix)
+    check_attention(got, lse, want, reach=float(case.slopes.max()) * 900)
