@@ -132,10 +132,11 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 struct PaColumns {
   float factor[pa::kColMax];    // 2^k of the split query * softmax scale * log2 e
   int limit[pa::kColMax];       // keys below it are seen
-  float pos[pa::kColMax];
+  float row[pa::kColMax];       // of the request: its position is start + row
   float slope[pa::kColMax];     // * log2 e
   int at[pa::kColMax];          // row * query heads + head
   int min_limit;                // over the columns
+  int start;                    // position of the request's first row
 };
 
 // kCE columns (8, 16 or 32); kModSet: score cap and distance bias compiled in
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
       if (lane < live) {
         cm.limit[lane] = limit;
-        cm.pos[lane] = (float)pos;
+        cm.row[lane] = (float)i;
         cm.at[lane] = (s.row0 + i) * a.kv_heads * a.group + head;
         cm.slope[lane] = slope;
       } else if (lane < kCE) {
@@ -450,7 +451,10 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         }
       }
       low = __reduce_min_sync(0xffffffffu, low);
-      if (lane == 0) cm.min_limit = low;
+      if (lane == 0) {
+        cm.min_limit = low;
+        cm.start = start;
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
@@ -491,6 +495,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         const float ks = sks[st][pg], vs = svs[st][pg];
         const bool exists = !kMasked || (j < s.len && !((sbad[st] >> pg) & 1u));
         const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
+        // Distances are taken from the request's first row in integers: they, and the small row numbers, are exact in fp32
+        // however far from 0 the positions are, up to 2^24 tokens away, and rounded like any fp32 value beyond.
+        const float ahead = kMods ? (float)(j - cm.start) : 0.f;
         if (kMasked) {
           // A key's values meet a probability of 0 where it is not seen, and 0 * NaN is NaN: what lies behind
           // the request's tokens is zeroed here, and NaN codes of keys that only some columns see are taken out.
@@ -543,7 +550,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           }
           if (kMods) {
 #pragma unroll
-            for (int c = 0; c < c1; ++c) z[c] = fmaf(-cm.slope[c0 + c], fabsf(cm.pos[c0 + c] - (float)j), z[c]);
+            for (int c = 0; c < c1; ++c) z[c] = fmaf(-cm.slope[c0 + c], fabsf(cm.row[c0 + c] - ahead), z[c]);
           }
           if (kMasked) {
 #pragma unroll

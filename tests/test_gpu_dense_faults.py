@@ -140,3 +140,23 @@ def test_a_large_cap_with_a_bias_and_a_prefix(shape, cap):
     got, lse = attend(case, scale=0.5, softcap=cap, slopes=case.slopes, prefix_lens=prefix)
     want = case.oracle(scale=0.5, softcap=cap, slopes=case.slopes, prefix=prefix)
     check_attention(got, lse, want, reach=float(case.slopes.max()) * 900)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 8, 20])
+@pytest.mark.parametrize("before", [1 << 24, 1 << 25])
+def test_a_distance_bias_past_two_to_the_24_tokens(rows, before):
+    """Keys further than 1,000 away weigh e^-500 and less: one page stands for all of them."""
+    import torch
+    import deepseek_sparse_mla_gb300 as dsa
+    case = DenseCase(36, [1001], [rows], 128, 1, 8)
+    filler = int(np.setdiff1d(np.arange(case.pages), case.table[0])[0])
+    for n in "kv":
+        case.codes[n][filler] = 0
+    slopes = np.full(case.heads, 0.5, np.float32)
+    want = case.oracle(slopes=slopes)
+    cache, batch, q = case.gpu()
+    table = torch.full((1, before // 128 + 8), filler, dtype=torch.int32, device="cuda")
+    table[0, before // 128:] = batch.block_table[0, :8]
+    far = dsa.Batch(table, batch.seq_lens + before, batch.query_start_loc, num_rows=rows, max_seq_len=before + 1001)
+    got, lse = attend(case, (cache, far, q), slopes=slopes)
+    check_attention(got, lse, want, reach=0.5 * 64)
