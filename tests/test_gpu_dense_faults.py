@@ -160,3 +160,21 @@ def test_a_distance_bias_past_two_to_the_24_tokens(rows, before):
     far = dsa.Batch(table, batch.seq_lens + before, batch.query_start_loc, num_rows=rows, max_seq_len=before + 1001)
     got, lse = attend(case, (cache, far, q), slopes=slopes)
     check_attention(got, lse, want, reach=0.5 * 64)
+
+
+def test_a_prompts_values_are_held_to_a_share_of_the_requests_largest_scale():
+    """The kernel for many rows holds V in half precision relative to the request's largest scale: half a step of its smallest
+    numbers, 2^-25 of that scale, also for rows that do not see the page with it."""
+    case = DenseCase(33, [600, 333], [40, 70], 16, 2, 8)
+    tops = np.zeros((case.rows, 1, 1))
+    for b, L in enumerate(case.seq_lens):
+        last = case.table[b, (L - 1) // 16]
+        case.scales["v"][last] *= np.float32(2.0 ** (14 + 4 * b))
+        tops[case.starts[b]:case.starts[b + 1]] = case.scales["v"][case.table[b, :-(-L // 16)]].max()
+    out, lse, A, C, Z = case.oracle()
+    got, got_lse = attend(case)
+    assert np.all(np.isfinite(got))
+    dz = 2.0 ** -15 * Z + 2.0 ** -20
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -9 + 2 * dz[..., None]) * A + 2.0 ** -25 * tops   # bf16, P's 11 bits and the sums, V
+    assert np.all(np.abs(got - out) <= tol)
+    assert np.all(np.abs(got_lse - lse) <= dz + 2.0 ** -20 * (1 + np.abs(lse)))
