@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const int min_limit = cm.min_limit;
       const int live = min(s.rows * a.group - s.cg * kCE, kCE);   // columns in use
       // the references of column `lane` (m: of z, mv: of z + log2 vs); every column's are in shared memory, as m and as
-      // kPOne * 2^(m - mv)
+      // 2^(m - mv)
       float m_lane = -INFINITY, mv_lane = -INFINITY;
       float* const ref_m = refs[wg][0];
       float* const ref_e = refs[wg][1];
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         constexpr int kNC = decltype(columns)::value;
         constexpr bool kMasked = decltype(with_masks)::value;
         const int st = i % kStages, sb = i % kSBufs, j = key0 + row, pg = row >> a.log2_page;
-        const float ks = sks[st][pg], vs = svs[st][pg];
+        const float ks = sks[st][pg], vs = svs[st][pg], vs_one = vs * kPOne;
         const bool exists = !kMasked || (j < s.len && !((sbad[st] >> pg) & 1u));
         const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
         // Distances are taken from the request's first row in integers: they, and the small row numbers, are exact in fp32
@@ -585,8 +585,8 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         // the exact maxima over the tile, where the references do not hold: they, and what was formed against them, move
         auto raise = [&]() {
           // rolled: it runs for a segment's first tile, where a second copy of all columns' scores would have to come from L2
-          // log2 of the key's scale, held at -118: 4 * kPOne * 2^(m - mv) stays finite for pages whose scales are smaller, or 0
-          const float lv = fmaxf(__log2f(fabsf(vs)), -118.f);
+          // log2 of the key's scale, -126 for one of 0: 2^(m - mv) and its product with a probability below 4 stay finite
+          const float lv = fmaxf(__log2f(fabsf(vs)), -126.f);
           float mine = -INFINITY, mine_v = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < kNC; c0 += 8) {
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           mv_lane = mv_new;
           if (quarter == 0 && lane < kCE) {
             ref_m[lane] = m_new == -INFINITY ? -1e30f : m_new;   // nothing seen yet: the first score that is exceeds it
-            ref_e[lane] = mv_new == -INFINITY ? kPOne : ex2_approx(m_new - mv_new) * kPOne;
+            ref_e[lane] = mv_new == -INFINITY ? 1.f : ex2_approx(m_new - mv_new);
           }
           if (!fresh) {
 #pragma unroll
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               z[c + q] = ex2_approx(z[c + q] - mm[q]);
-              x[q] = (z[c + q] * ee[q]) * vs;         // in this order: 0 stays 0 whatever the scale of an unseen key
+              x[q] = (z[c + q] * ee[q]) * vs_one;     // in this order: 0 stays 0 whatever the scale of an unseen key
               p_top = fmaxf(p_top, z[c + q]);
               x_top = fmaxf(x_top, x[q]);
             }
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          if (!group_or(bar, 128, !raised && (p_top > kSlackP || x_top > kSlackP * kPOne))) break;
+          if (!group_or(bar, 128, !raised && (p_top >= kSlackP || x_top > kSlackP * kPOne))) break;
           raised = true;                               // the same in all four warps
           raise();
         }
@@ -765,14 +765,15 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       // of a CTA's two cut segments, the one that it goes on with and the one that it begins
       const int slot = s.tile > 0 ? 2 * cta : 2 * cta + 1;
       if (quarter == 0 && lane < live) {
-        // out = sum_w f_w O_w: f_w = 2^(m_w - M) / (L 64 2^(m_w - mv_w)) = 2^(mv_w - M) / (64 L), without L for a piece
+        // out = sum_w f_w O_w: f_w = 2^(m_w - M) / (L 64 2^(m_w - mv_w)) = 2^(mv_w - M) / (64 L).  The factors stay apart, the
+        // first one as two square roots: V's scales go from 2^-126 to 2^120, and O_w / (64 L) brings O_w to the size of V's codes first.
         const float ma = stat[qb][0][0][lane], mb = stat[qb][1][0][lane], la = stat[qb][0][2][lane], lb = stat[qb][1][2][lane];
         const bool has_a = la > 0.f || la != la, has_b = lb > 0.f || lb != lb;   // NaN counts as seen
         const float M = fmaxf(ma, mb);
         const float L = (has_a ? la * ex2_approx(ma - M) : 0.f) + (has_b ? lb * ex2_approx(mb - M) : 0.f);
-        const float over = (whole ? 1.f / L : 1.f) / kPOne;
-        fin[wg][0][lane] = has_a ? ex2_approx(stat[qb][0][1][lane] - M) * over : 0.f;
-        fin[wg][1][lane] = has_b ? ex2_approx(stat[qb][1][1][lane] - M) * over : 0.f;
+        fin[wg][0][lane] = has_a ? ex2_approx(0.5f * (stat[qb][0][1][lane] - M)) : 0.f;
+        fin[wg][1][lane] = has_b ? ex2_approx(0.5f * (stat[qb][1][1][lane] - M)) : 0.f;
+        stat[qb][0][2][lane] = 1.f / L / kPOne;          // (la has been read)
         if (whole) {
           if (a.lse) a.lse[cm.at[lane]] = has_a || has_b ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
         } else {
@@ -798,11 +799,11 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           if (c0 + c >= live) break;
-          const float fa = fin[wg][0][c0 + c], fb = fin[wg][1][c0 + c];
+          const float fa = fin[wg][0][c0 + c], fb = fin[wg][1][c0 + c], over = stat[qb][0][2][c0 + c];
           // an accumulator without a seen key holds nothing of this column (or was never written)
           float v = 0.f;
-          if (fa != 0.f) v = fmaf(__uint_as_float(r[8 + c]), 0.0625f, __uint_as_float(r[c])) * fa;
-          if (fb != 0.f) v = fmaf(fmaf(__uint_as_float(r[24 + c]), 0.0625f, __uint_as_float(r[16 + c])), fb, v);
+          if (fa != 0.f) v = fmaf(__uint_as_float(r[8 + c]), 0.0625f, __uint_as_float(r[c])) * over * fa * fa;
+          if (fb != 0.f) v = fmaf(fmaf(__uint_as_float(r[24 + c]), 0.0625f, __uint_as_float(r[16 + c])) * over * fb, fb, v);
           if ((poison >> (c0 + c)) & 1u) v = __int_as_float(0x7FC00000);
           if (whole) {
             a.out[(int64_t)cm.at[c0 + c] * kKvDim + row] = __float2bfloat16_rn(v);

@@ -157,8 +157,10 @@ __device__ __forceinline__ bool pa_pieces(const PaRecord& r, int c, int ctas, in
   return true;
 }
 
-// Joins the pieces of the segments that CTA boundaries cut:
-//   out = sum_p w_p O_p,  w_p = 2^{m_p - M} / L,  L = sum_p 2^{m_p - M} l_p.
+// Joins the pieces of the segments that CTA boundaries cut, each an output o_p of its own keys:
+//   out = sum_p w_p o_p,  w_p = 2^{m_p - M} l_p / L,  L = sum_p 2^{m_p - M} l_p.
+// Pieces and running sum are weighted means of V throughout: V's scales go up to 2^120, and a sum over keys before its
+// division by L would leave fp32's range.
 // A block (c, y) handles the boundary in front of range c if it is the first that cuts its segment, and
 // columns 8 y .. 8 y + 7: a warp a column, four dims a lane.
 __device__ __forceinline__ void pa_join(const PagedAttnArgs& a, int ctas, int c, int y) {
@@ -192,16 +194,21 @@ __device__ __forceinline__ void pa_join(const PagedAttnArgs& a, int ctas, int c,
     float Mn = M;
 #pragma unroll
     for (int g = 0; g < kGroup; ++g) Mn = fmaxf(Mn, mj[g]);
-    const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn);
-    L *= sc;
-    acc.x *= sc;
-    acc.y *= sc;
-    acc.z *= sc;
-    acc.w *= sc;
+    const float Lo = M == -INFINITY ? 0.f : L * exp2f(M - Mn);
+    L = Lo;
 #pragma unroll
     for (int g = 0; g < kGroup; ++g) {
-      const float w = lj[g] == 0.f ? 0.f : exp2f(mj[g] - Mn);
-      L = fmaf(w, lj[g], L);
+      lj[g] = lj[g] == 0.f ? 0.f : lj[g] * exp2f(mj[g] - Mn);
+      L += lj[g];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L, w0 = Lo * inv;
+    acc.x *= w0;
+    acc.y *= w0;
+    acc.z *= w0;
+    acc.w *= w0;
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const float w = lj[g] * inv;
       acc.x = fmaf(w, x[g].x, acc.x);
       acc.y = fmaf(w, x[g].y, acc.y);
       acc.z = fmaf(w, x[g].z, acc.z);
@@ -209,10 +216,9 @@ __device__ __forceinline__ void pa_join(const PagedAttnArgs& a, int ctas, int c,
     }
     M = Mn;
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
   const int i = n / a.group;
   const int64_t at = (int64_t)(rec.row0 + i) * a.kv_heads * a.group + rec.h * a.group + (n - i * a.group);
-  const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), v1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc.x, acc.y), v1 = __floats2bfloat162_rn(acc.z, acc.w);
   reinterpret_cast<uint2*>(a.out + at * kKvDim)[lane] =
       make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
   if (a.lse && lane == 0) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;

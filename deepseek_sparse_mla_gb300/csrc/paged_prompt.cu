@@ -647,7 +647,9 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       const int64_t at = (int64_t)(s.row0 + r) * a.kv_heads * a.group + head;
       const int slot = s.slot;
       const float vref = v_ref[seg % kSegBufs];
-      const float f = !any ? 0.f : whole ? vref / l : vref;
+      // a mean of V before its scale comes in: sums over keys times the largest scales would leave fp32's range, and the smallest
+      // scales divided by the sums, too
+      const float inv = any ? 1.f / l : 0.f;
       const int* nk = nan_key[seg % kSegBufs];
 #pragma unroll 1
       for (int c = 0; c < kKvDim; c += 32) {
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           float x[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            x[k] = any ? __uint_as_float(o[k]) * f : 0.f;
+            x[k] = any ? __uint_as_float(o[k]) * inv * vref : 0.f;
             if (nk[c + k] < w.limit) x[k] = __int_as_float(0x7FC00000);
           }
           if (whole) {
@@ -1033,8 +1035,9 @@ __device__ __forceinline__ void pp_join(const PagedAttnArgs& a, int ctas, int c,
     for (int g = 0; g < kGroup; ++g) {
       if (ml[g].y == 0.f) continue;                        // a piece that sees nothing (NaN counts as seen)
       const float Mn = fmaxf(M, ml[g].x);
-      const float sc = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml[g].x - Mn);
-      L = L * sc + w * ml[g].y;
+      const float Lo = M == -INFINITY ? 0.f : L * exp2f(M - Mn), lg = ml[g].y * exp2f(ml[g].x - Mn);
+      L = Lo + lg;
+      const float inv = 1.f / L, sc = Lo * inv, w = lg * inv;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         acc[4 * k] = fmaf(w, x[g][k].x, acc[4 * k] * sc);
@@ -1045,13 +1048,12 @@ __device__ __forceinline__ void pp_join(const PagedAttnArgs& a, int ctas, int c,
       M = Mn;
     }
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
   const int i = n / a.group;
   const int64_t at = (int64_t)(rec.row0 + i) * a.kv_heads * a.group + rec.h * a.group + (n - i * a.group);
   uint4 v[2];
   __nv_bfloat162* xo = reinterpret_cast<__nv_bfloat162*>(v);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) xo[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  for (int e = 0; e < 8; ++e) xo[e] = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
   uint4* dst = reinterpret_cast<uint4*>(a.out + at * kKvDim) + 2 * y;
   dst[0] = v[0];
   dst[1] = v[1];

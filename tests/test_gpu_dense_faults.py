@@ -178,3 +178,36 @@ def test_a_prompts_values_are_held_to_a_share_of_the_requests_largest_scale():
     tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -9 + 2 * dz[..., None]) * A + 2.0 ** -25 * tops   # bf16, P's 11 bits and the sums, V
     assert np.all(np.abs(got - out) <= tol)
     assert np.all(np.abs(got_lse - lse) <= dz + 2.0 ** -20 * (1 + np.abs(lse)))
+
+
+FAR = {"decode": ([20000, 1100, 77], [1, 2, 2], 2, 8), "prompt": ([12000, 1100], [30, 45], 1, 8)}
+
+
+@pytest.mark.parametrize("k", [-119, -110, -80, 80, 110, 125])
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("shape", list(FAR))
+def test_values_of_any_size(shape, P, k):
+    """V's scales from 2^-126 to 2^119, with pieces of long requests to join: the output is that of scales near one, times a power
+    of two, up to the rounding of bf16's subnormal numbers."""
+    seq, new, kv, group = FAR[shape]
+    case = DenseCase(41, seq, new, P, kv, group, spread=0.0)
+    out, lse, A, C, Z = case.oracle()
+    assert np.abs(out).max() < 4.0 and case.scales["v"].min() >= 2.0 ** -7
+    tensors = case.gpu()
+    tensors[0].v_scales.copy_(put(np.ldexp(case.scales["v"], k).astype(np.float32)))
+    got, got_lse = attend(case, tensors)
+    C += 2.0 ** 18 * 2.0 ** (-134 - k)                       # half a step of those numbers (the bound takes 2^-18 of C)
+    check_attention(np.ldexp(got, -k), got_lse, (out, lse, A, C, Z))
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_the_most_requests_with_the_most_columns(many):
+    """The largest shared memory a call may ask for: 4,096 requests, most of them empty, and blocks of 32 columns."""
+    rng = np.random.default_rng(42)
+    seq = np.where(rng.random(4096) < 0.05, rng.integers(1, 200, 4096), 0)
+    new = np.minimum(seq, rng.integers(1, 3, 4096))
+    if many:
+        new[[17, 4000]] = seq[[17, 4000]] = 9, 30
+    case = DenseCase(42, seq.tolist(), new.tolist(), 16, 1, 32)
+    got, lse = attend(case)
+    check_attention(got, lse, case.oracle())
