@@ -476,12 +476,14 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     }
     const uint32_t before = block_sum(sum) - sum;
     for (int b = b0; b < b1; ++b) entry_end[b] += before;
+    if (b0 < b1 && b1 == B && (uint32_t)entry_end[B - 1] > most_entries) {
+      entry_end[B - 1] = 0;                            // no entries: nothing is taken
+      bits |= DSA_DEVICE_BAD_LENGTH;
+    }
     if (bits) atomicOr(&bits_all, bits);
   }
   __syncthreads();
-  const bool shared_rows = (uint32_t)entry_end[B - 1] > most_entries;
-  if (shared_rows && tid == 0) atomicOr(&bits_all, (uint32_t)DSA_DEVICE_BAD_LENGTH);
-  const int entries = shared_rows ? 0 : entry_end[B - 1];
+  const int entries = entry_end[B - 1];
   const int run = (entries + kRuns - 1) / kRuns;
   // the entry with index x
   auto find = [&](int x, PpCursor& c) {
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           float x[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            x[k] = any ? __uint_as_float(o[k]) * inv * vref : 0.f;
+            x[k] = __uint_as_float(o[k]) * inv * vref;
             if (nk[c + k] < w.limit) x[k] = __int_as_float(0x7FC00000);
           }
           if (whole) {

@@ -80,6 +80,6 @@ def test_the_sums_of_the_prompt_kernels_split_stay_in_32_bits():
     assert threads * (most + 1) < 2 ** 32
     text = source("paged_prompt.cu")
     assert "min(sum + pp_entries(a, pa_shape(a, b, bits)), most_entries + 1)" in text
-    assert re.search(r"const int entries = shared_rows \? 0 : entry_end\[B - 1\];", text)
+    assert re.search(r"entry_end\[B - 1\] > most_entries\) \{\s*entry_end\[B - 1\] = 0;", text)
     api = source("dsa_api.cu")
     assert "num_rows * q_heads > INT32_MAX / 2" in api and "num_rows * group / 256 + batch->num_requests" in api
