@@ -584,10 +584,10 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
         };
         // the exact maxima over the tile, where the references do not hold: they, and what was formed against them, move
         auto raise = [&]() {
-          // rolled: it runs for a segment's first tile, where a second copy of all columns' scores would have to come from L2
           // log2 of the key's scale, -126 for one of 0: 2^(m - mv) and its product with a probability below 4 stay finite
           const float lv = fmaxf(__log2f(fabsf(vs)), -126.f);
-          float mine = -INFINITY, mine_v = -INFINITY;
+          float mine = -INFINITY;
+          // rolled: it runs for a segment's first tile, where a second copy of all columns' scores would have to come from L2
 #pragma unroll 1
           for (int c0 = 0; c0 < kNC; c0 += 8) {
             float z[8];
@@ -597,8 +597,15 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
               const float r = warp_max_f32(z[c]);
               if (lane == c0 + c) mine = r;            // lane c of every warp ends up with column c's
             }
-            // a warp's 32 keys have one scale, but for pages of 16: there the maximum of z + lv may be another key's
-            if (a.log2_page == 4) {
+          }
+          // A warp's 32 keys have one scale, but for pages of 16: there the maximum of z + lv may be another key's.  (A loop
+          // of its own: inside the first one it took the verify case, whose pages are larger, 341 us instead of 334.)
+          float mine_v = mine + lv;
+          if (a.log2_page == 4) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < kNC; c0 += 8) {
+              float z[8];
+              scores8(z, c0);
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const float r = warp_max_f32(z[c] + lv);
@@ -606,7 +613,6 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
               }
             }
           }
-          if (a.log2_page != 4) mine_v = mine + lv;
           float* const wmax_v = reinterpret_cast<float*>(sP + wg * kPBytes);   // [4][kCE], before the tile's P is there
           if (lane < kCE) {
             wmax[wg][quarter][lane] = mine;
