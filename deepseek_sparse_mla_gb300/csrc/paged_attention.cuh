@@ -12,8 +12,9 @@ namespace dsa {
 
 constexpr int kPaTok = 128;          // keys per tile
 
-// Rows, first row and readable keys of request b.  rows is 0 where the call leaves the request alone: no rows, more
-// than max_rows (reported), or a number of (row, head) pairs outside (lo, hi], which the other kernel takes.
+// Rows, first row and readable keys of request b.  rows is 0 where the call leaves the request alone: no rows, more than
+// max_rows or rows that the batch does not have (reported), or a number of (row, head) pairs outside (lo, hi], which the
+// other kernel takes.
 struct PaShape {
   int rows, row0, len, tiles;        // tiles: of 128 keys, at least one
 };
@@ -25,8 +26,8 @@ __device__ __forceinline__ PaShape pa_shape(const PagedAttnArgs& a, int b, uint3
   if (a.query_start_loc) {
     s.row0 = a.query_start_loc[b];
     const int64_t d = (int64_t)a.query_start_loc[b + 1] - s.row0;
-    if (d <= 0 || s.row0 < 0 || s.row0 + d > a.num_rows) return s;
-    if (d > a.max_rows) {
+    if (d == 0) return s;
+    if (d < 0 || d > a.max_rows || s.row0 < 0 || s.row0 + d > a.num_rows) {
       bits |= DSA_DEVICE_BAD_LENGTH;
       return s;
     }

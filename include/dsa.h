@@ -588,8 +588,8 @@ typedef struct {
  *   q_heads    a multiple of kv_heads, at most DSA_MAX_GROUP per K/V head.
  *   max_query_len  host upper bound on every request's rows (a request with more is refused on the
  *              device: DSA_DEVICE_BAD_LENGTH, its rows are left as they were).
- *              Starts ascend; where they run back, so that requests of more than 64 rows * heads per K/V head
- *              name the same rows over and over, those are refused alike.
+ *              So is one whose offsets run back or leave the batch's rows; and where offsets that run back make
+ *              requests of more than 64 rows * heads per K/V head name the same rows over and over, all of those are.
  *   out        device bf16 [num_rows, q_heads, 128]; lse fp32 [num_rows, q_heads] or NULL.
  *   workspace  dsa_paged_attention_workspace_bytes(), 256-byte aligned; calls that may run at the same
  *              time take one each.

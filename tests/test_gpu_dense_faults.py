@@ -211,3 +211,23 @@ def test_the_most_requests_with_the_most_columns(many):
     case = DenseCase(42, seq.tolist(), new.tolist(), 16, 1, 32)
     got, lse = attend(case)
     check_attention(got, lse, case.oracle())
+
+
+@pytest.mark.parametrize("new", [[3, 2, 4], [40, 30, 50]])
+def test_offsets_that_run_back_or_leave_the_batch_are_reported(new):
+    import deepseek_sparse_mla_gb300 as dsa
+    case = DenseCase(43, [300, 77, 129], new, 32, 2, 8)
+    cache, batch, q = case.gpu()
+    end = int(case.starts[2])                                # the first two requests' rows
+    want = [np.array(x) for x in case.oracle()]
+    want[4][end:] = np.nan                                   # what is not compared
+    for last in (end - 1, case.rows + 1, -5):
+        batch.query_start_loc[3] = last
+        with pytest.raises(dsa.DsaError, match="BAD_LENGTH"):
+            attend(case, (cache, batch, q))
+        got, lse = attend(case, (cache, batch, q), check=False)
+        check_attention(got, lse, want)
+        assert np.all(got[end:] == -7.0) and np.all(lse[end:] == -7.0)
+    batch.query_start_loc.copy_(put(case.starts - 1))        # the first request's rows begin before the batch's
+    with pytest.raises(dsa.DsaError, match="BAD_LENGTH"):
+        attend(case, (cache, batch, q))
