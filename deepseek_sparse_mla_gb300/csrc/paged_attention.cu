@@ -66,7 +66,7 @@ constexpr uint32_t kColO = 256;
 constexpr int kSBufs = 4;                       // two a warpgroup: one is kept until its tile is known to be done
 constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
-constexpr uint32_t kPolls = 1u << 11;           // of a millisecond at most
+constexpr uint32_t kPolls = 1u << 18;           // of 3.8 us each or more: a second
 constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 }  // namespace pa
 
@@ -380,6 +380,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   } else {
     // ---------------------------------------------------------------- queries
     int seg = 0;
+    // This warp runs up to kQBufs segments ahead and then waits for a whole one to end, which may be long: 57 ms for 2^22
+    // tokens and 32 columns.  Every tile of the range adds two polls, four times what one takes.
+    const uint32_t polls = kPolls + 2u * (uint32_t)min(max(u1 - u0, (int64_t)0), int64_t(1) << 29);
     for (int64_t u = u0; u < u1; ++seg) {
       const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const int start = a.seq_lens[s.b] - s.rows;      // position of row 0
       const int prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
       const float slope = kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f;
-      if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kPolls)) break;
+      if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, polls)) break;
       uint8_t* q_hi = sQ + buf * kQBytes;
       PaColumns& cm = cols[buf];
       // then the values, 16 lanes a column: eight columns a step, the next eight on their way; a rolled loop, as code that a

@@ -231,3 +231,40 @@ def test_offsets_that_run_back_or_leave_the_batch_are_reported(new):
     batch.query_start_loc.copy_(put(case.starts - 1))        # the first request's rows begin before the batch's
     with pytest.raises(dsa.DsaError, match="BAD_LENGTH"):
         attend(case, (cache, batch, q))
+
+
+def repeated(seed, heads, rows):
+    """64 pages of 128 tokens that requests of 2^22 tokens repeat 512 times, and what rows at the end of such a request get."""
+    rng = np.random.default_rng(seed)
+    case = DenseCase(seed, [8192], [rows], 128, 1, heads, spread=0.5)
+    k = o.e4m3_to_f64(case.codes["k"][case.table[0, :64], 0]) * case.scales["k"][case.table[0, :64], 0][:, None, None].astype(np.float64)
+    v = o.e4m3_to_f64(case.codes["v"][case.table[0, :64], 0]) * case.scales["v"][case.table[0, :64], 0][:, None, None].astype(np.float64)
+    k, v = k.reshape(-1, 128), v.reshape(-1, 128)
+    out, A, lse = np.zeros((rows, heads, 128)), np.zeros((rows, heads, 128)), np.zeros((rows, heads))
+    for r in range(rows):
+        times = np.where(np.arange(8192) < 8192 - rows + r + 1, 512.0, 511.0)     # the last keys once less, where the row is before
+        for h in range(heads):
+            z = (k @ case.q[r, h]) * 128 ** -0.5
+            w = np.exp(z) * times
+            lse[r, h] = np.log(w.sum())
+            out[r, h], A[r, h] = w @ v / w.sum(), w @ np.abs(v) / w.sum()
+    return case, out, lse, A
+
+
+def test_many_long_requests():
+    """608 requests of 2^22 tokens, four to a CTA: the queries are ready three requests ahead, and wait 57 ms for the next."""
+    import torch
+    import deepseek_sparse_mla_gb300 as dsa
+    case, out, lse, A = repeated(44, 8, 4)
+    cache, _, q = case.gpu()
+    B, L = 608, 1 << 22
+    table = put(np.tile(case.table[0, :64], (B, L // 8192)).astype(np.int32))
+    batch = dsa.Batch(table, torch.full((B,), L, dtype=torch.int32, device="cuda"), put((np.arange(B + 1) * 4).astype(np.int32)),
+                      num_rows=4 * B, max_seq_len=L)
+    got_lse = torch.zeros((4 * B, 8), dtype=torch.float32, device="cuda")
+    got, _ = dsa.paged_attention(cache, batch, q.repeat(B, 1, 1), max_query_len=4, lse=got_lse, check=True)
+    got = o.bf16_to_f64(wlm.torch_to_bits(got)).reshape(B, 4, 8, 128)
+    got_lse = got_lse.cpu().numpy().astype(np.float64).reshape(B, 4, 8)
+    # two e4m3 terms of a contribution and bf16's half step, 2^-8 each; 2^-20 of the largest contribution times 2^10, for the sums of 2^15 tiles
+    assert np.all(np.abs(got - out) <= 2.0 ** -8 * np.abs(out) + 2.0 ** -7 * A + 2.0 ** -10)
+    assert np.all(np.abs(got_lse - lse) <= 2.0 ** -13 * 14)
