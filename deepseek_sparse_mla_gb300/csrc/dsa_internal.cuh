@@ -271,6 +271,7 @@ struct PagedAttnArgs {
   float* lse;
   int32_t max_rows;                 // of a request; one with more is refused
   bool whole;                       // segments are not cut (no pieces to join)
+  bool early;                       // the kernel for many rows may start before the one for few has ended
   int32_t lo_pairs, hi_pairs;       // a kernel takes requests of lo < rows * group <= hi pairs
   uint32_t* err;                    // the workspace header
   int32_t* rec;                     // [ctas][8]: where each CTA's first piece lies

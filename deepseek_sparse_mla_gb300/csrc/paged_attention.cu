@@ -67,6 +67,9 @@ constexpr int kSBufs = 4;                       // two a warpgroup: one is kept 
 constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
 constexpr uint32_t kPolls = 1u << 18;           // of 3.8 us each or more: a second
+// The query warp runs up to kQBufs segments ahead and then waits for a whole one to end: 57 ms for 2^22 tokens and 32
+// columns, 15 s for 2^30.
+constexpr uint32_t kSegPolls = 1u << 24;
 constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 }  // namespace pa
 
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   pdl_wait();
   // The prompt kernel may start as SMs fall free (mixed batch 107 -> 98 us in a replayed graph).  A join may not: its CTAs
   // coming early cost 32 requests at 8K 2 us.
-  if (a.hi_pairs != INT32_MAX) pdl_trigger();
+  if (a.early) pdl_trigger();
   if (tid == 0) reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;   // no piece to join until it has been written
   // running sums of the requests' units: every thread a run of consecutive requests
   {
@@ -380,9 +383,6 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
   } else {
     // ---------------------------------------------------------------- queries
     int seg = 0;
-    // This warp runs up to kQBufs segments ahead and then waits for a whole one to end, which may be long: 57 ms for 2^22
-    // tokens and 32 columns.  Every tile of the range adds two polls, four times what one takes.
-    const uint32_t polls = kPolls + 2u * (uint32_t)min(max(u1 - u0, (int64_t)0), int64_t(1) << 29);
     for (int64_t u = u0; u < u1; ++seg) {
       const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
       const int start = a.seq_lens[s.b] - s.rows;      // position of row 0
       const int prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
       const float slope = kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f;
-      if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, polls)) break;
+      if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kSegPolls)) break;
       uint8_t* q_hi = sQ + buf * kQBytes;
       PaColumns& cm = cols[buf];
       // then the values, 16 lanes a column: eight columns a step, the next eight on their way; a rolled loop, as code that a
@@ -915,6 +915,9 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, cons
   a.whole = max_seq_len <= 8 * kPaTok;
   a.lo_pairs = 0;
   a.hi_pairs = plan.prompt ? kPagedAttnDirect : INT32_MAX;
+  // The prompt kernel's warps wait for each other with a bound of a second, and its writers for this kernel's end, so they
+  // start early only where this kernel's CTAs cannot differ by as much: 2^23 tiles are 0.3 s of work for all of them.
+  a.early = plan.prompt && (int64_t)a.num_requests * ((max_seq_len + kPaTok - 1) / kPaTok) * a.kv_heads * 2 <= int64_t(1) << 23;
   a.part_ml = a.part_o + (size_t)2 * ctas * kPagedAttnColumns * kKvDim;
   const uint64_t rows = (uint64_t)a.num_pages * a.kv_heads << a.log2_page;
   CUtensorMap k_map, v_map;

@@ -52,7 +52,7 @@ constexpr uint32_t kRegsSoft = 128, kRegsConv = 80, kRegsRest = 64;   // 2 * 128
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
-constexpr uint32_t kPolls = 1u << 11;                // of a millisecond at most
+constexpr uint32_t kPolls = 1u << 18;                // of 3.8 us each or more: a second
 // A segment counts as this many tiles beside its own: loading its queries and writing its outputs is not hidden.  (2
 // prompts of 1,633 rows and 64 heads, 1 to 13 tiles a segment: 217 us; without, 390.)  Capped and biased tiles take
 // longer, so their segments' ends weigh less.

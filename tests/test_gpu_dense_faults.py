@@ -233,38 +233,54 @@ def test_offsets_that_run_back_or_leave_the_batch_are_reported(new):
         attend(case, (cache, batch, q))
 
 
-def repeated(seed, heads, rows):
-    """64 pages of 128 tokens that requests of 2^22 tokens repeat 512 times, and what rows at the end of such a request get."""
-    rng = np.random.default_rng(seed)
-    case = DenseCase(seed, [8192], [rows], 128, 1, heads, spread=0.5)
-    k = o.e4m3_to_f64(case.codes["k"][case.table[0, :64], 0]) * case.scales["k"][case.table[0, :64], 0][:, None, None].astype(np.float64)
-    v = o.e4m3_to_f64(case.codes["v"][case.table[0, :64], 0]) * case.scales["v"][case.table[0, :64], 0][:, None, None].astype(np.float64)
-    k, v = k.reshape(-1, 128), v.reshape(-1, 128)
-    out, A, lse = np.zeros((rows, heads, 128)), np.zeros((rows, heads, 128)), np.zeros((rows, heads))
-    for r in range(rows):
-        times = np.where(np.arange(8192) < 8192 - rows + r + 1, 512.0, 511.0)     # the last keys once less, where the row is before
-        for h in range(heads):
-            z = (k @ case.q[r, h]) * 128 ** -0.5
-            w = np.exp(z) * times
-            lse[r, h] = np.log(w.sum())
-            out[r, h], A[r, h] = w @ v / w.sum(), w @ np.abs(v) / w.sum()
-    return case, out, lse, A
+class Repeated:
+    """64 pages of 128 tokens that long requests have over and over, queries, and what a row gets that sees all tokens of
+    `times` rounds but the last `missing`."""
+
+    def __init__(self, seed, rows):
+        self.case = DenseCase(seed, [8192], [rows], 128, 1, 8, spread=0.5)
+        pages = self.case.table[0, :64]
+        self.k, self.v = ((o.e4m3_to_f64(self.case.codes[n][pages, 0]) * self.case.scales[n][pages, 0][:, None, None].astype(np.float64))
+                          .reshape(-1, 128) for n in "kv")
+        self.z = np.einsum("kd,rhd->rhk", self.k, self.case.q) * 128 ** -0.5
+
+    def row(self, r, times, missing):
+        w = np.exp(self.z[r]) * np.where(np.arange(8192) < 8192 - missing, times, times - 1.0)
+        total = w.sum(1)
+        return w @ self.v / total[:, None], np.log(total), w @ np.abs(self.v) / total[:, None]
+
+    def run(self, kinds):
+        """A call over requests of (count, rounds, rows); outputs and lse are checked for one of each kind, and all of a kind are
+        equal up to the rounding of pieces and their sums."""
+        import torch
+        import deepseek_sparse_mla_gb300 as dsa
+        cache, _, q = self.case.gpu()
+        B, most, rows = sum(n for n, _, _ in kinds), max(t for _, t, _ in kinds), sum(n * r for n, _, r in kinds)
+        table = put(np.tile(self.case.table[0, :64], (1, most)).astype(np.int32)).expand(B, 64 * most).contiguous()
+        lens = np.concatenate([np.full(n, 8192 * t) for n, t, _ in kinds]).astype(np.int32)
+        starts = np.concatenate([[0], np.cumsum(np.concatenate([np.full(n, r) for n, _, r in kinds]))]).astype(np.int32)
+        batch = dsa.Batch(table, put(lens), put(starts), num_rows=rows, max_seq_len=8192 * most)
+        q = torch.cat([q[:r].repeat(n, 1, 1) for n, _, r in kinds])
+        lse = torch.zeros((rows, 8), dtype=torch.float32, device="cuda")
+        out, _ = dsa.paged_attention(cache, batch, q, max_query_len=max(r for _, _, r in kinds), lse=lse, check=True)
+        out, lse = o.bf16_to_f64(wlm.torch_to_bits(out)), lse.cpu().numpy().astype(np.float64)
+        at = 0
+        for n, t, r in kinds:
+            got, got_lse = out[at:at + n * r].reshape(n, r, 8, 128), lse[at:at + n * r].reshape(n, r, 8)
+            at += n * r
+            for i in range(r):
+                want, want_lse, A = self.row(i, float(t), r - 1 - i)
+                # two e4m3 terms of a contribution and bf16's half step, 2^-8 each, and the sums over up to 2^15 tiles
+                assert np.all(np.abs(got[:, i] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -7 * A + 2.0 ** -10)
+                assert np.all(np.abs(got_lse[:, i] - want_lse) <= 2.0 ** -13 * 14)
 
 
 def test_many_long_requests():
     """608 requests of 2^22 tokens, four to a CTA: the queries are ready three requests ahead, and wait 57 ms for the next."""
-    import torch
-    import deepseek_sparse_mla_gb300 as dsa
-    case, out, lse, A = repeated(44, 8, 4)
-    cache, _, q = case.gpu()
-    B, L = 608, 1 << 22
-    table = put(np.tile(case.table[0, :64], (B, L // 8192)).astype(np.int32))
-    batch = dsa.Batch(table, torch.full((B,), L, dtype=torch.int32, device="cuda"), put((np.arange(B + 1) * 4).astype(np.int32)),
-                      num_rows=4 * B, max_seq_len=L)
-    got_lse = torch.zeros((4 * B, 8), dtype=torch.float32, device="cuda")
-    got, _ = dsa.paged_attention(cache, batch, q.repeat(B, 1, 1), max_query_len=4, lse=got_lse, check=True)
-    got = o.bf16_to_f64(wlm.torch_to_bits(got)).reshape(B, 4, 8, 128)
-    got_lse = got_lse.cpu().numpy().astype(np.float64).reshape(B, 4, 8)
-    # two e4m3 terms of a contribution and bf16's half step, 2^-8 each; 2^-20 of the largest contribution times 2^10, for the sums of 2^15 tiles
-    assert np.all(np.abs(got - out) <= 2.0 ** -8 * np.abs(out) + 2.0 ** -7 * A + 2.0 ** -10)
-    assert np.all(np.abs(got_lse - lse) <= 2.0 ** -13 * 14)
+    Repeated(44, 4).run([(608, 512, 4)])
+
+
+def test_prompts_beside_long_requests_that_keep_some_ctas_longer():
+    """Requests of one row and of eight have tiles of different cost: the first CTAs are done 10 ms and more before the last, and
+    the prompts' kernel starts on their SMs, with more than one prompt each, before it may write."""
+    Repeated(45, 16).run([(304, 64, 1), (76, 64, 8), (400, 1, 16)])
