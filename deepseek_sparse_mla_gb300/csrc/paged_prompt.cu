@@ -53,6 +53,10 @@ constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
 constexpr uint32_t kPolls = 1u << 18;                // of 3.8 us each or more: a second
+// Rolled: with four polls written out at each of the many waits, 4,096 rows at 64K take 3.33 ms instead of 3.01.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code, uint32_t polls) {
+  return mbar_wait_warp<1>(bar, parity, err, code, polls);
+}
 // A segment counts as this many tiles beside its own: loading its queries and writing its outputs is not hidden.  (2
 // prompts of 1,633 rows and 64 heads, 1 to 13 tiles a segment: 217 us; without, 390.)  Capped and biased tiles take
 // longer, so their segments' ends weigh less.
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       return cf;
     };
     int i = 0;
-    bool ok = mbar_wait_warp(&seg_full[0], 0, err, kErrMmaTimeout, kPolls);
+    bool ok = wait_warp(&seg_full[0], 0, err, kErrMmaTimeout, kPolls);
     float cf = 0.f;
     if (ok && segs[0].n) cf = load_queries(segs[0]);
     for (int seg = 0; ok; ++seg) {
@@ -588,7 +592,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           w.m = m_new;
           if (t > 0 || h > 0) {
             // the accumulator is settled when the 64 keys before have been added
-            ok = mbar_wait_warp(&pv_done[q][h ^ 1], (i - 1 + h) & 1, err, kErrMmaTimeout, kPolls);
+            ok = wait_warp(&pv_done[q][h ^ 1], (i - 1 + h) & 1, err, kErrMmaTimeout, kPolls);
             if (!ok) return false;
             tc_fence_after();
             pp_shrink(tO, al);
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
 #pragma unroll 1
         for (int h = 0; h < 2 && ok; ++h) {
           // the scores' arrival also stands for the tile's scales: K's own barrier may be a phase further by now
-          ok = mbar_wait_warp(&s_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
+          ok = wait_warp(&s_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
           if (!ok) break;
           tc_fence_after();
           const uint32_t bad = sbad[i % kMetaBufs];
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       }
       if (!ok) break;
       const int nx = (seg + 1) % kSegBufs;
-      ok = mbar_wait_warp(&seg_full[nx], ((seg + 1) / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+      ok = wait_warp(&seg_full[nx], ((seg + 1) / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
       if (segs[nx].n) cf = load_queries(segs[nx]);
       if (seg == 0) {
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       }
       // ---- the segment's end
       const bool whole = s.n == s.tiles;
-      ok = mbar_wait_warp(&o_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
+      ok = wait_warp(&o_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
       tc_fence_after();
       const float m = w.m, l = w.l;
@@ -716,7 +720,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     int i0 = 0;                                        // the CTA's tiles before this segment
     bool ok = true;
     for (int seg = 0;; ++seg) {
-      ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+      ok = wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
       const PpSeg s = segs[seg % kSegBufs];
       __syncwarp();
@@ -773,7 +777,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       if (t < s.n) load(s.tile_at(t) * kTok);
       for (; t < s.n; t += 2) {
         const int key0 = s.tile_at(t) * kTok, i = i0 + t;
-        if (i >= 2) ok = mbar_wait_warp(&v_empty[grp], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+        if (i >= 2) ok = wait_warp(&v_empty[grp], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         // NaN codes of a tile that only some rows see in full
         uint32_t any_nan = 0;
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       bool ok = true;
       int i = 0;
       for (int seg = 0;; ++seg) {
-        ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+        ok = wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         const int n = segs[seg % kSegBufs].n;
         __syncwarp();
@@ -845,13 +849,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (n == 0) break;
         for (int t = 0; t < n && ok; ++t, ++i) {
           const uint64_t v = d_v + (uint64_t)(((i & 1) * kVBytes) >> 4);
-          ok = mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
+          ok = wait_warp(&v_full[i & 1], (i >> 1) & 1, err, kErrMmaTimeout, kPolls);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              if (t == 0 && h == 0 && seg > 0) ok = ok && mbar_wait_warp(&o_empty[q], (seg - 1) & 1, err, kErrMmaTimeout, kPolls);
-              ok = ok && mbar_wait_warp(&p_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
+              if (t == 0 && h == 0 && seg > 0) ok = ok && wait_warp(&o_empty[q], (seg - 1) & 1, err, kErrMmaTimeout, kPolls);
+              ok = ok && wait_warp(&p_full[q][h], i & 1, err, kErrMmaTimeout, kPolls);
               if (!ok) break;
               tc_fence_after();
               if (leader) {
@@ -872,7 +876,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (!ok) break;
       }
       if (leader) mma_commit(&mma_done);
-      mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+      wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
     } else if (warp < kLoadWarp) {
       // ---------------------------------------------------------------- score products of one half
       const int q = warp - kScoreWarp0;
@@ -883,20 +887,20 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       bool ok = true;
       int i = 0;
       for (int seg = 0;; ++seg) {
-        ok = mbar_wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
+        ok = wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         const int n = segs[seg % kSegBufs].n;
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
         if (n == 0) break;
-        ok = mbar_wait_warp(&q_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
+        ok = wait_warp(&q_full[q], seg & 1, err, kErrMmaTimeout, kPolls);
         for (int t = 0; t < n && ok; ++t, ++i) {
           const int st = i % kKStages;
-          ok = mbar_wait_warp(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout, kPolls);
+          ok = wait_warp(&k_full[st], (i / kKStages) & 1, err, kErrTmaTimeout, kPolls);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // S takes the place of the P of the tile before, once O has read it
-            if (i > 0) ok = ok && mbar_wait_warp(&pv_done[q][h], (i - 1) & 1, err, kErrMmaTimeout, kPolls);
+            if (i > 0) ok = ok && wait_warp(&pv_done[q][h], (i - 1) & 1, err, kErrMmaTimeout, kPolls);
             if (!ok) break;
             tc_fence_after();
             const uint64_t k = d_k + (uint64_t)((st * kKBytes + 64 * h * kKvDim) >> 4);
@@ -915,7 +919,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         if (!ok) break;
       }
       if (leader) mma_commit(&mma_done);
-      mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
+      wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
     } else {
       // ---------------------------------------------------------------- segments (and an end mark), and their K tiles
       const uint64_t policy = l2_evict_normal();
@@ -925,7 +929,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       int64_t u = u0;
       bool ok = true;
       for (int seg = 0;; ++seg) {
-        if (seg >= kSegBufs) ok = mbar_wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls);
+        if (seg >= kSegBufs) ok = wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         PpSeg s = {};
         // segments are cut where the range ends, or (short requests) belong as a whole to the range with their first tile
@@ -967,7 +971,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             ks = page >= 0 ? a.k_scales[(int64_t)page * a.kv_heads + s.h] : 0.f;
           }
           const int st = i % kKStages, use = i / kKStages;
-          if (use > 0) ok = mbar_wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls);
+          if (use > 0) ok = wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls);
           if (!ok) break;
           const int o = p0 & 31;
           const int pg = __shfl_sync(0xffffffffu, page, (o + lane) & 31);
@@ -989,7 +993,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       }
       // nothing may still be landing in shared memory when the CTA exits
       for (int st = 0; st < kKStages; ++st)
-        if (i > st) mbar_wait_warp(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
+        if (i > st) wait_warp(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
     }
   }
   tc_fence_before();

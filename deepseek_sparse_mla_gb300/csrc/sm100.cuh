@@ -102,9 +102,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 // mbar_wait for a whole warp that goes on with warp-wide operations: every lane gets the same answer, also where
 // the polls run out just as the phase completes.  Each poll suspends the warp for 3.8 us (measured for a
 // warp alone; the hint of a millisecond is an upper bound): many warps that poll a shared-memory barrier in short turns delay
-// every other access to shared memory (a softmax warp's single load took 1,000 cycles beside a dozen of them).
+// every other access to shared memory (a softmax warp's single load took 1,000 cycles beside a dozen of them).  kUnroll:
+// polls written out one after the other; how many suit a kernel is a matter of its code's size and registers.
+template <int kUnroll = 4>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code,
                                                uint32_t max_polls) {
+#pragma unroll kUnroll
   for (uint32_t i = 0; i < max_polls; ++i) {
     uint32_t ok;
     asm volatile(
