@@ -789,23 +789,15 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           any_nan &= 0x80808080u;
         }
         const float ratio = scale * vinv;
-        auto widen = [&](auto scaled) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            uint4 lo = widen8(x[g].x, x[g].y), hi = widen8(x[g].z, x[g].w);
-            if constexpr (decltype(scaled)::value) {
-              const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, g));
-              lo = make_uint4(mul2(lo.x, f), mul2(lo.y, f), mul2(lo.z, f), mul2(lo.w, f));
-              hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
-            }
-            *reinterpret_cast<uint4*>(tile + 2048 * g + at_lo) = lo;
-            *reinterpret_cast<uint4*>(tile + 2048 * g + at_hi) = hi;
-          }
-        };
-        // a tile whose pages all have the reference's scale needs no factors (4,096 rows at 64K over such pages: 3.31 ms
-        // instead of 3.39)
-        if (__all_sync(0xffffffffu, ratio == 1.f)) widen(std::false_type{});
-        else widen(std::true_type{});
+        for (int g = 0; g < 8; ++g) {
+          const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio, g));
+          uint4 lo = widen8(x[g].x, x[g].y), hi = widen8(x[g].z, x[g].w);
+          lo = make_uint4(mul2(lo.x, f), mul2(lo.y, f), mul2(lo.z, f), mul2(lo.w, f));
+          hi = make_uint4(mul2(hi.x, f), mul2(hi.y, f), mul2(hi.z, f), mul2(hi.w, f));
+          *reinterpret_cast<uint4*>(tile + 2048 * g + at_lo) = lo;
+          *reinterpret_cast<uint4*>(tile + 2048 * g + at_hi) = hi;
+        }
         if (any_nan) {
           // out of the tile, and noted for the rows that see the key
 #pragma unroll 1
