@@ -280,8 +280,8 @@ struct PagedAttnArgs {
 };
 constexpr int kPagedAttnColumns = 32;     // (row, head) pairs of a K/V head taken together, at most
 // Requests of more pairs (rows times heads per K/V head) go to the prompt kernel, which takes 256 at a time.  Few-row kernel
-// against prompt kernel, 8 requests of up to 60,000 tokens and 4 K/V heads: 40 pairs 152 and 190 us, 64 pairs
-// 162 and 193, 96 pairs 214 and 196, 128 pairs 274 and 198.
+// against prompt kernel, 8 requests of up to 60,000 tokens and 4 K/V heads: 40 pairs 148 and 154 us, 64 pairs
+// 159 and 155, 96 pairs 211 and 157, 128 pairs 271 and 159.
 constexpr int kPagedAttnDirect = 64;
 constexpr int kPromptPairs = 256;         // pairs that it takes together
 struct PagedAttnPlan {

@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(pa::kThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  // The prompt kernel may start as SMs fall free (mixed batch 107 -> 98 us in a replayed graph).  A join may not: its CTAs
-  // coming early cost 32 requests at 8K 2 us.
+  // The prompt kernel may start as SMs fall free (3 pieces of 700 rows over up to 9,000 tokens 380 instead of 400 us; the mixed
+  // capped batch 95 instead of 93, both in replayed graphs).  A join may not: its CTAs coming early cost 32 requests at 8K
+  // 2 us.
   if (a.early) pdl_trigger();
   if (tid == 0) reinterpret_cast<PaRecord*>(a.rec)[cta].tile = -1;   // no piece to join until it has been written
   // running sums of the requests' units: every thread a run of consecutive requests
@@ -910,14 +911,14 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, cons
   a.rec = reinterpret_cast<int32_t*>(ws + plan.rec_offset);
   a.part_o = reinterpret_cast<float*>(ws + plan.part_offset);
   // Requests of at most 1,024 keys are not cut: a CTA takes such a segment in less time than a second launch to join
-  // its pieces would (one request of 300 keys: 17.5 instead of 27 us; 4 prompts of 1,000 rows: 101 instead of 112; a single
-  // prompt of 1,000 rows and one K/V head, which leaves most SMs idle: 37.5 instead of 32).
+  // its pieces would (in replayed graphs, one request of 300 keys: 10.4 instead of 19.8 us; 4 prompts of 1,000 rows: 89 instead
+  // of 97; a single prompt of 1,000 rows and one K/V head, which leaves most SMs idle: 35.1 instead of 31.4).
   a.whole = max_seq_len <= 8 * kPaTok;
   a.lo_pairs = 0;
   a.hi_pairs = plan.prompt ? kPagedAttnDirect : INT32_MAX;
   // The prompt kernel's warps wait for each other with a bound of a second, and its writers for this kernel's end, so they
   // start early only where this kernel's CTAs cannot differ by as much: 2^23 tiles are 0.3 s of work for all of them.
-  a.early = plan.prompt && (int64_t)a.num_requests * ((max_seq_len + kPaTok - 1) / kPaTok) * a.kv_heads * 2 <= int64_t(1) << 23;
+  a.early = plan.prompt && (int64_t)a.num_requests * (((int64_t)max_seq_len + kPaTok - 1) / kPaTok) * a.kv_heads * 2 <= int64_t(1) << 23;
   a.part_ml = a.part_o + (size_t)2 * ctas * kPagedAttnColumns * kKvDim;
   const uint64_t rows = (uint64_t)a.num_pages * a.kv_heads << a.log2_page;
   CUtensorMap k_map, v_map;

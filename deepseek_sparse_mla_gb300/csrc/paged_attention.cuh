@@ -84,7 +84,7 @@ cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few
 //   large caps: an error of the cap's size would be one of 0.1 at a cap of 1e6, and past 1e8 every score would be 0.  Where
 //   |z / cap| is below 0.3 the odd series takes over, t - t^3/3 + 2 t^5/15 - 17 t^7/315 + 62 t^9/2835 with t = z / cap =
 //   ln(2) / 2 y: the next term is below 2^-24 of the score, and a score is held to 2^-21 of itself.
-// The series' eight instructions a score cost the mixed capped batch 118 us instead of 102, and 109 even where a branch steps
+// The series' eight instructions a score cost the mixed capped batch 110 us instead of 95, and 6 % even where a branch steps
 // around them, so kernels for large caps are compiled apart.
 constexpr float kLargeCap = 64.f * 1.44269504f;         // log2 units
 enum PaMods : int { kPaPlain, kPaCapBias, kPaLargeCap };   // plain scores; a cap, a distance bias or both; with a large cap

@@ -20,10 +20,10 @@
 // cross-lane work at all).  A half goes through a tile as two times 64 keys, each with its own 64 columns of TMEM
 // for S and then P: while the softmax works on one, the tensor cores add the other to O and compute the next
 // tile's S in its place.  One S of 128 keys a half, its softmax and its products taking turns, took 4,500
-// cycles a tile (3.8 ms for 4,096 rows at 64K); the scores' products are a half slower at 64 keys, which this
-// more than pays for.  Warp 16 issues the output products, warps 17 and 18 one half's scores each, as soon as
+// cycles a tile (a quarter longer for 4,096 rows at 64K); the scores' products are a half slower at 64 keys, which
+// this more than pays for.  Warp 16 issues the output products, warps 17 and 18 one half's scores each, as soon as
 // the output product that read the P in their place is known to be done (products of different kinds are not
-// promised to run in order; one warp a half for both kinds, waiting for that, took 3.57 ms instead of 3.31).
+// promised to run in order; one warp a half for both kinds, waiting for that, took 8 % longer).
 // Warps 8-11 and 12-15 widen the V tiles, even and odd ones; warp 19 loads K tiles by TMA and finds the CTA's
 // segments for everyone (each role finding them for itself cost 30 registers, and spills).
 // TMEM (all 512 columns): S of half q and key half h at 128 q + 64 h, with P over its first 32; O of half q at 256 + 128 q.
@@ -53,12 +53,13 @@ constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
 constexpr uint32_t kPolls = 1u << 18;                // of 3.8 us each or more: a second
-// Rolled: with four polls written out at each of the many waits, 4,096 rows at 64K take 3.33 ms instead of 3.01.
+// Rolled: four polls written out at each of the many waits take 10 % longer (4,096 rows at 64K, 3.30 instead of 2.98 ms when
+// measured).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code, uint32_t polls) {
   return mbar_wait_warp<1>(bar, parity, err, code, polls);
 }
 // A segment counts as this many tiles beside its own: loading its queries and writing its outputs is not hidden.  (2
-// prompts of 1,633 rows and 64 heads, 1 to 13 tiles a segment: 217 us; without, 390.)  Capped and biased tiles take
+// prompts of 1,633 rows and 64 heads, 1 to 13 tiles a segment: 175 us; without, 358.)  Capped and biased tiles take
 // longer, so their segments' ends weigh less.
 constexpr int kSegUnits = 4, kModsSegUnits = 2;
 constexpr int kRuns = 512;                           // runs of (request, pairs) entries that are summed

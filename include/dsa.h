@@ -556,7 +556,10 @@ typedef struct {
  * grouped into calls, by roundings of codes below 2^-6 only.
  *   k, v      device bf16, token t's heads at k + t * k_stride (elements): [kv_heads, 128] contiguous,
  *             16-byte aligned, strides a multiple of 8 and at least kv_heads * 128.
- * A page that is written belongs to one request and stands once in its table row.  Out-of-range page ids are skipped.
+ * A page that is written belongs to one request and stands once in its table row.  Tokens whose page id is out of range or
+ * whose table row is too short are skipped, and so are requests with more rows than tokens or with offsets that do not fit
+ * the batch.  The call has no status of its own, like dsa_kv_append: dsa_paged_attention over the same batch
+ * reports bad ids and short rows (DSA_DEVICE_BAD_PAGE) and such offsets (DSA_DEVICE_BAD_LENGTH).
  */
 DSA_API dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride,
                                   const void* v, int64_t v_stride, void* stream);
@@ -566,8 +569,10 @@ DSA_API size_t dsa_paged_attention_workspace_bytes(int32_t q_heads, int32_t kv_h
 
 /*
  * What a dense attention call may add to the plain causal form (all optional).
- *   softcap      > 0: a score z becomes softcap * tanh(z / softcap); 0: none.
- *   slopes       device fp32 [q_heads] or NULL: after the cap, slopes[h] * |position - s| is subtracted.
+ *   softcap      > 0: a score z becomes softcap * tanh(z / softcap), up to 2^-21 of the cap for caps of at most 64,
+ *                up to 2^-20 of the score for larger ones; 0: none.
+ *   slopes       device fp32 [q_heads] or NULL: after the cap, slopes[h] * |position - s| is subtracted (the distance
+ *                is exact up to 2^24 and an fp32 number beyond).
  *   prefix_lens  device int32 [num_requests] or NULL: every row of request b also sees the positions
  *                below prefix_lens[b] (and below its length), its own future ones included.
  */
@@ -598,9 +603,12 @@ typedef struct {
  * are left as they were.  What lies in the cache behind a request's tokens is never used, NaN codes included.
  * A visible position without a valid page is skipped and reported (DSA_DEVICE_BAD_PAGE).
  * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-18 of its
- * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), a contribution to the output 8
- * bits or more with one of 2^-20 of the largest contribution; requests of more rows hold V to 2^-25 of the
- * largest V scale of the request's pages.
+ * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
+ * Requests of at most 64 rows * heads per K/V head keep 8 bits or more of a contribution p * v_scale to the output, with
+ * an absolute error of 2^-20 of the largest one; requests of more keep 11 bits of p, and hold V to 2^-25 of the largest V
+ * scale of the request's pages, those that a row does not see included.
+ * max_seq_len and max_query_len may be any bounds that hold, but close ones are faster: up to 1,024 tokens no request is
+ * cut into pieces to join, and only a max_query_len of more than 64 rows * heads per K/V head brings in the kernel for many rows.
  * DSA_ERR_UNSUPPORTED for more than DSA_MAX_REQUESTS requests, for block-table rows of more than 2^30 tokens, and where
  * (the table's tokens / 128 + 5) times max(2 * requests, rows * heads per K/V head / 256 + requests) exceeds 2^31.
  */
