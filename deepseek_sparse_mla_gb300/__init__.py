@@ -26,6 +26,7 @@ from ._lib import DEVICE_BAD_LENGTH, DEVICE_POOL_EMPTY, DEVICE_POOL_FULL, DEVICE
 
 INDEX_HEADS, INDEX_DIM, HEADS, LATENT_DIM, ROPE_DIM, ROW_DIM = 32, 128, 64, 512, 64, 576
 KV_DIM = 128                   # head width of the dense layer's K/V cache
+KV4_BLOCKS = 4                 # K scales of a token and head in the 4-bit cache: one for 32 dims
 DEFAULT_SCALE = 1.0 / 16.0     # 1/sqrt(192 + 64)
 _FORMATS = {"bf16": KEY_BF16, "fp8": KEY_FP8_E4M3, "int8": KEY_INT8, None: KEY_BF16}
 _LATENT_FORMATS = {"bf16": _lib.LATENT_BF16, "fp8": _lib.LATENT_E4M3}
@@ -34,7 +35,7 @@ __all__ = ["LayerCache", "Batch", "kv_append", "kv_append_layers", "indexer_scor
            "cache_bytes", "indexer_workspace_bytes", "mla_workspace_bytes", "DsaError", "DEFAULT_SCALE",
            "dcp_candidates", "dcp_select", "dcp_merge", "read_status",
            "PagePool", "StepPlan", "step_plan", "pages_release", "BlockKvCache", "kv8_append", "paged_attention",
-           "paged_attention_workspace_bytes"]
+           "paged_attention_workspace_bytes", "Kv4Cache", "RotaryTable", "kv4_append"]
 
 
 def _ptr(t):
@@ -573,26 +574,132 @@ class BlockKvCache:
                                 self.v_scales.data_ptr(), self.num_pages, self.page_size, self.kv_heads, 0)
 
 
+class Kv4Cache:
+    """A dense grouped-head layer's paged 4-bit K/V cache: k_codes / v_codes [num_pages, kv_heads, page_size, 64] uint8 (two e2m1
+    codes a byte, the even dim in the low half), k_scales [num_pages, kv_heads, page_size, 4] uint8 (exponent + 127 of a power of
+    two for each 32 dims) and v_scales [num_pages, kv_heads, page_size] bfloat16 (one a token and head)."""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, device="cuda"):
+        shape = (int(num_pages), int(kv_heads), int(page_size))
+        self._set(*(torch.zeros((*shape, KV_DIM // 2), dtype=torch.uint8, device=device) for _ in "kv"),
+                  torch.full((*shape, KV4_BLOCKS), 127, dtype=torch.uint8, device=device),
+                  torch.ones(shape, dtype=torch.bfloat16, device=device))
+
+    @classmethod
+    def of(cls, k_codes, v_codes, k_scales, v_scales):
+        """A cache over existing tensors."""
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            if t.dim() != 4 or t.shape[3] != KV_DIM // 2:
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (pages, heads, page size, {KV_DIM // 2})")
+            _need(t, torch.uint8, k_codes.shape, name)
+        _need(k_scales, torch.uint8, (*k_codes.shape[:3], KV4_BLOCKS), "k_scales")
+        _need(v_scales, torch.bfloat16, k_codes.shape[:3], "v_scales")
+        for t, name in ((v_codes, "v_codes"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+            _on_device(k_codes.device, t, name)
+        cache = cls.__new__(cls)
+        cache._set(k_codes, v_codes, k_scales, v_scales)
+        return cache
+
+    def _set(self, k_codes, v_codes, k_scales, v_scales):
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.num_pages, self.kv_heads, self.page_size = (int(n) for n in k_codes.shape[:3])
+
+    def struct(self) -> _lib.DsaKv4Cache:
+        return _lib.DsaKv4Cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
+                                self.v_scales.data_ptr(), self.num_pages, self.page_size, self.kv_heads, 0)
+
+
+class RotaryTable:
+    """cos and sin of every position's angles, for the appends to rotate by: cos_sin [positions, dim] float32, the dim / 2 cos
+    of a position and then its sin.  dim: the first dims of a head that are rotated (32, 64, 96 or 128).  interleaved: pairs are dims
+    (2i, 2i + 1) instead of (i, i + dim / 2).  The angles base^(-2i / dim) * position are formed in float64."""
+
+    def __init__(self, positions: int, dim: int = KV_DIM, base: float = 10000.0, interleaved: bool = False, device="cuda"):
+        rate = float(base) ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+        turn = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * rate
+        self.cos_sin, self.interleaved = torch.cat([turn.cos(), turn.sin()], 1).float(), bool(interleaved)
+
+    @classmethod
+    def of(cls, cos_sin, interleaved: bool = False):
+        """A table over an existing tensor (of scaled or otherwise changed angles, say)."""
+        if cos_sin.dim() != 2:
+            raise ValueError(f"cos_sin: shape {tuple(cos_sin.shape)}, expected (positions, dim)")
+        _need(cos_sin, torch.float32, cos_sin.shape, "cos_sin")
+        table = cls.__new__(cls)
+        table.cos_sin, table.interleaved = cos_sin, bool(interleaved)
+        return table
+
+
 def _batch_on(device, batch):
     _on_device(device, batch.block_table, "batch.block_table")
     _on_device(device, batch.seq_lens, "batch.seq_lens")
     _on_device(device, batch.query_start_loc, "batch.query_start_loc")
 
 
-def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None):
+def _rope(rope, q, q_out, rows, device):
+    """(struct, q_out) of an append's rotation."""
+    _on_device(device, rope.cos_sin, "rope.cos_sin")
+    positions, dim = rope.cos_sin.shape
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return _lib.DsaRope(rope.cos_sin.data_ptr(), positions, dim, rope.interleaved, 0, None, 0, None, 0), None
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected (rows, heads, {KV_DIM})")
+    heads = q.shape[1]
+    stride = _rows(q, rows, heads, device, "q")
+    if q_out is None:
+        q_out = torch.empty((rows, heads, KV_DIM), dtype=torch.bfloat16, device=device)
+    out_stride = _rows(q_out, rows, heads, device, "q_out")
+    return _lib.DsaRope(rope.cos_sin.data_ptr(), positions, dim, rope.interleaved, heads, q.data_ptr(), stride, q_out.data_ptr(),
+                        out_stride), q_out
+
+
+def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None, rope: RotaryTable | None = None, q=None, q_out=None):
     """Append the step's tokens to an 8-bit K/V cache: k, v [rows, kv_heads, 128] bf16 (rows may be strided), row r of
     the batch at its own position.  A page whose new tokens need a larger scale than it has is re-coded.  Tokens without a
-    valid page are skipped; paged_attention over the same batch reports them."""
+    valid page are skipped; paged_attention over the same batch reports them.  With a rope the cached keys are k rotated by their
+    positions, and q [rows, q_heads, 128] bf16 (optional) is rotated in the same launch, into q_out (which may be q; allocated
+    where it is not given).  Returns q_out, or None without q."""
     dev = cache.k_codes.device
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
-            return kv8_append(cache, batch, k, v)
+            return kv8_append(cache, batch, k, v, None, rope, q, q_out)
     k_stride = _rows(k, batch.num_rows, cache.kv_heads, dev, "k")
     v_stride = _rows(v, batch.num_rows, cache.kv_heads, dev, "v")
     _batch_on(dev, batch)
-    _lib.check(_lib.load().dsa_kv8_append(ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), k.data_ptr(), k_stride,
-                                          v.data_ptr(), v_stride, _raw_stream(dev.index)))
+    if rope is None:
+        if q is not None or q_out is not None:
+            raise ValueError("q is rotated along with k: it needs a rope")
+        _lib.check(_lib.load().dsa_kv8_append(ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), k.data_ptr(), k_stride,
+                                              v.data_ptr(), v_stride, _raw_stream(dev.index)))
+        return None
+    turn, q_out = _rope(rope, q, q_out, batch.num_rows, dev)
+    _lib.check(_lib.load().dsa_kv8_append_rope(ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), k.data_ptr(), k_stride,
+                                               v.data_ptr(), v_stride, ctypes.byref(turn), _raw_stream(dev.index)))
+    return q_out
+
+
+def kv4_append(cache: Kv4Cache, batch: Batch, k, v, rope: RotaryTable | None = None, q=None, q_out=None, stream=None):
+    """Append the step's tokens to a 4-bit K/V cache; arguments and result as for kv8_append.  No other token of a page is
+    touched.  Tokens without a valid page are skipped; paged_attention over the same batch reports them."""
+    dev = cache.k_codes.device
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return kv4_append(cache, batch, k, v, rope, q, q_out)
+    k_stride = _rows(k, batch.num_rows, cache.kv_heads, dev, "k")
+    v_stride = _rows(v, batch.num_rows, cache.kv_heads, dev, "v")
+    _batch_on(dev, batch)
+    turn = None
+    if rope is not None:
+        turn, q_out = _rope(rope, q, q_out, batch.num_rows, dev)
+    elif q is not None or q_out is not None:
+        raise ValueError("q is rotated along with k: it needs a rope")
+    _lib.check(_lib.load().dsa_kv4_append(ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), k.data_ptr(), k_stride,
+                                          v.data_ptr(), v_stride, None if turn is None else ctypes.byref(turn), _raw_stream(dev.index)))
+    return q_out
 
 
 def paged_attention_workspace_bytes(q_heads: int, kv_heads: int, max_query_len: int) -> int:
@@ -605,10 +712,10 @@ def _paged_attention_bytes(device_index, q_heads, kv_heads, max_query_len):
     return paged_attention_workspace_bytes(q_heads, kv_heads, max_query_len)
 
 
-def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM ** -0.5, max_query_len: int | None = None,
+def paged_attention(cache: BlockKvCache | Kv4Cache, batch: Batch, q, scale: float = KV_DIM ** -0.5, max_query_len: int | None = None,
                     softcap: float = 0.0, slopes=None, prefix_lens=None, out=None, lse=None, workspace=None, stream=None,
                     check=False):
-    """Dense attention over an 8-bit K/V cache for decode, verify and prompt rows: q [rows, q_heads, 128] bf16 (rows may
+    """Dense attention over an 8-bit or 4-bit K/V cache for decode, verify and prompt rows: q [rows, q_heads, 128] bf16 (rows may
     be strided); returns (out [rows, q_heads, 128] bf16, lse).  max_query_len is a host bound on the rows of a request
     (the number of rows where it is not given, which is slower for a batch of few rows each: 32 requests of 8K tokens take
     68 us instead of 48).  softcap > 0 caps scores by a tanh, slopes [q_heads] fp32 subtracts
@@ -647,7 +754,9 @@ def paged_attention(cache: BlockKvCache, batch: Batch, q, scale: float = KV_DIM 
     if workspace is None:
         workspace = _workspace(_paged_attention_bytes(dev.index, heads, cache.kv_heads, max_query_len), dev)
     _on_device(dev, workspace, "workspace")
-    _lib.check(_lib.load().dsa_paged_attention(
+    lib = _lib.load()
+    attend = lib.dsa_kv4_attention if isinstance(cache, Kv4Cache) else lib.dsa_paged_attention
+    _lib.check(attend(
         ctypes.byref(cache.struct()), ctypes.byref(batch.struct()), q.data_ptr(), q_stride, heads, float(scale), max_query_len,
         mods, out.data_ptr(), None if lse is None else lse.data_ptr(), *_workspace_args(workspace), _raw_stream(dev.index)))
     if check and R:                                   # without rows nothing ran, and the workspace holds what it held

@@ -28,7 +28,7 @@ EXPORTS = ("dsa_abi_version", "dsa_last_error", "dsa_kernel_launches", "dsa_cach
            "dsa_dcp_candidates", "dsa_dcp_select", "dsa_dcp_merge", "dsa_sparse_mla_decode_ragged",
            "dsa_kv_append_layers", "dsa_read_status", "dsa_check_device_status", "dsa_sparse_mla_decode_layers",
            "dsa_step_plan", "dsa_pages_release", "dsa_kv8_append", "dsa_paged_attention_workspace_bytes",
-           "dsa_paged_attention")
+           "dsa_paged_attention", "dsa_kv8_append_rope", "dsa_kv4_append", "dsa_kv4_attention")
 
 
 class DsaCache(ctypes.Structure):
@@ -48,6 +48,16 @@ class DsaKv8Cache(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class DsaKv4Cache(DsaKv8Cache):
+    """The same fields: k_scales and v_scales point to exponent bytes and to bf16."""
+
+
+class DsaRope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_int32), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_int64)]
 
 
 class DsaAttnMods(ctypes.Structure):
@@ -131,6 +141,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.dsa_paged_attention.restype = I32
     lib.dsa_paged_attention.argtypes = [ctypes.POINTER(DsaKv8Cache), ctypes.POINTER(DsaBatch), P, ctypes.c_int64, I32,
                                         ctypes.c_float, I32, ctypes.POINTER(DsaAttnMods), P, P, P, SZ, P]
+    lib.dsa_kv8_append_rope.restype = I32
+    lib.dsa_kv8_append_rope.argtypes = [ctypes.POINTER(DsaKv8Cache), ctypes.POINTER(DsaBatch), P, ctypes.c_int64, P, ctypes.c_int64,
+                                        ctypes.POINTER(DsaRope), P]
+    lib.dsa_kv4_append.restype = I32
+    lib.dsa_kv4_append.argtypes = [ctypes.POINTER(DsaKv4Cache), ctypes.POINTER(DsaBatch), P, ctypes.c_int64, P, ctypes.c_int64,
+                                   ctypes.POINTER(DsaRope), P]
+    lib.dsa_kv4_attention.restype = I32
+    lib.dsa_kv4_attention.argtypes = [ctypes.POINTER(DsaKv4Cache), *lib.dsa_paged_attention.argtypes[1:]]
     _lib = lib
     return lib
 

@@ -643,6 +643,18 @@ dsa_status dsa_pages_release(const int32_t* finished, int32_t* seq_lens, int32_t
   return cuda_status(launch_pages_release(a, (cudaStream_t)stream), "page release launch");
 }
 
+// the paged geometry of a dense layer's cache
+static dsa_status check_kv_pages(int num_pages, int page_size, int kv_heads, int reserved) {
+  if (num_pages <= 0) return fail(DSA_ERR_INVALID_ARG, "cache.num_pages must be positive (got %d)", num_pages);
+  if (!pow2(page_size) || page_size < kKvMinPage || page_size > kKvMaxPage)
+    return fail(DSA_ERR_UNSUPPORTED, "cache.page_size must be %d, 32, 64 or %d (got %d)", kKvMinPage, kKvMaxPage, page_size);
+  if (kv_heads <= 0) return fail(DSA_ERR_INVALID_ARG, "cache.kv_heads must be positive (got %d)", kv_heads);
+  if (kv_heads > 65535 || (int64_t)num_pages * kv_heads * page_size > (int64_t)INT32_MAX)
+    return fail(DSA_ERR_UNSUPPORTED, "cache holds more than 2^31 rows (pages * heads * page size)");
+  if (reserved) return fail(DSA_ERR_INVALID_ARG, "cache.reserved must be 0");
+  return ok();
+}
+
 static dsa_status check_kv8(const dsa_kv8_cache* c) {
   if (!c) return fail(DSA_ERR_INVALID_ARG, "cache is NULL");
   if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)
@@ -651,14 +663,7 @@ static dsa_status check_kv8(const dsa_kv8_cache* c) {
     return fail(DSA_ERR_INVALID_ARG, "cache.k_codes / v_codes is not 16-byte aligned");
   if (!aligned4(c->k_scales) || !aligned4(c->v_scales))
     return fail(DSA_ERR_INVALID_ARG, "cache.k_scales / v_scales is not 4-byte aligned");
-  if (c->num_pages <= 0) return fail(DSA_ERR_INVALID_ARG, "cache.num_pages must be positive (got %d)", c->num_pages);
-  if (!pow2(c->page_size) || c->page_size < kKvMinPage || c->page_size > kKvMaxPage)
-    return fail(DSA_ERR_UNSUPPORTED, "cache.page_size must be %d, 32, 64 or %d (got %d)", kKvMinPage, kKvMaxPage, c->page_size);
-  if (c->kv_heads <= 0) return fail(DSA_ERR_INVALID_ARG, "cache.kv_heads must be positive (got %d)", c->kv_heads);
-  if (c->kv_heads > 65535 || (int64_t)c->num_pages * c->kv_heads * c->page_size > (int64_t)INT32_MAX)
-    return fail(DSA_ERR_UNSUPPORTED, "cache holds more than 2^31 rows (pages * heads * page size)");
-  if (c->reserved) return fail(DSA_ERR_INVALID_ARG, "cache.reserved must be 0");
-  return ok();
+  return check_kv_pages(c->num_pages, c->page_size, c->kv_heads, c->reserved);
 }
 
 // rows of heads: 16-byte aligned, with a row stride that keeps them so and does not overlap
@@ -671,19 +676,74 @@ static dsa_status check_rows(const char* name, const void* p, int64_t stride, in
   return ok();
 }
 
-dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
-                          int64_t v_stride, void* stream) {
-  dsa_status st = check_kv8(cache);
+// What an append has in common: the batch, k and v.  Without rows there is nothing more to check.
+static dsa_status check_append(const dsa_batch* batch, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int heads) {
+  dsa_status st = check_batch(batch, false);
+  if (st != DSA_OK || batch->num_rows == 0) return st;
+  st = check_rows("k", k, k_stride, heads);
   if (st != DSA_OK) return st;
-  st = check_batch(batch, false);
-  if (st != DSA_OK) return st;
-  if (batch->num_rows == 0) return ok();
-  st = check_rows("k", k, k_stride, cache->kv_heads);
-  if (st != DSA_OK) return st;
-  st = check_rows("v", v, v_stride, cache->kv_heads);
+  st = check_rows("v", v, v_stride, heads);
   if (st != DSA_OK) return st;
   if ((int64_t)batch->num_rows + 2 * (int64_t)batch->num_requests > INT32_MAX)
     return fail(DSA_ERR_UNSUPPORTED, "num_rows / num_requests is too large");
+  return ok();
+}
+
+// CTAs (of at least 4 warps, a warp for 16 query heads of a row) that rotate queries stay well below the grid's 2^31
+static dsa_status check_rope(const dsa_rope* r, const dsa_batch* batch) {
+  if (!r->cos_sin) return fail(DSA_ERR_INVALID_ARG, "rope.cos_sin is NULL");
+  if (!aligned16(r->cos_sin)) return fail(DSA_ERR_INVALID_ARG, "rope.cos_sin is not 16-byte aligned");
+  if (r->dim != 32 && r->dim != 64 && r->dim != 96 && r->dim != 128)
+    return fail(DSA_ERR_UNSUPPORTED, "rope.dim must be 32, 64, 96 or 128 (got %d)", r->dim);
+  if (r->interleaved != 0 && r->interleaved != 1) return fail(DSA_ERR_INVALID_ARG, "rope.interleaved must be 0 or 1");
+  if (r->positions < batch->max_seq_len)
+    return fail(DSA_ERR_INVALID_ARG, "rope.cos_sin has %d positions, fewer than batch.max_seq_len %d", r->positions, batch->max_seq_len);
+  if (r->q_heads < 0) return fail(DSA_ERR_INVALID_ARG, "rope.q_heads is negative");
+  if (r->q_heads == 0) {
+    if (r->q || r->q_out) return fail(DSA_ERR_INVALID_ARG, "rope.q / q_out without rope.q_heads");
+    return ok();
+  }
+  if (r->q_heads > 65535) return fail(DSA_ERR_UNSUPPORTED, "rope.q_heads %d is more than 65535", r->q_heads);
+  if (batch->num_rows == 0) return ok();
+  dsa_status st = check_rows("rope.q", r->q, r->q_stride, r->q_heads);
+  if (st != DSA_OK) return st;
+  st = check_rows("rope.q_out", r->q_out, r->q_out_stride, r->q_heads);
+  if (st != DSA_OK) return st;
+  if (r->q == r->q_out && r->q_stride != r->q_out_stride)
+    return fail(DSA_ERR_INVALID_ARG, "rope.q_out is rope.q with another stride");
+  return ok();
+}
+
+static RopeArgs rope_args(const dsa_rope* r) {
+  RopeArgs a = {};
+  if (!r) return a;
+  a.cos_sin = r->cos_sin;
+  a.positions = r->positions;
+  a.dim = r->dim;
+  a.interleaved = r->interleaved;
+  a.q_heads = r->q_heads;
+  a.q = static_cast<const __nv_bfloat16*>(r->q);
+  a.q_out = static_cast<__nv_bfloat16*>(r->q_out);
+  a.q_stride = r->q_stride;
+  a.q_out_stride = r->q_out_stride;
+  return a;
+}
+
+// warps that an append with rotated queries takes, at 16 query heads and 8 K/V heads each
+static int64_t append_warps(const dsa_batch* batch, const dsa_rope* r, int kv_heads) {
+  return (int64_t)batch->num_rows * ((r ? (r->q_heads + 15) / 16 : 0) + (kv_heads + 7) / 8);
+}
+
+static dsa_status kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, const dsa_rope* rope, void* stream) {
+  dsa_status st = check_kv8(cache);
+  if (st != DSA_OK) return st;
+  st = check_append(batch, k, k_stride, v, v_stride, cache->kv_heads);
+  if (st == DSA_OK && rope) st = check_rope(rope, batch);
+  if (st != DSA_OK || batch->num_rows == 0) return st;
+  if (rope && append_warps(batch, rope, 0) / 4 + ((int64_t)batch->num_rows / cache->page_size + 2 * (int64_t)batch->num_requests) *
+                                                     cache->kv_heads * 2 + 1 > INT32_MAX / 8)
+    return fail(DSA_ERR_UNSUPPORTED, "num_rows * heads is too large");
   Kv8AppendArgs a = {};
   a.k_codes = static_cast<uint8_t*>(cache->k_codes);
   a.v_codes = static_cast<uint8_t*>(cache->v_codes);
@@ -702,7 +762,60 @@ dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, co
   a.v = v;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
+  a.rope = rope_args(rope);
   return cuda_status(launch_kv8_append(a, (cudaStream_t)stream), "8-bit K/V append launch");
+}
+
+dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, void* stream) {
+  return kv8_append(cache, batch, k, k_stride, v, v_stride, nullptr, stream);
+}
+
+dsa_status dsa_kv8_append_rope(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const dsa_rope* rope, void* stream) {
+  if (!rope) return fail(DSA_ERR_INVALID_ARG, "rope is NULL");
+  return kv8_append(cache, batch, k, k_stride, v, v_stride, rope, stream);
+}
+
+static dsa_status check_kv4(const dsa_kv4_cache* c) {
+  if (!c) return fail(DSA_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)
+    return fail(DSA_ERR_INVALID_ARG, "a code or scale array of the cache is NULL");
+  if ((reinterpret_cast<uintptr_t>(c->k_codes) | reinterpret_cast<uintptr_t>(c->v_codes)) & 31u)
+    return fail(DSA_ERR_INVALID_ARG, "cache.k_codes / v_codes is not 32-byte aligned");
+  if (!aligned16(c->k_scales) || !aligned16(c->v_scales))
+    return fail(DSA_ERR_INVALID_ARG, "cache.k_scales / v_scales is not 16-byte aligned");
+  return check_kv_pages(c->num_pages, c->page_size, c->kv_heads, c->reserved);
+}
+
+dsa_status dsa_kv4_append(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const dsa_rope* rope, void* stream) {
+  dsa_status st = check_kv4(cache);
+  if (st != DSA_OK) return st;
+  st = check_append(batch, k, k_stride, v, v_stride, cache->kv_heads);
+  if (st == DSA_OK && rope) st = check_rope(rope, batch);
+  if (st != DSA_OK || batch->num_rows == 0) return st;
+  if (append_warps(batch, rope, cache->kv_heads) > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "num_rows * heads is too large");
+  Kv4AppendArgs a = {};
+  a.k_codes = static_cast<uint8_t*>(cache->k_codes);
+  a.v_codes = static_cast<uint8_t*>(cache->v_codes);
+  a.k_scales = static_cast<uint8_t*>(cache->k_scales);
+  a.v_scales = static_cast<__nv_bfloat16*>(cache->v_scales);
+  a.num_pages = cache->num_pages;
+  a.log2_page = ilog2(cache->page_size);
+  a.kv_heads = cache->kv_heads;
+  a.block_table = batch->block_table;
+  a.seq_lens = batch->seq_lens;
+  a.query_start_loc = batch->query_start_loc;
+  a.num_requests = batch->num_requests;
+  a.num_rows = batch->num_rows;
+  a.table_stride = batch->block_table_stride;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.rope = rope_args(rope);
+  return cuda_status(launch_kv4_append(a, (cudaStream_t)stream), "4-bit K/V append launch");
 }
 
 size_t dsa_paged_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t max_query_len) {
@@ -710,20 +823,20 @@ size_t dsa_paged_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, in
   return plan_paged_attention(max_query_len, q_heads / kv_heads).workspace_bytes;
 }
 
-dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
-                               int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,
-                               float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  dsa_status st = check_kv8(cache);
-  if (st != DSA_OK) return st;
-  st = check_batch(batch, false);
+// Everything that a dense attention call checks beside its cache, and its kernels' arguments but for the cache's.
+// (Without rows there is nothing to do and nothing filled in.)
+static dsa_status attention_args(int num_pages, int page_size, int kv_heads, const dsa_batch* batch, const void* q, int64_t q_stride,
+                                 int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, PagedAttnArgs& a, PagedAttnPlan& plan) {
+  dsa_status st = check_batch(batch, false);
   if (st != DSA_OK) return st;
   if (batch->num_requests > DSA_MAX_REQUESTS)
     return fail(DSA_ERR_UNSUPPORTED, "batch.num_requests %d is more than %d", batch->num_requests, DSA_MAX_REQUESTS);
-  if ((int64_t)batch->block_table_stride * cache->page_size > int64_t(1) << 30)   // positions of the next tiles stay in 32 bits
+  if ((int64_t)batch->block_table_stride * page_size > int64_t(1) << 30)   // positions of the next tiles stay in 32 bits
     return fail(DSA_ERR_UNSUPPORTED, "block_table_stride * cache.page_size is more than 2^30 tokens");
-  if (q_heads <= 0 || q_heads % cache->kv_heads)
-    return fail(DSA_ERR_INVALID_ARG, "q_heads %d is not a multiple of cache.kv_heads %d", q_heads, cache->kv_heads);
-  const int group = q_heads / cache->kv_heads;
+  if (q_heads <= 0 || q_heads % kv_heads)
+    return fail(DSA_ERR_INVALID_ARG, "q_heads %d is not a multiple of cache.kv_heads %d", q_heads, kv_heads);
+  const int group = q_heads / kv_heads;
   if (group > DSA_MAX_GROUP)
     return fail(DSA_ERR_UNSUPPORTED, "%d query heads per K/V head are more than %d", group, DSA_MAX_GROUP);
   if (!(scale > 0.f) || scale > 1e30f) return fail(DSA_ERR_INVALID_ARG, "scale must be finite and positive");
@@ -744,30 +857,27 @@ dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batc
   if ((int64_t)batch->num_rows * q_heads > INT32_MAX / 2)
     return fail(DSA_ERR_UNSUPPORTED, "num_rows * q_heads is too large");
   // the kernels' running sums over the requests count (column group, tile of 128 keys) pairs in 32 bits
-  const int64_t tiles = (int64_t)batch->block_table_stride * cache->page_size / 128 + 5;   // a segment's ends count as 4
+  const int64_t tiles = (int64_t)batch->block_table_stride * page_size / 128 + 5;   // a segment's ends count as 4
   const int64_t groups = std::max<int64_t>(2 * (int64_t)batch->num_requests, (int64_t)batch->num_rows * group / 256 + batch->num_requests);
   if (tiles * groups > INT32_MAX)
     return fail(DSA_ERR_UNSUPPORTED, "the block table's rows could hold more than 2^31 tiles of 128 tokens for the batch's rows");
   const int rows_max = batch->query_start_loc ? std::min(max_query_len, batch->num_rows) : 1;
-  const PagedAttnPlan plan = plan_paged_attention(rows_max, group);
+  plan = plan_paged_attention(rows_max, group);
   if (!workspace || workspace_bytes < plan.workspace_bytes)
     return fail(DSA_ERR_WORKSPACE,
                 "workspace of %zu bytes is smaller than the %zu bytes dsa_paged_attention_workspace_bytes requires",
                 workspace_bytes, plan.workspace_bytes);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(DSA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
-  PagedAttnArgs a = {};
   a.block_table = batch->block_table;
   a.seq_lens = batch->seq_lens;
   a.query_start_loc = batch->query_start_loc;
   a.num_requests = batch->num_requests;
   a.num_rows = batch->num_rows;
   a.table_stride = batch->block_table_stride;
-  a.num_pages = cache->num_pages;
-  a.log2_page = ilog2(cache->page_size);
-  a.kv_heads = cache->kv_heads;
+  a.num_pages = num_pages;
+  a.log2_page = ilog2(page_size);
+  a.kv_heads = kv_heads;
   a.group = group;
-  a.k_scales = cache->k_scales;
-  a.v_scales = cache->v_scales;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
   a.scale_log2 = scale * 1.4426950408889634f;
@@ -777,10 +887,42 @@ dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batc
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.max_rows = rows_max;
+  return ok();
+}
+
+dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
+                               int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,
+                               float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  dsa_status st = check_kv8(cache);
+  if (st != DSA_OK) return st;
+  PagedAttnArgs a = {};
+  PagedAttnPlan plan = {};
+  st = attention_args(cache->num_pages, cache->page_size, cache->kv_heads, batch, q, q_stride, q_heads, scale, max_query_len, mods, out, lse,
+                      workspace, workspace_bytes, a, plan);
+  if (st != DSA_OK || batch->num_rows == 0) return st;
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
   return cuda_status(launch_paged_attention(a, static_cast<const uint8_t*>(cache->k_codes),
                                             static_cast<const uint8_t*>(cache->v_codes), batch->max_seq_len, workspace, plan,
                                             (cudaStream_t)stream),
                      "paged attention launch");
+}
+
+dsa_status dsa_kv4_attention(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride, int32_t q_heads,
+                             float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  dsa_status st = check_kv4(cache);
+  if (st != DSA_OK) return st;
+  PagedAttnArgs a = {};
+  PagedAttnPlan plan = {};
+  st = attention_args(cache->num_pages, cache->page_size, cache->kv_heads, batch, q, q_stride, q_heads, scale, max_query_len, mods, out, lse,
+                      workspace, workspace_bytes, a, plan);
+  if (st != DSA_OK || batch->num_rows == 0) return st;
+  a.k_scales4 = static_cast<const uint8_t*>(cache->k_scales);
+  a.v_scales4 = static_cast<const __nv_bfloat16*>(cache->v_scales);
+  return cuda_status(launch_kv4_attention(a, static_cast<const uint8_t*>(cache->k_codes), static_cast<const uint8_t*>(cache->v_codes),
+                                          batch->max_seq_len, workspace, plan, (cudaStream_t)stream),
+                     "4-bit paged attention launch");
 }
 
 }  // extern "C"

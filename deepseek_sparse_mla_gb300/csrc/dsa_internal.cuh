@@ -240,6 +240,17 @@ struct PagesReleaseArgs {
 };
 cudaError_t launch_pages_release(const PagesReleaseArgs& a, cudaStream_t s);
 
+// Rotation of the first `dim` dims of a head by its row's position, on the way into a cache (rope.cuh); cos_sin NULL: none.
+struct RopeArgs {
+  const float* cos_sin;             // [positions][dim]: cos of dim / 2 angles, then their sin
+  int32_t positions, dim;
+  int32_t interleaved;              // pairs (2i, 2i + 1) instead of (i, i + dim / 2)
+  int32_t q_heads;                  // of the queries that are rotated along; 0: none
+  const __nv_bfloat16* q;
+  __nv_bfloat16* q_out;
+  int64_t q_stride, q_out_stride;   // elements between rows
+};
+
 struct Kv8AppendArgs {
   uint8_t *k_codes, *v_codes;
   float *k_scales, *v_scales;
@@ -250,17 +261,37 @@ struct Kv8AppendArgs {
   int32_t num_requests, num_rows, table_stride;
   const void *k, *v;
   int64_t k_stride, v_stride;       // elements between tokens
+  RopeArgs rope;
 };
 cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s);
 
-// Dense attention over the 8-bit K/V cache (see paged_attention.cu).
+constexpr int kKv4Blocks = DSA_KV4_BLOCKS;       // K scales of a token: one for 32 dims
+constexpr int kKv4LowExp = DSA_KV4_MIN_EXP, kKv4HighExp = DSA_KV4_MAX_EXP;
+struct Kv4AppendArgs {
+  uint8_t *k_codes, *v_codes;       // two codes a byte
+  uint8_t* k_scales;                // exponent + 127, 255: NaN
+  __nv_bfloat16* v_scales;
+  int32_t num_pages, log2_page, kv_heads;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;   // nullptr: one row per request
+  int32_t num_requests, num_rows, table_stride;
+  const __nv_bfloat16 *k, *v;
+  int64_t k_stride, v_stride;       // elements between tokens
+  RopeArgs rope;
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t s);
+
+// Dense attention over an 8-bit or 4-bit K/V cache (see paged_attention.cu).
 struct PagedAttnArgs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* query_start_loc;   // nullptr: one row per request
   int32_t num_requests, num_rows, table_stride;
   int32_t num_pages, log2_page, kv_heads, group;   // group = query heads per K/V head
-  const float *k_scales, *v_scales;
+  const float *k_scales, *v_scales;                // 8-bit cache: of pages and heads
+  const uint8_t* k_scales4;                        // 4-bit cache: of tokens, heads and 32 dims
+  const __nv_bfloat16* v_scales4;                  // of tokens and heads
   const __nv_bfloat16* q;
   int64_t q_stride;                 // elements between rows
   float scale_log2;                 // softmax scale * log2(e)
@@ -291,6 +322,9 @@ struct PagedAttnPlan {
 PagedAttnPlan plan_paged_attention(int max_query_len, int group);
 cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_seq_len,
                                    void* workspace, const PagedAttnPlan& plan, cudaStream_t s);
+
+cudaError_t launch_kv4_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_seq_len,
+                                 void* workspace, const PagedAttnPlan& plan, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // device helpers

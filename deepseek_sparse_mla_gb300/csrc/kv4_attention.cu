@@ -1,0 +1,22 @@
+// Dense grouped-head attention over the paged 4-bit K/V cache: paged_attention.cu's kernel compiled for it, and its launch.
+#define DSA_PAGED_KERNEL_ONLY
+#include "paged_attention.cu"
+
+namespace dsa {
+
+cudaError_t launch_kv4_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_seq_len, void* workspace,
+                                 const PagedAttnPlan& plan, cudaStream_t s) {
+  const int ctas = device_sm_count();
+  pa_layout(a, workspace, plan, ctas, max_seq_len);
+  a.hi_pairs = INT32_MAX;
+  a.early = false;
+  const uint64_t rows = (uint64_t)a.num_pages * a.kv_heads << a.log2_page;
+  CUtensorMap k_map, v_map;
+  if (!encode_2d(&k_map, k_codes, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 1, kKvDim, rows, kKvDim / 2, kKvDim, 1u << a.log2_page) ||
+      !encode_2d(&v_map, v_codes, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 1, kKvDim, rows, kKvDim / 2, kKvDim, 1u << a.log2_page))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = launch_few_rows<true>(a, k_map, v_map, ctas, true, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace dsa

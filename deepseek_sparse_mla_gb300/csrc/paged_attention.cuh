@@ -78,6 +78,36 @@ __device__ __forceinline__ float pa_factor(uint32_t top, int E, float scale) {
 cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
                                 const uint8_t* v_codes, int ctas, cudaStream_t s);
 
+// Where the workspace's parts lie, and which requests the kernel for few rows takes
+inline void pa_layout(PagedAttnArgs& a, void* workspace, const PagedAttnPlan& plan, int ctas, int max_seq_len) {
+  char* ws = static_cast<char*>(workspace);
+  a.err = reinterpret_cast<uint32_t*>(ws);
+  a.rec = reinterpret_cast<int32_t*>(ws + plan.rec_offset);
+  a.part_o = reinterpret_cast<float*>(ws + plan.part_offset);
+  a.part_ml = a.part_o + (size_t)2 * ctas * kPagedAttnColumns * kKvDim;
+  // Requests of at most 1,024 keys are not cut: a CTA takes such a segment in less time than a second launch to join
+  // its pieces would (8-bit cache, in replayed graphs, one request of 300 keys: 10.4 instead of 19.8 us; 4 prompts of 1,000 rows: 89
+  // instead of 97; a single prompt of 1,000 rows and one K/V head, which leaves most SMs idle: 35.1 instead of 31.4).
+  a.whole = max_seq_len <= 8 * kPaTok;
+  a.lo_pairs = 0;
+  a.hi_pairs = plan.prompt ? kPagedAttnDirect : INT32_MAX;
+  // The prompt kernel's warps wait for each other with a bound of a second, and its writers for this kernel's end, so they
+  // start early only where this kernel's CTAs cannot differ by as much: 2^23 tiles are 0.3 s of work for all of them.
+  a.early = plan.prompt && (int64_t)a.num_requests * (((int64_t)max_seq_len + kPaTok - 1) / kPaTok) * a.kv_heads * 2 <= int64_t(1) << 23;
+}
+
+// The prompt kernel's requests and its parts of the workspace
+inline PagedAttnArgs pa_prompt_args(const PagedAttnArgs& few, void* workspace, const PagedAttnPlan& plan, int ctas) {
+  PagedAttnArgs a = few;
+  char* ws = static_cast<char*>(workspace);
+  a.lo_pairs = kPagedAttnDirect;
+  a.hi_pairs = INT32_MAX;
+  a.rec = reinterpret_cast<int32_t*>(ws + plan.prompt_rec_offset);
+  a.part_o = reinterpret_cast<float*>(ws + plan.prompt_part_offset);
+  a.part_ml = a.part_o + (size_t)2 * ctas * kPromptPairs * kKvDim;
+  return a;
+}
+
 // A capped score: cap * tanh(z / cap), with y = 2 log2(e) / cap * z and all in log2 units.
 //   small caps: cap * (1 - 2 / (1 + 2^y)), exact to about 2^-22 of the cap (1.5e-5 of a score at a cap of 64); past the
 //   range of 2^y the quotient is 0 or 2, and NaN stays.

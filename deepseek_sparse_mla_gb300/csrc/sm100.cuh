@@ -286,6 +286,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// bulk_load with an L2 cache policy.
+__device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+               ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+               : "memory");
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -482,6 +489,33 @@ __device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uint
 // Instruction descriptor for kind::f8f6f4 with e4m3 A and B, fp32 accumulation, K-major operands.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The operands' types in the instruction descriptors of kind::f8f6f4 and kind::mxf8f6f4.  4-bit operands lie in shared memory in
+// 16-byte units of which 16 codes fill the first half, in the layouts of 8-bit ones.
+constexpr uint32_t kFmtE4m3 = 0, kFmtE5m2 = 1, kFmtE2m1 = 5;
+
+// Instruction descriptor for kind::mxf8f6f4 (a power of two for each 32 elements along K, fp32 accumulation, K-major operands).
+// Bits 29 and 4 choose the byte of A's and of B's scale words.
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, uint32_t a_fmt, uint32_t b_fmt) {
+  return (a_fmt << 7) | (b_fmt << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T with block scales from TMEM: a row's word in lane row % 32 (of each 32 lanes), column row / 32
+__device__ __forceinline__ void mma_ss_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scales,
+                                          uint32_t b_scales, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(a_scales), "r"(b_scales)
+      : "memory");
+}
+
+// 32 rows of 16 bytes (unswizzled 8-row groups) from shared memory to four TMEM columns, the same in each 32 lanes.  Ordered
+// before the tcgen05.mma that this thread issues after it.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Arrive on the mbarrier once every previously issued tcgen05.mma of this thread has completed.

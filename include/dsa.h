@@ -14,7 +14,9 @@
  * Around the sparse layers: the step's block tables and slot maps built on the
  * device (dsa_step_plan, dsa_pages_release), and the dense grouped-head layer
  * that a draft (MTP) model runs over its own paged 8-bit K/V cache
- * (dsa_kv8_append, dsa_paged_attention).
+ * (dsa_kv8_append, dsa_paged_attention) or one of half its size
+ * (dsa_kv4_append, dsa_kv4_attention); both appends can rotate keys and
+ * queries by their positions on the way (dsa_rope).
  *
  * Sources: "GLM-5.2 on vLLM Ascend: Request-to-Backend Inference Path",
  * section 8 "The SFA backend, step by step" (write paged cache, select tokens,
@@ -75,6 +77,9 @@ extern "C" {
 #define DSA_ROPE_DIM 64      /* k_R / q_rope width                               */
 #define DSA_ROW_DIM 576      /* one cached latent row: [c_KV(512) | k_R(64)]     */
 #define DSA_KV_DIM 128       /* head width of the dense layer's K/V cache        */
+#define DSA_KV4_BLOCKS 4     /* K scales of a token and head in the 4-bit cache: one for 32 dims */
+#define DSA_KV4_MIN_EXP (-15) /* and the range of their exponents                */
+#define DSA_KV4_MAX_EXP 13
 #define DSA_MAX_GROUP 64     /* query heads per K/V head of the dense layer      */
 #define DSA_MAX_REQUESTS 4096 /* requests of a planned step or a dense attention call */
 #define DSA_MAX_TOPK 8192    /* largest supported top-k budget                   */
@@ -564,7 +569,77 @@ typedef struct {
 DSA_API dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride,
                                   const void* v, int64_t v_stride, void* stream);
 
-/* Scratch bytes dsa_paged_attention needs on the current device.  0 for invalid arguments. */
+/*
+ * Rotation by position, applied by an append to its keys (the cached ones are then rotated) and to the step's queries.
+ * ("vLLM Inference Path", "MLA Projections and KV State": only the RoPE part of queries and keys carries the position.)
+ * With c and s the cos and sin of angle i at the row's position, for i < dim / 2:
+ *   (a, b) -> (a c - b s, b c + a s),   a, b = dims i and i + dim / 2, or 2i and 2i + 1 (interleaved)
+ * Products and their sum are rounded to fp32 one by one; the other dims stay as they are.  Keys are quantised from the fp32
+ * values, queries rounded to bf16.
+ *   cos_sin     device fp32 [positions, dim], 16-byte aligned: row p holds the dim / 2 cos and then the dim / 2 sin of position p.
+ *   positions   at least the batch's max_seq_len.  (A row at a position beyond the table is skipped.)
+ *   dim         32, 64, 96 or 128.
+ *   q, q_out    device bf16, row r's heads at q + r * q_stride (elements): [q_heads, 128] contiguous, 16-byte aligned,
+ *               strides a multiple of 8 and at least q_heads * 128.  q_out may be q itself (with its stride), and else
+ *               does not overlap it.  Every row of a request is rotated, also one whose token has no valid page; rows behind
+ *               the last request's are left as they were.  q_heads 0: no queries (q and q_out NULL).
+ */
+typedef struct {
+  const float* cos_sin;
+  int32_t positions;
+  int32_t dim;
+  int32_t interleaved;   /* 0 or 1 */
+  int32_t q_heads;
+  const void* q;
+  int64_t q_stride;
+  void* q_out;
+  int64_t q_out_stride;
+} dsa_rope;
+
+/* dsa_kv8_append of rotated keys, with the step's queries rotated in the same launch. */
+DSA_API dsa_status dsa_kv8_append_rope(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride,
+                                       const void* v, int64_t v_stride, const dsa_rope* rope, void* stream);
+
+/*
+ * A dense grouped-head layer's paged 4-bit K/V cache (caller-owned device memory).
+ *   k_codes, v_codes  [num_pages, kv_heads, page_size, 64] bytes, 32-byte aligned: e2m1 codes (sign, two bits of exponent, one
+ *                     of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6), dim 2i in the low and dim 2i + 1 in the high half of byte i.
+ *   k_scales          [num_pages, kv_heads, page_size, 4] bytes, 16-byte aligned: byte e of block j stands for 2^(e - 127), the
+ *                     scale of dims 32j .. 32j + 31; 255 is NaN.  dsa_kv4_append writes exponents from DSA_KV4_MIN_EXP to
+ *                     DSA_KV4_MAX_EXP, and attention takes those.
+ *   v_scales          [num_pages, kv_heads, page_size] bf16, 16-byte aligned: one scale a token and head.  Attention takes any
+ *                     finite one whose size is 0 or from 2^-126 to 2^120.
+ * 134 bytes a token and head, where the 8-bit cache takes 256.  Token s of request b lies in page block_table[b][s / page_size],
+ * at offset s % page_size.
+ */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_scales;
+  void* v_scales;
+  int32_t num_pages;
+  int32_t page_size;     /* 16, 32, 64 or 128 */
+  int32_t kv_heads;
+  int32_t reserved;      /* 0 */
+} dsa_kv4_cache;
+
+/*
+ * Append the step's K and V to a 4-bit cache.  Rows, requests and positions come from batch (seq_lens after this append).
+ *   K, per token, head and 32 dims:  scale = 2^ceil(log2(amax / 6)), its exponent held in DSA_KV4_MIN_EXP .. DSA_KV4_MAX_EXP
+ *   V, per token and head:           scale = bf16(amax / 6), at least 2^-126
+ *   code = e2m1(x / scale), nearest-even, saturating (infinities too), with amax over the finite values
+ * A NaN makes the scale of its block (K) or token (V) NaN; the codes under it are unspecified.  Nothing that the step does not
+ * write is read or changed.
+ *   k, v      as for dsa_kv8_append.
+ *   rope      rotation of k, and of queries along with it, or NULL.
+ * Tokens whose page id is out of range or whose table row is too short are skipped, and so are requests with more rows than tokens
+ * or with offsets that do not fit the batch.  No two rows may name the same slot.  No status of its own: dsa_kv4_attention over
+ * the same batch reports bad ids, short rows and such offsets.
+ */
+DSA_API dsa_status dsa_kv4_append(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, const dsa_rope* rope, void* stream);
+
+/* Scratch bytes dsa_paged_attention and dsa_kv4_attention need on the current device.  0 for invalid arguments. */
 DSA_API size_t dsa_paged_attention_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t max_query_len);
 
 /*
@@ -616,6 +691,20 @@ DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_bat
                                        int64_t q_stride, int32_t q_heads, float scale, int32_t max_query_len,
                                        const dsa_attn_mods* mods, void* out, float* lse, void* workspace,
                                        size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_paged_attention over a 4-bit K/V cache: the same arguments, rows, modifiers, status and limits.
+ *   z_s = scale * q[r,h] . (k_code_s * k_scale_s)      out[r,h] = sum_s softmax(z)_s * (v_code_s * v_scale_s)
+ * What lies in the cache behind a request's tokens is never used, NaN scales included; a NaN scale makes the output of the rows
+ * that see its token NaN.
+ * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-22 of its
+ * row's largest value, taken as 2^-100 where it is smaller.  Requests of at most 64 rows * heads per K/V head keep 8 bits or more
+ * of a contribution p * v_scale to the output, with an absolute error of 2^-20 of the largest one; requests of more keep 11 bits
+ * of p and of v_code * v_scale, V to 2^-25 of the largest V scale of the request's tokens, those that a row does not see included.
+ */
+DSA_API dsa_status dsa_kv4_attention(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
+                                     int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
