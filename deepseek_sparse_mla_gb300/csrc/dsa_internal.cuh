@@ -290,6 +290,7 @@ struct PagedAttnArgs {
   int32_t num_requests, num_rows, table_stride;
   int32_t num_pages, log2_page, kv_heads, group;   // group = query heads per K/V head
   const float *k_scales, *v_scales;                // 8-bit cache: of pages and heads
+  const uint8_t* k_codes4;
   const uint8_t* k_scales4;                        // 4-bit cache: of tokens, heads and 32 dims
   const __nv_bfloat16* v_scales4;                  // of tokens and heads
   const __nv_bfloat16* q;

@@ -77,6 +77,9 @@ __device__ __forceinline__ float pa_factor(uint32_t top, int E, float scale) {
 // groups of 8 columns); k_map: the K codes in boxes of a page.
 cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
                                 const uint8_t* v_codes, int ctas, cudaStream_t s);
+cudaError_t launch_kv4_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map, const uint8_t* v_codes,
+                              int ctas, cudaStream_t s);
+cudaError_t launch_prompt_join(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, int ctas, cudaStream_t s);
 
 // Where the workspace's parts lie, and which requests the kernel for few rows takes
 inline void pa_layout(PagedAttnArgs& a, void* workspace, const PagedAttnPlan& plan, int ctas, int max_seq_len) {

@@ -1,5 +1,6 @@
-// Dense attention over the paged 8-bit K/V cache for requests of many rows (prompt pieces), on tcgen05 tensor
-// cores.  Definition as in paged_attention.cu:
+// Dense attention over the paged 8-bit or 4-bit K/V cache for requests of many rows (prompt pieces), on tcgen05 tensor
+// cores.  (Compiled here for the 8-bit cache; kv4_prompt.cu compiles the same kernel for the 4-bit one.)
+// Definition as in paged_attention.cu:
 //   z_s = scale * q[r,h] . (k_code_s * ks),  out = softmax(z) (v_code * vs),  lse = ln sum exp(z)
 //
 // Here the products bound the call (4 * 128 flop per visible pair and head), so the tiles are square:
@@ -26,12 +27,17 @@
 // promised to run in order; one warp a half for both kinds, waiting for that, took 8 % longer).
 // Warps 8-11 and 12-15 widen the V tiles, even and odd ones; warp 19 loads K tiles by TMA and finds the CTA's
 // segments for everyone (each role finding them for itself cost 30 registers, and spills).
+//
+// 4-bit cache: block scales in TMEM, as the kernel for few rows has them, need columns that S and O do not leave, so K's
+// codes are widened too: to e5m2, which holds code * 2^e exactly for the exponents of the cache (-15 .. 13).  V's fp16
+// values are code * scale relative to the largest scale of the piece's tokens, exact (10 bits) down to 2^-14 of it.  Warps 8-11 widen K, 12-15 V.
 // TMEM (all 512 columns): S of half q and key half h at 128 q + 64 h, with P over its first 32; O of half q at 256 + 128 q.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
 
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 
 #include <type_traits>
 
@@ -165,6 +171,17 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// four fp16 pairs of eight e2m1 codes
+__device__ __forceinline__ uint4 widen8(uint32_t w) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * i)), __NV_E2M1);
+    r[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 __device__ __forceinline__ uint32_t mul2(uint32_t x, __half2 f) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x), f);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -218,6 +235,8 @@ struct PpRow {
 // 16 in flight), and P = 2^(z - m + 8) is formed against the reference that the row has.  P stays in registers until
 // the largest score (returned) is known to exceed it by no more than the slack, as for nearly every tile; else
 // the pass is repeated.  (Two passes, as below, take 7 % longer for 4,096 rows at 64K.)
+// k4: the scores need no factor of their keys.
+template <bool k4>
 __device__ __forceinline__ float pp_half(const PpRow& w, uint32_t tS, const float* ks, uint32_t (&p)[32], float& sum_out) {
   const float shift = pp::kPLog2 - (w.m == -INFINITY ? 0.f : w.m);
   const uint64_t shift2 = pack2(shift, shift);
@@ -230,7 +249,7 @@ __device__ __forceinline__ float pp_half(const PpRow& w, uint32_t tS, const floa
     tmem_wait_ld();
     if (g < 3) tmem_ld16(tS + 16 * (g + 1), r[(g + 1) & 1]);
     const uint32_t* x = r[g & 1];
-    const float kc = ks[g] * w.cf;
+    const float kc = k4 ? w.cf : ks[g] * w.cf;
     float m = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
     const uint64_t kc2 = pack2(kc, kc);
 #pragma unroll
@@ -255,7 +274,7 @@ __device__ __forceinline__ float pp_half(const PpRow& w, uint32_t tS, const floa
 
 // 64 keys with masks, a cap or a bias, in two rolled passes (one body of each: unrolled like the plain form, the call
 // with a cap and a bias took a fifth longer): the scores are made final and written back, with their largest ..
-template <PaMods kModSet, bool kMasked>
+template <bool k4, PaMods kModSet, bool kMasked>
 __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a, uint32_t tS, int key0, uint32_t bad, const float* ks) {
   constexpr bool kMods = kModSet != kPaPlain;
   const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
@@ -268,7 +287,7 @@ __device__ __forceinline__ float pp_max64(const PpRow& w, const PagedAttnArgs& a
 #pragma unroll
     for (int gg = 0; gg < 2; ++gg) {
       uint32_t* x = r + 16 * gg;
-      const float kc = ks[g + gg] * (in != 0.f ? w.cf * in : w.cf);
+      const float own = in != 0.f ? w.cf * in : w.cf, kc = k4 ? own : ks[g + gg] * own;
       const int left = ((bad >> (g + gg)) & 1u) ? 0 : w.limit - key0 - 16 * (g + gg);   // keys of the group that are seen
       const float away = kMods ? (float)(w.pos - key0 - 16 * (g + gg)) : 0.f;           // of the row from the first of them
       // a loop each: a choice made inside one of them would leave the values no instructions to overlap with
@@ -389,7 +408,192 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
   return cf;
 }
 
-template <PaMods kModSet>
+// ---- the 4-bit cache's widening warps.  A thread takes 32 codes of a row (16 bytes, and for K one scale) a step: four lanes a
+// row, eight rows a warp and 32 the four warps, in four steps a tile.  The next tile's loads go out after the last tile's
+// fence, which would wait for loads in flight too.
+struct PpWiden {
+  const PagedAttnArgs& a;
+  int lp, cw, part, sub;
+  __device__ PpWiden(const PagedAttnArgs& args)
+      : a(args), lp(args.log2_page), cw((threadIdx.x >> 5) & 3), part(threadIdx.x & 3), sub((threadIdx.x >> 2) & 7) {}
+  __device__ __forceinline__ int row(int g) const { return 32 * g + 8 * cw + sub; }
+  // lane j (and j + 8, ..): the page of 16-key group j of the tile at key0, -1 where there is none (the loader reports bad ids)
+  __device__ __forceinline__ int id_of(const PpSeg& s, int key0) const {
+    const int p = (key0 + 16 * (threadIdx.x & 7)) >> lp, pages = (s.len + (1 << lp) - 1) >> lp;
+    const int id = p < pages ? a.block_table[(int64_t)s.b * a.table_stride + p] : -1;
+    return id < a.num_pages ? id : -1;
+  }
+  // the row in the cache of step g's key, -1 where there is none
+  __device__ __forceinline__ int64_t slot(const PpSeg& s, int id, int key0, int g) const {
+    const int page = __shfl_sync(0xffffffffu, id, 2 * g + (cw >> 1)), key = key0 + row(g);
+    return page >= 0 && key < s.len ? (((int64_t)page * a.kv_heads + s.h) << lp) + (key & ((1 << lp) - 1)) : -1;
+  }
+};
+
+// K tiles: code * 2^e as e5m2, the upper bytes of the same numbers in fp16
+__device__ __forceinline__ void pp_widen_k4(const PagedAttnArgs& a, const PpSeg* segs, uint64_t* seg_full, uint64_t* seg_empty,
+                                            uint64_t* k_full, uint64_t* k_empty, uint8_t* sK, uint32_t* err) {
+  using namespace pp;
+  const PpWiden w(a);
+  const int lane = threadIdx.x & 31;
+  int i = 0;
+  for (int seg = 0;; ++seg) {
+    if (!wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls)) return;
+    const PpSeg s = segs[seg % kSegBufs];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
+    if (s.n == 0) return;
+    uint4 x[4];
+    uint32_t e[4];
+    int id = w.id_of(s, s.tile_at(0) * kTok), id2 = s.n > 1 ? w.id_of(s, s.tile_at(1) * kTok) : -1;
+    auto load = [&](int key0) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t at = w.slot(s, id, key0, g);
+        x[g] = make_uint4(0, 0, 0, 0);
+        e[g] = 127;
+        if (at >= 0) {
+          x[g] = __ldg(reinterpret_cast<const uint4*>(a.k_codes4 + at * (kKvDim / 2)) + w.part);
+          e[g] = __ldg(a.k_scales4 + at * kKv4Blocks + w.part);
+        }
+      }
+    };
+    load(s.tile_at(0) * kTok);
+    for (int t = 0; t < s.n; ++t, ++i) {
+      const int st = i % kKStages, use = i / kKStages;
+      if (use > 0 && !wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) return;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        // 2^e in fp16 (2^-15 is a subnormal number); the NaN scale makes NaN codes
+        const int ex = min(max((int)e[g] - 127, kKv4LowExp), kKv4HighExp);
+        const uint32_t f1 = e[g] == 255u ? 0x7E00u : ex == -15 ? 0x0200u : (uint32_t)(ex + 15) << 10;
+        const uint32_t f2 = f1 | f1 << 16;
+        const __half2 f = *reinterpret_cast<const __half2*>(&f2);
+        const uint32_t in[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+        uint32_t out[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 h = widen8(in[q]);
+          out[2 * q] = __byte_perm(mul2(h.x, f), mul2(h.y, f), 0x7531);
+          out[2 * q + 1] = __byte_perm(mul2(h.z, f), mul2(h.w, f), 0x7531);
+        }
+        const int r = w.row(g);
+        uint8_t* const to = sK + st * kKBytes;
+        *reinterpret_cast<uint4*>(to + sw128_offset(r, 2 * w.part)) = make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint4*>(to + sw128_offset(r, 2 * w.part + 1)) = make_uint4(out[4], out[5], out[6], out[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[st]);
+      if (t + 1 < s.n) {
+        id = id2;
+        id2 = t + 2 < s.n ? w.id_of(s, s.tile_at(t + 2) * kTok) : -1;
+        load(s.tile_at(t + 1) * kTok);
+      }
+    }
+  }
+}
+
+// V tiles: code * scale in fp16, in units of the power of two at or below the piece's largest scale
+__device__ __forceinline__ void pp_widen_v4(const PagedAttnArgs& a, const uint8_t* v_codes, const PpSeg* segs, uint64_t* seg_full,
+                                            uint64_t* seg_empty, uint64_t* v_full, uint64_t* v_empty, uint8_t* sV, int* nan_key,
+                                            float* vmax_part, float* v_ref, uint32_t* err) {
+  using namespace pp;
+  const PpWiden w(a);
+  const int lane = threadIdx.x & 31;
+  int i = 0;
+  for (int seg = 0;; ++seg) {
+    const int sb = seg % kSegBufs;
+    if (!wait_warp(&seg_full[sb], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
+    const PpSeg s = segs[sb];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[sb]);
+    if (s.n == 0) break;
+    // the reference: eight tokens' scales a load, all in one page
+    uint32_t top = 0;                                  // bf16 bits, sign off, finite ones
+    const int c0 = s.tile * (kTok / 8), c1 = min((s.tile + s.n) * (kTok / 8), (s.len + 7) >> 3);
+    const int32_t* const table = a.block_table + (int64_t)s.b * a.table_stride;
+#pragma unroll 8
+    for (int c = c0 + 32 * w.cw + lane; c < c1; c += 128) {
+      const int id = table[(8 * c) >> w.lp];
+      if (id >= 0 && id < a.num_pages) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v_scales4 + (((int64_t)id * a.kv_heads + s.h) << w.lp) + ((8 * c) & ((1 << w.lp) - 1))));
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t lo = u[q] & 0x7FFFu, hi = (u[q] >> 16) & 0x7FFFu;
+          if (lo < 0x7F80u && 8 * c + 2 * q < s.len) top = max(top, lo);
+          if (hi < 0x7F80u && 8 * c + 2 * q + 1 < s.len) top = max(top, hi);
+        }
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) vmax_part[w.cw] = __uint_as_float(top);
+    if (w.cw == 0 && lane == 0) nan_key[sb * kKvDim] = INT32_MAX;
+    group_sync(2, 128);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(vmax_part[k]));
+    const uint32_t e_top = top & 0x7F80u;
+    const float vref = e_top ? __uint_as_float(e_top << 16) : 1.f, vinv = 1.f / vref;
+    if (w.cw == 0 && lane == 0) v_ref[sb] = vref;
+    group_sync(2, 128);                                // before the next segment's maxima
+
+    uint4 x[4];
+    float scale[4];
+    int id = w.id_of(s, s.tile_at(0) * kTok), id2 = s.n > 1 ? w.id_of(s, s.tile_at(1) * kTok) : -1;
+    auto load = [&](int key0) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t at = w.slot(s, id, key0, g);
+        x[g] = make_uint4(0, 0, 0, 0);
+        scale[g] = 0.f;
+        if (at >= 0) {
+          x[g] = __ldg(reinterpret_cast<const uint4*>(v_codes + at * (kKvDim / 2)) + w.part);
+          scale[g] = __bfloat162float(a.v_scales4[at]);
+        }
+      }
+    };
+    load(s.tile_at(0) * kTok);
+    bool ok = true;
+    for (int t = 0; t < s.n; ++t, ++i) {
+      const int key0 = s.tile_at(t) * kTok;
+      if (i >= 2) ok = wait_warp(&v_empty[i & 1], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
+      if (!ok) break;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float ratio = scale[g] * vinv;
+        if (!(fabsf(scale[g]) < INFINITY)) {           // a NaN for the rows that see the key, noted apart: 0 * NaN is NaN
+          ratio = 0.f;
+          atomicMin(&nan_key[sb * kKvDim], key0 + w.row(g));
+        }
+        const __half2 f = __float2half2_rn(ratio);
+        // dims 32 part .. + 31 are half a row of a 64-wide chunk; the two chunks' rows lie on the same banks, so lanes of
+        // the second one write their units in another order
+        const bool second = w.part >= 2;
+        const uint32_t in[4] = {second ? x[g].z : x[g].x, second ? x[g].w : x[g].y, second ? x[g].x : x[g].z, second ? x[g].y : x[g].w};
+        uint8_t* const to = sV + (i & 1) * kVBytes + (w.part >> 1) * kChunkBytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 h = widen8(in[q]);
+          h = make_uint4(mul2(h.x, f), mul2(h.y, f), mul2(h.z, f), mul2(h.w, f));
+          *reinterpret_cast<uint4*>(to + sw128_offset(w.row(g), 4 * (w.part & 1) + (q ^ (second ? 2 : 0)))) = h;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[i & 1]);
+      if (t + 1 < s.n) {
+        id = id2;
+        id2 = t + 2 < s.n ? w.id_of(s, s.tile_at(t + 2) * kTok) : -1;
+        load(s.tile_at(t + 1) * kTok);
+      }
+    }
+    if (!ok) break;
+  }
+  group_leave(2, 128);
+}
+
+template <bool k4, PaMods kModSet>
 __global__ void __launch_bounds__(pp::kThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap k_map, const uint8_t* __restrict__ v_codes,
                         const __grid_constant__ PagedAttnArgs a) {
@@ -421,7 +625,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   const int cta = blockIdx.x, ctas = gridDim.x;
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&k_full[i], 1);
+      mbar_init(&k_full[i], k4 ? 5 : 1);               // 4 bits: the widening warps, and the loader's note of bad pages
       mbar_init(&k_empty[i], 2);                       // both halves' scores
     }
     for (int i = 0; i < 2; ++i) {
@@ -602,13 +806,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           return true;
         };
         if constexpr (kMods || decltype(masked)::value) {
-          raise(pp_max64<kModSet, decltype(masked)::value>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks));
+          raise(pp_max64<k4, kModSet, decltype(masked)::value>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks));
           if (!ok) return;
           w.l += pp_exp64(w, tS + 64 * h);
         } else {
           uint32_t p[32];
           float sum;
-          while (raise(pp_half(w, tS + 64 * h, ks, p, sum))) {
+          while (raise(pp_half<k4>(w, tS + 64 * h, ks, p, sum))) {
           }
           if (!ok) return;
           w.l += sum;
@@ -657,7 +861,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       // a mean of V before its scale comes in: sums over keys times the largest scales would leave fp32's range, and the smallest
       // scales divided by the sums, too
       const float inv = any ? 1.f / l : 0.f;
-      const int* nk = nan_key[seg % kSegBufs];
+      const int* nk = nan_key[seg % kSegBufs];       // (4 bits: a key is NaN as a whole)
 #pragma unroll 1
       for (int c = 0; c < kKvDim; c += 32) {
         uint32_t o[32];
@@ -668,7 +872,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             x[k] = __uint_as_float(o[k]) * inv * vref;
-            if (nk[c + k] < w.limit) x[k] = __int_as_float(0x7FC00000);
+            if (nk[k4 ? 0 : c + k] < w.limit) x[k] = __int_as_float(0x7FC00000);
           }
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + at * kKvDim + c);
@@ -709,6 +913,13 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     }
   } else if (warp < kOutWarp) {
     regs_dec<kRegsConv>();
+    if constexpr (k4) {
+      if (warp < kConvWarp0 + 4) {
+        pp_widen_k4(a, segs, seg_full, seg_empty, k_full, k_empty, sK, err);
+      } else {
+        pp_widen_v4(a, v_codes, segs, seg_full, seg_empty, v_full, v_empty, sV, &nan_key[0][0], vmax_part, v_ref, err);
+      }
+    } else {
     // ---------------------------------------------------------------- V tiles: codes to fp16
     // Two groups of four warps take alternate tiles: eight lanes a row of 16-byte pieces, 16 rows a pass, so that a
     // pass is one 16-key group and lies in one page.  Eight neighbouring lanes hold half of two rows each, whose
@@ -823,6 +1034,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       if (!ok) break;
       i0 += s.n;
     }
+    }
     group_leave(1, 256);
   } else {
     regs_dec<kRegsRest>();
@@ -874,7 +1086,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       // ---------------------------------------------------------------- score products of one half
       const int q = warp - kScoreWarp0;
       const bool leader = elect_one();
-      const uint32_t id_s = idesc_e4m3(128, 64);
+      const uint32_t id_s = idesc_e4m3(128, 64) | (k4 ? kFmtE5m2 << 10 : 0u);
       const uint64_t d_q = smem_desc(smem_u32(sQ + 2 * q * kQTermBytes), 16, 1024, kSwizzle128B);
       const uint64_t d_k = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
       bool ok = true;
@@ -961,7 +1173,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
                 page = -1;
               }
             }
-            ks = page >= 0 ? a.k_scales[(int64_t)page * a.kv_heads + s.h] : 0.f;
+            ks = !k4 && page >= 0 ? a.k_scales[(int64_t)page * a.kv_heads + s.h] : 0.f;
           }
           const int st = i % kKStages, use = i / kKStages;
           if (use > 0) ok = wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls);
@@ -975,12 +1187,15 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && pg_g < 0);
           const bool load = lane < ppt && pg >= 0;
           const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-          if (lane < 8) sks[i % kMetaBufs][lane] = kg;
+          if (!k4 && lane < 8) sks[i % kMetaBufs][lane] = kg;
           if (lane == 0) sbad[i % kMetaBufs] = bad;
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&k_full[st], loads * page_bytes);
+          if (lane == 0) {
+            if (k4) mbar_arrive(&k_full[st]);
+            else mbar_arrive_expect_tx(&k_full[st], loads * page_bytes);
+          }
           __syncwarp();
-          if (load) tma_load_2d_hint(sK + st * kKBytes + lane * page_bytes, &k_map, 0, (pg * a.kv_heads + s.h) << lp, &k_full[st], policy);
+          if (!k4 && load) tma_load_2d_hint(sK + st * kKBytes + lane * page_bytes, &k_map, 0, (pg * a.kv_heads + s.h) << lp, &k_full[st], policy);
         }
         if (!ok) break;
       }
@@ -1002,6 +1217,27 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   }
 }
 
+template <bool k4>
+cudaError_t launch_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, const uint8_t* v_codes, int ctas, cudaStream_t s) {
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = once_per_device(ready, [] {
+    const int most = pp::kFixedSmem;
+    cudaError_t r = cudaFuncSetAttribute(paged_prompt_kernel<k4, kPaPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<k4, kPaCapBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<k4, kPaLargeCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  const PaMods mods = pa_mods(a);
+  auto kernel = mods == kPaPlain     ? paged_prompt_kernel<k4, kPaPlain>
+                : mods == kPaCapBias ? paged_prompt_kernel<k4, kPaCapBias>
+                                     : paged_prompt_kernel<k4, kPaLargeCap>;
+  e = launch_pdl(kernel, dim3(ctas), dim3(pp::kThreads), pp::kFixedSmem, s, k_map, v_codes, a);
+  count_launches(1);
+  return e;
+}
+
+#ifndef DSA_PAGED_KERNEL_ONLY
 // Joins the pieces of the segments that CTA boundaries cut, as pa_join: a thread a pair, 16 dims of it per y.
 __device__ __forceinline__ void pp_join(const PagedAttnArgs& a, int ctas, int c, int y) {
   const PaRecord rec = pa_load_record(a, c);
@@ -1070,29 +1306,18 @@ __global__ void __launch_bounds__(kPromptPairs)
   else pp_join(a, ctas, blockIdx.x + 1, y - few_y);
 }
 
-cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
-                                const uint8_t* v_codes, int ctas, cudaStream_t s) {
-  static std::atomic<uint64_t> ready{0};
-  cudaError_t e = once_per_device(ready, [] {
-    const int most = pp::kFixedSmem;
-    cudaError_t r = cudaFuncSetAttribute(paged_prompt_kernel<kPaPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<kPaCapBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<kPaLargeCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    return r;
-  });
-  if (e != cudaSuccess) return e;
-  const PaMods mods = pa_mods(a);
-  auto kernel = mods == kPaPlain     ? paged_prompt_kernel<kPaPlain>
-                : mods == kPaCapBias ? paged_prompt_kernel<kPaCapBias>
-                                     : paged_prompt_kernel<kPaLargeCap>;
-  e = launch_pdl(kernel, dim3(ctas), dim3(pp::kThreads), pp::kFixedSmem, s, k_map, v_codes, a);
+cudaError_t launch_prompt_join(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, int ctas, cudaStream_t s) {
+  if (ctas < 2 || a.whole) return cudaSuccess;
+  const cudaError_t e = launch_pdl(paged_prompt_join_kernel, dim3(ctas - 1, few_y + kKvDim / 16), dim3(kPromptPairs), 0, s, a, few, few_y, ctas);
   count_launches(1);
-  if (e != cudaSuccess) return e;
-  if (ctas > 1 && !a.whole) {
-    e = launch_pdl(paged_prompt_join_kernel, dim3(ctas - 1, few_y + kKvDim / 16), dim3(kPromptPairs), 0, s, a, few, few_y, ctas);
-    count_launches(1);
-  }
   return e;
 }
+
+cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
+                                const uint8_t* v_codes, int ctas, cudaStream_t s) {
+  const cudaError_t e = launch_prompt<false>(a, k_map, v_codes, ctas, s);
+  return e != cudaSuccess ? e : launch_prompt_join(a, few, few_y, ctas, s);
+}
+#endif  // DSA_PAGED_KERNEL_ONLY
 
 }  // namespace dsa

@@ -697,10 +697,11 @@ DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_bat
  *   z_s = scale * q[r,h] . (k_code_s * k_scale_s)      out[r,h] = sum_s softmax(z)_s * (v_code_s * v_scale_s)
  * What lies in the cache behind a request's tokens is never used, NaN scales included; a NaN scale makes the output of the rows
  * that see its token NaN.
- * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-22 of its
- * row's largest value, taken as 2^-100 where it is smaller.  Requests of at most 64 rows * heads per K/V head keep 8 bits or more
- * of a contribution p * v_scale to the output, with an absolute error of 2^-20 of the largest one; requests of more keep 11 bits
- * of p and of v_code * v_scale, V to 2^-25 of the largest V scale of the request's tokens, those that a row does not see included.
+ * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-18 of its
+ * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
+ * Requests of at most 64 rows * heads per K/V head keep 8 bits or more of a contribution p * v_scale to the output, with
+ * an absolute error of 2^-20 of the largest one; requests of more keep 11 bits of p, and hold V to 2^-25 of the largest V
+ * scale of the request's tokens, those that a row does not see included.
  */
 DSA_API dsa_status dsa_kv4_attention(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
                                      int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,
