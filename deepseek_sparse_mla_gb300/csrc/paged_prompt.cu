@@ -51,7 +51,10 @@ constexpr int kQTermBytes = kHalfPairs * kKvDim;     // 16 KB: one e4m3 term of 
 constexpr int kKBytes = kTok * kKvDim;               // 16 KB of codes
 constexpr int kVBytes = kTok * kKvDim * 2;           // 32 KB of fp16: two 64-wide column chunks of 128-byte rows
 constexpr int kChunkBytes = kTok * 128;
-constexpr int kKStages = 4;
+template <bool k4>
+constexpr int kKStages = k4 ? 3 : 4;
+// 4-bit cache: a tile's codes and scales as they are in the cache, on their way to the widening warps
+constexpr int kRawKBytes = kTok * (kKvDim / 2 + kKv4Blocks), kRawVBytes = kTok * (kKvDim / 2 + 2), kRawStages = 2;
 constexpr int kThreads = 640;
 constexpr int kConvWarp0 = 8, kOutWarp = 16, kScoreWarp0 = 17, kLoadWarp = 19;
 constexpr uint32_t kRegsSoft = 128, kRegsConv = 80, kRegsRest = 64;   // 2 * 128 + 2 * 80 + 64 = 480 = 5 * 96, the launch's
@@ -71,7 +74,8 @@ constexpr int kSegUnits = 4, kModsSegUnits = 2;
 constexpr int kRuns = 512;                           // runs of (request, pairs) entries that are summed
 constexpr int kMetaBufs = 8;                         // tiles whose K scales are kept (a tile's outlive its K stage)
 constexpr int kSegBufs = 4;
-constexpr int kFixedSmem = 4 * kQTermBytes + kKStages * kKBytes + 2 * kVBytes + 1024;
+template <bool k4>
+constexpr int kFixedSmem = 4 * kQTermBytes + kKStages<k4> * kKBytes + 2 * kVBytes + (k4 ? kRawStages * (kRawKBytes + kRawVBytes) : 0) + 1024;
 }  // namespace pp
 
 // (request, 256 pairs): its rows' last key, and the tiles that they see
@@ -408,101 +412,88 @@ __device__ __forceinline__ float pp_queries(const PagedAttnArgs& a, const PpSeg&
   return cf;
 }
 
-// ---- the 4-bit cache's widening warps.  A thread takes 32 codes of a row (16 bytes, and for K one scale) a step: four lanes a
-// row, eight rows a warp and 32 the four warps, in four steps a tile.  The next tile's loads go out after the last tile's
-// fence, which would wait for loads in flight too.
-struct PpWiden {
-  const PagedAttnArgs& a;
-  int lp, cw, part, sub;
-  __device__ PpWiden(const PagedAttnArgs& args)
-      : a(args), lp(args.log2_page), cw((threadIdx.x >> 5) & 3), part(threadIdx.x & 3), sub((threadIdx.x >> 2) & 7) {}
-  __device__ __forceinline__ int row(int g) const { return 32 * g + 8 * cw + sub; }
-  // lane j (and j + 8, ..): the page of 16-key group j of the tile at key0, -1 where there is none (the loader reports bad ids)
-  __device__ __forceinline__ int id_of(const PpSeg& s, int key0) const {
-    const int p = (key0 + 16 * (threadIdx.x & 7)) >> lp, pages = (s.len + (1 << lp) - 1) >> lp;
-    const int id = p < pages ? a.block_table[(int64_t)s.b * a.table_stride + p] : -1;
-    return id < a.num_pages ? id : -1;
-  }
-  // the row in the cache of step g's key, -1 where there is none
-  __device__ __forceinline__ int64_t slot(const PpSeg& s, int id, int key0, int g) const {
-    const int page = __shfl_sync(0xffffffffu, id, 2 * g + (cw >> 1)), key = key0 + row(g);
-    return page >= 0 && key < s.len ? (((int64_t)page * a.kv_heads + s.h) << lp) + (key & ((1 << lp) - 1)) : -1;
-  }
+// ---- the 4-bit cache's widening warps.  The loader copies a tile's codes and scales into shared memory as they are; a thread takes
+// 32 codes of a row (16 bytes, and for K one scale) a step: four lanes a row, eight rows a warp and 32 the four warps, in
+// four steps a tile.  (Loads from the cache straight into registers, a tile ahead, took 5.7 ms for 4,096 rows at 64K: a fence
+// waits for loads in flight, so they had only the time between two of them.)
+struct PpRaw {
+  uint8_t* bytes;                  // [stages] of codes, then scales
+  uint64_t *full, *empty;          // [stages]
+  const uint32_t* bad;             // [kMetaBufs] 16-key groups without a valid page
 };
 
-// K tiles: code * 2^e as e5m2, the upper bytes of the same numbers in fp16
-__device__ __forceinline__ void pp_widen_k4(const PagedAttnArgs& a, const PpSeg* segs, uint64_t* seg_full, uint64_t* seg_empty,
-                                            uint64_t* k_full, uint64_t* k_empty, uint8_t* sK, uint32_t* err) {
+// The bytes of e5m2(code * 2^e) for e2m1 codes 0 .. 3 and 4 .. 7 without their sign, from a scale byte; NaN for the NaN scale.  With
+// k = e + 14 >= 1 code c stands for exponent field k + (c >> 1) and mantissa bits c & 1, 0, but for 0 and for 1 = 2^-1,
+// whose mantissa is 0; below, the small ones are subnormal numbers.
+__device__ __forceinline__ void pp_e5m2_table(uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  static_assert(kKv4LowExp == -15 && kKv4HighExp == 13, "what e5m2 holds exactly");
+  const int k = min(max((int)scale - 127, kKv4LowExp), kKv4HighExp) + 14;
+  hi = 0x0E0C0A08u + (uint32_t)k * 0x04040404u;
+  lo = k > 0 ? 0x06040000u + (uint32_t)k * 0x04040400u : k == 0 ? 0x06040200u : 0x03020100u;
+  if (scale == 255u) lo = hi = 0x7F7F7F7Fu;
+}
+
+// Eight codes: magnitudes looked up four at a time by a byte permutation, whose other mode spreads the sign bits
+__device__ __forceinline__ uint2 pp_e5m2(uint32_t w, uint32_t lo, uint32_t hi) {
+  const uint32_t m = w & 0x77777777u, l = w << 4;
+  uint32_t s0, s1;
+  asm("prmt.b32 %0, %1, %2, 0xD9C8;" : "=r"(s0) : "r"(l), "r"(w));
+  asm("prmt.b32 %0, %1, %2, 0xFBEA;" : "=r"(s1) : "r"(l), "r"(w));
+  return make_uint2(__byte_perm(lo, hi, m) | (s0 & 0x80808080u), __byte_perm(lo, hi, m >> 16) | (s1 & 0x80808080u));
+}
+
+// K tiles: code * 2^e as e5m2
+__device__ __forceinline__ void pp_widen_k4(const PpSeg* segs, uint64_t* seg_full, uint64_t* seg_empty, uint64_t* k_full, uint64_t* k_empty,
+                                            uint8_t* sK, const PpRaw& raw, uint32_t* err) {
   using namespace pp;
-  const PpWiden w(a);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, part = lane & 3, row0 = 8 * ((threadIdx.x >> 5) & 3) + (lane >> 2);
   int i = 0;
   for (int seg = 0;; ++seg) {
     if (!wait_warp(&seg_full[seg % kSegBufs], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls)) return;
-    const PpSeg s = segs[seg % kSegBufs];
+    const int n = segs[seg % kSegBufs].n;
     __syncwarp();
     if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
-    if (s.n == 0) return;
-    uint4 x[4];
-    uint32_t e[4];
-    int id = w.id_of(s, s.tile_at(0) * kTok), id2 = s.n > 1 ? w.id_of(s, s.tile_at(1) * kTok) : -1;
-    auto load = [&](int key0) {
+    if (n == 0) return;
+    for (int t = 0; t < n; ++t, ++i) {
+      const int st = i % kKStages<true>, use = i / kKStages<true>, rb = i % kRawStages;
+      if (!wait_warp(&raw.full[rb], (i / kRawStages) & 1, err, kErrTmaTimeout, kPolls)) return;
+      const uint8_t* const from = raw.bytes + rb * kRawKBytes;
+      uint4 x[4];
+      uint32_t e[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int64_t at = w.slot(s, id, key0, g);
-        x[g] = make_uint4(0, 0, 0, 0);
-        e[g] = 127;
-        if (at >= 0) {
-          x[g] = __ldg(reinterpret_cast<const uint4*>(a.k_codes4 + at * (kKvDim / 2)) + w.part);
-          e[g] = __ldg(a.k_scales4 + at * kKv4Blocks + w.part);
-        }
+        x[g] = reinterpret_cast<const uint4*>(from)[(32 * g + row0) * 4 + part];
+        e[g] = from[kTok * kKvDim / 2 + (32 * g + row0) * kKv4Blocks + part];
       }
-    };
-    load(s.tile_at(0) * kTok);
-    for (int t = 0; t < s.n; ++t, ++i) {
-      const int st = i % kKStages, use = i / kKStages;
       if (use > 0 && !wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) return;
+      uint8_t* const to = sK + st * kKBytes;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        // 2^e in fp16 (2^-15 is a subnormal number); the NaN scale makes NaN codes
-        const int ex = min(max((int)e[g] - 127, kKv4LowExp), kKv4HighExp);
-        const uint32_t f1 = e[g] == 255u ? 0x7E00u : ex == -15 ? 0x0200u : (uint32_t)(ex + 15) << 10;
-        const uint32_t f2 = f1 | f1 << 16;
-        const __half2 f = *reinterpret_cast<const __half2*>(&f2);
-        const uint32_t in[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
-        uint32_t out[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint4 h = widen8(in[q]);
-          out[2 * q] = __byte_perm(mul2(h.x, f), mul2(h.y, f), 0x7531);
-          out[2 * q + 1] = __byte_perm(mul2(h.z, f), mul2(h.w, f), 0x7531);
-        }
-        const int r = w.row(g);
-        uint8_t* const to = sK + st * kKBytes;
-        *reinterpret_cast<uint4*>(to + sw128_offset(r, 2 * w.part)) = make_uint4(out[0], out[1], out[2], out[3]);
-        *reinterpret_cast<uint4*>(to + sw128_offset(r, 2 * w.part + 1)) = make_uint4(out[4], out[5], out[6], out[7]);
+        uint32_t lo, hi;
+        pp_e5m2_table(e[g], lo, hi);
+        const uint2 a = pp_e5m2(x[g].x, lo, hi), b = pp_e5m2(x[g].y, lo, hi), c = pp_e5m2(x[g].z, lo, hi), d = pp_e5m2(x[g].w, lo, hi);
+        *reinterpret_cast<uint4*>(to + sw128_offset(32 * g + row0, 2 * part)) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(to + sw128_offset(32 * g + row0, 2 * part + 1)) = make_uint4(c.x, c.y, d.x, d.y);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[st]);
-      if (t + 1 < s.n) {
-        id = id2;
-        id2 = t + 2 < s.n ? w.id_of(s, s.tile_at(t + 2) * kTok) : -1;
-        load(s.tile_at(t + 1) * kTok);
+      if (lane == 0) {
+        mbar_arrive(&k_full[st]);
+        mbar_arrive(&raw.empty[rb]);
       }
     }
   }
 }
 
 // V tiles: code * scale in fp16, in units of the power of two at or below the piece's largest scale
-__device__ __forceinline__ void pp_widen_v4(const PagedAttnArgs& a, const uint8_t* v_codes, const PpSeg* segs, uint64_t* seg_full,
-                                            uint64_t* seg_empty, uint64_t* v_full, uint64_t* v_empty, uint8_t* sV, int* nan_key,
+__device__ __forceinline__ void pp_widen_v4(const PagedAttnArgs& a, const PpSeg* segs, uint64_t* seg_full, uint64_t* seg_empty,
+                                            uint64_t* v_full, uint64_t* v_empty, uint8_t* sV, const PpRaw& raw, int* nan_key,
                                             float* vmax_part, float* v_ref, uint32_t* err) {
   using namespace pp;
-  const PpWiden w(a);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) & 3, part = lane & 3, row0 = 8 * cw + (lane >> 2), lp = a.log2_page;
   int i = 0;
-  for (int seg = 0;; ++seg) {
+  bool ok = true;
+  for (int seg = 0; ok; ++seg) {
     const int sb = seg % kSegBufs;
     if (!wait_warp(&seg_full[sb], (seg / kSegBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
     const PpSeg s = segs[sb];
@@ -514,10 +505,10 @@ __device__ __forceinline__ void pp_widen_v4(const PagedAttnArgs& a, const uint8_
     const int c0 = s.tile * (kTok / 8), c1 = min((s.tile + s.n) * (kTok / 8), (s.len + 7) >> 3);
     const int32_t* const table = a.block_table + (int64_t)s.b * a.table_stride;
 #pragma unroll 8
-    for (int c = c0 + 32 * w.cw + lane; c < c1; c += 128) {
-      const int id = table[(8 * c) >> w.lp];
+    for (int c = c0 + 32 * cw + lane; c < c1; c += 128) {
+      const int id = table[(8 * c) >> lp];
       if (id >= 0 && id < a.num_pages) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v_scales4 + (((int64_t)id * a.kv_heads + s.h) << w.lp) + ((8 * c) & ((1 << w.lp) - 1))));
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.v_scales4 + (((int64_t)id * a.kv_heads + s.h) << lp) + ((8 * c) & ((1 << lp) - 1))));
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -528,67 +519,60 @@ __device__ __forceinline__ void pp_widen_v4(const PagedAttnArgs& a, const uint8_
       }
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) vmax_part[w.cw] = __uint_as_float(top);
-    if (w.cw == 0 && lane == 0) nan_key[sb * kKvDim] = INT32_MAX;
+    if (lane == 0) vmax_part[cw] = __uint_as_float(top);
+    if (cw == 0 && lane == 0) nan_key[sb * kKvDim] = INT32_MAX;
     group_sync(2, 128);
 #pragma unroll
     for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(vmax_part[k]));
     const uint32_t e_top = top & 0x7F80u;
     const float vref = e_top ? __uint_as_float(e_top << 16) : 1.f, vinv = 1.f / vref;
-    if (w.cw == 0 && lane == 0) v_ref[sb] = vref;
+    if (cw == 0 && lane == 0) v_ref[sb] = vref;
     group_sync(2, 128);                                // before the next segment's maxima
-
-    uint4 x[4];
-    float scale[4];
-    int id = w.id_of(s, s.tile_at(0) * kTok), id2 = s.n > 1 ? w.id_of(s, s.tile_at(1) * kTok) : -1;
-    auto load = [&](int key0) {
+    for (int t = 0; t < s.n; ++t, ++i) {
+      const int key0 = s.tile_at(t) * kTok, rb = i % kRawStages;
+      ok = wait_warp(&raw.full[rb], (i / kRawStages) & 1, err, kErrTmaTimeout, kPolls);
+      if (!ok) break;
+      const uint8_t* const from = raw.bytes + rb * kRawVBytes;
+      const uint32_t bad = raw.bad[i % kMetaBufs];
+      uint4 x[4];
+      float scale[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int64_t at = w.slot(s, id, key0, g);
-        x[g] = make_uint4(0, 0, 0, 0);
-        scale[g] = 0.f;
-        if (at >= 0) {
-          x[g] = __ldg(reinterpret_cast<const uint4*>(v_codes + at * (kKvDim / 2)) + w.part);
-          scale[g] = __bfloat162float(a.v_scales4[at]);
-        }
+        const int row = 32 * g + row0;
+        x[g] = reinterpret_cast<const uint4*>(from)[row * 4 + part];
+        scale[g] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(from + kTok * kKvDim / 2)[row]);
+        // what lies behind the request's tokens, or in a page that was not loaded, is anything
+        if (key0 + row >= s.len || ((bad >> (row >> 4)) & 1u)) scale[g] = 0.f;
       }
-    };
-    load(s.tile_at(0) * kTok);
-    bool ok = true;
-    for (int t = 0; t < s.n; ++t, ++i) {
-      const int key0 = s.tile_at(t) * kTok;
       if (i >= 2) ok = wait_warp(&v_empty[i & 1], ((i >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
       if (!ok) break;
+      uint8_t* const to = sV + (i & 1) * kVBytes + (part >> 1) * kChunkBytes;
+      // dims 32 part .. + 31 are half a row of a 64-wide chunk; the two chunks' rows lie on the same banks, so lanes of the
+      // second one write their units in another order
+      const bool second = part >= 2;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float ratio = scale[g] * vinv;
         if (!(fabsf(scale[g]) < INFINITY)) {           // a NaN for the rows that see the key, noted apart: 0 * NaN is NaN
           ratio = 0.f;
-          atomicMin(&nan_key[sb * kKvDim], key0 + w.row(g));
+          atomicMin(&nan_key[sb * kKvDim], key0 + 32 * g + row0);
         }
         const __half2 f = __float2half2_rn(ratio);
-        // dims 32 part .. + 31 are half a row of a 64-wide chunk; the two chunks' rows lie on the same banks, so lanes of
-        // the second one write their units in another order
-        const bool second = w.part >= 2;
         const uint32_t in[4] = {second ? x[g].z : x[g].x, second ? x[g].w : x[g].y, second ? x[g].x : x[g].z, second ? x[g].y : x[g].w};
-        uint8_t* const to = sV + (i & 1) * kVBytes + (w.part >> 1) * kChunkBytes;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint4 h = widen8(in[q]);
           h = make_uint4(mul2(h.x, f), mul2(h.y, f), mul2(h.z, f), mul2(h.w, f));
-          *reinterpret_cast<uint4*>(to + sw128_offset(w.row(g), 4 * (w.part & 1) + (q ^ (second ? 2 : 0)))) = h;
+          *reinterpret_cast<uint4*>(to + sw128_offset(32 * g + row0, 4 * (part & 1) + (q ^ (second ? 2 : 0)))) = h;
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[i & 1]);
-      if (t + 1 < s.n) {
-        id = id2;
-        id2 = t + 2 < s.n ? w.id_of(s, s.tile_at(t + 2) * kTok) : -1;
-        load(s.tile_at(t + 1) * kTok);
+      if (lane == 0) {
+        mbar_arrive(&v_full[i & 1]);
+        mbar_arrive(&raw.empty[rb]);
       }
     }
-    if (!ok) break;
   }
   group_leave(2, 128);
 }
@@ -600,14 +584,17 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   using namespace pp;
   constexpr bool kMods = kModSet != kPaPlain;
   constexpr int kEnds = kMods ? kModsSegUnits : kSegUnits;
+  constexpr int kKStages = pp::kKStages<k4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + 4 * kQTermBytes;
   uint8_t* sV = sK + kKStages * kKBytes;
+  uint8_t* sRaw = sV + 2 * kVBytes;                      // 4 bits: [raw stages] of K, then of V
   int32_t* entry_end = reinterpret_cast<int32_t*>(sV);   // [requests] entries of requests 0 .. b, before V is there
 
   __shared__ uint64_t k_full[kKStages], k_empty[kKStages], v_full[2], v_empty[2];
+  __shared__ uint64_t rawk_full[kRawStages], rawk_empty[kRawStages], rawv_full[kRawStages], rawv_empty[kRawStages];
   __shared__ uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // by pairs' half and keys' half
   __shared__ uint64_t q_full[2], o_full[2], o_empty[2], mma_done;
   __shared__ __align__(16) float sks[kMetaBufs][8];   // K scale of each 16 keys of a tile
@@ -625,7 +612,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
   const int cta = blockIdx.x, ctas = gridDim.x;
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&k_full[i], k4 ? 5 : 1);               // 4 bits: the widening warps, and the loader's note of bad pages
+      mbar_init(&k_full[i], k4 ? 4 : 1);               // 4 bits: the widening warps
       mbar_init(&k_empty[i], 2);                       // both halves' scores
     }
     for (int i = 0; i < 2; ++i) {
@@ -639,6 +626,12 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       mbar_init(&q_full[i], 4);
       mbar_init(&o_full[i], 2);
       mbar_init(&o_empty[i], 4);
+    }
+    for (int i = 0; i < kRawStages; ++i) {
+      mbar_init(&rawk_full[i], 1);
+      mbar_init(&rawv_full[i], 1);
+      mbar_init(&rawk_empty[i], 4);
+      mbar_init(&rawv_empty[i], 4);
     }
     for (int i = 0; i < kSegBufs; ++i) {
       mbar_init(&seg_full[i], 1);
@@ -915,9 +908,10 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
     regs_dec<kRegsConv>();
     if constexpr (k4) {
       if (warp < kConvWarp0 + 4) {
-        pp_widen_k4(a, segs, seg_full, seg_empty, k_full, k_empty, sK, err);
+        pp_widen_k4(segs, seg_full, seg_empty, k_full, k_empty, sK, PpRaw{sRaw, rawk_full, rawk_empty, sbad}, err);
       } else {
-        pp_widen_v4(a, v_codes, segs, seg_full, seg_empty, v_full, v_empty, sV, &nan_key[0][0], vmax_part, v_ref, err);
+        pp_widen_v4(a, segs, seg_full, seg_empty, v_full, v_empty, sV,
+                    PpRaw{sRaw + kRawStages * kRawKBytes, rawv_full, rawv_empty, sbad}, &nan_key[0][0], vmax_part, v_ref, err);
       }
     } else {
     // ---------------------------------------------------------------- V tiles: codes to fp16
@@ -1175,10 +1169,42 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             }
             ks = !k4 && page >= 0 ? a.k_scales[(int64_t)page * a.kv_heads + s.h] : 0.f;
           }
-          const int st = i % kKStages, use = i / kKStages;
-          if (use > 0) ok = wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls);
+          const int st = i % kKStages, use = i / kKStages, rb = i % kRawStages;
+          if (k4) {
+            if (i >= kRawStages)
+              ok = wait_warp(&rawk_empty[rb], (i / kRawStages - 1) & 1, err, kErrMmaTimeout, kPolls) &&
+                   wait_warp(&rawv_empty[rb], (i / kRawStages - 1) & 1, err, kErrMmaTimeout, kPolls);
+          } else if (use > 0) {
+            ok = wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls);
+          }
           if (!ok) break;
           const int o = p0 & 31;
+          if constexpr (k4) {
+            // lanes 0 .. ppt - 1 copy the pages' K codes, 8 .. their scales, 16 .. V's codes, 24 .. their scales
+            const int mine = lane & 7, what = lane >> 3;
+            const int id = __shfl_sync(0xffffffffu, page, (o + mine) & 31);
+            const int of_group = __shfl_sync(0xffffffffu, page, (o + ((16 * mine) >> lp)) & 31);
+            const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && of_group < 0);
+            const bool load = mine < ppt && id >= 0;
+            const uint32_t loads = __popc(__ballot_sync(0xffffffffu, lane < 8 && load));
+            if (lane == 0) {
+              sbad[i % kMetaBufs] = bad;
+              mbar_arrive_expect_tx(&rawk_full[rb], loads * ((kKvDim / 2 + kKv4Blocks) << lp));
+              mbar_arrive_expect_tx(&rawv_full[rb], loads * ((kKvDim / 2 + 2) << lp));
+            }
+            __syncwarp();
+            if (load) {
+              const int64_t row = ((int64_t)id * a.kv_heads + s.h) << lp;
+              uint8_t* const tk = sRaw + rb * kRawKBytes;
+              uint8_t* const tv = sRaw + kRawStages * kRawKBytes + rb * kRawVBytes;
+              const void* src = what == 0 ? (const void*)(a.k_codes4 + row * (kKvDim / 2)) : what == 1 ? (const void*)(a.k_scales4 + row * kKv4Blocks)
+                              : what == 2 ? (const void*)(v_codes + row * (kKvDim / 2)) : (const void*)(a.v_scales4 + row);
+              const uint32_t bytes = (what & 1) ? (what == 1 ? kKv4Blocks << lp : 2 << lp) : (kKvDim / 2) << lp;
+              uint8_t* const to = (what < 2 ? tk : tv) + ((what & 1) ? kTok * kKvDim / 2 : 0) + mine * bytes;
+              bulk_load_hint(to, src, bytes, what < 2 ? &rawk_full[rb] : &rawv_full[rb], policy);
+            }
+            continue;
+          }
           const int pg = __shfl_sync(0xffffffffu, page, (o + lane) & 31);
           // 16-key group g lies in page g * 16 / page size of the tile
           const int of_group = (o + ((16 * (lane & 7)) >> lp)) & 31;
@@ -1187,21 +1213,27 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && pg_g < 0);
           const bool load = lane < ppt && pg >= 0;
           const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-          if (!k4 && lane < 8) sks[i % kMetaBufs][lane] = kg;
+          if (lane < 8) sks[i % kMetaBufs][lane] = kg;
           if (lane == 0) sbad[i % kMetaBufs] = bad;
           __syncwarp();
-          if (lane == 0) {
-            if (k4) mbar_arrive(&k_full[st]);
-            else mbar_arrive_expect_tx(&k_full[st], loads * page_bytes);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[st], loads * page_bytes);
           __syncwarp();
-          if (!k4 && load) tma_load_2d_hint(sK + st * kKBytes + lane * page_bytes, &k_map, 0, (pg * a.kv_heads + s.h) << lp, &k_full[st], policy);
+          if (load) tma_load_2d_hint(sK + st * kKBytes + lane * page_bytes, &k_map, 0, (pg * a.kv_heads + s.h) << lp, &k_full[st], policy);
         }
         if (!ok) break;
       }
       // nothing may still be landing in shared memory when the CTA exits
-      for (int st = 0; st < kKStages; ++st)
-        if (i > st) wait_warp(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
+      if constexpr (k4) {
+        for (int rb = 0; rb < kRawStages; ++rb)
+          if (i > rb) {
+            const uint32_t last = ((i - rb + kRawStages - 1) / kRawStages - 1) & 1;
+            wait_warp(&rawk_full[rb], last, err, kErrTmaTimeout, kPolls);
+            wait_warp(&rawv_full[rb], last, err, kErrTmaTimeout, kPolls);
+          }
+      } else {
+        for (int st = 0; st < kKStages; ++st)
+          if (i > st) wait_warp(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);
+      }
     }
   }
   tc_fence_before();
@@ -1221,7 +1253,7 @@ template <bool k4>
 cudaError_t launch_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, const uint8_t* v_codes, int ctas, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = once_per_device(ready, [] {
-    const int most = pp::kFixedSmem;
+    const int most = pp::kFixedSmem<k4>;
     cudaError_t r = cudaFuncSetAttribute(paged_prompt_kernel<k4, kPaPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<k4, kPaCapBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (r == cudaSuccess) r = cudaFuncSetAttribute(paged_prompt_kernel<k4, kPaLargeCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -1232,7 +1264,7 @@ cudaError_t launch_prompt(const PagedAttnArgs& a, const CUtensorMap& k_map, cons
   auto kernel = mods == kPaPlain     ? paged_prompt_kernel<k4, kPaPlain>
                 : mods == kPaCapBias ? paged_prompt_kernel<k4, kPaCapBias>
                                      : paged_prompt_kernel<k4, kPaLargeCap>;
-  e = launch_pdl(kernel, dim3(ctas), dim3(pp::kThreads), pp::kFixedSmem, s, k_map, v_codes, a);
+  e = launch_pdl(kernel, dim3(ctas), dim3(pp::kThreads), pp::kFixedSmem<k4>, s, k_map, v_codes, a);
   count_launches(1);
   return e;
 }
