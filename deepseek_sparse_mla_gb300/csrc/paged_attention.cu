@@ -55,7 +55,7 @@ constexpr int kTileBytes = kTok * kKvDim;       // 16 KB: codes of 8 bits, or of
 constexpr int kStageBytes = 2 * kTileBytes;     // K, then V
 constexpr int kColMax = kPagedAttnColumns;
 constexpr int kMaxPages = kTok / kKvMinPage;    // pages of a tile
-constexpr int kScoreWarp = 1, kOutWarp = 3, kSoftWarp0 = 4;
+constexpr int kScoreWarp = 1, kQueryWarp = 2, kOutWarp = 3, kLoadVWarp = 4;
 constexpr int kQBufs = 3;                       // the scores run two tiles a warpgroup, so up to two segments, ahead of the outputs
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
@@ -74,17 +74,25 @@ struct Form {
   static constexpr int kHalf = kCE < 16 ? 16 : kCE;   // columns of the hi half (and of the lo half)
   static constexpr int kN = 2 * kHalf;                // 32 or 64
   static constexpr int kWgs = 2;                      // softmax warpgroups
-  static constexpr int kThreads = 128 * (1 + kWgs);
-  static constexpr uint32_t kRegsLow = 88, kRegsSoft = 208;   // 88 + 2 * 208 = 3 * 168, the launch's
-  static constexpr int kStages = k4 ? 4 : 5;
+  static constexpr int kSoftWarp0 = k4 ? 8 : 4;       // warps before them: 4 bits take a second loader
+  static constexpr int kThreads = 32 * kSoftWarp0 + 128 * kWgs;
+  // 88 + 2 * 208 = 3 * 168, 2 * 64 + 2 * 192 = 4 * 128: the launch's
+  static constexpr uint32_t kRegsLow = k4 ? 64 : 88, kRegsSoft = k4 ? 192 : 208;
+  // 8 bits: one ring of stages (K, then V).  4 bits: a ring each, as K is done with after the scores' products.
+  static constexpr int kStages = k4 && kCE > 16 ? 4 : 5, kVStages = 5;
+  static constexpr int kKStride = k4 ? kTileBytes : kStageBytes, kVStride = kKStride;
+  static constexpr int kVOffset = k4 ? kStages * kTileBytes : kTileBytes;
+  static constexpr int kTilesBytes = k4 ? (kStages + kVStages) * kTileBytes : kStages * kStageBytes;
+  static constexpr int kPBufs = k4 ? 2 : 1;           // probabilities' buffers a warpgroup
   static constexpr int kSBufs = 2 * kWgs;             // two a warpgroup: one is kept until its tile is known to be done
   static constexpr int kColsS = k4 ? kHalf : 64;      // TMEM columns of a tile's scores
   static constexpr int kColScales = 192, kColQScales = 216;
   static constexpr int kColsO = k4 ? kN : 64, kOSeg = kWgs * kColsO;
-  static constexpr int kQBytes = 2 * kColMax * kKvDim;        // hi and lo rows of 32 columns
-  static constexpr int kPBytes = kTok * 2 * kColMax;
-  static constexpr int kScaleBytes = k4 ? kTok * (kKv4Blocks + 2) : 0;   // a tile's K scales, then V's
-  static constexpr int kFixedSmem = kStages * (kStageBytes + kScaleBytes) + kQBufs * kQBytes + kWgs * kPBytes + 1024;
+  static constexpr int kQBytes = (k4 ? kN : 2 * kColMax) * kKvDim;   // hi and lo rows of the columns
+  static constexpr int kPBytes = kTok * (k4 ? kN : 2 * kColMax);
+  static constexpr int kKScales = k4 ? kTok * kKv4Blocks : 0, kVScales = k4 ? kTok * 2 : 0;   // bytes of a tile's scales
+  static constexpr int kScaleBytes = kStages * kKScales + kVStages * kVScales;
+  static constexpr int kFixedSmem = kTilesBytes + kQBufs * kQBytes + kWgs * kPBufs * kPBytes + kScaleBytes + 1024;
   static_assert(!k4 || (kSBufs * kHalf <= kColScales && kColScales + 4 * kSBufs <= kColQScales), "TMEM columns");
   static_assert(kColO + 2 * kOSeg <= (int)kTmemCols, "TMEM columns");
 };
@@ -168,19 +176,21 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
   using F = Form<k4, kCE>;
   constexpr bool kMods = kModSet != kPaPlain;
   constexpr int kHalf = F::kHalf, kN = F::kN, kStages = F::kStages, kSBufs = F::kSBufs, kWgs = F::kWgs, kThreads = F::kThreads;
-  constexpr int kQBytes = F::kQBytes, kPBytes = F::kPBytes;
+  constexpr int kVStages = F::kVStages, kSoftWarp0 = F::kSoftWarp0;
+  constexpr int kQBytes = F::kQBytes, kPBytes = F::kPBytes, kPBufs = F::kPBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
-  uint8_t* sQ = sKV + kStages * kStageBytes;
+  uint8_t* sQ = sKV + F::kTilesBytes;
   uint8_t* sP = sQ + kQBufs * kQBytes;
-  uint8_t* sScale = sP + kWgs * kPBytes;                         // 4 bits: [stages] of K's scales, then V's
-  int32_t* end = reinterpret_cast<int32_t*>(sScale + kStages * F::kScaleBytes);   // [requests]
+  uint8_t* sScaleK = sP + kWgs * kPBufs * kPBytes;               // 4 bits: [stages] of K's scales, then V's
+  uint8_t* sScaleV = sScaleK + kStages * F::kKScales;
+  int32_t* end = reinterpret_cast<int32_t*>(sScaleK + F::kScaleBytes);   // [requests]
 
-  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], s_full[kSBufs], s_empty[kSBufs], p_full[kWgs];
+  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], v_ring[2 * kVStages], s_full[kSBufs], s_empty[kSBufs], p_full[kWgs * kPBufs], pv_done[kWgs * kPBufs];
   __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[2], o_empty[2], mma_done;
   __shared__ float sks[k4 ? 1 : kStages][kMaxPages], svs[k4 ? 1 : kStages][kMaxPages];
-  __shared__ uint32_t sbad[kStages];
+  __shared__ uint32_t sbad[kVStages];
   __shared__ __align__(16) PaColumns cols[kQBufs];
   __shared__ __align__(16) float refs[kWgs][2][kCE];
   __shared__ float wmax[kWgs][4][kCE], fin[kWgs][kWgs][kCE];
@@ -197,7 +207,12 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
-    for (int i = 0; i < kWgs; ++i) mbar_init(&p_full[i], 1);
+    if (k4)
+      for (int i = 0; i < 2 * kVStages; ++i) mbar_init(&v_ring[i], 1);
+    for (int i = 0; i < kWgs * kPBufs; ++i) {
+      mbar_init(&p_full[i], 1);
+      mbar_init(&pv_done[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 4);
@@ -279,14 +294,70 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
     if (s.tile > 0) u0 += s.n;
   }
   uint32_t* const err = &bits_all;                    // this CTA's status bits, stored at the end
+  uint64_t* const v_full = k4 ? v_ring : kv_full;     // 4 bits: kv_full and kv_empty are K's
+  uint64_t* const v_empty = k4 ? v_ring + kVStages : kv_empty;
 
   if (warp < kSoftWarp0) {
   regs_dec<F::kRegsLow>();
-  if (warp == 0) {
+  // 4 bits: a warp loads K (codes and scales) or V.  A load of 4-bit codes counts 64 bytes a row on the barrier: the other half
+  // of each 16-byte unit is not written.
+  auto load4 = [&](auto of_v, const CUtensorMap* map, const uint8_t* scales, uint64_t* full, uint64_t* empty, uint8_t* tiles, uint8_t* to) {
+    constexpr bool kV = decltype(of_v)::value;
+    constexpr int kRing = kV ? kVStages : kStages, kScale = kV ? 2 : kKv4Blocks;   // scale bytes of a token
+    const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
+    const int lp = a.log2_page, ppt = kTok >> lp, mine = lane & 7;
+    const bool codes = lane < 8, used = mine < ppt && lane < 16;   // lanes 0 .. ppt - 1 load codes, 8 .. scales
+    uint8_t* const dst = codes ? tiles + mine * (kKvDim << lp) : to + mine * (kScale << lp);
+    int i = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok;) {
+      const PaSeg s = pa_segment(a, end, u, cut);
+      const int pages = (s.len + (1 << lp) - 1) >> lp;
+      int batch = -1, first = -1;                      // 32 pages at a time, one a lane: the first row of its block
+      for (int t = 0; t < s.n && ok; ++t, ++i) {
+        const int p0 = s.template tile_at<kMods>(t) * ppt;
+        if ((p0 >> 5) != batch) {
+          batch = p0 >> 5;
+          const int p = 32 * batch + lane;
+          first = -1;
+          if (p < pages) {
+            const int page = a.block_table[(int64_t)s.b * a.table_stride + p];
+            if (page >= 0 && page < a.num_pages) first = (page * a.kv_heads + s.h) << lp;
+            else atomicOr(err, kErrBadPage);
+          }
+        }
+        const int st = i % kRing, use = i / kRing;
+        if (use > 0 && !mbar_wait_warp(&empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) {
+          ok = false;
+          break;
+        }
+        const int row = __shfl_sync(0xffffffffu, first, (p0 + mine) & 31);
+        const uint32_t bad = __ballot_sync(0xffffffffu, codes && used && row < 0);
+        if (lane == 0) {
+          if (kV) sbad[st] = bad;
+          mbar_arrive_expect_tx(&full[st], (uint32_t)(ppt - __popc(bad)) * ((uint32_t)(kKvDim / 2 + kScale) << lp));
+        }
+        __syncwarp();
+        if (used && row >= 0) {
+          if (codes) tma_load_2d_hint(dst + st * kTileBytes, map, 0, row, &full[st], policy);
+          else bulk_load_hint(dst + st * (kTok * kScale), scales + (int64_t)row * kScale, kScale << lp, &full[st], policy);
+        }
+      }
+      u += s.n;
+    }
+    // nothing may still be landing in shared memory when the CTA exits
+    for (int st = 0; st < kRing; ++st)
+      if (i > st) mbar_wait_warp(&full[st], ((i - st + kRing - 1) / kRing - 1) & 1, err, kErrTmaTimeout, kPolls);
+  };
+  if (k4 && warp == 0) {
+    load4(std::false_type{}, &k_map, a.k_scales4, kv_full, kv_empty, sKV, sScaleK);
+  } else if (k4 && warp == kLoadVWarp) {
+    load4(std::true_type{}, &v_map, reinterpret_cast<const uint8_t*>(a.v_scales4), v_full, v_empty, sKV + F::kVOffset, sScaleV);
+  } else if (!k4 && warp == 0) {
     // ---------------------------------------------------------------- producer
     const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
     const int lp = a.log2_page, ppt = kTok >> lp;
-    const uint32_t page_bytes = (uint32_t)kKvDim << lp;         // of a tile in shared memory
+    const uint32_t page_bytes = (uint32_t)kKvDim << lp;
     int i = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok;) {
@@ -308,7 +379,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
               page = -1;
             }
           }
-          if (!k4 && page >= 0) {                      // (not waited for until the tile's loads are out)
+          if (page >= 0) {                             // (not waited for until the tile's loads are out)
             ks = a.k_scales[(int64_t)page * a.kv_heads + s.h];
             vs = a.v_scales[(int64_t)page * a.kv_heads + s.h];
           }
@@ -318,53 +389,24 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
           ok = false;
           break;
         }
-        // this tile's pages sit in lanes o .. o + ppt - 1
-        const int o = p0 & 31;
-        if constexpr (k4) {
-          // lanes 0 .. ppt - 1 load K, 8 .. its scales, 16 .. V, 24 .. its scales.  A load of 4-bit codes counts 64 bytes a row
-          // on the barrier: the other half of each 16-byte unit is not written.
-          const int mine = lane & 7, what = lane >> 3;
-          const int pg = __shfl_sync(0xffffffffu, page, (o + mine) & 31);
-          const bool load = mine < ppt && pg >= 0;
-          const uint32_t bad = __ballot_sync(0xffffffffu, mine < ppt && pg < 0) & 0xFFu;
-          if (lane == 0) {
-            sbad[st] = bad;
-            mbar_arrive_expect_tx(&kv_full[st], (uint32_t)(ppt - __popc(bad)) * ((uint32_t)(kKvDim + kKv4Blocks + 2) << lp));
-          }
-          __syncwarp();
-          if (load) {
-            const int64_t block = (int64_t)pg * a.kv_heads + s.h;
-            if ((what & 1) == 0) {
-              tma_load_2d_hint(sKV + st * kStageBytes + (what >> 1) * kTileBytes + mine * page_bytes, what == 0 ? &k_map : &v_map, 0,
-                               (int32_t)(block << lp), &kv_full[st], policy);
-            } else {
-              uint8_t* const to = sScale + st * F::kScaleBytes;
-              if (what == 1)
-                bulk_load_hint(to + mine * (kKv4Blocks << lp), a.k_scales4 + (block << lp) * kKv4Blocks, kKv4Blocks << lp, &kv_full[st], policy);
-              else
-                bulk_load_hint(to + kTok * kKv4Blocks + mine * (2 << lp), a.v_scales4 + (block << lp), 2u << lp, &kv_full[st], policy);
-            }
-          }
-        } else {
-          // lanes 0 .. ppt - 1 load K, 16 .. 16 + ppt - 1 V
-          const int mine = lane & 15;
-          const int pg = __shfl_sync(0xffffffffu, page, (o + mine) & 31);
-          const bool load = mine < ppt && pg >= 0;
-          const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-          const uint32_t bad = __ballot_sync(0xffffffffu, mine < ppt && pg < 0) & 0xFFFFu;
-          if (load)
-            tma_load_2d_hint(sKV + st * kStageBytes + (lane >> 4) * kTileBytes + mine * page_bytes,
-                             lane < 16 ? &k_map : &v_map, 0, (pg * a.kv_heads + s.h) << lp, &kv_full[st], policy);
-          // the tile's arrival also stands for its scales
-          const float k1 = __shfl_sync(0xffffffffu, ks, (o + mine) & 31), v1 = __shfl_sync(0xffffffffu, vs, (o + mine) & 31);
-          if (lane < ppt) {
-            sks[st][lane] = k1;
-            svs[st][lane] = v1;
-          }
-          if (lane == 0) sbad[st] = bad;
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], loads * page_bytes);
+        // this tile's pages sit in lanes o .. o + ppt - 1; lanes 0 .. ppt - 1 load K, 16 .. 16 + ppt - 1 V
+        const int o = p0 & 31, mine = lane & 15;
+        const int pg = __shfl_sync(0xffffffffu, page, (o + mine) & 31);
+        const bool load = mine < ppt && pg >= 0;
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+        const uint32_t bad = __ballot_sync(0xffffffffu, mine < ppt && pg < 0) & 0xFFFFu;
+        if (load)
+          tma_load_2d_hint(sKV + st * kStageBytes + (lane >> 4) * kTileBytes + mine * page_bytes,
+                           lane < 16 ? &k_map : &v_map, 0, (pg * a.kv_heads + s.h) << lp, &kv_full[st], policy);
+        // the tile's arrival also stands for its scales
+        const float k1 = __shfl_sync(0xffffffffu, ks, (o + mine) & 31), v1 = __shfl_sync(0xffffffffu, vs, (o + mine) & 31);
+        if (lane < ppt) {
+          sks[st][lane] = k1;
+          svs[st][lane] = v1;
         }
+        if (lane == 0) sbad[st] = bad;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], loads * page_bytes);
       }
       u += s.n;
     }
@@ -394,8 +436,8 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
         if (ok && i >= kSBufs) ok = mbar_spin_warp(&s_empty[sb], (i / kSBufs - 1) & 1, err, kErrMmaTimeout);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k = d_k + (uint64_t)((st * kStageBytes) >> 4), q = d_q + (uint64_t)((qb * kQBytes) >> 4);
-        uint8_t* const raw = sScale + st * F::kScaleBytes;
+        const uint64_t k = d_k + (uint64_t)((st * F::kKStride) >> 4), q = d_q + (uint64_t)((qb * kQBytes) >> 4);
+        uint8_t* const raw = sScaleK + st * F::kKScales;
         if constexpr (k4) {
           // K's scales as tcgen05.cp takes them: those of keys l, l + 32, l + 64 and l + 96 in the l-th 16 bytes
           uint32_t w[4];
@@ -421,6 +463,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
             for (int kk = 0; kk < kKvDim / 32; ++kk) mma_ss_f8(tmem + F::kColsS * sb, k + 2 * kk, q + 2 * kk, id_qk, kk > 0);
           }
           mma_commit(&s_full[sb]);
+          if (k4) mma_commit(&kv_empty[st]);           // K and its scales have been read
           if (t + 1 == s.n) mma_commit(&q_empty[qb]);
         }
         __syncwarp();
@@ -434,7 +477,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
     const bool leader = elect_one();
     const uint32_t id_pv = idesc_e4m3(kKvDim, kN) | (1u << 15) | (1u << 16) | (k4 ? kFmtE2m1 << 7 : 0u);   // both operands MN-major
     constexpr SmemSwizzle kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
-    const uint64_t d_v = smem_desc(smem_u32(sKV + kTileBytes), 16, 1024, kSwizzle128B);
+    const uint64_t d_v = smem_desc(smem_u32(sKV + F::kVOffset), 16, 1024, kSwizzle128B);
     const uint64_t d_p = smem_desc(smem_u32(sP), 16, 8 * kN, kPSwizzle);
     int i = 0, seg = 0;
     bool ok = true;
@@ -444,11 +487,11 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       uint32_t fresh = (1u << kWgs) - 1;               // accumulators of the segment without a product yet
       if (seg >= 2) ok = mbar_wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
       for (int t = 0; t < s.n && ok; ++t, ++i) {
-        const int st = i % kStages, pb = (uint32_t)i % kWgs;
-        ok = mbar_spin_warp(&p_full[pb], ((uint32_t)i / kWgs) & 1, err, kErrMmaTimeout);
+        const int st = i % kVStages, pb = (uint32_t)i % kWgs, pn = (uint32_t)i % (kWgs * kPBufs);
+        ok = mbar_spin_warp(&p_full[pn], ((uint32_t)i / (kWgs * kPBufs)) & 1, err, kErrMmaTimeout);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t v = d_v + (uint64_t)((st * kStageBytes) >> 4), p = d_p + (uint64_t)((pb * kPBytes) >> 4);
+        const uint64_t v = d_v + (uint64_t)((st * F::kVStride) >> 4), p = d_p + (uint64_t)((pn * kPBytes) >> 4);
         const bool first = (fresh >> pb) & 1u;
         fresh &= ~(1u << pb);
         if (leader) {
@@ -456,7 +499,8 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
           for (int kk = 0; kk < kTok / 32; ++kk)
             mma_ss_f8(tmem + kColO + F::kOSeg * (seg & 1) + F::kColsO * pb, v + (uint64_t)((kk * 32 * kKvDim) >> 4),
                       p + (uint64_t)((kk * 32 * kN) >> 4), id_pv, !first || kk > 0);
-          mma_commit(&kv_empty[st]);                   // K, V and this tile's probabilities have been read
+          mma_commit(&v_empty[st]);                    // V (8 bits: K, too) and this tile's probabilities have been read
+          if (kPBufs > 1) mma_commit(&pv_done[pn]);
           if (t + 1 == s.n) mma_commit(&o_full[seg & 1]);
         }
         __syncwarp();
@@ -464,7 +508,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
     }
     if (leader) mma_commit(&mma_done);
     mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
-  } else {
+  } else if (warp == kQueryWarp) {
     // ---------------------------------------------------------------- queries
     int seg = 0;
     for (int64_t u = u0; u < u1; ++seg) {
@@ -578,11 +622,12 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       auto tile = [&](auto columns, auto with_masks, int i, int key0) {
         constexpr int kNC = decltype(columns)::value;
         constexpr bool kMasked = decltype(with_masks)::value;
-        const int st = i % kStages, sb = i % kSBufs, j = key0 + row, pg = row >> a.log2_page;
+        const int st = i % kVStages, sb = i % kSBufs, j = key0 + row, pg = row >> a.log2_page;
+        const int pn = kPBufs > 1 ? (int)((uint32_t)i % (kWgs * kPBufs)) : wg;
         const bool exists = !kMasked || (j < s.len && !((sbad[st] >> pg) & 1u));
         const float ks = k4 ? 1.f : sks[st][pg];
         float vs;
-        if constexpr (k4) vs = exists ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sScale + st * F::kScaleBytes + kTok * kKv4Blocks)[row]) : 0.f;
+        if constexpr (k4) vs = exists ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sScaleV + st * F::kVScales)[row]) : 0.f;
         else vs = svs[st][pg];
         const float vs_one = vs * kPOne;
         const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
@@ -706,7 +751,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
               }
             }
           }
-          float* const wmax_v = reinterpret_cast<float*>(sP + wg * kPBytes);   // [4][kCE], before the tile's P is there
+          float* const wmax_v = reinterpret_cast<float*>(sP + pn * kPBytes);   // [4][kCE], before the tile's P is there
           if (lane < kCE) {
             wmax[wg][quarter][lane] = mine;
             wmax_v[quarter * kCE + lane] = mine_v;
@@ -729,6 +774,8 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
             ref_e[lane] = mv_new == -INFINITY ? 1.f : ex2_approx(m_new - mv_new);
           }
           if (!fresh) {
+            if (kPBufs > 1)                            // the accumulator is settled when the tile before has been added
+              ok = mbar_wait_warp(&pv_done[(uint32_t)(i - kWgs) % (kWgs * kPBufs)], ((uint32_t)(i - kWgs) / (kWgs * kPBufs)) & 1, err, kErrMmaTimeout, kPolls) && ok;
 #pragma unroll
             for (int c = 0; c < kNC; ++c) l[c] *= __shfl_sync(0xffffffffu, al, c);
             tc_fence_after();
@@ -752,12 +799,15 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
           }
           group_sync(bar, 128);
         };
-        // the buffer is free, and the accumulator settled, once this warpgroup's previous product has completed
-        if (i >= kWgs) {
-          ok = mbar_wait_warp(&kv_empty[(i - kWgs) % kStages], ((i - kWgs) / kStages) & 1, err, kErrMmaTimeout, kPolls);
-          if (!ok) return;
+        if constexpr (kPBufs > 1) {
+          // the buffer is free once the tile that it held last has been added
+          if (i >= kWgs * kPBufs) ok = mbar_wait_warp(&pv_done[pn], ((uint32_t)i / (kWgs * kPBufs) - 1) & 1, err, kErrMmaTimeout, kPolls);
+        } else {
+          // the buffer is free, and the accumulator settled, once this warpgroup's previous product has completed
+          if (i >= kWgs) ok = mbar_wait_warp(&kv_empty[(i - kWgs) % kStages], ((i - kWgs) / kStages) & 1, err, kErrMmaTimeout, kPolls);
         }
-        uint8_t* prow = sP + wg * kPBytes + row * kN;
+        if (!ok) return;
+        uint8_t* prow = sP + pn * kPBytes + row * kN;
         const int sw = kN == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
         float z[kNC];                                  // scores, then probabilities
         bool raised = fresh;
@@ -803,17 +853,17 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kNC; ++c) l[c] += z[c];
         fresh = false;
-        if (row == 0) mbar_arrive(&p_full[wg]);
+        if (row == 0) mbar_arrive(&p_full[pn]);
         if (lane == 0) mbar_arrive(&s_empty[sb]);
       };
       for (int t = (uint32_t)(wg + kWgs - (uint32_t)i0 % kWgs) % kWgs; t < s.n && ok; t += kWgs) {
         const int i = i0 + t, key0 = s.template tile_at<kMods>(t) * kTok;
-        ok = mbar_wait_warp(&kv_full[i % kStages], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
+        ok = mbar_wait_warp(&v_full[i % kVStages], (i / kVStages) & 1, err, kErrTmaTimeout, kPolls) &&
              mbar_wait_warp(&s_full[i % kSBufs], (i / kSBufs) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         tc_fence_after();
         using std::integral_constant;
-        const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[i % kStages] != 0);
+        const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[i % kVStages] != 0);
         if constexpr (kCE > 16) {
           if (live > 16) {
             if (masked) tile(integral_constant<int, 32>{}, std::true_type{}, i, key0);
