@@ -1,5 +1,4 @@
-// Dense grouped-head attention over the paged 8-bit or 4-bit K/V cache, on tcgen05 tensor cores.  (Compiled here for the 8-bit
-// cache; kv4_attention.cu compiles the same kernel for the 4-bit one, beside it.)
+// Dense grouped-head attention over the paged 8-bit K/V cache, on tcgen05 tensor cores.
 //
 //   z_s = scale * q[r,h] . (k_code_s * ks)        [then the cap and the distance bias]
 //   out[r,h] = sum_s softmax(z)_s * (v_code_s * vs),   lse[r,h] = ln sum_s exp(z_s)
@@ -51,51 +50,27 @@ using namespace sm100;
 
 namespace pa {
 constexpr int kTok = kPaTok;                    // keys per tile
-constexpr int kTileBytes = kTok * kKvDim;       // 16 KB: codes of 8 bits, or of 4 bits in 16-byte units that are half used
+constexpr int kTileBytes = kTok * kKvDim;       // 16 KB of codes
 constexpr int kStageBytes = 2 * kTileBytes;     // K, then V
+constexpr int kStages = 5;
 constexpr int kColMax = kPagedAttnColumns;
+constexpr int kQBytes = 2 * kColMax * kKvDim;   // hi and lo rows of 32 columns
+constexpr int kPBytes = kTok * 2 * kColMax;
 constexpr int kMaxPages = kTok / kKvMinPage;    // pages of a tile
-constexpr int kScoreWarp = 1, kQueryWarp = 2, kOutWarp = 3, kLoadVWarp = 4;
-constexpr int kQBufs = 3;                       // the scores run two tiles a warpgroup, so up to two segments, ahead of the outputs
-constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr int kThreads = 384;
+constexpr int kScoreWarp = 1, kOutWarp = 3, kSoftWarp0 = 4;
+constexpr uint32_t kRegsLow = 88, kRegsSoft = 208;   // 88 + 2 * 208 = 3 * 168, the launch's
+constexpr int kQBufs = 3;                       // the scores run two tiles, so up to two segments, ahead of the outputs
+constexpr uint32_t kTmemCols = 512;             // S^T of tile i at 64 (i % 4), O^T at 256 + 128 (segment % 2) + 64 warpgroup
+constexpr uint32_t kColO = 256;
+constexpr int kSBufs = 4;                       // two a warpgroup: one is kept until its tile is known to be done
 constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
 constexpr uint32_t kPolls = 1u << 18;           // of 3.8 us each or more: a second
 // The query warp runs up to kQBufs segments ahead and then waits for a whole one to end: 57 ms for 2^22 tokens and 32
 // columns, 15 s for 2^30.
 constexpr uint32_t kSegPolls = 1u << 24;
-
-// What depends on the cache's format and on the columns.
-// TMEM, 8 bits: S^T of tile i (hi and lo columns) at 64 (i % 4), O^T at 256 + 128 (segment % 2) + 64 warpgroup.
-// 4 bits: S^T at kHalf (i % kSBufs), K's block scales of that tile at 192 + 4 (i % kSBufs), the queries' at 216, O^T at
-// 256 + kOSeg (segment % 2) + kN warpgroup.
-template <bool k4, int kCE>
-struct Form {
-  static constexpr int kHalf = kCE < 16 ? 16 : kCE;   // columns of the hi half (and of the lo half)
-  static constexpr int kN = 2 * kHalf;                // 32 or 64
-  static constexpr int kWgs = 2;                      // softmax warpgroups
-  static constexpr int kSoftWarp0 = k4 ? 8 : 4;       // warps before them: 4 bits take a second loader
-  static constexpr int kThreads = 32 * kSoftWarp0 + 128 * kWgs;
-  // 88 + 2 * 208 = 3 * 168, 2 * 64 + 2 * 192 = 4 * 128: the launch's
-  static constexpr uint32_t kRegsLow = k4 ? 64 : 88, kRegsSoft = k4 ? 192 : 208;
-  // 8 bits: one ring of stages (K, then V).  4 bits: a ring each, as K is done with after the scores' products.
-  static constexpr int kStages = k4 && kCE > 16 ? 4 : 5, kVStages = 5;
-  static constexpr int kKStride = k4 ? kTileBytes : kStageBytes, kVStride = kKStride;
-  static constexpr int kVOffset = k4 ? kStages * kTileBytes : kTileBytes;
-  static constexpr int kTilesBytes = k4 ? (kStages + kVStages) * kTileBytes : kStages * kStageBytes;
-  static constexpr int kPBufs = k4 ? 2 : 1;           // probabilities' buffers a warpgroup
-  static constexpr int kSBufs = 2 * kWgs;             // two a warpgroup: one is kept until its tile is known to be done
-  static constexpr int kColsS = k4 ? kHalf : 64;      // TMEM columns of a tile's scores
-  static constexpr int kColScales = 192, kColQScales = 216;
-  static constexpr int kColsO = k4 ? kN : 64, kOSeg = kWgs * kColsO;
-  static constexpr int kQBytes = (k4 ? kN : 2 * kColMax) * kKvDim;   // hi and lo rows of the columns
-  static constexpr int kPBytes = kTok * (k4 ? kN : 2 * kColMax);
-  static constexpr int kKScales = k4 ? kTok * kKv4Blocks : 0, kVScales = k4 ? kTok * 2 : 0;   // bytes of a tile's scales
-  static constexpr int kScaleBytes = kStages * kKScales + kVStages * kVScales;
-  static constexpr int kFixedSmem = kTilesBytes + kQBufs * kQBytes + kWgs * kPBufs * kPBytes + kScaleBytes + 1024;
-  static_assert(!k4 || (kSBufs * kHalf <= kColScales && kColScales + 4 * kSBufs <= kColQScales), "TMEM columns");
-  static_assert(kColO + 2 * kOSeg <= (int)kTmemCols, "TMEM columns");
-};
+constexpr int kFixedSmem = kStages * kStageBytes + kQBufs * kQBytes + 2 * kPBytes + 1024;
 }  // namespace pa
 
 // A run of tiles of one segment
@@ -137,17 +112,6 @@ __device__ __forceinline__ PaSeg pa_segment(const PagedAttnArgs& a, const int32_
   return s;
 }
 
-__device__ __forceinline__ void tmem_ld_cols8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // two e4m3 codes of (a, b), and of 16 times what they leave
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -156,47 +120,32 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = __nv_cvt_float2_to_fp8x2(make_float2(16.f * (a - back.x), 16.f * (b - back.y)), __NV_SATFINITE, __NV_E4M3);
 }
 
-// What the query warp leaves about a segment's columns
-struct PaColumns {
-  float factor[pa::kColMax];    // 2^k of the split query * softmax scale * log2 e
-  int limit[pa::kColMax];       // keys below it are seen
-  float row[pa::kColMax];       // of the request: its position is start + row
-  float slope[pa::kColMax];     // * log2 e
-  int at[pa::kColMax];          // row * query heads + head
-  int min_limit;                // over the columns
-  int start;                    // position of the request's first row
-};
-
-// k4: a 4-bit cache; kCE columns (8, 16 or 32); kModSet: score cap and distance bias compiled in
-template <bool k4, int kCE, PaMods kModSet>
-__global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
+// kCE columns (8, 16 or 32); kModSet: score cap and distance bias compiled in
+template <int kCE, PaMods kModSet>
+__global__ void __launch_bounds__(pa::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                            const __grid_constant__ PagedAttnArgs a, int shared_keys) {
   using namespace pa;
-  using F = Form<k4, kCE>;
   constexpr bool kMods = kModSet != kPaPlain;
-  constexpr int kHalf = F::kHalf, kN = F::kN, kStages = F::kStages, kSBufs = F::kSBufs, kWgs = F::kWgs, kThreads = F::kThreads;
-  constexpr int kVStages = F::kVStages, kSoftWarp0 = F::kSoftWarp0;
-  constexpr int kQBytes = F::kQBytes, kPBytes = F::kPBytes, kPBufs = F::kPBufs;
+  constexpr int kHalf = kCE < 16 ? 16 : kCE;          // columns of the hi half (and of the lo half)
+  constexpr int kN = 2 * kHalf;                       // MMA N: 32 or 64
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
-  uint8_t* sQ = sKV + F::kTilesBytes;
+  uint8_t* sQ = sKV + kStages * kStageBytes;
   uint8_t* sP = sQ + kQBufs * kQBytes;
-  uint8_t* sScaleK = sP + kWgs * kPBufs * kPBytes;               // 4 bits: [stages] of K's scales, then V's
-  uint8_t* sScaleV = sScaleK + kStages * F::kKScales;
-  int32_t* end = reinterpret_cast<int32_t*>(sScaleK + F::kScaleBytes);   // [requests]
+  int32_t* end = reinterpret_cast<int32_t*>(sP + 2 * kPBytes);   // [requests]
 
-  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], v_ring[2 * kVStages], s_full[kSBufs], s_empty[kSBufs], p_full[kWgs * kPBufs], pv_done[kWgs * kPBufs];
+  __shared__ uint64_t kv_full[kStages], kv_empty[kStages], s_full[kSBufs], s_empty[kSBufs], p_full[2];
   __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[2], o_empty[2], mma_done;
-  __shared__ float sks[k4 ? 1 : kStages][kMaxPages], svs[k4 ? 1 : kStages][kMaxPages];
-  __shared__ uint32_t sbad[kVStages];
+  __shared__ float sks[kStages][kMaxPages], svs[kStages][kMaxPages];
+  __shared__ uint32_t sbad[kStages];
   __shared__ __align__(16) PaColumns cols[kQBufs];
-  __shared__ __align__(16) float refs[kWgs][2][kCE];
-  __shared__ float wmax[kWgs][4][kCE], fin[kWgs][kWgs][kCE];
-  __shared__ float stat[kQBufs][kWgs][3][kCE];         // each warpgroup's m, mv and l of a segment
-  __shared__ uint32_t stat_nan[k4 ? 1 : kQBufs][kWgs][k4 ? 1 : kKvDim];
-  __shared__ uint32_t nan_keys[k4 ? 1 : kWgs][4];
+  __shared__ __align__(16) float refs[2][2][kCE];
+  __shared__ float wmax[2][4][kCE], fin[2][2][kCE];
+  __shared__ float stat[kQBufs][2][3][kCE];            // each warpgroup's m, mv and l of a segment
+  __shared__ uint32_t stat_nan[kQBufs][2][kKvDim];
+  __shared__ uint32_t nan_keys[2][4];
   __shared__ int32_t scan[kThreads / 32];
   __shared__ uint32_t tmem_base, bits_all;
 
@@ -207,13 +156,8 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
-    if (k4)
-      for (int i = 0; i < 2 * kVStages; ++i) mbar_init(&v_ring[i], 1);
-    for (int i = 0; i < kWgs * kPBufs; ++i) {
-      mbar_init(&p_full[i], 1);
-      mbar_init(&pv_done[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&p_full[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 4);
     }
@@ -223,8 +167,8 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
     }
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1 + 4 * kWgs);   // the last product that reads it, and the softmax warps
-      mbar_init(&stat_full[i], 4 * kWgs);
+      mbar_init(&q_empty[i], 9);          // the last product that reads it, and eight softmax warps
+      mbar_init(&stat_full[i], 8);
     }
     mbar_init(&mma_done, 2);
     bits_all = 0;
@@ -271,19 +215,6 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  if constexpr (k4) {
-    // the queries' block scales: 1 for the hi terms (byte 0 of a column), 2^-4 for the lo ones (byte 1), for every column
-    if (warp < 4) {
-      const uint32_t word = 0x7B7Fu;
-      asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tmem + F::kColQScales + ((uint32_t)(32 * warp) << 16)),
-                   "r"(word)
-                   : "memory");
-      tmem_wait_st();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-  }
   const int64_t units = (int64_t)end[a.num_requests - 1] * a.kv_heads;
   int64_t u0 = pa_unit_start(cta, units, ctas);
   const int64_t u1 = pa_unit_start(cta + 1, units, ctas);
@@ -294,66 +225,10 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
     if (s.tile > 0) u0 += s.n;
   }
   uint32_t* const err = &bits_all;                    // this CTA's status bits, stored at the end
-  uint64_t* const v_full = k4 ? v_ring : kv_full;     // 4 bits: kv_full and kv_empty are K's
-  uint64_t* const v_empty = k4 ? v_ring + kVStages : kv_empty;
 
   if (warp < kSoftWarp0) {
-  regs_dec<F::kRegsLow>();
-  // 4 bits: a warp loads K (codes and scales) or V.  A load of 4-bit codes counts 64 bytes a row on the barrier: the other half
-  // of each 16-byte unit is not written.
-  auto load4 = [&](auto of_v, const CUtensorMap* map, const uint8_t* scales, uint64_t* full, uint64_t* empty, uint8_t* tiles, uint8_t* to) {
-    constexpr bool kV = decltype(of_v)::value;
-    constexpr int kRing = kV ? kVStages : kStages, kScale = kV ? 2 : kKv4Blocks;   // scale bytes of a token
-    const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
-    const int lp = a.log2_page, ppt = kTok >> lp, mine = lane & 7;
-    const bool codes = lane < 8, used = mine < ppt && lane < 16;   // lanes 0 .. ppt - 1 load codes, 8 .. scales
-    uint8_t* const dst = codes ? tiles + mine * (kKvDim << lp) : to + mine * (kScale << lp);
-    int i = 0;
-    bool ok = true;
-    for (int64_t u = u0; u < u1 && ok;) {
-      const PaSeg s = pa_segment(a, end, u, cut);
-      const int pages = (s.len + (1 << lp) - 1) >> lp;
-      int batch = -1, first = -1;                      // 32 pages at a time, one a lane: the first row of its block
-      for (int t = 0; t < s.n && ok; ++t, ++i) {
-        const int p0 = s.template tile_at<kMods>(t) * ppt;
-        if ((p0 >> 5) != batch) {
-          batch = p0 >> 5;
-          const int p = 32 * batch + lane;
-          first = -1;
-          if (p < pages) {
-            const int page = a.block_table[(int64_t)s.b * a.table_stride + p];
-            if (page >= 0 && page < a.num_pages) first = (page * a.kv_heads + s.h) << lp;
-            else atomicOr(err, kErrBadPage);
-          }
-        }
-        const int st = i % kRing, use = i / kRing;
-        if (use > 0 && !mbar_wait_warp(&empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) {
-          ok = false;
-          break;
-        }
-        const int row = __shfl_sync(0xffffffffu, first, (p0 + mine) & 31);
-        const uint32_t bad = __ballot_sync(0xffffffffu, codes && used && row < 0);
-        if (lane == 0) {
-          if (kV) sbad[st] = bad;
-          mbar_arrive_expect_tx(&full[st], (uint32_t)(ppt - __popc(bad)) * ((uint32_t)(kKvDim / 2 + kScale) << lp));
-        }
-        __syncwarp();
-        if (used && row >= 0) {
-          if (codes) tma_load_2d_hint(dst + st * kTileBytes, map, 0, row, &full[st], policy);
-          else bulk_load_hint(dst + st * (kTok * kScale), scales + (int64_t)row * kScale, kScale << lp, &full[st], policy);
-        }
-      }
-      u += s.n;
-    }
-    // nothing may still be landing in shared memory when the CTA exits
-    for (int st = 0; st < kRing; ++st)
-      if (i > st) mbar_wait_warp(&full[st], ((i - st + kRing - 1) / kRing - 1) & 1, err, kErrTmaTimeout, kPolls);
-  };
-  if (k4 && warp == 0) {
-    load4(std::false_type{}, &k_map, a.k_scales4, kv_full, kv_empty, sKV, sScaleK);
-  } else if (k4 && warp == kLoadVWarp) {
-    load4(std::true_type{}, &v_map, reinterpret_cast<const uint8_t*>(a.v_scales4), v_full, v_empty, sKV + F::kVOffset, sScaleV);
-  } else if (!k4 && warp == 0) {
+  regs_dec<kRegsLow>();
+  if (warp == 0) {
     // ---------------------------------------------------------------- producer
     const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
     const int lp = a.log2_page, ppt = kTok >> lp;
@@ -420,7 +295,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
     // The warp walks together and one elected lane issues: addresses stay in uniform registers.  With
     // the walk itself inside a one-lane branch, issuing a tile's products took twice as long.
     const bool leader = elect_one();
-    const uint32_t id_qk = k4 ? idesc_mx(kTok, kHalf, kFmtE2m1, kFmtE4m3) : idesc_e4m3(kTok, kN);
+    const uint32_t id_qk = idesc_e4m3(kTok, kN);
     const uint64_t d_k = smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
     const uint64_t d_q = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
     int i = 0, seg = 0;
@@ -436,34 +311,11 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
         if (ok && i >= kSBufs) ok = mbar_spin_warp(&s_empty[sb], (i / kSBufs - 1) & 1, err, kErrMmaTimeout);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k = d_k + (uint64_t)((st * F::kKStride) >> 4), q = d_q + (uint64_t)((qb * kQBytes) >> 4);
-        uint8_t* const raw = sScaleK + st * F::kKScales;
-        if constexpr (k4) {
-          // K's scales as tcgen05.cp takes them: those of keys l, l + 32, l + 64 and l + 96 in the l-th 16 bytes
-          uint32_t w[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) w[c] = reinterpret_cast<const uint32_t*>(raw)[32 * c + lane];
-          __syncwarp();
-          reinterpret_cast<uint4*>(raw)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+        const uint64_t k = d_k + (uint64_t)((st * kStageBytes) >> 4), q = d_q + (uint64_t)((qb * kQBytes) >> 4);
         if (leader) {
-          if constexpr (k4) {
-            const uint32_t sf = tmem + F::kColScales + 4 * sb;
-            tmem_cp_scales(sf, smem_desc(smem_u32(raw), 16, 128, kSwizzleNone));
 #pragma unroll
-            for (int kk = 0; kk < 2 * kKvDim / 32; ++kk) {     // hi, then lo
-              const uint32_t block = kk & 3, term = kk >> 2;
-              mma_ss_mx(tmem + F::kColsS * sb, k + 2 * block, q + 2 * block + (uint64_t)((term * kHalf * kKvDim) >> 4),
-                        id_qk | block << 29 | term << 4, sf, tmem + F::kColQScales, kk > 0);
-            }
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < kKvDim / 32; ++kk) mma_ss_f8(tmem + F::kColsS * sb, k + 2 * kk, q + 2 * kk, id_qk, kk > 0);
-          }
+          for (int kk = 0; kk < kKvDim / 32; ++kk) mma_ss_f8(tmem + 64 * sb, k + 2 * kk, q + 2 * kk, id_qk, kk > 0);
           mma_commit(&s_full[sb]);
-          if (k4) mma_commit(&kv_empty[st]);           // K and its scales have been read
           if (t + 1 == s.n) mma_commit(&q_empty[qb]);
         }
         __syncwarp();
@@ -475,32 +327,31 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
   } else if (warp == kOutWarp) {
     // ---------------------------------------------------------------- products of the outputs
     const bool leader = elect_one();
-    const uint32_t id_pv = idesc_e4m3(kKvDim, kN) | (1u << 15) | (1u << 16) | (k4 ? kFmtE2m1 << 7 : 0u);   // both operands MN-major
+    const uint32_t id_pv = idesc_e4m3(kKvDim, kN) | (1u << 15) | (1u << 16);   // both operands MN-major
     constexpr SmemSwizzle kPSwizzle = kN == 64 ? kSwizzle64B : kSwizzle32B;
-    const uint64_t d_v = smem_desc(smem_u32(sKV + F::kVOffset), 16, 1024, kSwizzle128B);
+    const uint64_t d_v = smem_desc(smem_u32(sKV + kTileBytes), 16, 1024, kSwizzle128B);
     const uint64_t d_p = smem_desc(smem_u32(sP), 16, 8 * kN, kPSwizzle);
     int i = 0, seg = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
       const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
-      uint32_t fresh = (1u << kWgs) - 1;               // accumulators of the segment without a product yet
+      uint32_t fresh = 3;                              // accumulators of the segment without a product yet
       if (seg >= 2) ok = mbar_wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout, kPolls);
       for (int t = 0; t < s.n && ok; ++t, ++i) {
-        const int st = i % kVStages, pb = (uint32_t)i % kWgs, pn = (uint32_t)i % (kWgs * kPBufs);
-        ok = mbar_spin_warp(&p_full[pn], ((uint32_t)i / (kWgs * kPBufs)) & 1, err, kErrMmaTimeout);
+        const int st = i % kStages, pb = i & 1;
+        ok = mbar_spin_warp(&p_full[pb], (i >> 1) & 1, err, kErrMmaTimeout);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t v = d_v + (uint64_t)((st * F::kVStride) >> 4), p = d_p + (uint64_t)((pn * kPBytes) >> 4);
+        const uint64_t v = d_v + (uint64_t)((st * kStageBytes) >> 4), p = d_p + (uint64_t)((pb * kPBytes) >> 4);
         const bool first = (fresh >> pb) & 1u;
         fresh &= ~(1u << pb);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < kTok / 32; ++kk)
-            mma_ss_f8(tmem + kColO + F::kOSeg * (seg & 1) + F::kColsO * pb, v + (uint64_t)((kk * 32 * kKvDim) >> 4),
+            mma_ss_f8(tmem + kColO + 128 * (seg & 1) + 64 * pb, v + (uint64_t)((kk * 32 * kKvDim) >> 4),
                       p + (uint64_t)((kk * 32 * kN) >> 4), id_pv, !first || kk > 0);
-          mma_commit(&v_empty[st]);                    // V (8 bits: K, too) and this tile's probabilities have been read
-          if (kPBufs > 1) mma_commit(&pv_done[pn]);
+          mma_commit(&kv_empty[st]);                   // K, V and this tile's probabilities have been read
           if (t + 1 == s.n) mma_commit(&o_full[seg & 1]);
         }
         __syncwarp();
@@ -508,91 +359,24 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
     }
     if (leader) mma_commit(&mma_done);
     mbar_wait_warp(&mma_done, 0, err, kErrMmaTimeout, kPolls);
-  } else if (warp == kQueryWarp) {
+  } else {
     // ---------------------------------------------------------------- queries
     int seg = 0;
     for (int64_t u = u0; u < u1; ++seg) {
       const PaSeg s = pa_segment(a, end, u, cut);
       u += s.n;
       const int buf = seg % kQBufs;
-      // first what a lane knows of a column of its own.  A column without a pair scores NaN whatever an earlier segment or
-      // kernel left of it in shared memory: NaN is no maximum, so it moves no references, and nobody takes its output.
-      const int live = min(s.rows * a.group - s.cg * kCE, kCE);
-      const int n = s.cg * kCE + min(lane, live - 1), i = n / a.group, head = s.h * a.group + (n - i * a.group);
-      const int64_t from = (int64_t)(s.row0 + i) * a.q_stride + (int64_t)head * kKvDim;
-      const int start = a.seq_lens[s.b] - s.rows;      // position of row 0
-      const int prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
-      const float slope = kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f;
-      if (seg >= kQBufs && !mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kSegPolls)) break;
-      uint8_t* q_hi = sQ + buf * kQBytes;
-      PaColumns& cm = cols[buf];
-      // then the values, 16 lanes a column: eight columns a step, the next eight on their way; a rolled loop, as code that a
-      // CTA runs once or twice costs its way from L2
-      const int part = lane & 15, half = lane >> 4;
-      auto load = [&](int c) {
-        const int64_t at = __shfl_sync(0xffffffffu, from, c & 31);
-        return c < live ? *reinterpret_cast<const uint4*>(a.q + at + 8 * part) : make_uint4(0, 0, 0, 0);
-      };
-      uint4 x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = load(2 * k + half);
-      const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
-      if (lane < live) {
-        cm.limit[lane] = limit;
-        cm.row[lane] = (float)i;
-        cm.at[lane] = (s.row0 + i) * a.kv_heads * a.group + head;
-        cm.slope[lane] = slope;
-      } else if (lane < kCE) {
-        cm.factor[lane] = __int_as_float(0x7FC00000);
-      }
-      int low = limit;                                 // (lanes without a column hold the last one's)
-#pragma unroll 1
-      for (int c0 = 0; c0 < live; c0 += 8) {
-        uint4 y[4];
-        uint32_t tops[4];                              // the largest |x| of each column as bf16 bits, side by side
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y[k] = x[k];
-          const uint32_t m = __vmaxu2(__vmaxu2(y[k].x & 0x7FFF7FFFu, y[k].y & 0x7FFF7FFFu), __vmaxu2(y[k].z & 0x7FFF7FFFu, y[k].w & 0x7FFF7FFFu));
-          tops[k] = max(m & 0xFFFFu, m >> 16);
-        }
-        if (c0 + 8 < live) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = load(c0 + 8 + 2 * k + half);
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tops[k] = max(tops[k], __shfl_xor_sync(0xffffffffu, tops[k], o));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c = c0 + 2 * k + half;
-          const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w}, top = tops[k];
-          const int E = pa_exponent(top);
-          const __nv_bfloat162 up = pa_up(E);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pa_split<16>(w[e], up, hi[e], lo[e]);
-          if (c < live) {
-            const uint32_t at = (((part >> 1) ^ (c & 7)) << 4) + 8 * (part & 1);
-            *reinterpret_cast<uint2*>(q_hi + c * kKvDim + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2*>(q_hi + (kHalf + c) * kKvDim + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            if (part == 0) cm.factor[c] = pa_factor(top, E, a.scale_log2);
-          }
-        }
-      }
-      low = __reduce_min_sync(0xffffffffu, low);
-      if (lane == 0) {
-        cm.min_limit = low;
-        cm.start = start;
-      }
+      if (!pa_query_columns<kCE, kHalf, kMods>(a, s, sQ + buf * kQBytes, cols[buf], [&] {
+            return seg < kQBufs || mbar_wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kSegPolls);
+          }))
+        break;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[buf]);
     }
   }
   } else {
-    regs_inc<F::kRegsSoft>();
+    regs_inc<kRegsSoft>();
     // ---------------------------------------------------------------- softmax and outputs: one key a thread
     const int wg = (warp - kSoftWarp0) >> 2, bar = 1 + wg;
     const int quarter = warp & 3, row = 32 * quarter + lane;
@@ -603,7 +387,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       u += s.n;
       const int qb = seg % kQBufs;
       if (!mbar_wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout, kPolls)) break;
-      const uint32_t acc = tmem + lanes + kColO + F::kOSeg * (seg & 1);
+      const uint32_t acc = tmem + lanes + kColO + 128 * (seg & 1);
       const PaColumns& cm = cols[qb];
       const int min_limit = cm.min_limit;
       const int live = min(s.rows * a.group - s.cg * kCE, kCE);   // columns in use
@@ -622,20 +406,14 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       auto tile = [&](auto columns, auto with_masks, int i, int key0) {
         constexpr int kNC = decltype(columns)::value;
         constexpr bool kMasked = decltype(with_masks)::value;
-        const int st = i % kVStages, sb = i % kSBufs, j = key0 + row, pg = row >> a.log2_page;
-        const int pn = kPBufs > 1 ? (int)((uint32_t)i % (kWgs * kPBufs)) : wg;
+        const int st = i % kStages, sb = i % kSBufs, j = key0 + row, pg = row >> a.log2_page;
+        const float ks = sks[st][pg], vs = svs[st][pg], vs_one = vs * kPOne;
         const bool exists = !kMasked || (j < s.len && !((sbad[st] >> pg) & 1u));
-        const float ks = k4 ? 1.f : sks[st][pg];
-        float vs;
-        if constexpr (k4) vs = exists ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sScaleV + st * F::kVScales)[row]) : 0.f;
-        else vs = svs[st][pg];
-        const float vs_one = vs * kPOne;
         const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
         // Distances are taken from the request's first row in integers: they, and the small row numbers, are exact in fp32
         // however far from 0 the positions are, up to 2^24 tokens away, and rounded like any fp32 value beyond.
         const float ahead = kMods ? (float)(j - cm.start) : 0.f;
-        // (4-bit codes are finite whatever the bits: a probability of 0 is enough)
-        if constexpr (kMasked && !k4) {
+        if (kMasked) {
           // A key's values meet a probability of 0 where it is not seen, and 0 * NaN is NaN: what lies behind
           // the request's tokens is zeroed here, and NaN codes of keys that only some columns see are taken out.
           uint4* vrow = reinterpret_cast<uint4*>(sKV + st * kStageBytes + kTileBytes + row * kKvDim);
@@ -680,8 +458,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
         auto finish = [&](auto& z, const uint32_t* hi, const uint32_t* lo, int c0, int c1) {
           // a loop each: a choice made inside one of them would leave the values no instructions to overlap with
 #pragma unroll
-          for (int c = 0; c < c1; ++c)
-            z[c] = k4 ? __uint_as_float(hi[c]) * cm.factor[c0 + c] : fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
+          for (int c = 0; c < c1; ++c) z[c] = fmaf(__uint_as_float(lo[c]), 0.0625f, __uint_as_float(hi[c])) * (ks * cm.factor[c0 + c]);
           if (kMods && in != 0.f) {
 #pragma unroll
             for (int c = 0; c < c1; ++c) z[c] = capped<kModSet>(z[c] * in, a.cap_log2);
@@ -698,8 +475,8 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
         };
         auto scores8 = [&](float (&z)[8], int c0) {
           uint32_t hi[8], lo[8];
-          tmem_ld_cols8(tmem + lanes + F::kColsS * sb + c0, hi);
-          if (!k4) tmem_ld_cols8(tmem + lanes + F::kColsS * sb + kHalf + c0, lo);
+          tmem_ld_cols8(tmem + lanes + 64 * sb + c0, hi);
+          tmem_ld_cols8(tmem + lanes + 64 * sb + kHalf + c0, lo);
           tmem_wait_ld();
           finish(z, hi, lo, c0, 8);
         };
@@ -710,8 +487,8 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
             uint32_t hi[kC], lo[kC];
 #pragma unroll
             for (int c = 0; c < kC; c += 8) {
-              tmem_ld_cols8(tmem + lanes + F::kColsS * sb + c0 + c, hi + c);
-              if (!k4) tmem_ld_cols8(tmem + lanes + F::kColsS * sb + kHalf + c0 + c, lo + c);
+              tmem_ld_cols8(tmem + lanes + 64 * sb + c0 + c, hi + c);
+              tmem_ld_cols8(tmem + lanes + 64 * sb + kHalf + c0 + c, lo + c);
             }
             tmem_wait_ld();
             float y[kC];
@@ -739,7 +516,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
           // A warp's 32 keys have one scale, but for pages of 16: there the maximum of z + lv may be another key's.  (A loop
           // of its own: inside the first one it took the verify case, whose pages are larger, 341 us instead of 334.)
           float mine_v = mine + lv;
-          if (k4 || a.log2_page == 4) {                // (4 bits: every key has a scale of its own)
+          if (a.log2_page == 4) {
 #pragma unroll 1
             for (int c0 = 0; c0 < kNC; c0 += 8) {
               float z[8];
@@ -751,7 +528,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
               }
             }
           }
-          float* const wmax_v = reinterpret_cast<float*>(sP + pn * kPBytes);   // [4][kCE], before the tile's P is there
+          float* const wmax_v = reinterpret_cast<float*>(sP + wg * kPBytes);   // [4][kCE], before the tile's P is there
           if (lane < kCE) {
             wmax[wg][quarter][lane] = mine;
             wmax_v[quarter * kCE + lane] = mine_v;
@@ -774,12 +551,10 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
             ref_e[lane] = mv_new == -INFINITY ? 1.f : ex2_approx(m_new - mv_new);
           }
           if (!fresh) {
-            if (kPBufs > 1)                            // the accumulator is settled when the tile before has been added
-              ok = mbar_wait_warp(&pv_done[(uint32_t)(i - kWgs) % (kWgs * kPBufs)], ((uint32_t)(i - kWgs) / (kWgs * kPBufs)) & 1, err, kErrMmaTimeout, kPolls) && ok;
 #pragma unroll
             for (int c = 0; c < kNC; ++c) l[c] *= __shfl_sync(0xffffffffu, al, c);
             tc_fence_after();
-            const uint32_t o = acc + F::kColsO * wg;
+            const uint32_t o = acc + 64 * wg;
 #pragma unroll 1
             for (int c0 = 0; c0 < kNC; c0 += 8) {
               uint32_t r[16];
@@ -799,15 +574,12 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
           }
           group_sync(bar, 128);
         };
-        if constexpr (kPBufs > 1) {
-          // the buffer is free once the tile that it held last has been added
-          if (i >= kWgs * kPBufs) ok = mbar_wait_warp(&pv_done[pn], ((uint32_t)i / (kWgs * kPBufs) - 1) & 1, err, kErrMmaTimeout, kPolls);
-        } else {
-          // the buffer is free, and the accumulator settled, once this warpgroup's previous product has completed
-          if (i >= kWgs) ok = mbar_wait_warp(&kv_empty[(i - kWgs) % kStages], ((i - kWgs) / kStages) & 1, err, kErrMmaTimeout, kPolls);
+        // the buffer is free, and the accumulator settled, once this warpgroup's previous product has completed
+        if (i >= 2) {
+          ok = mbar_wait_warp(&kv_empty[(i - 2) % kStages], ((i - 2) / kStages) & 1, err, kErrMmaTimeout, kPolls);
+          if (!ok) return;
         }
-        if (!ok) return;
-        uint8_t* prow = sP + pn * kPBytes + row * kN;
+        uint8_t* prow = sP + wg * kPBytes + row * kN;
         const int sw = kN == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
         float z[kNC];                                  // scores, then probabilities
         bool raised = fresh;
@@ -827,8 +599,7 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               z[c + q] = ex2_approx(z[c + q] - mm[q]);
-              x[q] = (z[c + q] * ee[q]) * vs_one;     // in this order: 0 stays 0 whatever the scale of an unseen key ..
-              if (k4 && kMasked && j >= cm.limit[c + q]) x[q] = 0.f;   // .. and of 4 bits even NaN
+              x[q] = (z[c + q] * ee[q]) * vs_one;     // in this order: 0 stays 0 whatever the scale of an unseen key
               p_top = fmaxf(p_top, z[c + q]);
               x_top = fmaxf(x_top, x[q]);
             }
@@ -853,17 +624,17 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kNC; ++c) l[c] += z[c];
         fresh = false;
-        if (row == 0) mbar_arrive(&p_full[pn]);
+        if (row == 0) mbar_arrive(&p_full[wg]);
         if (lane == 0) mbar_arrive(&s_empty[sb]);
       };
-      for (int t = (uint32_t)(wg + kWgs - (uint32_t)i0 % kWgs) % kWgs; t < s.n && ok; t += kWgs) {
+      for (int t = (i0 + wg) & 1; t < s.n && ok; t += 2) {
         const int i = i0 + t, key0 = s.template tile_at<kMods>(t) * kTok;
-        ok = mbar_wait_warp(&v_full[i % kVStages], (i / kVStages) & 1, err, kErrTmaTimeout, kPolls) &&
+        ok = mbar_wait_warp(&kv_full[i % kStages], (i / kStages) & 1, err, kErrTmaTimeout, kPolls) &&
              mbar_wait_warp(&s_full[i % kSBufs], (i / kSBufs) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
         tc_fence_after();
         using std::integral_constant;
-        const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[i % kVStages] != 0);
+        const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[i % kStages] != 0);
         if constexpr (kCE > 16) {
           if (live > 16) {
             if (masked) tile(integral_constant<int, 32>{}, std::true_type{}, i, key0);
@@ -901,10 +672,10 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
         stat[qb][wg][1][lane] = mv_lane;
         stat[qb][wg][2][lane] = (wmax[wg][0][lane] + wmax[wg][1][lane]) + (wmax[wg][2][lane] + wmax[wg][3][lane]);
       }
-      if (!k4) stat_nan[qb][wg][row] = poison;
+      stat_nan[qb][wg][row] = poison;
       __syncwarp();
       if (lane == 0) mbar_arrive(&stat_full[qb]);
-      if ((seg & 1) != wg) {                           // (the first two write outputs in turn)
+      if ((seg & 1) != wg) {
         if (lane == 0) mbar_arrive(&q_empty[qb]);
         group_sync(bar, 128);                      // the next segment's maxima go where these sums were read
         continue;
@@ -917,21 +688,15 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       if (quarter == 0 && lane < live) {
         // out = sum_w f_w O_w: f_w = 2^(m_w - M) / (L 64 2^(m_w - mv_w)) = 2^(mv_w - M) / (64 L).  The factors stay apart, the
         // first one as two square roots: V's scales go from 2^-126 to 2^120, and O_w / (64 L) brings O_w to the size of V's codes first.
-        float M = -INFINITY, L = 0.f;
-        bool any = false;
-#pragma unroll
-        for (int w = 0; w < kWgs; ++w) M = fmaxf(M, stat[qb][w][0][lane]);
-#pragma unroll
-        for (int w = 0; w < kWgs; ++w) {
-          const float lw = stat[qb][w][2][lane];
-          const bool has = lw > 0.f || lw != lw;           // NaN counts as seen
-          if (has) L += lw * ex2_approx(stat[qb][w][0][lane] - M);
-          fin[wg][w][lane] = has ? ex2_approx(0.5f * (stat[qb][w][1][lane] - M)) : 0.f;
-          any |= has;
-        }
-        stat[qb][0][2][lane] = 1.f / L / kPOne;          // (it has been read)
+        const float ma = stat[qb][0][0][lane], mb = stat[qb][1][0][lane], la = stat[qb][0][2][lane], lb = stat[qb][1][2][lane];
+        const bool has_a = la > 0.f || la != la, has_b = lb > 0.f || lb != lb;   // NaN counts as seen
+        const float M = fmaxf(ma, mb);
+        const float L = (has_a ? la * ex2_approx(ma - M) : 0.f) + (has_b ? lb * ex2_approx(mb - M) : 0.f);
+        fin[wg][0][lane] = has_a ? ex2_approx(0.5f * (stat[qb][0][1][lane] - M)) : 0.f;
+        fin[wg][1][lane] = has_b ? ex2_approx(0.5f * (stat[qb][1][1][lane] - M)) : 0.f;
+        stat[qb][0][2][lane] = 1.f / L / kPOne;          // (la has been read)
         if (whole) {
-          if (a.lse) a.lse[cm.at[lane]] = any ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+          if (a.lse) a.lse[cm.at[lane]] = has_a || has_b ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
         } else {
           float* ml = a.part_ml + ((int64_t)slot * kColMax + lane) * 2;
           ml[0] = M;
@@ -940,35 +705,27 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
       }
       if (row == 0 && u - s.n == u0)                     // for the join: this CTA's first piece
         reinterpret_cast<PaRecord*>(a.rec)[cta] = {units, s.tile, s.tiles, s.row0, pairs, s.cg * kCE, s.h};
-      if constexpr (!k4) {
-#pragma unroll
-        for (int w = 0; w < kWgs; ++w) poison |= stat_nan[qb][w][row];
-      }
+      poison = stat_nan[qb][0][row] | stat_nan[qb][1][row];
       group_sync(bar, 128);
       if (!mbar_wait_warp(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout, kPolls)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < live; c0 += 8) {
-        uint32_t r[16 * kWgs];
-#pragma unroll
-        for (int w = 0; w < kWgs; ++w) {
-          tmem_ld_cols8(acc + F::kColsO * w + c0, r + 16 * w);
-          tmem_ld_cols8(acc + F::kColsO * w + kHalf + c0, r + 16 * w + 8);
-        }
+        uint32_t r[32];
+        tmem_ld_cols8(acc + c0, r);
+        tmem_ld_cols8(acc + kHalf + c0, r + 8);
+        tmem_ld_cols8(acc + 64 + c0, r + 16);
+        tmem_ld_cols8(acc + 64 + kHalf + c0, r + 24);
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           if (c0 + c >= live) break;
-          const float over = stat[qb][0][2][c0 + c];
+          const float fa = fin[wg][0][c0 + c], fb = fin[wg][1][c0 + c], over = stat[qb][0][2][c0 + c];
           // an accumulator without a seen key holds nothing of this column (or was never written)
           float v = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWgs; ++w) {
-            const float f = fin[wg][w][c0 + c];
-            if (f != 0.f)
-              v = fmaf(fmaf(__uint_as_float(r[16 * w + 8 + c]), 0.0625f, __uint_as_float(r[16 * w + c])) * over * f, f, v);
-          }
-          if (!k4 && ((poison >> (c0 + c)) & 1u)) v = __int_as_float(0x7FC00000);
+          if (fa != 0.f) v = fmaf(__uint_as_float(r[8 + c]), 0.0625f, __uint_as_float(r[c])) * over * fa * fa;
+          if (fb != 0.f) v = fmaf(fmaf(__uint_as_float(r[24 + c]), 0.0625f, __uint_as_float(r[16 + c])) * over * fb, fb, v);
+          if ((poison >> (c0 + c)) & 1u) v = __int_as_float(0x7FC00000);
           if (whole) {
             a.out[(int64_t)cm.at[c0 + c] * kKvDim + row] = __float2bfloat16_rn(v);
           } else {
@@ -1000,49 +757,6 @@ __global__ void __launch_bounds__(pa::Form<k4, kCE>::kThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------------------
-// host side
-// ---------------------------------------------------------------------------
-// The pieces of segments that were cut joined, where no request may have so many rows that the other kernel runs too
-cudaError_t launch_paged_join(const PagedAttnArgs& a, int ctas, int columns, cudaStream_t s);
-
-template <bool k4, int kCE>
-cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int ctas, bool join,
-                           cudaStream_t s) {
-  using F = pa::Form<k4, kCE>;
-  const size_t smem = F::kFixedSmem + (size_t)a.num_requests * sizeof(int32_t);
-  static std::atomic<uint64_t> ready{0};
-  cudaError_t e = once_per_device(ready, [] {
-    const int most = F::kFixedSmem + DSA_MAX_REQUESTS * (int)sizeof(int32_t);
-    cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<k4, kCE, kPaPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess)
-      r = cudaFuncSetAttribute(paged_attention_kernel<k4, kCE, kPaCapBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (r == cudaSuccess)
-      r = cudaFuncSetAttribute(paged_attention_kernel<k4, kCE, kPaLargeCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    return r;
-  });
-  if (e != cudaSuccess) return e;
-  const int shared_keys = std::min<int64_t>((int64_t)a.max_rows * a.group, a.hi_pairs) > kCE ? 1 : 0;   // column groups share keys
-  const PaMods mods = pa_mods(a);
-  auto kernel = mods == kPaPlain     ? paged_attention_kernel<k4, kCE, kPaPlain>
-                : mods == kPaCapBias ? paged_attention_kernel<k4, kCE, kPaCapBias>
-                                     : paged_attention_kernel<k4, kCE, kPaLargeCap>;
-  e = launch_pdl(kernel, dim3(ctas), dim3(F::kThreads), smem, s, k_map, v_map, a, shared_keys);
-  count_launches(1);
-  if (e == cudaSuccess && ctas > 1 && !a.whole && join) e = launch_paged_join(a, ctas, kCE, s);
-  return e;
-}
-
-// The kernel for few rows; join: its pieces are joined here, too
-template <bool k4>
-cudaError_t launch_few_rows(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int ctas, bool join, cudaStream_t s) {
-  const int64_t pairs = (int64_t)a.max_rows * a.group;
-  return pairs <= 8    ? launch_columns<k4, 8>(a, k_map, v_map, ctas, join, s)
-         : pairs <= 16 ? launch_columns<k4, 16>(a, k_map, v_map, ctas, join, s)
-                       : launch_columns<k4, 32>(a, k_map, v_map, ctas, join, s);
-}
-
-#ifndef DSA_PAGED_KERNEL_ONLY
 // Joins the pieces of segments that were cut, where no request may have so many rows that the other kernel runs too
 __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas) {
   pdl_wait();
@@ -1050,12 +764,9 @@ __global__ void __launch_bounds__(256) paged_attention_join_kernel(const __grid_
   pa_join(a, ctas, blockIdx.x + 1, blockIdx.y);
 }
 
-cudaError_t launch_paged_join(const PagedAttnArgs& a, int ctas, int columns, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(paged_attention_join_kernel, dim3(ctas - 1, columns / 8), dim3(256), 0, s, a, ctas);
-  count_launches(1);
-  return e;
-}
-
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
 PagedAttnPlan plan_paged_attention(int max_query_len, int group) {
   PagedAttnPlan p;
   const int ctas = device_sm_count();
@@ -1071,6 +782,41 @@ PagedAttnPlan plan_paged_attention(int max_query_len, int group) {
   return p;
 }
 
+namespace {
+template <int kCE>
+cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, const CUtensorMap& v_map, int ctas, bool join,
+                           cudaStream_t s) {
+  const size_t smem = pa::kFixedSmem + (size_t)a.num_requests * sizeof(int32_t);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = once_per_device(ready, [] {
+    const int most = pa::kFixedSmem + DSA_MAX_REQUESTS * (int)sizeof(int32_t);
+    cudaError_t r = cudaFuncSetAttribute(paged_attention_kernel<kCE, kPaPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(paged_attention_kernel<kCE, kPaCapBias>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(paged_attention_kernel<kCE, kPaLargeCap>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  const int shared_keys = std::min<int64_t>((int64_t)a.max_rows * a.group, a.hi_pairs) > kCE ? 1 : 0;   // column groups share keys
+  const PaMods mods = pa_mods(a);
+  auto kernel = mods == kPaPlain     ? paged_attention_kernel<kCE, kPaPlain>
+                : mods == kPaCapBias ? paged_attention_kernel<kCE, kPaCapBias>
+                                     : paged_attention_kernel<kCE, kPaLargeCap>;
+  e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, shared_keys);
+  count_launches(1);
+  if (e != cudaSuccess) return e;
+  if (e == cudaSuccess && ctas > 1 && !a.whole && join) e = launch_paged_join(a, ctas, kCE, s);
+  return e;
+}
+}  // namespace
+
+cudaError_t launch_paged_join(const PagedAttnArgs& a, int ctas, int columns, cudaStream_t s) {
+  const cudaError_t e = launch_pdl(paged_attention_join_kernel, dim3(ctas - 1, columns / 8), dim3(256), 0, s, a, ctas);
+  count_launches(1);
+  return e;
+}
+
 cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, const uint8_t* v_codes, int max_seq_len, void* workspace,
                                    const PagedAttnPlan& plan, cudaStream_t s) {
   const int ctas = device_sm_count();
@@ -1080,12 +826,13 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, const uint8_t* k_codes, cons
   if (!encode_2d(&k_map, k_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kKvDim, rows, kKvDim, kKvDim, 1u << a.log2_page) ||
       !encode_2d(&v_map, v_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kKvDim, rows, kKvDim, kKvDim, 1u << a.log2_page))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_few_rows<false>(a, k_map, v_map, ctas, !plan.prompt, s);
+  const int64_t pairs = (int64_t)a.max_rows * a.group;
+  cudaError_t e = pairs <= 8    ? launch_columns<8>(a, k_map, v_map, ctas, !plan.prompt, s)
+                  : pairs <= 16 ? launch_columns<16>(a, k_map, v_map, ctas, !plan.prompt, s)
+                                : launch_columns<32>(a, k_map, v_map, ctas, !plan.prompt, s);
   if (e == cudaSuccess && plan.prompt)
     e = launch_paged_prompt(pa_prompt_args(a, workspace, plan, ctas), a, kPagedAttnColumns / 8, k_map, v_codes, ctas, s);   // more than 64 pairs: 32 columns above
   return e != cudaSuccess ? e : cudaGetLastError();
 }
-
-#endif  // DSA_PAGED_KERNEL_ONLY
 
 }  // namespace dsa

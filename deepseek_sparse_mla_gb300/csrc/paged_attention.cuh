@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "dsa_internal.cuh"
+#include "sm100.cuh"
 
 namespace dsa {
 
@@ -73,12 +74,113 @@ __device__ __forceinline__ float pa_factor(uint32_t top, int E, float scale) {
   return top >= 0x7F80u ? __int_as_float(0x7FC00000) : __uint_as_float((uint32_t)(E - 7 + 127) << 23) * scale;
 }
 
+__device__ __forceinline__ void tmem_ld_cols8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// What the query warp leaves about a segment's columns
+struct PaColumns {
+  float factor[kPagedAttnColumns];    // 2^k of the split query * softmax scale * log2 e
+  int limit[kPagedAttnColumns];       // keys below it are seen
+  float row[kPagedAttnColumns];       // of the request: its position is start + row
+  float slope[kPagedAttnColumns];     // * log2 e
+  int at[kPagedAttnColumns];          // row * query heads + head
+  int min_limit;                // over the columns
+  int start;                    // position of the request's first row
+};
+
+// A segment's queries (requests' rows and heads from pair kCE * cg on), by one warp: their values in two e4m3 terms into the
+// rows of q_hi (lo: kHalf rows on), and what the softmax has to know of them into cm.  ready(): waits until both may be written.
+template <int kCE, int kHalf, bool kMods, class Seg, class Ready>
+__device__ __forceinline__ bool pa_query_columns(const PagedAttnArgs& a, const Seg& s, uint8_t* q_hi, PaColumns& cm, Ready ready) {
+  const int lane = threadIdx.x & 31;
+  // first what a lane knows of a column of its own.  A column without a pair scores NaN whatever an earlier segment or
+  // kernel left of it in shared memory: NaN is no maximum, so it moves no references, and nobody takes its output.
+  const int live = min(s.rows * a.group - s.cg * kCE, kCE);
+  const int n = s.cg * kCE + min(lane, live - 1), i = n / a.group, head = s.h * a.group + (n - i * a.group);
+  const int64_t from = (int64_t)(s.row0 + i) * a.q_stride + (int64_t)head * kKvDim;
+  const int start = a.seq_lens[s.b] - s.rows;      // position of row 0
+  const int prefix = a.prefix_lens ? min(a.prefix_lens[s.b], s.len) : 0;
+  const float slope = kMods && a.slopes ? a.slopes[head] * 1.4426950408889634f : 0.f;
+  if (!ready()) return false;
+  // then the values, 16 lanes a column: eight columns a step, the next eight on their way; a rolled loop, as code that a
+  // CTA runs once or twice costs its way from L2
+  const int part = lane & 15, half = lane >> 4;
+  auto load = [&](int c) {
+    const int64_t at = __shfl_sync(0xffffffffu, from, c & 31);
+    return c < live ? *reinterpret_cast<const uint4*>(a.q + at + 8 * part) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 x[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = load(2 * k + half);
+  const int pos = start + i, limit = min(max(pos + 1, prefix), s.len);
+  if (lane < live) {
+    cm.limit[lane] = limit;
+    cm.row[lane] = (float)i;
+    cm.at[lane] = (s.row0 + i) * a.kv_heads * a.group + head;
+    cm.slope[lane] = slope;
+  } else if (lane < kCE) {
+    cm.factor[lane] = __int_as_float(0x7FC00000);
+  }
+  int low = limit;                                 // (lanes without a column hold the last one's)
+#pragma unroll 1
+  for (int c0 = 0; c0 < live; c0 += 8) {
+    uint4 y[4];
+    uint32_t tops[4];                              // the largest |x| of each column as bf16 bits, side by side
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      y[k] = x[k];
+      const uint32_t m = __vmaxu2(__vmaxu2(y[k].x & 0x7FFF7FFFu, y[k].y & 0x7FFF7FFFu), __vmaxu2(y[k].z & 0x7FFF7FFFu, y[k].w & 0x7FFF7FFFu));
+      tops[k] = max(m & 0xFFFFu, m >> 16);
+    }
+    if (c0 + 8 < live) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = load(c0 + 8 + 2 * k + half);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tops[k] = max(tops[k], __shfl_xor_sync(0xffffffffu, tops[k], o));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 2 * k + half;
+      const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w}, top = tops[k];
+      const int E = pa_exponent(top);
+      const __nv_bfloat162 up = pa_up(E);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pa_split<16>(w[e], up, hi[e], lo[e]);
+      if (c < live) {
+        const uint32_t at = (((part >> 1) ^ (c & 7)) << 4) + 8 * (part & 1);
+        *reinterpret_cast<uint2*>(q_hi + c * kKvDim + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2*>(q_hi + (kHalf + c) * kKvDim + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        if (part == 0) cm.factor[c] = pa_factor(top, E, a.scale_log2);
+      }
+    }
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) {
+    cm.min_limit = low;
+    cm.start = start;
+  }
+  return true;
+}
+
 // Requests of many rows (paged_prompt.cu), and the join of both kernels' pieces (few: the first kernel's arguments, few_y
 // groups of 8 columns); k_map: the K codes in boxes of a page.
 cudaError_t launch_paged_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map,
                                 const uint8_t* v_codes, int ctas, cudaStream_t s);
 cudaError_t launch_kv4_prompt(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, const CUtensorMap& k_map, const uint8_t* v_codes,
                               int ctas, cudaStream_t s);
+// The pieces of the few-row kernel's cut segments joined, where no request may have so many rows that the prompt kernel runs too
+cudaError_t launch_paged_join(const PagedAttnArgs& a, int ctas, int columns, cudaStream_t s);
 cudaError_t launch_prompt_join(const PagedAttnArgs& a, const PagedAttnArgs& few, int few_y, int ctas, cudaStream_t s);
 
 // Where the workspace's parts lie, and which requests the kernel for few rows takes
