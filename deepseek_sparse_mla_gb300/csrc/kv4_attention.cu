@@ -22,8 +22,8 @@
 // and V apart, as K is done with early; one warp finds segments for all; references and factors of 8 columns stay in
 // registers; probabilities are formed in pairs (f32x2, then f16x2 for the two terms).
 //
-// Work, pieces and their join as in paged_attention.cu.  Per CTA (16 warps): 0 K's codes, 4 V's codes, 5 K's scales and their
-// order, 6 segments and V's scales; 1 products of the scores, 3 of the outputs; 2 queries; 8-11 and 12-15 the softmax of the
+// Work, pieces and their join as in paged_attention.cu.  Per CTA (16 warps): 0 K's codes, 4 V's codes, 5 the order of K's
+// scales, 6 segments; 1 products of the scores, 3 of the outputs; 2 queries; 8-11 and 12-15 the softmax of the
 // even and the odd tiles, one key a thread.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       mbar_init(&sf_full[i], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&v_full[i], 2);                        // codes and scales
+      mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -248,55 +248,61 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       return -1;
     };
     const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
-    // Codes of K or V: lanes 0 .. ppt - 1 load a page each.  4-bit codes count 64 bytes a row on the barrier.  K's scales are
-    // loaded along with its codes (lanes 8 ..).
-    auto load = [&](auto of_v, const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint8_t* tiles) {
+    // K or V, codes (lanes 0 .. ppt - 1, a page each) and scales (lanes 8 ..).  4-bit codes count 64 bytes a row on the barrier.
+    auto load_tiles = [&](auto of_v, const Seg& s, auto& r, bool& first, int& loaded) {
       constexpr bool kV = decltype(of_v)::value;
-      Ring<kV ? kVStages : kKStages> r;
+      constexpr int kRing = kV ? kVStages : kKStages, kScale = kV ? 2 : kKv4Blocks;   // scale bytes of a token
+      uint64_t* const full = kV ? v_full : k_full;
+      uint64_t* const empty = kV ? v_empty : k_empty;
+      const uint8_t* const scales = kV ? reinterpret_cast<const uint8_t*>(a.v_scales4) : a.k_scales4;
       const int mine = lane & 7;
-      const bool codes = lane < 8, used = mine < ppt && lane < (kV ? 8 : 16);
-      uint8_t* const dst = codes ? tiles + mine * (kKvDim << lp) : sScaleK + mine * (kKv4Blocks << lp);
-      bool first = true, ok = true;
-      int loaded = 0;
-      for (Seg s; ok && next_segment(s);) {
-        int batch = -1, row32 = -1;
-        for (int t = 0; t < s.n; ++t) {
-          const int p0 = s.template tile_at<kMods>(t) * ppt;
-          if ((p0 >> 5) != batch) {
-            batch = p0 >> 5;
-            row32 = rows_of(s, batch, kV);
-          }
-          if (!first && !wait_warp(&empty[r.st], r.turn ^ 1, err, kErrMmaTimeout)) {
-            ok = false;
-            break;
-          }
-          const int row = __shfl_sync(0xffffffffu, row32, (p0 + mine) & 31);
-          const uint32_t bad = __ballot_sync(0xffffffffu, codes && used && row < 0);
-          if (lane == 0) {
-            if (kV) sbad[r.st] = bad;
-            mbar_arrive_expect_tx(&full[r.st], (uint32_t)(ppt - __popc(bad)) * ((uint32_t)(kKvDim / 2 + (kV ? 0 : kKv4Blocks)) << lp));
-          }
-          __syncwarp();
-          if (used && row >= 0) {
-            if (codes) tma_load_2d_hint(dst + r.st * kTileBytes, map, 0, row, &full[r.st], policy);
-            else bulk_load_hint(dst + r.st * kKScales, a.k_scales4 + (int64_t)row * kKv4Blocks, kKv4Blocks << lp, &full[r.st], policy);
-          }
-          loaded = min(loaded + 1, kV ? kVStages : kKStages);
-          r.next();
-          if (r.st == 0) first = false;
+      const bool codes = lane < 8, used = mine < ppt && lane < 16;
+      uint8_t* const dst = codes ? (kV ? sV : sK) + mine * (kKvDim << lp) : (kV ? sScaleV : sScaleK) + mine * (kScale << lp);
+      int batch = -1, row32 = -1;
+      for (int t = 0; t < s.n; ++t) {
+        const int p0 = s.template tile_at<kMods>(t) * ppt;
+        if ((p0 >> 5) != batch) {
+          batch = p0 >> 5;
+          row32 = rows_of(s, batch, kV);
         }
+        if (!first && !wait_warp(&empty[r.st], r.turn ^ 1, err, kErrMmaTimeout)) return false;
+        const int row = __shfl_sync(0xffffffffu, row32, (p0 + mine) & 31);
+        const uint32_t bad = __ballot_sync(0xffffffffu, codes && used && row < 0);
+        if (lane == 0) {
+          if (kV) sbad[r.st] = bad;
+          mbar_arrive_expect_tx(&full[r.st], (uint32_t)(ppt - __popc(bad)) * ((uint32_t)(kKvDim / 2 + kScale) << lp));
+        }
+        __syncwarp();
+        if (used && row >= 0) {
+          if (codes) tma_load_2d_hint(dst + r.st * kTileBytes, kV ? &v_map : &k_map, 0, row, &full[r.st], policy);
+          else bulk_load_hint(dst + r.st * (kTok * kScale), scales + (int64_t)row * kScale, kScale << lp, &full[r.st], policy);
+        }
+        loaded = min(loaded + 1, kRing);
+        r.next();
+        if (r.st == 0) first = false;
       }
-      // nothing may still be landing in shared memory when the CTA exits: the last turn of each stage
+      return true;
+    };
+    // nothing may still be landing in shared memory when the CTA exits: the last turn of each stage
+    auto landed = [&](auto of_v, auto r, int loaded) {
+      constexpr int kRing = decltype(of_v)::value ? kVStages : kKStages;
       for (int k = 0; k < loaded; ++k) {
-        r.st = r.st == 0 ? (kV ? kVStages : kKStages) - 1 : r.st - 1;
-        if (r.st == (kV ? kVStages : kKStages) - 1) r.turn ^= 1;
-        wait_warp(&full[r.st], r.turn, err, kErrTmaTimeout);
+        r.st = r.st == 0 ? kRing - 1 : r.st - 1;
+        if (r.st == kRing - 1) r.turn ^= 1;
+        wait_warp(decltype(of_v)::value ? &v_full[r.st] : &k_full[r.st], r.turn, err, kErrTmaTimeout);
       }
     };
+    auto load = [&](auto of_v) {
+      Ring<decltype(of_v)::value ? kVStages : kKStages> r;
+      bool first = true, ok = true;
+      int loaded = 0;
+      for (Seg s; ok && next_segment(s);) ok = load_tiles(of_v, s, r, first, loaded);
+      landed(of_v, r, loaded);
+    };
     if (warp == kLoadKWarp) {
-      load(std::false_type{}, &k_map, k_full, k_empty, sK);
+      load(std::false_type{});
     } else if (warp == kLoadVWarp) {
-      load(std::true_type{}, &v_map, v_full, v_empty, sV);
+      load(std::true_type{});
     } else if (warp == kOrderWarp) {
       // ---------------------------------------------------------------- K's scales as tcgen05.cp takes them
       // Those of keys l, l + 32, l + 64 and l + 96 go into the l-th 16 bytes.
@@ -407,18 +413,15 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         if (lane == 0) mbar_arrive(&q_full[buf]);
       }
     } else if (warp == kSegWarp) {
-      // ---------------------------------------------------------------- segments (and an end mark), and V's scales
+        // ---------------------------------------------------------------- segments, and an end mark
       int64_t u = pa_unit_start(cta, units, ctas);
       const int64_t u1 = pa_unit_start(cta + 1, units, ctas);
       // segments are cut where the range ends, or (short requests) belong to the range they begin in as a whole
       const int64_t cut = a.whole ? units : u1;
       int b = 0;                                       // units of the requests before b, without heads
       int64_t before = 0;
-      Ring<kVStages> r;
-      bool first = true, ok = true;
-      int loaded = 0;
-      // the next segment, for everyone: one ahead of the one whose scales are loaded
-      auto publish = [&](Seg& s) {
+      bool ok = true;
+      for (Seg s;;) {
         s = {};
         while (u < u1 && s.n == 0) {
           // the request that holds u: 32 at a time
@@ -463,45 +466,14 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
           s.len = sh.len;
         }
         ++seg;
-        if (seg >= kSegBufs && !wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kSegPolls)) return false;
+        if (seg >= kSegBufs) ok = wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kSegPolls);
+        if (!ok) break;
         if (lane == 0) {
           segs[seg % kSegBufs] = s;
           mbar_arrive(&seg_full[seg % kSegBufs]);
         }
         __syncwarp();
-        return true;
-      };
-      Seg s, ahead;
-      for (ok = publish(ahead); ok;) {
-        s = ahead;
         if (s.n == 0) break;
-        ok = publish(ahead);
-        if (!ok) break;
-        int batch = -1, row32 = -1;
-        for (int t = 0; t < s.n; ++t) {
-          const int p0 = s.template tile_at<kMods>(t) * ppt;
-          if ((p0 >> 5) != batch) {
-            batch = p0 >> 5;
-            row32 = rows_of(s, batch, false);
-          }
-          ok = first || wait_warp(&v_empty[r.st], r.turn ^ 1, err, kErrMmaTimeout);
-          if (!ok) break;
-          const int row = __shfl_sync(0xffffffffu, row32, (p0 + lane) & 31);
-          const bool load_it = lane < ppt && row >= 0;
-          const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load_it));
-          if (lane == 0) mbar_arrive_expect_tx(&v_full[r.st], loads * (2u << lp));
-          __syncwarp();
-          if (load_it) bulk_load_hint(sScaleV + r.st * kVScales + lane * (2 << lp), a.v_scales4 + row, 2u << lp, &v_full[r.st], policy);
-          loaded = min(loaded + 1, kVStages);
-          r.next();
-          if (r.st == 0) first = false;
-        }
-      }
-      // as the loaders of codes
-      for (int k = 0; k < loaded; ++k) {
-        r.st = r.st == 0 ? kVStages - 1 : r.st - 1;
-        if (r.st == kVStages - 1) r.turn ^= 1;
-        wait_warp(&v_full[r.st], r.turn, err, kErrTmaTimeout);
       }
     }
   } else {
@@ -549,28 +521,44 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
         // distances in integers from the request's first row, exact up to 2^24 (see paged_attention.cu)
         const float ahead = kMods ? (float)(j - cm.start) : 0.f;
-        // 8 columns' products as they are, in pairs
-        auto products = [&](uint64_t (&z)[4], int c0) {
-          uint32_t hi[8], lo[8];
-          tmem_ld_cols8(from + c0, hi);
-          if (F::kApart) tmem_ld_cols8(from + kHalf + c0, lo);
+        // products as they are, in pairs: all columns at once, one wait
+        auto products = [&](auto& z, int c0) {
+          constexpr int kC = sizeof(z) / 4;
+          uint32_t hi[kC], lo[F::kApart ? kC : 1];
+#pragma unroll
+          for (int c = 0; c < kC; c += 8) {
+            tmem_ld_cols8(from + c0 + c, hi + c);
+            if (F::kApart) tmem_ld_cols8(from + kHalf + c0 + c, lo + c);
+          }
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kC / 2; ++c) {
             z[c] = pack2(__uint_as_float(hi[2 * c]), __uint_as_float(hi[2 * c + 1]));
             if (F::kApart) z[c] = add2(z[c], pack2(__uint_as_float(lo[2 * c]), __uint_as_float(lo[2 * c + 1])));
           }
         };
-        auto factor = [&](int c0, int c) {
-          return kHold ? hold_f[c] : *reinterpret_cast<const uint64_t*>(&cm.factor[c0 + 2 * c]);
+        // four columns of a shared array
+        auto four = [&](const float* x, uint64_t (&r)[2]) {
+          const float4 v = *reinterpret_cast<const float4*>(x);
+          r[0] = pack2(v.x, v.y);
+          r[1] = pack2(v.z, v.w);
         };
-        // .. and as scores
-        auto scores = [&](float (&z)[8], const uint64_t (&y)[4], int c0) {
+        // .. and 8 of them as scores
+        auto scores = [&](float (&z)[8], const uint64_t* y, int c0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 x = unpack2(mul2(y[c], factor(c0, c)));
-            z[2 * c] = x.x;
-            z[2 * c + 1] = x.y;
+          for (int c = 0; c < 4; c += 2) {
+            uint64_t f[2];
+            if (kHold) {
+              f[0] = hold_f[c];
+              f[1] = hold_f[c + 1];
+            } else {
+              four(cm.factor + c0 + 2 * c, f);
+            }
+            const float2 v = unpack2(mul2(y[c], f[0])), w = unpack2(mul2(y[c + 1], f[1]));
+            z[2 * c] = v.x;
+            z[2 * c + 1] = v.y;
+            z[2 * c + 2] = w.x;
+            z[2 * c + 3] = w.y;
           }
           if (kMods && in != 0.f) {
 #pragma unroll
@@ -670,6 +658,8 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         if (fresh) raise();
         for (;;) {
           // the probabilities, and their contributions in two e4m3 terms
+          uint64_t all[kNC / 2];
+          products(all, 0);
           uint32_t hi[kHalf / 4], lo[kHalf / 4];
           float p_top = 0.f;
           __half2 x_top = __float2half2_rn(0.f);
@@ -677,16 +667,28 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
           for (int c0 = 0; c0 < kHalf; c0 += 8) {
             hi[c0 / 4] = hi[c0 / 4 + 1] = lo[c0 / 4] = lo[c0 / 4 + 1] = 0;
             if (c0 >= kNC) continue;
-            uint64_t y[4];
-            products(y, c0);
+            uint64_t* const y = all + c0 / 2;
+            uint64_t mm[4], ee[4];
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+              uint64_t m2[2] = {}, e2[2] = {}, f2[2] = {};
+              if (!kHold) {
+                four(ref_m + c0 + 2 * c, m2);
+                four(ref_e + c0 + 2 * c, e2);
+                if (!kMods) four(cm.factor + c0 + 2 * c, f2);
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                mm[c + k] = kHold ? hold_m[c + k] : m2[k];
+                ee[c + k] = kHold ? hold_e[c + k] : e2[k];
+                if (!kMods) y[c + k] = fma2(y[c + k], kHold ? hold_f[c + k] : f2[k], mm[c + k]);
+              }
+            }
             if (kMods) {
               float z[8];
               scores(z, y, c0);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) y[c] = add2(pack2(z[2 * c], z[2 * c + 1]), kHold ? hold_m[c] : *reinterpret_cast<const uint64_t*>(ref_m + c0 + 2 * c));
-            } else {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) y[c] = fma2(y[c], factor(c0, c), kHold ? hold_m[c] : *reinterpret_cast<const uint64_t*>(ref_m + c0 + 2 * c));
+              for (int c = 0; c < 4; ++c) y[c] = add2(pack2(z[2 * c], z[2 * c + 1]), mm[c]);
             }
             uint32_t h8[4], l8[4];
 #pragma unroll
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
               p[(c0 >> 1) + c] = pack2(e.x, e.y);
               p_top = fmaxf(p_top, fmaxf(e.x, e.y));
               // in this order: 0 stays 0 whatever the scale of an unseen key ..
-              float2 x = unpack2(mul2(mul2(p[(c0 >> 1) + c], kHold ? hold_e[c] : *reinterpret_cast<const uint64_t*>(ref_e + c0 + 2 * c)), vs2));
+              float2 x = unpack2(mul2(mul2(p[(c0 >> 1) + c], ee[c]), vs2));
               if (kMasked) {                           // .. and of one that some columns do not see even NaN
                 if (!seen(c0 + 2 * c)) x.x = 0.f;
                 if (!seen(c0 + 2 * c + 1)) x.y = 0.f;

@@ -86,15 +86,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
 }
 
 // What the query warp leaves about a segment's columns
-struct PaColumns {
+struct __align__(16) PaColumns {      // (an array of them is read four floats at a time)
   float factor[kPagedAttnColumns];    // 2^k of the split query * softmax scale * log2 e
   int limit[kPagedAttnColumns];       // keys below it are seen
   float row[kPagedAttnColumns];       // of the request: its position is start + row
   float slope[kPagedAttnColumns];     // * log2 e
   int at[kPagedAttnColumns];          // row * query heads + head
-  int min_limit;                // over the columns
-  int start;                    // position of the request's first row
+  int min_limit;                      // over the columns
+  int start;                          // position of the request's first row
 };
+static_assert(sizeof(PaColumns) % 16 == 0, "every one of an array is aligned");
 
 // A segment's queries (requests' rows and heads from pair kCE * cg on), by one warp: their values in two e4m3 terms into the
 // rows of q_hi (lo: kHalf rows on), and what the softmax has to know of them into cm.  ready(): waits until both may be written.

@@ -71,3 +71,16 @@ def test_capped_scores_distance_bias_and_prefix(n, which):
         mods["prefix"] = np.array([min(L, 45 + 100 * i) for i, L in enumerate(seq)], np.int32)
     got, lse = run(case, **mods)
     check_attention(got, lse, case.oracle(**mods), softcap=mods.get("softcap", 0.0), reach=reach(case, mods))
+
+
+@pytest.mark.parametrize("rows,group", [(1, 8), (1, 1), (2, 8), (4, 8), (3, 5), (8, 8)])
+def test_many_requests_several_segments_a_cta(rows, group):
+    """More segments than CTAs in every form of the kernel: what it keeps of a segment lies in rings of places."""
+    rng = np.random.default_rng(rows * 100 + group)
+    seq = rng.integers(rows, 150, 320)
+    case = Kv4Case(230 + rows, seq, [rows] * 320, 32, 2, group)
+    got, lse = run(case)
+    check_attention(got, lse, case.oracle())
+    want = case.oracle(prefix=np.full(320, 40), slopes=case.slopes, softcap=4.0)
+    got, lse = run(case, prefix=np.full(320, 40, np.int32), slopes=case.slopes, softcap=4.0)
+    check_attention(got, lse, want, softcap=4.0, reach=reach(case, {"slopes": 1}))
