@@ -22,9 +22,9 @@
 // and V apart, as K is done with early; one warp finds segments for all; references and factors of 8 columns stay in
 // registers; probabilities are formed in pairs (f32x2, then f16x2 for the two terms).
 //
-// Work, pieces and their join as in paged_attention.cu.  Per CTA (16 warps): 0 K's codes, 4 V's codes, 5 the order of K's
-// scales, 6 segments; 1 products of the scores, 3 of the outputs; 2 queries; 8-11 and 12-15 the softmax of the
-// even and the odd tiles, one key a thread.
+// Work, pieces and their join as in paged_attention.cu.  Per CTA (16 warps): 0 and 4 load K, 2 and 6 V; 5 orders K's scales; 1 issues
+// the products of the scores, 3 of the outputs; 7 finds the segments and splits their queries; 8-11 and 12-15 are the softmax,
+// two warpgroups that take the tiles in turn, one key a thread.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
 #include "tmap.cuh"
@@ -39,11 +39,8 @@ namespace p4 {
 constexpr int kTok = kPaTok;                    // keys per tile
 constexpr int kTileBytes = kTok * kKvDim;       // of K or V in shared memory: 16-byte units, half used
 constexpr int kKScales = kTok * kKv4Blocks, kVScales = kTok * 2;   // bytes of a tile's scales
-constexpr int kLoadKWarp = 0, kScoreWarp = 1, kQueryWarp = 2, kOutWarp = 3, kLoadVWarp = 4, kOrderWarp = 5, kSegWarp = 6, kSoftWarp0 = 8;
-constexpr int kThreads = 512;
-constexpr uint32_t kRegsLow = 80, kRegsSoft = 176;   // 2 * 80 + 2 * 176 = 4 * 128: the launch's
+constexpr int kLoadKWarp = 0, kScoreWarp = 1, kLoadVWarp = 2, kOutWarp = 3, kOrderWarp = 5, kQueryWarp = 7, kSoftWarp0 = 8;   // loaders: 0 and 4, 2 and 6
 constexpr int kQBufs = 3, kSegBufs = 4;
-constexpr int kSBufs = 4;                       // two a warpgroup: one is kept until its tile is known to be done
 constexpr uint32_t kTmemCols = 512, kColScales = 192, kColQScales = 216, kColO = 256;
 constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
@@ -57,12 +54,16 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32
 template <int kCE>
 struct Form {
   static constexpr int kHalf = kCE < 16 ? 16 : kCE, kN = 2 * kHalf;   // columns of the hi terms, and of both
+  static constexpr int kWgs = 2;      // softmax warpgroups
+  static constexpr int kThreads = 256 + 128 * kWgs;
+  static constexpr uint32_t kRegsLow = kWgs == 3 ? 72 : 80, kRegsSoft = kWgs == 3 ? 112 : 176;   // 2 * 72 + 3 * 112 = 5 * 96, 2 * 80 + 2 * 176 = 4 * 128: the launch's
+  static constexpr int kSBufs = 2 * kWgs;             // two a warpgroup: one is kept until its tile is known to be done
   static constexpr bool kApart = kCE <= 16;           // Q's two terms have columns of their own
   static constexpr int kColsS = kApart ? kN : kHalf;  // TMEM columns of a tile's scores
   static constexpr int kKStages = kCE <= 16 ? 5 : 4, kVStages = kCE <= 16 ? 6 : 5;
   static constexpr int kQBytes = kN * kKvDim, kPBytes = kTok * kN;
-  static constexpr int kSmem = (kKStages + kVStages) * kTileBytes + kQBufs * kQBytes + 4 * kPBytes + kKStages * kKScales + kVStages * kVScales + 1024;
-  static_assert(kSBufs * kColsS <= (int)kColScales && kColO + 4 * kN <= (int)kTmemCols, "TMEM columns");
+  static constexpr int kSmem = (kKStages + kVStages) * kTileBytes + kQBufs * kQBytes + 2 * kWgs * kPBytes + kKStages * kKScales + kVStages * kVScales + 1024;
+  static_assert(kSBufs * kColsS <= (int)kColScales && kColScales + 4 * kSBufs <= kColQScales && kColO + 2 * kWgs * kN <= kTmemCols, "TMEM columns");
 };
 
 // A run of tiles of one segment, as the segment warp leaves it for the others
@@ -117,31 +118,32 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 
 // kCE columns (8, 16 or 32); kModSet: score cap and distance bias compiled in
 template <int kCE, PaMods kModSet>
-__global__ void __launch_bounds__(p4::kThreads, 1)
+__global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
     kv4_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const __grid_constant__ PagedAttnArgs a, int shared_keys) {
   using namespace p4;
   using F = Form<kCE>;
   constexpr bool kMods = kModSet != kPaPlain;
+  constexpr int kThreads = F::kThreads, kWgs = F::kWgs, kSBufs = F::kSBufs;
   constexpr int kHalf = F::kHalf, kN = F::kN, kKStages = F::kKStages, kVStages = F::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sK = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sV = sK + kKStages * kTileBytes;
   uint8_t* const sQ = sV + kVStages * kTileBytes;
   uint8_t* const sP = sQ + kQBufs * F::kQBytes;            // two buffers a warpgroup
-  uint8_t* const sScaleK = sP + 4 * F::kPBytes;
+  uint8_t* const sScaleK = sP + 2 * kWgs * F::kPBytes;
   uint8_t* const sScaleV = sScaleK + kKStages * kKScales;
 
   __shared__ uint64_t k_full[kKStages], k_empty[kKStages], sf_full[kKStages], v_full[kVStages], v_empty[kVStages];
-  __shared__ uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[4], pv_done[4];
+  __shared__ uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2 * kWgs], pv_done[2 * kWgs];
   __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[2], o_empty[2], mma_done;
   __shared__ uint64_t seg_full[kSegBufs], seg_empty[kSegBufs];
   __shared__ Seg segs[kSegBufs];
   __shared__ uint32_t sbad[kVStages];                  // pages of a tile that are not there
   __shared__ __align__(16) PaColumns cols[kQBufs];
-  __shared__ __align__(16) float refs[2][2][kCE];
-  __shared__ float wmax[2][4][kCE], fin[2][2][kCE];
-  __shared__ float stat[kQBufs][2][3][kCE];            // each warpgroup's m, mv and l of a segment
+  __shared__ __align__(16) float refs[kWgs][2][kCE];
+  __shared__ float wmax[kWgs][4][kCE], fin[kWgs][kWgs][kCE];
+  __shared__ float stat[kQBufs][kWgs][3][kCE];            // each warpgroup's m, mv and l of a segment
   __shared__ int32_t scan[kThreads / 32], total;
   __shared__ uint32_t tmem_base, bits_all;
 
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * kWgs; ++i) {
       mbar_init(&p_full[i], 1);
       mbar_init(&pv_done[i], 1);
       mbar_init(&s_full[i], 1);
@@ -169,12 +171,12 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
     }
     for (int i = 0; i < kQBufs; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 9);                       // the last product that reads it, and eight softmax warps
-      mbar_init(&stat_full[i], 8);
+      mbar_init(&q_empty[i], 1 + 4 * kWgs);            // the last product that reads it, and the softmax warps
+      mbar_init(&stat_full[i], 4 * kWgs);
     }
     for (int i = 0; i < kSegBufs; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 14);                    // every warp that reads it
+      mbar_init(&seg_empty[i], 7 + 4 * kWgs);                   // every warp that reads it
     }
     mbar_init(&mma_done, 2);
     bits_all = 0;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
   uint32_t* const err = &bits_all;                     // this CTA's status bits, stored at the end
 
   if (warp < kSoftWarp0) {
-    regs_dec<kRegsLow>();
+    regs_dec<F::kRegsLow>();
     const int lp = a.log2_page, ppt = kTok >> lp;
     // one segment after the other: its place in the ring, and a copy of what it is
     int seg = -1;
@@ -238,70 +240,77 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       if (lane == 0) mbar_arrive(&seg_empty[seg % kSegBufs]);
       return s.n > 0;
     };
-    // The first rows of 32 pages of a segment, one a lane (-1: not there), from page 32 * batch on
-    auto rows_of = [&](const Seg& s, int batch, bool report) {
+    // 32 pages of a segment from page 32 * batch on, one a lane: their ids (as they are in the table; -1 behind the request's
+    // tokens), asked for well before they are used, and then their first rows (-1: not there).
+    auto pages_of = [&](const Seg& s, int batch) {
       const int p = 32 * batch + lane;
-      if (p >= (s.len + (1 << lp) - 1) >> lp || p < 0) return -1;
-      const int page = a.block_table[(int64_t)s.b * a.table_stride + p];
+      return p >= 0 && p < (s.len + (1 << lp) - 1) >> lp ? a.block_table[(int64_t)s.b * a.table_stride + p] : -1;
+    };
+    auto rows_of = [&](const Seg& s, int batch, int page, bool report) {
       if (page >= 0 && page < a.num_pages) return (page * a.kv_heads + s.h) << lp;
-      if (report) atomicOr(err, kErrBadPage);
+      if (report && 32 * batch + lane < (s.len + (1 << lp) - 1) >> lp) atomicOr(err, kErrBadPage);
       return -1;
     };
     const uint64_t policy = shared_keys ? l2_evict_normal() : l2_evict_first();
-    // K or V, codes (lanes 0 .. ppt - 1, a page each) and scales (lanes 8 ..).  4-bit codes count 64 bytes a row on the barrier.
-    auto load_tiles = [&](auto of_v, const Seg& s, auto& r, bool& first, int& loaded) {
+    // Every other tile of K or V, codes (lanes 0 .. ppt - 1, a page each) and scales (lanes 8 ..).  4-bit codes count 64 bytes a row
+    // on the barrier.  Getting one tile's copies out takes a warp some 900 cycles of one thing after the other, so two warps
+    // take turns.
+    auto load = [&](auto of_v) {
       constexpr bool kV = decltype(of_v)::value;
-      constexpr int kRing = kV ? kVStages : kKStages, kScale = kV ? 2 : kKv4Blocks;   // scale bytes of a token
+      constexpr int kRing = kV ? kVStages : kKStages, kScale = kV ? 2 : kKv4Blocks, kWay = kMods ? -1 : 1;   // scale bytes of a token
       uint64_t* const full = kV ? v_full : k_full;
       uint64_t* const empty = kV ? v_empty : k_empty;
       const uint8_t* const scales = kV ? reinterpret_cast<const uint8_t*>(a.v_scales4) : a.k_scales4;
       const int mine = lane & 7;
       const bool codes = lane < 8, used = mine < ppt && lane < 16;
       uint8_t* const dst = codes ? (kV ? sV : sK) + mine * (kKvDim << lp) : (kV ? sScaleV : sScaleK) + mine * (kScale << lp);
-      int batch = -1, row32 = -1;
-      for (int t = 0; t < s.n; ++t) {
-        const int p0 = s.template tile_at<kMods>(t) * ppt;
-        if ((p0 >> 5) != batch) {
-          batch = p0 >> 5;
-          row32 = rows_of(s, batch, kV);
+      int i = warp >> 2, i0 = 0, st = i;               // the tile to load (its place in the ring, and the ring's turn), and the CTA's before the segment
+      uint32_t turn = 0;
+      bool ok = true;
+      for (Seg s; ok && next_segment(s); i0 += s.n) {
+        if (i - i0 >= s.n) continue;
+        int batch = (s.template tile_at<kMods>(i - i0) * ppt) >> 5, row32 = rows_of(s, batch, pages_of(s, batch), kV), ahead = pages_of(s, batch + kWay);
+        for (; i - i0 < s.n; i += 2) {
+          const int p0 = s.template tile_at<kMods>(i - i0) * ppt;
+          if ((p0 >> 5) != batch) {
+            batch += kWay;
+            row32 = rows_of(s, batch, ahead, kV);
+            ahead = pages_of(s, batch + kWay);
+          }
+          if (i >= kRing) ok = wait_warp(&empty[st], turn ^ 1, err, kErrMmaTimeout);
+          if (!ok) break;
+          const int row = __shfl_sync(0xffffffffu, row32, (p0 + mine) & 31);
+          const uint32_t bad = __ballot_sync(0xffffffffu, codes && used && row < 0);
+          if (lane == 0) {
+            if (kV) sbad[st] = bad;
+            mbar_arrive_expect_tx(&full[st], (uint32_t)(ppt - __popc(bad)) * ((uint32_t)(kKvDim / 2 + kScale) << lp));
+          }
+          __syncwarp();
+          if (used && row >= 0) {
+            if (codes) tma_load_2d_hint(dst + st * kTileBytes, kV ? &v_map : &k_map, 0, row, &full[st], policy);
+            else bulk_load_hint(dst + st * (kTok * kScale), scales + (int64_t)row * kScale, kScale << lp, &full[st], policy);
+          }
+          st += 2;
+          if (st >= kRing) {
+            st -= kRing;
+            turn ^= 1;
+          }
         }
-        if (!first && !wait_warp(&empty[r.st], r.turn ^ 1, err, kErrMmaTimeout)) return false;
-        const int row = __shfl_sync(0xffffffffu, row32, (p0 + mine) & 31);
-        const uint32_t bad = __ballot_sync(0xffffffffu, codes && used && row < 0);
-        if (lane == 0) {
-          if (kV) sbad[r.st] = bad;
-          mbar_arrive_expect_tx(&full[r.st], (uint32_t)(ppt - __popc(bad)) * ((uint32_t)(kKvDim / 2 + kScale) << lp));
-        }
-        __syncwarp();
-        if (used && row >= 0) {
-          if (codes) tma_load_2d_hint(dst + r.st * kTileBytes, kV ? &v_map : &k_map, 0, row, &full[r.st], policy);
-          else bulk_load_hint(dst + r.st * (kTok * kScale), scales + (int64_t)row * kScale, kScale << lp, &full[r.st], policy);
-        }
-        loaded = min(loaded + 1, kRing);
-        r.next();
-        if (r.st == 0) first = false;
       }
-      return true;
-    };
-    // nothing may still be landing in shared memory when the CTA exits: the last turn of each stage
-    auto landed = [&](auto of_v, auto r, int loaded) {
-      constexpr int kRing = decltype(of_v)::value ? kVStages : kKStages;
-      for (int k = 0; k < loaded; ++k) {
-        r.st = r.st == 0 ? kRing - 1 : r.st - 1;
-        if (r.st == kRing - 1) r.turn ^= 1;
-        wait_warp(decltype(of_v)::value ? &v_full[r.st] : &k_full[r.st], r.turn, err, kErrTmaTimeout);
+      // nothing may still be landing in shared memory when the CTA exits: this warp's among the last kRing tiles (the stages of
+      // earlier ones have been filled again since)
+      for (i -= 2; i >= 0 && i >= i0 - kRing; i -= 2) {
+        st -= 2;
+        if (st < 0) {
+          st += kRing;
+          turn ^= 1;
+        }
+        wait_warp(&full[st], turn, err, kErrTmaTimeout);
       }
     };
-    auto load = [&](auto of_v) {
-      Ring<decltype(of_v)::value ? kVStages : kKStages> r;
-      bool first = true, ok = true;
-      int loaded = 0;
-      for (Seg s; ok && next_segment(s);) ok = load_tiles(of_v, s, r, first, loaded);
-      landed(of_v, r, loaded);
-    };
-    if (warp == kLoadKWarp) {
+    if ((warp & 3) == kLoadKWarp) {
       load(std::false_type{});
-    } else if (warp == kLoadVWarp) {
+    } else if ((warp & 3) == kLoadVWarp) {
       load(std::true_type{});
     } else if (warp == kOrderWarp) {
       // ---------------------------------------------------------------- K's scales as tcgen05.cp takes them
@@ -372,18 +381,18 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       const uint64_t d_v = smem_desc(smem_u32(sV), 16, 1024, kSwizzle128B);
       const uint64_t d_p = smem_desc(smem_u32(sP), 16, 8 * kN, kN == 64 ? kSwizzle64B : kSwizzle32B);
       Ring<kVStages> r;
-      uint32_t i = 0;
+      uint32_t wg = 0, n = 0;                          // whose tile it is, and which of its own
       bool ok = true;
       for (Seg s; ok && next_segment(s);) {
-        uint32_t fresh = 3;                            // accumulators of the segment without a product yet
+        uint32_t fresh = (1u << kWgs) - 1;                            // accumulators of the segment without a product yet
         if (seg >= 2) ok = wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout);
-        for (int t = 0; t < s.n && ok; ++t, ++i) {
-          const uint32_t wg = i & 1, pn = 2 * wg + ((i >> 1) & 1);
-          ok = mbar_spin_warp(&p_full[pn], (i >> 2) & 1, err, kErrMmaTimeout);
+        for (int t = 0; t < s.n; ++t) {
+          const uint32_t pn = 2 * wg + (n & 1);
+          ok = ok && mbar_spin_warp(&p_full[pn], (n >> 1) & 1, err, kErrMmaTimeout);
           if (!ok) break;
           tc_fence_after();
           const uint64_t v = d_v + (uint64_t)((r.st * kTileBytes) >> 4), p = d_p + (uint64_t)((pn * F::kPBytes) >> 4);
-          const uint32_t to = tmem + kColO + 2 * kN * (seg & 1) + kN * wg;
+          const uint32_t to = tmem + kColO + kWgs * kN * (seg & 1) + kN * wg;
           const bool add = !((fresh >> wg) & 1u);
           fresh &= ~(1u << wg);
           if (leader) {
@@ -396,24 +405,16 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
           }
           __syncwarp();
           r.next();
+          if (++wg == kWgs) {
+            wg = 0;
+            ++n;
+          }
         }
       }
       if (leader) mma_commit(&mma_done);
       wait_warp(&mma_done, 0, err, kErrMmaTimeout);
     } else if (warp == kQueryWarp) {
-      // ---------------------------------------------------------------- queries
-      for (Seg s; next_segment(s);) {
-        const int buf = seg % kQBufs;
-        if (!pa_query_columns<kCE, kHalf, kMods>(a, s, sQ + buf * F::kQBytes, cols[buf], [&] {
-              return seg < kQBufs || wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kSegPolls);
-            }))
-          break;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[buf]);
-      }
-    } else if (warp == kSegWarp) {
-        // ---------------------------------------------------------------- segments, and an end mark
+      // ---------------------------------------------------------------- segments (and an end mark), and their queries
       int64_t u = pa_unit_start(cta, units, ctas);
       const int64_t u1 = pa_unit_start(cta + 1, units, ctas);
       // segments are cut where the range ends, or (short requests) belong to the range they begin in as a whole
@@ -474,10 +475,18 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         }
         __syncwarp();
         if (s.n == 0) break;
+        const int buf = seg % kQBufs;
+        if (!pa_query_columns<kCE, kHalf, kMods>(a, s, sQ + buf * F::kQBytes, cols[buf], [&] {
+              return seg < kQBufs || wait_warp(&q_empty[buf], (seg / kQBufs - 1) & 1, err, kErrMmaTimeout, kSegPolls);
+            }))
+          break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[buf]);
       }
     }
   } else {
-    regs_inc<kRegsSoft>();
+    regs_inc<F::kRegsSoft>();
     // ---------------------------------------------------------------- softmax and outputs: one key a thread
     const int wg = (warp - kSoftWarp0) >> 2, bar = 1 + wg;
     const int quarter = warp & 3, row = 32 * quarter + lane;
@@ -486,7 +495,9 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
     constexpr bool kHold = kCE == 8;                   // references and factors stay in registers
     float* const ref_m = refs[wg][0];                  // as -m
     float* const ref_e = refs[wg][1];                  // 2^(m - mv)
-    uint32_t i0 = 0;                                   // the CTA's tiles before this segment
+    uint32_t i0 = 0, own = 0;                          // the CTA's tiles before this segment; this warpgroup's so far: tile kWgs * own + wg is next
+    int vst = wg;                                      // V's stage of that tile (kVStages > kWgs), and its turn
+    uint32_t v_turn = 0;
     for (int seg = 0;; ++seg) {
       const int sb_ = seg % kSegBufs, qb = seg % kQBufs;
       if (!wait_warp(&seg_full[sb_], (seg / kSegBufs) & 1, err, kErrMmaTimeout)) break;
@@ -495,7 +506,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       if (lane == 0) mbar_arrive(&seg_empty[sb_]);
       if (s.n == 0) break;
       if (!wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout)) break;
-      const uint32_t acc = tmem + lanes + kColO + 2 * kN * (seg & 1);
+      const uint32_t acc = tmem + lanes + kColO + kWgs * kN * (seg & 1);
       const PaColumns& cm = cols[qb];
       const int min_limit = cm.min_limit;
       const int live = min(s.rows * a.group - s.cg * kCE, kCE);   // columns in use
@@ -510,10 +521,10 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       }
       bool ok = true, fresh = true;
       // One tile, with kNC columns in use (8, 16 or 32): a body of its own each, chosen once a tile
-      auto tile = [&](auto columns, auto with_masks, uint32_t i, int vst, int key0) {
+      auto tile = [&](auto columns, auto with_masks, uint32_t n, int vst, int key0) {
         constexpr int kNC = decltype(columns)::value;
         constexpr bool kMasked = decltype(with_masks)::value;
-        const uint32_t sb = i % kSBufs, pn = 2 * wg + ((i >> 1) & 1);
+        const uint32_t sb = wg + kWgs * (n & 1), pn = 2 * wg + (n & 1);
         const int j = key0 + row;
         const bool exists = !kMasked || (j < s.len && !((sbad[vst] >> (row >> a.log2_page)) & 1u));
         const float vs = exists ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sScaleV + vst * kVScales)[row]) : 0.f;
@@ -615,8 +626,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
           }
           if (!fresh) {
             // the accumulator is settled when the tile before has been added
-            const uint32_t before = i - 2;
-            ok = wait_warp(&pv_done[2 * wg + ((before >> 1) & 1)], (before >> 2) & 1, err, kErrMmaTimeout) && ok;
+            ok = wait_warp(&pv_done[2 * wg + ((n - 1) & 1)], ((n - 1) >> 1) & 1, err, kErrMmaTimeout) && ok;
 #pragma unroll
             for (int c = 0; c < kNC / 2; ++c)
               l2[c] = mul2(l2[c], pack2(__shfl_sync(0xffffffffu, al, 2 * c), __shfl_sync(0xffffffffu, al, 2 * c + 1)));
@@ -649,7 +659,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
           }
         };
         // P's buffer is free once the tile that it held last has been added
-        if (i >= 4) ok = wait_warp(&pv_done[pn], ((i >> 2) - 1) & 1, err, kErrMmaTimeout);
+        if (n >= 2) ok = wait_warp(&pv_done[pn], ((n >> 1) - 1) & 1, err, kErrMmaTimeout);
         if (!ok) return;
         uint8_t* const prow = sP + pn * F::kPBytes + row * kN;
         const uint64_t vs2 = pack2(vs * kPOne, vs * kPOne);
@@ -740,39 +750,38 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         if (lane == 0) mbar_arrive(&s_empty[sb]);
       };
       {
-        int t = (wg + i0) & 1;                         // this warpgroup's first tile of the segment
-        uint32_t i = i0 + t;
-        int vst = i % kVStages;
-        uint32_t v_turn = (i / kVStages) & 1;
-        for (; t < s.n && ok; t += 2, i += 2) {
+        for (; ok; ++own) {
+          const int t = (int)(kWgs * own + wg - i0);
+          if (t >= s.n) break;
+          const uint32_t n = own;
           const int key0 = s.template tile_at<kMods>(t) * kTok;
-          ok = wait_warp(&v_full[vst], v_turn, err, kErrTmaTimeout) && wait_warp(&s_full[i % kSBufs], (i / kSBufs) & 1, err, kErrMmaTimeout);
+          ok = wait_warp(&v_full[vst], v_turn, err, kErrTmaTimeout) && wait_warp(&s_full[wg + kWgs * (n & 1)], (n >> 1) & 1, err, kErrMmaTimeout);
           if (!ok) break;
           tc_fence_after();
           using std::integral_constant;
           const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[vst] != 0);
           const int st = vst;
-          vst += 2;
+          vst += kWgs;
           if (vst >= kVStages) {
             vst -= kVStages;
             v_turn ^= 1;
           }
           if constexpr (kCE > 16) {
             if (live > 16) {
-              if (masked) tile(integral_constant<int, 32>{}, std::true_type{}, i, st, key0);
-              else tile(integral_constant<int, 32>{}, std::false_type{}, i, st, key0);
+              if (masked) tile(integral_constant<int, 32>{}, std::true_type{}, n, st, key0);
+              else tile(integral_constant<int, 32>{}, std::false_type{}, n, st, key0);
               continue;
             }
           }
           if constexpr (kCE > 8) {
             if (live > 8) {
-              if (masked) tile(integral_constant<int, 16>{}, std::true_type{}, i, st, key0);
-              else tile(integral_constant<int, 16>{}, std::false_type{}, i, st, key0);
+              if (masked) tile(integral_constant<int, 16>{}, std::true_type{}, n, st, key0);
+              else tile(integral_constant<int, 16>{}, std::false_type{}, n, st, key0);
               continue;
             }
           }
-          if (masked) tile(integral_constant<int, 8>{}, std::true_type{}, i, st, key0);
-          else tile(integral_constant<int, 8>{}, std::false_type{}, i, st, key0);
+          if (masked) tile(integral_constant<int, 8>{}, std::true_type{}, n, st, key0);
+          else tile(integral_constant<int, 8>{}, std::false_type{}, n, st, key0);
         }
       }
       if (!ok) break;
@@ -803,7 +812,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&stat_full[qb]);
-      if ((seg & 1) != wg) {
+      if ((seg & 1) != wg) {                           // (the first two write outputs in turn)
         if (lane == 0) mbar_arrive(&q_empty[qb]);
         group_sync(bar, 128);                          // the next segment's maxima go where these sums were read
         continue;
@@ -815,15 +824,21 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       const int slot = s.tile > 0 ? 2 * cta : 2 * cta + 1;
       if (quarter == 0 && lane < live) {
         // out = sum_w f_w O_w, f_w = 2^(mv_w - M) / (64 L), in an order that keeps V's extreme scales finite (see paged_attention.cu)
-        const float ma = stat[qb][0][0][lane], mb = stat[qb][1][0][lane], la = stat[qb][0][2][lane], lb = stat[qb][1][2][lane];
-        const bool has_a = la > 0.f || la != la, has_b = lb > 0.f || lb != lb;   // NaN counts as seen
-        const float M = fmaxf(ma, mb);
-        const float L = (has_a ? la * ex2_approx(ma - M) : 0.f) + (has_b ? lb * ex2_approx(mb - M) : 0.f);
-        fin[wg][0][lane] = has_a ? ex2_approx(0.5f * (stat[qb][0][1][lane] - M)) : 0.f;
-        fin[wg][1][lane] = has_b ? ex2_approx(0.5f * (stat[qb][1][1][lane] - M)) : 0.f;
-        stat[qb][0][2][lane] = 1.f / L / kPOne;        // (la has been read)
+        float M = -INFINITY, L = 0.f;
+        bool any = false;
+#pragma unroll
+        for (int w = 0; w < kWgs; ++w) M = fmaxf(M, stat[qb][w][0][lane]);
+#pragma unroll
+        for (int w = 0; w < kWgs; ++w) {
+          const float lw = stat[qb][w][2][lane];
+          const bool has = lw > 0.f || lw != lw;           // NaN counts as seen
+          if (has) L += lw * ex2_approx(stat[qb][w][0][lane] - M);
+          fin[wg][w][lane] = has ? ex2_approx(0.5f * (stat[qb][w][1][lane] - M)) : 0.f;
+          any |= has;
+        }
+        stat[qb][0][2][lane] = 1.f / L / kPOne;        // (it has been read)
         if (whole) {
-          if (a.lse) a.lse[cm.at[lane]] = has_a || has_b ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+          if (a.lse) a.lse[cm.at[lane]] = any ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
         } else {
           float* ml = a.part_ml + ((int64_t)slot * kPagedAttnColumns + lane) * 2;
           ml[0] = M;
@@ -837,20 +852,24 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < live; c0 += 8) {
-        uint32_t r[32];
-        tmem_ld_cols8(acc + c0, r);
-        tmem_ld_cols8(acc + kHalf + c0, r + 8);
-        tmem_ld_cols8(acc + kN + c0, r + 16);
-        tmem_ld_cols8(acc + kN + kHalf + c0, r + 24);
+        uint32_t r[16 * kWgs];
+#pragma unroll
+        for (int w = 0; w < kWgs; ++w) {
+          tmem_ld_cols8(acc + kN * w + c0, r + 16 * w);
+          tmem_ld_cols8(acc + kN * w + kHalf + c0, r + 16 * w + 8);
+        }
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           if (c0 + c >= live) break;
-          const float fa = fin[wg][0][c0 + c], fb = fin[wg][1][c0 + c], over = stat[qb][0][2][c0 + c];
+          const float over = stat[qb][0][2][c0 + c];
           // an accumulator without a seen key holds nothing of this column (or was never written)
           float v = 0.f;
-          if (fa != 0.f) v = fmaf(__uint_as_float(r[8 + c]), 0.0625f, __uint_as_float(r[c])) * over * fa * fa;
-          if (fb != 0.f) v = fmaf(fmaf(__uint_as_float(r[24 + c]), 0.0625f, __uint_as_float(r[16 + c])) * over * fb, fb, v);
+#pragma unroll
+          for (int w = 0; w < kWgs; ++w) {
+            const float f = fin[wg][w][c0 + c];
+            if (f != 0.f) v = fmaf(fmaf(__uint_as_float(r[16 * w + 8 + c]), 0.0625f, __uint_as_float(r[16 * w + c])) * over * f, f, v);
+          }
           if (whole) a.out[(int64_t)cm.at[c0 + c] * kKvDim + row] = __float2bfloat16_rn(v);
           else a.part_o[((int64_t)slot * kPagedAttnColumns + c0 + c) * kKvDim + row] = v;
         }
@@ -899,7 +918,7 @@ cudaError_t launch_columns4(const PagedAttnArgs& a, const CUtensorMap& k_map, co
   auto kernel = mods == kPaPlain     ? kv4_attention_kernel<kCE, kPaPlain>
                 : mods == kPaCapBias ? kv4_attention_kernel<kCE, kPaCapBias>
                                      : kv4_attention_kernel<kCE, kPaLargeCap>;
-  e = launch_pdl(kernel, dim3(ctas), dim3(p4::kThreads), smem, s, k_map, v_map, a, shared_keys);
+  e = launch_pdl(kernel, dim3(ctas), dim3(p4::Form<kCE>::kThreads), smem, s, k_map, v_map, a, shared_keys);
   count_launches(1);
   if (e == cudaSuccess && ctas > 1 && !a.whole && join) e = launch_paged_join(a, ctas, kCE, s);
   return e;
