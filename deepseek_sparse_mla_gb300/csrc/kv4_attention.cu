@@ -57,13 +57,14 @@ struct Form {
   static constexpr int kWgs = 2;      // softmax warpgroups
   static constexpr int kThreads = 256 + 128 * kWgs;
   static constexpr uint32_t kRegsLow = kWgs == 3 ? 72 : 80, kRegsSoft = kWgs == 3 ? 112 : 176;   // 2 * 72 + 3 * 112 = 5 * 96, 2 * 80 + 2 * 176 = 4 * 128: the launch's
-  static constexpr int kSBufs = 2 * kWgs;             // two a warpgroup: one is kept until its tile is known to be done
   static constexpr bool kApart = kCE <= 16;           // Q's two terms have columns of their own
   static constexpr int kColsS = kApart ? kN : kHalf;  // TMEM columns of a tile's scores
+  // Rings: K's tiles and their scores, V's tiles and their probabilities.  One barrier says that a product has been computed,
+  // which frees what it read and hands over what it wrote.
   static constexpr int kKStages = kCE <= 16 ? 5 : 4, kVStages = kCE <= 16 ? 6 : 5;
   static constexpr int kQBytes = kN * kKvDim, kPBytes = kTok * kN;
-  static constexpr int kSmem = (kKStages + kVStages) * kTileBytes + kQBufs * kQBytes + 2 * kWgs * kPBytes + kKStages * kKScales + kVStages * kVScales + 1024;
-  static_assert(kSBufs * kColsS <= (int)kColScales && kColScales + 4 * kSBufs <= kColQScales && kColO + 2 * kWgs * kN <= kTmemCols, "TMEM columns");
+  static constexpr int kSmem = (kKStages + kVStages) * kTileBytes + kQBufs * kQBytes + kVStages * kPBytes + kKStages * kKScales + kVStages * kVScales + 1024;
+  static_assert(kKStages * kColsS <= (int)kColScales && kColScales + 4 * kKStages <= kColQScales && kColO + 2 * kWgs * kN <= kTmemCols, "TMEM columns");
 };
 
 // A run of tiles of one segment, as the segment warp leaves it for the others
@@ -124,18 +125,18 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
   using namespace p4;
   using F = Form<kCE>;
   constexpr bool kMods = kModSet != kPaPlain;
-  constexpr int kThreads = F::kThreads, kWgs = F::kWgs, kSBufs = F::kSBufs;
+  constexpr int kThreads = F::kThreads, kWgs = F::kWgs;
   constexpr int kHalf = F::kHalf, kN = F::kN, kKStages = F::kKStages, kVStages = F::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sK = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sV = sK + kKStages * kTileBytes;
   uint8_t* const sQ = sV + kVStages * kTileBytes;
-  uint8_t* const sP = sQ + kQBufs * F::kQBytes;            // two buffers a warpgroup
-  uint8_t* const sScaleK = sP + 2 * kWgs * F::kPBytes;
+  uint8_t* const sP = sQ + kQBufs * F::kQBytes;
+  uint8_t* const sScaleK = sP + kVStages * F::kPBytes;
   uint8_t* const sScaleV = sScaleK + kKStages * kKScales;
 
-  __shared__ uint64_t k_full[kKStages], k_empty[kKStages], sf_full[kKStages], v_full[kVStages], v_empty[kVStages];
-  __shared__ uint64_t s_full[kSBufs], s_empty[kSBufs], p_full[2 * kWgs], pv_done[2 * kWgs];
+  __shared__ uint64_t k_full[kKStages], sf_full[kKStages], s_full[kKStages], s_empty[kKStages];
+  __shared__ uint64_t v_full[kVStages], p_full[kVStages], pv_done[kVStages];
   __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[2], o_empty[2], mma_done;
   __shared__ uint64_t seg_full[kSegBufs], seg_empty[kSegBufs];
   __shared__ Seg segs[kSegBufs];
@@ -152,18 +153,14 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
       mbar_init(&sf_full[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
-    for (int i = 0; i < 2 * kWgs; ++i) {
       mbar_init(&p_full[i], 1);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&o_full[i], 1);
@@ -259,7 +256,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       constexpr bool kV = decltype(of_v)::value;
       constexpr int kRing = kV ? kVStages : kKStages, kScale = kV ? 2 : kKv4Blocks, kWay = kMods ? -1 : 1;   // scale bytes of a token
       uint64_t* const full = kV ? v_full : k_full;
-      uint64_t* const empty = kV ? v_empty : k_empty;
+      uint64_t* const empty = kV ? pv_done : s_full;
       const uint8_t* const scales = kV ? reinterpret_cast<const uint8_t*>(a.v_scales4) : a.k_scales4;
       const int mine = lane & 7;
       const bool codes = lane < 8, used = mine < ppt && lane < 16;
@@ -315,8 +312,9 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
     } else if (warp == kOrderWarp) {
       // ---------------------------------------------------------------- K's scales as tcgen05.cp takes them
       // Those of keys l, l + 32, l + 64 and l + 96 go into the l-th 16 bytes.
+      // The arrival on sf_full also says that the place of the tile's scores is free, so that the product's issuer waits once.
       Ring<kKStages> r;
-      bool ok = true;
+      bool ok = true, first = true;
       for (Seg s; ok && next_segment(s);)
         for (int t = 0; t < s.n; ++t) {
           ok = wait_warp(&k_full[r.st], r.turn, err, kErrTmaTimeout);
@@ -328,9 +326,12 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
           __syncwarp();
           reinterpret_cast<uint4*>(raw)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
           fence_proxy_async_smem();
+          ok = first || wait_warp(&s_empty[r.st], r.turn ^ 1, err, kErrMmaTimeout);
+          if (!ok) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sf_full[r.st]);
           r.next();
+          if (r.st == 0) first = false;
         }
     } else if (warp == kScoreWarp) {
       // ---------------------------------------------------------------- products of the scores
@@ -340,20 +341,18 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       const uint64_t d_k = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B), d_q = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
       const uint64_t d_sf = smem_desc(smem_u32(sScaleK), 16, 128, kSwizzleNone);
       Ring<kKStages> r;
-      Ring<kSBufs> sr;
-      bool ok = true, first = true;
+      bool ok = true;
       for (Seg s; ok && next_segment(s);) {
         const int qb = seg % kQBufs;
         ok = wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout);
         const uint64_t q = d_q + (uint64_t)((qb * F::kQBytes) >> 4);
         for (int t = 0; t < s.n && ok; ++t) {
           ok = mbar_spin_warp(&sf_full[r.st], r.turn, err, kErrTmaTimeout);
-          if (ok && !first) ok = mbar_spin_warp(&s_empty[sr.st], sr.turn ^ 1, err, kErrMmaTimeout);
           if (!ok) break;
           tc_fence_after();
           const uint64_t k = d_k + (uint64_t)((r.st * kTileBytes) >> 4);
           if (leader) {
-            const uint32_t sf = tmem + kColScales + 4 * sr.st, to = tmem + F::kColsS * sr.st;
+            const uint32_t sf = tmem + kColScales + 4 * r.st, to = tmem + F::kColsS * r.st;
             tmem_cp_scales(sf, d_sf + (uint64_t)((r.st * kKScales) >> 4));
 #pragma unroll
             for (int kk = 0; kk < (F::kApart ? 1 : 2) * kKvDim / 32; ++kk) {   // (in the same columns: hi, then lo)
@@ -361,14 +360,11 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
               mma_ss_mx(to, k + 2 * block, q + 2 * block + (uint64_t)((term * kHalf * kKvDim) >> 4), id_qk | block << 29 | term << 4, sf,
                         tmem + kColQScales, kk > 0);
             }
-            mma_commit(&s_full[sr.st]);
-            mma_commit(&k_empty[r.st]);
+            mma_commit(&s_full[r.st]);
             if (t + 1 == s.n) mma_commit(&q_empty[qb]);
           }
           __syncwarp();
           r.next();
-          sr.next();
-          if (sr.st == 0) first = false;
         }
       }
       // every MMA issued here has finished before TMEM is released
@@ -381,17 +377,16 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       const uint64_t d_v = smem_desc(smem_u32(sV), 16, 1024, kSwizzle128B);
       const uint64_t d_p = smem_desc(smem_u32(sP), 16, 8 * kN, kN == 64 ? kSwizzle64B : kSwizzle32B);
       Ring<kVStages> r;
-      uint32_t wg = 0, n = 0;                          // whose tile it is, and which of its own
+      uint32_t wg = 0;                                 // whose tile it is
       bool ok = true;
       for (Seg s; ok && next_segment(s);) {
         uint32_t fresh = (1u << kWgs) - 1;                            // accumulators of the segment without a product yet
         if (seg >= 2) ok = wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout);
         for (int t = 0; t < s.n; ++t) {
-          const uint32_t pn = 2 * wg + (n & 1);
-          ok = ok && mbar_spin_warp(&p_full[pn], (n >> 1) & 1, err, kErrMmaTimeout);
+          ok = ok && mbar_spin_warp(&p_full[r.st], r.turn, err, kErrMmaTimeout);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t v = d_v + (uint64_t)((r.st * kTileBytes) >> 4), p = d_p + (uint64_t)((pn * F::kPBytes) >> 4);
+          const uint64_t v = d_v + (uint64_t)((r.st * kTileBytes) >> 4), p = d_p + (uint64_t)((r.st * F::kPBytes) >> 4);
           const uint32_t to = tmem + kColO + kWgs * kN * (seg & 1) + kN * wg;
           const bool add = !((fresh >> wg) & 1u);
           fresh &= ~(1u << wg);
@@ -399,16 +394,12 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kTok / 32; ++kk)
               mma_ss_f8(to, v + (uint64_t)((kk * 32 * kKvDim) >> 4), p + (uint64_t)((kk * 32 * kN) >> 4), id_pv, add || kk > 0);
-            mma_commit(&v_empty[r.st]);
-            mma_commit(&pv_done[pn]);
+            mma_commit(&pv_done[r.st]);
             if (t + 1 == s.n) mma_commit(&o_full[seg & 1]);
           }
           __syncwarp();
           r.next();
-          if (++wg == kWgs) {
-            wg = 0;
-            ++n;
-          }
+          if (++wg == kWgs) wg = 0;
         }
       }
       if (leader) mma_commit(&mma_done);
@@ -495,9 +486,9 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
     constexpr bool kHold = kCE == 8;                   // references and factors stay in registers
     float* const ref_m = refs[wg][0];                  // as -m
     float* const ref_e = refs[wg][1];                  // 2^(m - mv)
-    uint32_t i0 = 0, own = 0;                          // the CTA's tiles before this segment; this warpgroup's so far: tile kWgs * own + wg is next
-    int vst = wg;                                      // V's stage of that tile (kVStages > kWgs), and its turn
-    uint32_t v_turn = 0;
+    int i0 = 0, i = wg;                                // the CTA's tiles before this segment; this warpgroup's next one
+    int kst = wg, vst = wg;                            // its places in the rings (longer than kWgs), and their turns
+    uint32_t k_turn = 0, v_turn = 0;
     for (int seg = 0;; ++seg) {
       const int sb_ = seg % kSegBufs, qb = seg % kQBufs;
       if (!wait_warp(&seg_full[sb_], (seg / kSegBufs) & 1, err, kErrMmaTimeout)) break;
@@ -521,14 +512,13 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       }
       bool ok = true, fresh = true;
       // One tile, with kNC columns in use (8, 16 or 32): a body of its own each, chosen once a tile
-      auto tile = [&](auto columns, auto with_masks, uint32_t n, int vst, int key0) {
+      auto tile = [&](auto columns, auto with_masks, int key0) {
         constexpr int kNC = decltype(columns)::value;
         constexpr bool kMasked = decltype(with_masks)::value;
-        const uint32_t sb = wg + kWgs * (n & 1), pn = 2 * wg + (n & 1);
         const int j = key0 + row;
         const bool exists = !kMasked || (j < s.len && !((sbad[vst] >> (row >> a.log2_page)) & 1u));
         const float vs = exists ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sScaleV + vst * kVScales)[row]) : 0.f;
-        const uint32_t from = tmem + lanes + F::kColsS * sb;
+        const uint32_t from = tmem + lanes + F::kColsS * kst;
         const float in = kMods && a.cap_log2 > 0.f ? 2.f * 1.4426950408889634f / a.cap_log2 : 0.f;
         // distances in integers from the request's first row, exact up to 2^24 (see paged_attention.cu)
         const float ahead = kMods ? (float)(j - cm.start) : 0.f;
@@ -602,7 +592,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
               }
             }
           }
-          float* const wmax_v = reinterpret_cast<float*>(sP + pn * F::kPBytes);   // [4][kCE], before the tile's P is there
+          float* const wmax_v = reinterpret_cast<float*>(sP + vst * F::kPBytes);   // [4][kCE], before the tile's P is there
           if (lane < kCE) {
             wmax[wg][quarter][lane] = mine;
             wmax_v[quarter * kCE + lane] = mine_v;
@@ -626,7 +616,8 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
           }
           if (!fresh) {
             // the accumulator is settled when the tile before has been added
-            ok = wait_warp(&pv_done[2 * wg + ((n - 1) & 1)], ((n - 1) >> 1) & 1, err, kErrMmaTimeout) && ok;
+            const bool back = vst < kWgs;
+            ok = wait_warp(&pv_done[back ? vst + kVStages - kWgs : vst - kWgs], back ? v_turn ^ 1 : v_turn, err, kErrMmaTimeout) && ok;
 #pragma unroll
             for (int c = 0; c < kNC / 2; ++c)
               l2[c] = mul2(l2[c], pack2(__shfl_sync(0xffffffffu, al, 2 * c), __shfl_sync(0xffffffffu, al, 2 * c + 1)));
@@ -658,10 +649,8 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
             }
           }
         };
-        // P's buffer is free once the tile that it held last has been added
-        if (n >= 2) ok = wait_warp(&pv_done[pn], ((n >> 1) - 1) & 1, err, kErrMmaTimeout);
-        if (!ok) return;
-        uint8_t* const prow = sP + pn * F::kPBytes + row * kN;
+        // (P's place is free: V's tile was loaded once the product that read both before had been computed)
+        uint8_t* const prow = sP + vst * F::kPBytes + row * kN;
         const uint64_t vs2 = pack2(vs * kPOne, vs * kPOne);
         uint64_t p[kNC / 2];
         bool raised = fresh;
@@ -746,42 +735,39 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kNC / 2; ++c) l2[c] = add2(l2[c], p[c]);
         fresh = false;
-        if (row == 0) mbar_arrive(&p_full[pn]);
-        if (lane == 0) mbar_arrive(&s_empty[sb]);
+        if (row == 0) mbar_arrive(&p_full[vst]);
+        if (lane == 0) mbar_arrive(&s_empty[kst]);
       };
-      {
-        for (; ok; ++own) {
-          const int t = (int)(kWgs * own + wg - i0);
-          if (t >= s.n) break;
-          const uint32_t n = own;
-          const int key0 = s.template tile_at<kMods>(t) * kTok;
-          ok = wait_warp(&v_full[vst], v_turn, err, kErrTmaTimeout) && wait_warp(&s_full[wg + kWgs * (n & 1)], (n >> 1) & 1, err, kErrMmaTimeout);
-          if (!ok) break;
-          tc_fence_after();
-          using std::integral_constant;
-          const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[vst] != 0);
-          const int st = vst;
-          vst += kWgs;
-          if (vst >= kVStages) {
-            vst -= kVStages;
-            v_turn ^= 1;
-          }
-          if constexpr (kCE > 16) {
-            if (live > 16) {
-              if (masked) tile(integral_constant<int, 32>{}, std::true_type{}, n, st, key0);
-              else tile(integral_constant<int, 32>{}, std::false_type{}, n, st, key0);
-              continue;
-            }
-          }
-          if constexpr (kCE > 8) {
-            if (live > 8) {
-              if (masked) tile(integral_constant<int, 16>{}, std::true_type{}, n, st, key0);
-              else tile(integral_constant<int, 16>{}, std::false_type{}, n, st, key0);
-              continue;
-            }
-          }
-          if (masked) tile(integral_constant<int, 8>{}, std::true_type{}, n, st, key0);
-          else tile(integral_constant<int, 8>{}, std::false_type{}, n, st, key0);
+      for (; ok && i - i0 < s.n; i += kWgs) {
+        const int key0 = s.template tile_at<kMods>(i - i0) * kTok;
+        ok = wait_warp(&v_full[vst], v_turn, err, kErrTmaTimeout) && wait_warp(&s_full[kst], k_turn, err, kErrMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        using std::integral_constant;
+        const bool masked = __any_sync(0xffffffffu, key0 + kTok > min_limit || sbad[vst] != 0);
+        auto with_columns = [&](auto columns) {
+          if (masked) tile(columns, std::true_type{}, key0);
+          else tile(columns, std::false_type{}, key0);
+        };
+        if constexpr (kCE == 32) {
+          if (live > 16) with_columns(integral_constant<int, 32>{});
+          else if (live > 8) with_columns(integral_constant<int, 16>{});
+          else with_columns(integral_constant<int, 8>{});
+        } else if constexpr (kCE == 16) {
+          if (live > 8) with_columns(integral_constant<int, 16>{});
+          else with_columns(integral_constant<int, 8>{});
+        } else {
+          with_columns(integral_constant<int, 8>{});
+        }
+        kst += kWgs;
+        if (kst >= kKStages) {
+          kst -= kKStages;
+          k_turn ^= 1;
+        }
+        vst += kWgs;
+        if (vst >= kVStages) {
+          vst -= kVStages;
+          v_turn ^= 1;
         }
       }
       if (!ok) break;
