@@ -40,7 +40,11 @@ constexpr int kTok = kPaTok;                    // keys per tile
 constexpr int kTileBytes = kTok * kKvDim;       // of K or V in shared memory: 16-byte units, half used
 constexpr int kKScales = kTok * kKv4Blocks, kVScales = kTok * 2;   // bytes of a tile's scales
 constexpr int kLoadKWarp = 0, kScoreWarp = 1, kLoadVWarp = 2, kOutWarp = 3, kOrderWarp = 5, kQueryWarp = 7, kSoftWarp0 = 8;   // loaders: 0 and 4, 2 and 6
-constexpr int kQBufs = 3, kSegBufs = 4;
+constexpr int kQBufs = 3, kSegBufs = 4, kOBufs = 2;   // segments with queries, with a description and with accumulators
+// Three softmax warpgroups instead of two: 480 us instead of 476 for 64 requests of 16K-128K, and with 32 columns (where TMEM then holds one
+// segment's accumulators) 291 instead of 301 for the verify rows at 240K but 92 instead of 90 for the mixed capped batch.
+constexpr int kWgs = 2, kThreads = 256 + 128 * kWgs;
+constexpr uint32_t kRegsLow = 80, kRegsSoft = 176;   // 2 * 80 + 2 * 176 = 4 * 128: the launch's
 constexpr uint32_t kTmemCols = 512, kColScales = 192, kColQScales = 216, kColO = 256;
 constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
@@ -54,9 +58,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32
 template <int kCE>
 struct Form {
   static constexpr int kHalf = kCE < 16 ? 16 : kCE, kN = 2 * kHalf;   // columns of the hi terms, and of both
-  static constexpr int kWgs = 2;      // softmax warpgroups
-  static constexpr int kThreads = 256 + 128 * kWgs;
-  static constexpr uint32_t kRegsLow = kWgs == 3 ? 72 : 80, kRegsSoft = kWgs == 3 ? 112 : 176;   // 2 * 72 + 3 * 112 = 5 * 96, 2 * 80 + 2 * 176 = 4 * 128: the launch's
   static constexpr bool kApart = kCE <= 16;           // Q's two terms have columns of their own
   static constexpr int kColsS = kApart ? kN : kHalf;  // TMEM columns of a tile's scores
   // Rings: K's tiles and their scores, V's tiles and their probabilities.  One barrier says that a product has been computed,
@@ -64,7 +65,7 @@ struct Form {
   static constexpr int kKStages = kCE <= 16 ? 5 : 4, kVStages = kCE <= 16 ? 6 : 5;
   static constexpr int kQBytes = kN * kKvDim, kPBytes = kTok * kN;
   static constexpr int kSmem = (kKStages + kVStages) * kTileBytes + kQBufs * kQBytes + kVStages * kPBytes + kKStages * kKScales + kVStages * kVScales + 1024;
-  static_assert(kKStages * kColsS <= (int)kColScales && kColScales + 4 * kKStages <= kColQScales && kColO + 2 * kWgs * kN <= kTmemCols, "TMEM columns");
+  static_assert(kKStages * kColsS <= (int)kColScales && kColScales + 4 * kKStages <= kColQScales && kColO + kOBufs * kWgs * kN <= kTmemCols, "TMEM columns");
 };
 
 // A run of tiles of one segment, as the segment warp leaves it for the others
@@ -119,13 +120,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 
 // kCE columns (8, 16 or 32); kModSet: score cap and distance bias compiled in
 template <int kCE, PaMods kModSet>
-__global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
+__global__ void __launch_bounds__(p4::kThreads, 1)
     kv4_attention_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const __grid_constant__ PagedAttnArgs a, int shared_keys) {
   using namespace p4;
   using F = Form<kCE>;
   constexpr bool kMods = kModSet != kPaPlain;
-  constexpr int kThreads = F::kThreads, kWgs = F::kWgs;
   constexpr int kHalf = F::kHalf, kN = F::kN, kKStages = F::kKStages, kVStages = F::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sK = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
 
   __shared__ uint64_t k_full[kKStages], sf_full[kKStages], s_full[kKStages], s_empty[kKStages];
   __shared__ uint64_t v_full[kVStages], p_full[kVStages], pv_done[kVStages];
-  __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[2], o_empty[2], mma_done;
+  __shared__ uint64_t q_full[kQBufs], q_empty[kQBufs], stat_full[kQBufs], o_full[kOBufs], o_empty[kOBufs], mma_done;
   __shared__ uint64_t seg_full[kSegBufs], seg_empty[kSegBufs];
   __shared__ Seg segs[kSegBufs];
   __shared__ uint32_t sbad[kVStages];                  // pages of a tile that are not there
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       mbar_init(&p_full[i], 1);
       mbar_init(&pv_done[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kOBufs; ++i) {
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 4);
     }
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
   uint32_t* const err = &bits_all;                     // this CTA's status bits, stored at the end
 
   if (warp < kSoftWarp0) {
-    regs_dec<F::kRegsLow>();
+    regs_dec<kRegsLow>();
     const int lp = a.log2_page, ppt = kTok >> lp;
     // one segment after the other: its place in the ring, and a copy of what it is
     int seg = -1;
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
         ok = wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout);
         const uint64_t q = d_q + (uint64_t)((qb * F::kQBytes) >> 4);
         for (int t = 0; t < s.n && ok; ++t) {
-          ok = mbar_spin_warp(&sf_full[r.st], r.turn, err, kErrTmaTimeout);
+          ok = wait_warp(&sf_full[r.st], r.turn, err, kErrTmaTimeout);
           if (!ok) break;
           tc_fence_after();
           const uint64_t k = d_k + (uint64_t)((r.st * kTileBytes) >> 4);
@@ -381,13 +381,13 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       bool ok = true;
       for (Seg s; ok && next_segment(s);) {
         uint32_t fresh = (1u << kWgs) - 1;                            // accumulators of the segment without a product yet
-        if (seg >= 2) ok = wait_warp(&o_empty[seg & 1], ((seg >> 1) - 1) & 1, err, kErrMmaTimeout);
+        if (seg >= kOBufs) ok = wait_warp(&o_empty[seg % kOBufs], (seg / kOBufs - 1) & 1, err, kErrMmaTimeout);
         for (int t = 0; t < s.n; ++t) {
-          ok = ok && mbar_spin_warp(&p_full[r.st], r.turn, err, kErrMmaTimeout);
+          ok = ok && wait_warp(&p_full[r.st], r.turn, err, kErrMmaTimeout);
           if (!ok) break;
           tc_fence_after();
           const uint64_t v = d_v + (uint64_t)((r.st * kTileBytes) >> 4), p = d_p + (uint64_t)((r.st * F::kPBytes) >> 4);
-          const uint32_t to = tmem + kColO + kWgs * kN * (seg & 1) + kN * wg;
+          const uint32_t to = tmem + kColO + kWgs * kN * (seg % kOBufs) + kN * wg;
           const bool add = !((fresh >> wg) & 1u);
           fresh &= ~(1u << wg);
           if (leader) {
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
             for (int kk = 0; kk < kTok / 32; ++kk)
               mma_ss_f8(to, v + (uint64_t)((kk * 32 * kKvDim) >> 4), p + (uint64_t)((kk * 32 * kN) >> 4), id_pv, add || kk > 0);
             mma_commit(&pv_done[r.st]);
-            if (t + 1 == s.n) mma_commit(&o_full[seg & 1]);
+            if (t + 1 == s.n) mma_commit(&o_full[seg % kOBufs]);
           }
           __syncwarp();
           r.next();
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       }
     }
   } else {
-    regs_inc<F::kRegsSoft>();
+    regs_inc<kRegsSoft>();
     // ---------------------------------------------------------------- softmax and outputs: one key a thread
     const int wg = (warp - kSoftWarp0) >> 2, bar = 1 + wg;
     const int quarter = warp & 3, row = 32 * quarter + lane;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       if (lane == 0) mbar_arrive(&seg_empty[sb_]);
       if (s.n == 0) break;
       if (!wait_warp(&q_full[qb], (seg / kQBufs) & 1, err, kErrMmaTimeout)) break;
-      const uint32_t acc = tmem + lanes + kColO + kWgs * kN * (seg & 1);
+      const uint32_t acc = tmem + lanes + kColO + kWgs * kN * (seg % kOBufs);
       const PaColumns& cm = cols[qb];
       const int min_limit = cm.min_limit;
       const int live = min(s.rows * a.group - s.cg * kCE, kCE);   // columns in use
@@ -658,14 +658,31 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
         for (;;) {
           // the probabilities, and their contributions in two e4m3 terms
           uint64_t all[kNC / 2];
-          products(all, 0);
+          uint32_t raw[kNC > 16 ? 16 : 1];
+          if constexpr (kNC > 16) {
+            uint64_t y16[8];
+            products(y16, 0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) all[c] = y16[c];
+            tmem_ld_cols8(from + 16, raw);
+            tmem_ld_cols8(from + 24, raw + 8);
+          } else {
+            products(all, 0);
+          }
           uint32_t hi[kHalf / 4], lo[kHalf / 4];
-          float p_top = 0.f;
+          int p_top = 0;                               // bits: p is not negative (a NaN counts as large, too)
           __half2 x_top = __float2half2_rn(0.f);
 #pragma unroll
           for (int c0 = 0; c0 < kHalf; c0 += 8) {
             hi[c0 / 4] = hi[c0 / 4 + 1] = lo[c0 / 4] = lo[c0 / 4 + 1] = 0;
             if (c0 >= kNC) continue;
+            if constexpr (kNC > 16) {
+              if (c0 == 16) {
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) all[8 + c] = pack2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1]));
+              }
+            }
             uint64_t* const y = all + c0 / 2;
             uint64_t mm[4], ee[4];
 #pragma unroll
@@ -699,7 +716,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
                 if (!seen(c0 + 2 * c + 1)) e.y = 0.f;
               }
               p[(c0 >> 1) + c] = pack2(e.x, e.y);
-              p_top = fmaxf(p_top, fmaxf(e.x, e.y));
+              p_top = __vimax3_s32(p_top, __float_as_int(e.x), __float_as_int(e.y));
               // in this order: 0 stays 0 whatever the scale of an unseen key ..
               float2 x = unpack2(mul2(mul2(p[(c0 >> 1) + c], ee[c]), vs2));
               if (kMasked) {                           // .. and of one that some columns do not see even NaN
@@ -728,7 +745,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
           fence_proxy_async_smem();
           tc_fence_before();
           const float x_most = fmaxf(__low2float(x_top), __high2float(x_top));
-          if (!group_or(bar, 128, !raised && (p_top >= kSlackP || x_most > kSlackP * kPOne))) break;
+          if (!group_or(bar, 128, !raised && (p_top >= __float_as_int(kSlackP) || x_most > kSlackP * kPOne))) break;
           raised = true;                               // the same in all four warps
           raise();
         }
@@ -834,7 +851,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       if (row == 0 && seg == 0)                        // for the join: this CTA's first piece
         reinterpret_cast<PaRecord*>(a.rec)[cta] = {units, s.tile, s.tiles, s.row0, pairs, s.cg * kCE, s.h};
       group_sync(bar, 128);
-      if (!wait_warp(&o_full[seg & 1], (seg >> 1) & 1, err, kErrMmaTimeout)) break;
+      if (!wait_warp(&o_full[seg % kOBufs], (seg / kOBufs) & 1, err, kErrMmaTimeout)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 0; c0 < live; c0 += 8) {
@@ -863,7 +880,7 @@ __global__ void __launch_bounds__(p4::Form<kCE>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&o_empty[seg & 1]);
+        mbar_arrive(&o_empty[seg % kOBufs]);
         mbar_arrive(&q_empty[qb]);
       }
     }
@@ -904,7 +921,7 @@ cudaError_t launch_columns4(const PagedAttnArgs& a, const CUtensorMap& k_map, co
   auto kernel = mods == kPaPlain     ? kv4_attention_kernel<kCE, kPaPlain>
                 : mods == kPaCapBias ? kv4_attention_kernel<kCE, kPaCapBias>
                                      : kv4_attention_kernel<kCE, kPaLargeCap>;
-  e = launch_pdl(kernel, dim3(ctas), dim3(p4::Form<kCE>::kThreads), smem, s, k_map, v_map, a, shared_keys);
+  e = launch_pdl(kernel, dim3(ctas), dim3(p4::kThreads), smem, s, k_map, v_map, a, shared_keys);
   count_launches(1);
   if (e == cudaSuccess && ctas > 1 && !a.whole && join) e = launch_paged_join(a, ctas, kCE, s);
   return e;
