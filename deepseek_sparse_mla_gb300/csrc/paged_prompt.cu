@@ -458,20 +458,14 @@ __device__ __forceinline__ void pp_widen_k4(const PpSeg* segs, uint64_t* seg_ful
       const int st = i % kKStages<true>, use = i / kKStages<true>, rb = i % kRawStages;
       if (!wait_warp(&raw.full[rb], (i / kRawStages) & 1, err, kErrTmaTimeout, kPolls)) return;
       const uint8_t* const from = raw.bytes + rb * kRawKBytes;
-      uint4 x[4];
-      uint32_t e[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        x[g] = reinterpret_cast<const uint4*>(from)[(32 * g + row0) * 4 + part];
-        e[g] = from[kTok * kKvDim / 2 + (32 * g + row0) * kKv4Blocks + part];
-      }
       if (use > 0 && !wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls)) return;
       uint8_t* const to = sK + st * kKBytes;
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < 4; ++g) {
+        const uint4 x = reinterpret_cast<const uint4*>(from)[(32 * g + row0) * 4 + part];
         uint32_t lo, hi;
-        pp_e5m2_table(e[g], lo, hi);
-        const uint2 a = pp_e5m2(x[g].x, lo, hi), b = pp_e5m2(x[g].y, lo, hi), c = pp_e5m2(x[g].z, lo, hi), d = pp_e5m2(x[g].w, lo, hi);
+        pp_e5m2_table(from[kTok * kKvDim / 2 + (32 * g + row0) * kKv4Blocks + part], lo, hi);
+        const uint2 a = pp_e5m2(x.x, lo, hi), b = pp_e5m2(x.y, lo, hi), c = pp_e5m2(x.z, lo, hi), d = pp_e5m2(x.w, lo, hi);
         *reinterpret_cast<uint4*>(to + sw128_offset(32 * g + row0, 2 * part)) = make_uint4(a.x, a.y, b.x, b.y);
         *reinterpret_cast<uint4*>(to + sw128_offset(32 * g + row0, 2 * part + 1)) = make_uint4(c.x, c.y, d.x, d.y);
       }
@@ -1127,6 +1121,27 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       int i = 0;
       int64_t u = u0;
       bool ok = true;
+      // 4 bits: a page a lane of the tile whose V is to be copied next (its first row, or -1), and how many there are
+      int v_row = -1;
+      uint32_t v_pages = 0;
+      // codes (lanes 0 .. ppt - 1, a page each) and scales (lanes 8 ..) of K or of V, of the rows from `row` on
+      auto copy_raw = [&](int row, uint32_t loads, uint8_t* to, uint64_t* full, const uint8_t* codes, const void* scales, int scale_bytes) {
+        if (lane == 0) mbar_arrive_expect_tx(full, loads * ((uint32_t)(kKvDim / 2 + scale_bytes) << lp));
+        __syncwarp();
+        if (lane < 16 && row >= 0) {
+          const int mine = lane & 7;
+          const uint32_t bytes = (uint32_t)(lane < 8 ? kKvDim / 2 : scale_bytes);
+          bulk_load_hint(to + (lane < 8 ? 0 : kTok * kKvDim / 2) + mine * (bytes << lp),
+                         (lane < 8 ? codes : static_cast<const uint8_t*>(scales)) + (int64_t)row * bytes, bytes << lp, full, policy);
+        }
+      };
+      // V lags a tile: it is widened later than K, and its place comes free later
+      auto copy_v = [&](int j) {
+        const int rb = j % kRawStages;
+        if (j >= kRawStages && !wait_warp(&rawv_empty[rb], (j / kRawStages - 1) & 1, err, kErrMmaTimeout, kPolls)) return false;
+        copy_raw(v_row, v_pages, sRaw + kRawStages * kRawKBytes + rb * kRawVBytes, &rawv_full[rb], v_codes, a.v_scales4, 2);
+        return true;
+      };
       for (int seg = 0;; ++seg) {
         if (seg >= kSegBufs) ok = wait_warp(&seg_empty[seg % kSegBufs], (seg / kSegBufs - 1) & 1, err, kErrMmaTimeout, kPolls);
         if (!ok) break;
@@ -1171,38 +1186,25 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           }
           const int st = i % kKStages, use = i / kKStages, rb = i % kRawStages;
           if (k4) {
-            if (i >= kRawStages)
-              ok = wait_warp(&rawk_empty[rb], (i / kRawStages - 1) & 1, err, kErrMmaTimeout, kPolls) &&
-                   wait_warp(&rawv_empty[rb], (i / kRawStages - 1) & 1, err, kErrMmaTimeout, kPolls);
+            if (i >= kRawStages) ok = wait_warp(&rawk_empty[rb], (i / kRawStages - 1) & 1, err, kErrMmaTimeout, kPolls);
           } else if (use > 0) {
             ok = wait_warp(&k_empty[st], (use - 1) & 1, err, kErrMmaTimeout, kPolls);
           }
           if (!ok) break;
           const int o = p0 & 31;
           if constexpr (k4) {
-            // lanes 0 .. ppt - 1 copy the pages' K codes, 8 .. their scales, 16 .. V's codes, 24 .. their scales
-            const int mine = lane & 7, what = lane >> 3;
+            const int mine = lane & 7;
             const int id = __shfl_sync(0xffffffffu, page, (o + mine) & 31);
             const int of_group = __shfl_sync(0xffffffffu, page, (o + ((16 * mine) >> lp)) & 31);
             const uint32_t bad = __ballot_sync(0xffffffffu, lane < 8 && of_group < 0);
-            const bool load = mine < ppt && id >= 0;
-            const uint32_t loads = __popc(__ballot_sync(0xffffffffu, lane < 8 && load));
-            if (lane == 0) {
-              sbad[i % kMetaBufs] = bad;
-              mbar_arrive_expect_tx(&rawk_full[rb], loads * ((kKvDim / 2 + kKv4Blocks) << lp));
-              mbar_arrive_expect_tx(&rawv_full[rb], loads * ((kKvDim / 2 + 2) << lp));
-            }
-            __syncwarp();
-            if (load) {
-              const int64_t row = ((int64_t)id * a.kv_heads + s.h) << lp;
-              uint8_t* const tk = sRaw + rb * kRawKBytes;
-              uint8_t* const tv = sRaw + kRawStages * kRawKBytes + rb * kRawVBytes;
-              const void* src = what == 0 ? (const void*)(a.k_codes4 + row * (kKvDim / 2)) : what == 1 ? (const void*)(a.k_scales4 + row * kKv4Blocks)
-                              : what == 2 ? (const void*)(v_codes + row * (kKvDim / 2)) : (const void*)(a.v_scales4 + row);
-              const uint32_t bytes = (what & 1) ? (what == 1 ? kKv4Blocks << lp : 2 << lp) : (kKvDim / 2) << lp;
-              uint8_t* const to = (what < 2 ? tk : tv) + ((what & 1) ? kTok * kKvDim / 2 : 0) + mine * bytes;
-              bulk_load_hint(to, src, bytes, what < 2 ? &rawk_full[rb] : &rawv_full[rb], policy);
-            }
+            const int row = mine < ppt && id >= 0 ? (id * a.kv_heads + s.h) << lp : -1;   // (the host holds rows below 2^31)
+            const uint32_t loads = __popc(__ballot_sync(0xffffffffu, lane < 8 && row >= 0));
+            if (lane == 0) sbad[i % kMetaBufs] = bad;
+            copy_raw(row, loads, sRaw + rb * kRawKBytes, &rawk_full[rb], a.k_codes4, a.k_scales4, kKv4Blocks);
+            if (i > 0) ok = copy_v(i - 1);
+            if (!ok) break;
+            v_row = row;
+            v_pages = loads;
             continue;
           }
           const int pg = __shfl_sync(0xffffffffu, page, (o + lane) & 31);
@@ -1224,6 +1226,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       }
       // nothing may still be landing in shared memory when the CTA exits
       if constexpr (k4) {
+        if (i > 0 && ok) ok = copy_v(i - 1);
         for (int rb = 0; rb < kRawStages; ++rb)
           if (i > rb) {
             const uint32_t last = ((i - rb + kRawStages - 1) / kRawStages - 1) & 1;
