@@ -267,8 +267,9 @@ __device__ __forceinline__ float pp_half(const PpRow& w, uint32_t tS, const floa
       const __half2 h = __floats2half2_rn(y0, y1);
       p[8 * g + (c >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    top = fmaxf(top, m * kc);
+    top = fmaxf(top, k4 ? m : m * kc);
   }
+  if (k4) top *= w.cf;
   float s0, s1, s2, s3;
   unpack2(sum[0], s0, s1);
   unpack2(sum[1], s2, s3);
