@@ -19,7 +19,7 @@
 namespace dsa {
 
 namespace {
-constexpr int kThreads = 256, kWarps = kThreads / 32, kKvHeadsAWarp = 8;
+constexpr int kThreads = 32, kWarps = kThreads / 32, kKvHeadsAWarp = 8;
 
 // the largest finite |x| (its bits), and whether there is a NaN
 __device__ __forceinline__ void largest(const float (&x)[16], uint32_t& top, bool& nan) {

@@ -5,7 +5,7 @@
 // Each product and the sum are rounded to fp32 apart (no fused multiply-add): a quantised value that lies near a border then
 // falls on the same side wherever the same three operations are done.
 //
-// Eight neighbouring lanes hold a head, 16 dims each.  dim is a multiple of 32, so that a lane's dims all belong to
+// Keys: eight neighbouring lanes hold a head, 16 dims each in a row, as it is quantised.  dim is a multiple of 32, so that a lane's dims all belong to
 // the same half: the other values of pairs (i, i + dim/2) are in one other lane, as bf16, half a register each.
 #pragma once
 
@@ -104,42 +104,72 @@ __device__ __forceinline__ bool row_place(const int32_t* query_start_loc, const 
   return true;
 }
 
-// Query heads 16 job .. 16 job + 15 of row r, rotated and rounded to bf16.  Loads first: they do not wait for the position.
+// Query heads 16 job .. 16 job + 15 of row r, rotated and rounded to bf16.  Loads first: they do not wait for the position.  Nothing
+// is quantised here, so a lane takes both halves of its pairs: eight dims and the eight that they turn with, and eight
+// angles (with 16 dims in a row, 16 angles and the other halves from another lane, four prompts of 4,096 took QUERYGAIN).
 __device__ __forceinline__ void rope_queries(const RopeArgs& rope, const int32_t* query_start_loc, const int32_t* seq_lens,
                                              int num_requests, int num_rows, int r, int job) {
   const int lane = threadIdx.x & 31, part = lane & 7, sub = lane >> 3;
+  const int half = rope.dim >> 1, parts = rope.dim / kRopeLaneDims;   // lanes with pairs to turn
+  const bool turned = part < parts, apart = turned && !rope.interleaved;
+  const int d0 = apart ? 8 * part : kRopeLaneDims * part, d1 = apart ? d0 + half : d0 + 8;
+  const __nv_bfloat16* const from = rope.q + (int64_t)r * rope.q_stride + (kRopeHeads * job + sub) * kKvDim;
+  const int heads = rope.q_heads - kRopeHeads * job - sub;            // from this lane's first on
   uint4 v[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int h = kRopeHeads * job + 4 * i + sub;
     v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-    if (h < rope.q_heads) {
-      const uint4* p = reinterpret_cast<const uint4*>(rope.q + (int64_t)r * rope.q_stride + h * kKvDim) + 2 * part;
-      v[i][0] = p[0];
-      v[i][1] = p[1];
+    if (4 * i < heads) {
+      v[i][0] = *reinterpret_cast<const uint4*>(from + 4 * i * kKvDim + d0);
+      v[i][1] = *reinterpret_cast<const uint4*>(from + 4 * i * kKvDim + d1);
     }
   }
   int b, pos;
   if (!row_place(query_start_loc, seq_lens, num_requests, num_rows, r, b, pos) || pos >= rope.positions) return;
-  RopeAngles a;
-  rope_load(rope, pos, part, a);
+  float c[8], s[8];
+  if (turned) {
+    const float* const at = rope.cos_sin + (int64_t)pos * rope.dim + 8 * part;
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+      *reinterpret_cast<float4*>(c + k) = __ldg(reinterpret_cast<const float4*>(at + k));
+      *reinterpret_cast<float4*>(s + k) = __ldg(reinterpret_cast<const float4*>(at + half + k));
+    }
+  }
+  __nv_bfloat16* const to = rope.q_out + (int64_t)r * rope.q_out_stride + (kRopeHeads * job + sub) * kKvDim;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int h = kRopeHeads * job + 4 * i + sub;
-    float x[16];
-    rope_turn(rope, a, part, v[i], x);
-    if (h < rope.q_heads) {
-      uint4 o[2];
-      uint32_t* w = reinterpret_cast<uint32_t*>(o);
+    if (4 * i >= heads) break;
+    uint4 o[2] = {v[i][0], v[i][1]};
+    if (turned) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(v[i]);
+      float x[16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 f = bf16x2(w[k]);
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+      }
+      auto turn = [](float& p, float& q, float c, float s) {
+        const float y = __fsub_rn(__fmul_rn(p, c), __fmul_rn(q, s));
+        q = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
+        p = y;
+      };
+      if (rope.interleaved) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) turn(x[2 * k], x[2 * k + 1], c[k], s[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) turn(x[k], x[8 + k], c[k], s[k]);
+      }
+      uint32_t* u = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t*>(&y);
+        u[k] = *reinterpret_cast<const uint32_t*>(&y);
       }
-      uint4* p = reinterpret_cast<uint4*>(rope.q_out + (int64_t)r * rope.q_out_stride + h * kKvDim) + 2 * part;
-      p[0] = o[0];
-      p[1] = o[1];
     }
+    *reinterpret_cast<uint4*>(to + 4 * i * kKvDim + d0) = o[0];
+    *reinterpret_cast<uint4*>(to + 4 * i * kKvDim + d1) = o[1];
   }
 }
 
