@@ -116,6 +116,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 }  // namespace p4
 
 // kCE columns (8, 16 or 32); kModSet: score cap and distance bias compiled in
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
             products(all, 0);
           }
           uint32_t hi[kHalf / 4], lo[kHalf / 4];
-          int p_top = 0;                               // bits: p is not negative (a NaN counts as large, too)
+          float p_top = 0.f;                           // (a NaN is no maximum: a column without a pair asks for nothing)
           __half2 x_top = __float2half2_rn(0.f);
 #pragma unroll
           for (int c0 = 0; c0 < kHalf; c0 += 8) {
@@ -716,7 +721,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
                 if (!seen(c0 + 2 * c + 1)) e.y = 0.f;
               }
               p[(c0 >> 1) + c] = pack2(e.x, e.y);
-              p_top = __vimax3_s32(p_top, __float_as_int(e.x), __float_as_int(e.y));
+              p_top = max3(p_top, e.x, e.y);
               // in this order: 0 stays 0 whatever the scale of an unseen key ..
               float2 x = unpack2(mul2(mul2(p[(c0 >> 1) + c], ee[c]), vs2));
               if (kMasked) {                           // .. and of one that some columns do not see even NaN
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
           fence_proxy_async_smem();
           tc_fence_before();
           const float x_most = fmaxf(__low2float(x_top), __high2float(x_top));
-          if (!group_or(bar, 128, !raised && (p_top >= __float_as_int(kSlackP) || x_most > kSlackP * kPOne))) break;
+          if (!group_or(bar, 128, !raised && (p_top >= kSlackP || x_most > kSlackP * kPOne))) break;
           raised = true;                               // the same in all four warps
           raise();
         }

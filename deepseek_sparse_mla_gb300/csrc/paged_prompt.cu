@@ -30,7 +30,8 @@
 //
 // 4-bit cache: block scales in TMEM, as the kernel for few rows has them, need columns that S and O do not leave, so K's
 // codes are widened too: to e5m2, which holds code * 2^e exactly for the exponents of the cache (-15 .. 13).  V's fp16
-// values are code * scale relative to the largest scale of the piece's tokens, exact (10 bits) down to 2^-14 of it.  Warps 8-11 widen K, 12-15 V.
+// values are code * scale in units that put the piece's largest scale at 2^12 (6 * 2^13 is the largest value, fp16's is 65,504): exact
+// for scales down to 2^-26 of it, a step of 2^-36 of it below (rows of a prompt that see only such tokens).  Warps 8-11 widen K, 12-15 V.
 // TMEM (all 512 columns): S of half q and key half h at 128 q + 64 h, with P over its first 32; O of half q at 256 + 128 q.
 #include "paged_attention.cuh"
 #include "sm100.cuh"
@@ -61,6 +62,7 @@ constexpr uint32_t kRegsSoft = 128, kRegsConv = 80, kRegsRest = 64;   // 2 * 128
 constexpr uint32_t kTmemCols = 512, kColO = 256;
 constexpr float kSlack = 6.f;                        // log2 by which a row's maximum may be exceeded
 constexpr float kPLog2 = 8.f;                        // P = 2^8 p
+constexpr float kV4Up = 4096.f;                      // 4 bits: the piece's largest scale of V in fp16, 2^12
 constexpr uint32_t kPolls = 1u << 18;                // of 3.8 us each or more: a second
 // Rolled: four polls written out at each of the many waits take 10 % longer (4,096 rows at 64K, 3.30 instead of 2.98 ms when
 // measured).
@@ -480,7 +482,7 @@ __device__ __forceinline__ void pp_widen_k4(const PpSeg* segs, uint64_t* seg_ful
   }
 }
 
-// V tiles: code * scale in fp16, in units of the power of two at or below the piece's largest scale
+// V tiles: code * scale in fp16, in units of 2^-12 of the power of two at or below the piece's largest scale
 __device__ __forceinline__ void pp_widen_v4(const PagedAttnArgs& a, const PpSeg* segs, uint64_t* seg_full, uint64_t* seg_empty,
                                             uint64_t* v_full, uint64_t* v_empty, uint8_t* sV, const PpRaw& raw, int* nan_key,
                                             float* vmax_part, float* v_ref, uint32_t* err) {
@@ -547,7 +549,7 @@ __device__ __forceinline__ void pp_widen_v4(const PagedAttnArgs& a, const PpSeg*
       const bool second = part >= 2;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        float ratio = scale[g] * vinv;
+        float ratio = scale[g] * vinv * kV4Up;         // below 2^13
         if (!(fabsf(scale[g]) < INFINITY)) {           // a NaN for the rows that see the key, noted apart: 0 * NaN is NaN
           ratio = 0.f;
           atomicMin(&nan_key[sb * kKvDim], key0 + 32 * g + row0);
@@ -848,7 +850,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       const float vref = v_ref[seg % kSegBufs];
       // a mean of V before its scale comes in: sums over keys times the largest scales would leave fp32's range, and the smallest
       // scales divided by the sums, too
-      const float inv = any ? 1.f / l : 0.f;
+      const float inv = any ? (k4 ? 1.f / kV4Up : 1.f) / l : 0.f;
       const int* nk = nan_key[seg % kSegBufs];       // (4 bits: a key is NaN as a whole)
 #pragma unroll 1
       for (int c = 0; c < kKvDim; c += 32) {

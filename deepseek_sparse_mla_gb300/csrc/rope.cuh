@@ -106,7 +106,7 @@ __device__ __forceinline__ bool row_place(const int32_t* query_start_loc, const 
 
 // Query heads 16 job .. 16 job + 15 of row r, rotated and rounded to bf16.  Loads first: they do not wait for the position.  Nothing
 // is quantised here, so a lane takes both halves of its pairs: eight dims and the eight that they turn with, and eight
-// angles (with 16 dims in a row, 16 angles and the other halves from another lane, four prompts of 4,096 took QUERYGAIN).
+// angles (with 16 dims in a row, 16 angles and the other halves from another lane, four prompts of 4,096 took 133 us instead of 100).
 __device__ __forceinline__ void rope_queries(const RopeArgs& rope, const int32_t* query_start_loc, const int32_t* seq_lens,
                                              int num_requests, int num_rows, int r, int job) {
   const int lane = threadIdx.x & 31, part = lane & 7, sub = lane >> 3;
