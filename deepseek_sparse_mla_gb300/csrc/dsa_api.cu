@@ -762,8 +762,7 @@ static dsa_status kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch,
   a.v = v;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  a.rope = rope_args(rope);
-  return cuda_status(launch_kv8_append(a, (cudaStream_t)stream), "8-bit K/V append launch");
+  return cuda_status(launch_kv8_append(a, rope_args(rope), (cudaStream_t)stream), "8-bit K/V append launch");
 }
 
 dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,

@@ -261,9 +261,8 @@ struct Kv8AppendArgs {
   int32_t num_requests, num_rows, table_stride;
   const void *k, *v;
   int64_t k_stride, v_stride;       // elements between tokens
-  RopeArgs rope;
 };
-cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s);
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, const RopeArgs& rope, cudaStream_t s);
 
 constexpr int kKv4Blocks = DSA_KV4_BLOCKS;       // K scales of a token: one for 32 dims
 constexpr int kKv4LowExp = DSA_KV4_MIN_EXP, kKv4HighExp = DSA_KV4_MAX_EXP;
@@ -289,10 +288,14 @@ struct PagedAttnArgs {
   const int32_t* query_start_loc;   // nullptr: one row per request
   int32_t num_requests, num_rows, table_stride;
   int32_t num_pages, log2_page, kv_heads, group;   // group = query heads per K/V head
-  const float *k_scales, *v_scales;                // 8-bit cache: of pages and heads
-  const uint8_t* k_codes4;
-  const uint8_t* k_scales4;                        // 4-bit cache: of tokens, heads and 32 dims
-  const __nv_bfloat16* v_scales4;                  // of tokens and heads
+  union {
+    const float* k_scales;                         // 8-bit cache: of pages and heads
+    const uint8_t* k_scales4;                      // 4-bit cache: of tokens, heads and 32 dims
+  };
+  union {
+    const float* v_scales;
+    const __nv_bfloat16* v_scales4;                // of tokens and heads
+  };
   const __nv_bfloat16* q;
   int64_t q_stride;                 // elements between rows
   float scale_log2;                 // softmax scale * log2(e)
@@ -309,6 +312,7 @@ struct PagedAttnArgs {
   int32_t* rec;                     // [ctas][8]: where each CTA's first piece lies
   float* part_o;                    // [2 * ctas] pieces of a segment: [columns][128]
   float* part_ml;                   // [2 * ctas][columns][2]
+  const uint8_t* k_codes4;          // 4-bit cache, prompt kernel
 };
 constexpr int kPagedAttnColumns = 32;     // (row, head) pairs of a K/V head taken together, at most
 // Requests of more pairs (rows times heads per K/V head) go to the prompt kernel, which takes 256 at a time.  Few-row kernel

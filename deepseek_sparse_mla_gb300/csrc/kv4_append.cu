@@ -19,6 +19,8 @@
 namespace dsa {
 
 namespace {
+// One warp a CTA: warps share nothing, and their rows end at different times (four prompts of 4,096 with 64 query heads: 256 threads 160 us,
+// 128 104, 64 100, 32 97).
 constexpr int kThreads = 32, kWarps = kThreads / 32, kKvHeadsAWarp = 8;
 
 // the largest finite |x| (its bits), and whether there is a NaN

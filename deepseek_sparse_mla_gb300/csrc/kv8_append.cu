@@ -19,6 +19,8 @@
 // the step's queries are rotated by further CTAs of the same launch, in front.
 #include "rope.cuh"
 
+#include <type_traits>
+
 namespace dsa {
 
 namespace {
@@ -83,25 +85,32 @@ __device__ __forceinline__ void recode(uint4* codes, int pieces, float ratio) {
   }
 }
 
+// What the kernel with a rotation has besides.  (In the arguments of both, it would cost the other one 2 % of four prompts of 4,096.)
+struct Rotation {
+  RopeArgs rope;
+  int q_ctas, q_jobs, units;
+};
+struct NoRotation {};
+
 // kItems: pieces of a full page a thread.  kRope: one row of CTAs, the first q_ctas of which rotate queries.
 template <int kThreads, int kItems, bool kRope>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArgs a, int q_ctas, int q_jobs, int units) {
+__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArgs a, const std::conditional_t<kRope, Rotation, NoRotation> turn) {
   __shared__ uint32_t warp_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   int unit = blockIdx.x, h = blockIdx.y;
   bool is_v = blockIdx.z != 0;
   pdl_wait();
   pdl_trigger();
-  if (kRope) {
-    if (unit < q_ctas) {
+  if constexpr (kRope) {
+    if (unit < turn.q_ctas) {
       const uint32_t w = (uint32_t)unit * (kThreads / 32) + (tid >> 5);
-      const int r = w / (uint32_t)q_jobs;
-      if (r < a.num_rows) rope_queries(a.rope, a.query_start_loc, a.seq_lens, a.num_requests, a.num_rows, r, w - r * q_jobs);
+      const int r = w / (uint32_t)turn.q_jobs;
+      if (r < a.num_rows) rope_queries(turn.rope, a.query_start_loc, a.seq_lens, a.num_requests, a.num_rows, r, w - r * turn.q_jobs);
       return;
     }
-    unit -= q_ctas;
-    const int of_head = unit / units;
-    unit -= of_head * units;
+    unit -= turn.q_ctas;
+    const int of_head = unit / turn.units;
+    unit -= of_head * turn.units;
     h = of_head >> 1;
     is_v = of_head & 1;
   }
@@ -138,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
   const int64_t page_pos = (int64_t)lp << a.log2_page;                    // position of the page's first token
   const int first = max((int)(start - page_pos), 0);                      // new tokens: offsets first .. last - 1
   int last = (int)min((int64_t)P, (int64_t)start + n - page_pos);
-  if (kRope) last = (int)min((int64_t)last, a.rope.positions - page_pos); // a token without a row of cos and sin is skipped
+  if constexpr (kRope) last = (int)min((int64_t)last, turn.rope.positions - page_pos); // a token without a row of cos and sin is skipped
   if (first >= last || lp >= a.table_stride) return;
   const uint4* src = reinterpret_cast<const uint4*>(is_v ? a.v : a.k);
   const int64_t src_stride = (is_v ? a.v_stride : a.k_stride) / 8;        // in 16-byte chunks
@@ -170,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
       const int i = tid + it * kThreads, pos = (int)page_pos + first + i / kRowParts;
       if (!is_v) {
         RopeAngles angles;
-        if (i < items && pos < a.rope.positions) rope_load(a.rope, pos, i % kRowParts, angles);
-        rope_turn(a.rope, angles, i % kRowParts, v[it], x[it]);
+        if (i < items && pos < turn.rope.positions) rope_load(turn.rope, pos, i % kRowParts, angles);
+        rope_turn(turn.rope, angles, i % kRowParts, v[it], x[it]);
       } else {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -243,22 +252,23 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8AppendArg
 
 namespace {
 template <int kThreads, int kItems>
-cudaError_t launch_pages(const Kv8AppendArgs& a, int64_t units, cudaStream_t s) {
-  if (!a.rope.cos_sin)
-    return launch_pdl(kv8_append_kernel<kThreads, kItems, false>, dim3((unsigned)units, a.kv_heads, 2), dim3(kThreads), 0, s, a, 0, 1, 0);
-  const int q_jobs = max((a.rope.q_heads + kRopeHeads - 1) / kRopeHeads, 1), warps = kThreads / 32;
-  const int64_t q_ctas = a.rope.q_heads ? ((int64_t)a.num_rows * q_jobs + warps - 1) / warps : 0, all = q_ctas + units * a.kv_heads * 2;
+cudaError_t launch_pages(const Kv8AppendArgs& a, const RopeArgs& rope, int64_t units, cudaStream_t s) {
+  if (!rope.cos_sin)
+    return launch_pdl(kv8_append_kernel<kThreads, kItems, false>, dim3((unsigned)units, a.kv_heads, 2), dim3(kThreads), 0, s, a, NoRotation{});
+  const int q_jobs = max((rope.q_heads + kRopeHeads - 1) / kRopeHeads, 1), warps = kThreads / 32;
+  const int64_t q_ctas = rope.q_heads ? ((int64_t)a.num_rows * q_jobs + warps - 1) / warps : 0, all = q_ctas + units * a.kv_heads * 2;
   if (all > INT32_MAX / 8) return cudaErrorInvalidValue;         // the entry point refuses such a call
-  return launch_pdl(kv8_append_kernel<kThreads, kItems, true>, dim3((unsigned)all), dim3(kThreads), 0, s, a, (int)q_ctas, q_jobs, (int)units);
+  return launch_pdl(kv8_append_kernel<kThreads, kItems, true>, dim3((unsigned)all), dim3(kThreads), 0, s, a,
+                    Rotation{rope, (int)q_ctas, q_jobs, (int)units});
 }
 }  // namespace
 
-cudaError_t launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t s) {
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, const RopeArgs& rope, cudaStream_t s) {
   const int64_t units = (a.query_start_loc ? (a.num_rows >> a.log2_page) : 0) + (int64_t)2 * a.num_requests;
-  const cudaError_t e = a.log2_page == 4   ? launch_pages<128, 1>(a, units, s)
-                        : a.log2_page == 5 ? launch_pages<256, 1>(a, units, s)
-                        : a.log2_page == 6 ? launch_pages<256, 2>(a, units, s)
-                                           : launch_pages<256, 4>(a, units, s);
+  const cudaError_t e = a.log2_page == 4   ? launch_pages<128, 1>(a, rope, units, s)
+                        : a.log2_page == 5 ? launch_pages<256, 1>(a, rope, units, s)
+                        : a.log2_page == 6 ? launch_pages<256, 2>(a, rope, units, s)
+                                           : launch_pages<256, 4>(a, rope, units, s);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
