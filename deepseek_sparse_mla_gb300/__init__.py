@@ -604,12 +604,9 @@ class Kv4Cache:
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.num_pages, self.kv_heads, self.page_size = (int(n) for n in k_codes.shape[:3])
 
-        self._struct = _lib.DsaKv4Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                                        self.num_pages, self.page_size, self.kv_heads, 0)
-
     def struct(self) -> _lib.DsaKv4Cache:
-        """Of the tensors that the cache was made over (made once: the calls only read it)."""
-        return self._struct
+        return _lib.DsaKv4Cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
+                                self.v_scales.data_ptr(), self.num_pages, self.page_size, self.kv_heads, 0)
 
 
 class RotaryTable:
@@ -634,7 +631,6 @@ class RotaryTable:
 
     def _set(self, cos_sin, interleaved):
         self.cos_sin, self.interleaved = cos_sin, bool(interleaved)
-        self._head = (cos_sin.data_ptr(), *cos_sin.shape, self.interleaved)      # the first fields of the struct
 
 
 def _batch_on(device, batch):
@@ -645,11 +641,13 @@ def _batch_on(device, batch):
 
 def _rope(rope, q, q_out, rows, device):
     """(struct, q_out) of an append's rotation."""
-    _on_device(device, rope.cos_sin, "rope.cos_sin")
+    table = rope.cos_sin
+    _on_device(device, table, "rope.cos_sin")
+    positions, dim = table.shape
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
-        return _lib.DsaRope(*rope._head), None
+        return _lib.DsaRope(table.data_ptr(), positions, dim, rope.interleaved), None
     if q.dim() != 3:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected (rows, heads, {KV_DIM})")
     heads = q.shape[1]
@@ -657,7 +655,7 @@ def _rope(rope, q, q_out, rows, device):
     if q_out is None:
         q_out = torch.empty((rows, heads, KV_DIM), dtype=torch.bfloat16, device=device)
     out_stride = _rows(q_out, rows, heads, device, "q_out")
-    return _lib.DsaRope(*rope._head, heads, q.data_ptr(), stride, q_out.data_ptr(), out_stride), q_out
+    return _lib.DsaRope(table.data_ptr(), positions, dim, rope.interleaved, heads, q.data_ptr(), stride, q_out.data_ptr(), out_stride), q_out
 
 
 def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None, rope: RotaryTable | None = None, q=None, q_out=None):

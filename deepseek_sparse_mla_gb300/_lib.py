@@ -50,8 +50,10 @@ class DsaKv8Cache(ctypes.Structure):
                 ("kv_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-class DsaKv4Cache(DsaKv8Cache):
-    """The same fields: k_scales and v_scales point to exponent bytes and to bf16."""
+class DsaKv4Cache(ctypes.Structure):
+    """The same fields (k_scales and v_scales point to exponent bytes and to bf16), but no kind of the other: a call that takes one
+    refuses the other."""
+    _fields_ = DsaKv8Cache._fields_
 
 
 class DsaRope(ctypes.Structure):

@@ -197,8 +197,8 @@ DSA_API uint64_t dsa_kernel_launches(void);
 /*
  * Device status of the last call that used `workspace`: the OR of the DSA_DEVICE_* bits its kernels
  * set.  workspace is a workspace passed to dsa_indexer_scores_topk, dsa_indexer_page_topk or
- * dsa_sparse_mla_decode / _decode_ragged / _prefill (the bits live in its first bytes, which every
- * such call rewrites), or NULL for the static scratch of dsa_indexer_scores_topk_static on the
+ * dsa_sparse_mla_decode / _decode_ragged / _prefill, or to the dense layer's attention (the bits live in its first
+ * bytes, which every such call rewrites), or NULL for the static scratch of dsa_indexer_scores_topk_static on the
  * current device.  ("GLM-5.2 on vLLM Ascend: Request-to-Backend Inference Path", "Failure and
  * Correctness Boundaries".)
  *   status_out  4 bytes of device memory, or of page-locked host memory mapped into the device's
@@ -700,8 +700,8 @@ DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_bat
  * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-18 of its
  * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
  * Requests of at most 64 rows * heads per K/V head keep 8 bits or more of a contribution p * v_scale to the output, with
- * an absolute error of 2^-20 of the largest one; requests of more keep 11 bits of p, and hold V to 2^-25 of the largest V
- * scale of the request's tokens, those that a row does not see included.
+ * an absolute error of 2^-20 of the largest one; requests of more keep 11 bits of p, and V exactly where its scale is at least
+ * 2^-26 of the largest one of the request's tokens (those that a row does not see included), else to 2^-34 of that.
  */
 DSA_API dsa_status dsa_kv4_attention(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
                                      int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,

@@ -129,6 +129,18 @@ def test_null_structs_and_calls_without_rows(lib):
     assert _append4(lib, batch=none, k=0, v=0) == 0 and _attend(lib, batch=none, q=0, out=0, ws=0) == 0
 
 
+def test_a_cache_of_the_other_kind_is_refused(lib):
+    b = ctypes.byref(_batch())
+    with pytest.raises(ctypes.ArgumentError):
+        lib.dsa_kv8_append(ctypes.byref(_cache()), b, A, 256, A, 256, None)
+    with pytest.raises(ctypes.ArgumentError):
+        lib.dsa_paged_attention(ctypes.byref(_cache()), b, A, 512, 4, 0.1, 1, None, A, 0, A, 1 << 40, None)
+    with pytest.raises(ctypes.ArgumentError):
+        lib.dsa_kv4_append(ctypes.byref(_cache8()), b, A, 256, A, 256, None, None)
+    with pytest.raises(ctypes.ArgumentError):
+        lib.dsa_kv4_attention(ctypes.byref(_cache8()), b, A, 512, 4, 0.1, 1, None, A, 0, A, 1 << 40, None)
+
+
 def test_attention_workspace_is_that_of_the_8_bit_cache(lib):
     size = lib.dsa_paged_attention_workspace_bytes
     for longest in (1, 40):
