@@ -349,6 +349,60 @@ __device__ __forceinline__ float pp_exp64(const PpRow& w, uint32_t tS) {
   return (s0 + s1) + (s2 + s3);
 }
 
+// The same for scores of the 4-bit cache without a cap or bias, which nothing but their row's factor separates from their final form:
+// their largest, and P formed from the products as they are (written back in between, 4,096 rows at 64K took 3.18 ms instead of 3.12).
+__device__ __forceinline__ float pp_max64(const PpRow& w, uint32_t tS, int key0, uint32_t bad) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int g = 0; g < 4; g += 2) {
+    uint32_t r[32];
+    tmem_ld32(tS + 16 * g, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int gg = 0; gg < 2; ++gg) {
+      const int left = ((bad >> (g + gg)) & 1u) ? 0 : w.limit - key0 - 16 * (g + gg);   // keys of the group that are seen
+      float m = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) m = fmaxf(m, c < left ? __uint_as_float(r[16 * gg + c]) : -INFINITY);
+      top = fmaxf(top, m);
+    }
+  }
+  return top == -INFINITY ? top : top * w.cf;          // (-inf whatever the factor, which may be 0)
+}
+
+// .. and P in their place
+__device__ __forceinline__ float pp_exp64(const PpRow& w, uint32_t tS, int key0, uint32_t bad) {
+  const float shift = pp::kPLog2 - (w.m == -INFINITY ? 0.f : w.m);
+  const uint64_t shift2 = pack2(shift, shift), kc2 = pack2(w.cf, w.cf);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+  for (int g = 0; g < 4; g += 2) {
+    uint32_t r[32], p[16];
+    tmem_ld32(tS + 16 * g, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int gg = 0; gg < 2; ++gg) {
+      const int left = ((bad >> (g + gg)) & 1u) ? 0 : w.limit - key0 - 16 * (g + gg);
+#pragma unroll
+      for (int c = 0; c < 16; c += 2) {
+        const uint32_t* x = r + 16 * gg + c;
+        float y0, y1;
+        unpack2(fma2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), kc2, shift2), y0, y1);
+        y0 = c < left ? ex2_approx(y0) : 0.f;
+        y1 = c + 1 < left ? ex2_approx(y1) : 0.f;
+        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(y0, y1));
+        const __half2 h = __floats2half2_rn(y0, y1);
+        p[8 * gg + (c >> 1)] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    tmem_st16(tS + 8 * g, p);
+  }
+  float s0, s1, s2, s3;
+  unpack2(sum[0], s0, s1);
+  unpack2(sum[1], s2, s3);
+  return (s0 + s1) + (s2 + s3);
+}
+
 // 16 columns a step: the accumulator of a row whose reference moved
 __device__ __forceinline__ void pp_shrink(uint32_t tO, float al) {
 #pragma unroll 1
@@ -795,7 +849,11 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
           }
           return true;
         };
-        if constexpr (kMods || decltype(masked)::value) {
+        if constexpr (k4 && !kMods && decltype(masked)::value) {
+          raise(pp_max64(w, tS + 64 * h, key0, bad >> (4 * h)));
+          if (!ok) return;
+          w.l += pp_exp64(w, tS + 64 * h, key0, bad >> (4 * h));
+        } else if constexpr (kMods || decltype(masked)::value) {
           raise(pp_max64<k4, kModSet, decltype(masked)::value>(w, a, tS + 64 * h, key0, bad >> (4 * h), ks));
           if (!ok) return;
           w.l += pp_exp64(w, tS + 64 * h);
