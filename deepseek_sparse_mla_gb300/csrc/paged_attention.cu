@@ -805,7 +805,6 @@ cudaError_t launch_columns(const PagedAttnArgs& a, const CUtensorMap& k_map, con
                                      : paged_attention_kernel<kCE, kPaLargeCap>;
   e = launch_pdl(kernel, dim3(ctas), dim3(pa::kThreads), smem, s, k_map, v_map, a, shared_keys);
   count_launches(1);
-  if (e != cudaSuccess) return e;
   if (e == cudaSuccess && ctas > 1 && !a.whole && join) e = launch_paged_join(a, ctas, kCE, s);
   return e;
 }
