@@ -48,6 +48,11 @@ constexpr uint32_t kRegsLow = 80, kRegsSoft = 176;   // 2 * 80 + 2 * 176 = 4 * 1
 constexpr uint32_t kTmemCols = 512, kColScales = 192, kColQScales = 216, kColO = 256;
 constexpr float kSlackP = 4.f;                  // a reference may be exceeded by this factor
 constexpr float kPOne = 64.f;                   // the code of a contribution at its reference: 2^2 above fits in 448
+// kPOne's factors: 2^4 comes in with a column's references and the rest with a key's scale, so that scales below 2^126 (more than the
+// append writes) stay finite.  References are formed with scales of at least 2^-121: 2^(m - mv + 4) times a probability below 4 stays finite, too.
+constexpr int kColumnLog2 = 4, kLowScaleLog2 = -121;
+constexpr float kKeyPOne = kPOne / (1 << kColumnLog2);
+static_assert(kColumnLog2 - kLowScaleLog2 + 2 < 128, "fp32's range");
 constexpr uint32_t kPolls = 1u << 18;           // of 3.8 us each or more: a second
 constexpr uint32_t kSegPolls = 1u << 24;        // for the end of a whole segment: a minute
 // Polls are rolled: the bodies of many roles share the instruction caches.
@@ -490,7 +495,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
     const int sw = kN == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
     constexpr bool kHold = kCE == 8;                   // references and factors stay in registers
     float* const ref_m = refs[wg][0];                  // as -m
-    float* const ref_e = refs[wg][1];                  // 2^(m - mv)
+    float* const ref_e = refs[wg][1];                  // 2^(m - mv + 4)
     int i0 = 0, i = wg;                                // the CTA's tiles before this segment; this warpgroup's next one
     int kst = wg, vst = wg;                            // its places in the rings (longer than kWgs), and their turns
     uint32_t k_turn = 0, v_turn = 0;
@@ -578,8 +583,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         auto seen = [&](int c) { return exists && j < cm.limit[c]; };
         // the exact maxima over the tile, where the references do not hold: they, and what was formed against them, move
         auto raise = [&]() {
-          // log2 of the key's scale, -126 for one of 0: 2^(m - mv) and its product with a probability below 4 stay finite
-          const float lv = fmaxf(__log2f(fabsf(vs)), -126.f);
+          const float lv = fmaxf(__log2f(fabsf(vs)), (float)kLowScaleLog2);   // log2 of the key's scale, which may be 0
           float mine = -INFINITY, mine_v = -INFINITY;
 #pragma unroll 1
           for (int c0 = 0; c0 < kNC; c0 += 8) {
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
           mv_lane = mv_new;
           if (quarter == 0 && lane < kCE) {
             ref_m[lane] = m_new == -INFINITY ? 1e30f : -m_new;   // nothing seen yet: the first score that is exceeds it
-            ref_e[lane] = mv_new == -INFINITY ? 1.f : ex2_approx(m_new - mv_new);
+            ref_e[lane] = mv_new == -INFINITY ? 1.f : ex2_approx(m_new - mv_new + (float)kColumnLog2);
           }
           if (!fresh) {
             // the accumulator is settled when the tile before has been added
@@ -656,7 +660,7 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         };
         // (P's place is free: V's tile was loaded once the product that read both before had been computed)
         uint8_t* const prow = sP + vst * F::kPBytes + row * kN;
-        const uint64_t vs2 = pack2(vs * kPOne, vs * kPOne);
+        const uint64_t vs2 = pack2(vs * kKeyPOne, vs * kKeyPOne);
         uint64_t p[kNC / 2];
         bool raised = fresh;
         if (fresh) raise();

@@ -296,8 +296,8 @@ __device__ __forceinline__ bool pa_pieces(const PaRecord& r, int c, int ctas, in
 
 // Joins the pieces of the segments that CTA boundaries cut, each an output o_p of its own keys:
 //   out = sum_p w_p o_p,  w_p = 2^{m_p - M} l_p / L,  L = sum_p 2^{m_p - M} l_p.
-// Pieces and running sum are weighted means of V throughout: V's scales go up to 2^120, and a sum over keys before its
-// division by L would leave fp32's range.
+// Pieces and running sum are weighted means of V throughout: V's scales go up to 2^120 (4-bit cache: 2^125.4), and a sum over keys
+// before its division by L would leave fp32's range.
 // A block (c, y) handles the boundary in front of range c if it is the first that cuts its segment, and
 // columns 8 y .. 8 y + 7: a warp a column, four dims a lane.
 __device__ __forceinline__ void pa_join(const PagedAttnArgs& a, int ctas, int c, int y) {

@@ -608,7 +608,7 @@ DSA_API dsa_status dsa_kv8_append_rope(const dsa_kv8_cache* cache, const dsa_bat
  *                     scale of dims 32j .. 32j + 31; 255 is NaN.  dsa_kv4_append writes exponents from DSA_KV4_MIN_EXP to
  *                     DSA_KV4_MAX_EXP, and attention takes those.
  *   v_scales          [num_pages, kv_heads, page_size] bf16, 16-byte aligned: one scale a token and head.  Attention takes any
- *                     finite one whose size is 0 or from 2^-126 to 2^120.
+ *                     one whose size is 0 or from 2^-126 to below 2^126 (dsa_kv4_append writes at most a sixth of bf16's largest number).
  * 134 bytes a token and head, where the 8-bit cache takes 256.  Token s of request b lies in page block_table[b][s / page_size],
  * at offset s % page_size.
  */
@@ -700,7 +700,8 @@ DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_bat
  * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-18 of its
  * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
  * Requests of at most 64 rows * heads per K/V head keep 8 bits or more of a contribution p * v_scale to the output, with
- * an absolute error of 2^-20 of the largest one; requests of more keep 11 bits of p, and V exactly where its scale is at least
+ * an absolute error of 2^-20 of the largest one (of v_scale taken as 2^-121 where it is smaller); requests of more keep 11 bits of p,
+ * and V exactly where its scale is at least
  * 2^-26 of the largest one of the request's tokens (those that a row does not see included), else to 2^-34 of that.
  */
 DSA_API dsa_status dsa_kv4_attention(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
