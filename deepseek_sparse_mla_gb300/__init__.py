@@ -663,7 +663,9 @@ def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None, rope: Rotar
     the batch at its own position.  A page whose new tokens need a larger scale than it has is re-coded.  Tokens without a
     valid page are skipped; paged_attention over the same batch reports them.  With a rope the cached keys are k rotated by their
     positions, and q [rows, q_heads, 128] bf16 (optional) is rotated in the same launch, into q_out (which may be q; allocated
-    where it is not given).  Returns q_out, or None without q."""
+    where it is not given).  Every row of a request is written to q_out (one in front of the request's first token as it is in q);
+    rows behind the last request's, of a request whose offsets do not fit the batch, and at positions beyond the rope's
+    are left as they were: what they hold in a q_out allocated here is unspecified.  Returns q_out, or None without q."""
     dev = cache.k_codes.device
     away = _elsewhere(dev, stream)
     if away is not None:

@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArg
       v[i][1] = q[1];
     }
   }
-  int b, pos;
-  if (!row_place(a.query_start_loc, a.seq_lens, a.num_requests, a.num_rows, r, b, pos)) return;
+  int b, pos, first;
+  if (!row_place(a.query_start_loc, a.seq_lens, a.num_requests, a.num_rows, r, b, pos, first) || first < 0) return;
   RopeAngles angles;
   if (kRope) {
     if (pos >= a.rope.positions) return;

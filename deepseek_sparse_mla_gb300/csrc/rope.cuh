@@ -78,14 +78,15 @@ __device__ __forceinline__ void rope_turn(const RopeArgs& r, const RopeAngles& a
   }
 }
 
-// Request and position of row r.  False where the row belongs to no request, or to one whose offsets or length make no sense.
-// Every lane of a warp asks for the same row; 32 probes a step.
+// Request and position of row r, and the position of the request's first row: below 0 where it has more rows than tokens.  False
+// where the row belongs to no request, or to one whose offsets make no sense.  Every lane of a warp asks for the same row; 32
+// probes a step.
 __device__ __forceinline__ bool row_place(const int32_t* query_start_loc, const int32_t* seq_lens, int num_requests, int num_rows, int r,
-                                          int& b, int& pos) {
+                                          int& b, int& pos, int& first) {
   if (query_start_loc == nullptr) {
     b = r;
-    pos = seq_lens[r] - 1;
-    return pos >= 0;
+    pos = first = max(seq_lens[r], 0) - 1;
+    return true;
   }
   const int lane = threadIdx.x & 31;
   int size = num_requests;
@@ -99,12 +100,14 @@ __device__ __forceinline__ bool row_place(const int32_t* query_start_loc, const 
     size = min(step, size - last * step);
   }
   const int row0 = query_start_loc[b], end = query_start_loc[b + 1], len = seq_lens[b];
-  if (row0 < 0 || r < row0 || r >= end || end > num_rows || len < end - row0) return false;
-  pos = len - (end - row0) + (r - row0);
+  if (row0 < 0 || r < row0 || r >= end || end > num_rows) return false;
+  first = max(len, 0) - (end - row0);
+  pos = first + (r - row0);
   return true;
 }
 
-// Query heads 16 job .. 16 job + 15 of row r, rotated and rounded to bf16.  Loads first: they do not wait for the position.  Nothing
+// Query heads 16 job .. 16 job + 15 of row r, rotated and rounded to bf16.  (A row in front of its request's first token has no
+// position: it may see a prefix, so its queries are copied as they are.)  Loads first: they do not wait for the position.  Nothing
 // is quantised here, so a lane takes both halves of its pairs: eight dims and the eight that they turn with, and eight
 // angles (with 16 dims in a row, 16 angles and the other halves from another lane, four prompts of 4,096 took 133 us instead of 100).
 __device__ __forceinline__ void rope_queries(const RopeArgs& rope, const int32_t* query_start_loc, const int32_t* seq_lens,
@@ -124,10 +127,11 @@ __device__ __forceinline__ void rope_queries(const RopeArgs& rope, const int32_t
       v[i][1] = *reinterpret_cast<const uint4*>(from + 4 * i * kKvDim + d1);
     }
   }
-  int b, pos;
-  if (!row_place(query_start_loc, seq_lens, num_requests, num_rows, r, b, pos) || pos >= rope.positions) return;
+  int b, pos, first;
+  if (!row_place(query_start_loc, seq_lens, num_requests, num_rows, r, b, pos, first) || pos >= rope.positions) return;
+  const bool turns = turned && pos >= 0;
   float c[8], s[8];
-  if (turned) {
+  if (turns) {
     const float* const at = rope.cos_sin + (int64_t)pos * rope.dim + 8 * part;
 #pragma unroll
     for (int k = 0; k < 8; k += 4) {
@@ -140,7 +144,7 @@ __device__ __forceinline__ void rope_queries(const RopeArgs& rope, const int32_t
   for (int i = 0; i < 4; ++i) {
     if (4 * i >= heads) break;
     uint4 o[2] = {v[i][0], v[i][1]};
-    if (turned) {
+    if (turns) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(v[i]);
       float x[16];
 #pragma unroll

@@ -577,12 +577,15 @@ DSA_API dsa_status dsa_kv8_append(const dsa_kv8_cache* cache, const dsa_batch* b
  * Products and their sum are rounded to fp32 one by one; the other dims stay as they are.  Keys are quantised from the fp32
  * values, queries rounded to bf16.
  *   cos_sin     device fp32 [positions, dim], 16-byte aligned: row p holds the dim / 2 cos and then the dim / 2 sin of position p.
- *   positions   at least the batch's max_seq_len.  (A row at a position beyond the table is skipped.)
+ *   positions   at least the batch's max_seq_len.  (A row at a position beyond the table is skipped: its key is not cached, its
+ *               queries are left as they were.)
  *   dim         32, 64, 96 or 128.
  *   q, q_out    device bf16, row r's heads at q + r * q_stride (elements): [q_heads, 128] contiguous, 16-byte aligned,
  *               strides a multiple of 8 and at least q_heads * 128.  q_out may be q itself (with its stride), and else
- *               does not overlap it.  Every row of a request is rotated, also one whose token has no valid page; rows behind
- *               the last request's are left as they were.  q_heads 0: no queries (q and q_out NULL).
+ *               does not overlap it.  Every row of a request is rotated, also one whose token has no valid page and, where
+ *               the request has more rows than tokens (its keys are skipped), those with a position; the rows in front of its
+ *               first token are copied as they are.  Rows behind the last request's, and those of a request whose offsets do not
+ *               fit the batch, are left as they were.  q_heads 0: no queries (q and q_out NULL).
  */
 typedef struct {
   const float* cos_sin;

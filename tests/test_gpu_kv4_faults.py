@@ -3,11 +3,13 @@ import numpy as np
 import pytest
 
 import workloads as wlm
-from dense_cases import check_attention
-from kv4_cases import Kv4Case
+from dense_cases import DenseCase, check_attention
+from kv4_cases import Kv4Case, rope_table
+from oracle import dense_oracle as d
+from oracle import dsa_oracle as o
 from oracle import kv4_oracle as f
 from test_gpu_dense_edges import attend
-from test_gpu_kv4_append import want4
+from test_gpu_kv4_append import append, positions, same4, want4
 from test_gpu_kv4_edges import BOTH
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +55,46 @@ def test_one_token_of_the_largest_value():
         case.cache["v"][at], case.cache["vs"][at] = f.quantise_v(np.full(128, 255 * 2.0 ** 120))
     got, lse = attend(case)
     assert np.all(got == 255 * 2.0 ** 120)                   # bf16's largest number
+
+
+@pytest.mark.parametrize("kind", [Kv4Case, DenseCase], ids=["4 bits", "8 bits"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_queries_of_requests_with_more_rows_than_tokens(kind, interleaved, in_place):
+    """Attention answers all rows of such a request, so all its queries are written: rotated where the row has a position, and as
+    they are in front of the first token.  Its keys are skipped."""
+    import torch
+    case = kind(48, [5, 0, 40, 33], [9, 7, 41, 2], 16, 1, 18, extra_rows=2)
+    rope, pos = rope_table(45, 64), positions(case)
+    live = np.arange(case.rows) < case.starts[-1]
+    q = wlm.bits_to_torch(case.q_bits, "cuda")
+    out = q if in_place else torch.full_like(q, -7.0)
+    got, turned = append(case, rope, interleaved, q, out)
+    want = np.where((pos >= 0)[:, None, None], f.rotate32(case.q, rope, np.maximum(pos, 0), interleaved), case.q)
+    assert np.array_equal(turned[live], wlm.bf16_bits(want.astype(np.float32))[live])
+    assert np.all(o.bf16_to_f64(turned[~live]) == (case.q[~live] if in_place else -7.0))
+    if kind is Kv4Case:
+        same4(case, got, want4(case, rope, interleaved))     # (the oracle skips such requests)
+    else:
+        k = f.rotate32(o.bf16_to_f64(case.new["k"]), rope, np.maximum(pos, 0), interleaved)
+        codes, scales = d.append(case.codes["k"], case.scales["k"], case.table, case.seq_lens, case.starts, k.astype(np.float64))
+        assert np.array_equal(got["ks"], scales) and np.array_equal(got["k"], codes)
+
+
+def test_a_step_over_requests_with_more_rows_than_tokens():
+    """Rows in front of the first token see a prefix, with queries that the append wrote into memory of its own."""
+    import torch
+    import deepseek_sparse_mla_gb300 as dsa
+    case = Kv4Case(49, [5, 40, 33], [9, 41, 2], 16, 1, 6)
+    rope, pos, prefix = rope_table(45, 128), positions(case), np.array([3, 20, 0], np.int32)
+    cache, batch, q = case.gpu()
+    k, v = (wlm.bits_to_torch(case.new[n], "cuda") for n in "kv")
+    stale = torch.full_like(q, float("nan"))                # what a new tensor's memory may hold
+    torch.cuda.synchronize()
+    del stale
+    turned = dsa.kv4_append(cache, batch, k, v, rope=dsa.RotaryTable.of(torch.from_numpy(rope).cuda()), q=q)
+    case.q_bits = np.where((pos >= 0)[:, None, None], wlm.bf16_bits(f.rotate32(case.q, rope, np.maximum(pos, 0))), case.q_bits)
+    assert np.array_equal(wlm.torch_to_bits(turned), case.q_bits)
+    case.cache = want4(case, rope)
+    got, lse = attend(case, (cache, batch, turned), prefix_lens=prefix)
+    check_attention(got, lse, case.oracle(prefix=prefix))
