@@ -305,8 +305,11 @@ __global__ void __launch_bounds__(p4::kThreads, 1)
         }
       }
       // nothing may still be landing in shared memory when the CTA exits: this warp's among the last kRing tiles (the stages of
-      // earlier ones have been filled again since)
-      for (i -= 2; i >= 0 && i >= i0 - kRing; i -= 2) {
+      // earlier ones have been filled again since).  Where the wait for tile i's place ran out, those before tile i, and what that
+      // place holds, whichever warp's it is.  (Tiles before that one have been used, and so have landed.)
+      const int end = ok ? i0 : i;
+      if (!ok) wait_warp(&full[st], turn ^ 1, err, kErrTmaTimeout);
+      for (i -= 2; i >= 0 && i >= end - kRing; i -= 2) {
         st -= 2;
         if (st < 0) {
           st += kRing;
