@@ -1182,9 +1182,11 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       int i = 0;
       int64_t u = u0;
       bool ok = true;
-      // 4 bits: a page a lane of the tile whose V is to be copied next (its first row, or -1), and how many there are
+      // 4 bits: a page a lane of the tile whose V is to be copied next (its first row, or -1), and how many there are; tiles of K and
+      // of V whose copies are under way or done
       int v_row = -1;
       uint32_t v_pages = 0;
+      int k_tiles = 0, v_tiles = 0;
       // codes (lanes 0 .. ppt - 1, a page each) and scales (lanes 8 ..) of K or of V, of the rows from `row` on
       auto copy_raw = [&](int row, uint32_t loads, uint8_t* to, uint64_t* full, const uint8_t* codes, const void* scales, int scale_bytes) {
         if (lane == 0) mbar_arrive_expect_tx(full, loads * ((uint32_t)(kKvDim / 2 + scale_bytes) << lp));
@@ -1201,6 +1203,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
         const int rb = j % kRawStages;
         if (j >= kRawStages && !wait_warp(&rawv_empty[rb], (j / kRawStages - 1) & 1, err, kErrMmaTimeout, kPolls)) return false;
         copy_raw(v_row, v_pages, sRaw + kRawStages * kRawKBytes + rb * kRawVBytes, &rawv_full[rb], v_codes, a.v_scales4, 2);
+        v_tiles = j + 1;
         return true;
       };
       for (int seg = 0;; ++seg) {
@@ -1262,6 +1265,7 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
             const uint32_t loads = __popc(__ballot_sync(0xffffffffu, lane < 8 && row >= 0));
             if (lane == 0) sbad[i % kMetaBufs] = bad;
             copy_raw(row, loads, sRaw + rb * kRawKBytes, &rawk_full[rb], a.k_codes4, a.k_scales4, kKv4Blocks);
+            k_tiles = i + 1;
             if (i > 0) ok = copy_v(i - 1);
             if (!ok) break;
             v_row = row;
@@ -1288,12 +1292,12 @@ __global__ void __launch_bounds__(pp::kThreads, 1)
       // nothing may still be landing in shared memory when the CTA exits
       if constexpr (k4) {
         if (i > 0 && ok) ok = copy_v(i - 1);
-        for (int rb = 0; rb < kRawStages; ++rb)
-          if (i > rb) {
-            const uint32_t last = ((i - rb + kRawStages - 1) / kRawStages - 1) & 1;
-            wait_warp(&rawk_full[rb], last, err, kErrTmaTimeout, kPolls);
-            wait_warp(&rawv_full[rb], last, err, kErrTmaTimeout, kPolls);
-          }
+        auto landed = [&](uint64_t* full, int tiles) {   // the last of these tiles in each place
+          for (int rb = 0; rb < kRawStages; ++rb)
+            if (tiles > rb) wait_warp(&full[rb], ((tiles - rb + kRawStages - 1) / kRawStages - 1) & 1, err, kErrTmaTimeout, kPolls);
+        };
+        landed(rawk_full, k_tiles);
+        landed(rawv_full, v_tiles);
       } else {
         for (int st = 0; st < kKStages; ++st)
           if (i > st) wait_warp(&k_full[st], ((i - st + kKStages - 1) / kKStages - 1) & 1, err, kErrTmaTimeout, kPolls);

@@ -52,3 +52,20 @@ def test_few_row_loaders_wait_for_their_last_copies(ring, segments):
                 assert waited == last & set(tiles)
         waited = both[0][1] | both[1][1]
         assert waited >= {t for t in issued if t >= stuck}, (stuck, both)   # those before it have been used
+
+
+def test_the_prompt_kernel_waits_for_every_tile_that_it_copies():
+    """Its loader notes a tile of K or V as it asks for it, whatever ends the loop after that, and the last of those in each of the two
+    places is waited for."""
+    text = source("paged_prompt.cu")
+    after = re.findall(r"\n\s*copy_raw\((?:[^;]*)\);\s*([^;]+);", text)
+    assert sorted(after) == ["k_tiles = i + 1", "v_tiles = j + 1"]
+    drain = text[text.index("auto landed = "):]
+    assert re.search(r"landed\(rawk_full, k_tiles\);\s*landed\(rawv_full, v_tiles\);", drain)
+    parity = re.search(r"if \(tiles > rb\) wait_warp\(&full\[rb\], (.+) & 1, err", drain).group(1).replace("/", "//")
+    places = int(re.search(r"kRawStages = (\d+);", text).group(1))
+    for tiles in range(12):
+        for rb in range(places):
+            uses = len(range(rb, tiles, places))
+            if uses:
+                assert eval(parity, {}, {"tiles": tiles, "rb": rb, "kRawStages": places}) & 1 == (uses - 1) & 1
