@@ -658,7 +658,7 @@ def _rope(rope, q, q_out, rows, device):
     return _lib.DsaRope(table.data_ptr(), positions, dim, rope.interleaved, heads, q.data_ptr(), stride, q_out.data_ptr(), out_stride), q_out
 
 
-def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None, rope: RotaryTable | None = None, q=None, q_out=None):
+def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None, *, rope: RotaryTable | None = None, q=None, q_out=None):
     """Append the step's tokens to an 8-bit K/V cache: k, v [rows, kv_heads, 128] bf16 (rows may be strided), row r of
     the batch at its own position.  A page whose new tokens need a larger scale than it has is re-coded.  Tokens without a
     valid page are skipped; paged_attention over the same batch reports them.  With a rope the cached keys are k rotated by their
@@ -670,7 +670,7 @@ def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None, rope: Rotar
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
-            return kv8_append(cache, batch, k, v, None, rope, q, q_out)
+            return kv8_append(cache, batch, k, v, rope=rope, q=q, q_out=q_out)
     k_stride = _rows(k, batch.num_rows, cache.kv_heads, dev, "k")
     v_stride = _rows(v, batch.num_rows, cache.kv_heads, dev, "v")
     _batch_on(dev, batch)
@@ -686,14 +686,14 @@ def kv8_append(cache: BlockKvCache, batch: Batch, k, v, stream=None, rope: Rotar
     return q_out
 
 
-def kv4_append(cache: Kv4Cache, batch: Batch, k, v, rope: RotaryTable | None = None, q=None, q_out=None, stream=None):
+def kv4_append(cache: Kv4Cache, batch: Batch, k, v, stream=None, *, rope: RotaryTable | None = None, q=None, q_out=None):
     """Append the step's tokens to a 4-bit K/V cache; arguments and result as for kv8_append.  No other token of a page is
     touched.  Tokens without a valid page are skipped; paged_attention over the same batch reports them."""
     dev = cache.k_codes.device
     away = _elsewhere(dev, stream)
     if away is not None:
         with away:
-            return kv4_append(cache, batch, k, v, rope, q, q_out)
+            return kv4_append(cache, batch, k, v, rope=rope, q=q, q_out=q_out)
     k_stride = _rows(k, batch.num_rows, cache.kv_heads, dev, "k")
     v_stride = _rows(v, batch.num_rows, cache.kv_heads, dev, "v")
     _batch_on(dev, batch)
