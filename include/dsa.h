@@ -636,8 +636,9 @@ typedef struct {
  *   k, v      as for dsa_kv8_append.
  *   rope      rotation of k, and of queries along with it, or NULL.
  * Tokens whose page id is out of range or whose table row is too short are skipped, and so are requests with more rows than tokens
- * or with offsets that do not fit the batch.  No two rows may name the same slot.  No status of its own: dsa_kv4_attention over
- * the same batch reports bad ids, short rows and such offsets.
+ * or with offsets that do not fit the batch.  (Where offsets run back, a row that they name twice is taken for one of its requests.)
+ * No two rows may name the same slot.  No status of its own: dsa_kv4_attention over the same batch reports bad ids, short rows
+ * and such offsets.
  */
 DSA_API dsa_status dsa_kv4_append(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* k, int64_t k_stride, const void* v,
                                   int64_t v_stride, const dsa_rope* rope, void* stream);

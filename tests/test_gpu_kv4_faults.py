@@ -98,3 +98,36 @@ def test_a_step_over_requests_with_more_rows_than_tokens():
     case.cache = want4(case, rope)
     got, lse = attend(case, (cache, batch, turned), prefix_lens=prefix)
     check_attention(got, lse, case.oracle(prefix=prefix))
+
+
+@pytest.mark.parametrize("kind", [Kv4Case, DenseCase], ids=["4 bits", "8 bits"])
+@pytest.mark.parametrize("starts,rows", [([0, 4, 9, 20], 12), ([-3, 2, 4, 6], 6), ([2, 4, 6, 8], 8), ([0, 4, 8, 12], 12)])
+def test_requests_beside_those_whose_offsets_do_not_fit(kind, starts, rows):
+    """Their keys, values and queries are written as ever; the others' rows are left alone."""
+    import torch
+    case = kind(50, [50, 33, 40], [4, 4, 4], 16, 2, 3)
+    case.starts, case.rows = np.array(starts, np.int32), rows
+    case.new = {n: wlm.bf16_bits(np.random.default_rng(50 + rows).standard_normal((rows, 2, 128)).astype(np.float32)) for n in "kv"}
+    case.q_bits = wlm.bf16_bits(np.random.default_rng(51).standard_normal((rows, case.heads, 128)).astype(np.float32))
+    pos = np.full(rows, -1)
+    for b, L in enumerate(case.seq_lens):
+        lo, hi = starts[b], starts[b + 1]
+        if 0 <= lo and hi <= rows:
+            pos[lo:hi] = L - (hi - lo) + np.arange(hi - lo)
+    rope, good = rope_table(50, 96), pos >= 0
+    assert 0 < good.sum()
+    q = wlm.bits_to_torch(case.q_bits, "cuda")
+    got, turned = append(case, rope, True, q, torch.full_like(q, -7.0))
+    k = f.rotate32(o.bf16_to_f64(case.new["k"]), rope, np.maximum(pos, 0), True)
+    assert np.array_equal(turned[good], wlm.bf16_bits(f.rotate32(case.q, rope, np.maximum(pos, 0), True))[good])
+    assert np.all(o.bf16_to_f64(turned[~good]) == -7.0)
+    if kind is Kv4Case:
+        same4(case, got, f.append(case.cache, case.table, case.seq_lens, case.starts, k, o.bf16_to_f64(case.new["v"])))
+    else:
+        for name, x in (("k", k.astype(np.float64)), ("v", o.bf16_to_f64(case.new["v"]))):
+            codes, scales = np.array(case.codes[name]), np.array(case.scales[name])
+            for b in range(3):                               # a request whose offsets fit, by itself
+                lo, hi = starts[b], starts[b + 1]
+                if 0 <= lo and hi <= rows:
+                    codes, scales = d.append(codes, scales, case.table[b:b + 1], case.seq_lens[b:b + 1], np.array([0, hi - lo]), x[lo:hi])
+            assert np.array_equal(got[name + "s"], scales) and np.array_equal(got[name], codes), name
