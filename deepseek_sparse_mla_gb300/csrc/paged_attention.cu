@@ -8,8 +8,8 @@
 // other operand is split into two e4m3 terms to keep its bits:
 //   x = (hi + lo / 16) * 2^k,  hi = e4m3(x / 2^k),  lo = e4m3(16 (x / 2^k - hi)).
 // e4m3 has 4 significant bits, so hi leaves a remainder of at most 2^-4 of x, which fits lo: bf16's 8 bits
-// are kept exactly for values down to 2^-14 of the row's largest, and a probability keeps 8 bits or more
-// (its remainder is rounded to 4 bits), with an absolute step of 2^-20 of the largest contribution.
+// are kept exactly for values down to 2^-13 of the row's largest, and a probability keeps 8 bits or more
+// (its remainder is rounded to 4 bits), with an absolute error of 2^-20 of the largest contribution.
 // hi and lo are separate columns of the small operand and are added in fp32 after the products, which
 // costs nothing: the large operand (128 keys, or 128 value dims) sets the time of these MMAs.
 //

@@ -7,11 +7,11 @@
 //   S [128 pairs x 128 keys]  = Q [128 x 128] K^T     K's codes as they are, Q in two e4m3 terms, from shared memory
 //   O [128 pairs x 128 dims] += P [128 x 128] V       P in fp16 from TMEM, V widened to fp16 in shared memory
 // Two e4m3 products take as long as one in fp16 or bf16 and K needs no widening.  Q = hi + lo in units of 2^-8 of
-// the row's largest value: 8 bits of bf16 are kept down to 2^-10 of it, with an absolute error of at most 2^-18
+// the row's largest value: 8 bits of bf16 are kept down to 2^-9 of it, with an absolute error of at most 2^-17
 // below (bf16 itself has 2^-9 of each value; one accumulator for both terms leaves no room for a scale
 // of lo's own).  ks multiplies the scores of its page, one fp32 factor per 16 keys.  V as fp16 holds codes exactly;
 // vs goes into it relative to the largest of the piece's pages, exactly for the powers of two that the append writes.
-// P carries 2^8 times the probability (11 bits of it, with an absolute step of 2^-33 of the row's largest).
+// P carries 2^8 times the probability (11 bits of it, with an absolute error of 2^-33 of the row's largest).
 //
 // Work: (request, 256 pairs, K/V head, tile of 128 keys) units split into one contiguous range per CTA
 // (persistent, one CTA per SM), as in paged_attention.cu; a segment that is cut leaves fp32 pieces for a join.

@@ -681,11 +681,12 @@ typedef struct {
  * A row that sees nothing (an empty request) gets zeros and an lse of -inf.  Rows behind the last request's
  * are left as they were.  What lies in the cache behind a request's tokens is never used, NaN codes included.
  * A visible position without a valid page is skipped and reported (DSA_DEVICE_BAD_PAGE).
- * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-18 of its
- * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
+ * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-17 of its
+ * row's largest value (2^-21 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
  * Requests of at most 64 rows * heads per K/V head keep 8 bits or more of a contribution p * v_scale to the output, with
- * an absolute error of 2^-20 of the largest one; requests of more keep 11 bits of p, and hold V to 2^-25 of the largest V
- * scale of the request's pages, those that a row does not see included.
+ * an absolute error of 2^-20 of the largest one (a p below 2^-126 counts as 0); requests of more keep 11 bits of p, with an absolute
+ * error of 2^-33 of the row's largest, and hold V to 2^-25 of the largest V scale of the request's pages, those that a row does not
+ * see included.
  * max_seq_len and max_query_len may be any bounds that hold, but close ones are faster: up to 1,024 tokens no request is
  * cut into pieces to join, and only a max_query_len of more than 64 rows * heads per K/V head brings in the kernel for many rows.
  * DSA_ERR_UNSUPPORTED for more than DSA_MAX_REQUESTS requests, for block-table rows of more than 2^30 tokens, and where
@@ -701,12 +702,12 @@ DSA_API dsa_status dsa_paged_attention(const dsa_kv8_cache* cache, const dsa_bat
  *   z_s = scale * q[r,h] . (k_code_s * k_scale_s)      out[r,h] = sum_s softmax(z)_s * (v_code_s * v_scale_s)
  * What lies in the cache behind a request's tokens is never used, NaN scales included; a NaN scale makes the output of the rows
  * that see its token NaN.
- * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-18 of its
- * row's largest value (2^-22 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
+ * Sums, maxima and lse are fp32.  In the products q keeps bf16's bits with an absolute error of at most 2^-17 of its
+ * row's largest value (2^-21 for requests of at most 64 rows * heads per K/V head), taken as 2^-100 where it is smaller.
  * Requests of at most 64 rows * heads per K/V head keep 8 bits or more of a contribution p * v_scale to the output, with
- * an absolute error of 2^-20 of the largest one (of v_scale taken as 2^-121 where it is smaller); requests of more keep 11 bits of p,
- * and V exactly where its scale is at least
- * 2^-26 of the largest one of the request's tokens (those that a row does not see included), else to 2^-34 of that.
+ * an absolute error of 2^-20 of the largest one (with v_scale taken as 2^-121 where it is smaller; a p below 2^-126 counts as 0);
+ * requests of more keep 11 bits of p, with an absolute error of 2^-33 of the row's largest, and V exactly where its scale is at
+ * least 2^-26 of the largest one of the request's tokens (those that a row does not see included), else to 2^-34 of that.
  */
 DSA_API dsa_status dsa_kv4_attention(const dsa_kv4_cache* cache, const dsa_batch* batch, const void* q, int64_t q_stride,
                                      int32_t q_heads, float scale, int32_t max_query_len, const dsa_attn_mods* mods, void* out,
